@@ -220,7 +220,7 @@ def _prepare_attend(c, g, s):
     if own:
         from block_sparse_paged_score_gb300 import bsp
         s["cache"] = bsp.KvCache(bsp.MXFP4, hkv, blocks, buffer=s["kv"])
-        s["ws"] = bsp.dense_pa_workspace(n * ql * hkv, c["group"], ql)
+        s["ws"] = bsp.dense_pa_workspace(n * ql * hkv, hkv, c["group"], ql)
         s["out"] = torch.empty(n * ql, hkv * c["group"], D, dtype=torch.bfloat16, device="cuda")
 
 
