@@ -17,7 +17,7 @@ BF16, FP8_E4M3, MXFP4 = 0, 1, 2
 FORCE_TAIL = 1
 REUSE_SELECTION = 2  # decode step: attend with another layer's sparse_bt / sparse_ctx
 SELECT_BLOCKS = 4  # top-k: 128-token blocks are the unit of selection
-DEVERR = {1: "page id", 2: "block id", 4: "group sequence", 8: "timeout", 16: "slot"}
+DEVERR = {1: "page id", 2: "block id", 4: "group sequence", 8: "timeout", 16: "slot", 32: "capacity", 64: "position"}
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error"}
 
 
@@ -52,6 +52,29 @@ class DecodeStepArgs(C.Structure):
                 ("ws_bytes", C.c_size_t), ("dev_err", C.c_void_p), ("sel_counters", C.c_void_p)]
 
 
+class StepTablesArgs(C.Structure):
+    _fields_ = [("context_lens", C.c_void_p), ("new_lens", C.c_void_p), ("num_seqs", C.c_int32),
+                ("bt_stride", C.c_int32), ("block_table", C.c_void_p), ("free_blocks", C.c_void_p),
+                ("free_head", C.c_void_p), ("num_free", C.c_int32), ("token_capacity", C.c_int32),
+                ("num_blocks", C.c_int64), ("seq_lens", C.c_void_p), ("cu_tokens", C.c_void_p),
+                ("blocks_taken", C.c_void_p), ("slot", C.c_void_p), ("query_req_id", C.c_void_p),
+                ("query_abs_pos", C.c_void_p), ("dev_err", C.c_void_p)]
+
+
+class NormRopeArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("idx_q", C.c_void_p),
+                ("idx_k", C.c_void_p), ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("idx_q_stride", C.c_int64), ("idx_k_stride", C.c_int64), ("num_tokens", C.c_int32),
+                ("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32), ("num_idx_heads", C.c_int32),
+                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("idx_q_weight", C.c_void_p),
+                ("idx_k_weight", C.c_void_p), ("weight_offset", C.c_float), ("eps", C.c_float),
+                ("rope_table", C.c_void_p), ("rope_rows", C.c_int64), ("rot_dim", C.c_int32),
+                ("rope_pairs", C.c_int32), ("positions", C.c_void_p), ("slot", C.c_void_p), ("q_out", C.c_void_p),
+                ("k_out", C.c_void_p), ("idx_q_out", C.c_void_p), ("q_out_dtype", C.c_int32),
+                ("idx_q_out_dtype", C.c_int32), ("kv", C.POINTER(KvCacheDesc)), ("idx", C.POINTER(IndexCacheDesc)),
+                ("dev_err", C.c_void_p)]
+
+
 _lib = None
 SYMBOLS = {
     "bsp_kv_cache_interleaved": [C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_float, C.c_float,
@@ -80,6 +103,14 @@ SYMBOLS = {
     "bsp_sparse_pa_decode_workspace_bytes": [C.c_int32, C.c_int32, C.c_int32],
     "bsp_sparse_pa_decode_splits": [C.c_int32, C.c_int32, C.c_int32],
     "bsp_sparse_decode_step": [C.POINTER(DecodeStepArgs), C.c_void_p, C.c_void_p],
+    "bsp_step_tables": [C.POINTER(StepTablesArgs), C.c_void_p],
+    "bsp_norm_rope_write": [C.POINTER(NormRopeArgs), C.c_void_p],
+    "bsp_kv_page_read": [C.POINTER(KvCacheDesc), C.POINTER(IndexCacheDesc), C.c_void_p, C.c_int32, C.c_void_p,
+                         C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p],
+    "bsp_dense_pa_workspace_bytes": [C.c_int32, C.c_int32, C.c_int32, C.c_int32],
+    "bsp_dense_pa_decode": [C.POINTER(KvCacheDesc), C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_int32,
+                            C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p,
+                            C.c_size_t, C.c_void_p, C.c_void_p],
     "bsp_kv_block_bytes": [C.c_int32, C.c_int32],
     "bsp_index_field_bytes": [C.c_int32],
     "bsp_status_str": [C.c_int32],
@@ -87,7 +118,8 @@ SYMBOLS = {
     "bsp_launch_count": [],
     "bsp_version": [],
 }
-RESTYPES = {"bsp_sparse_pa_decode_workspace_bytes": C.c_size_t, "bsp_kv_block_bytes": C.c_int64,
+RESTYPES = {"bsp_sparse_pa_decode_workspace_bytes": C.c_size_t, "bsp_dense_pa_workspace_bytes": C.c_size_t,
+            "bsp_kv_block_bytes": C.c_int64,
             "bsp_index_field_bytes": C.c_int64, "bsp_status_str": C.c_char_p, "bsp_launch_count": C.c_int64}
 
 
@@ -323,3 +355,108 @@ def sparse_decode_step(args, events=None, stream=None):
     if events is not None:
         ev = (C.c_void_p * len(events))(*[e.cuda_event for e in events])
     _check("bsp_sparse_decode_step", lib().bsp_sparse_decode_step(C.byref(args), ev, _stream(stream)))
+
+
+def _dense(name, t, dtype, stream, numel=None):
+    """The device address of a contiguous tensor of one of the given dtypes
+    on the stream's device, of at least `numel` elements."""
+    if t is None:
+        return None
+    if t.device != stream.device:
+        raise ValueError(f"{name} is on {t.device}, the stream on {stream.device}")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
+    return _ptr(t)
+
+
+def _head_rows(name, t, stream):
+    """(address, token stride) of bf16 rows [T, heads, 128] whose heads lie
+    side by side; the tokens may be any distance apart."""
+    if t is None:
+        return None, 0
+    if t.device != stream.device:
+        raise ValueError(f"{name} is on {t.device}, the stream on {stream.device}")
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != 128:
+        raise ValueError(f"{name} is not bf16 [tokens, heads, 128]")
+    st = t.stride()
+    if st[2] != 1 or (t.shape[1] > 1 and st[1] != 128):
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    return _ptr(t), st[0] if t.shape[0] > 1 else t.shape[1] * 128
+
+
+def step_tables(args, stream=None):
+    """Run bsp_step_tables on a filled StepTablesArgs (see step.StepTables)."""
+    _check("bsp_step_tables", lib().bsp_step_tables(C.byref(args), _stream(stream)))
+
+
+def norm_rope_write(args, stream=None):
+    """Run bsp_norm_rope_write on a filled NormRopeArgs (see step.NormRopeWrite)."""
+    _check("bsp_norm_rope_write", lib().bsp_norm_rope_write(C.byref(args), _stream(stream)))
+
+
+def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream=None):
+    """Cached tokens by slot as bf16 rows: (k, v, idx_k), k and v of the K/V
+    cache `kv`, idx_k of the index cache `idx`; either cache may be None."""
+    s = stream if stream is not None else torch.cuda.current_stream()
+    T = slot.numel()
+    if kv is not None:
+        shape = (T, kv.num_kv_heads, 128)
+        k = k if k is not None else torch.empty(shape, dtype=torch.bfloat16, device=slot.device)
+        v = v if v is not None else torch.empty(shape, dtype=torch.bfloat16, device=slot.device)
+    elif k is not None or v is not None:
+        raise ValueError("k and v need a K/V cache")
+    if idx is not None:
+        shape = (T, idx.num_heads, 128)
+        idx_k = idx_k if idx_k is not None else torch.empty(shape, dtype=torch.bfloat16, device=slot.device)
+    elif idx_k is not None:
+        raise ValueError("idx_k needs an index cache")
+    bf = torch.bfloat16
+    _check("bsp_kv_page_read",
+           lib().bsp_kv_page_read(C.byref(kv.desc) if kv is not None else None,
+                                  C.byref(idx.desc) if idx is not None else None,
+                                  _dense("slot", slot, torch.int64, s), T,
+                                  _dense("k", k, bf, s, T * kv.num_kv_heads * 128 if kv is not None else 0),
+                                  _dense("v", v, bf, s, T * kv.num_kv_heads * 128 if kv is not None else 0),
+                                  _dense("idx_k", idx_k, bf, s, T * idx.num_heads * 128 if idx is not None else 0),
+                                  _dense("dev_err", dev_err, torch.int32, s, 1), _stream(s)))
+    return k, v, idx_k
+
+
+def dense_pa_workspace_bytes(num_rows, num_kv_heads, group, q_group):
+    return int(lib().bsp_dense_pa_workspace_bytes(num_rows, num_kv_heads, group, q_group))
+
+
+def dense_pa_workspace(num_rows, num_kv_heads, group, q_group, device="cuda"):
+    """A workspace for dense attention calls of these sizes that never overlap
+    on the GPU (its contents need not be set)."""
+    n = dense_pa_workspace_bytes(num_rows, num_kv_heads, group, q_group)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, q_group, sm_scale=None, out=None,
+                    ws=None, dev_err=None, stream=None):
+    """Attention of each row over its whole context in an MXFP4 cache
+    (bsp_dense_pa_decode); q [tokens, num_q_heads, 128], rows = tokens * Hkv."""
+    s = stream if stream is not None else torch.cuda.current_stream()
+    rows = row_len.numel()
+    n = rows // kv.num_kv_heads * num_q_heads * 128
+    sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
+    out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if ws is None:
+        ws = dense_pa_workspace(rows, kv.num_kv_heads, num_q_heads // kv.num_kv_heads, q_group, q.device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table is not [sequences, blocks]")
+    qt = torch.bfloat16 if q_dtype == BF16 else (torch.uint8, torch.float8_e4m3fn)
+    i32 = torch.int32
+    _check("bsp_dense_pa_decode",
+           lib().bsp_dense_pa_decode(C.byref(kv.desc), _dense("q", q, qt, s, n), q_dtype, num_q_heads,
+                                     _dense("block_table", block_table, i32, s), block_table.shape[1],
+                                     _dense("row_seq", row_seq, i32, s, rows), _dense("row_len", row_len, i32, s),
+                                     rows, q_group, sm_scale, _dense("out", out, torch.bfloat16, s, n),
+                                     _dense("ws", ws, torch.uint8, s), ws.numel(),
+                                     _dense("dev_err", dev_err, i32, s, 1), _stream(s)))
+    return out

@@ -380,6 +380,235 @@ size_t sparse_pa_decode_ws_need(int32_t kv_dtype, int32_t num_rows, int32_t k_pa
 
 }  // namespace bsp
 
+namespace {
+
+// whether [a, a + an) and [b, b + bn) share a byte
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && an > 0 && bn > 0 && x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
+
+// the cache fields of a writer or reader
+void set_caches(KvWriteParams& p, const bsp_kv_cache* kv, const bsp_index_cache* idx) {
+  if (kv) {
+    p.kv_dtype = kv->dtype;
+    p.hkv = kv->num_kv_heads;
+    p.k_base = static_cast<uint8_t*>(kv->k_base);
+    p.v_base = static_cast<uint8_t*>(kv->v_base);
+    p.id_stride = kv->id_stride_bytes;
+    p.num_blocks = kv->num_blocks;
+    p.k_scale = kv->k_scale;
+    p.v_scale = kv->v_scale;
+  }
+  if (idx) {
+    p.idx_dtype = idx->dtype;
+    p.hidx = idx->num_heads;
+    p.idx_base = static_cast<uint8_t*>(idx->base);
+    p.idx_block_stride = idx->block_stride_bytes;
+    p.idx_num_blocks = idx->num_blocks;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+bsp_status bsp_step_tables(const bsp_step_tables_args* a, bsp_stream_t stream) {
+  if (!a || a->num_seqs < 0 || a->bt_stride < 1 || a->num_free < 0 || a->token_capacity < 0 || a->num_blocks < 0)
+    return BSP_ERR_INVALID_ARG;
+  if (a->num_seqs > 65536) return BSP_ERR_UNSUPPORTED;
+  if (!a->cu_tokens || !a->blocks_taken) return BSP_ERR_INVALID_ARG;
+  if (a->num_seqs && (!a->context_lens || !a->new_lens || !a->block_table || !a->seq_lens)) return BSP_ERR_INVALID_ARG;
+  if (a->num_free && !a->free_blocks) return BSP_ERR_INVALID_ARG;
+  if (a->token_capacity && (!a->slot || !a->query_req_id || !a->query_abs_pos)) return BSP_ERR_INVALID_ARG;
+  const int64_t n = a->num_seqs, cap = a->token_capacity;
+  struct Range {
+    const void* p;
+    int64_t bytes, align;
+  };
+  const Range in[] = {{a->context_lens, 4 * n, 4}, {a->new_lens, 4 * n, 4}, {a->free_blocks, 4LL * a->num_free, 4},
+                      {a->free_head, 4, 4}};
+  const Range out[] = {{a->block_table, 4 * n * a->bt_stride, 4}, {a->seq_lens, 4 * n, 4}, {a->cu_tokens, 4 * (n + 1), 4},
+                       {a->blocks_taken, 4, 4}, {a->slot, 8 * cap, 8}, {a->query_req_id, 4 * cap, 4},
+                       {a->query_abs_pos, 4 * cap, 4}, {a->dev_err, 4, 4}};
+  for (const Range& r : in)
+    if (!al(r.p, r.align)) return BSP_ERR_INVALID_ARG;
+  for (const Range& o : out) {
+    if (!al(o.p, o.align)) return BSP_ERR_INVALID_ARG;
+    for (const Range& r : in)
+      if (overlap(o.p, o.bytes, r.p, r.bytes)) return BSP_ERR_INVALID_ARG;
+    for (const Range& r : out)
+      if (&r != &o && overlap(o.p, o.bytes, r.p, r.bytes)) return BSP_ERR_INVALID_ARG;
+  }
+  StepTablesParams p{};
+  p.context_lens = a->context_lens;
+  p.new_lens = a->new_lens;
+  p.num_seqs = a->num_seqs;
+  p.block_table = a->block_table;
+  p.bt_stride = a->bt_stride;
+  p.free_blocks = a->free_blocks;
+  p.free_head = a->free_head;
+  p.num_free = a->num_free;
+  p.num_blocks = a->num_blocks;
+  p.token_capacity = a->token_capacity;
+  p.seq_lens = a->seq_lens;
+  p.cu_tokens = a->cu_tokens;
+  p.blocks_taken = a->blocks_taken;
+  p.slot = a->slot;
+  p.query_req_id = a->query_req_id;
+  p.query_abs_pos = a->query_abs_pos;
+  p.err = a->dev_err;
+  const bsp_status st = cuda_status(launch_step_tables(p, device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+  if (st == BSP_OK) ++g_launches;
+  return st;
+}
+
+bsp_status bsp_norm_rope_write(const bsp_norm_rope_args* a, bsp_stream_t stream) {
+  if (!a || a->num_tokens < 0) return BSP_ERR_INVALID_ARG;
+  bsp_status st;
+  if (a->kv && (st = check_kv(a->kv)) != BSP_OK) return st;
+  if (a->idx && (st = check_idx(a->idx)) != BSP_OK) return st;
+  if ((a->q_out && a->q_out_dtype != BSP_BF16 && a->q_out_dtype != BSP_FP8_E4M3) ||
+      (a->idx_q_out && a->idx_q_out_dtype != BSP_BF16 && a->idx_q_out_dtype != BSP_FP8_E4M3))
+    return BSP_ERR_UNSUPPORTED;
+  if (a->rot_dim < 0 || a->rot_dim > kDim || a->rot_dim % 16) return BSP_ERR_UNSUPPORTED;
+  if (!(a->eps >= 0.f) || !(a->weight_offset == a->weight_offset)) return BSP_ERR_INVALID_ARG;
+  // each input has somewhere to go, and each output comes from somewhere
+  if (!a->q != !a->q_out || !a->idx_q != !a->idx_q_out || !a->idx_k != !a->idx) return BSP_ERR_INVALID_ARG;
+  if ((a->kv && (!a->k || !a->v)) || (a->k_out && !a->k) || (a->k && !a->kv && !a->k_out) || (a->v && !a->kv))
+    return BSP_ERR_INVALID_ARG;
+  if ((a->kv && a->num_kv_heads != a->kv->num_kv_heads) || (a->idx && a->num_idx_heads != a->idx->num_heads))
+    return BSP_ERR_INVALID_ARG;
+  if (a->num_tokens == 0) return BSP_OK;
+  if ((a->kv || a->idx) && (!a->slot || !al(a->slot, 8))) return BSP_ERR_INVALID_ARG;
+  if (a->rot_dim && (!a->rope_table || !al(a->rope_table, 16) || a->rope_rows < 1 || !a->positions))
+    return BSP_ERR_INVALID_ARG;
+  if (a->positions && !al(a->positions, 4)) return BSP_ERR_INVALID_ARG;
+  const int64_t T = a->num_tokens;
+  NormRopeParams p{};
+  const void* src[kHeadTypes] = {a->q, a->k, a->v, a->idx_q, a->idx_k};
+  const int64_t stride[kHeadTypes] = {a->q_stride, a->k_stride, a->v_stride, a->idx_q_stride, a->idx_k_stride};
+  const int32_t heads[kHeadTypes] = {a->num_q_heads, a->num_kv_heads, a->num_kv_heads, a->num_idx_heads,
+                                     a->num_idx_heads};
+  const void* weight[kHeadTypes] = {a->q_weight, a->k_weight, nullptr, a->idx_q_weight, a->idx_k_weight};
+  void* out[kHeadTypes] = {a->q_out, a->k_out, nullptr, a->idx_q_out, nullptr};
+  const int32_t out_dtype[kHeadTypes] = {a->q_out_dtype, BSP_BF16, 0, a->idx_q_out_dtype, 0};
+  for (int i = 0; i < kHeadTypes; ++i) {
+    if (!src[i]) continue;
+    const int64_t row = static_cast<int64_t>(heads[i]) * kDim;
+    if (heads[i] < 1 || stride[i] < row || stride[i] % 8 || !al(src[i], 16) || !al(weight[i], 16) || !al(out[i], 16))
+      return BSP_ERR_INVALID_ARG;
+    if (heads[i] > (1 << 20)) return BSP_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(heads[i]) * T > (int64_t{1} << 40)) return BSP_ERR_UNSUPPORTED;
+    p.src[i] = static_cast<const uint16_t*>(src[i]);
+    p.stride[i] = stride[i];
+    p.heads[i] = heads[i];
+    p.weight[i] = static_cast<const uint16_t*>(weight[i]);
+    p.out[i] = out[i];
+    p.out_dtype[i] = out_dtype[i];
+  }
+  for (int i = 0; i < kHeadTypes; ++i) {
+    if (!p.out[i]) continue;
+    const int64_t bytes = T * p.heads[i] * kDim * (p.out_dtype[i] == BSP_BF16 ? 2 : 1);
+    for (int j = 0; j < kHeadTypes; ++j) {
+      if (j != i && overlap(p.out[i], bytes, p.out[j], T * p.heads[j] * kDim * (p.out_dtype[j] == BSP_BF16 ? 2 : 1)))
+        return BSP_ERR_INVALID_ARG;
+      const bool in_place = j == i && p.out[i] == src[j] && p.out_dtype[i] == BSP_BF16 && stride[j] == p.heads[j] * kDim;
+      if (!in_place && p.src[j] && overlap(p.out[i], bytes, src[j], ((T - 1) * stride[j] + p.heads[j] * kDim) * 2))
+        return BSP_ERR_INVALID_ARG;
+    }
+  }
+  p.weight_offset = a->weight_offset;
+  p.eps = a->eps;
+  p.rope = a->rope_table;
+  p.rope_rows = a->rope_rows;
+  p.rot_dim = a->rot_dim;
+  p.rope_pairs = a->rope_pairs ? 1 : 0;
+  p.positions = a->positions;
+  p.slot = a->slot;
+  p.num_tokens = a->num_tokens;
+  set_caches(p.cache, a->kv, a->idx);
+  p.err = a->dev_err;
+  if (!a->q && !a->k && !a->idx_q && !a->idx_k) return BSP_OK;
+  st = cuda_status(launch_norm_rope(p, device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+  if (st == BSP_OK) ++g_launches;
+  return st;
+}
+
+bsp_status bsp_kv_page_read(const bsp_kv_cache* kv, const bsp_index_cache* idx, const int64_t* slot,
+                            int32_t num_tokens, void* k, void* v, void* idx_k, int32_t* dev_err, bsp_stream_t stream) {
+  if (num_tokens < 0 || !k != !v) return BSP_ERR_INVALID_ARG;
+  bsp_status st;
+  if (k && (st = check_kv(kv)) != BSP_OK) return st;
+  if (idx_k && (st = check_idx(idx)) != BSP_OK) return st;
+  if (num_tokens == 0 || (!k && !idx_k)) return BSP_OK;
+  if (!slot || !al(slot, 8) || !al(k, 16) || !al(v, 16) || !al(idx_k, 16)) return BSP_ERR_INVALID_ARG;
+  const int64_t units = (k ? kv->num_kv_heads : 0) + (idx_k ? idx->num_heads : 0);
+  if ((static_cast<int64_t>(num_tokens) + 15) / 16 * units > INT32_MAX) return BSP_ERR_UNSUPPORTED;
+  KvReadParams p{};
+  set_caches(p.cache, k ? kv : nullptr, idx_k ? idx : nullptr);
+  p.cache.slot = slot;
+  p.cache.num_tokens = num_tokens;
+  p.cache.err = dev_err;
+  p.k = static_cast<uint16_t*>(k);
+  p.v = static_cast<uint16_t*>(v);
+  p.idx_k = static_cast<uint16_t*>(idx_k);
+  st = cuda_status(launch_kv_page_read(p, reinterpret_cast<cudaStream_t>(stream)));
+  if (st == BSP_OK) ++g_launches;
+  return st;
+}
+
+size_t bsp_dense_pa_workspace_bytes(int32_t num_rows, int32_t num_kv_heads, int32_t group, int32_t q_group) {
+  if (num_rows <= 0 || num_kv_heads < 1 || num_rows % num_kv_heads || !valid_group(group) || q_group < 1 || q_group > 8)
+    return 0;
+  return dense_pa_ws_bytes(num_rows, num_kv_heads, group, q_group, device_sms());
+}
+
+bsp_status bsp_dense_pa_decode(const bsp_kv_cache* kv, const void* q, int32_t q_dtype, int32_t num_q_heads,
+                               const int32_t* block_table, int32_t bt_stride, const int32_t* row_seq,
+                               const int32_t* row_len, int32_t num_rows, int32_t q_group, float sm_scale, void* out,
+                               void* ws, size_t ws_bytes, int32_t* dev_err, bsp_stream_t stream) {
+  bsp_status st = check_kv(kv);
+  if (st != BSP_OK) return st;
+  if (kv->dtype != BSP_MXFP4 || (q_dtype != BSP_BF16 && q_dtype != BSP_FP8_E4M3)) return BSP_ERR_UNSUPPORTED;
+  if (num_rows < 0 || num_q_heads < 1 || bt_stride < 1) return BSP_ERR_INVALID_ARG;
+  if (num_q_heads % kv->num_kv_heads || num_rows % kv->num_kv_heads) return BSP_ERR_INVALID_ARG;
+  const int32_t group = num_q_heads / kv->num_kv_heads;
+  if (!valid_group(group) || q_group < 1 || q_group > 8) return BSP_ERR_UNSUPPORTED;
+  if (!(sm_scale - sm_scale == 0.f)) return BSP_ERR_INVALID_ARG;  // infinite or NaN
+  if (num_rows == 0) return BSP_OK;
+  if (!q || !block_table || !row_seq || !row_len || !out || !al(q, 16) || !al(out, 16) || !al(block_table, 4) ||
+      !al(row_seq, 4) || !al(row_len, 4))
+    return BSP_ERR_INVALID_ARG;
+  const size_t need = dense_pa_ws_bytes(num_rows, kv->num_kv_heads, group, q_group, device_sms());
+  if (need && (!ws || ws_bytes < need || !al(ws, 16))) return BSP_ERR_WORKSPACE;
+  DensePaParams p{};
+  p.k_base = static_cast<const uint8_t*>(kv->k_base);
+  p.v_base = static_cast<const uint8_t*>(kv->v_base);
+  p.id_stride = kv->id_stride_bytes;
+  p.num_blocks = kv->num_blocks;
+  p.hkv = kv->num_kv_heads;
+  p.group = group;
+  p.q = q;
+  p.q_dtype = q_dtype;
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  p.row_seq = row_seq;
+  p.row_len = row_len;
+  p.num_rows = num_rows;
+  p.q_group = q_group;
+  p.sm_scale = sm_scale;
+  p.out = out;
+  p.ws = ws;
+  p.err = dev_err;
+  int launches = 0;
+  st = cuda_status(launch_dense_pa(p, device_sms(), reinterpret_cast<cudaStream_t>(stream), &launches));
+  g_launches += launches;
+  return st;
+}
+
+}  // extern "C"
+
 extern "C" {
 
 static bsp_status sparse_pa_common(const bsp_kv_cache* kv, const void* q, int32_t q_dtype, int32_t num_q_heads,

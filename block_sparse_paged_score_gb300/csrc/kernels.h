@@ -219,4 +219,78 @@ cudaError_t launch_index_score_prefill(const PrefillScoreParams& p, cudaStream_t
 // the same for an MXFP4 index cache (e2m1 keys, e8m0 scales per 32 dims)
 cudaError_t launch_index_score_prefill_mx(const PrefillScoreParams& p, cudaStream_t s);
 
+// block table, slot map and positions of a step from the requests' lengths
+struct StepTablesParams {
+  const int32_t* context_lens;
+  const int32_t* new_lens;
+  int32_t num_seqs;
+  int32_t* block_table;
+  int32_t bt_stride;
+  const int32_t* free_blocks;
+  const int32_t* free_head;  // NULL: 0
+  int32_t num_free;
+  int64_t num_blocks;
+  int32_t token_capacity;
+  int32_t* seq_lens;
+  int32_t* cu_tokens;
+  int32_t* blocks_taken;
+  int64_t* slot;
+  int32_t* query_req_id;
+  int32_t* query_abs_pos;
+  int32_t* err;
+};
+cudaError_t launch_step_tables(const StepTablesParams& p, int num_sms, cudaStream_t s);
+
+// per-head RMS norm and rotation of q, k, index q and index k; K, V and the
+// index key quantised into the caches.  Head types in the order below.
+enum { kHeadQ, kHeadK, kHeadV, kHeadIdxQ, kHeadIdxK, kHeadTypes };
+struct NormRopeParams {
+  const uint16_t* src[kHeadTypes];  // NULL: type absent
+  int64_t stride[kHeadTypes];       // elements between tokens
+  int32_t heads[kHeadTypes];        // 0: type absent
+  const uint16_t* weight[kHeadTypes];  // NULL: 1
+  float weight_offset, eps;
+  const float* rope;  // [rope_rows][rot_dim]: cos, then sin
+  int64_t rope_rows;
+  int32_t rot_dim, rope_pairs;
+  const int32_t* positions;
+  const int64_t* slot;
+  int32_t num_tokens;
+  void* out[kHeadTypes];      // dense rows of q, k, index q (NULL: none)
+  int32_t out_dtype[kHeadTypes];
+  KvWriteParams cache;  // k_base NULL: no K/V cache; idx_base NULL: no index cache
+  int32_t* err;
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t s);
+
+// cached tokens gathered by slot as bf16
+struct KvReadParams {
+  KvWriteParams cache;  // k, v, idx_k unused; slot, num_tokens, err and the cache fields used
+  uint16_t* k;
+  uint16_t* v;
+  uint16_t* idx_k;
+};
+cudaError_t launch_kv_page_read(const KvReadParams& p, cudaStream_t s);
+
+// dense attention over an MXFP4 cache
+struct DensePaParams {
+  const uint8_t* k_base;
+  const uint8_t* v_base;
+  int64_t id_stride, num_blocks;
+  int32_t hkv, group;
+  const void* q;
+  int32_t q_dtype;
+  const int32_t* block_table;
+  int32_t bt_stride;
+  const int32_t* row_seq;
+  const int32_t* row_len;
+  int32_t num_rows, q_group;
+  float sm_scale;
+  void* out;
+  void* ws;
+  int32_t* err;
+};
+size_t dense_pa_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms);
+cudaError_t launch_dense_pa(const DensePaParams& p, int num_sms, cudaStream_t s, int* launches);
+
 }  // namespace bsp

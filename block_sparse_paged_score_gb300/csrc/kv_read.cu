@@ -1,0 +1,164 @@
+// kv_read.cu -- the writer's inverse: cached K, V and index keys gathered by
+// slot and dequantised to bf16 rows (bsp_kv_page_read).
+//
+//   bf16   as stored;  fp8  e4m3 * scale, rounded to bf16
+//   MXFP4  e2m1 * 2^(e8m0 - 127), exact in bf16 (until it leaves its range)
+//
+// One CTA reads 16 consecutive tokens of one head, so that slots which follow
+// each other (the usual case: a sequence's page) share sectors.  Rows that
+// are contiguous per token (K pages' 16-byte chunks, MXFP4 fields, index
+// fields) are read 8 dims a lane, 16 lanes a token.  An interleaved cache's V
+// page holds 16 (fp8) or 8 (bf16) tokens of one dim together; there a lane
+// is a token, a warp reads two dims at a time, and the tile is turned around
+// in shared memory before it is stored in rows.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace bsp {
+
+namespace {
+
+constexpr int kTok = 16;  // tokens of a CTA
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+// 8 e4m3 bytes times sc
+__device__ __forceinline__ uint4 from_e4m3(uint2 w, float sc) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = e4m3_to_float((i < 4 ? w.x : w.y) >> (8 * (i & 3))) * sc;
+  return pack8(x);
+}
+
+// dims 8*l.. of token o of an MXFP4 field
+__device__ __forceinline__ uint4 from_mx(const uint8_t* field, int o, int l) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(field + o * 64 + 4 * l);
+  const float sc = e8m0_to_float(field[kMxScaleOff + o * 4 + (l >> 2)]);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = f16x2_to_float2(e2m1x2_to_f16x2((w >> (8 * i)) & 0xFF));
+    x[2 * i] = f.x * sc, x[2 * i + 1] = f.y * sc;
+  }
+  return pack8(x);
+}
+
+__global__ void __launch_bounds__(128) kv_page_read_kernel(KvReadParams p) {
+  __shared__ int64_t s_slot[kTok];
+  __shared__ __align__(16) uint16_t s_v[kTok][kDim + 8];
+  pdl_wait();
+  pdl_trigger();
+  const KvWriteParams& c = p.cache;
+  const int units = (p.k ? c.hkv : 0) + (p.idx_k ? c.hidx : 0);
+  const int u = static_cast<int>(blockIdx.x % units);
+  const int64_t tok0 = static_cast<int64_t>(blockIdx.x / units) * kTok;
+  const bool is_idx = !(p.k && u < c.hkv);
+  const int h = is_idx ? u - (p.k ? c.hkv : 0) : u;
+  const int tid = threadIdx.x;
+  if (tid < kTok) {  // slots outside the cache read as -1
+    int64_t slot = tok0 + tid < c.num_tokens ? c.slot[tok0 + tid] : -1;
+    if (slot >= (is_idx ? c.idx_num_blocks : c.num_blocks) * kBlock) {
+      set_err(c.err, BSP_DEVERR_SLOT);
+      slot = -1;
+    }
+    s_slot[tid] = slot;
+  }
+  __syncthreads();
+  const int l = tid & 15;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {  // K (or the index key), then V
+    if (side == 1 && is_idx) break;
+    const int dtype = is_idx ? c.idx_dtype : c.kv_dtype;
+    uint16_t* out = is_idx ? p.idx_k : (side == 0 ? p.k : p.v);
+    const int heads = is_idx ? c.hidx : c.hkv;
+    if (side == 1 && dtype != BSP_MXFP4) {
+      // V page of an interleaved cache: lane = token, 2 dims a warp at a time
+      const int t = tid & 15, dd = tid >> 4;  // dims dd, dd + 8, ...
+      const int64_t slot = s_slot[t];
+      const int64_t page = slot / kBlock * 16 + slot % kBlock / kPage;
+      const int pt = static_cast<int>(slot % kPage);
+      if (slot < 0) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s_v[t][dd + 8 * i] = 0;
+      } else if (dtype == BSP_FP8_E4M3) {
+        const uint8_t* src = c.v_base + page * c.id_stride + static_cast<int64_t>(h) * 2048 + pt;
+        uint8_t b[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) b[i] = src[(dd + 8 * i) * 16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s_v[t][dd + 8 * i] = static_cast<uint16_t>(pack_bf16x2(e4m3_to_float(b[i]) * c.v_scale, 0.f));
+      } else {
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(c.v_base + page * c.id_stride +
+                                                                static_cast<int64_t>(h) * 4096) +
+                              (pt >> 3) * 1024 + (pt & 7);
+        uint16_t b[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) b[i] = src[(dd + 8 * i) * 8];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s_v[t][dd + 8 * i] = b[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int tk = (tid >> 4) + 8 * r;
+        if (tok0 + tk < c.num_tokens)
+          *reinterpret_cast<uint4*>(out + ((tok0 + tk) * heads + h) * kDim + 8 * l) =
+              *reinterpret_cast<const uint4*>(&s_v[tk][8 * l]);
+      }
+      continue;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int tk = (tid >> 4) + 8 * r;
+      if (tok0 + tk >= c.num_tokens) continue;
+      const int64_t slot = s_slot[tk];
+      uint4 w = zero;
+      if (slot >= 0) {
+        const int64_t block = slot / kBlock;
+        const int o = static_cast<int>(slot % kBlock);
+        if (is_idx) {
+          const uint8_t* f = c.idx_base + block * c.idx_block_stride;
+          if (dtype == BSP_BF16) {
+            w = *reinterpret_cast<const uint4*>(f + static_cast<int64_t>(h) * kBf16IndexField + o * 256 + 16 * l);
+          } else if (dtype == BSP_FP8_E4M3) {
+            f += static_cast<int64_t>(h) * kFp8IndexField;
+            w = from_e4m3(*reinterpret_cast<const uint2*>(f + o * 128 + 8 * l),
+                          *reinterpret_cast<const float*>(f + kFp8IndexScaleOff + o * 4));
+          } else {
+            w = from_mx(f + static_cast<int64_t>(h) * kMxField, o, l);
+          }
+        } else if (dtype == BSP_MXFP4) {
+          w = from_mx((side == 0 ? c.k_base : c.v_base) + block * c.id_stride + static_cast<int64_t>(h) * kMxField, o,
+                      l);
+        } else {  // K page [d/x][16 tokens][x]
+          const uint8_t* page = c.k_base + (block * 16 + o / kPage) * c.id_stride;
+          const int t = o % kPage;
+          if (dtype == BSP_FP8_E4M3)
+            w = from_e4m3(*reinterpret_cast<const uint2*>(page + static_cast<int64_t>(h) * 2048 + (l >> 1) * 256 +
+                                                          t * 16 + (l & 1) * 8),
+                          c.k_scale);
+          else
+            w = *reinterpret_cast<const uint4*>(page + static_cast<int64_t>(h) * 4096 + l * 256 + t * 16);
+        }
+      }
+      *reinterpret_cast<uint4*>(out + ((tok0 + tk) * heads + h) * kDim + 8 * l) = w;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_page_read(const KvReadParams& p, cudaStream_t s) {
+  const int64_t units = (p.k ? p.cache.hkv : 0) + (p.idx_k ? p.cache.hidx : 0);
+  const int64_t ctas = (static_cast<int64_t>(p.cache.num_tokens) + kTok - 1) / kTok * units;
+  if (ctas == 0) return cudaSuccess;
+  const cudaError_t e = launch_kernel(kv_page_read_kernel, dim3(static_cast<unsigned>(ctas)), dim3(128), 0, s, 0, p);
+  return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+}  // namespace bsp

@@ -11,22 +11,12 @@
 // the 8704 B MXFP4 field.  The writer is built without fast-math: divisions
 // are IEEE round-to-nearest, so its bytes are reproducible bit for bit.
 #include "common.cuh"
+#include "encode.cuh"
 #include "kernels.h"
 
 namespace bsp {
 
 namespace {
-
-// Shared exponent of an MXFP4 group: clamp(floor(log2(amax)) - 2, -127, 127),
-// floor(log2) read exactly off the fp32 bits (OCP MX v1.0 rule).
-__device__ __forceinline__ int mx_shared_exp(float amax) {
-  uint32_t b = __float_as_uint(amax);
-  if (b == 0) return -127;
-  int ex = (b >> 23) & 0xFF;
-  int E = ex ? ex - 127 : (31 - __clz(b & 0x7FFFFFu)) - 149;
-  int e = E - 2;
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
-}
 
 // Write dims 4*lane..+3 of token o of an MXFP4 field.
 __device__ __forceinline__ void write_mx(uint8_t* field, int o, int lane, const float (&x)[4]) {

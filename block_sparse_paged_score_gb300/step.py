@@ -13,6 +13,12 @@ there.  Each direction either crosses by one copy-engine copy or is read or
 written in place by the step's kernels (zero-copy).  ``MixedStep`` is the
 chunked-prefill batch (decode rows first, then prefill chunks and pad rows)
 as separate calls on one stream.
+
+``StepTables``, ``NormRopeWrite`` and ``DenseStep`` are the step of a layer
+without an indexer over a 4-bit cache, from the requests' lengths and the
+projections' rows to the attention output: the block table and slot map, the
+norms and rotation with the cache write, and the dense attention.
+``StepTables`` and ``NormRopeWrite`` serve layers with an indexer as well.
 """
 import ctypes as C
 
@@ -200,3 +206,159 @@ class MixedStep:
                               w.k_pages, w.sm_scale, self.out[ndt:], self.dev_err, s)
         mark(4)
         return self.out
+
+
+class StepTables:
+    """Block table, slot map and positions of a step, built on the GPU from
+    the requests' lengths (bsp_step_tables).  Owns the outputs: block_table
+    [num_seqs, bt_stride] (kept from step to step; entries of blocks that hold
+    no tokens are -1 at first, or block_table is the caller's), seq_lens,
+    cu_tokens, blocks_taken, and slot, query_req_id, query_abs_pos of
+    token_capacity rows, the last of them pad rows where the step has fewer
+    tokens."""
+
+    def __init__(self, num_seqs, bt_stride, token_capacity, num_blocks, block_table=None, device="cuda"):
+        e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=device)  # noqa: E731
+        self.num_seqs, self.token_capacity = num_seqs, token_capacity
+        if block_table is None:
+            block_table = torch.full((num_seqs, bt_stride), -1, dtype=torch.int32, device=device)
+        if tuple(block_table.shape) != (num_seqs, bt_stride):
+            raise ValueError(f"block_table is not [{num_seqs}, {bt_stride}]")
+        self.block_table = block_table
+        self.seq_lens, self.cu_tokens, self.blocks_taken = e(num_seqs), e(num_seqs + 1), e(1)
+        self.slot = e(token_capacity, torch.int64)
+        self.query_req_id, self.query_abs_pos = e(token_capacity), e(token_capacity)
+        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
+        a = self.args = bsp.StepTablesArgs()
+        a.num_seqs, a.bt_stride, a.token_capacity, a.num_blocks = num_seqs, bt_stride, token_capacity, num_blocks
+        s = torch.cuda.current_stream(self.seq_lens.device)
+        a.block_table = bsp._dense("block_table", block_table, torch.int32, s)
+        a.seq_lens, a.cu_tokens, a.blocks_taken = (self.seq_lens.data_ptr(), self.cu_tokens.data_ptr(),
+                                                   self.blocks_taken.data_ptr())
+        a.slot, a.query_req_id, a.query_abs_pos = (self.slot.data_ptr(), self.query_req_id.data_ptr(),
+                                                   self.query_abs_pos.data_ptr())
+        a.dev_err = self.dev_err.data_ptr()
+
+    def run(self, context_lens, new_lens, free_blocks, free_head=None, stream=None):
+        """int32 lengths [num_seqs] before the step and of the step, the free
+        block ids, and how many of them were taken before (a device scalar;
+        None: 0); fills the outputs."""
+        s = stream if stream is not None else torch.cuda.current_stream()
+        a, i32 = self.args, torch.int32
+        if self.seq_lens.device != s.device:
+            raise ValueError(f"the tables are on {self.seq_lens.device}, the stream on {s.device}")
+        a.context_lens = bsp._dense("context_lens", context_lens, i32, s, self.num_seqs)
+        a.new_lens = bsp._dense("new_lens", new_lens, i32, s, self.num_seqs)
+        a.free_blocks, a.num_free = bsp._dense("free_blocks", free_blocks, i32, s), free_blocks.numel()
+        a.free_head = bsp._dense("free_head", free_head, i32, s, 1)
+        bsp.step_tables(a, s)
+        return self
+
+
+class NormRopeWrite:
+    """Norms, position rotation and cache write of a step's projections
+    (bsp_norm_rope_write) for up to max_tokens tokens.  kv and idx are the
+    caches (idx None: a layer without an indexer; kv None: queries and index
+    keys alone).  Weights are bf16 [128] or None; rope_table is fp32
+    [positions, rot_dim], cosines then sines (see rope_table), or None."""
+
+    def __init__(self, kv, idx, num_q_heads, max_tokens, q_weight=None, k_weight=None, idx_q_weight=None,
+                 idx_k_weight=None, weight_offset=0.0, eps=1e-6, rope_table=None, rope_pairs=False, q_dtype=bsp.BF16,
+                 idx_q_dtype=bsp.BF16, device="cuda"):
+        self.kv, self.idx, self.max_tokens = kv, idx, max_tokens
+        a = self.args = bsp.NormRopeArgs()
+        self.q_out = torch.empty(max_tokens, num_q_heads, 128, device=device,
+                                 dtype=torch.uint8 if q_dtype == bsp.FP8_E4M3 else torch.bfloat16)
+        self.idx_q_out = None
+        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
+        s = torch.cuda.current_stream(self.q_out.device)
+        a.num_q_heads, a.q_out_dtype, a.idx_q_out_dtype = num_q_heads, q_dtype, idx_q_dtype
+        if kv is not None:
+            a.kv, a.num_kv_heads = C.pointer(kv.desc), kv.num_kv_heads
+        if idx is not None:
+            a.idx, a.num_idx_heads = C.pointer(idx.desc), idx.num_heads
+            self.idx_q_out = torch.empty(max_tokens, idx.num_heads, 128, device=device,
+                                         dtype=torch.uint8 if idx_q_dtype == bsp.FP8_E4M3 else torch.bfloat16)
+        self.weights = (q_weight, k_weight, idx_q_weight, idx_k_weight)
+        a.q_weight, a.k_weight, a.idx_q_weight, a.idx_k_weight = (
+            bsp._dense("weight", w, torch.bfloat16, s, 128) for w in self.weights)
+        a.weight_offset, a.eps = weight_offset, eps
+        self.rope_table = rope_table
+        if rope_table is not None:
+            a.rope_table = bsp._dense("rope_table", rope_table, torch.float32, s)
+            a.rope_rows, a.rot_dim = rope_table.shape
+            a.rope_pairs = int(rope_pairs)
+        a.dev_err = self.dev_err.data_ptr()
+
+    def run(self, q, k, v, idx_q, idx_k, positions, slot, stream=None):
+        """bf16 rows [T, heads, 128] (heads side by side, tokens any distance
+        apart; idx_q and idx_k None without an index cache), int32 positions
+        and int64 slots [T]; returns the queries and index queries (views of
+        the object's buffers)."""
+        s = stream if stream is not None else torch.cuda.current_stream()
+        a = self.args
+        T = q.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens, the buffers hold {self.max_tokens}")
+        if self.q_out.device != s.device:
+            raise ValueError(f"the buffers are on {self.q_out.device}, the stream on {s.device}")
+        rows = (("q", q, a.num_q_heads), ("k", k, a.num_kv_heads), ("v", v, a.num_kv_heads),
+                ("idx_q", idx_q, a.num_idx_heads), ("idx_k", idx_k, a.num_idx_heads))
+        for name, t, heads in rows:
+            if t is not None and tuple(t.shape[:2]) != (T, heads):
+                raise ValueError(f"{name} is not [{T}, {heads}, 128]")
+        a.num_tokens = T
+        a.q, a.q_stride = bsp._head_rows("q", q, s)
+        a.k, a.k_stride = bsp._head_rows("k", k, s)
+        a.v, a.v_stride = bsp._head_rows("v", v, s)
+        a.idx_q, a.idx_q_stride = bsp._head_rows("idx_q", idx_q, s)
+        a.idx_k, a.idx_k_stride = bsp._head_rows("idx_k", idx_k, s)
+        a.positions = bsp._dense("positions", positions, torch.int32, s, T)
+        a.slot = bsp._dense("slot", slot, torch.int64, s, T)
+        a.q_out = self.q_out.data_ptr()
+        a.idx_q_out = self.idx_q_out.data_ptr() if idx_q is not None and self.idx_q_out is not None else None
+        bsp.norm_rope_write(a, s)
+        return self.q_out[:T], self.idx_q_out[:T] if a.idx_q_out else None
+
+
+def rope_table(positions, rot_dim, theta=10000.0, device="cuda"):
+    """fp32 [positions, rot_dim]: cosines, then sines, of P * theta^(-2i/rot_dim)
+    (angles in fp64: at far positions fp32 ones would be off by whole turns' parts)."""
+    h = rot_dim // 2
+    inv = float(theta) ** (-torch.arange(h, dtype=torch.float64, device=device) / h)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+class DenseStep:
+    """One step of a layer without an indexer over an MXFP4 cache, from the
+    requests' lengths to the attention output: the step's tables, norms and
+    rotation with the cache write, row lengths, dense attention.  Every
+    request brings q_len tokens (1..8) or none; batches padded to num_seqs
+    have requests of context 0 and no tokens."""
+
+    def __init__(self, kv, num_q_heads, num_seqs, q_len, bt_stride, sm_scale=None, q_dtype=bsp.FP8_E4M3,
+                 device="cuda", **norm):
+        tokens = num_seqs * q_len
+        self.kv, self.q_len, self.num_q_heads, self.sm_scale, self.q_dtype = kv, q_len, num_q_heads, sm_scale, q_dtype
+        self.tables = StepTables(num_seqs, bt_stride, tokens, kv.num_blocks, device=device)
+        self.norm = NormRopeWrite(kv, None, num_q_heads, tokens, q_dtype=q_dtype, device=device, **norm)
+        rows = tokens * kv.num_kv_heads
+        self.row_seq = torch.empty(rows, dtype=torch.int32, device=device)
+        self.row_len = torch.empty(rows, dtype=torch.int32, device=device)
+        self.ws = bsp.dense_pa_workspace(rows, kv.num_kv_heads, num_q_heads // kv.num_kv_heads, q_len, device)
+        self.out = torch.empty(tokens, num_q_heads, 128, dtype=torch.bfloat16, device=device)
+        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def run(self, context_lens, new_lens, free_blocks, free_head, q, k, v, stream=None):
+        """Lengths and free blocks as in StepTables.run; q, k, v bf16 rows of
+        the step's tokens (num_seqs * q_len rows, pad rows last).  Returns the
+        attention output; a request's rows are consecutive from
+        tables.cu_tokens, pad rows are zero."""
+        t = self.tables.run(context_lens, new_lens, free_blocks, free_head, stream=stream)
+        qr, _ = self.norm.run(q, k, v, None, None, t.query_abs_pos, t.slot, stream=stream)
+        bsp.row_lengths_prefill(t.query_req_id, t.query_abs_pos, self.kv.num_kv_heads, self.row_seq, self.row_len,
+                                stream=stream)
+        return bsp.dense_pa_decode(self.kv, qr, self.q_dtype, self.num_q_heads, t.block_table, self.row_seq,
+                                   self.row_len, self.q_len, sm_scale=self.sm_scale, out=self.out, ws=self.ws,
+                                   dev_err=self.dev_err, stream=stream)

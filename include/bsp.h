@@ -23,6 +23,13 @@
  *       -> bsp_topk_select -> bsp_sparse_pa_decode / bsp_sparse_pa_prefill
  * and bsp_sparse_decode_step runs it as one call.
  *
+ * Around it: bsp_step_tables builds a step's block table, slot map and
+ * positions on the GPU; bsp_norm_rope_write norms, rotates and stores the
+ * projections' rows (in place of bsp_kv_page_write, which takes rows that are
+ * normed and rotated already); bsp_dense_pa_decode attends over a whole
+ * MXFP4 cache, for layers without an indexer; bsp_kv_page_read gathers
+ * cached tokens back as bf16.
+ *
  * Conventions shared by every call
  *  - Fixed sizes: 128-token blocks, 16-token pages, 8 pages per block side,
  *    head_dim 128 (the index key dim is 128 too).  Query heads per KV head
@@ -90,6 +97,8 @@ typedef enum {
 #define BSP_DEVERR_GROUP_SEQ 4    /* rows of one query group name different sequences */
 #define BSP_DEVERR_TIMEOUT 8      /* a bounded wait for a TMA copy gave up */
 #define BSP_DEVERR_SLOT 16        /* a slot beyond the cache */
+#define BSP_DEVERR_CAPACITY 32    /* a step that does not fit: tokens, block-table rows or free blocks ran out */
+#define BSP_DEVERR_POSITION 64    /* a position beyond the rotation table */
 
 /* top-k flags */
 #define BSP_FORCE_TAIL 1 /* the tail page of every row is always selected */
@@ -426,6 +435,162 @@ typedef struct bsp_decode_step_args {
 } bsp_decode_step_args;
 
 bsp_status bsp_sparse_decode_step(const bsp_decode_step_args* a, bsp_event_t* events, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsp_step_tables -- the paged bookkeeping of one step from the requests'
+ * lengths: the block table extended by the step's fresh blocks, and for every
+ * token its slot, request and position.  With B(n) = ceil(n / 128):
+ *   block_table[s][B(context_s) + i] = free_blocks[*free_head + F_s + i],
+ *       i < B(context_s + new_s) - B(context_s), F_s = the fresh blocks of
+ *       requests before s (the free list is taken from the front, in order);
+ *       entries below B(context_s) are read, all others left as they are
+ *   seq_lens[s]  = context_s + new_s
+ *   cu_tokens[s] = sum of new_r, r < s (num_seqs + 1 entries, at most token_capacity)
+ *   token t in [cu_tokens[s], cu_tokens[s+1]): position P = context_s + t - cu_tokens[s],
+ *       query_req_id = s, query_abs_pos = P, slot = block_table[s][P/128]*128 + P%128
+ *   token t in [cu_tokens[num_seqs], token_capacity), a pad row of a batch
+ *       padded to a captured size: slot -1, query_req_id 0, query_abs_pos -1
+ *       (row length 0 in bsp_row_lengths_prefill, skipped by the writers)
+ *   *blocks_taken = fresh blocks of the step (the caller advances its head)
+ * Negative lengths count as 0; sums saturate at 2^31 - 1.  A step that does
+ * not fit sets BSP_DEVERR_CAPACITY: tokens at or past token_capacity are left
+ * out, tokens past a request's bt_stride blocks and tokens whose block the
+ * free list (num_free ids) does not have get slot -1, and such a table entry
+ * -1.  Ids outside [0, num_blocks), free or in the table, set
+ * BSP_DEVERR_BLOCK_ID and count as absent.
+ * One launch.  Outputs must not overlap inputs or each other (else
+ * BSP_ERR_INVALID_ARG); num_seqs <= 65536 (else BSP_ERR_UNSUPPORTED).
+ * ---------------------------------------------------------------------- */
+typedef struct bsp_step_tables_args {
+  const int32_t* context_lens; /* [num_seqs] tokens in the cache before the step */
+  const int32_t* new_lens;     /* [num_seqs] tokens of the step */
+  int32_t num_seqs;
+  int32_t bt_stride;
+  int32_t* block_table;        /* [num_seqs, bt_stride], in and out */
+  const int32_t* free_blocks;  /* [num_free] */
+  const int32_t* free_head;    /* device scalar, or NULL: 0 */
+  int32_t num_free;
+  int32_t token_capacity;      /* rows of the three per-token outputs */
+  int64_t num_blocks;          /* blocks of the cache */
+  int32_t* seq_lens;           /* [num_seqs] */
+  int32_t* cu_tokens;          /* [num_seqs + 1] */
+  int32_t* blocks_taken;       /* [1] */
+  int64_t* slot;               /* [token_capacity] */
+  int32_t* query_req_id;       /* [token_capacity] */
+  int32_t* query_abs_pos;      /* [token_capacity] */
+  int32_t* dev_err;
+} bsp_step_tables_args;
+
+bsp_status bsp_step_tables(const bsp_step_tables_args* a, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsp_norm_rope_write -- the projections' rows normed per head, rotated by
+ * position and stored, in one pass ([ATOM-2962] commit "... index key": the
+ * fused writer).  For each head x[128] of q, k, idx_q and idx_k
+ *   y_d = x_d / sqrt(mean(x^2) + eps) * (weight_d + weight_offset)
+ *   the first rot_dim dims turn by the angles of the token's position: pairs
+ *   (i, i + rot_dim/2), or (2i, 2i+1) with rope_pairs,
+ *   (y_a, y_b) <- (y_a cos_i - y_b sin_i, y_b cos_i + y_a sin_i)
+ * in fp32; v is stored as it is.  q and idx_q go to q_out and idx_q_out (bf16,
+ * or e4m3 by the unit-scale saturating cast); k to k_out (bf16) and, with v,
+ * to the K/V cache; idx_k to the index cache, in the encodings of
+ * bsp_kv_page_write.  Every output is rounded once, from fp32: the cached
+ * bytes can differ by a step from those of bsp_kv_page_write on rows that
+ * were rounded to bf16 first.
+ *  - Inputs bf16, head h of token t at base + t*stride + h*128 (strides in
+ *    elements, multiples of 8, >= heads*128: the parts of one fused
+ *    projection row may be given as they lie).  Any of q, idx_q, idx_k may be
+ *    NULL, and k and v together; k without v needs kv NULL.
+ *  - Weights bf16 [128], or NULL: factor 1 (weight_offset then unused).
+ *  - rope_table fp32 [rope_rows, rot_dim]: row P holds the rot_dim/2 cosines,
+ *    then the rot_dim/2 sines, of position P.  rot_dim 0 or a multiple of 16
+ *    up to 128 (else BSP_ERR_UNSUPPORTED); 0: no rotation, the table unused.
+ *  - positions int32 [T] (may be NULL when rot_dim is 0).  A negative
+ *    position is a pad row: its outputs are zeros and nothing is cached.  A
+ *    position >= rope_rows sets BSP_DEVERR_POSITION and counts as a pad row.
+ *  - slot int64 [T] as in bsp_kv_page_write (negative: not cached); needed
+ *    with kv or idx.  The same slot twice in a call: one of the rows is kept.
+ *  - q_out, k_out and idx_q_out are dense [T, heads, 128].  A bf16 output may
+ *    be its own dense input; any other overlap of an output with an input or
+ *    another output is BSP_ERR_INVALID_ARG.  The inputs must be device memory.
+ * One launch.
+ * ---------------------------------------------------------------------- */
+typedef struct bsp_norm_rope_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* idx_q;
+  const void* idx_k;
+  int64_t q_stride, k_stride, v_stride, idx_q_stride, idx_k_stride;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;  /* = kv->num_kv_heads with kv */
+  int32_t num_idx_heads; /* = idx->num_heads with idx */
+  const void* q_weight;
+  const void* k_weight;
+  const void* idx_q_weight;
+  const void* idx_k_weight;
+  float weight_offset;
+  float eps;
+  const float* rope_table;
+  int64_t rope_rows;
+  int32_t rot_dim;
+  int32_t rope_pairs;
+  const int32_t* positions;
+  const int64_t* slot;
+  void* q_out;
+  void* k_out;
+  void* idx_q_out;
+  int32_t q_out_dtype;     /* BSP_BF16 or BSP_FP8_E4M3 */
+  int32_t idx_q_out_dtype;
+  const bsp_kv_cache* kv;
+  const bsp_index_cache* idx;
+  int32_t* dev_err;
+} bsp_norm_rope_args;
+
+bsp_status bsp_norm_rope_write(const bsp_norm_rope_args* a, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsp_kv_page_read -- cached tokens gathered by slot as bf16 rows, the
+ * writer's inverse ([ATOM-2962] dequantize_pages):
+ *   k, v   bf16 [T, Hkv, 128], both or neither (then kv may be NULL)
+ *   idx_k  bf16 [T, idx->num_heads, 128], or NULL (then idx may be NULL)
+ *   slot   int64 [T]: block*128 + offset; negative gives a row of zeros, one
+ *          beyond the cache too, and sets BSP_DEVERR_SLOT
+ * fp8 values are e4m3 * scale in fp32, rounded to bf16; MXFP4 values are
+ * exact in bf16 (scale bytes 255 are never written).
+ * ---------------------------------------------------------------------- */
+bsp_status bsp_kv_page_read(const bsp_kv_cache* kv, const bsp_index_cache* idx, const int64_t* slot,
+                            int32_t num_tokens, void* k, void* v, void* idx_k, int32_t* dev_err,
+                            bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsp_dense_pa_decode -- grouped-query attention of each row over its whole
+ * context in an MXFP4 cache (layers without an indexer; contexts of any
+ * length the block table covers):
+ *   out = softmax(sm_scale * q K^T) V over tokens t < L_r, token t at offset
+ *         t % 128 of block block_table[row_seq[r]][t / 128]
+ *   kv    an MXFP4 cache (else BSP_ERR_UNSUPPORTED)
+ *   q     [tokens, Hkv*G, 128], bf16 or e4m3 (q_dtype); out bf16, the same shape
+ *   block_table int32 [*, bt_stride]; row_seq, row_len int32 [rows], rows =
+ *         tokens * Hkv; L_r is clamped to [0, 128 * bt_stride]; a row with
+ *         L_r = 0 gets zeros
+ *   q_group 1..8 as in bsp_index_score: consecutive tokens that share a
+ *         sequence; the cache is streamed once per group and KV head.  Rows of
+ *         a group that name another sequence set BSP_DEVERR_GROUP_SEQ and are
+ *         computed with the first row's.
+ * A block id out of range sets BSP_DEVERR_BLOCK_ID and its tokens are left
+ * out.  Bytes at and past L_r are never used, whatever they hold.
+ * ws: device workspace of bsp_dense_pa_workspace_bytes() bytes, 16-byte
+ * aligned (its contents need not be set, and carry nothing from call to
+ * call).  Calls that may overlap on the GPU, captured ones included, need
+ * workspaces of their own.  The same inputs give the same bits.
+ * ---------------------------------------------------------------------- */
+size_t bsp_dense_pa_workspace_bytes(int32_t num_rows, int32_t num_kv_heads, int32_t group, int32_t q_group);
+bsp_status bsp_dense_pa_decode(const bsp_kv_cache* kv, const void* q, int32_t q_dtype, int32_t num_q_heads,
+                               const int32_t* block_table, int32_t bt_stride, const int32_t* row_seq,
+                               const int32_t* row_len, int32_t num_rows, int32_t q_group, float sm_scale, void* out,
+                               void* ws, size_t ws_bytes, int32_t* dev_err, bsp_stream_t stream);
 
 /* ---- misc -------------------------------------------------------------- */
 const char* bsp_status_str(bsp_status s);
