@@ -575,6 +575,8 @@ bsp_status bsp_dense_pa_decode(const bsp_kv_cache* kv, const void* q, int32_t q_
   if (num_q_heads % kv->num_kv_heads || num_rows % kv->num_kv_heads) return BSP_ERR_INVALID_ARG;
   const int32_t group = num_q_heads / kv->num_kv_heads;
   if (!valid_group(group) || q_group < 1 || q_group > 8) return BSP_ERR_UNSUPPORTED;
+  // the keys' 4-bit tensor copies
+  if (!al(kv->k_base, 32) || kv->id_stride_bytes % 32) return BSP_ERR_UNSUPPORTED;
   if (!(sm_scale - sm_scale == 0.f)) return BSP_ERR_INVALID_ARG;  // infinite or NaN
   if (num_rows == 0) return BSP_OK;
   if (!q || !block_table || !row_seq || !row_len || !out || !al(q, 16) || !al(out, 16) || !al(block_table, 4) ||

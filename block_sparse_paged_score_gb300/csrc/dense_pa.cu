@@ -6,35 +6,43 @@
 //
 // with k4, v4 the e2m1 values, e the e8m0 bytes of the four 32-dim groups c.
 //
-// Unit = (query group, KV head): its rows, q_group tokens times G heads, share
-// every byte of the cache.  The units' 128-token blocks laid end to end are
-// cut into equal shares, one per resident CTA, so ragged batches load every SM
-// alike; a CTA finds its share by a prefix sum over the groups' lengths.  A
-// unit that lies in one share is written at once; of a unit cut by share
-// borders each CTA leaves (m, l, O) in the workspace, and a second kernel joins
-// them (it reads a list of cut units, no counters, so the workspace carries
-// nothing from call to call and the sums' order is fixed).
+// Work.  A unit = (query group, KV head, at most 64 rows): its rows, tokens
+// times G heads, share every byte of the cache.  The units' 128-token blocks
+// laid end to end are cut into equal shares, one per resident CTA, so ragged
+// batches load every SM alike; a CTA finds its share by a prefix sum over the
+// groups' lengths.  A unit that lies in one share is written at once; of a
+// unit cut by share borders each CTA leaves (m, l, O) in the workspace, and a
+// second kernel joins them (it reads a list of cut units, no counters: the
+// workspace carries nothing from call to call and the sums' order is fixed).
 //
-// A warp takes 32 tokens (a slice) at a time.  Slices arrive by TMA in a ring
-// of each team's own: 2 KB of K and of V by tensor copies with the 64-byte
-// swizzle (ldmatrix rows are 64 bytes apart; without it four would share a
-// bank), 128 B of each side's scales by plain bulk copies.  The warps of a team
-// hold different rows (MT tiles of 16) and read the same slice.
+// A CTA is one producer warp and 4 * sets compute warps; each set has 16 rows.
+//   - The producer loads blocks by TMA (K unpacked to one byte slot a value,
+//     the layout the tensor core reads; V packed, 64-byte swizzle; the scales
+//     as they lie) and issues, per block, four tcgen05.mma block-scaled by the
+//     cache's own e8m0 bytes: z^T = K Q^T, M = 128 tokens, N = 16 * sets rows,
+//     K = 32 = one scale group each, in TMEM, double-buffered.  Row 32j + i of
+//     the tile is token 4i + j (a tensor-map order): then the 512 scale bytes
+//     are, as they lie in the cache, the cells tcgen05.cp wants.  A bf16 query is
+//     the sum of two e4m3 parts (see stage_q), eight MMAs.
+//   - A compute warp reads 32 tokens x 16 rows of z^T (thread = token), takes
+//     the exponentials, turns the f16 weights around through shared memory
+//     into mma A fragments and multiplies by V: mma.sync m16n8k16 f16.  V
+//     comes through ldmatrix.trans as four nibbles of two tokens a register;
+//     bit moves turn them into f16 pairs, times 2^-14 exactly.  V's scales go
+//     onto P: 2^(ev - R_c), a power of two at most 1, multiplies the weights of
+//     each group.  R_c is the largest scale byte so far (O is rescaled when it
+//     grows).  Tokens whose scale is 15 or more binades below R_c, which f16
+//     could not hold, make the warp take its tokens again in bands of 15.
+//   - p is f16, at most half a step, 2^-11, off; weights are kept times 2^7 so
+//     that f16's range, down to 2^-25, reaches 2^-32 of the largest.
+// tcgen05 takes the scores because it reads e2m1 and the scales itself: on
+// mma.sync the conversions of K cost more issue slots than all else.  PV stays
+// on mma.sync: with V^T as A its dequantised tile would have to go through
+// shared memory, 32 KB written and read a block, more than a block's time at
+// the memory's rate.
 //
-//   z: mma.sync m16n8k32 e4m3, one k-step per scale group into accumulators of
-//      its own, multiplied by the token's scale as it is added to z.  e2m1
-//      bits moved under the e4m3 exponent are the value times 2^-6, exactly,
-//      so four ALU operations convert four values.  A bf16 query is the sum of
-//      two e4m3 parts, each with its own power of two (see stage_q).
-//   o: mma.sync m16n8k16 f16.  V's bytes come through ldmatrix.trans as four
-//      nibbles of two neighbouring tokens a register, which bit moves turn into
-//      f16 pairs, times 2^-14 exactly.  V's scales go onto P: 2^(ev - R_c), a
-//      power of two at most 1, multiplies the f16 weights of each group.  R_c
-//      is the largest scale byte so far (O is rescaled when it grows).  Tokens
-//      whose scale is 15 or more binades below R_c, which f16 could not hold,
-//      make the warp take the slice again in bands of 15 binades.
-//   p is f16: at most half a step, 2^-11, off; weights are kept times 2^7 so that
-//      the f16 range, down to 2^-25, reaches 2^-32 of the largest.
+// Every wait is bounded; after a timed-out wait a role waits no more (the
+// error word is set) and the CTA frees its TMEM and returns.
 #include <algorithm>
 
 #include "common.cuh"
@@ -46,75 +54,100 @@ namespace bsp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kSlice = 32;
-constexpr int kStages = 2;             // slices in flight per team
-constexpr int kTileBytes = kSlice * 64;  // one side of a slice
-constexpr int kRowPad = kDim + 4;      // floats of a row in the teams' merge area
-constexpr float kMaxGrow = 8.f;        // the reference maximum moves when a row's maximum grows by more (log2)
-constexpr float kBias = 7.f;           // weights are 2^(z - m + kBias)
-constexpr float kNoMax = -1e30f;       // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
-constexpr int kBand = 15;              // binades a band of V scales spans
-
-// rows of a unit split over the CTA's warps: `sets` warps of MT tiles make a
-// team, `teams` teams share the slices
-struct Shape {
-  int mt, sets, teams;
-  __host__ __device__ int warps() const { return sets * teams; }
-  __host__ __device__ int rows() const { return sets * mt * 16; }
-};
-__host__ __device__ inline Shape shape_of(int rows) {
-  if (rows <= 16) return {1, 1, 4};
-  const int sets = (rows + 31) / 32;
-  return {2, sets, sets <= 2 ? 4 : 2};
-}
+constexpr int kMaxRows = 64;       // rows of a unit
+constexpr int kKStages = 2, kVStages = 3;
+constexpr int kKTile = kBlock * 128;  // unpacked keys of a block
+constexpr int kVTile = kBlock * 64;   // packed values of a block
+constexpr int kRowPad = kDim + 4;  // floats of a row in the merge buffer
+constexpr float kMaxGrow = 8.f;    // the reference maximum moves when a row's maximum grows by more (log2)
+constexpr float kBias = 7.f;       // weights are 2^(z - m + kBias)
+constexpr float kNoMax = -1e30f;   // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
+constexpr int kBand = 15;          // binades a band of V scales spans
+constexpr int kQueue = 8;          // blocks the producer knows ahead
 
 // bytes of the list of cut units at the start of the workspace
 __host__ __device__ constexpr int64_t list_bytes(int64_t ctas) { return (ctas * 8 + 255) / 256 * 256; }
 
 struct Params {
   DensePaParams a;
-  float qk_scale;  // sm_scale * log2(e) * 2^6 (K's exponent shift)
-  int32_t groups, units, ctas, sets, teams;
+  float qk_scale;  // sm_scale * log2(e)
+  int32_t groups, subs, sub_tokens;  // query groups; units a group and head is cut into, of sub_tokens tokens
+  int32_t units, ctas;
   int32_t by_unit;  // the list of cut units has an entry per unit (else per CTA)
 };
 
 // ---- shared memory -----------------------------------------------------------
-struct Layout {
-  int scales, merge_ml, q, scratch, bars, bad, total;
+// per compute warp: P [32 tokens][16 rows] f16, V's scales [4][16 pairs] f16x2,
+// reference maxima and rescale factors of 16 rows; the sets' merge buffers
+// take the same place once a unit's blocks are done
+constexpr int kScratch = 1024 + 256 + 64 + 64;
+template <int SETS>
+struct Smem {
+  static constexpr int kCompute = 4 * SETS;
+  static constexpr int kThreads = 32 * (kCompute + 1);
+  static constexpr int kRows = 16 * SETS;
+  static constexpr int kMerge = 16 * kRowPad * 4 + 128;  // a set's O, m, l
+  static constexpr int v = kKStages * kKTile;
+  static constexpr int ks = v + kVStages * kVTile;  // K scales, with K's stages
+  static constexpr int vs = ks + kKStages * 512;
+  static constexpr int scratch = vs + kVStages * 512;
+  static constexpr int scratch_bytes = std::max(kCompute * kScratch, SETS * kMerge);
+  static constexpr int len = scratch + scratch_bytes;  // [rows] lengths
+  static constexpr int sfq = len + kRows * 4;          // [2][rows] scale cells of q
+  static constexpr int bars = sfq + 2 * kRows * 4;
+  static constexpr int queue = bars + 20 * 8;
+  static constexpr int q = (queue + kQueue * 8 + 16 + 1023) / 1024 * 1024;
+  static constexpr int total(bool q16) { return q + kRows * 128 * (q16 ? 2 : 1) + 1024; }
 };
-__host__ __device__ inline Layout layout(const Shape& s, bool q16) {
-  Layout l;
-  const int ring = s.teams * kStages;
-  l.scales = ring * 2 * kTileBytes;
-  const int ring_bytes = l.scales + ring * 256;
-  l.merge_ml = s.warps() * s.mt * 16 * kRowPad * 4;
-  const int merge_bytes = l.merge_ml + s.warps() * s.mt * 16 * 8;
-  l.q = (std::max(ring_bytes, merge_bytes) + 127) / 128 * 128;
-  l.scratch = l.q + s.rows() / 16 * 4 * 512 * (q16 ? 2 : 1) + s.rows() * 4;
-  l.bars = l.scratch + s.warps() * 768;
-  l.bad = l.bars + 2 * ring * 8;
-  l.total = l.bad + ring * 4 + 1024;  // slack: the tiles start on 1024 bytes
-  return l;
-}
 
 // ---- device helpers ------------------------------------------------------------
-__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* m, int row, int block, uint64_t* bar) {
+__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* m, int head, int block, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(dst)),
-      "l"(m), "r"(0), "r"(row), "r"(block), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(0), "r"(head), "r"(block), "r"(smem_u32(bar))
       : "memory");
+}
+// 512 bytes (32 rows of 16) to four TMEM columns of every 32-lane sub-partition
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
+  uint64_t d = (saddr & 0x3FFFF) >> 4;            // start address
+  d |= static_cast<uint64_t>(128 >> 4) << 16;     // leading byte offset (one core matrix wide: unused)
+  d |= static_cast<uint64_t>(128 >> 4) << 32;     // 8-row core matrices 128 bytes apart
+  d |= static_cast<uint64_t>(1) << 46;            // descriptor version; no swizzle
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
-__device__ __forceinline__ void mma_e4m3_zero(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float4 lds128f(uint32_t addr) {
+  const uint4 v = lds128(addr);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void stsf(uint32_t addr, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ float ldsf(uint32_t addr) { return __uint_as_float(lds32(addr)); }
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   uint64_t x, y, z, r;
@@ -126,15 +159,19 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
   return o;
 }
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t x, y, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-// eight e2m1 nibbles -> e4m3 bytes of the even (b0) and odd (b1) nibbles, times 2^-6
-__device__ __forceinline__ void e2m1x8_to_e4m3(uint32_t w, uint32_t& b0, uint32_t& b1) {
-  b0 = ((w << 4) & 0x80808080u) | ((w << 2) & 0x1C1C1C1Cu);
-  b1 = (w & 0x80808080u) | ((w >> 2) & 0x1C1C1C1Cu);
 }
 // four nibbles of token a (low half) and of token b (high half) -> f16x2
 // (a_i, b_i) times 2^-14: sign to bit 15, the three magnitude bits under the exponent
@@ -146,566 +183,703 @@ __device__ __forceinline__ void e2m1x4x2_to_f16x2(uint32_t z, uint32_t (&v)[4]) 
   v[2] = even & 0xFF00FF00u;
   v[3] = odd & 0xFF00FF00u;
 }
-// 2^e for any e (two factors, each a normal float, where one would overflow)
+// x * 2^e for any e (two factors, each a normal float, where one would overflow)
 __device__ __forceinline__ float scale_pow2(float x, int e) {
   const int a = max(-126, min(127, e)), b = max(-126, min(127, e - a));
   return x * __uint_as_float(static_cast<uint32_t>(a + 127) << 23) * __uint_as_float(static_cast<uint32_t>(b + 127) << 23);
 }
+// largest of the warp's values
+__device__ __forceinline__ float warp_max(float x) {
+  const int b = __float_as_int(x), k = b ^ ((b >> 31) & 0x7FFFFFFF);  // ordered as integers
+  const int m = __reduce_max_sync(0xffffffffu, k);
+  return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
+}
 
-// one warp's running softmax over MT tiles of 16 rows (rows g and g + 8 of a
-// tile in a thread)
-template <int MT>
-struct State {
-  float o[MT][16][4];  // tile 4c + i: dims 32c + 8t + i and 32c + 8t + 4 + i
-  float m[MT][2], l[MT][2];
-  uint32_t r;  // R_c: the largest V scale byte so far, group c in byte c
-};
-
+// ---- units ---------------------------------------------------------------------
 // blocks of group g: the longest of its rows, at least one (an empty unit
 // still writes its zeros)
-__device__ __forceinline__ int group_blocks(const DensePaParams& a, int g) {
-  const int tokens = a.num_rows / a.hkv;
-  const int64_t r0 = static_cast<int64_t>(g) * a.q_group * a.hkv;
-  const int n = min(a.q_group, tokens - g * a.q_group) * a.hkv;
+__device__ __forceinline__ int blocks_of(const DensePaParams& a, int len) {
+  return static_cast<int>(max(1u, min((static_cast<uint32_t>(len) + 127u) / 128u, static_cast<uint32_t>(a.bt_stride))));
+}
+__device__ __forceinline__ int group_len(const DensePaParams& a, int g, int first, int step) {
+  const int64_t tok0 = static_cast<int64_t>(g) * a.q_group;
+  const int n = static_cast<int>(min(static_cast<int64_t>(a.q_group), a.num_rows / a.hkv - tok0)) * a.hkv;
   int len = 0;
-  for (int i = 0; i < n; ++i) len = max(len, a.row_len[r0 + i]);
-  return max(1, min((len + 127u) / 128u, static_cast<uint32_t>(a.bt_stride)));
+  for (int i = first; i < n; i += step) len = max(len, a.row_len[tok0 * a.hkv + i]);
+  return len;
 }
 
-// q of a unit as mma A fragments: [tile][group c][lane] of 16 bytes, thread
-// (g, t) rows g, g + 8 and dims 32c + 8t + (0,2,4,6 | 1,3,5,7), the order in
-// which the K conversion hands out its nibbles.  A bf16 row is scaled by 2^-a,
-// its largest magnitude then in [128, 256), and split: hi = e4m3(x), lo =
-// e4m3((x - hi) * 2^4).  bf16 has 8 significant bits and each part 4, so the sum is exact
-// for elements down to 2^-13 of the row's largest and off by at most 2^-21 of it below.  The row's 2^a goes to row_scale.
+// A warp's walk over the pieces of a share [at, end) of the units' blocks.
+// Every lane holds the same values.
+struct Walk {
+  int64_t at, end, c0;  // c0: blocks of the groups before g
+  int g, nb;
+  // the piece at `at`
+  int unit, h, tok0, tokens, seq, b0, b1, max_len, min_len, len;  // len: of the lane's token
+  bool starts, ends;  // the unit's first and last blocks are in the piece
+
+  __device__ __forceinline__ bool next(const Params& p, int lane) {
+    if (at >= end) return false;
+    const DensePaParams& a = p.a;
+    const int64_t per = static_cast<int64_t>(a.hkv) * p.subs;
+    while ((c0 + nb) * per <= at) {
+      c0 += nb;
+      ++g;
+      nb = blocks_of(a, __reduce_max_sync(0xffffffffu, group_len(a, g, lane, 32)));
+    }
+    const int x = static_cast<int>((at - c0 * per) / nb);
+    const int64_t ustart = c0 * per + static_cast<int64_t>(x) * nb, uend = ustart + nb;
+    unit = static_cast<int>(g * per + x);
+    h = x / p.subs;
+    const int sub = x % p.subs;
+    const int gtok = g * a.q_group;
+    tok0 = gtok + sub * p.sub_tokens;
+    tokens = min(min(p.sub_tokens, a.q_group - sub * p.sub_tokens), a.num_rows / a.hkv - tok0);
+    seq = a.row_seq[static_cast<int64_t>(gtok) * a.hkv];
+    const int cap = static_cast<int>(min(static_cast<int64_t>(a.bt_stride) * kBlock, int64_t{0x7FFFFFFF}));
+    len = 0;
+    if (lane < tokens) len = min(max(a.row_len[static_cast<int64_t>(tok0 + lane) * a.hkv + h], 0), cap);
+    max_len = __reduce_max_sync(0xffffffffu, len);
+    min_len = __reduce_min_sync(0xffffffffu, lane < tokens ? len : 0x7FFFFFFF);
+    if (tokens <= 0) max_len = 0;  // the last group may lack this unit's tokens
+    b0 = static_cast<int>(at - ustart);
+    b1 = min(static_cast<int>(min(end, uend) - ustart), (max_len + 127) >> 7);
+    starts = at == ustart, ends = end >= uend;
+    at = min(end, uend);
+    return true;
+  }
+};
+
+// q of a unit in shared memory as the MMA reads it (rows of 128 e4m3 bytes,
+// 128-byte swizzle), with its scale cells: thread = 16-byte chunk j of row n.
+// e4m3 queries are copied, scales 1.  Of a bf16 row each 32-dim group is scaled
+// by 2^-a, its largest magnitude then in [128, 256), and split: hi = e4m3(x), lo
+// = e4m3((x - hi) * 2^4), multiplied by 2^a and 2^(a-4) in the MMAs.  bf16 has 8
+// significant bits and each part 4, so the sum is exact for elements down to
+// 2^-13 of the group's largest, and off by at most 2^-21 of it below.
 template <bool Q16>
-__device__ __forceinline__ void stage_q(const DensePaParams& a, int tok0, int tokens, int h, uint8_t* qs, int rows,
-                                        int tid, int threads) {
-  float* row_scale = reinterpret_cast<float*>(qs + rows / 16 * 4 * 512 * (Q16 ? 2 : 1));
+__device__ __forceinline__ void stage_q(const DensePaParams& a, int tok0, int tokens, int h, uint8_t* q, int rows,
+                                        uint8_t* cells, int tid) {
+  const int n = tid >> 3, j = tid & 7;
   const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
-  // a quad of lanes per (row, group c): lane t of it owns dims 32c + 8t..+7
-  for (int i = tid; i < rows * 16; i += threads) {
-    const int row = i >> 4, c = (i >> 2) & 3, t = i & 3;
-    const int j = row / a.group, hh = row % a.group;
-    const bool live = j < tokens;
-    const int64_t e = ((tok0 + j) * hq + static_cast<int64_t>(h) * a.group + hh) * kDim + 32 * c + 8 * t;
-    const int g = row & 7, half = (row >> 3) & 1;
-    uint8_t* dst = qs + (((row >> 4) * 4 + c) * 32 + g * 4 + t) * 16 + half * 4;
-    if (Q16) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (live) w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + e);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-      float x[8], top = 0.f;
+  const bool live = n / a.group < tokens;
+  const int64_t e = ((tok0 + n / a.group) * hq + static_cast<int64_t>(h) * a.group + n % a.group) * kDim + 16 * j;
+  uint8_t* dst = q + n * 128 + ((j ^ (n & 7)) << 4);
+  if (!Q16) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (live) w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + e);
+    *reinterpret_cast<uint4*>(dst) = w;
+    if (!(j & 1)) cells[n * 4 + (j >> 1)] = 127;
+    return;
+  }
+  uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (live) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + e);
+    w[0] = src[0], w[1] = src[1];
+  }
+  const uint32_t ws[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+  float x[16], top = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[k] = bf16_bits_to_float(k & 1 ? ws[k >> 1] >> 16 : ws[k >> 1] & 0xFFFF);
-        top = fmaxf(top, fabsf(x[k]));
-      }
-      // the row's 16 lanes are one half-warp
+  for (int k = 0; k < 16; ++k) {
+    x[k] = bf16_bits_to_float(k & 1 ? ws[k >> 1] >> 16 : ws[k >> 1] & 0xFFFF);
+    top = fmaxf(top, fabsf(x[k]));
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the group's other chunk
+  const int ex = max(-110, static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127) - 7;
+  uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int m = 1; m < 16; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-      const int ex = max(-110, static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127) - 7;  // 2^ex * [128, 256)
-      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+  for (int k = 0; k < 16; k += 4) {
+    uint32_t hb[2], lb[2];
 #pragma unroll
-      for (int k = 0; k < 8; k += 4) {
-#pragma unroll
-        for (int par = 0; par < 2; ++par) {  // par 0: even dims, 1: odd
-          const float u = scale_pow2(x[k + par], -ex), v = scale_pow2(x[k + 2 + par], -ex);
-          const uint32_t hb = float2_to_e4m3x2(u, v);
-          const uint32_t lb = float2_to_e4m3x2((u - e4m3_to_float(hb)) * 16.f, (v - e4m3_to_float(hb >> 8)) * 16.f);
-          hi[par] |= hb << (8 * (k >> 1));
-          lo[par] |= lb << (8 * (k >> 1));
-        }
-      }
-      *reinterpret_cast<uint32_t*>(dst) = hi[0];
-      *reinterpret_cast<uint32_t*>(dst + 8) = hi[1];
-      uint8_t* dl = dst + rows / 16 * 4 * 512;
-      *reinterpret_cast<uint32_t*>(dl) = lo[0];
-      *reinterpret_cast<uint32_t*>(dl + 8) = lo[1];
-      if (c == 0 && t == 0) row_scale[row] = scale_pow2(1.f, ex);
-    } else {
-      uint2 w = make_uint2(0, 0);
-      if (live) w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.q) + e);
-      *reinterpret_cast<uint32_t*>(dst) = __byte_perm(w.x, w.y, 0x6420);
-      *reinterpret_cast<uint32_t*>(dst + 8) = __byte_perm(w.x, w.y, 0x7531);
-      if (c == 0 && t == 0) row_scale[row] = 1.f;
+    for (int i = 0; i < 2; ++i) {
+      const float u = scale_pow2(x[k + 2 * i], -ex), v = scale_pow2(x[k + 2 * i + 1], -ex);
+      hb[i] = float2_to_e4m3x2(u, v);
+      lb[i] = float2_to_e4m3x2((u - e4m3_to_float(hb[i])) * 16.f, (v - e4m3_to_float(hb[i] >> 8)) * 16.f);
     }
+    hi[k >> 2] = hb[0] | (hb[1] << 16);
+    lo[k >> 2] = lb[0] | (lb[1] << 16);
+  }
+  *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(dst + rows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  if (!(j & 1)) {
+    cells[n * 4 + (j >> 1)] = static_cast<uint8_t>(ex + 127);
+    cells[(rows + n) * 4 + (j >> 1)] = static_cast<uint8_t>(ex + 123);
   }
 }
 
-// One slice: K, V tiles and scales in shared memory, tokens n0 .. n0 + 31 of
-// the sequence; rows see tokens below len[tile][half] (all zero for a bad block).
-template <int MT, bool Q16>
-__device__ __forceinline__ void slice(State<MT>& st, uint32_t kt, uint32_t vt, const uint8_t* sc, uint32_t qs,
-                                      uint32_t qlo, uint8_t* scratch, int n0, const int (&len)[MT][2], int max_len,
-                                      bool whole, const float (&zs)[MT][2], int lane) {
-  const int t = lane & 3;
-  const uint32_t kp = smem_u32(scratch), vp = kp + 512;
-  // -- scales: lane = token.  Neighbours trade words, so that the even lane
-  // writes groups 0, 1 and the odd one groups 2, 3 of their pair of tokens:
-  // K's as float pairs [c][t][octet], V's as f16 pairs in the same order.
-  const int odd = lane & 1, sh = odd * 16;
-  const uint32_t kw = *reinterpret_cast<const uint32_t*>(sc + 4 * lane);
-  const uint32_t vw = n0 + lane < max_len ? *reinterpret_cast<const uint32_t*>(sc + 128 + 4 * lane) : 0;
-  const uint32_t kx = __shfl_xor_sync(0xffffffffu, kw, 1), vx = __shfl_xor_sync(0xffffffffu, vw, 1);
-  const int cell = ((lane >> 1) & 3) * 4 + (lane >> 3);  // [t][octet]
-  {
-    const uint32_t a = (odd ? kx : kw) >> sh, b = (odd ? kw : kx) >> sh;
-    const uint32_t at = kp + (2 * odd * 16 + cell) * 8;
-    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"((a << 23) & 0x7F800000u), "r"((b << 23) & 0x7F800000u)
-                 : "memory");
-    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + 128), "r"((a << 15) & 0x7F800000u),
-                 "r"((b << 15) & 0x7F800000u)
-                 : "memory");
-  }
-  const uint32_t va = (odd ? vx : vw) >> sh, vb = (odd ? vw : vx) >> sh;  // bytes 0, 1: this lane's groups
-  {
-    const uint32_t rr = st.r >> sh;
-    const bool up = (va & 0xFF) > (rr & 0xFF) || (vb & 0xFF) > (rr & 0xFF) || (va >> 8 & 0xFF) > (rr >> 8 & 0xFF) ||
-                    (vb >> 8 & 0xFF) > (rr >> 8 & 0xFF);
-    if (__any_sync(0xffffffffu, up)) {  // R_c grows: O moves to the new unit
-      uint32_t nr = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t old = st.r >> (8 * c) & 0xFF;
-        const uint32_t now = max(old, __reduce_max_sync(0xffffffffu, vw >> (8 * c) & 0xFF));
-        nr |= now << (8 * c);
-        const float f = scale_pow2(1.f, static_cast<int>(old) - static_cast<int>(now));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st.o[mt][4 * c + i][e] *= f;
-      }
-      st.r = nr;
-    }
-  }
-  // f16 2^(byte - R_c + kBand*band) of this lane's groups and pair, 0 outside the band
-  auto put_vscales = [&](int band) {
-    const uint32_t rr = st.r >> sh;
-    bool low = false;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = rr >> (8 * k) & 0xFF;
-      uint32_t h[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int b = (e ? vb : va) >> (8 * k) & 0xFF;
-        const int x = b - r + kBand * band + 15;  // f16 exponent field: 1..15 within the band
-        h[e] = x > 0 && x <= 15 && b ? x << 10 : 0;
-        low |= b != 0 && x <= 0;
-      }
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(vp + ((2 * odd + k) * 16 + cell) * 4), "r"(h[0] | (h[1] << 16))
-                   : "memory");
-    }
-    return __any_sync(0xffffffffu, low);
-  };
-  bool more = put_vscales(0);
-  __syncwarp();
+// one compute warp's running softmax: O of 16 rows in mma accumulators (tile
+// 4c + i: dims 32c + 8t + i and 32c + 8t + 4 + i of rows g and g + 8), the sums l
+// as a tile of their own (P times ones), and 271 - R_c of groups (0, 2) and (1, 3)
+// in the halves of two words
+struct State {
+  float o[16][4];
+  float l[4];
+  uint32_t r02, r13;
+};
+constexpr uint32_t kHalves = 0x00010001u;
+constexpr uint32_t kNoScale = 271 * kHalves;  // R_c = 0
 
-  // -- z
-  float z[MT][4][4];
-  const int row8 = lane & 7, mat = lane >> 3;
-  const uint32_t row_off = (mat * 8 + row8) * 64;
-  const int swz = (row8 >> 1) & 3;
+// V's scales where some byte is above R_c, zero or 15 binades and more below it:
+// raises R_c (O moves to the new unit), writes band `band`'s f16 scales, and says
+// whether lower ones are left
+__device__ __forceinline__ bool odd_vscales(State& st, uint32_t vw, uint32_t vcell, int band) {
+  const uint32_t rr[4] = {271 - (st.r02 & 0xFFFF), 271 - (st.r13 & 0xFFFF), 271 - (st.r02 >> 16), 271 - (st.r13 >> 16)};
+  uint32_t now[4];
+  bool low = false;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    uint32_t kr[4];
-    ldsm_x4(kr[0], kr[1], kr[2], kr[3], kt + row_off + ((c ^ swz) << 4));
-    const uint4 s01 = lds128(kp + (c * 16 + t * 4) * 8), s23 = lds128(kp + (c * 16 + t * 4) * 8 + 16);
-    const float2 ks[4] = {{__uint_as_float(s01.x), __uint_as_float(s01.y)},
-                          {__uint_as_float(s01.z), __uint_as_float(s01.w)},
-                          {__uint_as_float(s23.x), __uint_as_float(s23.y)},
-                          {__uint_as_float(s23.z), __uint_as_float(s23.w)}};
-    uint4 qa[MT], ql[MT];
+    const uint32_t b = vw >> (8 * c) & 0xFF;
+    now[c] = band ? rr[c] : max(rr[c], __reduce_max_sync(0xffffffffu, b));
+    if (now[c] != rr[c]) {
+      const float f = scale_pow2(1.f, static_cast<int>(rr[c]) - static_cast<int>(now[c]));
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      qa[mt] = lds128(qs + (mt * 4 + c) * 512 + lane * 16);
-      if (Q16) ql[mt] = lds128(qlo + (mt * 4 + c) * 512 + lane * 16);
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[4 * c + i][e] *= f;
     }
-#pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      uint32_t b0, b1;
-      e2m1x8_to_e4m3(kr[o], b0, b1);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float acc[4];
-        if (Q16) {
-          mma_e4m3_zero(acc, ql[mt], b0, b1);
-          const float2 lo = fmul2({acc[0], acc[1]}, {0.0625f, 0.0625f}), hi = fmul2({acc[2], acc[3]}, {0.0625f, 0.0625f});
-          acc[0] = lo.x, acc[1] = lo.y, acc[2] = hi.x, acc[3] = hi.y;
-          mma_e4m3(acc, qa[mt].x, qa[mt].y, qa[mt].z, qa[mt].w, b0, b1);
-        } else {
-          mma_e4m3_zero(acc, qa[mt], b0, b1);
-        }
-        float2 x, y;
-        if (c == 0) {
-          x = fmul2({acc[0], acc[1]}, ks[o]), y = fmul2({acc[2], acc[3]}, ks[o]);
-        } else {
-          x = ffma2({acc[0], acc[1]}, ks[o], {z[mt][o][0], z[mt][o][1]});
-          y = ffma2({acc[2], acc[3]}, ks[o], {z[mt][o][2], z[mt][o][3]});
-        }
-        z[mt][o][0] = x.x, z[mt][o][1] = x.y, z[mt][o][2] = y.x, z[mt][o][3] = y.y;
-      }
+    const int x = static_cast<int>(b) - static_cast<int>(now[c]) + kBand * band + 15;  // f16 exponent field
+    low |= b && x <= 0;
+    sts16(vcell + c * 64, b && x > 0 && x <= 15 ? x << 10 : 0);
+  }
+  st.r02 = kNoScale - (now[0] | (now[2] << 16));
+  st.r13 = kNoScale - (now[1] | (now[3] << 16));
+  return __any_sync(0xffffffffu, low);
+}
+
+// 32 tokens of the warp: their logits are at TMEM address zt (thread = the lane's
+// token n, column = row h, which sees the token if n < lens[h]; whole: every row
+// sees every token); vw the token's V scale bytes (0 where no row sees it), vt the
+// V rows.  Arrives at z_empty once the logits are read.
+__device__ __forceinline__ void attend(State& st, uint32_t zt, uint64_t* z_empty, float qk, bool whole, int n,
+                                       const int* lens, uint32_t vw, uint32_t vt, uint32_t scratch, int lane) {
+  const uint32_t vp = scratch + 1024, mp = scratch + 1280, ap = scratch + 1344;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t vcell = vp + ((lane >> 1) & 3) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;  // [c][pair][octet][2]
+  // -- V's scales as f16 2^(byte - R_c): exponent fields 1..15, two groups a word.
+  // y = byte + 271 - R_c; in 257..271 where f16 holds the scale.
+  bool more = false;
+  {
+    const uint32_t y02 = (vw & 0x00FF00FFu) + st.r02, y13 = (vw >> 8 & 0x00FF00FFu) + st.r13;
+    const uint32_t over = (y02 + 240 * kHalves) | (y13 + 240 * kHalves);   // bit 9: y >= 272
+    const uint32_t in = (y02 + 255 * kHalves) & (y13 + 255 * kHalves);     // bit 9: y >= 257
+    const bool plain = (over & (512 * kHalves)) == 0 && (in & (512 * kHalves)) == 512 * kHalves;
+    if (__all_sync(0xffffffffu, plain)) {
+      const uint32_t h02 = (y02 - 256 * kHalves) << 10, h13 = (y13 - 256 * kHalves) << 10;
+      sts16(vcell, h02), sts16(vcell + 64, h13);
+      sts16(vcell + 128, h02 >> 16), sts16(vcell + 192, h13 >> 16);
+    } else {
+      more = odd_vscales(st, vw, vcell, 0);
     }
   }
 
-  // -- weights
-  uint32_t pa[MT][4], pb[MT][4];
+  // -- weights: 2^(z - m + kBias), m the rows' reference maxima
+  float2 x[8];
+  {
+    float z[16];
+    tmem_ld16(zt, z);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      const float2 x = fmul2({z[mt][o][0], z[mt][o][1]}, {zs[mt][0], zs[mt][0]});
-      const float2 y = fmul2({z[mt][o][2], z[mt][o][3]}, {zs[mt][1], zs[mt][1]});
-      z[mt][o][0] = x.x, z[mt][o][1] = x.y, z[mt][o][2] = y.x, z[mt][o][3] = y.y;
-      if (!whole) {
-        const int n = n0 + 8 * o + 2 * t;
-        if (n >= len[mt][0]) z[mt][o][0] = -INFINITY;
-        if (n + 1 >= len[mt][0]) z[mt][o][1] = -INFINITY;
-        if (n >= len[mt][1]) z[mt][o][2] = -INFINITY;
-        if (n + 1 >= len[mt][1]) z[mt][o][3] = -INFINITY;
-      }
-      mx0 = fmax3(mx0, z[mt][o][0], z[mt][o][1]);
-      mx1 = fmax3(mx1, z[mt][o][2], z[mt][o][3]);
+    for (int i = 0; i < 4; ++i) {
+      const float4 m = lds128f(mp + 16 * i);  // kBias - m
+      x[2 * i] = ffma2({z[4 * i], z[4 * i + 1]}, {qk, qk}, {m.x, m.y});
+      x[2 * i + 1] = ffma2({z[4 * i + 2], z[4 * i + 3]}, {qk, qk}, {m.z, m.w});
     }
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-    const bool mv0 = mx0 > st.m[mt][0] + kMaxGrow, mv1 = mx1 > st.m[mt][1] + kMaxGrow;
-    if (__any_sync(0xffffffffu, mv0 || mv1)) {
-      const float n0m = mv0 ? mx0 : st.m[mt][0], n1m = mv1 ? mx1 : st.m[mt][1];
-      const float a0 = ex2_approx(st.m[mt][0] - n0m), a1 = ex2_approx(st.m[mt][1] - n1m);
-      st.m[mt][0] = n0m, st.m[mt][1] = n1m;
-      st.l[mt][0] *= a0, st.l[mt][1] *= a1;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        st.o[mt][i][0] *= a0, st.o[mt][i][1] *= a0, st.o[mt][i][2] *= a1, st.o[mt][i][3] *= a1;
-    }
-    const float r0 = st.m[mt][0] - kBias, r1 = st.m[mt][1] - kBias;
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int o = 0; o < 4; ++o) {
-      const float p0 = ex2_approx(z[mt][o][0] - r0), p1 = ex2_approx(z[mt][o][1] - r0);
-      const float p2 = ex2_approx(z[mt][o][2] - r1), p3 = ex2_approx(z[mt][o][3] - r1);
-      s0 += p0 + p1;
-      s1 += p2 + p3;
-      pa[mt][o] = pack_f16x2(p0, p1);
-      pb[mt][o] = pack_f16x2(p2, p3);
-    }
-    st.l[mt][0] += s0, st.l[mt][1] += s1;
   }
+  if (!whole) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (n >= lens[i]) (i & 1 ? x[i >> 1].y : x[i >> 1].x) = -INFINITY;
+  }
+  float top = fmaxf(x[0].x, x[0].y);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = fmax3(top, x[i].x, x[i].y);
+  if (__any_sync(0xffffffffu, top > kBias + kMaxGrow)) {  // some row's maximum grew: new references
+    float z[16];
+    tmem_ld16(zt, z);  // x no longer has z where the reference was that of no tokens
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float y = whole || n < lens[i] ? z[i] * qk : -INFINITY, mx = warp_max(y);
+      const float old = ldsf(mp + 4 * i);  // kBias - m
+      const float now = mx > kBias - old + kMaxGrow ? kBias - mx : old;
+      (i & 1 ? x[i >> 1].y : x[i >> 1].x) = y + now;
+      __syncwarp();  // every lane has the old reference
+      if (lane == 0) stsf(ap + 4 * i, ex2_approx(now - old)), stsf(mp + 4 * i, now);
+    }
+    __syncwarp();
+    const float a0 = ldsf(ap + 4 * g), a1 = ldsf(ap + 4 * g + 32);
+    st.l[0] *= a0, st.l[2] *= a1;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st.o[i][0] *= a0, st.o[i][1] *= a0, st.o[i][2] *= a1, st.o[i][3] *= a1;
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  uint32_t pk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(ex2_approx(x[i].x), ex2_approx(x[i].y));
+  // [token][16 rows]; the halves of rows 4..7 of each 8 swap places (banks)
+  const uint32_t prow = scratch + lane * 32, flip = (lane & 4) << 2;
+  sts128(prow + flip, pk[0], pk[1], pk[2], pk[3]);
+  sts128(prow + (16 ^ flip), pk[4], pk[5], pk[6], pk[7]);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(z_empty);
+  uint32_t pa[4], pb[4];  // rows g / g + 8, tokens 8o + 2t, + 1
+  const int row8 = lane & 7, mat = lane >> 3;
+  {
+    // matrices: octet 2k, 2k + 1 x row halves
+    const uint32_t at = scratch + ((mat >> 1) * 8 + row8) * 32 + (((mat & 1) << 4) ^ ((row8 & 4) << 2));
+    uint32_t r[4];
+    ldsm_x4_trans(r, at);
+    pa[0] = r[0], pb[0] = r[1], pa[1] = r[2], pb[1] = r[3];
+    ldsm_x4_trans(r, at + 512);
+    pa[2] = r[0], pb[2] = r[1], pa[3] = r[2], pb[3] = r[3];
+  }
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+    mma_f16(st.l, pa[2 * ks], pb[2 * ks], pa[2 * ks + 1], pb[2 * ks + 1], 0x3C003C00u, 0x3C003C00u);
 
-  // -- o
-  const uint32_t vrow = vt + row_off;
-  for (int band = 0;; ++band) {
-    const bool direct = band == 0 && !more;
-    const float f = band == 0 ? 1.f : scale_pow2(1.f, -kBand * band);
+  // -- O += P V
+  const int swz = (row8 >> 1) & 3;
+  const uint32_t vrow = vt + (mat * 8 + row8) * 64;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t zr[4];
+    ldsm_x4_trans(zr, vrow + ((c ^ swz) << 4));
+    const uint4 s4 = lds128(vp + c * 64 + t * 16);
+    const uint32_t vs[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      uint32_t v0[4], v1[4];
+      e2m1x4x2_to_f16x2(zr[2 * ks], v0);
+      e2m1x4x2_to_f16x2(zr[2 * ks + 1], v1);
+      const uint32_t a0 = hmul2(pa[2 * ks], vs[2 * ks]), a1 = hmul2(pb[2 * ks], vs[2 * ks]);
+      const uint32_t a2 = hmul2(pa[2 * ks + 1], vs[2 * ks + 1]), a3 = hmul2(pb[2 * ks + 1], vs[2 * ks + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mma_f16(st.o[4 * c + i], a0, a1, a2, a3, v0[i], v1[i]);
+    }
+  }
+  for (int band = 1; more; ++band) {  // the lower bands of V's scales
+    __syncwarp();
+    more = odd_vscales(st, vw, vcell, band);
+    __syncwarp();
+    const float f = scale_pow2(1.f, -kBand * band);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t zr[4];
       ldsm_x4_trans(zr, vrow + ((c ^ swz) << 4));
-      const uint4 vs4 = lds128(vp + (c * 16 + t * 4) * 4);
-      const uint32_t vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
-      uint32_t v[4][4];
+      const uint4 s4 = lds128(vp + c * 64 + t * 16);
+      const uint32_t vs[4] = {s4.x, s4.y, s4.z, s4.w};
+      float y[4][4];
 #pragma unroll
-      for (int o = 0; o < 4; ++o) e2m1x4x2_to_f16x2(zr[o], v[o]);
+      for (int i = 0; i < 4; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        uint32_t a[4], b[4];
+      for (int ks = 0; ks < 2; ++ks) {
+        uint32_t v0[4], v1[4];
+        e2m1x4x2_to_f16x2(zr[2 * ks], v0);
+        e2m1x4x2_to_f16x2(zr[2 * ks + 1], v1);
+        const uint32_t a0 = hmul2(pa[2 * ks], vs[2 * ks]), a1 = hmul2(pb[2 * ks], vs[2 * ks]);
+        const uint32_t a2 = hmul2(pa[2 * ks + 1], vs[2 * ks + 1]), a3 = hmul2(pb[2 * ks + 1], vs[2 * ks + 1]);
 #pragma unroll
-        for (int o = 0; o < 4; ++o) a[o] = hmul2(pa[mt][o], vs[o]), b[o] = hmul2(pb[mt][o], vs[o]);
-        if (direct) {
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_f16(st.o[mt][4 * c + i], a[2 * ks], b[2 * ks], a[2 * ks + 1], b[2 * ks + 1], v[2 * ks][i],
-                      v[2 * ks + 1][i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-              mma_f16(x, a[2 * ks], b[2 * ks], a[2 * ks + 1], b[2 * ks + 1], v[2 * ks][i], v[2 * ks + 1][i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st.o[mt][4 * c + i][e] += x[e] * f;
-          }
-        }
+        for (int i = 0; i < 4; ++i) mma_f16(y[i], a0, a1, a2, a3, v0[i], v1[i]);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[4 * c + i][e] += y[i][e] * f;
     }
-    if (!more) break;
-    __syncwarp();  // the band's scales are read
-    more = put_vscales(band + 1);
-    __syncwarp();
   }
 }
 
 // ---- the main kernel -----------------------------------------------------------
-template <int MT, bool Q16>
-__global__ void __launch_bounds__(MT == 1 ? 128 : 256, MT == 1 ? 4 : 1)
+template <int SETS>
+struct Bars {
+  uint64_t* b;
+  __device__ uint64_t* k_full(int i) const { return b + i; }
+  __device__ uint64_t* k_empty(int i) const { return b + kKStages + i; }
+  __device__ uint64_t* v_full(int i) const { return b + 2 * kKStages + i; }
+  __device__ uint64_t* v_empty(int i) const { return b + 2 * kKStages + kVStages + i; }
+  __device__ uint64_t* z_full(int i) const { return b + 2 * kKStages + 2 * kVStages + i; }
+  __device__ uint64_t* z_empty(int i) const { return b + 2 * kKStages + 2 * kVStages + 2 + i; }
+  __device__ uint64_t* q_full() const { return b + 2 * kKStages + 2 * kVStages + 4; }
+};
+
+template <int SETS>
+constexpr int min_ctas() {
+  return SETS == 1 ? 3 : 1;
+}
+// TMEM columns: two z buffers, the scale cells of K (per stage) and q
+template <int SETS>
+struct Tmem {
+  static constexpr int z = 0, sk = 32 * SETS, sq = sk + 4 * kKStages, used = sq + 8;
+  static constexpr int columns = used <= 64 ? 64 : (used <= 128 ? 128 : 256);
+};
+
+template <int SETS, bool Q16>
+__global__ void __launch_bounds__(Smem<SETS>::kThreads, min_ctas<SETS>())
     dense_pa_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ Params p) {
+  using S = Smem<SETS>;
+  using T = Tmem<SETS>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int64_t s_cum[257];  // blocks before group tile_g0 + i
-  __shared__ int64_t s_part[8];
+  __shared__ int64_t s_sum[17];
+  __shared__ int64_t s_start[2];  // the share's first group and the blocks before it
+  __shared__ int s_nb;
+  __shared__ uint32_t s_tmem;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
-  const Shape sh{MT, p.sets, p.teams};
-  const Layout lay = layout(sh, Q16);
   const DensePaParams& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
-  const int set = warp % p.sets, team = warp / p.sets;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars) + team * kStages;
-  uint64_t* empty = full + p.teams * kStages;
-  volatile uint32_t* bad = reinterpret_cast<uint32_t*>(smem + lay.bad) + team * kStages;
-  uint8_t* ring = smem + team * kStages * 2 * kTileBytes;
-  uint8_t* ring_sc = smem + lay.scales + team * kStages * 256;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Bars<SETS> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
   if (tid == 0) {
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + lay.bars);
-    for (int i = 0; i < p.teams * kStages; ++i) {
-      mbar_init(&bars[i], 1);
-      mbar_init(&bars[p.teams * kStages + i], p.sets);
-    }
+    for (int i = 0; i < kKStages; ++i) mbar_init(bars.k_full(i), 1), mbar_init(bars.k_empty(i), 1);
+    for (int i = 0; i < kVStages; ++i) mbar_init(bars.v_full(i), 1), mbar_init(bars.v_empty(i), S::kCompute);
+    for (int i = 0; i < 2; ++i) mbar_init(bars.z_full(i), 1), mbar_init(bars.z_empty(i), S::kCompute);
+    mbar_init(bars.q_full(), S::kCompute);
     mbar_fence_init();
   }
   pdl_wait();
   pdl_trigger();
-
-  // the groups' blocks, scanned a tile of `threads` groups at a time
-  auto scan_tile = [&](int g0, int64_t base) -> int64_t {  // returns the blocks up to the tile's end
-    const int g = g0 + tid;
-    const int64_t nb = g < p.groups ? group_blocks(a, g) : 0;
-    int64_t x = nb;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_part[warp] = x;
-    __syncthreads();
-    int64_t before = base, all = base;
-    for (int w = 0; w < threads / 32; ++w) {
-      if (w < warp) before += s_part[w];
-      all += s_part[w];
-    }
-    s_cum[tid] = before + x - nb;
-    if (tid == 0) s_cum[threads] = all;
-    __syncthreads();
-    return all;
-  };
-  int64_t total = 0;
-  int tile_g0 = 0;
-  for (int g0 = 0; g0 < p.groups; g0 += threads) {
-    total = scan_tile(g0, total);
-    tile_g0 = g0;
+  // TMEM only after the wait: a CTA that held columns while it waited could
+  // keep the kernel before it from getting its own
+  if (warp == S::kCompute) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "n"(T::columns));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  const int64_t work = total * a.hkv;
-  const int64_t share = (work + p.ctas - 1) / p.ctas;
-  int64_t at = blockIdx.x * share;  // this CTA's blocks: [at, end)
-  const int64_t end = min(at + share, work);
+
+  // the groups' blocks, kThreads groups at a time: first their sum, then the
+  // group the share starts in
+  const int64_t per = static_cast<int64_t>(a.hkv) * p.subs;
+  int64_t total = 0, at = 0, share = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t base = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += S::kThreads) {
+      const int g = g0 + tid;
+      const int nb = g < p.groups ? blocks_of(a, group_len(a, g, 0, 1)) : 0;
+      int64_t x = nb;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = x;
+      __syncthreads();
+      int64_t before = base;
+      for (int w = 0; w <= S::kCompute; ++w) {
+        if (w < warp) before += s_sum[w];
+        base += s_sum[w];
+      }
+      const int64_t c1 = before + x, c0 = c1 - nb;  // blocks before and up to group g
+      if (pass == 0 && p.groups <= S::kThreads) {  // one tile: the sum and the start at once
+        total = base;
+        share = (total * per + p.ctas - 1) / p.ctas;
+        at = blockIdx.x * share;
+      }
+      if ((pass == 1 || p.groups <= S::kThreads) && nb && c0 * per <= at && at < c1 * per)
+        s_start[0] = g, s_start[1] = c0, s_nb = nb;
+      if (pass == 1 && base * per > at) break;
+    }
+    if (pass == 0) {
+      total = base;
+      share = (total * per + p.ctas - 1) / p.ctas;
+      at = blockIdx.x * share;
+      if (p.groups <= S::kThreads) break;
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+  Walk w;
+  w.at = at, w.end = min(at + share, total * per);
+  w.g = static_cast<int>(s_start[0]), w.c0 = s_start[1], w.nb = s_nb;  // unset, and unused, past the last share
   // cut units: (first CTA, pieces) per unit, or (unit, pieces) per first CTA
   int2* cut = reinterpret_cast<int2*>(a.ws);
   if (!p.by_unit && tid == 0) cut[blockIdx.x] = make_int2(0, 0);
-  if (at >= end) return;
-  // back to the tile the share starts in
-  if (s_cum[0] * a.hkv > at) {
-    int64_t base = 0;
-    for (tile_g0 = 0;; tile_g0 += threads) {
-      base = scan_tile(tile_g0, base);
-      if (base * a.hkv > at) break;
+  volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(smem + S::queue + kQueue * 8);  // per V stage
+  bool alive = true;
+
+  if (warp == S::kCompute) {
+    // ---- producer ----
+    struct Block {
+      int32_t id, head;  // head < 0: ~head, the first block of a piece
+    };
+    volatile Block* queue = reinterpret_cast<volatile Block*>(smem + S::queue);
+    const int32_t* table = nullptr;
+    int nblk = 0, blk = 0, chunk = 0, head = 0;
+    int32_t ids = 0;
+    bool done = false, first = false;
+    int known = 0;  // blocks in the queue so far
+    auto learn = [&]() {  // the next block of the share; false at its end
+      while (!done && blk == nblk) {
+        if (!w.next(p, lane)) {
+          done = true;
+          break;
+        }
+        table = a.block_table + static_cast<int64_t>(w.seq) * a.bt_stride + w.b0;
+        nblk = max(0, w.b1 - w.b0), blk = 0, chunk = -1, head = w.h, first = true;
+      }
+      if (done) return false;
+      if ((blk >> 5) != chunk) {
+        chunk = blk >> 5;
+        ids = 32 * chunk + lane < nblk ? table[32 * chunk + lane] : 0;
+      }
+      int32_t id = __shfl_sync(0xffffffffu, ids, blk & 31);
+      if (id < 0 || id >= a.num_blocks) {
+        if (lane == 0) set_err(a.err, BSP_DEVERR_BLOCK_ID);
+        id = -1;
+      }
+      if (lane == 0) queue[known % kQueue].id = id, queue[known % kQueue].head = first ? ~head : head;
+      first = false;
+      ++blk, ++known;
+      return true;
+    };
+    // a bad block's stages complete without data; the compute warps leave it out
+    auto load_k = [&](int i) {
+      const int st = i % kKStages;
+      const int32_t id = queue[i % kQueue].id, hh = queue[i % kQueue].head, h = hh < 0 ? ~hh : hh;
+      if (id < 0) return mbar_arrive(bars.k_full(st));
+      mbar_arrive_expect_tx(bars.k_full(st), kBlock * 64 + 512);
+      tile_g2s(smem + st * kKTile, &map_k, h, id, bars.k_full(st));
+      bulk_g2s(smem + S::ks + st * 512,
+               a.k_base + static_cast<int64_t>(id) * a.id_stride + static_cast<int64_t>(h) * kMxField + kMxScaleOff, 512,
+               bars.k_full(st));
+    };
+    auto load_v = [&](int i) {
+      const int st = i % kVStages;
+      const int32_t id = queue[i % kQueue].id, hh = queue[i % kQueue].head, h = hh < 0 ? ~hh : hh;
+      bad[st] = id < 0;
+      if (id < 0) return mbar_arrive(bars.v_full(st));
+      mbar_arrive_expect_tx(bars.v_full(st), kVTile + 512);
+      tile_g2s(smem + S::v + st * kVTile, &map_v, h, id, bars.v_full(st));
+      bulk_g2s(smem + S::vs + st * 512,
+               a.v_base + static_cast<int64_t>(id) * a.id_stride + static_cast<int64_t>(h) * kMxField + kMxScaleOff, 512,
+               bars.v_full(st));
+    };
+    // ahead of block 0: V of two blocks, K of one
+    for (int i = 0; i < 2; ++i)
+      if (learn() && lane == 0) load_v(i);
+    if (known > 0 && lane == 0) load_k(0);
+    const uint32_t q_addr = smem_u32(smem + S::q);
+    int pieces = 0;
+    for (int i = 0; i < known; ++i) {
+      const bool more = learn();  // block i + 2
+      if (lane == 0) {
+        const int st = i % kKStages, buf = i & 1;
+        const int32_t id = queue[i % kQueue].id;
+        if (queue[i % kQueue].head < 0) {
+          if (alive) alive = mbar_wait_sleep(bars.q_full(), pieces & 1, a.err);
+          ++pieces;
+        }
+        if (alive && i + 1 < known) {  // K of the next block, once block i - 1's MMAs have left its stage
+          if (i > 0) alive = mbar_wait_sleep(bars.k_empty((i + 1) % kKStages), ((i - 1) / kKStages) & 1, a.err);
+          if (alive) load_k(i + 1);
+        }
+        if (alive) alive = mbar_wait_sleep(bars.k_full(st), (i / kKStages) & 1, a.err);
+        if (alive && i > 1) alive = mbar_wait_sleep(bars.z_empty(buf), ((i >> 1) - 1) & 1, a.err);
+        if (alive) {
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (id >= 0) {
+            const uint32_t k_addr = smem_u32(smem + st * kKTile), sk = tmem + T::sk + 4 * st;
+            scales_to_tmem(sk, smem_u32(smem + S::ks + st * 512));
+#pragma unroll
+            for (int part = 0; part < (Q16 ? 2 : 1); ++part)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                umma_mx(tmem + T::z + buf * S::kRows, smem_desc_sw128(k_addr + 32 * c),
+                        smem_desc_sw128(q_addr + part * S::kRows * 128 + 32 * c),
+                        idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, S::kRows, 128, c, c), sk, tmem + T::sq + 4 * part,
+                        part > 0 || c > 0);
+          }
+          umma_commit(bars.k_empty(st));
+          umma_commit(bars.z_full(buf));
+          if (more) {  // V of block i + 2, once the compute warps have left its stage
+            if (i + 2 >= kVStages)
+              alive = mbar_wait_sleep(bars.v_empty((i + 2) % kVStages), ((i + 2) / kVStages - 1) & 1, a.err);
+            if (alive) {
+              fence_proxy_async();
+              load_v(i + 2);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+    // nothing may still be writing shared memory or TMEM when the CTA leaves
+    if (lane == 0 && alive && known > 0)
+      mbar_wait_sleep(bars.k_empty((known - 1) % kKStages), ((known - 1) / kKStages) & 1, a.err);
+    __syncwarp();
+  } else {
+    // ---- compute ----
+    const int set = warp >> 2, part = warp & 3;
+    const uint32_t scratch = smem_u32(smem + S::scratch) + warp * kScratch;
+    const uint32_t merge = smem_u32(smem + S::scratch) + set * S::kMerge;
+    int* lens = reinterpret_cast<int*>(smem + S::len);
+    uint8_t* cells = smem + S::sfq;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * part) << 16;
+    const int g = lane >> 2, t = lane & 3;
+    int i = 0;  // blocks so far
+    while (w.next(p, lane)) {
+      const int nblk = max(0, w.b1 - w.b0);
+      bar_sync(1, 32 * S::kCompute);  // the last unit's q, lengths and merge buffers are no longer read
+      if (nblk) stage_q<Q16>(a, w.tok0, w.tokens, w.h, smem + S::q, S::kRows, cells, tid);
+      if (tid < S::kRows) {
+        const int j = tid / a.group;
+        lens[tid] = j < w.tokens ? min(max(a.row_len[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h], 0), w.max_len) : 0;
+      }
+      if (tid == 0)
+        for (int j = 0; j < w.tokens; ++j)
+          if (a.row_seq[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h] != w.seq) set_err(a.err, BSP_DEVERR_GROUP_SEQ);
+      State st;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) st.o[k][0] = st.o[k][1] = st.o[k][2] = st.o[k][3] = 0.f;
+      st.l[0] = st.l[1] = st.l[2] = st.l[3] = 0.f;
+      st.r02 = st.r13 = kNoScale;
+      if (lane < 16) stsf(scratch + 1280 + 4 * lane, kBias - kNoMax);
+      fence_proxy_async();  // the tensor core reads q through the async proxy
+      bar_sync(1, 32 * S::kCompute);
+      if (nblk) {
+        if (set == 0) {  // q's scale cells, in this sub-partition's copy
+#pragma unroll
+          for (int k = 0; k < (Q16 ? 2 : 1); ++k) {
+            uint32_t cell[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              cell[c] = 32 * c + lane < S::kRows
+                            ? *reinterpret_cast<const uint32_t*>(cells + (k * S::kRows + 32 * c + lane) * 4)
+                            : 0x7F7F7F7Fu;
+            tmem_st4(tmem + lane_base + T::sq + 4 * k, cell[0], cell[1], 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.q_full());
+      }
+      for (int b = w.b0; b < w.b0 + nblk; ++b, ++i) {
+        const int vst = i % kVStages, buf = i & 1;
+        if (alive) alive = mbar_wait_sleep(bars.v_full(vst), (i / kVStages) & 1, a.err);
+        const int n = b * kBlock + 4 * lane + part;  // the lane's token
+        uint32_t vw = lds32(smem_u32(smem + S::vs) + vst * 512 + lane * 16 + part * 4);
+        if (n >= w.max_len) vw = 0;
+        if (alive) alive = mbar_wait_sleep(bars.z_full(buf), (i >> 1) & 1, a.err);
+        alive = __all_sync(0xffffffffu, alive);  // the rest is warp-wide
+        if (!alive) continue;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (!bad[vst]) {
+          attend(st, tmem + lane_base + T::z + buf * S::kRows + 16 * set, bars.z_empty(buf), p.qk_scale,
+                 (b + 1) * kBlock <= w.min_len, n, lens + 16 * set, vw,
+                 smem_u32(smem + S::v) + vst * kVTile + part * 2048, scratch, lane);
+        } else if (lane == 0) {
+          mbar_arrive(bars.z_empty(buf));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.v_empty(vst));
+      }
+
+      // -- the four warps of a set joined: 1, 2, 3 hand theirs to 0 in turn
+      float m0 = kBias - ldsf(scratch + 1280 + 4 * g), m1 = kBias - ldsf(scratch + 1280 + 4 * (g + 8));
+      float l0 = st.l[0], l1 = st.l[2];  // every column of the tile is the sum
+      const uint32_t rr[4] = {271 - (st.r02 & 0xFFFF), 271 - (st.r13 & 0xFFFF), 271 - (st.r02 >> 16),
+                              271 - (st.r13 >> 16)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int e = static_cast<int>(rr[c]) - 127 + 14;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st.o[4 * c + k][j] = scale_pow2(st.o[4 * c + k][j], e);
+      }
+      bar_sync(1, 32 * S::kCompute);  // the scratch becomes the merge buffers
+      const uint32_t mrow = merge + (g * kRowPad + 8 * t) * 4, mml = merge + 16 * kRowPad * 4;
+      for (int k = 1; k < 4; ++k) {
+        if (part == k) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                sts128(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4, __float_as_uint(st.o[4 * c][2 * e + j]),
+                       __float_as_uint(st.o[4 * c + 1][2 * e + j]), __float_as_uint(st.o[4 * c + 2][2 * e + j]),
+                       __float_as_uint(st.o[4 * c + 3][2 * e + j]));
+          if (t == 0) {
+            stsf(mml + 8 * g, m0), stsf(mml + 8 * g + 4, l0);
+            stsf(mml + 8 * (g + 8), m1), stsf(mml + 8 * (g + 8) + 4, l1);
+          }
+        }
+        bar_sync(2 + set, 128);
+        if (part == 0) {
+          const float n0 = ldsf(mml + 8 * g), n1 = ldsf(mml + 8 * (g + 8));
+          const float M0 = fmaxf(m0, n0), M1 = fmaxf(m1, n1);
+          const float f0 = ex2_approx(m0 - M0), f1 = ex2_approx(m1 - M1), h0 = ex2_approx(n0 - M0), h1 = ex2_approx(n1 - M1);
+          l0 = l0 * f0 + h0 * ldsf(mml + 8 * g + 4);
+          l1 = l1 * f1 + h1 * ldsf(mml + 8 * (g + 8) + 4);
+          m0 = M0, m1 = M1;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float4 y = lds128f(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4);
+                const float f = e ? f1 : f0, hh = e ? h1 : h0;
+                st.o[4 * c][2 * e + j] = st.o[4 * c][2 * e + j] * f + y.x * hh;
+                st.o[4 * c + 1][2 * e + j] = st.o[4 * c + 1][2 * e + j] * f + y.y * hh;
+                st.o[4 * c + 2][2 * e + j] = st.o[4 * c + 2][2 * e + j] * f + y.z * hh;
+                st.o[4 * c + 3][2 * e + j] = st.o[4 * c + 3][2 * e + j] * f + y.w * hh;
+              }
+        }
+        bar_sync(2 + set, 128);
+      }
+      if (part == 0) {
+        // a CTA's slots: 2 * CTA for a unit that began before its share, + 1
+        // for one that goes on after it
+        float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
+                    (2LL * blockIdx.x + (w.starts ? 1 : 0)) * S::kRows * (kDim + 2);
+        const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * set + g + 8 * e;
+          if (r >= w.tokens * a.group) continue;
+          const float l = e ? l1 : l0;
+          if (w.starts && w.ends) {
+            const float f = l > 0.f ? 1.f / l : 0.f;
+            uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                            ((w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group) * kDim + 8 * t;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(dst + 32 * c) =
+                  make_uint4(pack_bf16x2(st.o[4 * c][2 * e] * f, st.o[4 * c + 1][2 * e] * f),
+                             pack_bf16x2(st.o[4 * c + 2][2 * e] * f, st.o[4 * c + 3][2 * e] * f),
+                             pack_bf16x2(st.o[4 * c][2 * e + 1] * f, st.o[4 * c + 1][2 * e + 1] * f),
+                             pack_bf16x2(st.o[4 * c + 2][2 * e + 1] * f, st.o[4 * c + 3][2 * e + 1] * f));
+          } else {
+            float* dst = po + r * kDim + 8 * t;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<float4*>(dst + 32 * c + 4 * j) =
+                    make_float4(st.o[4 * c][2 * e + j], st.o[4 * c + 1][2 * e + j], st.o[4 * c + 2][2 * e + j],
+                                st.o[4 * c + 3][2 * e + j]);
+            if (t == 0) *reinterpret_cast<float2*>(po + S::kRows * kDim + 2 * r) = make_float2(e ? m1 : m0, l);
+          }
+        }
+      }
+      if (w.starts && tid == 0) {
+        // the pieces of the unit: shares from this one to that of its last block
+        const int pieces =
+            w.ends ? 0 : static_cast<int>((static_cast<int64_t>(w.c0) * per + (w.unit - w.g * per + 1) * w.nb - 1) / share -
+                                          blockIdx.x + 1);
+        if (p.by_unit)
+          cut[w.unit] = make_int2(blockIdx.x, pieces);
+        else if (pieces)
+          cut[blockIdx.x] = make_int2(w.unit, pieces);
+      }
     }
   }
-
-  const int rows_pad = sh.rows();
-  uint8_t* qs = smem + lay.q;
-  const uint32_t qs_set = smem_u32(qs) + set * MT * 4 * 512, qlo_set = qs_set + rows_pad / 16 * 4 * 512;
-  const float* row_scale = reinterpret_cast<const float*>(qs + rows_pad / 16 * 4 * 512 * (Q16 ? 2 : 1));
-  uint8_t* scratch = smem + lay.scratch + warp * 768;
-  uint32_t fill = 0, used = 0;  // slices issued and consumed by this team
-  bool alive = true;
-  int gi = 0;
-
-  while (at < end) {
-    // the unit at `at`
-    while (s_cum[gi + 1] * a.hkv <= at) {
-      if (++gi == threads) {
-        const int64_t base = s_cum[threads];
-        __syncthreads();
-        tile_g0 += threads, gi = 0;
-        scan_tile(tile_g0, base);
-      }
-    }
-    const int g = tile_g0 + gi;
-    const int64_t c0 = s_cum[gi], nb = s_cum[gi + 1] - c0;
-    const int h = static_cast<int>((at - c0 * a.hkv) / nb);
-    const int64_t ustart = c0 * a.hkv + h * nb, uend = ustart + nb;
-    const int b0 = static_cast<int>(at - ustart), b1 = static_cast<int>(min(end, uend) - ustart);
-    const int tok0 = g * a.q_group, tokens = min(a.q_group, a.num_rows / a.hkv - tok0);
-    const int64_t row0 = static_cast<int64_t>(tok0) * a.hkv + h;
-    const int seq = a.row_seq[static_cast<int64_t>(tok0) * a.hkv];
-    const int32_t* table = a.block_table + static_cast<int64_t>(seq) * a.bt_stride;
-    const int cap = min(static_cast<int64_t>(a.bt_stride) * kBlock, int64_t{0x7FFFFFFF});
-    int max_len = 0, min_len = 0x7FFFFFFF;
-    for (int j = 0; j < tokens; ++j) {
-      const int n = min(max(a.row_len[row0 + static_cast<int64_t>(j) * a.hkv], 0), cap);
-      max_len = max(max_len, n), min_len = min(min_len, n);
-      if (tid == 0 && a.row_seq[row0 + static_cast<int64_t>(j) * a.hkv] != seq) set_err(a.err, BSP_DEVERR_GROUP_SEQ);
-    }
-    // this team's slices of blocks [b0, b1), none past the rows' tokens
-    const int s0 = b0 * 4, s1 = min(b1 * 4, (max_len + kSlice - 1) / kSlice);
-    const int n = s1 > s0 + team ? (s1 - s0 - team + p.teams - 1) / p.teams : 0;
-
-    int32_t ids = 0;  // lane i: the block id of the team's slice 32 * chunk + i
-    int chunk = -1;
-    auto issue = [&](int i) {  // slice i of the team into its ring (warp `set` 0)
-      if ((i >> 5) != chunk) {
-        chunk = i >> 5;
-        const int k = 32 * chunk + lane;
-        ids = k < n ? table[(s0 + team + k * p.teams) >> 2] : 0;
-      }
-      const int32_t id = __shfl_sync(0xffffffffu, ids, i & 31);
-      if (lane == 0) {
-        const int stg = fill % kStages;
-        if (p.sets > 1 && fill >= kStages && alive)
-          alive = mbar_wait(&empty[stg], ((fill / kStages) - 1) & 1, a.err);
-        if (id < 0 || id >= a.num_blocks) {
-          set_err(a.err, BSP_DEVERR_BLOCK_ID);
-          bad[stg] = 1;
-          mbar_arrive(&full[stg]);
-        } else {
-          bad[stg] = 0;
-          const int o0 = ((s0 + team + i * p.teams) & 3) * kSlice;
-          const int64_t off = static_cast<int64_t>(id) * a.id_stride + static_cast<int64_t>(h) * kMxField + kMxScaleOff + o0 * 4;
-          uint8_t* dst = ring + stg * 2 * kTileBytes;
-          fence_proxy_async();
-          mbar_arrive_expect_tx(&full[stg], 2 * kTileBytes + 256);
-          tile_g2s(dst, &map_k, h * (kMxField / 64) + o0, id, &full[stg]);
-          tile_g2s(dst + kTileBytes, &map_v, h * (kMxField / 64) + o0, id, &full[stg]);
-          bulk_g2s(ring_sc + stg * 256, a.k_base + off, 128, &full[stg]);
-          bulk_g2s(ring_sc + stg * 256 + 128, a.v_base + off, 128, &full[stg]);
-        }
-      }
-      ++fill;
-    };
-    if (set == 0)
-      for (int i = 0; i < min(n, kStages); ++i) issue(i);
-
-    stage_q<Q16>(a, tok0, tokens, h, qs, rows_pad, tid, threads);
-    State<MT> st;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) st.o[mt][i][0] = st.o[mt][i][1] = st.o[mt][i][2] = st.o[mt][i][3] = 0.f;
-      st.m[mt][0] = st.m[mt][1] = kNoMax, st.l[mt][0] = st.l[mt][1] = 0.f;
-    }
-    st.r = 0;
-    int len[MT][2];
-    float zs[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int row = (set * MT + mt) * 16 + (lane >> 2) + 8 * k, j = row / a.group;
-        len[mt][k] = j < tokens ? min(max(a.row_len[row0 + static_cast<int64_t>(j) * a.hkv], 0), cap) : 0;
-      }
-    __syncthreads();
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) zs[mt][k] = p.qk_scale * row_scale[(set * MT + mt) * 16 + (lane >> 2) + 8 * k];
-
-    for (int i = 0; i < n; ++i) {
-      const int stg = used % kStages;
-      if (alive) alive = mbar_wait_sleep(&full[stg], (used / kStages) & 1, a.err);
-      alive = __all_sync(0xffffffffu, alive);  // after a timed-out wait the warp waits no more
-      ++used;
-      const int n0 = (s0 + team + i * p.teams) * kSlice;
-      const bool skip = !alive || bad[stg];  // nothing of the slice is used
-      const uint32_t kt = smem_u32(ring + stg * 2 * kTileBytes);
-      if (!skip)
-        slice<MT, Q16>(st, kt, kt + kTileBytes, ring_sc + stg * 256, qs_set, qlo_set, scratch, n0, len, max_len,
-                       n0 + kSlice <= min_len, zs, lane);
-      __syncwarp();
-      if (p.sets > 1 && lane == 0) mbar_arrive(&empty[stg]);
-      if (set == 0 && i + kStages < n) issue(i + kStages);
-    }
-
-    // -- the teams' states joined in shared memory (the ring is drained)
-    __syncthreads();
-    float* mo = reinterpret_cast<float*>(smem);
-    float2* ml = reinterpret_cast<float2*>(smem + lay.merge_ml);
-    const int gq = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float l = st.l[mt][k];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int r = (warp * MT + mt) * 16 + gq + 8 * k;
-        if (t == 0) ml[r] = make_float2(st.m[mt][k], l);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int e = static_cast<int>(st.r >> (8 * c) & 0xFF) - 127 + 14;
-          float x[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            x[q] = scale_pow2(st.o[mt][4 * c + q][2 * k], e);
-            x[4 + q] = scale_pow2(st.o[mt][4 * c + q][2 * k + 1], e);
-          }
-          float* dst = mo + r * kRowPad + 32 * c + 8 * t;
-          *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<float4*>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        }
-      }
-    __syncthreads();
-    const bool whole_unit = at == ustart && end >= uend;
-    // a CTA's slots: 2 * CTA for a unit that began before its share, + 1 for
-    // one that goes on after it
-    const int64_t piece = 2LL * blockIdx.x + (at == ustart ? 1 : 0);
-    float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) + piece * rows_pad * (kDim + 2);
-    float2* pml = reinterpret_cast<float2*>(po + rows_pad * kDim);
-    const int live_rows = tokens * a.group;
-    const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
-    for (int r = warp; r < live_rows; r += threads / 32) {
-      const int rs = r / (MT * 16), ri = r % (MT * 16);
-      float M = kNoMax;
-      for (int k = 0; k < p.teams; ++k) M = fmaxf(M, ml[(k * p.sets + rs) * MT * 16 + ri].x);
-      float L = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < p.teams; ++k) {
-        const int s = (k * p.sets + rs) * MT * 16 + ri;
-        const float2 v = ml[s];
-        const float w = ex2_approx(v.x - M);
-        const float4 y = *reinterpret_cast<const float4*>(mo + s * kRowPad + 4 * lane);
-        L += w * v.y;
-        x.x += w * y.x, x.y += w * y.y, x.z += w * y.z, x.w += w * y.w;
-      }
-      if (whole_unit) {
-        const float f = L > 0.f ? 1.f / L : 0.f;
-        const int64_t e = ((tok0 + r / a.group) * hq + static_cast<int64_t>(h) * a.group + r % a.group) * kDim + 4 * lane;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e) =
-            make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-      } else {
-        *reinterpret_cast<float4*>(po + r * kDim + 4 * lane) = x;
-        if (lane == 0) pml[r] = make_float2(M, L);
-      }
-    }
-    if (at == ustart && tid == 0) {
-      const int pieces = whole_unit ? 0 : static_cast<int>((uend - 1) / share - blockIdx.x + 1);
-      const int unit = g * a.hkv + h;
-      if (p.by_unit)
-        cut[unit] = make_int2(blockIdx.x, pieces);
-      else if (pieces)
-        cut[blockIdx.x] = make_int2(unit, pieces);
-    }
-    __syncthreads();  // the merge area becomes the ring again
-    at = min(end, uend);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == S::kCompute) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(T::columns));
   }
 }
 
@@ -721,14 +895,15 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
   const DensePaParams& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_cta = 8 / parts;  // rows of a CTA
-  const int chunks = (a.q_group * a.group + per_cta - 1) / per_cta;
+  const int chunks = (p.sub_tokens * a.group + per_cta - 1) / per_cta;
   const int item = blockIdx.x / chunks, row = (blockIdx.x % chunks) * per_cta + warp / parts, part = warp % parts;
   const int2 info = reinterpret_cast<const int2*>(a.ws)[item];
   const int pieces = info.y, c0 = p.by_unit ? info.x : item, unit = p.by_unit ? item : info.x;
   if (pieces == 0) return;
-  const int g = unit / a.hkv, h = unit % a.hkv;
-  const int64_t tok0 = static_cast<int64_t>(g) * a.q_group;
-  const int tokens = static_cast<int>(min(static_cast<int64_t>(a.q_group), a.num_rows / a.hkv - tok0));
+  const int per = a.hkv * p.subs, g = unit / per, h = unit % per / p.subs, sub = unit % p.subs;
+  const int64_t tok0 = static_cast<int64_t>(g) * a.q_group + sub * p.sub_tokens;
+  const int tokens = static_cast<int>(
+      min(static_cast<int64_t>(min(p.sub_tokens, a.q_group - sub * p.sub_tokens)), a.num_rows / a.hkv - tok0));
   const bool live = row < tokens * a.group;
   const float* base = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + list_bytes(p.ctas));
   const int64_t slot_floats = static_cast<int64_t>(rows_pad) * (kDim + 2);
@@ -787,89 +962,114 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
 }
 
 // ---- host ------------------------------------------------------------------------
-// [rows of 64 B][blocks] of one side, boxes of one slice
-bool make_map_side(CUtensorMap* m, const void* base, uint64_t rows, uint64_t blocks, uint64_t stride) {
+// One side of the cache as [blocks][heads][4][32][row]: row 32j + i of a box
+// is token 4i + j.  K's rows are 128 4-bit values, unpacked to 16-byte slots of
+// 16 with 128-byte swizzle; V's are 64 bytes, 64-byte swizzle.
+bool make_map_side(CUtensorMap* m, bool unpack, const void* base, uint64_t heads, uint64_t blocks, uint64_t stride) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {64, rows, blocks};
-  const cuuint64_t strides[2] = {64, stride};
-  const cuuint32_t box[3] = {64, kSlice, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims[5] = {unpack ? 128u : 64u, 32, 4, heads, blocks};
+  const cuuint64_t strides[4] = {256, 64, kMxField, stride};
+  const cuuint32_t box[5] = {unpack ? 128u : 64u, 32, 4, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, unpack ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            unpack ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// resident CTAs per SM, with the shared-memory opt-in (once per device and shape)
-template <int MT, bool Q16>
-int occupancy(const Shape& sh) {
-  static std::atomic<int> table[5][kMaxDevices];
-  return cached_per_device(table[sh.sets], [&] {
-    int n = 0;
-    const int bytes = layout(sh, Q16).total;
-    int most = 0;  // of the shapes this kernel runs in
-    for (int rows = MT == 1 ? 16 : 32; rows <= (MT == 1 ? 16 : 128); rows += 32)
-      most = std::max(most, layout(shape_of(rows), Q16).total);
-    const cudaError_t e =
-        cudaFuncSetAttribute(dense_pa_kernel<MT, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess || cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, dense_pa_kernel<MT, Q16>,
-                                                                           sh.warps() * 32, bytes) != cudaSuccess)
-      n = 0;
-    return n > 0 ? n : 1;
-  });
-}
-int occupancy_of(const Shape& sh, bool q16) {
-  if (sh.mt == 1) return q16 ? occupancy<1, true>(sh) : occupancy<1, false>(sh);
-  return q16 ? occupancy<2, true>(sh) : occupancy<2, false>(sh);
+// how a group's rows are cut into units
+struct Plan {
+  int sub_tokens, subs, sets;
+};
+Plan plan_of(int group, int q_group) {
+  const int sub = std::min(q_group, kMaxRows / group), subs = (q_group + sub - 1) / sub;
+  const int even = (q_group + subs - 1) / subs;  // units of about the same size
+  return {even, subs, (even * group + 15) / 16};
 }
 
-template <int MT, bool Q16>
-cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, const Shape& sh, cudaStream_t s) {
-  return launch_kernel(dense_pa_kernel<MT, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(sh.warps() * 32),
-                       layout(sh, Q16).total, s, 0, mk, mv, p);
+// CTAs per SM: what the register bound allows, as far as shared memory holds
+// them (TMEM: 512 columns).  The occupancy query answers 1 for a kernel that
+// allocates TMEM.
+template <int SETS, bool Q16>
+constexpr int ctas_per_sm() {
+  return std::min(min_ctas<SETS>(), 228 * 1024 / (Smem<SETS>::total(Q16) + 1024 + 256));
+}
+int ctas_of(int sets, bool q16) {
+  switch (sets) {
+    case 1:
+      return q16 ? ctas_per_sm<1, true>() : ctas_per_sm<1, false>();
+    case 2:
+      return q16 ? ctas_per_sm<2, true>() : ctas_per_sm<2, false>();
+    case 3:
+      return q16 ? ctas_per_sm<3, true>() : ctas_per_sm<3, false>();
+    default:
+      return q16 ? ctas_per_sm<4, true>() : ctas_per_sm<4, false>();
+  }
+}
+
+template <int SETS, bool Q16>
+cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
+  static_assert(Smem<SETS>::total(Q16) <= 227 * 1024 && Tmem<SETS>::used <= Tmem<SETS>::columns);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = once_per_device(done, [] {  // the shared-memory opt-in
+    return cudaFuncSetAttribute(dense_pa_kernel<SETS, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<SETS>::total(Q16));
+  });
+  if (e != cudaSuccess) return e;
+  return launch_kernel(dense_pa_kernel<SETS, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(Smem<SETS>::kThreads),
+                       Smem<SETS>::total(Q16), s, 0, mk, mv, p);
+}
+template <bool Q16>
+cudaError_t launch_sets(int sets, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
+  return sets == 1   ? launch_main<1, Q16>(mk, mv, p, s)
+         : sets == 2 ? launch_main<2, Q16>(mk, mv, p, s)
+         : sets == 3 ? launch_main<3, Q16>(mk, mv, p, s)
+                     : launch_main<4, Q16>(mk, mv, p, s);
 }
 
 }  // namespace
 
 size_t dense_pa_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms) {
   (void)num_rows, (void)hkv;
-  const Shape sh = shape_of(group * q_group);
-  const int64_t ctas = static_cast<int64_t>(std::max(occupancy_of(sh, false), occupancy_of(sh, true))) * num_sms;
-  return list_bytes(ctas) + 2 * ctas * sh.rows() * (kDim + 2) * sizeof(float);
+  const Plan pl = plan_of(group, q_group);
+  const int64_t ctas = static_cast<int64_t>(std::max(ctas_of(pl.sets, false), ctas_of(pl.sets, true))) * num_sms;
+  return list_bytes(ctas) + 2 * ctas * 16 * pl.sets * (kDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s, int* launches) {
   if (a.num_rows == 0) return cudaSuccess;
-  const Shape sh = shape_of(a.group * a.q_group);
+  const Plan pl = plan_of(a.group, a.q_group);
   const bool q16 = a.q_dtype == BSP_BF16;
   Params p{};
   p.a = a;
-  p.qk_scale = a.sm_scale * kLog2e * 64.f;
+  p.qk_scale = a.sm_scale * kLog2e;
   const int tokens = a.num_rows / a.hkv;
   p.groups = (tokens + a.q_group - 1) / a.q_group;
-  const int64_t units = static_cast<int64_t>(p.groups) * a.hkv;
+  p.subs = pl.subs;
+  p.sub_tokens = pl.sub_tokens;
+  const int64_t units = static_cast<int64_t>(p.groups) * a.hkv * pl.subs;
+  if (units > INT32_MAX) return cudaErrorNotSupported;
   p.units = static_cast<int32_t>(units);
-  p.ctas = static_cast<int32_t>(
-      std::min<int64_t>(static_cast<int64_t>(occupancy_of(sh, q16)) * num_sms, units * a.bt_stride));
-  p.sets = sh.sets;
-  p.teams = sh.teams;
+  const int per_sm = ctas_of(pl.sets, q16);
+  p.ctas = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(per_sm) * num_sms, units * a.bt_stride));
   p.by_unit = units <= p.ctas;
   CUtensorMap mk, mv;
-  const uint64_t rows = static_cast<uint64_t>(a.hkv) * (kMxField / 64), blocks = std::max<int64_t>(a.num_blocks, 1);
-  if (!make_map_side(&mk, a.k_base, rows, blocks, a.id_stride) || !make_map_side(&mv, a.v_base, rows, blocks, a.id_stride))
+  const uint64_t blocks = std::max<int64_t>(a.num_blocks, 1);
+  if (!make_map_side(&mk, true, a.k_base, a.hkv, blocks, a.id_stride) ||
+      !make_map_side(&mv, false, a.v_base, a.hkv, blocks, a.id_stride))
     return cudaErrorInvalidValue;
-  cudaError_t e = sh.mt == 1 ? (q16 ? launch_main<1, true>(mk, mv, p, sh, s) : launch_main<1, false>(mk, mv, p, sh, s))
-                             : (q16 ? launch_main<2, true>(mk, mv, p, sh, s) : launch_main<2, false>(mk, mv, p, sh, s));
+  cudaError_t e = q16 ? launch_sets<true>(pl.sets, mk, mv, p, s) : launch_sets<false>(pl.sets, mk, mv, p, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.ctas > 1) {
     // pieces of a unit are about ctas / units: more warps a row where they are many
     const int64_t pieces = std::min<int64_t>(p.ctas / units + 1, a.bt_stride);
     const int parts = pieces >= 64 ? 8 : (pieces >= 32 ? 4 : (pieces >= 16 ? 2 : 1));
-    const int64_t chunks = (a.q_group * a.group + 8 / parts - 1) / (8 / parts);
+    const int64_t chunks = (pl.sub_tokens * a.group + 8 / parts - 1) / (8 / parts);
     const int64_t items = p.by_unit ? units : p.ctas;
     e = launch_kernel(dense_pa_join_kernel, dim3(static_cast<unsigned>(items * chunks)), dim3(256), 0, s, 0, p,
-                      sh.rows(), parts);
+                      16 * pl.sets, parts);
     if (e != cudaSuccess) return e;
     ++*launches;
   }

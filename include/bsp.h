@@ -570,7 +570,8 @@ bsp_status bsp_kv_page_read(const bsp_kv_cache* kv, const bsp_index_cache* idx, 
  * length the block table covers):
  *   out = softmax(sm_scale * q K^T) V over tokens t < L_r, token t at offset
  *         t % 128 of block block_table[row_seq[r]][t / 128]
- *   kv    an MXFP4 cache (else BSP_ERR_UNSUPPORTED)
+ *   kv    an MXFP4 cache whose k_base and id_stride_bytes are multiples of 32
+ *         (else BSP_ERR_UNSUPPORTED)
  *   q     [tokens, Hkv*G, 128], bf16 or e4m3 (q_dtype); out bf16, the same shape
  *   block_table int32 [*, bt_stride]; row_seq, row_len int32 [rows], rows =
  *         tokens * Hkv; L_r is clamped to [0, 128 * bt_stride]; a row with

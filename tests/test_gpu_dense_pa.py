@@ -207,7 +207,7 @@ def test_bytes_past_the_length_are_never_used(q_len):
 
 
 def test_a_table_wider_than_the_contexts_and_a_padded_cache():
-    c = Case([300, 5, 777], seed=10, width=40, pad_bytes=48)
+    c = Case([300, 5, 777], seed=10, width=40, pad_bytes=96)
     want = _close(c).clone()
     for s, n in enumerate(c.lens):  # entries past a context are never read
         c.table[s, -(-n // 128):] = -1 if s else 1 << 30

@@ -126,6 +126,11 @@ def test_dense_pa_decode(bsp):
 
     n0 = bsp.launch_count()
     assert status(kv=None) == 1 and status(kv=fp8) == 2
+    for f, v in (("k_base", (1 << 40) + 16), ("id_stride_bytes", mx.id_stride_bytes + 16)):
+        odd = bsp.KvCacheDesc()
+        C.memmove(C.byref(odd), C.byref(mx), C.sizeof(odd))
+        setattr(odd, f, v)
+        assert status(kv=odd) == 2, f
     assert status(qt=bsp.MXFP4) == 2
     for k in ("q", "bt", "seq", "ln", "out"):
         assert status(**{k: None}) == 1, k
