@@ -149,6 +149,29 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// mbarriers by shared address
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kSleepNs)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t* err) {
+  for (uint32_t i = 0; i < kSleepWaitLimit; ++i)
+    if (try_wait(bar, parity)) return true;
+  set_err(err, BSP_DEVERR_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t* err) {
+  if (__builtin_expect(try_wait(bar, parity), 1)) return true;
+  return wait_slow(bar, parity, err);
+}
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   uint64_t x, y, z, r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
@@ -346,33 +369,48 @@ __device__ __forceinline__ bool odd_vscales(State& st, uint32_t vw, uint32_t vce
   return __any_sync(0xffffffffu, low);
 }
 
+// The uncommon half of attend(): a block that some row does not see whole, V
+// scales outside R_c's band, or a row whose maximum grew (x then starts afresh
+// from the logits, as it does not hold them where the reference was that of no
+// tokens).  Returns whether lower bands of V scales are left.
+__device__ __forceinline__ bool adjust(State& st, float2 (&x)[8], uint32_t zt, float qk, int n, uint32_t lens,
+                                       uint32_t vw, uint32_t vcell, uint32_t scratch, int lane) {
+  const uint32_t mp = scratch + 1280, ap = scratch + 1344;
+  const bool more = odd_vscales(st, vw, vcell, 0);
+  float z[16];
+  tmem_ld16(zt, z);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float y = n < static_cast<int>(lds32(lens + 4 * i)) ? z[i] * qk : -INFINITY, mx = warp_max(y);
+    const float old = ldsf(mp + 4 * i);  // kBias - m
+    const float now = mx > kBias - old + kMaxGrow ? kBias - mx : old;
+    (i & 1 ? x[i >> 1].y : x[i >> 1].x) = y + now;
+    __syncwarp();  // every lane has the old reference
+    if (lane == 0) stsf(ap + 4 * i, ex2_approx(now - old)), stsf(mp + 4 * i, now);
+  }
+  __syncwarp();
+  const float a0 = ldsf(ap + 4 * (lane >> 2)), a1 = ldsf(ap + 4 * (lane >> 2) + 32);
+  st.l[0] *= a0, st.l[2] *= a1;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) st.o[i][0] *= a0, st.o[i][1] *= a0, st.o[i][2] *= a1, st.o[i][3] *= a1;
+  return more;
+}
+
 // 32 tokens of the warp: their logits are at TMEM address zt (thread = the lane's
 // token n, column = row h, which sees the token if n < lens[h]; whole: every row
 // sees every token); vw the token's V scale bytes (0 where no row sees it), vt the
 // V rows.  Arrives at z_empty once the logits are read.
-__device__ __forceinline__ void attend(State& st, uint32_t zt, uint64_t* z_empty, float qk, bool whole, int n,
-                                       const int* lens, uint32_t vw, uint32_t vt, uint32_t scratch, int lane) {
-  const uint32_t vp = scratch + 1024, mp = scratch + 1280, ap = scratch + 1344;
-  const int g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void attend(State& st, uint32_t zt, uint32_t z_empty, float qk, bool whole, int n,
+                                       uint32_t lens, uint32_t vw, uint32_t vt, uint32_t scratch, int lane) {
+  const uint32_t vp = scratch + 1024, mp = scratch + 1280;
+  const int t = lane & 3;
   const uint32_t vcell = vp + ((lane >> 1) & 3) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;  // [c][pair][octet][2]
-  // -- V's scales as f16 2^(byte - R_c): exponent fields 1..15, two groups a word.
+  // V's scales as f16 2^(byte - R_c): exponent fields 1..15, two groups a word.
   // y = byte + 271 - R_c; in 257..271 where f16 holds the scale.
-  bool more = false;
-  {
-    const uint32_t y02 = (vw & 0x00FF00FFu) + st.r02, y13 = (vw >> 8 & 0x00FF00FFu) + st.r13;
-    const uint32_t over = (y02 + 240 * kHalves) | (y13 + 240 * kHalves);   // bit 9: y >= 272
-    const uint32_t in = (y02 + 255 * kHalves) & (y13 + 255 * kHalves);     // bit 9: y >= 257
-    const bool plain = (over & (512 * kHalves)) == 0 && (in & (512 * kHalves)) == 512 * kHalves;
-    if (__all_sync(0xffffffffu, plain)) {
-      const uint32_t h02 = (y02 - 256 * kHalves) << 10, h13 = (y13 - 256 * kHalves) << 10;
-      sts16(vcell, h02), sts16(vcell + 64, h13);
-      sts16(vcell + 128, h02 >> 16), sts16(vcell + 192, h13 >> 16);
-    } else {
-      more = odd_vscales(st, vw, vcell, 0);
-    }
-  }
-
-  // -- weights: 2^(z - m + kBias), m the rows' reference maxima
+  const uint32_t y02 = (vw & 0x00FF00FFu) + st.r02, y13 = (vw >> 8 & 0x00FF00FFu) + st.r13;
+  const uint32_t over = (y02 + 240 * kHalves) | (y13 + 240 * kHalves);  // bit 9: y >= 272
+  const uint32_t in = (y02 + 255 * kHalves) & (y13 + 255 * kHalves);    // bit 9: y >= 257
+  // weights: 2^(z - m + kBias), m the rows' reference maxima
   float2 x[8];
   {
     float z[16];
@@ -384,31 +422,18 @@ __device__ __forceinline__ void attend(State& st, uint32_t zt, uint64_t* z_empty
       x[2 * i + 1] = ffma2({z[4 * i + 2], z[4 * i + 3]}, {qk, qk}, {m.z, m.w});
     }
   }
-  if (!whole) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (n >= lens[i]) (i & 1 ? x[i >> 1].y : x[i >> 1].x) = -INFINITY;
-  }
   float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
   for (int i = 1; i < 8; ++i) top = fmax3(top, x[i].x, x[i].y);
-  if (__any_sync(0xffffffffu, top > kBias + kMaxGrow)) {  // some row's maximum grew: new references
-    float z[16];
-    tmem_ld16(zt, z);  // x no longer has z where the reference was that of no tokens
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float y = whole || n < lens[i] ? z[i] * qk : -INFINITY, mx = warp_max(y);
-      const float old = ldsf(mp + 4 * i);  // kBias - m
-      const float now = mx > kBias - old + kMaxGrow ? kBias - mx : old;
-      (i & 1 ? x[i >> 1].y : x[i >> 1].x) = y + now;
-      __syncwarp();  // every lane has the old reference
-      if (lane == 0) stsf(ap + 4 * i, ex2_approx(now - old)), stsf(mp + 4 * i, now);
-    }
-    __syncwarp();
-    const float a0 = ldsf(ap + 4 * g), a1 = ldsf(ap + 4 * g + 32);
-    st.l[0] *= a0, st.l[2] *= a1;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) st.o[i][0] *= a0, st.o[i][1] *= a0, st.o[i][2] *= a1, st.o[i][3] *= a1;
+  const bool plain = whole && top <= kBias + kMaxGrow && (over & (512 * kHalves)) == 0 &&
+                     (in & (512 * kHalves)) == 512 * kHalves;
+  bool more = false;
+  if (__builtin_expect(__all_sync(0xffffffffu, plain), 1)) {
+    const uint32_t h02 = (y02 - 256 * kHalves) << 10, h13 = (y13 - 256 * kHalves) << 10;
+    sts16(vcell, h02), sts16(vcell + 64, h13);
+    sts16(vcell + 128, h02 >> 16), sts16(vcell + 192, h13 >> 16);
+  } else {
+    more = adjust(st, x, zt, qk, n, lens, vw, vcell, scratch, lane);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   uint32_t pk[8];
@@ -419,7 +444,7 @@ __device__ __forceinline__ void attend(State& st, uint32_t zt, uint64_t* z_empty
   sts128(prow + flip, pk[0], pk[1], pk[2], pk[3]);
   sts128(prow + (16 ^ flip), pk[4], pk[5], pk[6], pk[7]);
   __syncwarp();
-  if (lane == 0) mbar_arrive(z_empty);
+  if (lane == 0) arrive(z_empty);
   uint32_t pa[4], pb[4];  // rows g / g + 8, tokens 8o + 2t, + 1
   const int row8 = lane & 7, mat = lane >> 3;
   {
@@ -455,7 +480,7 @@ __device__ __forceinline__ void attend(State& st, uint32_t zt, uint64_t* z_empty
       for (int i = 0; i < 4; ++i) mma_f16(st.o[4 * c + i], a0, a1, a2, a3, v0[i], v1[i]);
     }
   }
-  for (int band = 1; more; ++band) {  // the lower bands of V's scales
+  for (int band = 1; __builtin_expect(more, 0); ++band) {  // the lower bands of V's scales
     __syncwarp();
     more = odd_vscales(st, vw, vcell, band);
     __syncwarp();
@@ -715,7 +740,11 @@ __global__ void __launch_bounds__(Smem<SETS>::kThreads, min_ctas<SETS>())
     uint8_t* cells = smem + S::sfq;
     const uint32_t lane_base = static_cast<uint32_t>(32 * part) << 16;
     const int g = lane >> 2, t = lane & 3;
-    int i = 0;  // blocks so far
+    const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0));
+    const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
+    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(bad)), z_at = tmem + lane_base + T::z + 16 * set;
+    const uint32_t vs_at = smem_u32(smem + S::vs) + lane * 16 + part * 4, v_at = smem_u32(smem + S::v) + part * 2048;
+    uint32_t buf = 0, z_phase = 0, vst = 0, v_phase = 0;  // of the next block
     while (w.next(p, lane)) {
       const int nblk = max(0, w.b1 - w.b0);
       bar_sync(1, 32 * S::kCompute);  // the last unit's q, lengths and merge buffers are no longer read
@@ -752,25 +781,27 @@ __global__ void __launch_bounds__(Smem<SETS>::kThreads, min_ctas<SETS>())
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.q_full());
       }
-      for (int b = w.b0; b < w.b0 + nblk; ++b, ++i) {
-        const int vst = i % kVStages, buf = i & 1;
-        if (alive) alive = mbar_wait_sleep(bars.v_full(vst), (i / kVStages) & 1, a.err);
-        const int n = b * kBlock + 4 * lane + part;  // the lane's token
-        uint32_t vw = lds32(smem_u32(smem + S::vs) + vst * 512 + lane * 16 + part * 4);
-        if (n >= w.max_len) vw = 0;
-        if (alive) alive = mbar_wait_sleep(bars.z_full(buf), (i >> 1) & 1, a.err);
+      const uint32_t lens_at = smem_u32(lens + 16 * set);
+      int n = w.b0 * kBlock + 4 * lane + part;  // the lane's token
+      const int n_whole = w.min_len - (kBlock - 1) + (4 * lane + part);  // blocks up to here are whole for every row
+      for (int k = 0; k < nblk; ++k, n += kBlock) {
+        // one test of both barriers: V is there before z is
+        if (alive) alive = wait_for(z_full + 8 * buf, z_phase, a.err) && wait_for(v_full + 8 * vst, v_phase, a.err);
         alive = __all_sync(0xffffffffu, alive);  // the rest is warp-wide
-        if (!alive) continue;
+        if (!alive) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (!bad[vst]) {
-          attend(st, tmem + lane_base + T::z + buf * S::kRows + 16 * set, bars.z_empty(buf), p.qk_scale,
-                 (b + 1) * kBlock <= w.min_len, n, lens + 16 * set, vw,
-                 smem_u32(smem + S::v) + vst * kVTile + part * 2048, scratch, lane);
+        if (lds32(bad_at + 4 * vst) == 0) {
+          uint32_t vw = lds32(vs_at + vst * 512);
+          if (n >= w.max_len) vw = 0;
+          attend(st, z_at + buf * S::kRows, z_empty + 8 * buf, p.qk_scale, n < n_whole, n, lens_at, vw,
+                 v_at + vst * kVTile, scratch, lane);
         } else if (lane == 0) {
-          mbar_arrive(bars.z_empty(buf));
+          arrive(z_empty + 8 * buf);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.v_empty(vst));
+        if (lane == 0) arrive(v_empty + 8 * vst);
+        buf ^= 1, z_phase ^= buf ^ 1;
+        if (++vst == kVStages) vst = 0, v_phase ^= 1;
       }
 
       // -- the four warps of a set joined: 1, 2, 3 hand theirs to 0 in turn
