@@ -6,43 +6,47 @@
 //
 // with k4, v4 the e2m1 values, e the e8m0 bytes of the four 32-dim groups c.
 //
-// Work.  A unit = (query group, KV head, at most 64 rows): its rows, tokens
-// times G heads, share every byte of the cache.  The units' 128-token blocks
-// laid end to end are cut into equal shares, one per resident CTA, so ragged
-// batches load every SM alike; a CTA finds its share by a prefix sum over the
-// groups' lengths.  A unit that lies in one share is written at once; of a
-// unit cut by share borders each CTA leaves (m, l, O) in the workspace, and a
-// second kernel joins them (it reads a list of cut units, no counters: the
-// workspace carries nothing from call to call and the sums' order is fixed).
+// Work.  A unit = (query group, KV head): its rows, q_group tokens times G
+// heads, share every byte of the cache; more than 32 rows are cut into units
+// that neighbouring CTAs take at the same time (the second finds the bytes in
+// L2).  The units' 128-token blocks laid end to end are cut into equal
+// shares, one per resident CTA, so ragged batches load every SM alike; a CTA
+// finds its share by a prefix sum over the groups' lengths.  A unit that lies
+// in one share is written at once; of a unit cut by share borders each CTA
+// leaves (m, l, O) in the workspace, and a second kernel joins them (it reads
+// a list of cut units, no counters: the workspace carries nothing from call to
+// call and the sums' order is fixed).
 //
-// A CTA is one producer warp and 4 * sets compute warps; each set has 16 rows.
+// A CTA is a producer warp and four compute warps, for MT tiles of 16 rows.
 //   - The producer loads blocks by TMA (K unpacked to one byte slot a value,
-//     the layout the tensor core reads; V packed, 64-byte swizzle; the scales
-//     as they lie) and issues, per block, four tcgen05.mma block-scaled by the
-//     cache's own e8m0 bytes: z^T = K Q^T, M = 128 tokens, N = 16 * sets rows,
-//     K = 32 = one scale group each, in TMEM, double-buffered.  Row 32j + i of
-//     the tile is token 4i + j (a tensor-map order): then the 512 scale bytes
-//     are, as they lie in the cache, the cells tcgen05.cp wants.  A bf16 query is
-//     the sum of two e4m3 parts (see stage_q), eight MMAs.
-//   - A compute warp reads 32 tokens x 16 rows of z^T (thread = token), takes
-//     the exponentials, turns the f16 weights around through shared memory
-//     into mma A fragments and multiplies by V: mma.sync m16n8k16 f16.  V
-//     comes through ldmatrix.trans as four nibbles of two tokens a register;
-//     bit moves turn them into f16 pairs, times 2^-14 exactly.  V's scales go
-//     onto P: 2^(ev - R_c), a power of two at most 1, multiplies the weights of
-//     each group.  R_c is the largest scale byte so far (O is rescaled when it
-//     grows).  Tokens whose scale is 15 or more binades below R_c, which f16
-//     could not hold, make the warp take its tokens again in bands of 15.
+//     the layout the tensor core reads; V packed; the scales as they lie) and
+//     issues, per block, four tcgen05.mma block-scaled by the cache's own e8m0
+//     bytes: z^T = K Q^T, M = 128 tokens, N = 16 * MT rows, K = 32 = one scale
+//     group each, in TMEM, double-buffered.  A bf16 query is the sum of two e4m3
+//     parts (see stage_q), eight MMAs.
+//   - A compute warp takes the exponentials of 32 tokens (thread = token) and
+//     leaves the f16 weights in shared memory, where it and its partner pick
+//     them up as mma A fragments: a pair of warps shares 64 tokens, each
+//     multiplies them by its half of V's dims (mma.sync m16n8k16 f16), so that O
+//     takes 32 registers a tile.  V comes through ldmatrix.trans as four
+//     nibbles of two tokens a register; bit moves turn them into f16 pairs,
+//     times 2^-14 exactly.  V's scales go onto P: 2^(ev - R_c), a power of two
+//     at most 1, multiplies the weights of each group.  R_c is the largest
+//     scale byte so far (O is rescaled when it grows).  Tokens whose scale is
+//     15 or more binades below R_c, which f16 could not hold, make the pair
+//     take its tokens again in bands of 15.
 //   - p is f16, at most half a step, 2^-11, off; weights are kept times 2^7 so
-//     that f16's range, down to 2^-25, reaches 2^-32 of the largest.
+//     that f16's range, down to 2^-25, reaches 2^-32 of the largest.  Row sums
+//     are an mma column of ones over the rounded weights.
 // tcgen05 takes the scores because it reads e2m1 and the scales itself: on
 // mma.sync the conversions of K cost more issue slots than all else.  PV stays
 // on mma.sync: with V^T as A its dequantised tile would have to go through
 // shared memory, 32 KB written and read a block, more than a block's time at
 // the memory's rate.
 //
-// Every wait is bounded; after a timed-out wait a role waits no more (the
-// error word is set) and the CTA frees its TMEM and returns.
+// Every wait for a copy or an MMA is bounded; after a timed-out wait a role
+// waits no more (the error word is set, the results are void), walks through its
+// blocks and the CTA frees its TMEM and returns.
 #include <algorithm>
 
 #include "common.cuh"
@@ -54,16 +58,17 @@ namespace bsp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxRows = 64;       // rows of a unit
-constexpr int kKStages = 2, kVStages = 3;
-constexpr int kKTile = kBlock * 128;  // unpacked keys of a block
-constexpr int kVTile = kBlock * 64;   // packed values of a block
-constexpr int kRowPad = kDim + 4;  // floats of a row in the merge buffer
+constexpr int kMaxRows = 32;  // rows of a unit
+// A field (128 tokens x 64 bytes, then 128 x 4 bytes of scales) comes as one box.
+// K: 136 rows of 64 bytes, unpacked to 128; V: 68 rows of 128 bytes.
+constexpr int kKRows = 136, kVRows = 68;
+constexpr int kKTile = kKRows * 128, kVTile = (kVRows + 7) / 8 * 8 * 128;
+static_assert(kKRows * 64 == kMxField && kVRows * 128 == kMxField && kKTile % 1024 == 0);
+constexpr int kRowPad = 64 + 4;    // floats of a row (half its dims) in the merge buffer
 constexpr float kMaxGrow = 8.f;    // the reference maximum moves when a row's maximum grows by more (log2)
 constexpr float kBias = 7.f;       // weights are 2^(z - m + kBias)
 constexpr float kNoMax = -1e30f;   // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
 constexpr int kBand = 15;          // binades a band of V scales spans
-constexpr int kQueue = 8;          // blocks the producer knows ahead
 
 // bytes of the list of cut units at the start of the workspace
 __host__ __device__ constexpr int64_t list_bytes(int64_t ctas) { return (ctas * 8 + 255) / 256 * 256; }
@@ -71,41 +76,47 @@ __host__ __device__ constexpr int64_t list_bytes(int64_t ctas) { return (ctas * 
 struct Params {
   DensePaParams a;
   float qk_scale;  // sm_scale * log2(e)
-  int32_t groups, subs, sub_tokens;  // query groups; units a group and head is cut into, of sub_tokens tokens
-  int32_t units, ctas;
-  int32_t by_unit;  // the list of cut units has an entry per unit (else per CTA)
+  int32_t groups, subs, sub_tokens;  // query groups; units each is cut into, of sub_tokens tokens
+  int32_t units, ctas, shares;       // shares = ctas / subs
+  int32_t by_unit;                   // the list of cut units has an entry per unit (else per CTA)
 };
 
 // ---- shared memory -----------------------------------------------------------
-// per compute warp: P [32 tokens][16 rows] f16, V's scales [4][16 pairs] f16x2,
-// reference maxima and rescale factors of 16 rows; the sets' merge buffers
-// take the same place once a unit's blocks are done
-constexpr int kScratch = 1024 + 256 + 64 + 64;
-template <int SETS>
+constexpr int kCompute = 4;  // warps
+constexpr int kThreads = 32 * (kCompute + 1);
+// A K stage is free again as soon as its MMAs are done, a block ahead of the
+// weights, so K has fewer stages than V
+template <int MT>
 struct Smem {
-  static constexpr int kCompute = 4 * SETS;
-  static constexpr int kThreads = 32 * (kCompute + 1);
-  static constexpr int kRows = 16 * SETS;
-  static constexpr int kMerge = 16 * kRowPad * 4 + 128;  // a set's O, m, l
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kKStages = MT == 1 ? 2 : 1, kVStages = MT == 1 ? 2 : 3;
   static constexpr int v = kKStages * kKTile;
-  static constexpr int ks = v + kVStages * kVTile;  // K scales, with K's stages
-  static constexpr int vs = ks + kKStages * 512;
-  static constexpr int scratch = vs + kVStages * 512;
-  static constexpr int scratch_bytes = std::max(kCompute * kScratch, SETS * kMerge);
-  static constexpr int len = scratch + scratch_bytes;  // [rows] lengths
-  static constexpr int sfq = len + kRows * 4;          // [2][rows] scale cells of q
+  static constexpr int cells = v + kVStages * kVTile;  // K's scales as TMEM cells, per stage
+  // per pair of warps, twice: P [part][tile][32 tokens][16 rows] f16, then V's
+  // scales [part][c][4][4][2] f16
+  static constexpr int kP = 2 * MT * 1024, kPair = kP + 512;
+  static constexpr int pairs = cells + kKStages * 512;
+  // the pairs' place is the merge buffer once a unit's blocks are done
+  static constexpr int kMergeWarp = kRows * kRowPad * 4;
+  static constexpr int pairs_bytes = std::max(4 * kPair, 2 * kMergeWarp);
+  static constexpr int refs = pairs + pairs_bytes;          // per warp: reference maxima, rescale factors
+  static constexpr int tops = refs + kCompute * 2 * kRows * 4;  // per warp: row maxima, 4 scale maxima
+  static constexpr int kTop = kRows * 4 + 16;
+  static constexpr int sums = tops + kCompute * kTop;       // per warp: l
+  static constexpr int len = sums + kCompute * kRows * 4;   // [rows] lengths
+  static constexpr int sfq = len + kRows * 4;               // [2][rows] scale cells of q
   static constexpr int bars = sfq + 2 * kRows * 4;
-  static constexpr int queue = bars + 20 * 8;
-  static constexpr int q = (queue + kQueue * 8 + 16 + 1023) / 1024 * 1024;
+  static constexpr int misc = bars + 16 * 8;                // bad[4], TMEM address
+  static constexpr int q = (misc + 32 + 1023) / 1024 * 1024;
   static constexpr int total(bool q16) { return q + kRows * 128 * (q16 ? 2 : 1) + 1024; }
 };
 
 // ---- device helpers ------------------------------------------------------------
-__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* m, int head, int block, uint64_t* bar) {
+__device__ __forceinline__ void tile_g2s(uint32_t dst, const CUtensorMap* m, int head, int block, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], "
-      "[%5];" ::"r"(smem_u32(dst)),
-      "l"(m), "r"(0), "r"(head), "r"(block), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(m), "r"(0), "r"(head), "r"(block), "r"(bar)
       : "memory");
 }
 // 512 bytes (32 rows of 16) to four TMEM columns of every 32-lane sub-partition
@@ -149,7 +160,24 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// mbarriers by shared address
+// barrier of a pair of warps that returns whether every / any thread says so
+__device__ __forceinline__ bool pair_all(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool pair_any(int id, bool x) { return !pair_all(id, !x); }
+// mbarriers and copies by shared address
+__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -163,6 +191,7 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t* err) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kSleepWaitLimit; ++i)
     if (try_wait(bar, parity)) return true;
   set_err(err, BSP_DEVERR_TIMEOUT);
@@ -178,15 +207,6 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
   asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  float2 o;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
-  return o;
-}
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  uint64_t x, y, r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   float2 o;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
   return o;
@@ -238,35 +258,31 @@ struct Walk {
   int64_t at, end, c0;  // c0: blocks of the groups before g
   int g, nb;
   // the piece at `at`
-  int unit, h, tok0, tokens, seq, b0, b1, max_len, min_len, len;  // len: of the lane's token
+  int unit, h, tok0, tokens, seq, b0, nblk, max_len, min_len;
   bool starts, ends;  // the unit's first and last blocks are in the piece
 
-  __device__ __forceinline__ bool next(const Params& p, int lane) {
+  __device__ __noinline__ bool next(const Params& p, int sub, int lane) {
     if (at >= end) return false;
     const DensePaParams& a = p.a;
-    const int64_t per = static_cast<int64_t>(a.hkv) * p.subs;
-    while ((c0 + nb) * per <= at) {
+    while ((c0 + nb) * a.hkv <= at) {
       c0 += nb;
       ++g;
       nb = blocks_of(a, __reduce_max_sync(0xffffffffu, group_len(a, g, lane, 32)));
     }
-    const int x = static_cast<int>((at - c0 * per) / nb);
-    const int64_t ustart = c0 * per + static_cast<int64_t>(x) * nb, uend = ustart + nb;
-    unit = static_cast<int>(g * per + x);
-    h = x / p.subs;
-    const int sub = x % p.subs;
+    h = static_cast<int>((at - c0 * a.hkv) / nb);
+    const int64_t ustart = c0 * a.hkv + static_cast<int64_t>(h) * nb, uend = ustart + nb;
+    unit = (g * a.hkv + h) * p.subs + sub;
     const int gtok = g * a.q_group;
     tok0 = gtok + sub * p.sub_tokens;
     tokens = min(min(p.sub_tokens, a.q_group - sub * p.sub_tokens), a.num_rows / a.hkv - tok0);
     seq = a.row_seq[static_cast<int64_t>(gtok) * a.hkv];
     const int cap = static_cast<int>(min(static_cast<int64_t>(a.bt_stride) * kBlock, int64_t{0x7FFFFFFF}));
-    len = 0;
+    int len = 0;
     if (lane < tokens) len = min(max(a.row_len[static_cast<int64_t>(tok0 + lane) * a.hkv + h], 0), cap);
-    max_len = __reduce_max_sync(0xffffffffu, len);
+    max_len = __reduce_max_sync(0xffffffffu, len);  // 0 where the last group lacks this unit's tokens
     min_len = __reduce_min_sync(0xffffffffu, lane < tokens ? len : 0x7FFFFFFF);
-    if (tokens <= 0) max_len = 0;  // the last group may lack this unit's tokens
     b0 = static_cast<int>(at - ustart);
-    b1 = min(static_cast<int>(min(end, uend) - ustart), (max_len + 127) >> 7);
+    nblk = max(0, min(static_cast<int>(min(end, uend) - ustart), (max_len >> 7) + ((max_len & 127) != 0)) - b0);
     starts = at == ustart, ends = end >= uend;
     at = min(end, uend);
     return true;
@@ -281,7 +297,7 @@ struct Walk {
 // significant bits and each part 4, so the sum is exact for elements down to
 // 2^-13 of the group's largest, and off by at most 2^-21 of it below.
 template <bool Q16>
-__device__ __forceinline__ void stage_q(const DensePaParams& a, int tok0, int tokens, int h, uint8_t* q, int rows,
+__device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int tokens, int h, uint8_t* q, int rows,
                                         uint8_t* cells, int tid) {
   const int n = tid >> 3, j = tid & 7;
   const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
@@ -330,251 +346,319 @@ __device__ __forceinline__ void stage_q(const DensePaParams& a, int tok0, int to
   }
 }
 
-// one compute warp's running softmax: O of 16 rows in mma accumulators (tile
-// 4c + i: dims 32c + 8t + i and 32c + 8t + 4 + i of rows g and g + 8), the sums l
-// as a tile of their own (P times ones), and 271 - R_c of groups (0, 2) and (1, 3)
-// in the halves of two words
+// One compute warp's running softmax: O of MT tiles of 16 rows in mma
+// accumulators, for the warp's two of the four 32-dim groups (tile 4k + i: dims
+// 8t + i and 8t + 4 + i of group k, of rows g and g + 8); the sums l of the warp's own
+// tokens, a tile of P times ones; and 271 - R_c of groups (0, 2) and (1, 3) in
+// the halves of two words.
+template <int MT>
 struct State {
-  float o[16][4];
-  float l[4];
+  float o[MT][8][4];
+  float l[MT][4];
   uint32_t r02, r13;
 };
 constexpr uint32_t kHalves = 0x00010001u;
 constexpr uint32_t kNoScale = 271 * kHalves;  // R_c = 0
 
-// V's scales where some byte is above R_c, zero or 15 binades and more below it:
-// raises R_c (O moves to the new unit), writes band `band`'s f16 scales, and says
-// whether lower ones are left
-__device__ __forceinline__ bool odd_vscales(State& st, uint32_t vw, uint32_t vcell, int band) {
-  const uint32_t rr[4] = {271 - (st.r02 & 0xFFFF), 271 - (st.r13 & 0xFFFF), 271 - (st.r02 >> 16), 271 - (st.r13 >> 16)};
-  uint32_t now[4];
+// where a warp and its pair find things (shared addresses)
+struct Place {
+  uint32_t pair;   // P and V's scales, two buffers
+  uint32_t refs;   // the warp's copy of kBias - m, then rescale factors
+  uint32_t tops;   // the pair's row and scale maxima (both warps')
+  uint32_t lens;
+  int bar, member, lane;
+};
+
+// f16 2^(byte - R_c) of band `band` of the lane's token, 0 outside the band;
+// whether lower bands are left
+template <int MT>
+__device__ __forceinline__ bool put_band(const State<MT>& st, uint32_t vw, uint32_t vcell, int band) {
   bool low = false;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const uint32_t b = vw >> (8 * c) & 0xFF;
-    now[c] = band ? rr[c] : max(rr[c], __reduce_max_sync(0xffffffffu, b));
-    if (now[c] != rr[c]) {
-      const float f = scale_pow2(1.f, static_cast<int>(rr[c]) - static_cast<int>(now[c]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[4 * c + i][e] *= f;
-    }
-    const int x = static_cast<int>(b) - static_cast<int>(now[c]) + kBand * band + 15;  // f16 exponent field
+    const int b = vw >> (8 * c) & 0xFF;
+    const int r = 271 - static_cast<int>((c & 1 ? st.r13 : st.r02) >> (c & 2 ? 16 : 0) & 0xFFFF);
+    const int x = b - r + kBand * band + 15;  // f16 exponent field
     low |= b && x <= 0;
     sts16(vcell + c * 64, b && x > 0 && x <= 15 ? x << 10 : 0);
   }
+  return low;
+}
+
+// the lane's weights to its place in P; the halves of rows 4..7 of each 8
+// tokens swap places (banks)
+__device__ __forceinline__ void put_weights(uint32_t p, int lane, const float2 (&x)[8]) {
+  uint32_t pk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(ex2_approx(x[i].x), ex2_approx(x[i].y));
+  const uint32_t at = p + lane * 32, flip = (lane & 4) << 2;
+  sts128(at + flip, pk[0], pk[1], pk[2], pk[3]);
+  sts128(at + (16 ^ flip), pk[4], pk[5], pk[6], pk[7]);
+}
+
+// The uncommon way of a block: one that some row does not see whole, V scales
+// outside R_c's band, or a row whose maximum grew.  Both warps of the pair go
+// through it: new references and R_c from both, O rescaled, the weights and V's
+// scales written afresh.  Returns whether lower bands of V scales are left.
+template <int MT>
+__device__ __forceinline__ bool adjust(State<MT>& st, const Place& w, uint32_t zt, float qk, int n, uint32_t vw,
+                                    uint32_t pbuf, uint32_t vcell) {
+  constexpr int kRows = 16 * MT;
+  const uint32_t mine = w.tops + w.member * Smem<MT>::kTop;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float z[16];
+    tmem_ld16(zt + 16 * mt, z);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float y = n < static_cast<int>(lds32(w.lens + (16 * mt + i) * 4)) ? z[i] * qk : -INFINITY;
+      const float mx = warp_max(y);
+      if (w.lane == 0) stsf(mine + (16 * mt + i) * 4, mx);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t mx = __reduce_max_sync(0xffffffffu, vw >> (8 * c) & 0xFF);
+    if (w.lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(mine + kRows * 4 + 4 * c), "r"(mx) : "memory");
+  }
+  bar_sync(w.bar, 64);
+  uint32_t now[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t at = w.tops + kRows * 4 + 4 * c;
+    const uint32_t old = 271 - ((c & 1 ? st.r13 : st.r02) >> (c & 2 ? 16 : 0) & 0xFFFF);
+    now[c] = max(old, max(lds32(at), lds32(at + Smem<MT>::kTop)));
+    if (now[c] != old && (c >> 1) == w.member) {
+      const float f = scale_pow2(1.f, static_cast<int>(old) - static_cast<int>(now[c]));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st.o[mt][4 * (c & 1) + i][e] *= f;
+    }
+  }
   st.r02 = kNoScale - (now[0] | (now[2] << 16));
   st.r13 = kNoScale - (now[1] | (now[3] << 16));
-  return __any_sync(0xffffffffu, low);
-}
-
-// The uncommon half of attend(): a block that some row does not see whole, V
-// scales outside R_c's band, or a row whose maximum grew (x then starts afresh
-// from the logits, as it does not hold them where the reference was that of no
-// tokens).  Returns whether lower bands of V scales are left.
-__device__ __forceinline__ bool adjust(State& st, float2 (&x)[8], uint32_t zt, float qk, int n, uint32_t lens,
-                                       uint32_t vw, uint32_t vcell, uint32_t scratch, int lane) {
-  const uint32_t mp = scratch + 1280, ap = scratch + 1344;
-  const bool more = odd_vscales(st, vw, vcell, 0);
-  float z[16];
-  tmem_ld16(zt, z);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float y = n < static_cast<int>(lds32(lens + 4 * i)) ? z[i] * qk : -INFINITY, mx = warp_max(y);
-    const float old = ldsf(mp + 4 * i);  // kBias - m
-    const float now = mx > kBias - old + kMaxGrow ? kBias - mx : old;
-    (i & 1 ? x[i >> 1].y : x[i >> 1].x) = y + now;
-    __syncwarp();  // every lane has the old reference
-    if (lane == 0) stsf(ap + 4 * i, ex2_approx(now - old)), stsf(mp + 4 * i, now);
+  for (int mt = 0; mt < MT; ++mt) {
+    float z[16];
+    tmem_ld16(zt + 16 * mt, z);
+    float2 x[8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 16 * mt + i;
+      const float y = n < static_cast<int>(lds32(w.lens + r * 4)) ? z[i] * qk : -INFINITY;
+      const float mx = fmaxf(ldsf(w.tops + r * 4), ldsf(w.tops + Smem<MT>::kTop + r * 4));
+      const float old = ldsf(w.refs + r * 4);  // kBias - m
+      const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
+      (i & 1 ? x[i >> 1].y : x[i >> 1].x) = y + ref;
+      __syncwarp();  // every lane has the old reference
+      if (w.lane == 0) stsf(w.refs + (kRows + r) * 4, ex2_approx(ref - old)), stsf(w.refs + r * 4, ref);
+    }
+    put_weights(pbuf + mt * 1024, w.lane, x);
+    __syncwarp();
+    const uint32_t f = w.refs + (kRows + 16 * mt + (w.lane >> 2)) * 4;
+    const float a0 = ldsf(f), a1 = ldsf(f + 32);
+    st.l[mt][0] *= a0, st.l[mt][2] *= a1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      st.o[mt][i][0] *= a0, st.o[mt][i][1] *= a0, st.o[mt][i][2] *= a1, st.o[mt][i][3] *= a1;
   }
-  __syncwarp();
-  const float a0 = ldsf(ap + 4 * (lane >> 2)), a1 = ldsf(ap + 4 * (lane >> 2) + 32);
-  st.l[0] *= a0, st.l[2] *= a1;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) st.o[i][0] *= a0, st.o[i][1] *= a0, st.o[i][2] *= a1, st.o[i][3] *= a1;
-  return more;
+  return pair_any(w.bar, put_band(st, vw, vcell, 0));
 }
 
-// 32 tokens of the warp: their logits are at TMEM address zt (thread = the lane's
-// token n, column = row h, which sees the token if n < lens[h]; whole: every row
-// sees every token); vw the token's V scale bytes (0 where no row sees it), vt the
-// V rows.  Arrives at z_empty once the logits are read.
-__device__ __forceinline__ void attend(State& st, uint32_t zt, uint32_t z_empty, float qk, bool whole, int n,
-                                       uint32_t lens, uint32_t vw, uint32_t vt, uint32_t scratch, int lane) {
-  const uint32_t vp = scratch + 1024, mp = scratch + 1280;
-  const int t = lane & 3;
-  const uint32_t vcell = vp + ((lane >> 1) & 3) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;  // [c][pair][octet][2]
+// O (+)= P V of the pair's 64 tokens and the warp's half of the dims; the first
+// time also the sums of the warp's own tokens.  DIRECT: into O, else times f
+// through accumulators of their own (a lower band).
+template <int MT, bool DIRECT>
+__device__ __forceinline__ void multiply(State<MT>& st, uint32_t pair, uint32_t vt, int member, int lane, float f) {
+  const int t = lane & 3, row8 = lane & 7, mat = lane >> 3;
+  const uint32_t prow = pair + ((mat >> 1) * 8 + row8) * 32 + (((mat & 1) << 4) ^ ((row8 & 4) << 2));
+  // V rows of 128 bytes hold two tokens; 16-byte chunk j of row r is at j ^ (r % 8)
+  const int vr = mat * 4 + (row8 >> 1);
+  const uint32_t vrow = vt + vr * 128 + ((((row8 & 1) * 4 + 2 * member) ^ (vr & 7)) << 4), vsc = pair + Smem<MT>::kP + member * 128 + t * 16;
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    uint32_t pf[MT][2][4];  // A fragments (rows g, g + 8 x token octets), k-steps 0 and 1 of the part
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) ldsm_x4_trans(pf[mt][k], prow + part * MT * 1024 + mt * 1024 + k * 512);
+    if (DIRECT && part == member) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          mma_f16(st.l[mt], pf[mt][k][0], pf[mt][k][1], pf[mt][k][2], pf[mt][k][3], 0x3C003C00u, 0x3C003C00u);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t zr[4];
+      ldsm_x4_trans(zr, (vrow + part * 2048) ^ (c << 4));
+      const uint4 s4 = lds128(vsc + part * 256 + c * 64);
+      const uint32_t vs[4] = {s4.x, s4.y, s4.z, s4.w};
+      float y[MT][4][4];
+      if (!DIRECT) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[mt][i][0] = y[mt][i][1] = y[mt][i][2] = y[mt][i][3] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t v0[4], v1[4];
+        e2m1x4x2_to_f16x2(zr[2 * k], v0);
+        e2m1x4x2_to_f16x2(zr[2 * k + 1], v1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t a0 = hmul2(pf[mt][k][0], vs[2 * k]), a1 = hmul2(pf[mt][k][1], vs[2 * k]);
+          const uint32_t a2 = hmul2(pf[mt][k][2], vs[2 * k + 1]), a3 = hmul2(pf[mt][k][3], vs[2 * k + 1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_f16(DIRECT ? st.o[mt][4 * c + i] : y[mt][i], a0, a1, a2, a3, v0[i], v1[i]);
+        }
+      }
+      if (!DIRECT) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[mt][4 * c + i][e] += y[mt][i][e] * f;
+      }
+    }
+  }
+}
+
+// the lower bands of V's scales
+template <int MT>
+__device__ __forceinline__ void lower_bands(State<MT>& st, const Place& w, uint32_t pair, uint32_t vt, uint32_t vw,
+                                         uint32_t vcell) {
+  bool more = true;
+#pragma unroll 1
+  for (int band = 1; more; ++band) {
+    bar_sync(w.bar, 64);  // the last band's scales are read
+    more = pair_any(w.bar, put_band(st, vw, vcell, band));
+    multiply<MT, false>(st, pair, vt, w.member, w.lane, scale_pow2(1.f, -kBand * band));
+  }
+}
+
+// A block's 32 tokens of the warp: their logits are at TMEM address zt (thread =
+// the lane's token n, column = row h, which sees the token if n < lens[h]; whole:
+// every row sees every token); vw the token's V scale bytes (0 where no row sees
+// it), vt the pair's V rows.  Arrives at z_empty once the logits are read.
+template <int MT>
+__device__ __forceinline__ void attend(State<MT>& st, const Place& w, uint32_t zt, uint32_t z_empty, float qk,
+                                       bool whole, int n, uint32_t vw, uint32_t vt, uint32_t buf) {
+  const uint32_t pair = w.pair + buf * Smem<MT>::kPair, pbuf = pair + w.member * MT * 1024;
+  const uint32_t vcell = pair + Smem<MT>::kP + w.member * 256 + ((w.lane >> 1) & 3) * 16 + (w.lane >> 3) * 4 +
+                         (w.lane & 1) * 2;  // [part][c][pair of tokens][octet][2]
   // V's scales as f16 2^(byte - R_c): exponent fields 1..15, two groups a word.
   // y = byte + 271 - R_c; in 257..271 where f16 holds the scale.
   const uint32_t y02 = (vw & 0x00FF00FFu) + st.r02, y13 = (vw >> 8 & 0x00FF00FFu) + st.r13;
   const uint32_t over = (y02 + 240 * kHalves) | (y13 + 240 * kHalves);  // bit 9: y >= 272
   const uint32_t in = (y02 + 255 * kHalves) & (y13 + 255 * kHalves);    // bit 9: y >= 257
-  // weights: 2^(z - m + kBias), m the rows' reference maxima
-  float2 x[8];
-  {
+  bool plain = whole && (over & (512 * kHalves)) == 0 && (in & (512 * kHalves)) == 512 * kHalves;
+  const uint32_t h02 = (y02 - 256 * kHalves) << 10, h13 = (y13 - 256 * kHalves) << 10;
+  sts16(vcell, h02), sts16(vcell + 64, h13);
+  sts16(vcell + 128, h02 >> 16), sts16(vcell + 192, h13 >> 16);
+  // weights 2^(z - m + kBias), m the rows' reference maxima, taken as if nothing
+  // were uncommon
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float2 x[8];
     float z[16];
-    tmem_ld16(zt, z);
+    tmem_ld16(zt + 16 * mt, z);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 m = lds128f(mp + 16 * i);  // kBias - m
+      const float4 m = lds128f(w.refs + 64 * mt + 16 * i);  // kBias - m
       x[2 * i] = ffma2({z[4 * i], z[4 * i + 1]}, {qk, qk}, {m.x, m.y});
       x[2 * i + 1] = ffma2({z[4 * i + 2], z[4 * i + 3]}, {qk, qk}, {m.z, m.w});
     }
-  }
-  float top = fmaxf(x[0].x, x[0].y);
+    float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) top = fmax3(top, x[i].x, x[i].y);
-  const bool plain = whole && top <= kBias + kMaxGrow && (over & (512 * kHalves)) == 0 &&
-                     (in & (512 * kHalves)) == 512 * kHalves;
+    for (int i = 1; i < 8; ++i) top = fmax3(top, x[i].x, x[i].y);
+    plain = plain && top <= kBias + kMaxGrow;
+    put_weights(pbuf + mt * 1024, w.lane, x);
+  }
   bool more = false;
-  if (__builtin_expect(__all_sync(0xffffffffu, plain), 1)) {
-    const uint32_t h02 = (y02 - 256 * kHalves) << 10, h13 = (y13 - 256 * kHalves) << 10;
-    sts16(vcell, h02), sts16(vcell + 64, h13);
-    sts16(vcell + 128, h02 >> 16), sts16(vcell + 192, h13 >> 16);
-  } else {
-    more = adjust(st, x, zt, qk, n, lens, vw, vcell, scratch, lane);
+  if (__builtin_expect(!pair_all(w.bar, plain), 0)) {
+    more = adjust(st, w, zt, qk, n, vw, pbuf, vcell);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  uint32_t pk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(ex2_approx(x[i].x), ex2_approx(x[i].y));
-  // [token][16 rows]; the halves of rows 4..7 of each 8 swap places (banks)
-  const uint32_t prow = scratch + lane * 32, flip = (lane & 4) << 2;
-  sts128(prow + flip, pk[0], pk[1], pk[2], pk[3]);
-  sts128(prow + (16 ^ flip), pk[4], pk[5], pk[6], pk[7]);
   __syncwarp();
-  if (lane == 0) arrive(z_empty);
-  uint32_t pa[4], pb[4];  // rows g / g + 8, tokens 8o + 2t, + 1
-  const int row8 = lane & 7, mat = lane >> 3;
-  {
-    // matrices: octet 2k, 2k + 1 x row halves
-    const uint32_t at = scratch + ((mat >> 1) * 8 + row8) * 32 + (((mat & 1) << 4) ^ ((row8 & 4) << 2));
-    uint32_t r[4];
-    ldsm_x4_trans(r, at);
-    pa[0] = r[0], pb[0] = r[1], pa[1] = r[2], pb[1] = r[3];
-    ldsm_x4_trans(r, at + 512);
-    pa[2] = r[0], pb[2] = r[1], pa[3] = r[2], pb[3] = r[3];
-  }
-#pragma unroll
-  for (int ks = 0; ks < 2; ++ks)
-    mma_f16(st.l, pa[2 * ks], pb[2 * ks], pa[2 * ks + 1], pb[2 * ks + 1], 0x3C003C00u, 0x3C003C00u);
-
-  // -- O += P V
-  const int swz = (row8 >> 1) & 3;
-  const uint32_t vrow = vt + (mat * 8 + row8) * 64;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t zr[4];
-    ldsm_x4_trans(zr, vrow + ((c ^ swz) << 4));
-    const uint4 s4 = lds128(vp + c * 64 + t * 16);
-    const uint32_t vs[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      uint32_t v0[4], v1[4];
-      e2m1x4x2_to_f16x2(zr[2 * ks], v0);
-      e2m1x4x2_to_f16x2(zr[2 * ks + 1], v1);
-      const uint32_t a0 = hmul2(pa[2 * ks], vs[2 * ks]), a1 = hmul2(pb[2 * ks], vs[2 * ks]);
-      const uint32_t a2 = hmul2(pa[2 * ks + 1], vs[2 * ks + 1]), a3 = hmul2(pb[2 * ks + 1], vs[2 * ks + 1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mma_f16(st.o[4 * c + i], a0, a1, a2, a3, v0[i], v1[i]);
-    }
-  }
-  for (int band = 1; __builtin_expect(more, 0); ++band) {  // the lower bands of V's scales
-    __syncwarp();
-    more = odd_vscales(st, vw, vcell, band);
-    __syncwarp();
-    const float f = scale_pow2(1.f, -kBand * band);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t zr[4];
-      ldsm_x4_trans(zr, vrow + ((c ^ swz) << 4));
-      const uint4 s4 = lds128(vp + c * 64 + t * 16);
-      const uint32_t vs[4] = {s4.x, s4.y, s4.z, s4.w};
-      float y[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        uint32_t v0[4], v1[4];
-        e2m1x4x2_to_f16x2(zr[2 * ks], v0);
-        e2m1x4x2_to_f16x2(zr[2 * ks + 1], v1);
-        const uint32_t a0 = hmul2(pa[2 * ks], vs[2 * ks]), a1 = hmul2(pb[2 * ks], vs[2 * ks]);
-        const uint32_t a2 = hmul2(pa[2 * ks + 1], vs[2 * ks + 1]), a3 = hmul2(pb[2 * ks + 1], vs[2 * ks + 1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma_f16(y[i], a0, a1, a2, a3, v0[i], v1[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[4 * c + i][e] += y[i][e] * f;
-    }
+  if (w.lane == 0) arrive(z_empty);
+  multiply<MT, true>(st, pair, vt, w.member, w.lane, 1.f);
+  if (__builtin_expect(more, 0)) {
+    lower_bands(st, w, pair, vt, vw, vcell);
   }
 }
 
 // ---- the main kernel -----------------------------------------------------------
-template <int SETS>
+template <int MT>
 struct Bars {
+  static constexpr int NK = Smem<MT>::kKStages, NV = Smem<MT>::kVStages;
+  static_assert(2 * NK + 2 * NV + 5 <= 16);
   uint64_t* b;
   __device__ uint64_t* k_full(int i) const { return b + i; }
-  __device__ uint64_t* k_empty(int i) const { return b + kKStages + i; }
-  __device__ uint64_t* v_full(int i) const { return b + 2 * kKStages + i; }
-  __device__ uint64_t* v_empty(int i) const { return b + 2 * kKStages + kVStages + i; }
-  __device__ uint64_t* z_full(int i) const { return b + 2 * kKStages + 2 * kVStages + i; }
-  __device__ uint64_t* z_empty(int i) const { return b + 2 * kKStages + 2 * kVStages + 2 + i; }
-  __device__ uint64_t* q_full() const { return b + 2 * kKStages + 2 * kVStages + 4; }
+  __device__ uint64_t* k_empty(int i) const { return b + NK + i; }
+  __device__ uint64_t* v_full(int i) const { return b + 2 * NK + i; }
+  __device__ uint64_t* v_empty(int i) const { return b + 2 * NK + NV + i; }
+  __device__ uint64_t* z_full(int i) const { return b + 2 * NK + 2 * NV + i; }
+  __device__ uint64_t* z_empty(int i) const { return b + 2 * NK + 2 * NV + 2 + i; }
+  __device__ uint64_t* q_full() const { return b + 2 * NK + 2 * NV + 4; }
 };
 
-template <int SETS>
+template <int MT>
 constexpr int min_ctas() {
-  return SETS == 1 ? 3 : 1;
+  return 3;
 }
-// TMEM columns: two z buffers, the scale cells of K (per stage) and q
-template <int SETS>
+// TMEM columns: two z buffers, the scale cells of K and q
+template <int MT>
 struct Tmem {
-  static constexpr int z = 0, sk = 32 * SETS, sq = sk + 4 * kKStages, used = sq + 8;
-  static constexpr int columns = used <= 64 ? 64 : (used <= 128 ? 128 : 256);
+  static constexpr int z = 0, sk = 32 * MT, sq = sk + 4 * Smem<MT>::kKStages, used = sq + 8, columns = used <= 64 ? 64 : 128;
 };
 
-template <int SETS, bool Q16>
-__global__ void __launch_bounds__(Smem<SETS>::kThreads, min_ctas<SETS>())
+template <int MT, bool Q16>
+__global__ void __launch_bounds__(kThreads, min_ctas<MT>())
     dense_pa_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ Params p) {
-  using S = Smem<SETS>;
-  using T = Tmem<SETS>;
+  using S = Smem<MT>;
+  using T = Tmem<MT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int64_t s_sum[17];
-  __shared__ int64_t s_start[2];  // the share's first group and the blocks before it
-  __shared__ int s_nb;
-  __shared__ uint32_t s_tmem;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  // before the first block the pairs' place serves the scan
+  int64_t* s_sum = reinterpret_cast<int64_t*>(smem + S::pairs);  // [warps]
+  int64_t* s_start = s_sum + kCompute + 1;  // the share's first group, the blocks before it, its blocks
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
   const DensePaParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Bars<SETS> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
+  const Bars<MT> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
   if (tid == 0) {
-    for (int i = 0; i < kKStages; ++i) mbar_init(bars.k_full(i), 1), mbar_init(bars.k_empty(i), 1);
-    for (int i = 0; i < kVStages; ++i) mbar_init(bars.v_full(i), 1), mbar_init(bars.v_empty(i), S::kCompute);
-    for (int i = 0; i < 2; ++i) mbar_init(bars.z_full(i), 1), mbar_init(bars.z_empty(i), S::kCompute);
-    mbar_init(bars.q_full(), S::kCompute);
+    for (int i = 0; i < S::kKStages; ++i) mbar_init(bars.k_full(i), 1), mbar_init(bars.k_empty(i), 1);
+    for (int i = 0; i < S::kVStages; ++i) mbar_init(bars.v_full(i), 1), mbar_init(bars.v_empty(i), kCompute);
+    for (int i = 0; i < 2; ++i) mbar_init(bars.z_full(i), 1), mbar_init(bars.z_empty(i), kCompute);
+    mbar_init(bars.q_full(), kCompute);
     mbar_fence_init();
   }
   pdl_wait();
   pdl_trigger();
   // TMEM only after the wait: a CTA that held columns while it waited could
   // keep the kernel before it from getting its own
-  if (warp == S::kCompute) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+  if (warp == kCompute) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(const_cast<const uint32_t*>(misc + 4))),
                  "n"(T::columns));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
 
   // the groups' blocks, kThreads groups at a time: first their sum, then the
   // group the share starts in
-  const int64_t per = static_cast<int64_t>(a.hkv) * p.subs;
+  const int sub = blockIdx.x % p.subs, turn = blockIdx.x / p.subs;
   int64_t total = 0, at = 0, share = 0;
   for (int pass = 0; pass < 2; ++pass) {
     int64_t base = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += S::kThreads) {
+    for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
       const int g = g0 + tid;
       const int nb = g < p.groups ? blocks_of(a, group_len(a, g, 0, 1)) : 0;
       int64_t x = nb;
@@ -587,318 +671,325 @@ __global__ void __launch_bounds__(Smem<SETS>::kThreads, min_ctas<SETS>())
       if (lane == 31) s_sum[warp] = x;
       __syncthreads();
       int64_t before = base;
-      for (int w = 0; w <= S::kCompute; ++w) {
+      for (int w = 0; w <= kCompute; ++w) {
         if (w < warp) before += s_sum[w];
         base += s_sum[w];
       }
       const int64_t c1 = before + x, c0 = c1 - nb;  // blocks before and up to group g
-      if (pass == 0 && p.groups <= S::kThreads) {  // one tile: the sum and the start at once
+      if (pass == 0 && p.groups <= kThreads) {  // one tile: the sum and the start at once
         total = base;
-        share = (total * per + p.ctas - 1) / p.ctas;
-        at = blockIdx.x * share;
+        share = (total * a.hkv + p.shares - 1) / p.shares;
+        at = turn * share;
       }
-      if ((pass == 1 || p.groups <= S::kThreads) && nb && c0 * per <= at && at < c1 * per)
-        s_start[0] = g, s_start[1] = c0, s_nb = nb;
-      if (pass == 1 && base * per > at) break;
+      if ((pass == 1 || p.groups <= kThreads) && nb && c0 * a.hkv <= at && at < c1 * a.hkv)
+        s_start[0] = g, s_start[1] = c0, s_start[2] = nb;
+      if (pass == 1 && base * a.hkv > at) break;
     }
     if (pass == 0) {
       total = base;
-      share = (total * per + p.ctas - 1) / p.ctas;
-      at = blockIdx.x * share;
-      if (p.groups <= S::kThreads) break;
+      share = (total * a.hkv + p.shares - 1) / p.shares;
+      at = turn * share;
+      if (p.groups <= kThreads) break;
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = misc[4];
   Walk w;
-  w.at = at, w.end = min(at + share, total * per);
-  w.g = static_cast<int>(s_start[0]), w.c0 = s_start[1], w.nb = s_nb;  // unset, and unused, past the last share
+  w.at = at, w.end = min(at + share, total * a.hkv);
+  w.g = 0, w.c0 = 0, w.nb = 1;
+  if (w.at < w.end) w.g = static_cast<int>(s_start[0]), w.c0 = s_start[1], w.nb = static_cast<int>(s_start[2]);
+  __syncthreads();  // the pairs' place is theirs again
   // cut units: (first CTA, pieces) per unit, or (unit, pieces) per first CTA
   int2* cut = reinterpret_cast<int2*>(a.ws);
   if (!p.by_unit && tid == 0) cut[blockIdx.x] = make_int2(0, 0);
-  volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(smem + S::queue + kQueue * 8);  // per V stage
   bool alive = true;
 
-  if (warp == S::kCompute) {
+  if (warp == kCompute) {
     // ---- producer ----
-    struct Block {
-      int32_t id, head;  // head < 0: ~head, the first block of a piece
-    };
-    volatile Block* queue = reinterpret_cast<volatile Block*>(smem + S::queue);
+    // Lane 0 issues; the warp walks the share and reads the block table, 32
+    // entries at a time.  Loads run kAheadV and kAheadK blocks ahead of the MMAs.
+    // (One warp does all of it, and its code is out of the instruction cache
+    // most of the time: what counts here is few instructions.)
+    constexpr int kAheadV = S::kVStages - 1, kAheadK = S::kKStages, kAhead = std::max(kAheadV, kAheadK);
+    const uint32_t base = smem_u32(smem), k_full = smem_u32(bars.k_full(0)), k_empty = smem_u32(bars.k_empty(0));
+    const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0)), q_full = smem_u32(bars.q_full());
+    const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
+    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc));
+    const uint64_t k_desc = smem_desc_sw128(base), q_desc = smem_desc_sw128(base + S::q);
+    const int limit = static_cast<int>(min(a.num_blocks, int64_t{0x7FFFFFFF}));
+    // scales of tokens 32j + lane in K's unpacked rows 128..: 16 tokens a row, two an
+    // 8-byte piece, each piece in a 16-byte chunk at j ^ (row % 8)
+    uint32_t from[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int tok = 32 * j + lane, row = tok >> 4;
+      from[j] = base + (128 + row) * 128 + ((((tok & 15) >> 1) ^ (row & 7)) << 4) + (tok & 1) * 4;
+    }
     const int32_t* table = nullptr;
-    int nblk = 0, blk = 0, chunk = 0, head = 0;
+    int left = 0, at_id = 32, head = 0;  // blocks left of the piece, the next one's lane in ids
     int32_t ids = 0;
-    bool done = false, first = false;
-    int known = 0;  // blocks in the queue so far
-    auto learn = [&]() {  // the next block of the share; false at its end
-      while (!done && blk == nblk) {
-        if (!w.next(p, lane)) {
-          done = true;
-          break;
+    bool done = false;
+    // the next blocks to be multiplied: id (limit: a bad one, out of the map's
+    // range: its copies write zeros; kNone: none) and head (~head: the first of its piece)
+    constexpr int kNone = -1;
+    int q_id[kAhead + 1], q_head[kAhead + 1];
+    uint32_t vst = 0, v_phase = 1;  // of the next V load (an empty stage's wait passes at once)
+    uint32_t kst = 0, k_phase = 1;  // of the next K load
+    uint32_t mst = 0, m_phase = 0, z_phase = 1, q_phase = 0, buf = 0;  // of the next MMAs
+    auto learn = [&](int& id, int& hd) {  // the next block of the share
+      hd = head;
+      if (__builtin_expect(left == 0, 0)) {
+        while (left == 0 && !done) {
+          done = !w.next(p, sub, lane);
+          if (!done) {
+            table = a.block_table + static_cast<int64_t>(w.seq) * a.bt_stride + w.b0;
+            left = w.nblk, at_id = 32, head = w.h;
+          }
         }
-        table = a.block_table + static_cast<int64_t>(w.seq) * a.bt_stride + w.b0;
-        nblk = max(0, w.b1 - w.b0), blk = 0, chunk = -1, head = w.h, first = true;
+        id = kNone, hd = ~head;
+        if (done) return;
       }
-      if (done) return false;
-      if ((blk >> 5) != chunk) {
-        chunk = blk >> 5;
-        ids = 32 * chunk + lane < nblk ? table[32 * chunk + lane] : 0;
+      if (__builtin_expect(at_id == 32, 0)) {
+        ids = lane < left ? table[lane] : 0;
+        if (static_cast<uint32_t>(ids) >= static_cast<uint32_t>(limit)) {
+          set_err(a.err, BSP_DEVERR_BLOCK_ID);
+          ids = limit;
+        }
+        table += 32, at_id = 0;
       }
-      int32_t id = __shfl_sync(0xffffffffu, ids, blk & 31);
-      if (id < 0 || id >= a.num_blocks) {
-        if (lane == 0) set_err(a.err, BSP_DEVERR_BLOCK_ID);
-        id = -1;
+      id = __shfl_sync(0xffffffffu, ids, at_id);
+      ++at_id, --left;
+    };
+    auto load_v = [&](int id, int hd) {
+      if (alive) alive = wait_for(v_empty + 8 * vst, v_phase, a.err);
+      const uint32_t bar = v_full + 8 * vst;
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(bad_at + 4 * vst), "r"(static_cast<uint32_t>(id == limit)) : "memory");
+      fence_proxy_async();
+      arrive_expect(bar, kMxField);
+      tile_g2s(base + S::v + vst * kVTile, &map_v, hd ^ (hd >> 31), id, bar);
+      if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
+    };
+    auto load_k = [&](int id, int hd) {
+      if (alive) alive = wait_for(k_empty + 8 * kst, k_phase, a.err);
+      const uint32_t bar = k_full + 8 * kst;
+      arrive_expect(bar, kMxField);
+      tile_g2s(base + kst * kKTile, &map_k, hd ^ (hd >> 31), id, bar);
+      if (++kst == S::kKStages) kst = 0, k_phase ^= 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      learn(q_id[i], q_head[i]);
+      if (lane == 0 && q_id[i] != kNone) {
+        if (i < kAheadK) load_k(q_id[i], q_head[i]);
+        if (i < kAheadV) load_v(q_id[i], q_head[i]);
       }
-      if (lane == 0) queue[known % kQueue].id = id, queue[known % kQueue].head = first ? ~head : head;
-      first = false;
-      ++blk, ++known;
-      return true;
-    };
-    // a bad block's stages complete without data; the compute warps leave it out
-    auto load_k = [&](int i) {
-      const int st = i % kKStages;
-      const int32_t id = queue[i % kQueue].id, hh = queue[i % kQueue].head, h = hh < 0 ? ~hh : hh;
-      if (id < 0) return mbar_arrive(bars.k_full(st));
-      mbar_arrive_expect_tx(bars.k_full(st), kBlock * 64 + 512);
-      tile_g2s(smem + st * kKTile, &map_k, h, id, bars.k_full(st));
-      bulk_g2s(smem + S::ks + st * 512,
-               a.k_base + static_cast<int64_t>(id) * a.id_stride + static_cast<int64_t>(h) * kMxField + kMxScaleOff, 512,
-               bars.k_full(st));
-    };
-    auto load_v = [&](int i) {
-      const int st = i % kVStages;
-      const int32_t id = queue[i % kQueue].id, hh = queue[i % kQueue].head, h = hh < 0 ? ~hh : hh;
-      bad[st] = id < 0;
-      if (id < 0) return mbar_arrive(bars.v_full(st));
-      mbar_arrive_expect_tx(bars.v_full(st), kVTile + 512);
-      tile_g2s(smem + S::v + st * kVTile, &map_v, h, id, bars.v_full(st));
-      bulk_g2s(smem + S::vs + st * 512,
-               a.v_base + static_cast<int64_t>(id) * a.id_stride + static_cast<int64_t>(h) * kMxField + kMxScaleOff, 512,
-               bars.v_full(st));
-    };
-    // ahead of block 0: V of two blocks, K of one
-    for (int i = 0; i < 2; ++i)
-      if (learn() && lane == 0) load_v(i);
-    if (known > 0 && lane == 0) load_k(0);
-    const uint32_t q_addr = smem_u32(smem + S::q);
-    int pieces = 0;
-    for (int i = 0; i < known; ++i) {
-      const bool more = learn();  // block i + 2
+    }
+    uint32_t last = 0, last_phase = 0;  // the last MMAs' barrier
+#pragma unroll 1
+    while (q_id[0] != kNone) {
+      learn(q_id[kAhead], q_head[kAhead]);
+      // K is there: its scales from token order to the cells tcgen05.cp reads,
+      // lane i of column j = token 32j + i
+      if (alive) alive = wait_for(k_full + 8 * mst, m_phase, a.err);
+      const uint32_t off = mst * kKTile, cells = base + S::cells + mst * 512;
+      sts128(cells + lane * 16, lds32(from[0] + off), lds32(from[1] + off), lds32(from[2] + off), lds32(from[3] + off));
+      fence_proxy_async();
+      __syncwarp();
       if (lane == 0) {
-        const int st = i % kKStages, buf = i & 1;
-        const int32_t id = queue[i % kQueue].id;
-        if (queue[i % kQueue].head < 0) {
-          if (alive) alive = mbar_wait_sleep(bars.q_full(), pieces & 1, a.err);
-          ++pieces;
+        if (__builtin_expect(q_head[0] < 0, 0)) {
+          if (alive) alive = wait_for(q_full, q_phase, a.err);
+          q_phase ^= 1;
         }
-        if (alive && i + 1 < known) {  // K of the next block, once block i - 1's MMAs have left its stage
-          if (i > 0) alive = mbar_wait_sleep(bars.k_empty((i + 1) % kKStages), ((i - 1) / kKStages) & 1, a.err);
-          if (alive) load_k(i + 1);
-        }
-        if (alive) alive = mbar_wait_sleep(bars.k_full(st), (i / kKStages) & 1, a.err);
-        if (alive && i > 1) alive = mbar_wait_sleep(bars.z_empty(buf), ((i >> 1) - 1) & 1, a.err);
-        if (alive) {
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (id >= 0) {
-            const uint32_t k_addr = smem_u32(smem + st * kKTile), sk = tmem + T::sk + 4 * st;
-            scales_to_tmem(sk, smem_u32(smem + S::ks + st * 512));
+        if (alive) alive = wait_for(z_empty + 8 * buf, z_phase, a.err);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t sk = tmem + T::sk + 4 * mst, z = tmem + T::z + buf * S::kRows;
+        const uint64_t kd = k_desc + mst * (kKTile / 16);
+        scales_to_tmem(sk, cells);
 #pragma unroll
-            for (int part = 0; part < (Q16 ? 2 : 1); ++part)
+        for (int part = 0; part < (Q16 ? 2 : 1); ++part)
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                umma_mx(tmem + T::z + buf * S::kRows, smem_desc_sw128(k_addr + 32 * c),
-                        smem_desc_sw128(q_addr + part * S::kRows * 128 + 32 * c),
-                        idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, S::kRows, 128, c, c), sk, tmem + T::sq + 4 * part,
-                        part > 0 || c > 0);
-          }
-          umma_commit(bars.k_empty(st));
-          umma_commit(bars.z_full(buf));
-          if (more) {  // V of block i + 2, once the compute warps have left its stage
-            if (i + 2 >= kVStages)
-              alive = mbar_wait_sleep(bars.v_empty((i + 2) % kVStages), ((i + 2) / kVStages - 1) & 1, a.err);
-            if (alive) {
-              fence_proxy_async();
-              load_v(i + 2);
-            }
-          }
-        }
+          for (int c = 0; c < 4; ++c)
+            umma_mx(z, kd + 2 * c, q_desc + (part * S::kRows * 128 + 32 * c) / 16,
+                    idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, S::kRows, 128, c, c), sk, tmem + T::sq + 4 * part,
+                    part > 0 || c > 0);
+        commit(k_empty + 8 * mst);
+        commit(z_full + 8 * buf);
+        // K of kAheadK blocks on, once the MMAs that used its stage are done; V of
+        // kAheadV blocks on, once the compute warps have left its stage
+        if (q_id[kAheadK] != kNone) load_k(q_id[kAheadK], q_head[kAheadK]);
+        if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);
       }
+      last = k_empty + 8 * mst, last_phase = m_phase;
+      if (++mst == S::kKStages) mst = 0, m_phase ^= 1;
+      buf ^= 1, z_phase ^= buf ^ 1;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) q_id[j] = q_id[j + 1], q_head[j] = q_head[j + 1];
       __syncwarp();
     }
-    // nothing may still be writing shared memory or TMEM when the CTA leaves
-    if (lane == 0 && alive && known > 0)
-      mbar_wait_sleep(bars.k_empty((known - 1) % kKStages), ((known - 1) / kKStages) & 1, a.err);
+    // nothing may still write shared memory or TMEM when the CTA leaves
+    if (lane == 0 && alive && last) wait_for(last, last_phase, a.err);
     __syncwarp();
   } else {
     // ---- compute ----
-    const int set = warp >> 2, part = warp & 3;
-    const uint32_t scratch = smem_u32(smem + S::scratch) + warp * kScratch;
-    const uint32_t merge = smem_u32(smem + S::scratch) + set * S::kMerge;
+    const int member = warp & 1;
+    Place at_;
+    at_.pair = smem_u32(smem + S::pairs) + (warp >> 1) * 2 * S::kPair;
+    at_.refs = smem_u32(smem + S::refs) + warp * 2 * S::kRows * 4;
+    at_.tops = smem_u32(smem + S::tops) + (warp >> 1) * 2 * S::kTop;
+    at_.lens = smem_u32(smem + S::len);
+    at_.bar = 2 + (warp >> 1), at_.member = member, at_.lane = lane;
+    const uint32_t merge = smem_u32(smem + S::pairs) + member * S::kMergeWarp, sums = smem_u32(smem + S::sums);
     int* lens = reinterpret_cast<int*>(smem + S::len);
     uint8_t* cells = smem + S::sfq;
-    const uint32_t lane_base = static_cast<uint32_t>(32 * part) << 16;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0));
     const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
-    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(bad)), z_at = tmem + lane_base + T::z + 16 * set;
-    const uint32_t vs_at = smem_u32(smem + S::vs) + lane * 16 + part * 4, v_at = smem_u32(smem + S::v) + part * 2048;
+    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc)), z_at = tmem + lane_base + T::z;
+    // the token's scales: row 64 + warp of V's tile, 16-byte chunk lane / 4 at its swizzled place
+    const uint32_t vs_at = smem_u32(smem + S::v) + (64 + warp) * 128 + (((lane >> 2) ^ warp) << 4) + (lane & 3) * 4;
+    const uint32_t v_at = smem_u32(smem + S::v) + (warp >> 1) * 4096;
     uint32_t buf = 0, z_phase = 0, vst = 0, v_phase = 0;  // of the next block
-    while (w.next(p, lane)) {
-      const int nblk = max(0, w.b1 - w.b0);
-      bar_sync(1, 32 * S::kCompute);  // the last unit's q, lengths and merge buffers are no longer read
-      if (nblk) stage_q<Q16>(a, w.tok0, w.tokens, w.h, smem + S::q, S::kRows, cells, tid);
+    while (w.next(p, sub, lane)) {
+      bar_sync(1, 32 * kCompute);  // the last unit's q, lengths and merge buffers are no longer read
+      if (w.nblk)
+        for (int i = tid; i < S::kRows * 8; i += 32 * kCompute)
+          stage_q<Q16>(a, w.tok0, w.tokens, w.h, smem + S::q, S::kRows, cells, i);
       if (tid < S::kRows) {
         const int j = tid / a.group;
         lens[tid] = j < w.tokens ? min(max(a.row_len[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h], 0), w.max_len) : 0;
       }
-      if (tid == 0)
-        for (int j = 0; j < w.tokens; ++j)
-          if (a.row_seq[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h] != w.seq) set_err(a.err, BSP_DEVERR_GROUP_SEQ);
-      State st;
+      if (tid < w.tokens && a.row_seq[static_cast<int64_t>(w.tok0 + tid) * a.hkv + w.h] != w.seq)
+        set_err(a.err, BSP_DEVERR_GROUP_SEQ);
+      State<MT> st;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) st.o[k][0] = st.o[k][1] = st.o[k][2] = st.o[k][3] = 0.f;
-      st.l[0] = st.l[1] = st.l[2] = st.l[3] = 0.f;
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) st.o[mt][k][0] = st.o[mt][k][1] = st.o[mt][k][2] = st.o[mt][k][3] = 0.f;
+        st.l[mt][0] = st.l[mt][1] = st.l[mt][2] = st.l[mt][3] = 0.f;
+      }
       st.r02 = st.r13 = kNoScale;
-      if (lane < 16) stsf(scratch + 1280 + 4 * lane, kBias - kNoMax);
+      if (lane < S::kRows) stsf(at_.refs + 4 * lane, kBias - kNoMax);
       fence_proxy_async();  // the tensor core reads q through the async proxy
-      bar_sync(1, 32 * S::kCompute);
-      if (nblk) {
-        if (set == 0) {  // q's scale cells, in this sub-partition's copy
+      bar_sync(1, 32 * kCompute);
+      if (w.nblk) {
 #pragma unroll
-          for (int k = 0; k < (Q16 ? 2 : 1); ++k) {
-            uint32_t cell[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              cell[c] = 32 * c + lane < S::kRows
-                            ? *reinterpret_cast<const uint32_t*>(cells + (k * S::kRows + 32 * c + lane) * 4)
-                            : 0x7F7F7F7Fu;
-            tmem_st4(tmem + lane_base + T::sq + 4 * k, cell[0], cell[1], 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          }
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        for (int k = 0; k < (Q16 ? 2 : 1); ++k) {  // q's scale cells, in this sub-partition's copy
+          const uint32_t cell =
+              lane < S::kRows ? *reinterpret_cast<const uint32_t*>(cells + (k * S::kRows + lane) * 4) : 0x7F7F7F7Fu;
+          tmem_st4(tmem + lane_base + T::sq + 4 * k, cell, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.q_full());
       }
-      const uint32_t lens_at = smem_u32(lens + 16 * set);
-      int n = w.b0 * kBlock + 4 * lane + part;  // the lane's token
-      const int n_whole = w.min_len - (kBlock - 1) + (4 * lane + part);  // blocks up to here are whole for every row
-      for (int k = 0; k < nblk; ++k, n += kBlock) {
-        // one test of both barriers: V is there before z is
+      int n = w.b0 * kBlock + tid;                       // the lane's token
+      const int n_whole = w.min_len - (kBlock - 1) + tid;  // below: every row sees the block whole
+      const int max_len = w.max_len;
+      for (int k = w.nblk; k > 0; --k, n += kBlock) {
+        // after a timed-out wait the warp goes on without waits (the pair's
+        // barriers need both warps); its results are void
         if (alive) alive = wait_for(z_full + 8 * buf, z_phase, a.err) && wait_for(v_full + 8 * vst, v_phase, a.err);
-        alive = __all_sync(0xffffffffu, alive);  // the rest is warp-wide
-        if (!alive) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         if (lds32(bad_at + 4 * vst) == 0) {
-          uint32_t vw = lds32(vs_at + vst * 512);
-          if (n >= w.max_len) vw = 0;
-          attend(st, z_at + buf * S::kRows, z_empty + 8 * buf, p.qk_scale, n < n_whole, n, lens_at, vw,
-                 v_at + vst * kVTile, scratch, lane);
+          uint32_t vw = lds32(vs_at + vst * kVTile);
+          if (n >= max_len) vw = 0;
+          attend(st, at_, z_at + buf * S::kRows, z_empty + 8 * buf, p.qk_scale, n < n_whole, n, vw,
+                 v_at + vst * kVTile, buf);
         } else if (lane == 0) {
           arrive(z_empty + 8 * buf);
         }
         __syncwarp();
         if (lane == 0) arrive(v_empty + 8 * vst);
         buf ^= 1, z_phase ^= buf ^ 1;
-        if (++vst == kVStages) vst = 0, v_phase ^= 1;
+        if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
       }
 
-      // -- the four warps of a set joined: 1, 2, 3 hand theirs to 0 in turn
-      float m0 = kBias - ldsf(scratch + 1280 + 4 * g), m1 = kBias - ldsf(scratch + 1280 + 4 * (g + 8));
-      float l0 = st.l[0], l1 = st.l[2];  // every column of the tile is the sum
+      // -- the two pairs joined: warps 2 and 3 hand their O to 0 and 1
       const uint32_t rr[4] = {271 - (st.r02 & 0xFFFF), 271 - (st.r13 & 0xFFFF), 271 - (st.r02 >> 16),
                               271 - (st.r13 >> 16)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int e = static_cast<int>(rr[c]) - 127 + 14;
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int c = 0; c < 2; ++c) {
+          const int e = static_cast<int>(member ? rr[2 + c] : rr[c]) - 127 + 14;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) st.o[4 * c + k][j] = scale_pow2(st.o[4 * c + k][j], e);
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) st.o[mt][4 * c + k][j] = scale_pow2(st.o[mt][4 * c + k][j], e);
+        }
+        if (t == 0) {  // every column of the tile is the sum
+          stsf(sums + (warp * S::kRows + 16 * mt + g) * 4, st.l[mt][0]);
+          stsf(sums + (warp * S::kRows + 16 * mt + g + 8) * 4, st.l[mt][2]);
+        }
       }
-      bar_sync(1, 32 * S::kCompute);  // the scratch becomes the merge buffers
-      const uint32_t mrow = merge + (g * kRowPad + 8 * t) * 4, mml = merge + 16 * kRowPad * 4;
-      for (int k = 1; k < 4; ++k) {
-        if (part == k) {
+      bar_sync(1, 32 * kCompute);  // the pairs' place becomes the merge buffer
+      const uint32_t mrow = merge + (g * kRowPad + 8 * t) * 4;
+      if (warp >= 2) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                sts128(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4, __float_as_uint(st.o[4 * c][2 * e + j]),
-                       __float_as_uint(st.o[4 * c + 1][2 * e + j]), __float_as_uint(st.o[4 * c + 2][2 * e + j]),
-                       __float_as_uint(st.o[4 * c + 3][2 * e + j]));
-          if (t == 0) {
-            stsf(mml + 8 * g, m0), stsf(mml + 8 * g + 4, l0);
-            stsf(mml + 8 * (g + 8), m1), stsf(mml + 8 * (g + 8) + 4, l1);
-          }
-        }
-        bar_sync(2 + set, 128);
-        if (part == 0) {
-          const float n0 = ldsf(mml + 8 * g), n1 = ldsf(mml + 8 * (g + 8));
-          const float M0 = fmaxf(m0, n0), M1 = fmaxf(m1, n1);
-          const float f0 = ex2_approx(m0 - M0), f1 = ex2_approx(m1 - M1), h0 = ex2_approx(n0 - M0), h1 = ex2_approx(n1 - M1);
-          l0 = l0 * f0 + h0 * ldsf(mml + 8 * g + 4);
-          l1 = l1 * f1 + h1 * ldsf(mml + 8 * (g + 8) + 4);
-          m0 = M0, m1 = M1;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float4 y = lds128f(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4);
-                const float f = e ? f1 : f0, hh = e ? h1 : h0;
-                st.o[4 * c][2 * e + j] = st.o[4 * c][2 * e + j] * f + y.x * hh;
-                st.o[4 * c + 1][2 * e + j] = st.o[4 * c + 1][2 * e + j] * f + y.y * hh;
-                st.o[4 * c + 2][2 * e + j] = st.o[4 * c + 2][2 * e + j] * f + y.z * hh;
-                st.o[4 * c + 3][2 * e + j] = st.o[4 * c + 3][2 * e + j] * f + y.w * hh;
-              }
-        }
-        bar_sync(2 + set, 128);
+                sts128(mrow + ((16 * mt + 8 * e) * kRowPad + 32 * c + 4 * j) * 4, __float_as_uint(st.o[mt][4 * c][2 * e + j]),
+                       __float_as_uint(st.o[mt][4 * c + 1][2 * e + j]), __float_as_uint(st.o[mt][4 * c + 2][2 * e + j]),
+                       __float_as_uint(st.o[mt][4 * c + 3][2 * e + j]));
       }
-      if (part == 0) {
+      bar_sync(1, 32 * kCompute);
+      if (warp < 2) {
         // a CTA's slots: 2 * CTA for a unit that began before its share, + 1
         // for one that goes on after it
         float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
                     (2LL * blockIdx.x + (w.starts ? 1 : 0)) * S::kRows * (kDim + 2);
         const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 16 * set + g + 8 * e;
-          if (r >= w.tokens * a.group) continue;
-          const float l = e ? l1 : l0;
-          if (w.starts && w.ends) {
-            const float f = l > 0.f ? 1.f / l : 0.f;
-            uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                            ((w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group) * kDim + 8 * t;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(dst + 32 * c) =
-                  make_uint4(pack_bf16x2(st.o[4 * c][2 * e] * f, st.o[4 * c + 1][2 * e] * f),
-                             pack_bf16x2(st.o[4 * c + 2][2 * e] * f, st.o[4 * c + 3][2 * e] * f),
-                             pack_bf16x2(st.o[4 * c][2 * e + 1] * f, st.o[4 * c + 1][2 * e + 1] * f),
-                             pack_bf16x2(st.o[4 * c + 2][2 * e + 1] * f, st.o[4 * c + 3][2 * e + 1] * f));
-          } else {
-            float* dst = po + r * kDim + 8 * t;
+          for (int e = 0; e < 2; ++e) {
+            const int r = 16 * mt + 8 * e + g;
+            if (r >= w.tokens * a.group) continue;
+            const float m0 = kBias - ldsf(at_.refs + 4 * r);
+            const float m1 = kBias - ldsf(smem_u32(smem + S::refs) + (2 * 2 * S::kRows + r) * 4);
+            const float M = fmaxf(m0, m1), f0 = ex2_approx(m0 - M), f1 = ex2_approx(m1 - M);
+            const float l = f0 * (ldsf(sums + r * 4) + ldsf(sums + (S::kRows + r) * 4)) +
+                            f1 * (ldsf(sums + (2 * S::kRows + r) * 4) + ldsf(sums + (3 * S::kRows + r) * 4));
+            const bool all = w.starts && w.ends;
+            const float inv = all ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c) {
+              float x[8];
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<float4*>(dst + 32 * c + 4 * j) =
-                    make_float4(st.o[4 * c][2 * e + j], st.o[4 * c + 1][2 * e + j], st.o[4 * c + 2][2 * e + j],
-                                st.o[4 * c + 3][2 * e + j]);
-            if (t == 0) *reinterpret_cast<float2*>(po + S::kRows * kDim + 2 * r) = make_float2(e ? m1 : m0, l);
+              for (int j = 0; j < 2; ++j) {
+                const float4 y = lds128f(mrow + ((16 * mt + 8 * e) * kRowPad + 32 * c + 4 * j) * 4);
+                x[4 * j] = (st.o[mt][4 * c][2 * e + j] * f0 + y.x * f1) * inv;
+                x[4 * j + 1] = (st.o[mt][4 * c + 1][2 * e + j] * f0 + y.y * f1) * inv;
+                x[4 * j + 2] = (st.o[mt][4 * c + 2][2 * e + j] * f0 + y.z * f1) * inv;
+                x[4 * j + 3] = (st.o[mt][4 * c + 3][2 * e + j] * f0 + y.w * f1) * inv;
+              }
+              const int d = 64 * member + 32 * c + 8 * t;
+              if (all) {
+                const int64_t row = (w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group;
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * kDim + d) =
+                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                               pack_bf16x2(x[6], x[7]));
+              } else {
+                *reinterpret_cast<float4*>(po + r * kDim + d) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(po + r * kDim + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+              }
+            }
+            if (!all && member == 0 && t == 0)
+              *reinterpret_cast<float2*>(po + S::kRows * kDim + 2 * r) = make_float2(M, l);
           }
-        }
       }
       if (w.starts && tid == 0) {
         // the pieces of the unit: shares from this one to that of its last block
-        const int pieces =
-            w.ends ? 0 : static_cast<int>((static_cast<int64_t>(w.c0) * per + (w.unit - w.g * per + 1) * w.nb - 1) / share -
-                                          blockIdx.x + 1);
+        const int64_t last = w.c0 * a.hkv + static_cast<int64_t>(w.h + 1) * w.nb - 1;
+        const int pieces = w.ends ? 0 : static_cast<int>(last / share) - turn + 1;
         if (p.by_unit)
           cut[w.unit] = make_int2(blockIdx.x, pieces);
         else if (pieces)
@@ -908,7 +999,7 @@ __global__ void __launch_bounds__(Smem<SETS>::kThreads, min_ctas<SETS>())
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == S::kCompute) {
+  if (warp == kCompute) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(T::columns));
   }
@@ -931,7 +1022,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
   const int2 info = reinterpret_cast<const int2*>(a.ws)[item];
   const int pieces = info.y, c0 = p.by_unit ? info.x : item, unit = p.by_unit ? item : info.x;
   if (pieces == 0) return;
-  const int per = a.hkv * p.subs, g = unit / per, h = unit % per / p.subs, sub = unit % p.subs;
+  const int sub = unit % p.subs, h = unit / p.subs % a.hkv, g = unit / p.subs / a.hkv;
   const int64_t tok0 = static_cast<int64_t>(g) * a.q_group + sub * p.sub_tokens;
   const int tokens = static_cast<int>(
       min(static_cast<int64_t>(min(p.sub_tokens, a.q_group - sub * p.sub_tokens)), a.num_rows / a.hkv - tok0));
@@ -945,7 +1036,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
     for (int k0 = part; k0 < pieces; k0 += 32 * parts) {
       // lane j: piece k0 + j * parts
       const int k = k0 + lane * parts;
-      const int64_t slot = k == 0 ? 2LL * c0 + 1 : 2LL * (c0 + k);
+      const int64_t slot = k == 0 ? 2LL * c0 + 1 : 2LL * (c0 + static_cast<int64_t>(k) * p.subs);
       float2 ml = make_float2(kNoMax, 0.f);
       if (k < pieces) ml = *reinterpret_cast<const float2*>(base + slot * slot_floats + rows_pad * kDim + 2 * row);
       float mx = ml.x;
@@ -962,7 +1053,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
 #pragma unroll 8
       for (int j = 0; j < here; ++j) {
         const int kj = k0 + j * parts;
-        const int64_t sj = kj == 0 ? 2LL * c0 + 1 : 2LL * (c0 + kj);
+        const int64_t sj = kj == 0 ? 2LL * c0 + 1 : 2LL * (c0 + static_cast<int64_t>(kj) * p.subs);
         const float wj = __shfl_sync(0xffffffffu, w, j);
         const float4 y = *reinterpret_cast<const float4*>(base + sj * slot_floats + row * kDim + 4 * lane);
         x.x += wj * y.x, x.y += wj * y.y, x.z += wj * y.z, x.w += wj * y.w;
@@ -993,25 +1084,26 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
 }
 
 // ---- host ------------------------------------------------------------------------
-// One side of the cache as [blocks][heads][4][32][row]: row 32j + i of a box
-// is token 4i + j.  K's rows are 128 4-bit values, unpacked to 16-byte slots of
-// 16 with 128-byte swizzle; V's are 64 bytes, 64-byte swizzle.
+// One side of the cache as [blocks][heads][rows][row].  K: a row is a token's 128
+// 4-bit values, unpacked to 16-byte slots of 16; V: 128 bytes, two tokens (half
+// the rows for the copy engine to fetch).  128-byte swizzle.
 bool make_map_side(CUtensorMap* m, bool unpack, const void* base, uint64_t heads, uint64_t blocks, uint64_t stride) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[5] = {unpack ? 128u : 64u, 32, 4, heads, blocks};
-  const cuuint64_t strides[4] = {256, 64, kMxField, stride};
-  const cuuint32_t box[5] = {unpack ? 128u : 64u, 32, 4, 1, 1};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(m, unpack ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5,
+  const uint32_t rows = unpack ? kKRows : kVRows;
+  const cuuint64_t dims[4] = {128, rows, heads, blocks};
+  const cuuint64_t strides[3] = {unpack ? 64u : 128u, kMxField, stride};
+  const cuuint32_t box[4] = {128, rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, unpack ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            unpack ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 // how a group's rows are cut into units
 struct Plan {
-  int sub_tokens, subs, sets;
+  int sub_tokens, subs, mt;
 };
 Plan plan_of(int group, int q_group) {
   const int sub = std::min(q_group, kMaxRows / group), subs = (q_group + sub - 1) / sub;
@@ -1022,41 +1114,28 @@ Plan plan_of(int group, int q_group) {
 // CTAs per SM: what the register bound allows, as far as shared memory holds
 // them (TMEM: 512 columns).  The occupancy query answers 1 for a kernel that
 // allocates TMEM.
-template <int SETS, bool Q16>
+template <int MT, bool Q16>
 constexpr int ctas_per_sm() {
-  return std::min(min_ctas<SETS>(), 228 * 1024 / (Smem<SETS>::total(Q16) + 1024 + 256));
+  return std::min(min_ctas<MT>(), 228 * 1024 / (Smem<MT>::total(Q16) + 1024));
 }
-int ctas_of(int sets, bool q16) {
-  switch (sets) {
-    case 1:
-      return q16 ? ctas_per_sm<1, true>() : ctas_per_sm<1, false>();
-    case 2:
-      return q16 ? ctas_per_sm<2, true>() : ctas_per_sm<2, false>();
-    case 3:
-      return q16 ? ctas_per_sm<3, true>() : ctas_per_sm<3, false>();
-    default:
-      return q16 ? ctas_per_sm<4, true>() : ctas_per_sm<4, false>();
-  }
+static_assert(ctas_per_sm<1, false>() == 3 && ctas_per_sm<1, true>() == 3 && ctas_per_sm<2, false>() == 3 &&
+              ctas_per_sm<2, true>() == 3);
+int ctas_of(int mt, bool q16) {
+  return mt == 1 ? (q16 ? ctas_per_sm<1, true>() : ctas_per_sm<1, false>())
+                 : (q16 ? ctas_per_sm<2, true>() : ctas_per_sm<2, false>());
 }
 
-template <int SETS, bool Q16>
+template <int MT, bool Q16>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
-  static_assert(Smem<SETS>::total(Q16) <= 227 * 1024 && Tmem<SETS>::used <= Tmem<SETS>::columns);
+  static_assert(Tmem<MT>::used <= Tmem<MT>::columns && Tmem<MT>::columns * min_ctas<MT>() <= 512);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {  // the shared-memory opt-in
-    return cudaFuncSetAttribute(dense_pa_kernel<SETS, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<SETS>::total(Q16));
+    return cudaFuncSetAttribute(dense_pa_kernel<MT, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<MT>::total(Q16));
   });
   if (e != cudaSuccess) return e;
-  return launch_kernel(dense_pa_kernel<SETS, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(Smem<SETS>::kThreads),
-                       Smem<SETS>::total(Q16), s, 0, mk, mv, p);
-}
-template <bool Q16>
-cudaError_t launch_sets(int sets, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
-  return sets == 1   ? launch_main<1, Q16>(mk, mv, p, s)
-         : sets == 2 ? launch_main<2, Q16>(mk, mv, p, s)
-         : sets == 3 ? launch_main<3, Q16>(mk, mv, p, s)
-                     : launch_main<4, Q16>(mk, mv, p, s);
+  return launch_kernel(dense_pa_kernel<MT, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
+                       Smem<MT>::total(Q16), s, 0, mk, mv, p);
 }
 
 }  // namespace
@@ -1064,8 +1143,8 @@ cudaError_t launch_sets(int sets, const CUtensorMap& mk, const CUtensorMap& mv, 
 size_t dense_pa_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms) {
   (void)num_rows, (void)hkv;
   const Plan pl = plan_of(group, q_group);
-  const int64_t ctas = static_cast<int64_t>(std::max(ctas_of(pl.sets, false), ctas_of(pl.sets, true))) * num_sms;
-  return list_bytes(ctas) + 2 * ctas * 16 * pl.sets * (kDim + 2) * sizeof(float);
+  const int64_t ctas = static_cast<int64_t>(std::max(ctas_of(pl.mt, false), ctas_of(pl.mt, true))) * num_sms;
+  return list_bytes(ctas) + 2 * ctas * 16 * pl.mt * (kDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s, int* launches) {
@@ -1079,28 +1158,30 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   p.groups = (tokens + a.q_group - 1) / a.q_group;
   p.subs = pl.subs;
   p.sub_tokens = pl.sub_tokens;
-  const int64_t units = static_cast<int64_t>(p.groups) * a.hkv * pl.subs;
+  const int64_t pairs = static_cast<int64_t>(p.groups) * a.hkv, units = pairs * pl.subs;
   if (units > INT32_MAX) return cudaErrorNotSupported;
   p.units = static_cast<int32_t>(units);
-  const int per_sm = ctas_of(pl.sets, q16);
-  p.ctas = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(per_sm) * num_sms, units * a.bt_stride));
+  p.shares = static_cast<int32_t>(
+      std::min<int64_t>(static_cast<int64_t>(ctas_of(pl.mt, q16)) * num_sms / pl.subs, pairs * a.bt_stride));
+  p.ctas = p.shares * pl.subs;
   p.by_unit = units <= p.ctas;
   CUtensorMap mk, mv;
   const uint64_t blocks = std::max<int64_t>(a.num_blocks, 1);
   if (!make_map_side(&mk, true, a.k_base, a.hkv, blocks, a.id_stride) ||
       !make_map_side(&mv, false, a.v_base, a.hkv, blocks, a.id_stride))
     return cudaErrorInvalidValue;
-  cudaError_t e = q16 ? launch_sets<true>(pl.sets, mk, mv, p, s) : launch_sets<false>(pl.sets, mk, mv, p, s);
+  cudaError_t e = pl.mt == 1 ? (q16 ? launch_main<1, true>(mk, mv, p, s) : launch_main<1, false>(mk, mv, p, s))
+                             : (q16 ? launch_main<2, true>(mk, mv, p, s) : launch_main<2, false>(mk, mv, p, s));
   if (e != cudaSuccess) return e;
   ++*launches;
-  if (p.ctas > 1) {
-    // pieces of a unit are about ctas / units: more warps a row where they are many
-    const int64_t pieces = std::min<int64_t>(p.ctas / units + 1, a.bt_stride);
+  if (p.shares > 1) {
+    // pieces of a unit are about shares / (groups x heads): more warps a row where they are many
+    const int64_t pieces = std::min<int64_t>(p.shares / pairs + 1, a.bt_stride);
     const int parts = pieces >= 64 ? 8 : (pieces >= 32 ? 4 : (pieces >= 16 ? 2 : 1));
     const int64_t chunks = (pl.sub_tokens * a.group + 8 / parts - 1) / (8 / parts);
     const int64_t items = p.by_unit ? units : p.ctas;
     e = launch_kernel(dense_pa_join_kernel, dim3(static_cast<unsigned>(items * chunks)), dim3(256), 0, s, 0, p,
-                      16 * pl.sets, parts);
+                      16 * pl.mt, parts);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
