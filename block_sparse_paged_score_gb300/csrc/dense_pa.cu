@@ -83,32 +83,33 @@ struct Params {
 
 // ---- shared memory -----------------------------------------------------------
 constexpr int kCompute = 4;  // warps
-constexpr int kThreads = 32 * (kCompute + 1);
-// A K stage is free again as soon as its MMAs are done, a block ahead of the
-// weights, so K has fewer stages than V
+// a pair's buffer: P [part][tile][32 tokens][16 rows] f16, V's scales
+// [part][c][4][4][2] f16; a warp's maxima: its rows', then four of scales
 template <int MT>
+struct Pair {
+  static constexpr int kP = 2 * MT * 1024, kBytes = kP + 512, kTop = 16 * MT * 4 + 16;
+};
+constexpr int kThreads = 32 * (kCompute + 1);
+// (as much as three CTAs an SM leave room for)
+template <int MT, bool Q16>
 struct Smem {
   static constexpr int kRows = 16 * MT;
-  static constexpr int kKStages = MT == 1 ? 2 : 1, kVStages = MT == 1 ? 2 : 3;
+  static constexpr int kKStages = MT == 1 ? 2 : 1, kVStages = MT == 1 && Q16 ? 2 : 3;
   static constexpr int v = kKStages * kKTile;
-  static constexpr int cells = v + kVStages * kVTile;  // K's scales as TMEM cells, per stage
-  // per pair of warps, twice: P [part][tile][32 tokens][16 rows] f16, then V's
-  // scales [part][c][4][4][2] f16
-  static constexpr int kP = 2 * MT * 1024, kPair = kP + 512;
-  static constexpr int pairs = cells + kKStages * 512;
+  // two buffers per pair of warps
+  static constexpr int pairs = v + kVStages * kVTile;
   // the pairs' place is the merge buffer once a unit's blocks are done
   static constexpr int kMergeWarp = kRows * kRowPad * 4;
-  static constexpr int pairs_bytes = std::max(4 * kPair, 2 * kMergeWarp);
+  static constexpr int pairs_bytes = std::max(4 * Pair<MT>::kBytes, 2 * kMergeWarp);
   static constexpr int refs = pairs + pairs_bytes;          // per warp: reference maxima, rescale factors
   static constexpr int tops = refs + kCompute * 2 * kRows * 4;  // per warp: row maxima, 4 scale maxima
-  static constexpr int kTop = kRows * 4 + 16;
-  static constexpr int sums = tops + kCompute * kTop;       // per warp: l
+  static constexpr int sums = tops + kCompute * Pair<MT>::kTop;       // per warp: l
   static constexpr int len = sums + kCompute * kRows * 4;   // [rows] lengths
   static constexpr int sfq = len + kRows * 4;               // [2][rows] scale cells of q
   static constexpr int bars = sfq + 2 * kRows * 4;
   static constexpr int misc = bars + 16 * 8;                // bad[4], TMEM address
   static constexpr int q = (misc + 32 + 1023) / 1024 * 1024;
-  static constexpr int total(bool q16) { return q + kRows * 128 * (q16 ? 2 : 1) + 1024; }
+  static constexpr int total = q + kRows * 128 * (Q16 ? 2 : 1);
 };
 
 // ---- device helpers ------------------------------------------------------------
@@ -197,8 +198,17 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t
   set_err(err, BSP_DEVERR_TIMEOUT);
   return false;
 }
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t* err) {
-  if (__builtin_expect(try_wait(bar, parity), 1)) return true;
+  if (__builtin_expect(test_wait(bar, parity), 1)) return true;
   return wait_slow(bar, parity, err);
 }
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
@@ -404,7 +414,7 @@ template <int MT>
 __device__ __forceinline__ bool adjust(State<MT>& st, const Place& w, uint32_t zt, float qk, int n, uint32_t vw,
                                     uint32_t pbuf, uint32_t vcell) {
   constexpr int kRows = 16 * MT;
-  const uint32_t mine = w.tops + w.member * Smem<MT>::kTop;
+  const uint32_t mine = w.tops + w.member * Pair<MT>::kTop;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     float z[16];
@@ -427,7 +437,7 @@ __device__ __forceinline__ bool adjust(State<MT>& st, const Place& w, uint32_t z
   for (int c = 0; c < 4; ++c) {
     const uint32_t at = w.tops + kRows * 4 + 4 * c;
     const uint32_t old = 271 - ((c & 1 ? st.r13 : st.r02) >> (c & 2 ? 16 : 0) & 0xFFFF);
-    now[c] = max(old, max(lds32(at), lds32(at + Smem<MT>::kTop)));
+    now[c] = max(old, max(lds32(at), lds32(at + Pair<MT>::kTop)));
     if (now[c] != old && (c >> 1) == w.member) {
       const float f = scale_pow2(1.f, static_cast<int>(old) - static_cast<int>(now[c]));
 #pragma unroll
@@ -449,7 +459,7 @@ __device__ __forceinline__ bool adjust(State<MT>& st, const Place& w, uint32_t z
     for (int i = 0; i < 16; ++i) {
       const int r = 16 * mt + i;
       const float y = n < static_cast<int>(lds32(w.lens + r * 4)) ? z[i] * qk : -INFINITY;
-      const float mx = fmaxf(ldsf(w.tops + r * 4), ldsf(w.tops + Smem<MT>::kTop + r * 4));
+      const float mx = fmaxf(ldsf(w.tops + r * 4), ldsf(w.tops + Pair<MT>::kTop + r * 4));
       const float old = ldsf(w.refs + r * 4);  // kBias - m
       const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
       (i & 1 ? x[i >> 1].y : x[i >> 1].x) = y + ref;
@@ -477,7 +487,7 @@ __device__ __forceinline__ void multiply(State<MT>& st, uint32_t pair, uint32_t 
   const uint32_t prow = pair + ((mat >> 1) * 8 + row8) * 32 + (((mat & 1) << 4) ^ ((row8 & 4) << 2));
   // V rows of 128 bytes hold two tokens; 16-byte chunk j of row r is at j ^ (r % 8)
   const int vr = mat * 4 + (row8 >> 1);
-  const uint32_t vrow = vt + vr * 128 + ((((row8 & 1) * 4 + 2 * member) ^ (vr & 7)) << 4), vsc = pair + Smem<MT>::kP + member * 128 + t * 16;
+  const uint32_t vrow = vt + vr * 128 + ((((row8 & 1) * 4 + 2 * member) ^ (vr & 7)) << 4), vsc = pair + Pair<MT>::kP + member * 128 + t * 16;
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
     uint32_t pf[MT][2][4];  // A fragments (rows g, g + 8 x token octets), k-steps 0 and 1 of the part
@@ -550,8 +560,8 @@ __device__ __forceinline__ void lower_bands(State<MT>& st, const Place& w, uint3
 template <int MT>
 __device__ __forceinline__ void attend(State<MT>& st, const Place& w, uint32_t zt, uint32_t z_empty, float qk,
                                        bool whole, int n, uint32_t vw, uint32_t vt, uint32_t buf) {
-  const uint32_t pair = w.pair + buf * Smem<MT>::kPair, pbuf = pair + w.member * MT * 1024;
-  const uint32_t vcell = pair + Smem<MT>::kP + w.member * 256 + ((w.lane >> 1) & 3) * 16 + (w.lane >> 3) * 4 +
+  const uint32_t pair = w.pair + buf * Pair<MT>::kBytes, pbuf = pair + w.member * MT * 1024;
+  const uint32_t vcell = pair + Pair<MT>::kP + w.member * 256 + ((w.lane >> 1) & 3) * 16 + (w.lane >> 3) * 4 +
                          (w.lane & 1) * 2;  // [part][c][pair of tokens][octet][2]
   // V's scales as f16 2^(byte - R_c): exponent fields 1..15, two groups a word.
   // y = byte + 271 - R_c; in 257..271 where f16 holds the scale.
@@ -595,9 +605,9 @@ __device__ __forceinline__ void attend(State<MT>& st, const Place& w, uint32_t z
 }
 
 // ---- the main kernel -----------------------------------------------------------
-template <int MT>
+template <int MT, bool Q16>
 struct Bars {
-  static constexpr int NK = Smem<MT>::kKStages, NV = Smem<MT>::kVStages;
+  static constexpr int NK = Smem<MT, Q16>::kKStages, NV = Smem<MT, Q16>::kVStages;
   static_assert(2 * NK + 2 * NV + 5 <= 16);
   uint64_t* b;
   __device__ uint64_t* k_full(int i) const { return b + i; }
@@ -611,29 +621,28 @@ struct Bars {
 
 template <int MT>
 constexpr int min_ctas() {
-  return 3;
+  return 3;  // 128 registers a thread
 }
 // TMEM columns: two z buffers, the scale cells of K and q
-template <int MT>
+template <int MT, bool Q16>
 struct Tmem {
-  static constexpr int z = 0, sk = 32 * MT, sq = sk + 4 * Smem<MT>::kKStages, used = sq + 8, columns = used <= 64 ? 64 : 128;
+  static constexpr int z = 0, sk = 32 * MT, sq = sk + 4 * Smem<MT, Q16>::kKStages, used = sq + 8, columns = used <= 64 ? 64 : 128;
 };
 
 template <int MT, bool Q16>
 __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
     dense_pa_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ Params p) {
-  using S = Smem<MT>;
-  using T = Tmem<MT>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  using S = Smem<MT, Q16>;
+  using T = Tmem<MT, Q16>;
+  extern __shared__ __align__(1024) uint8_t smem[];  // (all of it: no static shared memory moves its start)
   // before the first block the pairs' place serves the scan
   int64_t* s_sum = reinterpret_cast<int64_t*>(smem + S::pairs);  // [warps]
   int64_t* s_start = s_sum + kCompute + 1;  // the share's first group, the blocks before it, its blocks
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
   const DensePaParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Bars<MT> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
+  const Bars<MT, Q16> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
   if (tid == 0) {
     for (int i = 0; i < S::kKStages; ++i) mbar_init(bars.k_full(i), 1), mbar_init(bars.k_empty(i), 1);
     for (int i = 0; i < S::kVStages; ++i) mbar_init(bars.v_full(i), 1), mbar_init(bars.v_empty(i), kCompute);
@@ -709,10 +718,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
   if (warp == kCompute) {
     // ---- producer ----
     // Lane 0 issues; the warp walks the share and reads the block table, 32
-    // entries at a time.  Loads run kAheadV and kAheadK blocks ahead of the MMAs.
+    // entries at a time.  K is loaded kAhead blocks ahead of the MMAs, V kAheadV: a
+    // block less than its stages would hold, so that waiting for a stage does not
+    // hold up the next MMAs.
     // (One warp does all of it, and its code is out of the instruction cache
     // most of the time: what counts here is few instructions.)
-    constexpr int kAheadV = S::kVStages - 1, kAheadK = S::kKStages, kAhead = std::max(kAheadV, kAheadK);
+    constexpr int kAheadV = S::kVStages - 2, kAhead = S::kKStages;
+    static_assert(kAheadV <= kAhead);
     const uint32_t base = smem_u32(smem), k_full = smem_u32(bars.k_full(0)), k_empty = smem_u32(bars.k_empty(0));
     const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0)), q_full = smem_u32(bars.q_full());
     const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
@@ -782,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
     for (int i = 0; i < kAhead; ++i) {
       learn(q_id[i], q_head[i]);
       if (lane == 0 && q_id[i] != kNone) {
-        if (i < kAheadK) load_k(q_id[i], q_head[i]);
+        load_k(q_id[i], q_head[i]);
         if (i < kAheadV) load_v(q_id[i], q_head[i]);
       }
     }
@@ -793,8 +805,10 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
       // K is there: its scales from token order to the cells tcgen05.cp reads,
       // lane i of column j = token 32j + i
       if (alive) alive = wait_for(k_full + 8 * mst, m_phase, a.err);
-      const uint32_t off = mst * kKTile, cells = base + S::cells + mst * 512;
-      sts128(cells + lane * 16, lds32(from[0] + off), lds32(from[1] + off), lds32(from[2] + off), lds32(from[3] + off));
+      const uint32_t off = mst * kKTile, cells = base + off + kBlock * 128;  // (in their own rows)
+      const uint32_t cell[4] = {lds32(from[0] + off), lds32(from[1] + off), lds32(from[2] + off), lds32(from[3] + off)};
+      __syncwarp();
+      sts128(cells + lane * 16, cell[0], cell[1], cell[2], cell[3]);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
@@ -816,10 +830,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
                     part > 0 || c > 0);
         commit(k_empty + 8 * mst);
         commit(z_full + 8 * buf);
-        // K of kAheadK blocks on, once the MMAs that used its stage are done; V of
-        // kAheadV blocks on, once the compute warps have left its stage
-        if (q_id[kAheadK] != kNone) load_k(q_id[kAheadK], q_head[kAheadK]);
-        if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);
+        if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);  // once the compute warps have left its stage
+        if (q_id[kAhead] != kNone) load_k(q_id[kAhead], q_head[kAhead]);     // once the MMAs that used it are done
       }
       last = k_empty + 8 * mst, last_phase = m_phase;
       if (++mst == S::kKStages) mst = 0, m_phase ^= 1;
@@ -835,9 +847,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
     // ---- compute ----
     const int member = warp & 1;
     Place at_;
-    at_.pair = smem_u32(smem + S::pairs) + (warp >> 1) * 2 * S::kPair;
+    at_.pair = smem_u32(smem + S::pairs) + (warp >> 1) * 2 * Pair<MT>::kBytes;
     at_.refs = smem_u32(smem + S::refs) + warp * 2 * S::kRows * 4;
-    at_.tops = smem_u32(smem + S::tops) + (warp >> 1) * 2 * S::kTop;
+    at_.tops = smem_u32(smem + S::tops) + (warp >> 1) * 2 * Pair<MT>::kTop;
     at_.lens = smem_u32(smem + S::len);
     at_.bar = 2 + (warp >> 1), at_.member = member, at_.lane = lane;
     const uint32_t merge = smem_u32(smem + S::pairs) + member * S::kMergeWarp, sums = smem_u32(smem + S::sums);
@@ -1116,7 +1128,7 @@ Plan plan_of(int group, int q_group) {
 // allocates TMEM.
 template <int MT, bool Q16>
 constexpr int ctas_per_sm() {
-  return std::min(min_ctas<MT>(), 228 * 1024 / (Smem<MT>::total(Q16) + 1024));
+  return std::min(min_ctas<MT>(), 228 * 1024 / (Smem<MT, Q16>::total + 1024));
 }
 static_assert(ctas_per_sm<1, false>() == 3 && ctas_per_sm<1, true>() == 3 && ctas_per_sm<2, false>() == 3 &&
               ctas_per_sm<2, true>() == 3);
@@ -1127,15 +1139,16 @@ int ctas_of(int mt, bool q16) {
 
 template <int MT, bool Q16>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
-  static_assert(Tmem<MT>::used <= Tmem<MT>::columns && Tmem<MT>::columns * min_ctas<MT>() <= 512);
+  using T = Tmem<MT, Q16>;
+  static_assert(T::used <= T::columns && T::columns * min_ctas<MT>() <= 512);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {  // the shared-memory opt-in
     return cudaFuncSetAttribute(dense_pa_kernel<MT, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<MT>::total(Q16));
+                                Smem<MT, Q16>::total);
   });
   if (e != cudaSuccess) return e;
   return launch_kernel(dense_pa_kernel<MT, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
-                       Smem<MT>::total(Q16), s, 0, mk, mv, p);
+                       Smem<MT, Q16>::total, s, 0, mk, mv, p);
 }
 
 }  // namespace
