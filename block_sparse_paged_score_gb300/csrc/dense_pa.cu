@@ -7,7 +7,7 @@
 // with k4, v4 the e2m1 values, e the e8m0 bytes of the four 32-dim groups c.
 //
 // Work.  A unit = (query group, KV head): its rows, q_group tokens times G
-// heads, share every byte of the cache; more than 32 rows are cut into units
+// heads, share every byte of the cache; more than 16 rows are cut into units
 // that neighbouring CTAs take at the same time (the second finds the bytes in
 // L2).  The units' 128-token blocks laid end to end are cut into equal
 // shares, one per resident CTA, so ragged batches load every SM alike; a CTA
@@ -17,26 +17,27 @@
 // a list of cut units, no counters: the workspace carries nothing from call to
 // call and the sums' order is fixed).
 //
-// A CTA is a producer warp and four compute warps, for MT tiles of 16 rows.
+// A CTA is a producer warp and four compute warps.
 //   - The producer loads blocks by TMA (K unpacked to one byte slot a value,
 //     the layout the tensor core reads; V packed; the scales as they lie) and
 //     issues, per block, four tcgen05.mma block-scaled by the cache's own e8m0
-//     bytes: z^T = K Q^T, M = 128 tokens, N = 16 * MT rows, K = 32 = one scale
-//     group each, in TMEM, double-buffered.  A bf16 query is the sum of two e4m3
+//     bytes: z^T = K Q^T, M = 128 tokens, N = 16 rows, K = 32 = one scale group
+//     each, in TMEM, double-buffered.  A bf16 query is the sum of two e4m3
 //     parts (see stage_q), eight MMAs.
 //   - A compute warp takes the exponentials of 32 tokens (thread = token) and
 //     leaves the f16 weights in shared memory, where it and its partner pick
 //     them up as mma A fragments: a pair of warps shares 64 tokens, each
 //     multiplies them by its half of V's dims (mma.sync m16n8k16 f16), so that O
-//     takes 32 registers a tile.  V comes through ldmatrix.trans as four
+//     takes 32 registers.  V comes through ldmatrix.trans as four
 //     nibbles of two tokens a register; bit moves turn them into f16 pairs,
 //     times 2^-14 exactly.  V's scales go onto P: 2^(ev - R_c), a power of two
-//     at most 1, multiplies the weights of each group.  R_c is the largest
-//     scale byte so far (O is rescaled when it grows).  Tokens whose scale is
-//     15 or more binades below R_c, which f16 could not hold, make the pair
+//     at most 1, multiplies the weights of each group.  R_c is at least
+//     the largest scale byte so far (O is rescaled when it grows).  Tokens whose
+//     scale is 15 or more binades below R_c, which f16 could not hold, make the pair
 //     take its tokens again in bands of 15.
-//   - p is f16, at most half a step, 2^-11, off; weights are kept times 2^7 so
-//     that f16's range, down to 2^-25, reaches 2^-32 of the largest.  Row sums
+//   - p is f16, at most half a step, 2^-11, off; weights are kept times 2^9 and
+//     R_c two binades high, so that f16's range, down to 2^-25, reaches 2^-32 of the
+//     largest.  Row sums
 //     are an mma column of ones over the rounded weights.
 // tcgen05 takes the scores because it reads e2m1 and the scales itself: on
 // mma.sync the conversions of K cost more issue slots than all else.  PV stays
@@ -58,15 +59,16 @@ namespace bsp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxRows = 32;  // rows of a unit
+constexpr int kRows = 16;  // rows of a unit
 // A field (128 tokens x 64 bytes, then 128 x 4 bytes of scales) comes as one box.
 // K: 136 rows of 64 bytes, unpacked to 128; V: 68 rows of 128 bytes.
 constexpr int kKRows = 136, kVRows = 68;
 constexpr int kKTile = kKRows * 128, kVTile = (kVRows + 7) / 8 * 8 * 128;
 static_assert(kKRows * 64 == kMxField && kVRows * 128 == kMxField && kKTile % 1024 == 0);
 constexpr int kRowPad = 64 + 4;    // floats of a row (half its dims) in the merge buffer
-constexpr float kMaxGrow = 8.f;    // the reference maximum moves when a row's maximum grows by more (log2)
-constexpr float kBias = 7.f;       // weights are 2^(z - m + kBias)
+constexpr float kMaxGrow = 6.f;    // the reference maximum moves when a row's maximum grows by more (log2)
+constexpr float kBias = 9.f;       // weights are 2^(z - m + kBias): at most 2^15
+constexpr uint32_t kHeadroom = 2;  // R_c is taken this much above the largest scale byte, so that it seldom grows
 constexpr float kNoMax = -1e30f;   // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
 constexpr int kBand = 15;          // binades a band of V scales spans
 
@@ -82,32 +84,27 @@ struct Params {
 };
 
 // ---- shared memory -----------------------------------------------------------
-constexpr int kCompute = 4;  // warps
-// a pair's buffer: P [part][tile][32 tokens][16 rows] f16, V's scales
-// [part][c][4][4][2] f16; a warp's maxima: its rows', then four of scales
-template <int MT>
-struct Pair {
-  static constexpr int kP = 2 * MT * 1024, kBytes = kP + 512, kTop = 16 * MT * 4 + 16;
-};
-constexpr int kThreads = 32 * (kCompute + 1);
-// (as much as three CTAs an SM leave room for)
-template <int MT, bool Q16>
+constexpr int kCompute = 4, kThreads = 32 * (kCompute + 1);  // compute warps; and the producer
+// a pair's buffer: P [part][32 tokens][16 rows] f16, V's scales [part][c][4][4][2]
+// f16; a warp's maxima: its rows', then four of scales
+constexpr int kPBytes = 2048, kPairBytes = kPBytes + 512, kTopBytes = kRows * 4 + 16;
+template <bool Q16>
 struct Smem {
-  static constexpr int kRows = 16 * MT;
-  static constexpr int kKStages = MT == 1 ? 2 : 1, kVStages = MT == 1 && Q16 ? 2 : 3;
+  // (as much as three CTAs an SM leave room for)
+  static constexpr int kKStages = 2, kVStages = Q16 ? 2 : 3;
   static constexpr int v = kKStages * kKTile;
-  // two buffers per pair of warps
+  // two buffers per pair of warps; their place is the merge buffer once a
+  // unit's blocks are done
   static constexpr int pairs = v + kVStages * kVTile;
-  // the pairs' place is the merge buffer once a unit's blocks are done
   static constexpr int kMergeWarp = kRows * kRowPad * 4;
-  static constexpr int pairs_bytes = std::max(4 * Pair<MT>::kBytes, 2 * kMergeWarp);
-  static constexpr int refs = pairs + pairs_bytes;          // per warp: reference maxima, rescale factors
-  static constexpr int tops = refs + kCompute * 2 * kRows * 4;  // per warp: row maxima, 4 scale maxima
-  static constexpr int sums = tops + kCompute * Pair<MT>::kTop;       // per warp: l
-  static constexpr int len = sums + kCompute * kRows * 4;   // [rows] lengths
-  static constexpr int sfq = len + kRows * 4;               // [2][rows] scale cells of q
+  static constexpr int pairs_bytes = std::max(4 * kPairBytes, 2 * kMergeWarp);
+  static constexpr int refs = pairs + pairs_bytes;              // per warp: reference maxima, rescale factors
+  static constexpr int tops = refs + kCompute * 2 * kRows * 4;  // per warp
+  static constexpr int sums = tops + kCompute * kTopBytes;      // per warp: l
+  static constexpr int len = sums + kCompute * kRows * 4;       // [rows] lengths
+  static constexpr int sfq = len + kRows * 4;                   // [2][rows] scale cells of q
   static constexpr int bars = sfq + 2 * kRows * 4;
-  static constexpr int misc = bars + 16 * 8;                // bad[4], TMEM address
+  static constexpr int misc = bars + 16 * 8;                    // bad[4], TMEM address
   static constexpr int q = (misc + 32 + 1023) / 1024 * 1024;
   static constexpr int total = q + kRows * 128 * (Q16 ? 2 : 1);
 };
@@ -356,19 +353,20 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
   }
 }
 
-// One compute warp's running softmax: O of MT tiles of 16 rows in mma
-// accumulators, for the warp's two of the four 32-dim groups (tile 4k + i: dims
-// 8t + i and 8t + 4 + i of group k, of rows g and g + 8); the sums l of the warp's own
-// tokens, a tile of P times ones; and 271 - R_c of groups (0, 2) and (1, 3) in
-// the halves of two words.
-template <int MT>
+// One compute warp's running softmax: O of 16 rows in mma accumulators, for the
+// warp's two of the four 32-dim groups (tile 4k + i: dims 8t + i and 8t + 4 + i of
+// group k, of rows g and g + 8); the sums l of the warp's own tokens, a tile of P
+// times ones; and 271 - R_c of groups (0, 2) and (1, 3) in the halves of two words.
 struct State {
-  float o[MT][8][4];
-  float l[MT][4];
+  float o[8][4];
+  float l[4];
   uint32_t r02, r13;
 };
 constexpr uint32_t kHalves = 0x00010001u;
 constexpr uint32_t kNoScale = 271 * kHalves;  // R_c = 0
+__device__ __forceinline__ uint32_t scale_ref(const State& st, int c) {  // R_c
+  return 271 - ((c & 1 ? st.r13 : st.r02) >> (c & 2 ? 16 : 0) & 0xFFFF);
+}
 
 // where a warp and its pair find things (shared addresses)
 struct Place {
@@ -381,14 +379,12 @@ struct Place {
 
 // f16 2^(byte - R_c) of band `band` of the lane's token, 0 outside the band;
 // whether lower bands are left
-template <int MT>
-__device__ __forceinline__ bool put_band(const State<MT>& st, uint32_t vw, uint32_t vcell, int band) {
+__device__ __forceinline__ bool put_band(const State& st, uint32_t vw, uint32_t vcell, int band) {
   bool low = false;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int b = vw >> (8 * c) & 0xFF;
-    const int r = 271 - static_cast<int>((c & 1 ? st.r13 : st.r02) >> (c & 2 ? 16 : 0) & 0xFFFF);
-    const int x = b - r + kBand * band + 15;  // f16 exponent field
+    const int x = b - static_cast<int>(scale_ref(st, c)) + kBand * band + 15;  // f16 exponent field
     low |= b && x <= 0;
     sts16(vcell + c * 64, b && x > 0 && x <= 15 ? x << 10 : 0);
   }
@@ -408,99 +404,83 @@ __device__ __forceinline__ void put_weights(uint32_t p, int lane, const float2 (
 
 // The uncommon way of a block: one that some row does not see whole, V scales
 // outside R_c's band, or a row whose maximum grew.  Both warps of the pair go
-// through it: new references and R_c from both, O rescaled, the weights and V's
-// scales written afresh.  Returns whether lower bands of V scales are left.
-template <int MT>
-__device__ __forceinline__ bool adjust(State<MT>& st, const Place& w, uint32_t zt, float qk, int n, uint32_t vw,
-                                    uint32_t pbuf, uint32_t vcell) {
-  constexpr int kRows = 16 * MT;
-  const uint32_t mine = w.tops + w.member * Pair<MT>::kTop;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float z[16];
-    tmem_ld16(zt + 16 * mt, z);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float y = n < static_cast<int>(lds32(w.lens + (16 * mt + i) * 4)) ? z[i] * qk : -INFINITY;
-      const float mx = warp_max(y);
-      if (w.lane == 0) stsf(mine + (16 * mt + i) * 4, mx);
-    }
-  }
+// through it: new R_c, and if any row asks for it new references, from both;
+// O rescaled; the scales and weights written afresh.  Returns whether lower bands
+// of V scales are left.
+__device__ __forceinline__ bool adjust(State& st, const Place& w, uint32_t zt, float qk, bool rows, int n, uint32_t vw,
+                                       uint32_t pbuf, uint32_t vcell) {
+  const uint32_t mine = w.tops + w.member * kTopBytes;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const uint32_t mx = __reduce_max_sync(0xffffffffu, vw >> (8 * c) & 0xFF);
     if (w.lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(mine + kRows * 4 + 4 * c), "r"(mx) : "memory");
   }
-  bar_sync(w.bar, 64);
+  if (pair_any(w.bar, rows)) {
+    float z[16];
+    tmem_ld16(zt, z);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      z[i] = n < static_cast<int>(lds32(w.lens + i * 4)) ? z[i] * qk : -INFINITY;
+      const float mx = warp_max(z[i]);
+      if (w.lane == 0) stsf(mine + i * 4, mx);
+    }
+    bar_sync(w.bar, 64);
+    float2 x[8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float mx = fmaxf(ldsf(w.tops + i * 4), ldsf(w.tops + kTopBytes + i * 4));
+      const float old = ldsf(w.refs + i * 4);  // kBias - m
+      const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
+      (i & 1 ? x[i >> 1].y : x[i >> 1].x) = z[i] + ref;
+      __syncwarp();  // every lane has the old reference
+      if (w.lane == 0) stsf(w.refs + (kRows + i) * 4, ex2_approx(ref - old)), stsf(w.refs + i * 4, ref);
+    }
+    put_weights(pbuf, w.lane, x);
+    __syncwarp();
+    const uint32_t f = w.refs + (kRows + (w.lane >> 2)) * 4;
+    const float a0 = ldsf(f), a1 = ldsf(f + 32);
+    st.l[0] *= a0, st.l[2] *= a1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st.o[i][0] *= a0, st.o[i][1] *= a0, st.o[i][2] *= a1, st.o[i][3] *= a1;
+  }
   uint32_t now[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const uint32_t at = w.tops + kRows * 4 + 4 * c;
-    const uint32_t old = 271 - ((c & 1 ? st.r13 : st.r02) >> (c & 2 ? 16 : 0) & 0xFFFF);
-    now[c] = max(old, max(lds32(at), lds32(at + Pair<MT>::kTop)));
+    const uint32_t at = w.tops + kRows * 4 + 4 * c, old = scale_ref(st, c);
+    const uint32_t mx = max(lds32(at), lds32(at + kTopBytes));
+    now[c] = mx > old ? min(mx + kHeadroom, 255u) : old;
     if (now[c] != old && (c >> 1) == w.member) {
       const float f = scale_pow2(1.f, static_cast<int>(old) - static_cast<int>(now[c]));
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) st.o[mt][4 * (c & 1) + i][e] *= f;
+        for (int e = 0; e < 4; ++e) st.o[4 * (c & 1) + i][e] *= f;
     }
   }
   st.r02 = kNoScale - (now[0] | (now[2] << 16));
   st.r13 = kNoScale - (now[1] | (now[3] << 16));
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float z[16];
-    tmem_ld16(zt + 16 * mt, z);
-    float2 x[8];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 16 * mt + i;
-      const float y = n < static_cast<int>(lds32(w.lens + r * 4)) ? z[i] * qk : -INFINITY;
-      const float mx = fmaxf(ldsf(w.tops + r * 4), ldsf(w.tops + Pair<MT>::kTop + r * 4));
-      const float old = ldsf(w.refs + r * 4);  // kBias - m
-      const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
-      (i & 1 ? x[i >> 1].y : x[i >> 1].x) = y + ref;
-      __syncwarp();  // every lane has the old reference
-      if (w.lane == 0) stsf(w.refs + (kRows + r) * 4, ex2_approx(ref - old)), stsf(w.refs + r * 4, ref);
-    }
-    put_weights(pbuf + mt * 1024, w.lane, x);
-    __syncwarp();
-    const uint32_t f = w.refs + (kRows + 16 * mt + (w.lane >> 2)) * 4;
-    const float a0 = ldsf(f), a1 = ldsf(f + 32);
-    st.l[mt][0] *= a0, st.l[mt][2] *= a1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      st.o[mt][i][0] *= a0, st.o[mt][i][1] *= a0, st.o[mt][i][2] *= a1, st.o[mt][i][3] *= a1;
-  }
   return pair_any(w.bar, put_band(st, vw, vcell, 0));
 }
 
 // O (+)= P V of the pair's 64 tokens and the warp's half of the dims; the first
 // time also the sums of the warp's own tokens.  DIRECT: into O, else times f
 // through accumulators of their own (a lower band).
-template <int MT, bool DIRECT>
-__device__ __forceinline__ void multiply(State<MT>& st, uint32_t pair, uint32_t vt, int member, int lane, float f) {
+template <bool DIRECT>
+__device__ __forceinline__ void multiply(State& st, uint32_t pair, uint32_t vt, int member, int lane, float f) {
   const int t = lane & 3, row8 = lane & 7, mat = lane >> 3;
   const uint32_t prow = pair + ((mat >> 1) * 8 + row8) * 32 + (((mat & 1) << 4) ^ ((row8 & 4) << 2));
   // V rows of 128 bytes hold two tokens; 16-byte chunk j of row r is at j ^ (r % 8)
   const int vr = mat * 4 + (row8 >> 1);
-  const uint32_t vrow = vt + vr * 128 + ((((row8 & 1) * 4 + 2 * member) ^ (vr & 7)) << 4), vsc = pair + Pair<MT>::kP + member * 128 + t * 16;
+  const uint32_t vrow = vt + vr * 128 + ((((row8 & 1) * 4 + 2 * member) ^ (vr & 7)) << 4);
+  const uint32_t vsc = pair + kPBytes + member * 128 + t * 16;
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
-    uint32_t pf[MT][2][4];  // A fragments (rows g, g + 8 x token octets), k-steps 0 and 1 of the part
+    uint32_t pf[2][4];  // A fragments (rows g, g + 8 x token octets), k-steps 0 and 1 of the part
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) ldsm_x4_trans(pf[mt][k], prow + part * MT * 1024 + mt * 1024 + k * 512);
+    for (int k = 0; k < 2; ++k) ldsm_x4_trans(pf[k], prow + part * 1024 + k * 512);
     if (DIRECT && part == member) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          mma_f16(st.l[mt], pf[mt][k][0], pf[mt][k][1], pf[mt][k][2], pf[mt][k][3], 0x3C003C00u, 0x3C003C00u);
+      for (int k = 0; k < 2; ++k) mma_f16(st.l, pf[k][0], pf[k][1], pf[k][2], pf[k][3], 0x3C003C00u, 0x3C003C00u);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -508,48 +488,28 @@ __device__ __forceinline__ void multiply(State<MT>& st, uint32_t pair, uint32_t 
       ldsm_x4_trans(zr, (vrow + part * 2048) ^ (c << 4));
       const uint4 s4 = lds128(vsc + part * 256 + c * 64);
       const uint32_t vs[4] = {s4.x, s4.y, s4.z, s4.w};
-      float y[MT][4][4];
+      float y[4][4];
       if (!DIRECT) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[mt][i][0] = y[mt][i][1] = y[mt][i][2] = y[mt][i][3] = 0.f;
+        for (int i = 0; i < 4; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint32_t v0[4], v1[4];
         e2m1x4x2_to_f16x2(zr[2 * k], v0);
         e2m1x4x2_to_f16x2(zr[2 * k + 1], v1);
+        const uint32_t a0 = hmul2(pf[k][0], vs[2 * k]), a1 = hmul2(pf[k][1], vs[2 * k]);
+        const uint32_t a2 = hmul2(pf[k][2], vs[2 * k + 1]), a3 = hmul2(pf[k][3], vs[2 * k + 1]);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint32_t a0 = hmul2(pf[mt][k][0], vs[2 * k]), a1 = hmul2(pf[mt][k][1], vs[2 * k]);
-          const uint32_t a2 = hmul2(pf[mt][k][2], vs[2 * k + 1]), a3 = hmul2(pf[mt][k][3], vs[2 * k + 1]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16(DIRECT ? st.o[mt][4 * c + i] : y[mt][i], a0, a1, a2, a3, v0[i], v1[i]);
-        }
+        for (int i = 0; i < 4; ++i) mma_f16(DIRECT ? st.o[4 * c + i] : y[i], a0, a1, a2, a3, v0[i], v1[i]);
       }
       if (!DIRECT) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st.o[mt][4 * c + i][e] += y[mt][i][e] * f;
+          for (int e = 0; e < 4; ++e) st.o[4 * c + i][e] += y[i][e] * f;
       }
     }
-  }
-}
-
-// the lower bands of V's scales
-template <int MT>
-__device__ __forceinline__ void lower_bands(State<MT>& st, const Place& w, uint32_t pair, uint32_t vt, uint32_t vw,
-                                         uint32_t vcell) {
-  bool more = true;
-#pragma unroll 1
-  for (int band = 1; more; ++band) {
-    bar_sync(w.bar, 64);  // the last band's scales are read
-    more = pair_any(w.bar, put_band(st, vw, vcell, band));
-    multiply<MT, false>(st, pair, vt, w.member, w.lane, scale_pow2(1.f, -kBand * band));
   }
 }
 
@@ -557,57 +517,58 @@ __device__ __forceinline__ void lower_bands(State<MT>& st, const Place& w, uint3
 // the lane's token n, column = row h, which sees the token if n < lens[h]; whole:
 // every row sees every token); vw the token's V scale bytes (0 where no row sees
 // it), vt the pair's V rows.  Arrives at z_empty once the logits are read.
-template <int MT>
-__device__ __forceinline__ void attend(State<MT>& st, const Place& w, uint32_t zt, uint32_t z_empty, float qk,
-                                       bool whole, int n, uint32_t vw, uint32_t vt, uint32_t buf) {
-  const uint32_t pair = w.pair + buf * Pair<MT>::kBytes, pbuf = pair + w.member * MT * 1024;
-  const uint32_t vcell = pair + Pair<MT>::kP + w.member * 256 + ((w.lane >> 1) & 3) * 16 + (w.lane >> 3) * 4 +
+__device__ __forceinline__ void attend(State& st, const Place& w, uint32_t zt, uint32_t z_empty, float qk, bool whole,
+                                       int n, uint32_t vw, uint32_t vt, uint32_t buf) {
+  const uint32_t pair = w.pair + buf * kPairBytes, pbuf = pair + w.member * 1024;
+  const uint32_t vcell = pair + kPBytes + w.member * 256 + ((w.lane >> 1) & 3) * 16 + (w.lane >> 3) * 4 +
                          (w.lane & 1) * 2;  // [part][c][pair of tokens][octet][2]
   // V's scales as f16 2^(byte - R_c): exponent fields 1..15, two groups a word.
   // y = byte + 271 - R_c; in 257..271 where f16 holds the scale.
   const uint32_t y02 = (vw & 0x00FF00FFu) + st.r02, y13 = (vw >> 8 & 0x00FF00FFu) + st.r13;
   const uint32_t over = (y02 + 240 * kHalves) | (y13 + 240 * kHalves);  // bit 9: y >= 272
   const uint32_t in = (y02 + 255 * kHalves) & (y13 + 255 * kHalves);    // bit 9: y >= 257
-  bool plain = whole && (over & (512 * kHalves)) == 0 && (in & (512 * kHalves)) == 512 * kHalves;
+  const bool scales = (over & (512 * kHalves)) == 0 && (in & (512 * kHalves)) == 512 * kHalves;
   const uint32_t h02 = (y02 - 256 * kHalves) << 10, h13 = (y13 - 256 * kHalves) << 10;
   sts16(vcell, h02), sts16(vcell + 64, h13);
   sts16(vcell + 128, h02 >> 16), sts16(vcell + 192, h13 >> 16);
   // weights 2^(z - m + kBias), m the rows' reference maxima, taken as if nothing
   // were uncommon
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float2 x[8];
+  float2 x[8];
+  {
     float z[16];
-    tmem_ld16(zt + 16 * mt, z);
+    tmem_ld16(zt, z);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 m = lds128f(w.refs + 64 * mt + 16 * i);  // kBias - m
+      const float4 m = lds128f(w.refs + 16 * i);  // kBias - m
       x[2 * i] = ffma2({z[4 * i], z[4 * i + 1]}, {qk, qk}, {m.x, m.y});
       x[2 * i + 1] = ffma2({z[4 * i + 2], z[4 * i + 3]}, {qk, qk}, {m.z, m.w});
     }
-    float top = fmaxf(x[0].x, x[0].y);
+  }
+  float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmax3(top, x[i].x, x[i].y);
-    plain = plain && top <= kBias + kMaxGrow;
-    put_weights(pbuf + mt * 1024, w.lane, x);
-  }
+  for (int i = 1; i < 8; ++i) top = fmax3(top, x[i].x, x[i].y);
+  const bool rows = whole && top <= kBias + kMaxGrow;
+  put_weights(pbuf, w.lane, x);
   bool more = false;
-  if (__builtin_expect(!pair_all(w.bar, plain), 0)) {
-    more = adjust(st, w, zt, qk, n, vw, pbuf, vcell);
-  }
+  if (__builtin_expect(!pair_all(w.bar, rows && scales), 0)) more = adjust(st, w, zt, qk, !rows, n, vw, pbuf, vcell);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();
   if (w.lane == 0) arrive(z_empty);
-  multiply<MT, true>(st, pair, vt, w.member, w.lane, 1.f);
-  if (__builtin_expect(more, 0)) {
-    lower_bands(st, w, pair, vt, vw, vcell);
+  multiply<true>(st, pair, vt, w.member, w.lane, 1.f);
+  if (__builtin_expect(more, 0)) {  // the lower bands of V's scales
+#pragma unroll 1
+    for (int band = 1; more; ++band) {
+      bar_sync(w.bar, 64);  // the last band's scales are read
+      more = pair_any(w.bar, put_band(st, vw, vcell, band));
+      multiply<false>(st, pair, vt, w.member, w.lane, scale_pow2(1.f, -kBand * band));
+    }
   }
 }
 
 // ---- the main kernel -----------------------------------------------------------
-template <int MT, bool Q16>
+template <bool Q16>
 struct Bars {
-  static constexpr int NK = Smem<MT, Q16>::kKStages, NV = Smem<MT, Q16>::kVStages;
+  static constexpr int NK = Smem<Q16>::kKStages, NV = Smem<Q16>::kVStages;
   static_assert(2 * NK + 2 * NV + 5 <= 16);
   uint64_t* b;
   __device__ uint64_t* k_full(int i) const { return b + i; }
@@ -619,22 +580,18 @@ struct Bars {
   __device__ uint64_t* q_full() const { return b + 2 * NK + 2 * NV + 4; }
 };
 
-template <int MT>
-constexpr int min_ctas() {
-  return 3;  // 128 registers a thread
-}
+// CTAs per SM: 128 registers a thread (with 96, for four, the state spills to an
+// L1 that shared memory leaves next to nothing of: 64 x 128k took 519 us, not 297)
+constexpr int kCtasPerSm = 3;
 // TMEM columns: two z buffers, the scale cells of K and q
-template <int MT, bool Q16>
-struct Tmem {
-  static constexpr int z = 0, sk = 32 * MT, sq = sk + 4 * Smem<MT, Q16>::kKStages, used = sq + 8, columns = used <= 64 ? 64 : 128;
-};
+constexpr int kTmemZ = 0, kTmemK = 2 * kRows, kTmemQ = kTmemK + 8, kTmemColumns = 64;
+static_assert(kTmemQ + 8 <= kTmemColumns && kTmemColumns * kCtasPerSm <= 512);
 
-template <int MT, bool Q16>
-__global__ void __launch_bounds__(kThreads, min_ctas<MT>())
+template <bool Q16>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     dense_pa_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ Params p) {
-  using S = Smem<MT, Q16>;
-  using T = Tmem<MT, Q16>;
+  using S = Smem<Q16>;
   extern __shared__ __align__(1024) uint8_t smem[];  // (all of it: no static shared memory moves its start)
   // before the first block the pairs' place serves the scan
   int64_t* s_sum = reinterpret_cast<int64_t*>(smem + S::pairs);  // [warps]
@@ -642,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
   const DensePaParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Bars<MT, Q16> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
+  const Bars<Q16> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
   if (tid == 0) {
     for (int i = 0; i < S::kKStages; ++i) mbar_init(bars.k_full(i), 1), mbar_init(bars.k_empty(i), 1);
     for (int i = 0; i < S::kVStages; ++i) mbar_init(bars.v_full(i), 1), mbar_init(bars.v_empty(i), kCompute);
@@ -657,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
   if (warp == kCompute) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(const_cast<const uint32_t*>(misc + 4))),
-                 "n"(T::columns));
+                 "n"(kTmemColumns));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
 
@@ -818,15 +775,15 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
         }
         if (alive) alive = wait_for(z_empty + 8 * buf, z_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t sk = tmem + T::sk + 4 * mst, z = tmem + T::z + buf * S::kRows;
+        const uint32_t sk = tmem + kTmemK + 4 * mst, z = tmem + kTmemZ + buf * kRows;
         const uint64_t kd = k_desc + mst * (kKTile / 16);
         scales_to_tmem(sk, cells);
 #pragma unroll
         for (int part = 0; part < (Q16 ? 2 : 1); ++part)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            umma_mx(z, kd + 2 * c, q_desc + (part * S::kRows * 128 + 32 * c) / 16,
-                    idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, S::kRows, 128, c, c), sk, tmem + T::sq + 4 * part,
+            umma_mx(z, kd + 2 * c, q_desc + (part * kRows * 128 + 32 * c) / 16,
+                    idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, kRows, 128, c, c), sk, tmem + kTmemQ + 4 * part,
                     part > 0 || c > 0);
         commit(k_empty + 8 * mst);
         commit(z_full + 8 * buf);
@@ -847,9 +804,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
     // ---- compute ----
     const int member = warp & 1;
     Place at_;
-    at_.pair = smem_u32(smem + S::pairs) + (warp >> 1) * 2 * Pair<MT>::kBytes;
-    at_.refs = smem_u32(smem + S::refs) + warp * 2 * S::kRows * 4;
-    at_.tops = smem_u32(smem + S::tops) + (warp >> 1) * 2 * Pair<MT>::kTop;
+    at_.pair = smem_u32(smem + S::pairs) + (warp >> 1) * 2 * kPairBytes;
+    at_.refs = smem_u32(smem + S::refs) + warp * 2 * kRows * 4;
+    at_.tops = smem_u32(smem + S::tops) + (warp >> 1) * 2 * kTopBytes;
     at_.lens = smem_u32(smem + S::len);
     at_.bar = 2 + (warp >> 1), at_.member = member, at_.lane = lane;
     const uint32_t merge = smem_u32(smem + S::pairs) + member * S::kMergeWarp, sums = smem_u32(smem + S::sums);
@@ -859,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
     const int g = lane >> 2, t = lane & 3;
     const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0));
     const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
-    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc)), z_at = tmem + lane_base + T::z;
+    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc)), z_at = tmem + lane_base + kTmemZ;
     // the token's scales: row 64 + warp of V's tile, 16-byte chunk lane / 4 at its swizzled place
     const uint32_t vs_at = smem_u32(smem + S::v) + (64 + warp) * 128 + (((lane >> 2) ^ warp) << 4) + (lane & 3) * 4;
     const uint32_t v_at = smem_u32(smem + S::v) + (warp >> 1) * 4096;
@@ -867,31 +824,28 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
     while (w.next(p, sub, lane)) {
       bar_sync(1, 32 * kCompute);  // the last unit's q, lengths and merge buffers are no longer read
       if (w.nblk)
-        for (int i = tid; i < S::kRows * 8; i += 32 * kCompute)
-          stage_q<Q16>(a, w.tok0, w.tokens, w.h, smem + S::q, S::kRows, cells, i);
-      if (tid < S::kRows) {
+        for (int i = tid; i < kRows * 8; i += 32 * kCompute)
+          stage_q<Q16>(a, w.tok0, w.tokens, w.h, smem + S::q, kRows, cells, i);
+      if (tid < kRows) {
         const int j = tid / a.group;
         lens[tid] = j < w.tokens ? min(max(a.row_len[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h], 0), w.max_len) : 0;
       }
       if (tid < w.tokens && a.row_seq[static_cast<int64_t>(w.tok0 + tid) * a.hkv + w.h] != w.seq)
         set_err(a.err, BSP_DEVERR_GROUP_SEQ);
-      State<MT> st;
+      State st;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) st.o[mt][k][0] = st.o[mt][k][1] = st.o[mt][k][2] = st.o[mt][k][3] = 0.f;
-        st.l[mt][0] = st.l[mt][1] = st.l[mt][2] = st.l[mt][3] = 0.f;
-      }
+      for (int k = 0; k < 8; ++k) st.o[k][0] = st.o[k][1] = st.o[k][2] = st.o[k][3] = 0.f;
+      st.l[0] = st.l[1] = st.l[2] = st.l[3] = 0.f;
       st.r02 = st.r13 = kNoScale;
-      if (lane < S::kRows) stsf(at_.refs + 4 * lane, kBias - kNoMax);
+      if (lane < kRows) stsf(at_.refs + 4 * lane, kBias - kNoMax);
       fence_proxy_async();  // the tensor core reads q through the async proxy
       bar_sync(1, 32 * kCompute);
       if (w.nblk) {
 #pragma unroll
         for (int k = 0; k < (Q16 ? 2 : 1); ++k) {  // q's scale cells, in this sub-partition's copy
           const uint32_t cell =
-              lane < S::kRows ? *reinterpret_cast<const uint32_t*>(cells + (k * S::kRows + lane) * 4) : 0x7F7F7F7Fu;
-          tmem_st4(tmem + lane_base + T::sq + 4 * k, cell, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              lane < kRows ? *reinterpret_cast<const uint32_t*>(cells + (k * kRows + lane) * 4) : 0x7F7F7F7Fu;
+          tmem_st4(tmem + lane_base + kTmemQ + 4 * k, cell, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
@@ -908,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
         if (lds32(bad_at + 4 * vst) == 0) {
           uint32_t vw = lds32(vs_at + vst * kVTile);
           if (n >= max_len) vw = 0;
-          attend(st, at_, z_at + buf * S::kRows, z_empty + 8 * buf, p.qk_scale, n < n_whole, n, vw,
+          attend(st, at_, z_at + buf * kRows, z_empty + 8 * buf, p.qk_scale, n < n_whole, n, vw,
                  v_at + vst * kVTile, buf);
         } else if (lane == 0) {
           arrive(z_empty + 8 * buf);
@@ -920,82 +874,73 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
       }
 
       // -- the two pairs joined: warps 2 and 3 hand their O to 0 and 1
-      const uint32_t rr[4] = {271 - (st.r02 & 0xFFFF), 271 - (st.r13 & 0xFFFF), 271 - (st.r02 >> 16),
-                              271 - (st.r13 >> 16)};
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int c = 0; c < 2; ++c) {
+        const int e = static_cast<int>(member ? scale_ref(st, 2 + c) : scale_ref(st, c)) - 127 + 14;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int e = static_cast<int>(member ? rr[2 + c] : rr[c]) - 127 + 14;
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) st.o[mt][4 * c + k][j] = scale_pow2(st.o[mt][4 * c + k][j], e);
-        }
-        if (t == 0) {  // every column of the tile is the sum
-          stsf(sums + (warp * S::kRows + 16 * mt + g) * 4, st.l[mt][0]);
-          stsf(sums + (warp * S::kRows + 16 * mt + g + 8) * 4, st.l[mt][2]);
-        }
+          for (int j = 0; j < 4; ++j) st.o[4 * c + k][j] = scale_pow2(st.o[4 * c + k][j], e);
+      }
+      if (t == 0) {  // every column of the tile is the sum
+        stsf(sums + (warp * kRows + g) * 4, st.l[0]);
+        stsf(sums + (warp * kRows + g + 8) * 4, st.l[2]);
       }
       bar_sync(1, 32 * kCompute);  // the pairs' place becomes the merge buffer
       const uint32_t mrow = merge + (g * kRowPad + 8 * t) * 4;
       if (warp >= 2) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                sts128(mrow + ((16 * mt + 8 * e) * kRowPad + 32 * c + 4 * j) * 4, __float_as_uint(st.o[mt][4 * c][2 * e + j]),
-                       __float_as_uint(st.o[mt][4 * c + 1][2 * e + j]), __float_as_uint(st.o[mt][4 * c + 2][2 * e + j]),
-                       __float_as_uint(st.o[mt][4 * c + 3][2 * e + j]));
+            for (int j = 0; j < 2; ++j)
+              sts128(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4, __float_as_uint(st.o[4 * c][2 * e + j]),
+                     __float_as_uint(st.o[4 * c + 1][2 * e + j]), __float_as_uint(st.o[4 * c + 2][2 * e + j]),
+                     __float_as_uint(st.o[4 * c + 3][2 * e + j]));
       }
       bar_sync(1, 32 * kCompute);
       if (warp < 2) {
         // a CTA's slots: 2 * CTA for a unit that began before its share, + 1
         // for one that goes on after it
         float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
-                    (2LL * blockIdx.x + (w.starts ? 1 : 0)) * S::kRows * (kDim + 2);
+                    (2LL * blockIdx.x + (w.starts ? 1 : 0)) * kRows * (kDim + 2);
         const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 16 * mt + 8 * e + g;
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * e + g;
             if (r >= w.tokens * a.group) continue;
-            const float m0 = kBias - ldsf(at_.refs + 4 * r);
-            const float m1 = kBias - ldsf(smem_u32(smem + S::refs) + (2 * 2 * S::kRows + r) * 4);
-            const float M = fmaxf(m0, m1), f0 = ex2_approx(m0 - M), f1 = ex2_approx(m1 - M);
-            const float l = f0 * (ldsf(sums + r * 4) + ldsf(sums + (S::kRows + r) * 4)) +
-                            f1 * (ldsf(sums + (2 * S::kRows + r) * 4) + ldsf(sums + (3 * S::kRows + r) * 4));
-            const bool all = w.starts && w.ends;
-            const float inv = all ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+          const float m0 = kBias - ldsf(at_.refs + 4 * r);
+          const float m1 = kBias - ldsf(smem_u32(smem + S::refs) + (2 * 2 * kRows + r) * 4);
+          const float M = fmaxf(m0, m1), f0 = ex2_approx(m0 - M), f1 = ex2_approx(m1 - M);
+          const float l = f0 * (ldsf(sums + r * 4) + ldsf(sums + (kRows + r) * 4)) +
+                          f1 * (ldsf(sums + (2 * kRows + r) * 4) + ldsf(sums + (3 * kRows + r) * 4));
+          const bool all = w.starts && w.ends;
+          const float inv = all ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float x[8];
+          for (int c = 0; c < 2; ++c) {
+            float x[8];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float4 y = lds128f(mrow + ((16 * mt + 8 * e) * kRowPad + 32 * c + 4 * j) * 4);
-                x[4 * j] = (st.o[mt][4 * c][2 * e + j] * f0 + y.x * f1) * inv;
-                x[4 * j + 1] = (st.o[mt][4 * c + 1][2 * e + j] * f0 + y.y * f1) * inv;
-                x[4 * j + 2] = (st.o[mt][4 * c + 2][2 * e + j] * f0 + y.z * f1) * inv;
-                x[4 * j + 3] = (st.o[mt][4 * c + 3][2 * e + j] * f0 + y.w * f1) * inv;
-              }
-              const int d = 64 * member + 32 * c + 8 * t;
-              if (all) {
-                const int64_t row = (w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group;
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * kDim + d) =
-                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                               pack_bf16x2(x[6], x[7]));
-              } else {
-                *reinterpret_cast<float4*>(po + r * kDim + d) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4*>(po + r * kDim + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
-              }
+            for (int j = 0; j < 2; ++j) {
+              const float4 y = lds128f(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4);
+              x[4 * j] = (st.o[4 * c][2 * e + j] * f0 + y.x * f1) * inv;
+              x[4 * j + 1] = (st.o[4 * c + 1][2 * e + j] * f0 + y.y * f1) * inv;
+              x[4 * j + 2] = (st.o[4 * c + 2][2 * e + j] * f0 + y.z * f1) * inv;
+              x[4 * j + 3] = (st.o[4 * c + 3][2 * e + j] * f0 + y.w * f1) * inv;
             }
-            if (!all && member == 0 && t == 0)
-              *reinterpret_cast<float2*>(po + S::kRows * kDim + 2 * r) = make_float2(M, l);
+            const int d = 64 * member + 32 * c + 8 * t;
+            if (all) {
+              const int64_t row = (w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group;
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * kDim + d) =
+                  make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                             pack_bf16x2(x[6], x[7]));
+            } else {
+              *reinterpret_cast<float4*>(po + r * kDim + d) = make_float4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<float4*>(po + r * kDim + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            }
+          }
+          if (!all && member == 0 && t == 0)
+            *reinterpret_cast<float2*>(po + kRows * kDim + 2 * r) = make_float2(M, l);
           }
       }
       if (w.starts && tid == 0) {
@@ -1013,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
   __syncthreads();
   if (warp == kCompute) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(T::columns));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemColumns));
   }
 }
 
@@ -1021,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<MT>())
 // Joins the pieces of the units that share borders cut.  A warp takes one row
 // and every `parts`-th of its pieces; the `parts` warps of a row are joined in
 // shared memory.
-__global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constant__ Params p, int rows_pad, int parts) {
+__global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constant__ Params p, int parts) {
   __shared__ float4 s_o[8][32];
   __shared__ float2 s_ml[8];
   pdl_wait();
@@ -1040,7 +985,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
       min(static_cast<int64_t>(min(p.sub_tokens, a.q_group - sub * p.sub_tokens)), a.num_rows / a.hkv - tok0));
   const bool live = row < tokens * a.group;
   const float* base = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + list_bytes(p.ctas));
-  const int64_t slot_floats = static_cast<int64_t>(rows_pad) * (kDim + 2);
+  const int64_t slot_floats = kRows * (kDim + 2);
 
   float M = kNoMax, L = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1050,7 +995,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
       const int k = k0 + lane * parts;
       const int64_t slot = k == 0 ? 2LL * c0 + 1 : 2LL * (c0 + static_cast<int64_t>(k) * p.subs);
       float2 ml = make_float2(kNoMax, 0.f);
-      if (k < pieces) ml = *reinterpret_cast<const float2*>(base + slot * slot_floats + rows_pad * kDim + 2 * row);
+      if (k < pieces) ml = *reinterpret_cast<const float2*>(base + slot * slot_floats + kRows * kDim + 2 * row);
       float mx = ml.x;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -1113,51 +1058,35 @@ bool make_map_side(CUtensorMap* m, bool unpack, const void* base, uint64_t heads
          CUDA_SUCCESS;
 }
 
-// how a group's rows are cut into units
+// How a group's rows are cut into units of 16.  (Warps of 32 rows, which convert
+// V's bytes once for both halves, were tried: their state leaves too few
+// registers, 128 x 32k with 64 rows a group took 581-647 us, 8 or 12 warps an SM.)
 struct Plan {
-  int sub_tokens, subs, mt;
+  int sub_tokens, subs;
 };
 Plan plan_of(int group, int q_group) {
-  const int sub = std::min(q_group, kMaxRows / group), subs = (q_group + sub - 1) / sub;
-  const int even = (q_group + subs - 1) / subs;  // units of about the same size
-  return {even, subs, (even * group + 15) / 16};
+  const int sub = std::min(q_group, kRows / group), subs = (q_group + sub - 1) / sub;
+  return {(q_group + subs - 1) / subs, subs};  // units of about the same size
 }
 
-// CTAs per SM: what the register bound allows, as far as shared memory holds
-// them (TMEM: 512 columns).  The occupancy query answers 1 for a kernel that
-// allocates TMEM.
-template <int MT, bool Q16>
-constexpr int ctas_per_sm() {
-  return std::min(min_ctas<MT>(), 228 * 1024 / (Smem<MT, Q16>::total + 1024));
-}
-static_assert(ctas_per_sm<1, false>() == 3 && ctas_per_sm<1, true>() == 3 && ctas_per_sm<2, false>() == 3 &&
-              ctas_per_sm<2, true>() == 3);
-int ctas_of(int mt, bool q16) {
-  return mt == 1 ? (q16 ? ctas_per_sm<1, true>() : ctas_per_sm<1, false>())
-                 : (q16 ? ctas_per_sm<2, true>() : ctas_per_sm<2, false>());
-}
-
-template <int MT, bool Q16>
+template <bool Q16>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
-  using T = Tmem<MT, Q16>;
-  static_assert(T::used <= T::columns && T::columns * min_ctas<MT>() <= 512);
+  static_assert((Smem<Q16>::total + 1024) * kCtasPerSm <= 228 * 1024);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {  // the shared-memory opt-in
-    return cudaFuncSetAttribute(dense_pa_kernel<MT, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<MT, Q16>::total);
+    return cudaFuncSetAttribute(dense_pa_kernel<Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<Q16>::total);
   });
   if (e != cudaSuccess) return e;
-  return launch_kernel(dense_pa_kernel<MT, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
-                       Smem<MT, Q16>::total, s, 0, mk, mv, p);
+  return launch_kernel(dense_pa_kernel<Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), Smem<Q16>::total, s,
+                       0, mk, mv, p);
 }
 
 }  // namespace
 
 size_t dense_pa_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms) {
-  (void)num_rows, (void)hkv;
-  const Plan pl = plan_of(group, q_group);
-  const int64_t ctas = static_cast<int64_t>(std::max(ctas_of(pl.mt, false), ctas_of(pl.mt, true))) * num_sms;
-  return list_bytes(ctas) + 2 * ctas * 16 * pl.mt * (kDim + 2) * sizeof(float);
+  (void)num_rows, (void)hkv, (void)group, (void)q_group;
+  const int64_t ctas = static_cast<int64_t>(kCtasPerSm) * num_sms;
+  return list_bytes(ctas) + 2 * ctas * kRows * (kDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s, int* launches) {
@@ -1175,7 +1104,7 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   if (units > INT32_MAX) return cudaErrorNotSupported;
   p.units = static_cast<int32_t>(units);
   p.shares = static_cast<int32_t>(
-      std::min<int64_t>(static_cast<int64_t>(ctas_of(pl.mt, q16)) * num_sms / pl.subs, pairs * a.bt_stride));
+      std::min<int64_t>(static_cast<int64_t>(kCtasPerSm) * num_sms / pl.subs, pairs * a.bt_stride));
   p.ctas = p.shares * pl.subs;
   p.by_unit = units <= p.ctas;
   CUtensorMap mk, mv;
@@ -1183,8 +1112,7 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   if (!make_map_side(&mk, true, a.k_base, a.hkv, blocks, a.id_stride) ||
       !make_map_side(&mv, false, a.v_base, a.hkv, blocks, a.id_stride))
     return cudaErrorInvalidValue;
-  cudaError_t e = pl.mt == 1 ? (q16 ? launch_main<1, true>(mk, mv, p, s) : launch_main<1, false>(mk, mv, p, s))
-                             : (q16 ? launch_main<2, true>(mk, mv, p, s) : launch_main<2, false>(mk, mv, p, s));
+  cudaError_t e = q16 ? launch_main<true>(mk, mv, p, s) : launch_main<false>(mk, mv, p, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.shares > 1) {
@@ -1194,7 +1122,7 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
     const int64_t chunks = (pl.sub_tokens * a.group + 8 / parts - 1) / (8 / parts);
     const int64_t items = p.by_unit ? units : p.ctas;
     e = launch_kernel(dense_pa_join_kernel, dim3(static_cast<unsigned>(items * chunks)), dim3(256), 0, s, 0, p,
-                      16 * pl.mt, parts);
+                      parts);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
