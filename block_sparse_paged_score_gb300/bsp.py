@@ -357,35 +357,39 @@ def sparse_decode_step(args, events=None, stream=None):
     _check("bsp_sparse_decode_step", lib().bsp_sparse_decode_step(C.byref(args), ev, _stream(stream)))
 
 
-def _dense(name, t, dtype, stream, numel=None):
-    """The device address of a contiguous tensor of one of the given dtypes
-    on the stream's device, of at least `numel` elements."""
+def _dense(name, t, dtype, device, numel=0):
+    """The device address of a contiguous tensor of the given dtype on the
+    stream's device, of at least `numel` elements (None: NULL)."""
     if t is None:
         return None
-    if t.device != stream.device:
-        raise ValueError(f"{name} is on {t.device}, the stream on {stream.device}")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or t.numel() < numel:
+        _complain(name, t, dtype, device, numel)
+    return t.data_ptr()
+
+
+def _complain(name, t, dtype, device, numel):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the stream on {device}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    if numel is not None and t.numel() < numel:
-        raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
-    return _ptr(t)
+    raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
 
 
-def _head_rows(name, t, stream):
-    """(address, token stride) of bf16 rows [T, heads, 128] whose heads lie
-    side by side; the tokens may be any distance apart."""
+def _head_rows(name, t, tokens, heads, device):
+    """(address, token stride) of bf16 rows [tokens, heads, 128] whose heads
+    lie side by side; the tokens may be any distance apart."""
     if t is None:
         return None, 0
-    if t.device != stream.device:
-        raise ValueError(f"{name} is on {t.device}, the stream on {stream.device}")
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != 128:
-        raise ValueError(f"{name} is not bf16 [tokens, heads, 128]")
+    if t.dtype is not torch.bfloat16 or t.shape != (tokens, heads, 128):
+        raise ValueError(f"{name} is not bf16 [{tokens}, {heads}, 128]")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the stream on {device}")
     st = t.stride()
-    if st[2] != 1 or (t.shape[1] > 1 and st[1] != 128):
+    if st[2] != 1 or (st[1] != 128 and heads > 1):
         raise ValueError(f"{name}: the heads of a token must lie side by side")
-    return _ptr(t), st[0] if t.shape[0] > 1 else t.shape[1] * 128
+    return t.data_ptr(), st[0] if tokens > 1 else heads * 128
 
 
 def step_tables(args, stream=None):
@@ -402,6 +406,7 @@ def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream
     """Cached tokens by slot as bf16 rows: (k, v, idx_k), k and v of the K/V
     cache `kv`, idx_k of the index cache `idx`; either cache may be None."""
     s = stream if stream is not None else torch.cuda.current_stream()
+    dev = s.device
     T = slot.numel()
     if kv is not None:
         shape = (T, kv.num_kv_heads, 128)
@@ -415,14 +420,13 @@ def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream
     elif idx_k is not None:
         raise ValueError("idx_k needs an index cache")
     bf = torch.bfloat16
+    n, ni = T * kv.num_kv_heads * 128 if kv is not None else 0, T * idx.num_heads * 128 if idx is not None else 0
     _check("bsp_kv_page_read",
            lib().bsp_kv_page_read(C.byref(kv.desc) if kv is not None else None,
                                   C.byref(idx.desc) if idx is not None else None,
-                                  _dense("slot", slot, torch.int64, s), T,
-                                  _dense("k", k, bf, s, T * kv.num_kv_heads * 128 if kv is not None else 0),
-                                  _dense("v", v, bf, s, T * kv.num_kv_heads * 128 if kv is not None else 0),
-                                  _dense("idx_k", idx_k, bf, s, T * idx.num_heads * 128 if idx is not None else 0),
-                                  _dense("dev_err", dev_err, torch.int32, s, 1), _stream(s)))
+                                  _dense("slot", slot, torch.int64, dev), T, _dense("k", k, bf, dev, n),
+                                  _dense("v", v, bf, dev, n), _dense("idx_k", idx_k, bf, dev, ni),
+                                  _dense("dev_err", dev_err, torch.int32, dev, 1), s.cuda_stream))
     return k, v, idx_k
 
 
@@ -442,21 +446,22 @@ def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, 
     """Attention of each row over its whole context in an MXFP4 cache
     (bsp_dense_pa_decode); q [tokens, num_q_heads, 128], rows = tokens * Hkv."""
     s = stream if stream is not None else torch.cuda.current_stream()
-    rows = row_len.numel()
-    n = rows // kv.num_kv_heads * num_q_heads * 128
+    dev, i32 = s.device, torch.int32
+    rows, hkv = row_len.numel(), kv.num_kv_heads
+    n = rows // hkv * num_q_heads * 128
     sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
     out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if ws is None:
-        ws = dense_pa_workspace(rows, kv.num_kv_heads, num_q_heads // kv.num_kv_heads, q_group, q.device)
+        ws = dense_pa_workspace(rows, hkv, num_q_heads // hkv, q_group, q.device)
     if block_table.dim() != 2:
         raise ValueError("block_table is not [sequences, blocks]")
-    qt = torch.bfloat16 if q_dtype == BF16 else (torch.uint8, torch.float8_e4m3fn)
-    i32 = torch.int32
+    # e4m3 queries may be given as the type or as bytes
+    qt = torch.bfloat16 if q_dtype == BF16 else torch.float8_e4m3fn if q.dtype is torch.float8_e4m3fn else torch.uint8
     _check("bsp_dense_pa_decode",
-           lib().bsp_dense_pa_decode(C.byref(kv.desc), _dense("q", q, qt, s, n), q_dtype, num_q_heads,
-                                     _dense("block_table", block_table, i32, s), block_table.shape[1],
-                                     _dense("row_seq", row_seq, i32, s, rows), _dense("row_len", row_len, i32, s),
-                                     rows, q_group, sm_scale, _dense("out", out, torch.bfloat16, s, n),
-                                     _dense("ws", ws, torch.uint8, s), ws.numel(),
-                                     _dense("dev_err", dev_err, i32, s, 1), _stream(s)))
+           lib().bsp_dense_pa_decode(C.byref(kv.desc), _dense("q", q, qt, dev, n), q_dtype, num_q_heads,
+                                     _dense("block_table", block_table, i32, dev), block_table.shape[1],
+                                     _dense("row_seq", row_seq, i32, dev, rows), _dense("row_len", row_len, i32, dev),
+                                     rows, q_group, sm_scale, _dense("out", out, torch.bfloat16, dev, n),
+                                     _dense("ws", ws, torch.uint8, dev), ws.numel(),
+                                     _dense("dev_err", dev_err, i32, dev, 1), s.cuda_stream))
     return out

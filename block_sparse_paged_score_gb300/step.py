@@ -231,8 +231,7 @@ class StepTables:
         self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
         a = self.args = bsp.StepTablesArgs()
         a.num_seqs, a.bt_stride, a.token_capacity, a.num_blocks = num_seqs, bt_stride, token_capacity, num_blocks
-        s = torch.cuda.current_stream(self.seq_lens.device)
-        a.block_table = bsp._dense("block_table", block_table, torch.int32, s)
+        a.block_table = bsp._dense("block_table", block_table, torch.int32, self.seq_lens.device)
         a.seq_lens, a.cu_tokens, a.blocks_taken = (self.seq_lens.data_ptr(), self.cu_tokens.data_ptr(),
                                                    self.blocks_taken.data_ptr())
         a.slot, a.query_req_id, a.query_abs_pos = (self.slot.data_ptr(), self.query_req_id.data_ptr(),
@@ -244,13 +243,13 @@ class StepTables:
         block ids, and how many of them were taken before (a device scalar;
         None: 0); fills the outputs."""
         s = stream if stream is not None else torch.cuda.current_stream()
-        a, i32 = self.args, torch.int32
-        if self.seq_lens.device != s.device:
-            raise ValueError(f"the tables are on {self.seq_lens.device}, the stream on {s.device}")
-        a.context_lens = bsp._dense("context_lens", context_lens, i32, s, self.num_seqs)
-        a.new_lens = bsp._dense("new_lens", new_lens, i32, s, self.num_seqs)
-        a.free_blocks, a.num_free = bsp._dense("free_blocks", free_blocks, i32, s), free_blocks.numel()
-        a.free_head = bsp._dense("free_head", free_head, i32, s, 1)
+        a, i32, dev = self.args, torch.int32, s.device
+        if self.seq_lens.device != dev:
+            raise ValueError(f"the tables are on {self.seq_lens.device}, the stream on {dev}")
+        a.context_lens = bsp._dense("context_lens", context_lens, i32, dev, self.num_seqs)
+        a.new_lens = bsp._dense("new_lens", new_lens, i32, dev, self.num_seqs)
+        a.free_blocks, a.num_free = bsp._dense("free_blocks", free_blocks, i32, dev), free_blocks.numel()
+        a.free_head = bsp._dense("free_head", free_head, i32, dev, 1)
         bsp.step_tables(a, s)
         return self
 
@@ -271,7 +270,8 @@ class NormRopeWrite:
                                  dtype=torch.uint8 if q_dtype == bsp.FP8_E4M3 else torch.bfloat16)
         self.idx_q_out = None
         self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
-        s = torch.cuda.current_stream(self.q_out.device)
+        dev = self.device = self.q_out.device
+        self.heads = (num_q_heads, kv.num_kv_heads if kv is not None else 0, idx.num_heads if idx is not None else 0)
         a.num_q_heads, a.q_out_dtype, a.idx_q_out_dtype = num_q_heads, q_dtype, idx_q_dtype
         if kv is not None:
             a.kv, a.num_kv_heads = C.pointer(kv.desc), kv.num_kv_heads
@@ -281,14 +281,15 @@ class NormRopeWrite:
                                          dtype=torch.uint8 if idx_q_dtype == bsp.FP8_E4M3 else torch.bfloat16)
         self.weights = (q_weight, k_weight, idx_q_weight, idx_k_weight)
         a.q_weight, a.k_weight, a.idx_q_weight, a.idx_k_weight = (
-            bsp._dense("weight", w, torch.bfloat16, s, 128) for w in self.weights)
+            bsp._dense("weight", w, torch.bfloat16, dev, 128) for w in self.weights)
         a.weight_offset, a.eps = weight_offset, eps
         self.rope_table = rope_table
         if rope_table is not None:
-            a.rope_table = bsp._dense("rope_table", rope_table, torch.float32, s)
+            a.rope_table = bsp._dense("rope_table", rope_table, torch.float32, dev)
             a.rope_rows, a.rot_dim = rope_table.shape
             a.rope_pairs = int(rope_pairs)
         a.dev_err = self.dev_err.data_ptr()
+        a.q_out = self.q_out.data_ptr()
 
     def run(self, q, k, v, idx_q, idx_k, positions, slot, stream=None):
         """bf16 rows [T, heads, 128] (heads side by side, tokens any distance
@@ -296,29 +297,27 @@ class NormRopeWrite:
         and int64 slots [T]; returns the queries and index queries (views of
         the object's buffers)."""
         s = stream if stream is not None else torch.cuda.current_stream()
-        a = self.args
+        a, dev, rows = self.args, self.device, bsp._head_rows
         T = q.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens, the buffers hold {self.max_tokens}")
-        if self.q_out.device != s.device:
-            raise ValueError(f"the buffers are on {self.q_out.device}, the stream on {s.device}")
-        rows = (("q", q, a.num_q_heads), ("k", k, a.num_kv_heads), ("v", v, a.num_kv_heads),
-                ("idx_q", idx_q, a.num_idx_heads), ("idx_k", idx_k, a.num_idx_heads))
-        for name, t, heads in rows:
-            if t is not None and tuple(t.shape[:2]) != (T, heads):
-                raise ValueError(f"{name} is not [{T}, {heads}, 128]")
+        if s.device != dev:
+            raise ValueError(f"the buffers are on {dev}, the stream on {s.device}")
+        hq, hkv, hidx = self.heads
         a.num_tokens = T
-        a.q, a.q_stride = bsp._head_rows("q", q, s)
-        a.k, a.k_stride = bsp._head_rows("k", k, s)
-        a.v, a.v_stride = bsp._head_rows("v", v, s)
-        a.idx_q, a.idx_q_stride = bsp._head_rows("idx_q", idx_q, s)
-        a.idx_k, a.idx_k_stride = bsp._head_rows("idx_k", idx_k, s)
-        a.positions = bsp._dense("positions", positions, torch.int32, s, T)
-        a.slot = bsp._dense("slot", slot, torch.int64, s, T)
-        a.q_out = self.q_out.data_ptr()
-        a.idx_q_out = self.idx_q_out.data_ptr() if idx_q is not None and self.idx_q_out is not None else None
+        a.q, a.q_stride = rows("q", q, T, hq, dev)
+        a.k, a.k_stride = rows("k", k, T, hkv, dev)
+        a.v, a.v_stride = rows("v", v, T, hkv, dev)
+        a.idx_q, a.idx_q_stride = rows("idx_q", idx_q, T, hidx, dev)
+        a.idx_k, a.idx_k_stride = rows("idx_k", idx_k, T, hidx, dev)
+        a.positions = bsp._dense("positions", positions, torch.int32, dev, T)
+        a.slot = bsp._dense("slot", slot, torch.int64, dev, T)
+        has_idx_q = idx_q is not None and self.idx_q_out is not None
+        a.idx_q_out = self.idx_q_out.data_ptr() if has_idx_q else None
         bsp.norm_rope_write(a, s)
-        return self.q_out[:T], self.idx_q_out[:T] if a.idx_q_out else None
+        if T == self.max_tokens:
+            return self.q_out, self.idx_q_out if has_idx_q else None
+        return self.q_out[:T], self.idx_q_out[:T] if has_idx_q else None
 
 
 def rope_table(positions, rot_dim, theta=10000.0, device="cuda"):

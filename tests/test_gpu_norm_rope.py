@@ -2,11 +2,11 @@
 
 Error of the fp32 row before its one rounding, u = 2^-24: the mean of 128
 squares is off by at most 13u (8 products and sums in a lane, 4 shuffle adds,
-one scaling), so 1/sqrt by 7u + 2u; two products and the weight's sum add 4u;
-the rotation two products and a sum, 3u of |a c| + |b s| <= 2 hypot(a, b).
-Together under 32u hypot(a, b) = 2^-19 hypot(a, b).  A rounding adds half a
-step: 2^-8 |y| for bf16; max(2^-4 |y|, 2^-10) for e4m3; a quarter, a half or
-one below 2, 4 and 6 for e2m1."""
+one scaling), so its inverse root by 7u, and by 4u of the root itself; two
+products and the weight's sum add 4u; the rotation two products and a sum, 3u
+of |a c| + |b s| <= 2 hypot(a, b).  Together under 32u hypot(a, b) = 2^-19
+hypot(a, b).  A rounding adds half a step: 2^-8 |y| for bf16; max(2^-4 |y|,
+2^-10) for e4m3; a quarter, a half or one below 2, 4 and 6 for e2m1."""
 import numpy as np
 import pytest
 import torch

@@ -148,21 +148,25 @@ def test_dense_pa_decode(bsp):
 
 
 def test_the_binding_refuses_other_dtypes_devices_and_strides(bsp):
-    class Stream:
-        device = torch.device("cpu")
+    cpu, other = torch.device("cpu"), torch.device("cuda", 1)
     x = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    assert bsp._dense("x", x, torch.bfloat16, cpu, 4 * 2 * 128) == x.data_ptr() and bsp._dense("x", None, None, cpu) is None
     with pytest.raises(ValueError, match="dtype"):
-        bsp._dense("x", x, torch.int32, Stream)
+        bsp._dense("x", x, torch.int32, cpu)
     with pytest.raises(ValueError, match="contiguous"):
-        bsp._dense("x", x[:, ::2], torch.bfloat16, Stream)
+        bsp._dense("x", x[:, ::2], torch.bfloat16, cpu)
     with pytest.raises(ValueError, match="needed"):
-        bsp._dense("x", x, torch.bfloat16, Stream, 4 * 2 * 128 + 1)
+        bsp._dense("x", x, torch.bfloat16, cpu, 4 * 2 * 128 + 1)
+    with pytest.raises(ValueError, match="stream"):
+        bsp._dense("x", x, torch.bfloat16, other)
+    wide = torch.zeros(4, 4, 128, dtype=torch.bfloat16)
+    assert bsp._head_rows("x", wide[:, 1:3], 4, 2, cpu) == (wide.data_ptr() + 256, 512)
+    assert bsp._head_rows("x", wide[2:3, :1], 1, 1, cpu)[1] == 128 and bsp._head_rows("x", None, 4, 2, cpu) == (None, 0)
     with pytest.raises(ValueError, match="side by side"):
-        bsp._head_rows("x", torch.zeros(4, 4, 128, dtype=torch.bfloat16)[:, ::2], Stream)
+        bsp._head_rows("x", wide[:, ::2], 4, 2, cpu)
     with pytest.raises(ValueError, match="bf16"):
-        bsp._head_rows("x", torch.zeros(4, 4, 64, dtype=torch.bfloat16), Stream)
-    Stream.device = torch.device("cuda", 1)
+        bsp._head_rows("x", torch.zeros(4, 4, 64, dtype=torch.bfloat16), 4, 4, cpu)
+    with pytest.raises(ValueError, match="bf16"):
+        bsp._head_rows("x", x, 4, 3, cpu)
     with pytest.raises(ValueError, match="stream"):
-        bsp._dense("x", x, torch.bfloat16, Stream)
-    with pytest.raises(ValueError, match="stream"):
-        bsp._head_rows("x", x, Stream)
+        bsp._head_rows("x", x, 4, 2, other)
