@@ -59,18 +59,18 @@ namespace bsp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kRows = 16;  // rows of a unit
 // A field (128 tokens x 64 bytes, then 128 x 4 bytes of scales) comes as one box.
 // K: 136 rows of 64 bytes, unpacked to 128; V: 68 rows of 128 bytes.
 constexpr int kKRows = 136, kVRows = 68;
 constexpr int kKTile = kKRows * 128, kVTile = (kVRows + 7) / 8 * 8 * 128;
 static_assert(kKRows * 64 == kMxField && kVRows * 128 == kMxField && kKTile % 1024 == 0);
-constexpr int kRowPad = 64 + 4;    // floats of a row (half its dims) in the merge buffer
-constexpr float kMaxGrow = 6.f;    // the reference maximum moves when a row's maximum grows by more (log2)
-constexpr float kBias = 9.f;       // weights are 2^(z - m + kBias): at most 2^15
-constexpr uint32_t kHeadroom = 2;  // R_c is taken this much above the largest scale byte, so that it seldom grows
-constexpr float kNoMax = -1e30f;   // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
-constexpr int kBand = 15;          // binades a band of V scales spans
+constexpr float kMaxGrow = 6.f;   // the reference maximum moves when a row's maximum grows by more (log2)
+constexpr float kBias = 9.f;      // weights are 2^(z - m + kBias): at most 2^15
+constexpr float kNoMax = -1e30f;  // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
+// V enters the MMA as v * 2^(scale byte - kVRef).  f16 holds that exactly for
+// bytes from kVLow to kVHigh (2^-17 to 2^7); see scale_words.
+constexpr uint32_t kNever = 0x80000000u;  // of a token no row sees
+constexpr int kVRef = 133, kVLow = kVRef - 23, kVHigh = kVRef + 1;
 
 // bytes of the list of cut units at the start of the workspace
 __host__ __device__ constexpr int64_t list_bytes(int64_t ctas) { return (ctas * 8 + 255) / 256 * 256; }
@@ -80,33 +80,31 @@ struct Params {
   float qk_scale;  // sm_scale * log2(e)
   int32_t groups, subs, sub_tokens;  // query groups; units each is cut into, of sub_tokens tokens
   int32_t units, ctas, shares;       // shares = ctas / subs
+  int32_t rows;                      // of a unit's slot in the workspace
   int32_t by_unit;                   // the list of cut units has an entry per unit (else per CTA)
 };
 
 // ---- shared memory -----------------------------------------------------------
-constexpr int kCompute = 4, kThreads = 32 * (kCompute + 1);  // compute warps; and the producer
-// a pair's buffer: P [part][32 tokens][16 rows] f16, V's scales [part][c][4][4][2]
-// f16; a warp's maxima: its rows', then four of scales
-constexpr int kPBytes = 2048, kPairBytes = kPBytes + 512, kTopBytes = kRows * 4 + 16;
-template <bool Q16>
+constexpr int kCompute = 8, kThreads = 32 * (kCompute + 2);  // compute warps, the producer, the warp that issues PV
+template <int N, bool Q16>
 struct Smem {
-  // (as much as three CTAs an SM leave room for)
-  static constexpr int kKStages = 2, kVStages = Q16 ? 2 : 3;
+  // (as much as two CTAs an SM leave room for)
+  static constexpr int kKStages = N == 64 ? 2 : 3, kVStages = N == 16 ? 4 : 3;
+  static constexpr int kPBytes = kBlock * N * 2;  // P [128 tokens][N rows] f16, two of them
   static constexpr int v = kKStages * kKTile;
-  // two buffers per pair of warps; their place is the merge buffer once a
-  // unit's blocks are done
-  static constexpr int pairs = v + kVStages * kVTile;
-  static constexpr int kMergeWarp = kRows * kRowPad * 4;
-  static constexpr int pairs_bytes = std::max(4 * kPairBytes, 2 * kMergeWarp);
-  static constexpr int refs = pairs + pairs_bytes;              // per warp: reference maxima, rescale factors
-  static constexpr int tops = refs + kCompute * 2 * kRows * 4;  // per warp
-  static constexpr int sums = tops + kCompute * kTopBytes;      // per warp: l
-  static constexpr int len = sums + kCompute * kRows * 4;       // [rows] lengths
-  static constexpr int sfq = len + kRows * 4;                   // [2][rows] scale cells of q
-  static constexpr int bars = sfq + 2 * kRows * 4;
-  static constexpr int misc = bars + 16 * 8;                    // bad[4], TMEM address
-  static constexpr int q = (misc + 32 + 1023) / 1024 * 1024;
-  static constexpr int total = q + kRows * 128 * (Q16 ? 2 : 1);
+  static constexpr int p = v + kVStages * kVTile;
+  static constexpr int q = p + 2 * kPBytes;
+  static constexpr int scales = q + N * 128 * (Q16 ? 2 : 1);  // per compute warp: 32 words
+  static constexpr int refs = scales + kCompute * 128;        // [2][N] kBias - m
+  static constexpr int fac = refs + 2 * N * 4;                // [N] rescale factors
+  static constexpr int tops = fac + N * 4;                    // [4][N] maxima, later sums
+  static constexpr int len = tops + 4 * N * 4;                // [N] lengths
+  static constexpr int nan = len + N * 4;                     // [N] 32-dim groups that hold a NaN scale
+  static constexpr int sfq = nan + N * 4;                     // [2][N] scale cells of q
+  static constexpr int bars = sfq + 2 * N * 4;
+  static constexpr int misc = bars + 24 * 8;  // bad[4], TMEM address, commands[2]
+  static constexpr int total = misc + 32;
+  static_assert(p % 1024 == 0 && q % 1024 == 0 && refs % 16 == 0);
 };
 
 // ---- device helpers ------------------------------------------------------------
@@ -125,16 +123,47 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
   d |= static_cast<uint64_t>(1) << 46;            // descriptor version; no swizzle
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// C fp32 columns of the warp's 32 TMEM lanes, and back
+template <int C>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[C]) {
+  static_assert(C == 8 || C == 16);
+  uint32_t r[C];
+  if constexpr (C == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < C; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int C>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[C]) {
+#pragma unroll
+  for (int i = 0; i < C; i += 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr + i),
+                 "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]), "f"(v[i + 6]),
+                 "f"(v[i + 7])
+                 : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 16 lanes x 16 columns: register 2j + h of thread t is lane t / 4 + 8h, column 4j + t % 4
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// D (+)= A B: A [128][16] in TMEM (two 16-bit values a column), B in shared memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -152,23 +181,20 @@ __device__ __forceinline__ void stsf(uint32_t addr, float x) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 __device__ __forceinline__ float ldsf(uint32_t addr) { return __uint_as_float(lds32(addr)); }
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t x) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(x)) : "memory");
-}
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// barrier of a pair of warps that returns whether every / any thread says so
-__device__ __forceinline__ bool pair_all(int id, bool x) {
+// barrier of the compute warps that returns whether every / any thread says so
+__device__ __forceinline__ bool all_of(bool x) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "r"(static_cast<uint32_t>(x)), "n"(32 * kCompute)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ bool pair_any(int id, bool x) { return !pair_all(id, !x); }
+__device__ __forceinline__ bool any_of(bool x) { return !all_of(!x); }
 // mbarriers and copies by shared address
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -218,9 +244,23 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
   return o;
 }
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t x, y, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 // four nibbles of token a (low half) and of token b (high half) -> f16x2
@@ -232,6 +272,14 @@ __device__ __forceinline__ void e2m1x4x2_to_f16x2(uint32_t z, uint32_t (&v)[4]) 
   v[1] = __byte_perm(odd, 0, 0x2404);
   v[2] = even & 0xFF00FF00u;
   v[3] = odd & 0xFF00FF00u;
+}
+// the same as bf16x2, exactly
+__device__ __forceinline__ void e2m1x4x2_to_bf16x2(uint32_t z, uint32_t (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t = z >> (4 * i);  // the magnitude bits under the exponent: times 2^-126
+    v[i] = bmul2(((t & 0x00080008u) << 12) | ((t & 0x00070007u) << 6), 0x7E807E80u);  // times 2^126
+  }
 }
 // x * 2^e for any e (two factors, each a normal float, where one would overflow)
 __device__ __forceinline__ float scale_pow2(float x, int e) {
@@ -353,223 +401,103 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
   }
 }
 
-// One compute warp's running softmax: O of 16 rows in mma accumulators, for the
-// warp's two of the four 32-dim groups (tile 4k + i: dims 8t + i and 8t + 4 + i of
-// group k, of rows g and g + 8); the sums l of the warp's own tokens, a tile of P
-// times ones; and 271 - R_c of groups (0, 2) and (1, 3) in the halves of two words.
-struct State {
-  float o[8][4];
-  float l[4];
-  uint32_t r02, r13;
-};
-constexpr uint32_t kHalves = 0x00010001u;
-constexpr uint32_t kNoScale = 271 * kHalves;  // R_c = 0
-__device__ __forceinline__ uint32_t scale_ref(const State& st, int c) {  // R_c
-  return 271 - ((c & 1 ? st.r13 : st.r02) >> (c & 2 ? 16 : 0) & 0xFFFF);
-}
-
-// where a warp and its pair find things (shared addresses)
-struct Place {
-  uint32_t pair;   // P and V's scales, two buffers
-  uint32_t refs;   // the warp's copy of kBias - m, then rescale factors
-  uint32_t tops;   // the pair's row and scale maxima (both warps')
-  uint32_t lens;
-  int bar, member, lane;
-};
-
-// f16 2^(byte - R_c) of band `band` of the lane's token, 0 outside the band;
-// whether lower bands are left
-__device__ __forceinline__ bool put_band(const State& st, uint32_t vw, uint32_t vcell, int band) {
-  bool low = false;
+// ---- pieces of a compute warp's block -------------------------------------------
+// V's scale bytes s0, s1 of two neighbouring tokens (of which `left` are in the
+// context) as the pair of factors that put_v multiplies by, to the warp's words:
+// f16 2^(byte - kVRef + 14).  Returns whether f16 holds v * 2^(byte - kVRef)
+// exactly; a group of zeros may have any scale below.
+__device__ __forceinline__ bool scale_words(uint32_t s0, uint32_t s1, int left, uint32_t word_at, uint32_t vt, int vtok,
+                                            int quad) {
+  const uint32_t y0 = left > 0 ? s0 - kVLow : kNever, y1 = left > 1 ? s1 - kVLow : kNever;
+  constexpr uint32_t span = kVHigh - kVLow;
+  const uint32_t w0 = y0 <= span ? (y0 + 6) << 10 : 0, w1 = y1 <= span ? (y1 + 6) << 26 : 0;
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at), "r"(w0 | w1) : "memory");
+  bool in = (y0 <= span || y0 == kNever) && (y1 <= span || y1 == kNever);
+  if (__builtin_expect(!in, 0)) {
+    in = true;
+    const uint32_t row = vt + (vtok >> 1) * 128;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int b = vw >> (8 * c) & 0xFF;
-    const int x = b - static_cast<int>(scale_ref(st, c)) + kBand * band + 15;  // f16 exponent field
-    low |= b && x <= 0;
-    sts16(vcell + c * 64, b && x > 0 && x <= 15 ? x << 10 : 0);
-  }
-  return low;
-}
-
-// the lane's weights to its place in P; the halves of rows 4..7 of each 8
-// tokens swap places (banks)
-__device__ __forceinline__ void put_weights(uint32_t p, int lane, const float2 (&x)[8]) {
-  uint32_t pk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) pk[i] = pack_f16x2(ex2_approx(x[i].x), ex2_approx(x[i].y));
-  const uint32_t at = p + lane * 32, flip = (lane & 4) << 2;
-  sts128(at + flip, pk[0], pk[1], pk[2], pk[3]);
-  sts128(at + (16 ^ flip), pk[4], pk[5], pk[6], pk[7]);
-}
-
-// The uncommon way of a block: one that some row does not see whole, V scales
-// outside R_c's band, or a row whose maximum grew.  Both warps of the pair go
-// through it: new R_c, and if any row asks for it new references, from both;
-// O rescaled; the scales and weights written afresh.  Returns whether lower bands
-// of V scales are left.
-__device__ __forceinline__ bool adjust(State& st, const Place& w, uint32_t zt, float qk, bool rows, int n, uint32_t vw,
-                                       uint32_t pbuf, uint32_t vcell) {
-  const uint32_t mine = w.tops + w.member * kTopBytes;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t mx = __reduce_max_sync(0xffffffffu, vw >> (8 * c) & 0xFF);
-    if (w.lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(mine + kRows * 4 + 4 * c), "r"(mx) : "memory");
-  }
-  if (pair_any(w.bar, rows)) {
-    float z[16];
-    tmem_ld16(zt, z);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      z[i] = n < static_cast<int>(lds32(w.lens + i * 4)) ? z[i] * qk : -INFINITY;
-      const float mx = warp_max(z[i]);
-      if (w.lane == 0) stsf(mine + i * 4, mx);
-    }
-    bar_sync(w.bar, 64);
-    float2 x[8];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float mx = fmaxf(ldsf(w.tops + i * 4), ldsf(w.tops + kTopBytes + i * 4));
-      const float old = ldsf(w.refs + i * 4);  // kBias - m
-      const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
-      (i & 1 ? x[i >> 1].y : x[i >> 1].x) = z[i] + ref;
-      __syncwarp();  // every lane has the old reference
-      if (w.lane == 0) stsf(w.refs + (kRows + i) * 4, ex2_approx(ref - old)), stsf(w.refs + i * 4, ref);
-    }
-    put_weights(pbuf, w.lane, x);
-    __syncwarp();
-    const uint32_t f = w.refs + (kRows + (w.lane >> 2)) * 4;
-    const float a0 = ldsf(f), a1 = ldsf(f + 32);
-    st.l[0] *= a0, st.l[2] *= a1;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) st.o[i][0] *= a0, st.o[i][1] *= a0, st.o[i][2] *= a1, st.o[i][3] *= a1;
-  }
-  uint32_t now[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t at = w.tops + kRows * 4 + 4 * c, old = scale_ref(st, c);
-    const uint32_t mx = max(lds32(at), lds32(at + kTopBytes));
-    now[c] = mx > old ? min(mx + kHeadroom, 255u) : old;
-    if (now[c] != old && (c >> 1) == w.member) {
-      const float f = scale_pow2(1.f, static_cast<int>(old) - static_cast<int>(now[c]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[4 * (c & 1) + i][e] *= f;
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t s = i ? s1 : s0, y = i ? y1 : y0;
+      const uint4 v = lds128(row + (((i * 4 + quad) ^ ((vtok >> 1) & 7)) << 4));
+      in &= y <= span || y == kNever || (s < kVLow && ((v.x | v.y | v.z | v.w) & 0x77777777u) == 0);
     }
   }
-  st.r02 = kNoScale - (now[0] | (now[2] << 16));
-  st.r13 = kNoScale - (now[1] | (now[3] << 16));
-  return pair_any(w.bar, put_band(st, vw, vcell, 0));
+  return in;
+}
+// The factors for bf16, 2^(byte - kVRef), over f16's (for any byte but the NaN's,
+// whose tokens count as 0 here); which rows see a NaN in the group.
+__device__ __noinline__ void mark_nan(uint32_t s0, uint32_t s1, int left, int n, uint32_t word_at, const int* lens,
+                                      uint32_t* nan_of, int rows, int quad) {
+  uint32_t word = 0;
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t s = i ? s1 : s0;
+    if (left <= i) continue;
+    if (s == 255) {
+      for (int r = 0; r < rows; ++r)
+        if (n + i < lens[r]) atomicOr(nan_of + r, 1u << quad);
+    } else {
+      word |= (s > kVRef - 127 ? (s - (kVRef - 127)) << 7 : 1u << s) << (16 * i);
+    }
+  }
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at), "r"(word) : "memory");
 }
 
-// O (+)= P V of the pair's 64 tokens and the warp's half of the dims; the first
-// time also the sums of the warp's own tokens.  DIRECT: into O, else times f
-// through accumulators of their own (a lower band).
-template <bool DIRECT>
-__device__ __forceinline__ void multiply(State& st, uint32_t pair, uint32_t vt, int member, int lane, float f) {
-  const int t = lane & 3, row8 = lane & 7, mat = lane >> 3;
-  const uint32_t prow = pair + ((mat >> 1) * 8 + row8) * 32 + (((mat & 1) << 4) ^ ((row8 & 4) << 2));
-  // V rows of 128 bytes hold two tokens; 16-byte chunk j of row r is at j ^ (r % 8)
-  const int vr = mat * 4 + (row8 >> 1);
-  const uint32_t vrow = vt + vr * 128 + ((((row8 & 1) * 4 + 2 * member) ^ (vr & 7)) << 4);
-  const uint32_t vsc = pair + kPBytes + member * 128 + t * 16;
+// x = z * qk + (kBias - m) of CH rows
+template <int CH>
+__device__ __forceinline__ void load_logits(float2 (&x)[CH / 2], uint32_t zt, uint32_t refs, float qk) {
+  float z[CH];
+  tmem_ld<CH>(zt, z);
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    uint32_t pf[2][4];  // A fragments (rows g, g + 8 x token octets), k-steps 0 and 1 of the part
+  for (int i = 0; i < CH / 4; ++i) {
+    const float4 m = lds128f(refs + 16 * i);
+    x[2 * i] = ffma2({z[4 * i], z[4 * i + 1]}, {qk, qk}, {m.x, m.y});
+    x[2 * i + 1] = ffma2({z[4 * i + 2], z[4 * i + 3]}, {qk, qk}, {m.z, m.w});
+  }
+}
+template <int CH>
+__device__ __forceinline__ void mask_logits(float2 (&x)[CH / 2], int n, uint32_t lens) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) ldsm_x4_trans(pf[k], prow + part * 1024 + k * 512);
-    if (DIRECT && part == member) {
+  for (int i = 0; i < CH / 2; ++i) {
+    if (n >= static_cast<int>(lds32(lens + 8 * i))) x[i].x = -INFINITY;
+    if (n >= static_cast<int>(lds32(lens + 8 * i + 4))) x[i].y = -INFINITY;
+  }
+}
+
+// V of 64 tokens and the warp's 32 dims to TMEM: lane = dim, column = two tokens.
+// ldmatrix.trans hands thread t four nibbles (dims 4 (t / 4) + i) of tokens 2 (t % 4)
+// and + 1 of each 8: dim 4 r + i goes to lane 8 i + r, which the 16x128b stores want.
+template <bool BF16>
+__device__ __forceinline__ void put_v(uint32_t vt, uint32_t ld_at, uint32_t words) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) mma_f16(st.l, pf[k][0], pf[k][1], pf[k][2], pf[k][3], 0x3C003C00u, 0x3C003C00u);
-    }
+  for (int k = 0; k < 2; ++k) {  // 32 tokens
+    uint32_t z[4], lo[8], hi[8];
+    ldsm_x4_trans(z, ld_at + k * 2048);
+    const uint4 s4 = lds128(words + 16 * k);
+    const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t zr[4];
-      ldsm_x4_trans(zr, (vrow + part * 2048) ^ (c << 4));
-      const uint4 s4 = lds128(vsc + part * 256 + c * 64);
-      const uint32_t vs[4] = {s4.x, s4.y, s4.z, s4.w};
-      float y[4][4];
-      if (!DIRECT) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t v0[4], v1[4];
-        e2m1x4x2_to_f16x2(zr[2 * k], v0);
-        e2m1x4x2_to_f16x2(zr[2 * k + 1], v1);
-        const uint32_t a0 = hmul2(pf[k][0], vs[2 * k]), a1 = hmul2(pf[k][1], vs[2 * k]);
-        const uint32_t a2 = hmul2(pf[k][2], vs[2 * k + 1]), a3 = hmul2(pf[k][3], vs[2 * k + 1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma_f16(DIRECT ? st.o[4 * c + i] : y[i], a0, a1, a2, a3, v0[i], v1[i]);
-      }
-      if (!DIRECT) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) st.o[4 * c + i][e] += y[i][e] * f;
+    for (int j = 0; j < 4; ++j) {
+      uint32_t v[4];
+      if (BF16) {
+        e2m1x4x2_to_bf16x2(z[j], v);
+        lo[2 * j] = bmul2(v[0], s[j]), lo[2 * j + 1] = bmul2(v[1], s[j]);
+        hi[2 * j] = bmul2(v[2], s[j]), hi[2 * j + 1] = bmul2(v[3], s[j]);
+      } else {
+        e2m1x4x2_to_f16x2(z[j], v);
+        lo[2 * j] = hmul2(v[0], s[j]), lo[2 * j + 1] = hmul2(v[1], s[j]);
+        hi[2 * j] = hmul2(v[2], s[j]), hi[2 * j + 1] = hmul2(v[3], s[j]);
       }
     }
-  }
-}
-
-// A block's 32 tokens of the warp: their logits are at TMEM address zt (thread =
-// the lane's token n, column = row h, which sees the token if n < lens[h]; whole:
-// every row sees every token); vw the token's V scale bytes (0 where no row sees
-// it), vt the pair's V rows.  Arrives at z_empty once the logits are read.
-__device__ __forceinline__ void attend(State& st, const Place& w, uint32_t zt, uint32_t z_empty, float qk, bool whole,
-                                       int n, uint32_t vw, uint32_t vt, uint32_t buf) {
-  const uint32_t pair = w.pair + buf * kPairBytes, pbuf = pair + w.member * 1024;
-  const uint32_t vcell = pair + kPBytes + w.member * 256 + ((w.lane >> 1) & 3) * 16 + (w.lane >> 3) * 4 +
-                         (w.lane & 1) * 2;  // [part][c][pair of tokens][octet][2]
-  // V's scales as f16 2^(byte - R_c): exponent fields 1..15, two groups a word.
-  // y = byte + 271 - R_c; in 257..271 where f16 holds the scale.
-  const uint32_t y02 = (vw & 0x00FF00FFu) + st.r02, y13 = (vw >> 8 & 0x00FF00FFu) + st.r13;
-  const uint32_t over = (y02 + 240 * kHalves) | (y13 + 240 * kHalves);  // bit 9: y >= 272
-  const uint32_t in = (y02 + 255 * kHalves) & (y13 + 255 * kHalves);    // bit 9: y >= 257
-  const bool scales = (over & (512 * kHalves)) == 0 && (in & (512 * kHalves)) == 512 * kHalves;
-  const uint32_t h02 = (y02 - 256 * kHalves) << 10, h13 = (y13 - 256 * kHalves) << 10;
-  sts16(vcell, h02), sts16(vcell + 64, h13);
-  sts16(vcell + 128, h02 >> 16), sts16(vcell + 192, h13 >> 16);
-  // weights 2^(z - m + kBias), m the rows' reference maxima, taken as if nothing
-  // were uncommon
-  float2 x[8];
-  {
-    float z[16];
-    tmem_ld16(zt, z);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 m = lds128f(w.refs + 16 * i);  // kBias - m
-      x[2 * i] = ffma2({z[4 * i], z[4 * i + 1]}, {qk, qk}, {m.x, m.y});
-      x[2 * i + 1] = ffma2({z[4 * i + 2], z[4 * i + 3]}, {qk, qk}, {m.z, m.w});
-    }
-  }
-  float top = fmaxf(x[0].x, x[0].y);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) top = fmax3(top, x[i].x, x[i].y);
-  const bool rows = whole && top <= kBias + kMaxGrow;
-  put_weights(pbuf, w.lane, x);
-  bool more = false;
-  if (__builtin_expect(!pair_all(w.bar, rows && scales), 0)) more = adjust(st, w, zt, qk, !rows, n, vw, pbuf, vcell);
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncwarp();
-  if (w.lane == 0) arrive(z_empty);
-  multiply<true>(st, pair, vt, w.member, w.lane, 1.f);
-  if (__builtin_expect(more, 0)) {  // the lower bands of V's scales
-#pragma unroll 1
-    for (int band = 1; more; ++band) {
-      bar_sync(w.bar, 64);  // the last band's scales are read
-      more = pair_any(w.bar, put_band(st, vw, vcell, band));
-      multiply<false>(st, pair, vt, w.member, w.lane, scale_pow2(1.f, -kBand * band));
-    }
+    tmem_st_16x128(vt + 16 * k, lo);
+    tmem_st_16x128(vt + 16 * k + (16u << 16), hi);
   }
 }
 
 // ---- the main kernel -----------------------------------------------------------
-template <bool Q16>
+template <int N, bool Q16>
 struct Bars {
-  static constexpr int NK = Smem<Q16>::kKStages, NV = Smem<Q16>::kVStages;
-  static_assert(2 * NK + 2 * NV + 5 <= 16);
+  static constexpr int NK = Smem<N, Q16>::kKStages, NV = Smem<N, Q16>::kVStages;
+  static_assert(2 * NK + 2 * NV + 9 <= 24);
   uint64_t* b;
   __device__ uint64_t* k_full(int i) const { return b + i; }
   __device__ uint64_t* k_empty(int i) const { return b + NK + i; }
@@ -577,34 +505,46 @@ struct Bars {
   __device__ uint64_t* v_empty(int i) const { return b + 2 * NK + NV + i; }
   __device__ uint64_t* z_full(int i) const { return b + 2 * NK + 2 * NV + i; }
   __device__ uint64_t* z_empty(int i) const { return b + 2 * NK + 2 * NV + 2 + i; }
-  __device__ uint64_t* q_full() const { return b + 2 * NK + 2 * NV + 4; }
+  __device__ uint64_t* pv_full(int i) const { return b + 2 * NK + 2 * NV + 4 + i; }  // P and V's tile are written
+  __device__ uint64_t* pv_done(int i) const { return b + 2 * NK + 2 * NV + 6 + i; }  // and multiplied
+  __device__ uint64_t* q_full() const { return b + 2 * NK + 2 * NV + 8; }
 };
 
-// CTAs per SM: 128 registers a thread (with 96, for four, the state spills to an
-// L1 that shared memory leaves next to nothing of: 64 x 128k took 519 us, not 297)
-constexpr int kCtasPerSm = 3;
-// TMEM columns: two z buffers, the scale cells of K and q
-constexpr int kTmemZ = 0, kTmemK = 2 * kRows, kTmemQ = kTmemK + 8, kTmemColumns = 64;
-static_assert(kTmemQ + 8 <= kTmemColumns && kTmemColumns * kCtasPerSm <= 512);
+constexpr int kCtasPerSm = 2;
+// TMEM columns: V's tiles (64 columns of token pairs), O, the logits, the scale
+// cells of K and q
+template <int N, bool Q16>
+struct Tmem {
+  static constexpr int kV = N == 64 ? 1 : 2, kZ = N == 64 ? 1 : 2;  // buffers
+  static constexpr int v = 0, o = v + kV * 64, z = o + N, k = z + kZ * N, q = k + 4 * Smem<N, Q16>::kKStages;
+  static constexpr int kColumns = 256;
+  static_assert(q + 8 <= kColumns && kColumns * kCtasPerSm <= 512);
+};
+// commands to the warp that issues PV
+constexpr uint32_t kAccumulate = 1, kBf16 = 2, kStop = 4;
 
-template <bool Q16>
+template <int N, bool Q16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     dense_pa_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ Params p) {
-  using S = Smem<Q16>;
+  using S = Smem<N, Q16>;
+  using T = Tmem<N, Q16>;
   extern __shared__ __align__(1024) uint8_t smem[];  // (all of it: no static shared memory moves its start)
-  // before the first block the pairs' place serves the scan
-  int64_t* s_sum = reinterpret_cast<int64_t*>(smem + S::pairs);  // [warps]
-  int64_t* s_start = s_sum + kCompute + 1;  // the share's first group, the blocks before it, its blocks
+  // before the first block P's place serves the scan
+  int64_t* s_sum = reinterpret_cast<int64_t*>(smem + S::p);  // [warps]
+  int64_t* s_start = s_sum + kThreads / 32;  // the share's first group, the blocks before it, its blocks
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
   const DensePaParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Bars<Q16> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
+  const Bars<N, Q16> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
   if (tid == 0) {
     for (int i = 0; i < S::kKStages; ++i) mbar_init(bars.k_full(i), 1), mbar_init(bars.k_empty(i), 1);
     for (int i = 0; i < S::kVStages; ++i) mbar_init(bars.v_full(i), 1), mbar_init(bars.v_empty(i), kCompute);
-    for (int i = 0; i < 2; ++i) mbar_init(bars.z_full(i), 1), mbar_init(bars.z_empty(i), kCompute);
-    mbar_init(bars.q_full(), kCompute);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars.z_full(i), 1), mbar_init(bars.z_empty(i), kCompute);
+      mbar_init(bars.pv_full(i), kCompute), mbar_init(bars.pv_done(i), 1);
+    }
+    mbar_init(bars.q_full(), 4);
     mbar_fence_init();
   }
   pdl_wait();
@@ -614,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (warp == kCompute) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(const_cast<const uint32_t*>(misc + 4))),
-                 "n"(kTmemColumns));
+                 "n"(T::kColumns));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
 
@@ -637,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (lane == 31) s_sum[warp] = x;
       __syncthreads();
       int64_t before = base;
-      for (int w = 0; w <= kCompute; ++w) {
+      for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += s_sum[w];
         base += s_sum[w];
       }
@@ -666,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   w.at = at, w.end = min(at + share, total * a.hkv);
   w.g = 0, w.c0 = 0, w.nb = 1;
   if (w.at < w.end) w.g = static_cast<int>(s_start[0]), w.c0 = s_start[1], w.nb = static_cast<int>(s_start[2]);
-  __syncthreads();  // the pairs' place is theirs again
+  __syncthreads();  // the scan's place is P's again
   // cut units: (first CTA, pieces) per unit, or (unit, pieces) per first CTA
   int2* cut = reinterpret_cast<int2*>(a.ws);
   if (!p.by_unit && tid == 0) cut[blockIdx.x] = make_int2(0, 0);
@@ -775,15 +715,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         if (alive) alive = wait_for(z_empty + 8 * buf, z_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t sk = tmem + kTmemK + 4 * mst, z = tmem + kTmemZ + buf * kRows;
+        const uint32_t sk = tmem + T::k + 4 * mst, z = tmem + T::z + buf * N;
         const uint64_t kd = k_desc + mst * (kKTile / 16);
         scales_to_tmem(sk, cells);
 #pragma unroll
         for (int part = 0; part < (Q16 ? 2 : 1); ++part)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            umma_mx(z, kd + 2 * c, q_desc + (part * kRows * 128 + 32 * c) / 16,
-                    idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, kRows, 128, c, c), sk, tmem + kTmemQ + 4 * part,
+            umma_mx(z, kd + 2 * c, q_desc + (part * N * 128 + 32 * c) / 16,
+                    idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, N, 128, c, c), sk, tmem + T::q + 4 * part,
                     part > 0 || c > 0);
         commit(k_empty + 8 * mst);
         commit(z_full + 8 * buf);
@@ -792,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       last = k_empty + 8 * mst, last_phase = m_phase;
       if (++mst == S::kKStages) mst = 0, m_phase ^= 1;
-      buf ^= 1, z_phase ^= buf ^ 1;
+      if (++buf == T::kZ) buf = 0, z_phase ^= 1;
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) q_id[j] = q_id[j + 1], q_head[j] = q_head[j + 1];
       __syncwarp();
@@ -800,149 +740,297 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // nothing may still write shared memory or TMEM when the CTA leaves
     if (lane == 0 && alive && last) wait_for(last, last_phase, a.err);
     __syncwarp();
+  } else if (warp == kCompute + 1) {
+    // ---- O += V^T P, a round at a time, as the compute warps ask for it ----
+    const uint32_t pv_full = smem_u32(bars.pv_full(0)), pv_done = smem_u32(bars.pv_done(0));
+    // P: rows of 2N bytes, one atom of the 2N-byte swizzle wide, 8 tokens an atom
+    uint64_t desc = (smem_u32(smem + S::p) & 0x3FFFF) >> 4;
+    desc |= static_cast<uint64_t>(1) << 16;                  // leading offset: unused
+    desc |= static_cast<uint64_t>(8 * 2 * N >> 4) << 32;     // 8 tokens
+    desc |= static_cast<uint64_t>(1) << 46;                  // descriptor version
+    desc |= static_cast<uint64_t>(N == 16 ? 6 : N == 32 ? 4 : 2) << 61;  // 32-, 64-, 128-byte swizzle
+    constexpr uint32_t idesc = (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);  // B: rows contiguous
+    if (lane == 0) {
+      uint32_t r = 0;
+#pragma unroll 1
+      for (; alive; ++r) {
+        const uint32_t b = r & 1;
+        alive = wait_for(pv_full + 8 * b, (r >> 1) & 1, a.err);
+        const uint32_t cmd = misc[5 + b];
+        if (!alive || (cmd & kStop)) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t id = idesc | (cmd & kBf16 ? (1u << 7) | (1u << 10) : 0);
+        const uint32_t v = tmem + T::v + (T::kV == 2 ? b * 64 : 0);
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k)
+          umma_ts(tmem + T::o, v + 8 * k, desc + (b * S::kPBytes + k * 16 * 2 * N) / 16, id, k > 0 || (cmd & kAccumulate));
+        commit(pv_done + 8 * b);
+      }
+      // the last round has ended when the CTA leaves
+      if (alive && r) wait_for(pv_done + 8 * ((r - 1) & 1), ((r - 1) >> 1) & 1, a.err);
+    }
+    __syncwarp();
   } else {
     // ---- compute ----
-    const int member = warp & 1;
-    Place at_;
-    at_.pair = smem_u32(smem + S::pairs) + (warp >> 1) * 2 * kPairBytes;
-    at_.refs = smem_u32(smem + S::refs) + warp * 2 * kRows * 4;
-    at_.tops = smem_u32(smem + S::tops) + (warp >> 1) * 2 * kTopBytes;
-    at_.lens = smem_u32(smem + S::len);
-    at_.bar = 2 + (warp >> 1), at_.member = member, at_.lane = lane;
-    const uint32_t merge = smem_u32(smem + S::pairs) + member * S::kMergeWarp, sums = smem_u32(smem + S::sums);
+    // Warp: TMEM lanes 32 * quad .., that is the logits of the block's tokens
+    // 32 * quad .. and O's dims of 32-dim group quad; of both the half of the rows.
+    // Of V it takes that group of 64 tokens.
+    constexpr int R = N / 2, CH = R < 16 ? R : 16;  // rows of a warp, and of them at a time
+    constexpr bool kHold = R == CH;                 // the logits stay in registers between the two passes
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t tops = base + S::tops, lens_at = base + S::len, fac = base + S::fac;
     int* lens = reinterpret_cast<int*>(smem + S::len);
-    uint8_t* cells = smem + S::sfq;
-    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
-    const int g = lane >> 2, t = lane & 3;
+    uint32_t* nan_of = reinterpret_cast<uint32_t*>(smem + S::nan);
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t z_at = tmem + lane_base + T::z + half * R, o_at = tmem + lane_base + T::o + half * R;
+    const uint32_t vt_at = tmem + lane_base + T::v + half * 32;
     const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0));
     const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
-    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc)), z_at = tmem + lane_base + kTmemZ;
-    // the token's scales: row 64 + warp of V's tile, 16-byte chunk lane / 4 at its swizzled place
-    const uint32_t vs_at = smem_u32(smem + S::v) + (64 + warp) * 128 + (((lane >> 2) ^ warp) << 4) + (lane & 3) * 4;
-    const uint32_t v_at = smem_u32(smem + S::v) + (warp >> 1) * 4096;
-    uint32_t buf = 0, z_phase = 0, vst = 0, v_phase = 0;  // of the next block
+    const uint32_t pv_full = smem_u32(bars.pv_full(0)), pv_done = smem_u32(bars.pv_done(0));
+    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc));
+    // scales of V: lane's tokens vtok, vtok + 1; their cells, in row 64 + token / 32
+    const int vtok = 64 * half + 2 * lane;
+    const uint32_t cell_at = base + S::v + (64 + (vtok >> 5)) * 128 + ((((vtok & 31) >> 2) ^ (vtok >> 5)) << 4) +
+                             (vtok & 3) * 4;
+    const uint32_t words = base + S::scales + warp * 128;
+    const uint32_t word_at = words + ((lane & 3) * 8 + (lane >> 2)) * 4, my_words = words + (lane & 3) * 32;
+    // the lane's row for ldmatrix: token 64 * half + lane (+ 32), two tokens a row of 128 bytes
+    const int vrow = 32 * half + (lane >> 1);
+    const uint32_t ld_at = base + S::v + vrow * 128 + ((((lane & 1) * 4 + quad) ^ (vrow & 7)) << 4);
+    // the lane's token in P
+    const int tok = 32 * quad + lane;
+    const uint32_t swz = (tok & 7) >> (N == 16 ? 2 : N == 32 ? 1 : 0);
+    const uint32_t p_at = base + S::p + tok * 2 * N;
+    uint32_t zb = 0, z_phase = 0, vst = 0, v_phase = 0;  // of the next block
+    uint32_t round = 0;                                  // of PV
+    uint32_t cur = 0;                                    // which reference maxima
+    auto done = [&](uint32_t r) {  // round r - 1 has ended
+      if (r && alive) alive = wait_for(pv_done + 8 * ((r - 1) & 1), ((r - 1) >> 1) & 1, a.err);
+    };
     while (w.next(p, sub, lane)) {
-      bar_sync(1, 32 * kCompute);  // the last unit's q, lengths and merge buffers are no longer read
+      bar_sync(1, 32 * kCompute);  // the last unit's q, lengths and sums are no longer read
       if (w.nblk)
-        for (int i = tid; i < kRows * 8; i += 32 * kCompute)
-          stage_q<Q16>(a, w.tok0, w.tokens, w.h, smem + S::q, kRows, cells, i);
-      if (tid < kRows) {
+        for (int i = tid; i < N * 8; i += 32 * kCompute)
+          stage_q<Q16>(a, w.tok0, w.tokens, w.h, smem + S::q, N, smem + S::sfq, i);
+      if (tid < N) {
         const int j = tid / a.group;
-        lens[tid] = j < w.tokens ? min(max(a.row_len[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h], 0), w.max_len) : 0;
+        // (rows that no token has see what the longest sees: they must not look uncommon)
+        lens[tid] = j < w.tokens ? min(max(a.row_len[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h], 0), w.max_len)
+                                 : w.max_len;
+        nan_of[tid] = 0;
+        stsf(base + S::refs + (cur * N + tid) * 4, kBias - kNoMax);
       }
       if (tid < w.tokens && a.row_seq[static_cast<int64_t>(w.tok0 + tid) * a.hkv + w.h] != w.seq)
         set_err(a.err, BSP_DEVERR_GROUP_SEQ);
-      State st;
+      float2 l[R / 2];  // of the lane's token in every block
 #pragma unroll
-      for (int k = 0; k < 8; ++k) st.o[k][0] = st.o[k][1] = st.o[k][2] = st.o[k][3] = 0.f;
-      st.l[0] = st.l[1] = st.l[2] = st.l[3] = 0.f;
-      st.r02 = st.r13 = kNoScale;
-      if (lane < kRows) stsf(at_.refs + 4 * lane, kBias - kNoMax);
+      for (int i = 0; i < R / 2; ++i) l[i] = make_float2(0.f, 0.f);
       fence_proxy_async();  // the tensor core reads q through the async proxy
       bar_sync(1, 32 * kCompute);
-      if (w.nblk) {
+      if (w.nblk && half == 0) {
 #pragma unroll
         for (int k = 0; k < (Q16 ? 2 : 1); ++k) {  // q's scale cells, in this sub-partition's copy
-          const uint32_t cell =
-              lane < kRows ? *reinterpret_cast<const uint32_t*>(cells + (k * kRows + lane) * 4) : 0x7F7F7F7Fu;
-          tmem_st4(tmem + lane_base + kTmemQ + 4 * k, cell, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          const uint32_t* c = reinterpret_cast<const uint32_t*>(smem + S::sfq) + k * N;
+          tmem_st4(tmem + lane_base + T::q + 4 * k, lane < N ? c[lane] : 0x7F7F7F7Fu,
+                   32 + lane < N ? c[32 + lane] : 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.q_full());
       }
-      int n = w.b0 * kBlock + tid;                       // the lane's token
-      const int n_whole = w.min_len - (kBlock - 1) + tid;  // below: every row sees the block whole
-      const int max_len = w.max_len;
-      for (int k = w.nblk; k > 0; --k, n += kBlock) {
-        // after a timed-out wait the warp goes on without waits (the pair's
-        // barriers need both warps); its results are void
-        if (alive) alive = wait_for(z_full + 8 * buf, z_phase, a.err) && wait_for(v_full + 8 * vst, v_phase, a.err);
+      bool first = true;  // no PV round of the unit yet
+      int n0 = w.b0 * kBlock;
+#pragma unroll 1
+      for (int k = w.nblk; k > 0; --k, n0 += kBlock) {
+        // after a timed-out wait the warp goes on without waits (the barriers need
+        // every warp); its results are void
+        if (alive) alive = wait_for(z_full + 8 * zb, z_phase, a.err) && wait_for(v_full + 8 * vst, v_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (lds32(bad_at + 4 * vst) == 0) {
-          uint32_t vw = lds32(vs_at + vst * kVTile);
-          if (n >= max_len) vw = 0;
-          attend(st, at_, z_at + buf * kRows, z_empty + 8 * buf, p.qk_scale, n < n_whole, n, vw,
-                 v_at + vst * kVTile, buf);
-        } else if (lane == 0) {
-          arrive(z_empty + 8 * buf);
+        const bool bad = lds32(bad_at + 4 * vst) != 0;
+        bool skip = false;
+        {
+          const uint32_t z = z_at + zb * N, voff = vst * kVTile;
+          // V's scales: bytes of the lane's two tokens, 0 where no row sees the token
+          const int vn = n0 + vtok;
+          uint32_t s0 = lds32(cell_at + voff) >> (8 * quad) & 0xFF, s1 = lds32(cell_at + voff + 4) >> (8 * quad) & 0xFF;
+          const bool in = scale_words(s0, s1, w.max_len - vn, word_at, base + S::v + voff, vtok, quad);
+          // first pass: does a row's maximum grow?
+          float2 x[CH / 2];
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < R; c += CH) {
+            load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
+          }
+          const bool whole = n0 + kBlock <= w.min_len;
+          bool wide = false;
+          if (__builtin_expect(!all_of(!bad && whole && in && top <= kBias + kMaxGrow), 0)) {
+            // The uncommon way: the rows' maxima, where a row may not see the
+            // token, new references, and O and l in their terms; are V's scales
+            // outside f16's range?
+            skip = any_of(bad);  // (a block whose id is out of range)
+            wide = any_of(!in);
+            const int n = n0 + tok;
+            if (skip) wide = false;
+#pragma unroll 1
+            for (int c = 0; c < (skip ? 0 : R); c += CH) {
+              float y[CH];
+              tmem_ld<CH>(z + c, y);
+#pragma unroll
+              for (int i = 0; i < CH; ++i) {
+                const int row = half * R + c + i;
+                const float mx = warp_max(n < static_cast<int>(lds32(lens_at + row * 4)) ? y[i] * p.qk_scale : -INFINITY);
+                if (lane == 0) stsf(tops + (quad * N + row) * 4, mx);
+              }
+            }
+            bar_sync(1, 32 * kCompute);
+            float f = 1.f;
+            if (tid < N && !skip) {
+              float mx = ldsf(tops + tid * 4);
+#pragma unroll
+              for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + tid) * 4));
+              const float old = ldsf(base + S::refs + (cur * N + tid) * 4);  // kBias - m
+              const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
+              f = ex2_approx(ref - old);
+              stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, ref);
+              stsf(fac + tid * 4, f);
+            }
+            if (!skip) cur ^= 1;
+            if (any_of(f != 1.f) && !first) {
+              done(round);
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+              for (int c = 0; c < R; c += CH) {
+                float y[CH];
+                tmem_ld<CH>(o_at + c, y);
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                  const float g = ldsf(fac + (half * R + c + i) * 4);
+                  y[i] *= g;
+                  (i & 1 ? l[(c + i) >> 1].y : l[(c + i) >> 1].x) *= g;
+                }
+                tmem_st<CH>(o_at + c, y);
+              }
+            }
+            if (kHold) load_logits<CH>(x, z, base + S::refs + (cur * N + half * R) * 4, p.qk_scale);
+            if (kHold && !whole) mask_logits<CH>(x, n, lens_at + half * R * 4);
+            if (wide) {
+              mark_nan(s0, s1, w.max_len - vn, vn, word_at, lens, nan_of, N, quad);
+            }
+          }
+          // second pass: the weights, and V as the MMA reads it.  Where V's scales
+          // are beyond f16, both are bf16 and the weights go in two parts.
+#pragma unroll 1
+          for (int part = 0; part < (skip ? 0 : wide ? 2 : 1); ++part, ++round) {
+            const uint32_t b = round & 1;
+            done(round < 2 ? 0 : round - 1);  // the last round of this P (and V, if there are two) has ended
+#pragma unroll
+            for (int c = 0; c < R; c += CH) {
+              if (!kHold) {
+                load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+                if (!whole) mask_logits<CH>(x, n0 + tok, lens_at + (half * R + c) * 4);
+              }
+              uint32_t pk[CH / 2];
+#pragma unroll
+              for (int i = 0; i < CH / 2; ++i) {
+                const float2 e = make_float2(ex2_approx(x[i].x), ex2_approx(x[i].y));
+                if (part == 0) l[c / 2 + i] = fadd2(l[c / 2 + i], e);
+                pk[i] = pack_f16x2(e.x, e.y);
+                if (__builtin_expect(wide, 0)) {
+                  pk[i] = pack_bf16x2(e.x, e.y);
+                  if (part)
+                    pk[i] = pack_bf16x2(e.x - bf16_bits_to_float(pk[i] & 0xFFFF), e.y - bf16_bits_to_float(pk[i] >> 16));
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < CH / 8; ++i)
+                sts128(p_at + b * S::kPBytes + (((half * R + c) / 8 + i) ^ swz) * 16, pk[4 * i], pk[4 * i + 1],
+                       pk[4 * i + 2], pk[4 * i + 3]);
+            }
+            if (!wide || part) {  // the logits are read
+              asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) arrive(z_empty + 8 * zb);
+            }
+            if (T::kV == 1) done(round);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            __syncwarp();  // the factors are written
+            const uint32_t vt = vt_at + (T::kV == 2 ? b * 64 : 0);
+            if (__builtin_expect(wide, 0))
+              put_v<true>(vt, ld_at + voff, my_words);
+            else
+              put_v<false>(vt, ld_at + voff, my_words);
+            if (tid == 0) misc[5 + b] = (first ? 0 : kAccumulate) | (wide ? kBf16 : 0);
+            first = false;
+            fence_proxy_async();  // the tensor core reads P through the async proxy
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive(pv_full + 8 * b);
+          }
+        }
+        if (__builtin_expect(skip, 0)) {
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) arrive(z_empty + 8 * zb);
         }
         __syncwarp();
         if (lane == 0) arrive(v_empty + 8 * vst);
-        buf ^= 1, z_phase ^= buf ^ 1;
+        if (++zb == T::kZ) zb = 0, z_phase ^= 1;
         if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
       }
 
-      // -- the two pairs joined: warps 2 and 3 hand their O to 0 and 1
+      // -- the unit's sums, and O to where it goes
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int e = static_cast<int>(member ? scale_ref(st, 2 + c) : scale_ref(st, c)) - 127 + 14;
+      for (int i = 0; i < R; ++i) {
+        float y = i & 1 ? l[i >> 1].y : l[i >> 1].x;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) st.o[4 * c + k][j] = scale_pow2(st.o[4 * c + k][j], e);
-      }
-      if (t == 0) {  // every column of the tile is the sum
-        stsf(sums + (warp * kRows + g) * 4, st.l[0]);
-        stsf(sums + (warp * kRows + g + 8) * 4, st.l[2]);
-      }
-      bar_sync(1, 32 * kCompute);  // the pairs' place becomes the merge buffer
-      const uint32_t mrow = merge + (g * kRowPad + 8 * t) * 4;
-      if (warp >= 2) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              sts128(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4, __float_as_uint(st.o[4 * c][2 * e + j]),
-                     __float_as_uint(st.o[4 * c + 1][2 * e + j]), __float_as_uint(st.o[4 * c + 2][2 * e + j]),
-                     __float_as_uint(st.o[4 * c + 3][2 * e + j]));
+        for (int d = 1; d < 32; d <<= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+        if (lane == 0) stsf(tops + (quad * N + half * R + i) * 4, y);
       }
       bar_sync(1, 32 * kCompute);
-      if (warp < 2) {
-        // a CTA's slots: 2 * CTA for a unit that began before its share, + 1
-        // for one that goes on after it
-        float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
-                    (2LL * blockIdx.x + (w.starts ? 1 : 0)) * kRows * (kDim + 2);
-        const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
+      if (!first) done(round);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const bool all = w.starts && w.ends;
+      // a CTA's slots: 2 * CTA for a unit that began before its share, + 1 for one
+      // that goes on after it
+      float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
+                  (2LL * blockIdx.x + (w.starts ? 1 : 0)) * N * (kDim + 2);
+      const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
+      const int d = 32 * quad + 4 * (lane & 7) + (lane >> 3);  // the lane's dim (see put_v)
+#pragma unroll 1
+      for (int c = 0; c < R; c += CH) {
+        float y[CH];
+        if (!first) {
+          tmem_ld<CH>(o_at + c, y);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * e + g;
-            if (r >= w.tokens * a.group) continue;
-          const float m0 = kBias - ldsf(at_.refs + 4 * r);
-          const float m1 = kBias - ldsf(smem_u32(smem + S::refs) + (2 * 2 * kRows + r) * 4);
-          const float M = fmaxf(m0, m1), f0 = ex2_approx(m0 - M), f1 = ex2_approx(m1 - M);
-          const float l = f0 * (ldsf(sums + r * 4) + ldsf(sums + (kRows + r) * 4)) +
-                          f1 * (ldsf(sums + (2 * kRows + r) * 4) + ldsf(sums + (3 * kRows + r) * 4));
-          const bool all = w.starts && w.ends;
-          const float inv = all ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+          for (int i = 0; i < CH; ++i) y[i] = 0.f;
+        }
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x[8];
+        for (int i = 0; i < CH; ++i) {
+          const int r = half * R + c + i;
+          if (r >= w.tokens * a.group) break;
+          float sum = ldsf(tops + r * 4);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float4 y = lds128f(mrow + (8 * e * kRowPad + 32 * c + 4 * j) * 4);
-              x[4 * j] = (st.o[4 * c][2 * e + j] * f0 + y.x * f1) * inv;
-              x[4 * j + 1] = (st.o[4 * c + 1][2 * e + j] * f0 + y.y * f1) * inv;
-              x[4 * j + 2] = (st.o[4 * c + 2][2 * e + j] * f0 + y.z * f1) * inv;
-              x[4 * j + 3] = (st.o[4 * c + 3][2 * e + j] * f0 + y.w * f1) * inv;
-            }
-            const int d = 64 * member + 32 * c + 8 * t;
-            if (all) {
-              const int64_t row = (w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group;
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * kDim + d) =
-                  make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                             pack_bf16x2(x[6], x[7]));
-            } else {
-              *reinterpret_cast<float4*>(po + r * kDim + d) = make_float4(x[0], x[1], x[2], x[3]);
-              *reinterpret_cast<float4*>(po + r * kDim + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
-            }
+          for (int j = 1; j < 4; ++j) sum += ldsf(tops + (j * N + r) * 4);
+          float o = y[i] * static_cast<float>(1 << (kVRef - 127));
+          if (nan_of[r] >> quad & 1) o = __uint_as_float(0x7FC00000u);
+          if (all) {
+            const int64_t row = (w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group;
+            o *= sum == 0.f ? 0.f : 1.f / sum;
+            static_cast<__nv_bfloat16*>(a.out)[row * kDim + d] = __float2bfloat16_rn(o);
+          } else {
+            po[r * kDim + d] = o;
+            if (quad == 0 && lane == 0)
+              *reinterpret_cast<float2*>(po + N * kDim + 2 * r) =
+                  make_float2(kBias - ldsf(base + S::refs + (cur * N + r) * 4), sum);
           }
-          if (!all && member == 0 && t == 0)
-            *reinterpret_cast<float2*>(po + kRows * kDim + 2 * r) = make_float2(M, l);
-          }
+        }
       }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       if (w.starts && tid == 0) {
         // the pieces of the unit: shares from this one to that of its last block
         const int64_t last = w.c0 * a.hkv + static_cast<int64_t>(w.h + 1) * w.nb - 1;
@@ -953,12 +1041,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           cut[blockIdx.x] = make_int2(w.unit, pieces);
       }
     }
+    if (tid == 0) misc[5 + (round & 1)] = kStop;
+    __syncwarp();
+    if (lane == 0) arrive(pv_full + 8 * (round & 1));
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == kCompute) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemColumns));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(T::kColumns));
   }
 }
 
@@ -985,7 +1076,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
       min(static_cast<int64_t>(min(p.sub_tokens, a.q_group - sub * p.sub_tokens)), a.num_rows / a.hkv - tok0));
   const bool live = row < tokens * a.group;
   const float* base = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + list_bytes(p.ctas));
-  const int64_t slot_floats = kRows * (kDim + 2);
+  const int64_t slot_floats = static_cast<int64_t>(p.rows) * (kDim + 2);
 
   float M = kNoMax, L = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -995,7 +1086,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
       const int k = k0 + lane * parts;
       const int64_t slot = k == 0 ? 2LL * c0 + 1 : 2LL * (c0 + static_cast<int64_t>(k) * p.subs);
       float2 ml = make_float2(kNoMax, 0.f);
-      if (k < pieces) ml = *reinterpret_cast<const float2*>(base + slot * slot_floats + kRows * kDim + 2 * row);
+      if (k < pieces) ml = *reinterpret_cast<const float2*>(base + slot * slot_floats + p.rows * kDim + 2 * row);
       float mx = ml.x;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -1033,7 +1124,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
     }
   }
   if (!live) return;
-  const float f = L > 0.f ? 1.f / L : 0.f;
+  const float f = L == 0.f ? 0.f : 1.f / L;
   const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
   const int64_t e = ((tok0 + row / a.group) * hq + static_cast<int64_t>(h) * a.group + row % a.group) * kDim + 4 * lane;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e) =
@@ -1058,35 +1149,36 @@ bool make_map_side(CUtensorMap* m, bool unpack, const void* base, uint64_t heads
          CUDA_SUCCESS;
 }
 
-// How a group's rows are cut into units of 16.  (Warps of 32 rows, which convert
-// V's bytes once for both halves, were tried: their state leaves too few
-// registers, 128 x 32k with 64 rows a group took 581-647 us, 8 or 12 warps an SM.)
+// How a group's rows are cut into units of at most 64, and the rows the kernel is
+// built for.
 struct Plan {
-  int sub_tokens, subs;
+  int sub_tokens, subs, rows;
 };
 Plan plan_of(int group, int q_group) {
-  const int sub = std::min(q_group, kRows / group), subs = (q_group + sub - 1) / sub;
-  return {(q_group + subs - 1) / subs, subs};  // units of about the same size
+  const int sub = std::min(q_group, 64 / group), subs = (q_group + sub - 1) / sub;
+  const int tokens = (q_group + subs - 1) / subs, rows = tokens * group;  // units of about the same size
+  return {tokens, subs, rows <= 16 ? 16 : rows <= 32 ? 32 : 64};
 }
 
-template <bool Q16>
+template <int N, bool Q16>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
-  static_assert((Smem<Q16>::total + 1024) * kCtasPerSm <= 228 * 1024);
+  using S = Smem<N, Q16>;
+  static_assert((S::total + 1024) * kCtasPerSm <= 228 * 1024);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {  // the shared-memory opt-in
-    return cudaFuncSetAttribute(dense_pa_kernel<Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<Q16>::total);
+    return cudaFuncSetAttribute(dense_pa_kernel<N, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
   });
   if (e != cudaSuccess) return e;
-  return launch_kernel(dense_pa_kernel<Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), Smem<Q16>::total, s,
-                       0, mk, mv, p);
+  return launch_kernel(dense_pa_kernel<N, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), S::total, s, 0, mk,
+                       mv, p);
 }
 
 }  // namespace
 
 size_t dense_pa_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms) {
-  (void)num_rows, (void)hkv, (void)group, (void)q_group;
+  (void)num_rows, (void)hkv;
   const int64_t ctas = static_cast<int64_t>(kCtasPerSm) * num_sms;
-  return list_bytes(ctas) + 2 * ctas * kRows * (kDim + 2) * sizeof(float);
+  return list_bytes(ctas) + 2 * ctas * plan_of(group, q_group).rows * (kDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s, int* launches) {
@@ -1100,6 +1192,7 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   p.groups = (tokens + a.q_group - 1) / a.q_group;
   p.subs = pl.subs;
   p.sub_tokens = pl.sub_tokens;
+  p.rows = pl.rows;
   const int64_t pairs = static_cast<int64_t>(p.groups) * a.hkv, units = pairs * pl.subs;
   if (units > INT32_MAX) return cudaErrorNotSupported;
   p.units = static_cast<int32_t>(units);
@@ -1112,7 +1205,13 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   if (!make_map_side(&mk, true, a.k_base, a.hkv, blocks, a.id_stride) ||
       !make_map_side(&mv, false, a.v_base, a.hkv, blocks, a.id_stride))
     return cudaErrorInvalidValue;
-  cudaError_t e = q16 ? launch_main<true>(mk, mv, p, s) : launch_main<false>(mk, mv, p, s);
+  cudaError_t e;
+  if (pl.rows == 16)
+    e = q16 ? launch_main<16, true>(mk, mv, p, s) : launch_main<16, false>(mk, mv, p, s);
+  else if (pl.rows == 32)
+    e = q16 ? launch_main<32, true>(mk, mv, p, s) : launch_main<32, false>(mk, mv, p, s);
+  else
+    e = q16 ? launch_main<64, true>(mk, mv, p, s) : launch_main<64, false>(mk, mv, p, s);
   if (e != cudaSuccess) return e;
   ++*launches;
   if (p.shares > 1) {
