@@ -49,6 +49,7 @@
 // waits no more (the error word is set, the results are void), walks through its
 // blocks and the CTA frees its TMEM and returns.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -64,8 +65,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKRows = 136, kVRows = 68;
 constexpr int kKTile = kKRows * 128, kVTile = (kVRows + 7) / 8 * 8 * 128;
 static_assert(kKRows * 64 == kMxField && kVRows * 128 == kMxField && kKTile % 1024 == 0);
-constexpr float kMaxGrow = 6.f;   // the reference maximum moves when a row's maximum grows by more (log2)
-constexpr float kBias = 9.f;      // weights are 2^(z - m + kBias): at most 2^15
+constexpr float kMaxGrow = 8.f;   // the reference maximum moves when a row's maximum grows by more (log2)
+constexpr float kBias = 7.f;      // weights are 2^(z - m + kBias): at most 2^15
 constexpr float kNoMax = -1e30f;  // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
 // V enters the MMA as v * 2^(scale byte - kVRef).  f16 holds that exactly for
 // bytes from kVLow to kVHigh (2^-17 to 2^7); see scale_words.
@@ -85,17 +86,26 @@ struct Params {
 };
 
 // ---- shared memory -----------------------------------------------------------
-constexpr int kCompute = 8, kThreads = 32 * (kCompute + 2);  // compute warps, the producer, the warp that issues PV
+// Units of 16 rows: four compute warps a CTA, three CTAs an SM; of more: eight, two.
+// Then the producer and the warp that issues PV.
+template <int N>
+struct Shape {
+  static constexpr int kCompute = N == 16 ? 4 : 8, kThreads = 32 * (kCompute + 2), kCtasPerSm = N == 16 ? 3 : 2;
+  static constexpr int kHalves = kCompute / 4;          // warps that share 32 TMEM lanes
+  static constexpr int kRows = N / kHalves;             // a compute warp's
+  static constexpr int kTokens = kBlock / kHalves;      // of V
+};
 template <int N, bool Q16>
 struct Smem {
   // (as much as two CTAs an SM leave room for)
-  static constexpr int kKStages = N == 64 ? 2 : 3, kVStages = N == 16 ? 4 : 3;
+  static constexpr int kCompute = Shape<N>::kCompute;
+  static constexpr int kKStages = N == 32 ? 3 : 2, kVStages = N == 16 && Q16 ? 2 : 3;
   static constexpr int kPBytes = kBlock * N * 2;  // P [128 tokens][N rows] f16, two of them
   static constexpr int v = kKStages * kKTile;
   static constexpr int p = v + kVStages * kVTile;
   static constexpr int q = p + 2 * kPBytes;
-  static constexpr int scales = q + N * 128 * (Q16 ? 2 : 1);  // per compute warp: 32 words
-  static constexpr int refs = scales + kCompute * 128;        // [2][N] kBias - m
+  static constexpr int scales = q + N * 128 * (Q16 ? 2 : 1);  // per compute warp: a word for two tokens
+  static constexpr int refs = scales + kCompute * Shape<N>::kTokens * 2;        // [2][N] kBias - m
   static constexpr int fac = refs + 2 * N * 4;                // [N] rescale factors
   static constexpr int tops = fac + N * 4;                    // [4][N] maxima, later sums
   static constexpr int len = tops + 4 * N * 4;                // [N] lengths
@@ -173,6 +183,11 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ float4 lds128f(uint32_t addr) {
   const uint4 v = lds128(addr);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
@@ -185,16 +200,20 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // barrier of the compute warps that returns whether every / any thread says so
+template <int THREADS>
 __device__ __forceinline__ bool all_of(bool x) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "n"(32 * kCompute)
+      : "r"(static_cast<uint32_t>(x)), "n"(THREADS)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ bool any_of(bool x) { return !all_of(!x); }
+template <int THREADS>
+__device__ __forceinline__ bool any_of(bool x) {
+  return !all_of<THREADS>(!x);
+}
 // mbarriers and copies by shared address
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -402,45 +421,55 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
 }
 
 // ---- pieces of a compute warp's block -------------------------------------------
-// V's scale bytes s0, s1 of two neighbouring tokens (of which `left` are in the
-// context) as the pair of factors that put_v multiplies by, to the warp's words:
-// f16 2^(byte - kVRef + 14).  Returns whether f16 holds v * 2^(byte - kVRef)
-// exactly; a group of zeros may have any scale below.
-__device__ __forceinline__ bool scale_words(uint32_t s0, uint32_t s1, int left, uint32_t word_at, uint32_t vt, int vtok,
-                                            int quad) {
-  const uint32_t y0 = left > 0 ? s0 - kVLow : kNever, y1 = left > 1 ? s1 - kVLow : kNever;
+// The scale bytes of V's tokens tok + i and the next (i: 0 or 64; tokens n + i and on
+// of the context of max_len), cells at `cell` for i = 0.  Of tokens behind the
+// context: kNever.
+__device__ __forceinline__ uint2 scale_bytes(uint32_t cell, int quad, int i) {
+  // 64 tokens are two rows of 128 bytes: the chunk's place in its row turns by two
+  const uint2 c = lds64(i ? (cell + 256) ^ 32 : cell);
+  return make_uint2(c.x >> (8 * quad) & 0xFF, c.y >> (8 * quad) & 0xFF);
+}
+// The pair of factors that put_v multiplies the two tokens by, f16
+// 2^(byte - kVRef + 14), to the warp's words.  Returns whether f16 holds
+// v * 2^(byte - kVRef) exactly; a group of zeros may have any scale below.
+__device__ __forceinline__ bool scale_words(uint32_t cell, int n, int max_len, uint32_t word_at, uint32_t vt, int tok,
+                                            int quad, int i) {
+  const uint2 s = scale_bytes(cell, quad, i);
+  const int left = max_len - n - i;
+  const uint32_t y0 = left > 0 ? s.x - kVLow : kNever, y1 = left > 1 ? s.y - kVLow : kNever;
   constexpr uint32_t span = kVHigh - kVLow;
   const uint32_t w0 = y0 <= span ? (y0 + 6) << 10 : 0, w1 = y1 <= span ? (y1 + 6) << 26 : 0;
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at), "r"(w0 | w1) : "memory");
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at + 2 * i), "r"(w0 | w1) : "memory");
   bool in = (y0 <= span || y0 == kNever) && (y1 <= span || y1 == kNever);
   if (__builtin_expect(!in, 0)) {
     in = true;
-    const uint32_t row = vt + (vtok >> 1) * 128;
+    const int r = (tok + i) >> 1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t s = i ? s1 : s0, y = i ? y1 : y0;
-      const uint4 v = lds128(row + (((i * 4 + quad) ^ ((vtok >> 1) & 7)) << 4));
-      in &= y <= span || y == kNever || (s < kVLow && ((v.x | v.y | v.z | v.w) & 0x77777777u) == 0);
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t b = k ? s.y : s.x, y = k ? y1 : y0;
+      const uint4 v = lds128(vt + r * 128 + (((k * 4 + quad) ^ (r & 7)) << 4));
+      in &= y <= span || y == kNever || (b < kVLow && ((v.x | v.y | v.z | v.w) & 0x77777777u) == 0);
     }
   }
   return in;
 }
 // The factors for bf16, 2^(byte - kVRef), over f16's (for any byte but the NaN's,
 // whose tokens count as 0 here); which rows see a NaN in the group.
-__device__ __noinline__ void mark_nan(uint32_t s0, uint32_t s1, int left, int n, uint32_t word_at, const int* lens,
-                                      uint32_t* nan_of, int rows, int quad) {
+__device__ __noinline__ void wide_words(uint32_t cell, int n, int max_len, uint32_t word_at, int quad, int i,
+                                        const int* lens, uint32_t* nan_of, int rows) {
+  const uint2 s = scale_bytes(cell, quad, i);
   uint32_t word = 0;
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t s = i ? s1 : s0;
-    if (left <= i) continue;
-    if (s == 255) {
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t b = k ? s.y : s.x;
+    if (n + i + k >= max_len) continue;
+    if (b == 255) {
       for (int r = 0; r < rows; ++r)
-        if (n + i < lens[r]) atomicOr(nan_of + r, 1u << quad);
+        if (n + i + k < lens[r]) atomicOr(nan_of + r, 1u << quad);
     } else {
-      word |= (s > kVRef - 127 ? (s - (kVRef - 127)) << 7 : 1u << s) << (16 * i);
+      word |= (b > kVRef - 127 ? (b - (kVRef - 127)) << 7 : 1u << b) << (16 * k);
     }
   }
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at), "r"(word) : "memory");
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at + 2 * i), "r"(word) : "memory");
 }
 
 // x = z * qk + (kBias - m) of CH rows
@@ -464,16 +493,16 @@ __device__ __forceinline__ void mask_logits(float2 (&x)[CH / 2], int n, uint32_t
   }
 }
 
-// V of 64 tokens and the warp's 32 dims to TMEM: lane = dim, column = two tokens.
+// V of TOKENS tokens and the warp's 32 dims to TMEM: lane = dim, column = two tokens.
 // ldmatrix.trans hands thread t four nibbles (dims 4 (t / 4) + i) of tokens 2 (t % 4)
 // and + 1 of each 8: dim 4 r + i goes to lane 8 i + r, which the 16x128b stores want.
-template <bool BF16>
+template <bool BF16, int TOKENS>
 __device__ __forceinline__ void put_v(uint32_t vt, uint32_t ld_at, uint32_t words) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {  // 32 tokens
+  for (int k = 0; k < TOKENS / 32; ++k) {
     uint32_t z[4], lo[8], hi[8];
     ldsm_x4_trans(z, ld_at + k * 2048);
-    const uint4 s4 = lds128(words + 16 * k);
+    const uint4 s4 = lds128(words + (k >> 1) * 128 + (k & 1) * 16);
     const uint32_t s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -510,25 +539,25 @@ struct Bars {
   __device__ uint64_t* q_full() const { return b + 2 * NK + 2 * NV + 8; }
 };
 
-constexpr int kCtasPerSm = 2;
 // TMEM columns: V's tiles (64 columns of token pairs), O, the logits, the scale
 // cells of K and q
 template <int N, bool Q16>
 struct Tmem {
-  static constexpr int kV = N == 64 ? 1 : 2, kZ = N == 64 ? 1 : 2;  // buffers
+  static constexpr int kV = N == 32 ? 2 : 1, kZ = N == 64 ? 1 : 2;  // buffers
   static constexpr int v = 0, o = v + kV * 64, z = o + N, k = z + kZ * N, q = k + 4 * Smem<N, Q16>::kKStages;
-  static constexpr int kColumns = 256;
-  static_assert(q + 8 <= kColumns && kColumns * kCtasPerSm <= 512);
+  static constexpr int kColumns = N == 16 ? 128 : 256;
+  static_assert(q + 8 <= kColumns && kColumns * Shape<N>::kCtasPerSm <= 512);
 };
 // commands to the warp that issues PV
 constexpr uint32_t kAccumulate = 1, kBf16 = 2, kStop = 4;
 
 template <int N, bool Q16>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     dense_pa_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                     const __grid_constant__ Params p) {
   using S = Smem<N, Q16>;
   using T = Tmem<N, Q16>;
+  constexpr int kCompute = Shape<N>::kCompute, kThreads = Shape<N>::kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];  // (all of it: no static shared memory moves its start)
   // before the first block P's place serves the scan
   int64_t* s_sum = reinterpret_cast<int64_t*>(smem + S::p);  // [warps]
@@ -773,9 +802,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   } else {
     // ---- compute ----
     // Warp: TMEM lanes 32 * quad .., that is the logits of the block's tokens
-    // 32 * quad .. and O's dims of 32-dim group quad; of both the half of the rows.
-    // Of V it takes that group of 64 tokens.
-    constexpr int R = N / 2, CH = R < 16 ? R : 16;  // rows of a warp, and of them at a time
+    // 32 * quad .. and O's dims of 32-dim group quad; R rows of both.  Of V it takes
+    // that group of VT tokens.
+    constexpr int R = Shape<N>::kRows, CH = 16, VT = Shape<N>::kTokens;  // rows of a warp, and of them at a time
     constexpr bool kHold = R == CH;                 // the logits stay in registers between the two passes
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t base = smem_u32(smem);
@@ -784,19 +813,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint32_t* nan_of = reinterpret_cast<uint32_t*>(smem + S::nan);
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t z_at = tmem + lane_base + T::z + half * R, o_at = tmem + lane_base + T::o + half * R;
-    const uint32_t vt_at = tmem + lane_base + T::v + half * 32;
+    const uint32_t vt_at = tmem + lane_base + T::v + half * (VT / 2);
     const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0));
     const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
     const uint32_t pv_full = smem_u32(bars.pv_full(0)), pv_done = smem_u32(bars.pv_done(0));
     const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc));
-    // scales of V: lane's tokens vtok, vtok + 1; their cells, in row 64 + token / 32
-    const int vtok = 64 * half + 2 * lane;
+    // scales of V: the lane's tokens vtok, vtok + 1 (and 64 further on); their cells,
+    // in row 64 + token / 32
+    const int vtok = VT * half + 2 * lane;
     const uint32_t cell_at = base + S::v + (64 + (vtok >> 5)) * 128 + ((((vtok & 31) >> 2) ^ (vtok >> 5)) << 4) +
                              (vtok & 3) * 4;
-    const uint32_t words = base + S::scales + warp * 128;
+    const uint32_t words = base + S::scales + warp * VT * 2;
     const uint32_t word_at = words + ((lane & 3) * 8 + (lane >> 2)) * 4, my_words = words + (lane & 3) * 32;
-    // the lane's row for ldmatrix: token 64 * half + lane (+ 32), two tokens a row of 128 bytes
-    const int vrow = 32 * half + (lane >> 1);
+    // the lane's row for ldmatrix: token VT * half + lane (+ 32 k), two tokens a row of 128 bytes
+    const int vrow = VT / 2 * half + (lane >> 1);
     const uint32_t ld_at = base + S::v + vrow * 128 + ((((lane & 1) * 4 + quad) ^ (vrow & 7)) << 4);
     // the lane's token in P
     const int tok = 32 * quad + lane;
@@ -840,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (lane == 0) mbar_arrive(bars.q_full());
       }
       bool first = true;  // no PV round of the unit yet
+      const int max_len = w.max_len, min_len = w.min_len;
       int n0 = w.b0 * kBlock;
 #pragma unroll 1
       for (int k = w.nblk; k > 0; --k, n0 += kBlock) {
@@ -847,129 +878,130 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // every warp); its results are void
         if (alive) alive = wait_for(z_full + 8 * zb, z_phase, a.err) && wait_for(v_full + 8 * vst, v_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const bool bad = lds32(bad_at + 4 * vst) != 0;
+        const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 + kBlock <= min_len;
         bool skip = false;
-        {
-          const uint32_t z = z_at + zb * N, voff = vst * kVTile;
-          // V's scales: bytes of the lane's two tokens, 0 where no row sees the token
-          const int vn = n0 + vtok;
-          uint32_t s0 = lds32(cell_at + voff) >> (8 * quad) & 0xFF, s1 = lds32(cell_at + voff + 4) >> (8 * quad) & 0xFF;
-          const bool in = scale_words(s0, s1, w.max_len - vn, word_at, base + S::v + voff, vtok, quad);
-          // first pass: does a row's maximum grow?
-          float2 x[CH / 2];
-          float top = -INFINITY;
+        const uint32_t z = z_at + zb * N, voff = vst * kVTile;
+        float2 x[CH / 2];
+        // one PV round: the weights (of bf16 ones part 0 or 1) and V's tile
+        auto send = [&](auto wide, int part) {
+          const uint32_t b = round & 1;
+          done(round < 2 ? 0 : round - 1);  // the last round of this P (and V, if there are two) has ended
 #pragma unroll
           for (int c = 0; c < R; c += CH) {
-            load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+            if (!kHold) {
+              load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+              if (!whole) mask_logits<CH>(x, n0 + tok, lens_at + (half * R + c) * 4);
+            }
+            uint32_t pk[CH / 2];
 #pragma unroll
-            for (int i = 0; i < CH / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
-          }
-          const bool whole = n0 + kBlock <= w.min_len;
-          bool wide = false;
-          if (__builtin_expect(!all_of(!bad && whole && in && top <= kBias + kMaxGrow), 0)) {
-            // The uncommon way: the rows' maxima, where a row may not see the
-            // token, new references, and O and l in their terms; are V's scales
-            // outside f16's range?
-            skip = any_of(bad);  // (a block whose id is out of range)
-            wide = any_of(!in);
-            const int n = n0 + tok;
-            if (skip) wide = false;
-#pragma unroll 1
-            for (int c = 0; c < (skip ? 0 : R); c += CH) {
-              float y[CH];
-              tmem_ld<CH>(z + c, y);
-#pragma unroll
-              for (int i = 0; i < CH; ++i) {
-                const int row = half * R + c + i;
-                const float mx = warp_max(n < static_cast<int>(lds32(lens_at + row * 4)) ? y[i] * p.qk_scale : -INFINITY);
-                if (lane == 0) stsf(tops + (quad * N + row) * 4, mx);
+            for (int i = 0; i < CH / 2; ++i) {
+              const float2 e = make_float2(ex2_approx(x[i].x), ex2_approx(x[i].y));
+              if (!wide) {
+                l[c / 2 + i] = fadd2(l[c / 2 + i], e);
+                pk[i] = pack_f16x2(e.x, e.y);
+              } else {
+                pk[i] = pack_bf16x2(e.x, e.y);
+                if (part == 0)
+                  l[c / 2 + i] = fadd2(l[c / 2 + i], e);
+                else
+                  pk[i] = pack_bf16x2(e.x - bf16_bits_to_float(pk[i] & 0xFFFF), e.y - bf16_bits_to_float(pk[i] >> 16));
               }
             }
-            bar_sync(1, 32 * kCompute);
-            float f = 1.f;
-            if (tid < N && !skip) {
-              float mx = ldsf(tops + tid * 4);
 #pragma unroll
-              for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + tid) * 4));
-              const float old = ldsf(base + S::refs + (cur * N + tid) * 4);  // kBias - m
-              const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
-              f = ex2_approx(ref - old);
-              stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, ref);
-              stsf(fac + tid * 4, f);
-            }
-            if (!skip) cur ^= 1;
-            if (any_of(f != 1.f) && !first) {
-              done(round);
-              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (int i = 0; i < CH / 8; ++i)
+              sts128(p_at + b * S::kPBytes + (((half * R + c) / 8 + i) ^ swz) * 16, pk[4 * i], pk[4 * i + 1],
+                     pk[4 * i + 2], pk[4 * i + 3]);
+          }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();  // the logits are read, V's factors written
+          if ((!wide || part) && lane == 0) arrive(z_empty + 8 * zb);
+          if (T::kV == 1) done(round);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          put_v<wide, VT>(vt_at + (T::kV == 2 ? b * 64 : 0), ld_at + voff, my_words);
+          if (tid == 0) misc[5 + b] = (first ? 0 : kAccumulate) | (wide ? kBf16 : 0);
+          first = false;
+          fence_proxy_async();  // the tensor core reads P through the async proxy
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) arrive(pv_full + 8 * b);
+          ++round;
+        };
+        // V's factors
+        bool in = true;
 #pragma unroll
-              for (int c = 0; c < R; c += CH) {
-                float y[CH];
-                tmem_ld<CH>(o_at + c, y);
+        for (int i = 0; i < VT; i += 64)
+          in &= scale_words(cell_at + voff, n0 + vtok, max_len, word_at, base + S::v + voff, vtok, quad, i);
+        // first pass: does a row's maximum grow?
+        float top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                  const float g = ldsf(fac + (half * R + c + i) * 4);
-                  y[i] *= g;
-                  (i & 1 ? l[(c + i) >> 1].y : l[(c + i) >> 1].x) *= g;
-                }
-                tmem_st<CH>(o_at + c, y);
-              }
-            }
-            if (kHold) load_logits<CH>(x, z, base + S::refs + (cur * N + half * R) * 4, p.qk_scale);
-            if (kHold && !whole) mask_logits<CH>(x, n, lens_at + half * R * 4);
-            if (wide) {
-              mark_nan(s0, s1, w.max_len - vn, vn, word_at, lens, nan_of, N, quad);
+        for (int c = 0; c < R; c += CH) {
+          load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
+        }
+        bool wide = false;
+        if (__builtin_expect(!all_of<32 * kCompute>(!bad && whole && in && top <= kBias + kMaxGrow), 0)) {
+          // The uncommon way: the rows' maxima, where a row may not see the
+          // token, new references, and O and l in their terms; are V's scales
+          // outside f16's range?
+          skip = any_of<32 * kCompute>(bad);  // (a block whose id is out of range)
+          wide = any_of<32 * kCompute>(!in);
+          const int n = n0 + tok;
+          if (skip) wide = false;
+#pragma unroll 1
+          for (int c = 0; c < (skip ? 0 : R); c += CH) {
+            float y[CH];
+            tmem_ld<CH>(z + c, y);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const int row = half * R + c + i;
+              const float mx = warp_max(n < static_cast<int>(lds32(lens_at + row * 4)) ? y[i] * p.qk_scale : -INFINITY);
+              if (lane == 0) stsf(tops + (quad * N + row) * 4, mx);
             }
           }
-          // second pass: the weights, and V as the MMA reads it.  Where V's scales
-          // are beyond f16, both are bf16 and the weights go in two parts.
-#pragma unroll 1
-          for (int part = 0; part < (skip ? 0 : wide ? 2 : 1); ++part, ++round) {
-            const uint32_t b = round & 1;
-            done(round < 2 ? 0 : round - 1);  // the last round of this P (and V, if there are two) has ended
+          bar_sync(1, 32 * kCompute);
+          float f = 1.f;
+          if (tid < N && !skip) {
+            float mx = ldsf(tops + tid * 4);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + tid) * 4));
+            const float old = ldsf(base + S::refs + (cur * N + tid) * 4);  // kBias - m
+            const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
+            f = ex2_approx(ref - old);
+            stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, ref);
+            stsf(fac + tid * 4, f);
+          }
+          if (!skip) cur ^= 1;
+          if (any_of<32 * kCompute>(f != 1.f) && !first) {
+            done(round);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
             for (int c = 0; c < R; c += CH) {
-              if (!kHold) {
-                load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
-                if (!whole) mask_logits<CH>(x, n0 + tok, lens_at + (half * R + c) * 4);
-              }
-              uint32_t pk[CH / 2];
+              float y[CH];
+              tmem_ld<CH>(o_at + c, y);
 #pragma unroll
-              for (int i = 0; i < CH / 2; ++i) {
-                const float2 e = make_float2(ex2_approx(x[i].x), ex2_approx(x[i].y));
-                if (part == 0) l[c / 2 + i] = fadd2(l[c / 2 + i], e);
-                pk[i] = pack_f16x2(e.x, e.y);
-                if (__builtin_expect(wide, 0)) {
-                  pk[i] = pack_bf16x2(e.x, e.y);
-                  if (part)
-                    pk[i] = pack_bf16x2(e.x - bf16_bits_to_float(pk[i] & 0xFFFF), e.y - bf16_bits_to_float(pk[i] >> 16));
-                }
+              for (int i = 0; i < CH; ++i) {
+                const float g = ldsf(fac + (half * R + c + i) * 4);
+                y[i] *= g;
+                (i & 1 ? l[(c + i) >> 1].y : l[(c + i) >> 1].x) *= g;
               }
-#pragma unroll
-              for (int i = 0; i < CH / 8; ++i)
-                sts128(p_at + b * S::kPBytes + (((half * R + c) / 8 + i) ^ swz) * 16, pk[4 * i], pk[4 * i + 1],
-                       pk[4 * i + 2], pk[4 * i + 3]);
+              tmem_st<CH>(o_at + c, y);
             }
-            if (!wide || part) {  // the logits are read
-              asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) arrive(z_empty + 8 * zb);
-            }
-            if (T::kV == 1) done(round);
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            __syncwarp();  // the factors are written
-            const uint32_t vt = vt_at + (T::kV == 2 ? b * 64 : 0);
-            if (__builtin_expect(wide, 0))
-              put_v<true>(vt, ld_at + voff, my_words);
-            else
-              put_v<false>(vt, ld_at + voff, my_words);
-            if (tid == 0) misc[5 + b] = (first ? 0 : kAccumulate) | (wide ? kBf16 : 0);
-            first = false;
-            fence_proxy_async();  // the tensor core reads P through the async proxy
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) arrive(pv_full + 8 * b);
           }
+          if (kHold) load_logits<CH>(x, z, base + S::refs + (cur * N + half * R) * 4, p.qk_scale);
+          if (kHold && !whole) mask_logits<CH>(x, n, lens_at + half * R * 4);
+          if (wide)
+            for (int i = 0; i < VT; i += 64)
+              wide_words(cell_at + voff, n0 + vtok, max_len, word_at, quad, i, lens, nan_of, N);
+        }
+        // second pass: the weights, and V as the MMA reads it.  Where V's scales
+        // are beyond f16, both are bf16 and the weights go in two parts.
+        if (__builtin_expect(wide, 0)) {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) send(std::true_type{}, part);
+        } else if (!skip) {
+          send(std::false_type{}, 0);
         }
         if (__builtin_expect(skip, 0)) {
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1152,24 +1184,26 @@ bool make_map_side(CUtensorMap* m, bool unpack, const void* base, uint64_t heads
 // How a group's rows are cut into units of at most 64, and the rows the kernel is
 // built for.
 struct Plan {
-  int sub_tokens, subs, rows;
+  int sub_tokens, subs, rows, ctas_per_sm;
 };
 Plan plan_of(int group, int q_group) {
   const int sub = std::min(q_group, 64 / group), subs = (q_group + sub - 1) / sub;
   const int tokens = (q_group + subs - 1) / subs, rows = tokens * group;  // units of about the same size
-  return {tokens, subs, rows <= 16 ? 16 : rows <= 32 ? 32 : 64};
+  if (rows <= 16) return {tokens, subs, 16, Shape<16>::kCtasPerSm};
+  if (rows <= 32) return {tokens, subs, 32, Shape<32>::kCtasPerSm};
+  return {tokens, subs, 64, Shape<64>::kCtasPerSm};
 }
 
 template <int N, bool Q16>
 cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, cudaStream_t s) {
   using S = Smem<N, Q16>;
-  static_assert((S::total + 1024) * kCtasPerSm <= 228 * 1024);
+  static_assert((S::total + 1024) * Shape<N>::kCtasPerSm <= 228 * 1024);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = once_per_device(done, [] {  // the shared-memory opt-in
     return cudaFuncSetAttribute(dense_pa_kernel<N, Q16>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
   });
   if (e != cudaSuccess) return e;
-  return launch_kernel(dense_pa_kernel<N, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), S::total, s, 0, mk,
+  return launch_kernel(dense_pa_kernel<N, Q16>, dim3(static_cast<unsigned>(p.ctas)), dim3(Shape<N>::kThreads), S::total, s, 0, mk,
                        mv, p);
 }
 
@@ -1177,8 +1211,9 @@ cudaError_t launch_main(const CUtensorMap& mk, const CUtensorMap& mv, const Para
 
 size_t dense_pa_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms) {
   (void)num_rows, (void)hkv;
-  const int64_t ctas = static_cast<int64_t>(kCtasPerSm) * num_sms;
-  return list_bytes(ctas) + 2 * ctas * plan_of(group, q_group).rows * (kDim + 2) * sizeof(float);
+  const Plan pl = plan_of(group, q_group);
+  const int64_t ctas = static_cast<int64_t>(pl.ctas_per_sm) * num_sms;
+  return list_bytes(ctas) + 2 * ctas * pl.rows * (kDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s, int* launches) {
@@ -1197,7 +1232,7 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   if (units > INT32_MAX) return cudaErrorNotSupported;
   p.units = static_cast<int32_t>(units);
   p.shares = static_cast<int32_t>(
-      std::min<int64_t>(static_cast<int64_t>(kCtasPerSm) * num_sms / pl.subs, pairs * a.bt_stride));
+      std::min<int64_t>(static_cast<int64_t>(pl.ctas_per_sm) * num_sms / pl.subs, pairs * a.bt_stride));
   p.ctas = p.shares * pl.subs;
   p.by_unit = units <= p.ctas;
   CUtensorMap mk, mv;
