@@ -87,10 +87,10 @@ struct Params {
 
 // ---- shared memory -----------------------------------------------------------
 // Units of 16 rows: four compute warps a CTA, three CTAs an SM; of more: eight, two.
-// Then the producer and the warp that issues PV.
+// Then the producer.
 template <int N>
 struct Shape {
-  static constexpr int kCompute = N == 16 ? 4 : 8, kThreads = 32 * (kCompute + 2), kCtasPerSm = N == 16 ? 3 : 2;
+  static constexpr int kCompute = N == 16 ? 4 : 8, kThreads = 32 * (kCompute + 1), kCtasPerSm = N == 16 ? 3 : 2;
   static constexpr int kHalves = kCompute / 4;          // warps that share 32 TMEM lanes
   static constexpr int kRows = N / kHalves;             // a compute warp's
   static constexpr int kTokens = kBlock / kHalves;      // of V
@@ -151,6 +151,12 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[C]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < C; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  return __uint_as_float(r);
 }
 template <int C>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[C]) {
@@ -305,11 +311,22 @@ __device__ __forceinline__ float scale_pow2(float x, int e) {
   const int a = max(-126, min(127, e)), b = max(-126, min(127, e - a));
   return x * __uint_as_float(static_cast<uint32_t>(a + 127) << 23) * __uint_as_float(static_cast<uint32_t>(b + 127) << 23);
 }
-// largest of the warp's values
-__device__ __forceinline__ float warp_max(float x) {
-  const int b = __float_as_int(x), k = b ^ ((b >> 31) & 0x7FFFFFFF);  // ordered as integers
-  const int m = __reduce_max_sync(0xffffffffu, k);
-  return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
+// R values of each lane reduced over the warp, all of them at once: each step hands
+// half of the values to the lane that differs in one bit.  Lane i ends with value
+// i * R / 32 (of R = 16, lanes 2j and 2j + 1 both with value j).
+template <int R, typename OP>
+__device__ __forceinline__ float warp_reduce(float (&x)[R], int lane, OP op) {
+  static_assert(R == 16 || R == 32);
+#pragma unroll
+  for (int h = R / 2, d = 16; h >= 1; h >>= 1, d >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float mine = up ? x[i + h] : x[i], theirs = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + h], d);
+      x[i] = op(mine, theirs);
+    }
+  }
+  return R == 32 ? x[0] : op(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
 }
 
 // ---- units ---------------------------------------------------------------------
@@ -322,6 +339,7 @@ __device__ __forceinline__ int group_len(const DensePaParams& a, int g, int firs
   const int64_t tok0 = static_cast<int64_t>(g) * a.q_group;
   const int n = static_cast<int>(min(static_cast<int64_t>(a.q_group), a.num_rows / a.hkv - tok0)) * a.hkv;
   int len = 0;
+#pragma unroll 1
   for (int i = first; i < n; i += step) len = max(len, a.row_len[tok0 * a.hkv + i]);
   return len;
 }
@@ -523,20 +541,16 @@ __device__ __forceinline__ void put_v(uint32_t vt, uint32_t ld_at, uint32_t word
 }
 
 // ---- the main kernel -----------------------------------------------------------
+// barriers, by their byte offset in shared memory
 template <int N, bool Q16>
 struct Bars {
   static constexpr int NK = Smem<N, Q16>::kKStages, NV = Smem<N, Q16>::kVStages;
-  static_assert(2 * NK + 2 * NV + 9 <= 24);
-  uint64_t* b;
-  __device__ uint64_t* k_full(int i) const { return b + i; }
-  __device__ uint64_t* k_empty(int i) const { return b + NK + i; }
-  __device__ uint64_t* v_full(int i) const { return b + 2 * NK + i; }
-  __device__ uint64_t* v_empty(int i) const { return b + 2 * NK + NV + i; }
-  __device__ uint64_t* z_full(int i) const { return b + 2 * NK + 2 * NV + i; }
-  __device__ uint64_t* z_empty(int i) const { return b + 2 * NK + 2 * NV + 2 + i; }
-  __device__ uint64_t* pv_full(int i) const { return b + 2 * NK + 2 * NV + 4 + i; }  // P and V's tile are written
-  __device__ uint64_t* pv_done(int i) const { return b + 2 * NK + 2 * NV + 6 + i; }  // and multiplied
-  __device__ uint64_t* q_full() const { return b + 2 * NK + 2 * NV + 8; }
+  static constexpr int k_full = Smem<N, Q16>::bars, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK,
+                       v_empty = v_full + 8 * NV, z_full = v_empty + 8 * NV, z_empty = z_full + 16,
+                       pv_full = z_empty + 16,  // P and V's tile are written
+      pv_done = pv_full + 16,                   // and multiplied
+      q_full = pv_done + 16;
+  static_assert(q_full + 8 <= Smem<N, Q16>::misc);
 };
 
 // TMEM columns: V's tiles (64 columns of token pairs), O, the logits, the scale
@@ -548,8 +562,8 @@ struct Tmem {
   static constexpr int kColumns = N == 16 ? 128 : 256;
   static_assert(q + 8 <= kColumns && kColumns * Shape<N>::kCtasPerSm <= 512);
 };
-// commands to the warp that issues PV
-constexpr uint32_t kAccumulate = 1, kBf16 = 2, kStop = 4;
+// what a PV round is
+constexpr uint32_t kAccumulate = 1, kBf16 = 2, kMore = 4, kNothing = 8;
 
 template <int N, bool Q16>
 __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
@@ -565,15 +579,17 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
   const DensePaParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Bars<N, Q16> bars{reinterpret_cast<uint64_t*>(smem + S::bars)};
+  using B = Bars<N, Q16>;
+  const uint32_t base = smem_u32(smem);
   if (tid == 0) {
-    for (int i = 0; i < S::kKStages; ++i) mbar_init(bars.k_full(i), 1), mbar_init(bars.k_empty(i), 1);
-    for (int i = 0; i < S::kVStages; ++i) mbar_init(bars.v_full(i), 1), mbar_init(bars.v_empty(i), kCompute);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars.z_full(i), 1), mbar_init(bars.z_empty(i), kCompute);
-      mbar_init(bars.pv_full(i), kCompute), mbar_init(bars.pv_done(i), 1);
-    }
-    mbar_init(bars.q_full(), 4);
+    auto init = [&](int at, int n, uint32_t count) {
+      for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + at) + i, count);
+    };
+    init(B::k_full, S::kKStages, 1), init(B::k_empty, S::kKStages, 1);
+    init(B::v_full, S::kVStages, 1), init(B::v_empty, S::kVStages, kCompute);
+    init(B::z_full, 2, 1), init(B::z_empty, 2, kCompute);
+    init(B::pv_full, 2, kCompute), init(B::pv_done, 2, 1);
+    init(B::q_full, 1, 4);
     mbar_fence_init();
   }
   pdl_wait();
@@ -582,7 +598,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
   // keep the kernel before it from getting its own
   if (warp == kCompute) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(const_cast<const uint32_t*>(misc + 4))),
+                     base + S::misc + 16),
                  "n"(T::kColumns));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -591,8 +607,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
   // group the share starts in
   const int sub = blockIdx.x % p.subs, turn = blockIdx.x / p.subs;
   int64_t total = 0, at = 0, share = 0;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    int64_t base = 0;
+    int64_t sum = 0;
+#pragma unroll 1
     for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
       const int g = g0 + tid;
       const int nb = g < p.groups ? blocks_of(a, group_len(a, g, 0, 1)) : 0;
@@ -605,23 +623,24 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       __syncthreads();
       if (lane == 31) s_sum[warp] = x;
       __syncthreads();
-      int64_t before = base;
+      int64_t before = sum;
+#pragma unroll 1
       for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += s_sum[w];
-        base += s_sum[w];
+        sum += s_sum[w];
       }
       const int64_t c1 = before + x, c0 = c1 - nb;  // blocks before and up to group g
       if (pass == 0 && p.groups <= kThreads) {  // one tile: the sum and the start at once
-        total = base;
+        total = sum;
         share = (total * a.hkv + p.shares - 1) / p.shares;
         at = turn * share;
       }
       if ((pass == 1 || p.groups <= kThreads) && nb && c0 * a.hkv <= at && at < c1 * a.hkv)
         s_start[0] = g, s_start[1] = c0, s_start[2] = nb;
-      if (pass == 1 && base * a.hkv > at) break;
+      if (pass == 1 && sum * a.hkv > at) break;
     }
     if (pass == 0) {
-      total = base;
+      total = sum;
       share = (total * a.hkv + p.shares - 1) / p.shares;
       at = turn * share;
       if (p.groups <= kThreads) break;
@@ -651,10 +670,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     // most of the time: what counts here is few instructions.)
     constexpr int kAheadV = S::kVStages - 2, kAhead = S::kKStages;
     static_assert(kAheadV <= kAhead);
-    const uint32_t base = smem_u32(smem), k_full = smem_u32(bars.k_full(0)), k_empty = smem_u32(bars.k_empty(0));
-    const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0)), q_full = smem_u32(bars.q_full());
-    const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
-    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc));
+    const uint32_t k_full = base + B::k_full, k_empty = base + B::k_empty, v_full = base + B::v_full;
+    const uint32_t v_empty = base + B::v_empty, z_full = base + B::z_full, z_empty = base + B::z_empty;
+    const uint32_t q_full = base + B::q_full, bad_at = base + S::misc;
     const uint64_t k_desc = smem_desc_sw128(base), q_desc = smem_desc_sw128(base + S::q);
     const int limit = static_cast<int>(min(a.num_blocks, int64_t{0x7FFFFFFF}));
     // scales of tokens 32j + lane in K's unpacked rows 128..: 16 tokens a row, two an
@@ -724,10 +742,47 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         if (i < kAheadV) load_v(q_id[i], q_head[i]);
       }
     }
-    uint32_t last = 0, last_phase = 0;  // the last MMAs' barrier
+    // O += V^T P of the next block, in a round, or in two (kMore)
+    uint64_t p_desc = ((base + S::p) & 0x3FFFF) >> 4;
+    // P: rows of 2N bytes, one atom of the 2N-byte swizzle wide, 8 tokens an atom
+    p_desc |= static_cast<uint64_t>(1) << 16;                                // leading offset: unused
+    p_desc |= static_cast<uint64_t>(8 * 2 * N >> 4) << 32;                   // 8 tokens
+    p_desc |= static_cast<uint64_t>(1) << 46;                                // descriptor version
+    p_desc |= static_cast<uint64_t>(N == 16 ? 6 : N == 32 ? 4 : 2) << 61;    // 32-, 64-, 128-byte swizzle
+    uint32_t round = 0;
+    auto multiply = [&]() {
+      uint32_t cmd = kMore;
+      while (cmd & kMore) {
+        const uint32_t b = round & 1;
+        if (alive) alive = wait_for(base + B::pv_full + 8 * b, (round >> 1) & 1, a.err);
+        cmd = alive ? misc[5 + b] : +kNothing;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        // f32 += A (f16 or bf16, TMEM) B (the same, rows contiguous), M = 128
+        const uint32_t id = (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24) |
+                            (cmd & kBf16 ? (1u << 7) | (1u << 10) : 0);
+        const uint32_t v = tmem + T::v + (T::kV == 2 ? b * 64 : 0);
+        if (!(cmd & kNothing)) {
+#pragma unroll
+          for (int k = 0; k < kBlock / 16; ++k)
+            umma_ts(tmem + T::o, v + 8 * k, p_desc + (b * S::kPBytes + k * 16 * 2 * N) / 16, id,
+                    k > 0 || (cmd & kAccumulate));
+        }
+        commit(base + B::pv_done + 8 * b);
+        ++round;
+      }
+    };
+    int behind = 0;  // blocks whose logits are under way and whose PV is not
 #pragma unroll 1
     while (q_id[0] != kNone) {
       learn(q_id[kAhead], q_head[kAhead]);
+      // PV of the block before the last; of all of them before another piece's q,
+      // which comes once the piece's O has been read
+      while (behind > (q_head[0] < 0 ? 0 : 1)) {
+        if (lane == 0) multiply();
+        --behind;
+      }
+      ++behind;
+      __syncwarp();
       // K is there: its scales from token order to the cells tcgen05.cp reads,
       // lane i of column j = token 32j + i
       if (alive) alive = wait_for(k_full + 8 * mst, m_phase, a.err);
@@ -759,44 +814,16 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);  // once the compute warps have left its stage
         if (q_id[kAhead] != kNone) load_k(q_id[kAhead], q_head[kAhead]);     // once the MMAs that used it are done
       }
-      last = k_empty + 8 * mst, last_phase = m_phase;
       if (++mst == S::kKStages) mst = 0, m_phase ^= 1;
       if (++buf == T::kZ) buf = 0, z_phase ^= 1;
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) q_id[j] = q_id[j + 1], q_head[j] = q_head[j + 1];
       __syncwarp();
     }
-    // nothing may still write shared memory or TMEM when the CTA leaves
-    if (lane == 0 && alive && last) wait_for(last, last_phase, a.err);
-    __syncwarp();
-  } else if (warp == kCompute + 1) {
-    // ---- O += V^T P, a round at a time, as the compute warps ask for it ----
-    const uint32_t pv_full = smem_u32(bars.pv_full(0)), pv_done = smem_u32(bars.pv_done(0));
-    // P: rows of 2N bytes, one atom of the 2N-byte swizzle wide, 8 tokens an atom
-    uint64_t desc = (smem_u32(smem + S::p) & 0x3FFFF) >> 4;
-    desc |= static_cast<uint64_t>(1) << 16;                  // leading offset: unused
-    desc |= static_cast<uint64_t>(8 * 2 * N >> 4) << 32;     // 8 tokens
-    desc |= static_cast<uint64_t>(1) << 46;                  // descriptor version
-    desc |= static_cast<uint64_t>(N == 16 ? 6 : N == 32 ? 4 : 2) << 61;  // 32-, 64-, 128-byte swizzle
-    constexpr uint32_t idesc = (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);  // B: rows contiguous
     if (lane == 0) {
-      uint32_t r = 0;
-#pragma unroll 1
-      for (; alive; ++r) {
-        const uint32_t b = r & 1;
-        alive = wait_for(pv_full + 8 * b, (r >> 1) & 1, a.err);
-        const uint32_t cmd = misc[5 + b];
-        if (!alive || (cmd & kStop)) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t id = idesc | (cmd & kBf16 ? (1u << 7) | (1u << 10) : 0);
-        const uint32_t v = tmem + T::v + (T::kV == 2 ? b * 64 : 0);
-#pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)
-          umma_ts(tmem + T::o, v + 8 * k, desc + (b * S::kPBytes + k * 16 * 2 * N) / 16, id, k > 0 || (cmd & kAccumulate));
-        commit(pv_done + 8 * b);
-      }
-      // the last round has ended when the CTA leaves
-      if (alive && r) wait_for(pv_done + 8 * ((r - 1) & 1), ((r - 1) >> 1) & 1, a.err);
+      while (behind-- > 0) multiply();
+      // nothing may still write shared memory or TMEM when the CTA leaves
+      if (alive && round) wait_for(base + B::pv_done + 8 * ((round - 1) & 1), ((round - 1) >> 1) & 1, a.err);
     }
     __syncwarp();
   } else {
@@ -807,17 +834,15 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     constexpr int R = Shape<N>::kRows, CH = 16, VT = Shape<N>::kTokens;  // rows of a warp, and of them at a time
     constexpr bool kHold = R == CH;                 // the logits stay in registers between the two passes
     const int quad = warp & 3, half = warp >> 2;
-    const uint32_t base = smem_u32(smem);
     const uint32_t tops = base + S::tops, lens_at = base + S::len, fac = base + S::fac;
     int* lens = reinterpret_cast<int*>(smem + S::len);
     uint32_t* nan_of = reinterpret_cast<uint32_t*>(smem + S::nan);
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t z_at = tmem + lane_base + T::z + half * R, o_at = tmem + lane_base + T::o + half * R;
     const uint32_t vt_at = tmem + lane_base + T::v + half * (VT / 2);
-    const uint32_t z_full = smem_u32(bars.z_full(0)), z_empty = smem_u32(bars.z_empty(0));
-    const uint32_t v_full = smem_u32(bars.v_full(0)), v_empty = smem_u32(bars.v_empty(0));
-    const uint32_t pv_full = smem_u32(bars.pv_full(0)), pv_done = smem_u32(bars.pv_done(0));
-    const uint32_t bad_at = smem_u32(const_cast<const uint32_t*>(misc));
+    const uint32_t z_full = base + B::z_full, z_empty = base + B::z_empty, v_full = base + B::v_full;
+    const uint32_t v_empty = base + B::v_empty, pv_full = base + B::pv_full, pv_done = base + B::pv_done;
+    const uint32_t bad_at = base + S::misc;
     // scales of V: the lane's tokens vtok, vtok + 1 (and 64 further on); their cells,
     // in row 64 + token / 32
     const int vtok = VT * half + 2 * lane;
@@ -867,7 +892,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.q_full());
+        if (lane == 0) arrive(base + B::q_full);
       }
       bool first = true;  // no PV round of the unit yet
       const int max_len = w.max_len, min_len = w.min_len;
@@ -918,7 +943,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           if (T::kV == 1) done(round);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           put_v<wide, VT>(vt_at + (T::kV == 2 ? b * 64 : 0), ld_at + voff, my_words);
-          if (tid == 0) misc[5 + b] = (first ? 0 : kAccumulate) | (wide ? kBf16 : 0);
+          if (tid == 0) misc[5 + b] = (first ? 0 : kAccumulate) | (wide ? kBf16 | (part ? 0 : kMore) : 0);
           first = false;
           fence_proxy_async();  // the tensor core reads P through the async proxy
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -954,11 +979,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
             float y[CH];
             tmem_ld<CH>(z + c, y);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const int row = half * R + c + i;
-              const float mx = warp_max(n < static_cast<int>(lds32(lens_at + row * 4)) ? y[i] * p.qk_scale : -INFINITY);
-              if (lane == 0) stsf(tops + (quad * N + row) * 4, mx);
-            }
+            for (int i = 0; i < CH; ++i)
+              y[i] = n < static_cast<int>(lds32(lens_at + (half * R + c + i) * 4)) ? y[i] * p.qk_scale : -INFINITY;
+            const float mx = warp_reduce<CH>(y, lane, [](float u, float v) { return fmaxf(u, v); });
+            if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, mx);
           }
           bar_sync(1, 32 * kCompute);
           float f = 1.f;
@@ -1004,9 +1028,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           send(std::false_type{}, 0);
         }
         if (__builtin_expect(skip, 0)) {
+          done(round < 2 ? 0 : round - 1);
+          if (tid == 0) misc[5 + (round & 1)] = kNothing;
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          if (lane == 0) arrive(z_empty + 8 * zb);
+          if (lane == 0) arrive(z_empty + 8 * zb), arrive(pv_full + 8 * (round & 1));
+          ++round;
         }
         __syncwarp();
         if (lane == 0) arrive(v_empty + 8 * vst);
@@ -1016,11 +1043,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 
       // -- the unit's sums, and O to where it goes
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float y = i & 1 ? l[i >> 1].y : l[i >> 1].x;
+      for (int c = 0; c < R; c += CH) {
+        float y[CH];
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
-        if (lane == 0) stsf(tops + (quad * N + half * R + i) * 4, y);
+        for (int i = 0; i < CH; ++i) y[i] = i & 1 ? l[(c + i) >> 1].y : l[(c + i) >> 1].x;
+        const float sum = warp_reduce<CH>(y, lane, [](float u, float v) { return u + v; });
+        if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, sum);
       }
       bar_sync(1, 32 * kCompute);
       if (!first) done(round);
@@ -1030,36 +1058,32 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       // that goes on after it
       float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
                   (2LL * blockIdx.x + (w.starts ? 1 : 0)) * N * (kDim + 2);
-      const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
       const int d = 32 * quad + 4 * (lane & 7) + (lane >> 3);  // the lane's dim (see put_v)
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                           (static_cast<int64_t>(w.tok0) * a.hkv + w.h) * a.group * kDim + d;
+      const int rows = w.tokens * a.group;
+      const int64_t skip_rows = static_cast<int64_t>(a.hkv - 1) * a.group * kDim;  // from a token's rows to the next's
+      int in_token = (half * R) % a.group;
+      out += (half * R) / a.group * skip_rows + half * R * kDim;
 #pragma unroll 1
-      for (int c = 0; c < R; c += CH) {
-        float y[CH];
-        if (!first) {
-          tmem_ld<CH>(o_at + c, y);
+      for (int i = 0; i < R; ++i) {
+        const int r = half * R + i;
+        if (r >= rows) break;
+        float o = 0.f;
+        if (!first) o = tmem_ld1(o_at + i);
+        const float sum = (ldsf(tops + r * 4) + ldsf(tops + (N + r) * 4)) +
+                          (ldsf(tops + (2 * N + r) * 4) + ldsf(tops + (3 * N + r) * 4));
+        o *= static_cast<float>(1 << (kVRef - 127));
+        if (nan_of[r] >> quad & 1) o = __uint_as_float(0x7FC00000u);
+        if (all) {
+          *out = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+          out += kDim;
+          if (++in_token == a.group) in_token = 0, out += skip_rows;
         } else {
-#pragma unroll
-          for (int i = 0; i < CH; ++i) y[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int r = half * R + c + i;
-          if (r >= w.tokens * a.group) break;
-          float sum = ldsf(tops + r * 4);
-#pragma unroll
-          for (int j = 1; j < 4; ++j) sum += ldsf(tops + (j * N + r) * 4);
-          float o = y[i] * static_cast<float>(1 << (kVRef - 127));
-          if (nan_of[r] >> quad & 1) o = __uint_as_float(0x7FC00000u);
-          if (all) {
-            const int64_t row = (w.tok0 + r / a.group) * hq + static_cast<int64_t>(w.h) * a.group + r % a.group;
-            o *= sum == 0.f ? 0.f : 1.f / sum;
-            static_cast<__nv_bfloat16*>(a.out)[row * kDim + d] = __float2bfloat16_rn(o);
-          } else {
-            po[r * kDim + d] = o;
-            if (quad == 0 && lane == 0)
-              *reinterpret_cast<float2*>(po + N * kDim + 2 * r) =
-                  make_float2(kBias - ldsf(base + S::refs + (cur * N + r) * 4), sum);
-          }
+          po[r * kDim + d] = o;
+          if (quad == 0 && lane == 0)
+            *reinterpret_cast<float2*>(po + N * kDim + 2 * r) =
+                make_float2(kBias - ldsf(base + S::refs + (cur * N + r) * 4), sum);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1073,9 +1097,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           cut[blockIdx.x] = make_int2(w.unit, pieces);
       }
     }
-    if (tid == 0) misc[5 + (round & 1)] = kStop;
-    __syncwarp();
-    if (lane == 0) arrive(pv_full + 8 * (round & 1));
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
