@@ -118,11 +118,15 @@ struct Smem {
 };
 
 // ---- device helpers ------------------------------------------------------------
+// The producer warp runs converged and one lane of it, always the same, issues:
+// with a branch around each issue the descriptors would be vector registers,
+// moved to uniform ones one by one (765 clocks for the eight MMAs of a block).
+#define BSP_ELECT "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
 __device__ __forceinline__ void tile_g2s(uint32_t dst, const CUtensorMap* m, int head, int block, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], "
-      "[%5];" ::"r"(dst),
-      "l"(m), "r"(0), "r"(head), "r"(block), "r"(bar)
+      BSP_ELECT " @e cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
+                "[%1, {%2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
+      "l"(m), "r"(0), "r"(0), "r"(head), "r"(block), "r"(bar)
       : "memory");
 }
 // 512 bytes (32 rows of 16) to four TMEM columns of every 32-lane sub-partition
@@ -131,7 +135,7 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
   d |= static_cast<uint64_t>(128 >> 4) << 16;     // leading byte offset (one core matrix wide: unused)
   d |= static_cast<uint64_t>(128 >> 4) << 32;     // 8-row core matrices 128 bytes apart
   d |= static_cast<uint64_t>(1) << 46;            // descriptor version; no swizzle
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  asm volatile(BSP_ELECT " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(taddr), "l"(d) : "memory");
 }
 // C fp32 columns of the warp's 32 TMEM lanes, and back
 template <int C>
@@ -177,9 +181,18 @@ __device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&
 // D (+)= A B: A [128][16] in TMEM (two 16-bit values a column), B in shared memory
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      BSP_ELECT " .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// D (+)= (A * 2^(sa - 127)) (B * 2^(sb - 127)), both in shared memory (see umma_mx)
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        uint32_t accumulate) {
+  asm volatile(
+      BSP_ELECT " .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+                " @e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], "
+                "p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate));
 }
 __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -222,10 +235,13 @@ __device__ __forceinline__ bool any_of(bool x) {
 }
 // mbarriers and copies by shared address
 __device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile(BSP_ELECT " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar), "r"(bytes)
+               : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(BSP_ELECT
+               " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -258,6 +274,11 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t* err) {
   if (__builtin_expect(test_wait(bar, parity), 1)) return true;
   return wait_slow(bar, parity, err);
+}
+// the same for a converged warp, with one answer for all of its lanes
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* err) {
+  if (__builtin_expect(__all_sync(0xffffffffu, test_wait(bar, parity)), 1)) return true;
+  return __all_sync(0xffffffffu, wait_slow(bar, parity, err));
 }
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   uint64_t x, y, z, r;
@@ -662,8 +683,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 
   if (warp == kCompute) {
     // ---- producer ----
-    // Lane 0 issues; the warp walks the share and reads the block table, 32
-    // entries at a time.  K is loaded kAhead blocks ahead of the MMAs, V kAheadV: a
+    // It walks the share, reads the block table, 32 entries at a time, loads, and
+    // issues all MMAs.  K is loaded kAhead blocks ahead of the MMAs, V kAheadV: a
     // block less than its stages would hold, so that waiting for a stage does not
     // hold up the next MMAs.
     // (One warp does all of it, and its code is out of the instruction cache
@@ -719,16 +740,16 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       ++at_id, --left;
     };
     auto load_v = [&](int id, int hd) {
-      if (alive) alive = wait_for(v_empty + 8 * vst, v_phase, a.err);
+      if (alive) alive = wait_warp(v_empty + 8 * vst, v_phase, a.err);
       const uint32_t bar = v_full + 8 * vst;
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(bad_at + 4 * vst), "r"(static_cast<uint32_t>(id == limit)) : "memory");
-      fence_proxy_async();
+      __syncwarp();
       arrive_expect(bar, kMxField);
       tile_g2s(base + S::v + vst * kVTile, &map_v, hd ^ (hd >> 31), id, bar);
       if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
     };
     auto load_k = [&](int id, int hd) {
-      if (alive) alive = wait_for(k_empty + 8 * kst, k_phase, a.err);
+      if (alive) alive = wait_warp(k_empty + 8 * kst, k_phase, a.err);
       const uint32_t bar = k_full + 8 * kst;
       arrive_expect(bar, kMxField);
       tile_g2s(base + kst * kKTile, &map_k, hd ^ (hd >> 31), id, bar);
@@ -737,7 +758,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       learn(q_id[i], q_head[i]);
-      if (lane == 0 && q_id[i] != kNone) {
+      if (q_id[i] != kNone) {
         load_k(q_id[i], q_head[i]);
         if (i < kAheadV) load_v(q_id[i], q_head[i]);
       }
@@ -754,7 +775,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       uint32_t cmd = kMore;
       while (cmd & kMore) {
         const uint32_t b = round & 1;
-        if (alive) alive = wait_for(base + B::pv_full + 8 * b, (round >> 1) & 1, a.err);
+        if (alive) alive = wait_warp(base + B::pv_full + 8 * b, (round >> 1) & 1, a.err);
         cmd = alive ? misc[5 + b] : +kNothing;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         // f32 += A (f16 or bf16, TMEM) B (the same, rows contiguous), M = 128
@@ -778,53 +799,48 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       // PV of the block before the last; of all of them before another piece's q,
       // which comes once the piece's O has been read
       while (behind > (q_head[0] < 0 ? 0 : 1)) {
-        if (lane == 0) multiply();
+        multiply();
         --behind;
       }
       ++behind;
-      __syncwarp();
       // K is there: its scales from token order to the cells tcgen05.cp reads,
       // lane i of column j = token 32j + i
-      if (alive) alive = wait_for(k_full + 8 * mst, m_phase, a.err);
+      if (alive) alive = wait_warp(k_full + 8 * mst, m_phase, a.err);
       const uint32_t off = mst * kKTile, cells = base + off + kBlock * 128;  // (in their own rows)
       const uint32_t cell[4] = {lds32(from[0] + off), lds32(from[1] + off), lds32(from[2] + off), lds32(from[3] + off)};
       __syncwarp();
       sts128(cells + lane * 16, cell[0], cell[1], cell[2], cell[3]);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) {
-        if (__builtin_expect(q_head[0] < 0, 0)) {
-          if (alive) alive = wait_for(q_full, q_phase, a.err);
-          q_phase ^= 1;
-        }
-        if (alive) alive = wait_for(z_empty + 8 * buf, z_phase, a.err);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t sk = tmem + T::k + 4 * mst, z = tmem + T::z + buf * N;
-        const uint64_t kd = k_desc + mst * (kKTile / 16);
-        scales_to_tmem(sk, cells);
-#pragma unroll
-        for (int part = 0; part < (Q16 ? 2 : 1); ++part)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            umma_mx(z, kd + 2 * c, q_desc + (part * N * 128 + 32 * c) / 16,
-                    idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, N, 128, c, c), sk, tmem + T::q + 4 * part,
-                    part > 0 || c > 0);
-        commit(k_empty + 8 * mst);
-        commit(z_full + 8 * buf);
-        if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);  // once the compute warps have left its stage
-        if (q_id[kAhead] != kNone) load_k(q_id[kAhead], q_head[kAhead]);     // once the MMAs that used it are done
+      if (__builtin_expect(q_head[0] < 0, 0)) {
+        if (alive) alive = wait_warp(q_full, q_phase, a.err);
+        q_phase ^= 1;
       }
+      if (alive) alive = wait_warp(z_empty + 8 * buf, z_phase, a.err);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t sk = tmem + T::k + 4 * mst, z = tmem + T::z + buf * N;
+      const uint64_t kd = k_desc + mst * (kKTile / 16);
+      scales_to_tmem(sk, cells);
+#pragma unroll
+      for (int part = 0; part < (Q16 ? 2 : 1); ++part)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          umma_ss(z, kd + 2 * c, q_desc + (part * N * 128 + 32 * c) / 16,
+                  idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, N, 128, c, c), sk, tmem + T::q + 4 * part,
+                  part > 0 || c > 0);
+      commit(k_empty + 8 * mst);
+      commit(z_full + 8 * buf);
+      if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);  // once the compute warps have left its stage
+      if (q_id[kAhead] != kNone) load_k(q_id[kAhead], q_head[kAhead]);     // once the MMAs that used it are done
       if (++mst == S::kKStages) mst = 0, m_phase ^= 1;
       if (++buf == T::kZ) buf = 0, z_phase ^= 1;
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) q_id[j] = q_id[j + 1], q_head[j] = q_head[j + 1];
       __syncwarp();
     }
-    if (lane == 0) {
-      while (behind-- > 0) multiply();
-      // nothing may still write shared memory or TMEM when the CTA leaves
-      if (alive && round) wait_for(base + B::pv_done + 8 * ((round - 1) & 1), ((round - 1) >> 1) & 1, a.err);
-    }
+    while (behind-- > 0) multiply();
+    // nothing may still write shared memory or TMEM when the CTA leaves
+    if (alive && round) wait_warp(base + B::pv_done + 8 * ((round - 1) & 1), ((round - 1) >> 1) & 1, a.err);
     __syncwarp();
   } else {
     // ---- compute ----
