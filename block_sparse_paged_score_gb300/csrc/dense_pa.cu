@@ -567,7 +567,8 @@ template <int N, bool Q16>
 struct Bars {
   static constexpr int NK = Smem<N, Q16>::kKStages, NV = Smem<N, Q16>::kVStages;
   static constexpr int k_full = Smem<N, Q16>::bars, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK,
-                       v_empty = v_full + 8 * NV, z_full = v_empty + 8 * NV, z_empty = z_full + 16,
+                       v_empty = v_full + 8 * NV,  // v_full: V is loaded, and the block's logits are there
+                       z_empty = v_empty + 8 * NV,
                        pv_full = z_empty + 16,  // P and V's tile are written
       pv_done = pv_full + 16,                   // and multiplied
       q_full = pv_done + 16;
@@ -607,8 +608,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + at) + i, count);
     };
     init(B::k_full, S::kKStages, 1), init(B::k_empty, S::kKStages, 1);
-    init(B::v_full, S::kVStages, 1), init(B::v_empty, S::kVStages, kCompute);
-    init(B::z_full, 2, 1), init(B::z_empty, 2, kCompute);
+    init(B::v_full, S::kVStages, 2), init(B::v_empty, S::kVStages, kCompute);
+    init(B::z_empty, 2, kCompute);
     init(B::pv_full, 2, kCompute), init(B::pv_done, 2, 1);
     init(B::q_full, 1, 4);
     mbar_fence_init();
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     constexpr int kAheadV = S::kVStages - 2, kAhead = S::kKStages;
     static_assert(kAheadV <= kAhead);
     const uint32_t k_full = base + B::k_full, k_empty = base + B::k_empty, v_full = base + B::v_full;
-    const uint32_t v_empty = base + B::v_empty, z_full = base + B::z_full, z_empty = base + B::z_empty;
+    const uint32_t v_empty = base + B::v_empty, z_empty = base + B::z_empty;
     const uint32_t q_full = base + B::q_full, bad_at = base + S::misc;
     const uint64_t k_desc = smem_desc_sw128(base), q_desc = smem_desc_sw128(base + S::q);
     const int limit = static_cast<int>(min(a.num_blocks, int64_t{0x7FFFFFFF}));
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     int q_id[kAhead + 1], q_head[kAhead + 1];
     uint32_t vst = 0, v_phase = 1;  // of the next V load (an empty stage's wait passes at once)
     uint32_t kst = 0, k_phase = 1;  // of the next K load
-    uint32_t mst = 0, m_phase = 0, z_phase = 1, q_phase = 0, buf = 0;  // of the next MMAs
+    uint32_t mst = 0, m_phase = 0, z_phase = 1, q_phase = 0, buf = 0, sst = 0;  // of the next MMAs
     auto learn = [&](int& id, int& hd) {  // the next block of the share
       hd = head;
       if (__builtin_expect(left == 0, 0)) {
@@ -829,7 +830,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
                   idesc_mxf8f6f4(kFmtE2m1, kFmtE4m3, N, 128, c, c), sk, tmem + T::q + 4 * part,
                   part > 0 || c > 0);
       commit(k_empty + 8 * mst);
-      commit(z_full + 8 * buf);
+      commit(v_full + 8 * sst);
+      if (++sst == S::kVStages) sst = 0;
       if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);  // once the compute warps have left its stage
       if (q_id[kAhead] != kNone) load_k(q_id[kAhead], q_head[kAhead]);     // once the MMAs that used it are done
       if (++mst == S::kKStages) mst = 0, m_phase ^= 1;
@@ -856,7 +858,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t z_at = tmem + lane_base + T::z + half * R, o_at = tmem + lane_base + T::o + half * R;
     const uint32_t vt_at = tmem + lane_base + T::v + half * (VT / 2);
-    const uint32_t z_full = base + B::z_full, z_empty = base + B::z_empty, v_full = base + B::v_full;
+    const uint32_t z_empty = base + B::z_empty, v_full = base + B::v_full;
     const uint32_t v_empty = base + B::v_empty, pv_full = base + B::pv_full, pv_done = base + B::pv_done;
     const uint32_t bad_at = base + S::misc;
     // scales of V: the lane's tokens vtok, vtok + 1 (and 64 further on); their cells,
@@ -873,7 +875,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     const int tok = 32 * quad + lane;
     const uint32_t swz = (tok & 7) >> (N == 16 ? 2 : N == 32 ? 1 : 0);
     const uint32_t p_at = base + S::p + tok * 2 * N;
-    uint32_t zb = 0, z_phase = 0, vst = 0, v_phase = 0;  // of the next block
+    uint32_t zb = 0, vst = 0, v_phase = 0;  // of the next block
     uint32_t round = 0;                                  // of PV
     uint32_t cur = 0;                                    // which reference maxima
     auto done = [&](uint32_t r) {  // round r - 1 has ended
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       for (int k = w.nblk; k > 0; --k, n0 += kBlock) {
         // after a timed-out wait the warp goes on without waits (the barriers need
         // every warp); its results are void
-        if (alive) alive = wait_for(z_full + 8 * zb, z_phase, a.err) && wait_for(v_full + 8 * vst, v_phase, a.err);
+        if (alive) alive = wait_for(v_full + 8 * vst, v_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 + kBlock <= min_len;
         bool skip = false;
@@ -926,7 +928,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         // one PV round: the weights (of bf16 ones part 0 or 1) and V's tile
         auto send = [&](auto wide, int part) {
           const uint32_t b = round & 1;
-          done(round < 2 ? 0 : round - 1);  // the last round of this P (and V, if there are two) has ended
+          // P and V's tile are free: of two the round before the last, which used
+          // them, has ended; with one tile the wait below for the last round was that
+          // for P's sake too
+          if (T::kV == 2) done(round < 2 ? 0 : round - 1);
 #pragma unroll
           for (int c = 0; c < R; c += CH) {
             if (!kHold) {
@@ -1044,7 +1049,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           send(std::false_type{}, 0);
         }
         if (__builtin_expect(skip, 0)) {
-          done(round < 2 ? 0 : round - 1);
+          done(round);
           if (tid == 0) misc[5 + (round & 1)] = kNothing;
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
@@ -1053,7 +1058,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         }
         __syncwarp();
         if (lane == 0) arrive(v_empty + 8 * vst);
-        if (++zb == T::kZ) zb = 0, z_phase ^= 1;
+        if (++zb == T::kZ) zb = 0;
         if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
       }
 
