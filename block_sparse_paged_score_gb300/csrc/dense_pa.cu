@@ -460,46 +460,51 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
 }
 
 // ---- pieces of a compute warp's block -------------------------------------------
-// The scale bytes of V's tokens tok + i and the next (i: 0 or 64; tokens n + i and on
-// of the context of max_len), cells at `cell` for i = 0.  Of tokens behind the
-// context: kNever.
-__device__ __forceinline__ uint2 scale_bytes(uint32_t cell, int quad, int i) {
-  // 64 tokens are two rows of 128 bytes: the chunk's place in its row turns by two
-  const uint2 c = lds64(i ? (cell + 256) ^ 32 : cell);
-  return make_uint2(c.x >> (8 * quad) & 0xFF, c.y >> (8 * quad) & 0xFF);
-}
-// The pair of factors that put_v multiplies the two tokens by, f16
+// The cells of V's scales of a lane's two tokens, at `cell`, and of the two 64 tokens
+// on (i = 64): two rows of 128 bytes on, where a chunk's place in its row turns by two
+__device__ __forceinline__ uint2 scale_cells(uint32_t cell, int i) { return lds64(i ? (cell + 256) ^ 32 : cell); }
+// The pair of factors that put_v multiplies the lane's two tokens by, f16
 // 2^(byte - kVRef + 14), to the warp's words.  Returns whether f16 holds
-// v * 2^(byte - kVRef) exactly; a group of zeros may have any scale below.
-__device__ __forceinline__ bool scale_words(uint32_t cell, int n, int max_len, uint32_t word_at, uint32_t vt, int tok,
-                                            int quad, int i) {
-  const uint2 s = scale_bytes(cell, quad, i);
-  const int left = max_len - n - i;
-  const uint32_t y0 = left > 0 ? s.x - kVLow : kNever, y1 = left > 1 ? s.y - kVLow : kNever;
-  constexpr uint32_t span = kVHigh - kVLow;
-  const uint32_t w0 = y0 <= span ? (y0 + 6) << 10 : 0, w1 = y1 <= span ? (y1 + 6) << 26 : 0;
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at + 2 * i), "r"(w0 | w1) : "memory");
-  bool in = (y0 <= span || y0 == kNever) && (y1 <= span || y1 == kNever);
-  if (__builtin_expect(!in, 0)) {
-    in = true;
-    const int r = (tok + i) >> 1;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t b = k ? s.y : s.x, y = k ? y1 : y0;
+// v * 2^(byte - kVRef) exactly for both (and then the words are right).
+__device__ __forceinline__ bool scale_words(uint32_t cell, uint32_t word_at, uint32_t pick, int i) {
+  constexpr uint32_t k2 = 0x00010001u;
+  const uint2 c = scale_cells(cell, i);
+  const uint32_t b = __byte_perm(c.x, c.y, pick) & 0x00FF00FFu;
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at + 2 * i), "r"((b - (kVLow - 6) * k2) << 10) : "memory");
+  const uint32_t low = b + (512 - kVLow) * k2, high = b + (512 - kVHigh - 1) * k2;  // bit 9: not below, above
+  return (low & ~high & (512 * k2)) == 512 * k2;
+}
+// The same with care: factors 0 for tokens at or behind max_len, and for groups of
+// zeros, which may have any scale below the range.
+__device__ __noinline__ bool scale_words_exact(uint32_t cell, int n, int max_len, uint32_t word_at, uint32_t vt,
+                                               int tok, int quad, int i) {
+  const uint2 c = scale_cells(cell, i);
+  uint32_t word = 0;
+  bool in = true;
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (n + i + k >= max_len) continue;
+    const uint32_t b = (k ? c.y : c.x) >> (8 * quad) & 0xFF;
+    if (b >= kVLow && b <= kVHigh) {
+      word |= (b - (kVLow - 6)) << (10 + 16 * k);
+    } else {
+      const int r = (tok + i) >> 1;
       const uint4 v = lds128(vt + r * 128 + (((k * 4 + quad) ^ (r & 7)) << 4));
-      in &= y <= span || y == kNever || (b < kVLow && ((v.x | v.y | v.z | v.w) & 0x77777777u) == 0);
+      in &= b < kVLow && ((v.x | v.y | v.z | v.w) & 0x77777777u) == 0;
     }
   }
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at + 2 * i), "r"(word) : "memory");
   return in;
 }
 // The factors for bf16, 2^(byte - kVRef), over f16's (for any byte but the NaN's,
 // whose tokens count as 0 here); which rows see a NaN in the group.
 __device__ __noinline__ void wide_words(uint32_t cell, int n, int max_len, uint32_t word_at, int quad, int i,
                                         const int* lens, uint32_t* nan_of, int rows) {
-  const uint2 s = scale_bytes(cell, quad, i);
+  const uint2 c = scale_cells(cell, i);
   uint32_t word = 0;
+#pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    const uint32_t b = k ? s.y : s.x;
+    const uint32_t b = (k ? c.y : c.x) >> (8 * quad) & 0xFF;
     if (n + i + k >= max_len) continue;
     if (b == 255) {
       for (int r = 0; r < rows; ++r)
@@ -866,6 +871,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     const int vtok = VT * half + 2 * lane;
     const uint32_t cell_at = base + S::v + (64 + (vtok >> 5)) * 128 + ((((vtok & 31) >> 2) ^ (vtok >> 5)) << 4) +
                              (vtok & 3) * 4;
+    const uint32_t pick = quad | (4 + quad) << 8;  // byte quad of two cells, to bytes 0 and 2
     const uint32_t words = base + S::scales + warp * VT * 2;
     const uint32_t word_at = words + ((lane & 3) * 8 + (lane >> 2)) * 4, my_words = words + (lane & 3) * 32;
     // the lane's row for ldmatrix: token VT * half + lane (+ 32 k), two tokens a row of 128 bytes
@@ -925,6 +931,13 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         bool skip = false;
         const uint32_t z = z_at + zb * N, voff = vst * kVTile;
         float2 x[CH / 2];
+        auto exact = [&]() {
+          bool in = true;
+#pragma unroll 1
+          for (int i = 0; i < VT; i += 64)
+            in &= scale_words_exact(cell_at + voff, n0 + vtok, max_len, word_at, base + S::v + voff, vtok, quad, i);
+          return in;
+        };
         // one PV round: the weights (of bf16 ones part 0 or 1) and V's tile
         auto send = [&](auto wide, int part) {
           const uint32_t b = round & 1;
@@ -976,8 +989,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         // V's factors
         bool in = true;
 #pragma unroll
-        for (int i = 0; i < VT; i += 64)
-          in &= scale_words(cell_at + voff, n0 + vtok, max_len, word_at, base + S::v + voff, vtok, quad, i);
+        for (int i = 0; i < VT; i += 64) in &= scale_words(cell_at + voff, word_at, pick, i);
+        if (__builtin_expect(!in, 0)) in = exact();
         // first pass: does a row's maximum grow?
         float top = -INFINITY;
 #pragma unroll
@@ -992,7 +1005,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           // token, new references, and O and l in their terms; are V's scales
           // outside f16's range?
           skip = any_of<32 * kCompute>(bad);  // (a block whose id is out of range)
-          wide = any_of<32 * kCompute>(!in);
+          wide = any_of<32 * kCompute>(!exact());
           const int n = n0 + tok;
           if (skip) wide = false;
 #pragma unroll 1
@@ -1037,6 +1050,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           if (kHold) load_logits<CH>(x, z, base + S::refs + (cur * N + half * R) * 4, p.qk_scale);
           if (kHold && !whole) mask_logits<CH>(x, n, lens_at + half * R * 4);
           if (wide)
+#pragma unroll 1
             for (int i = 0; i < VT; i += 64)
               wide_words(cell_at + voff, n0 + vtok, max_len, word_at, quad, i, lens, nan_of, N);
         }
