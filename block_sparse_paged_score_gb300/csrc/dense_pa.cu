@@ -7,7 +7,7 @@
 // with k4, v4 the e2m1 values, e the e8m0 bytes of the four 32-dim groups c.
 //
 // Work.  A unit = (query group, KV head): its rows, q_group tokens times G
-// heads, share every byte of the cache; more than 16 rows are cut into units
+// heads, share every byte of the cache; more than 64 rows are cut into units
 // that neighbouring CTAs take at the same time (the second finds the bytes in
 // L2).  The units' 128-token blocks laid end to end are cut into equal
 // shares, one per resident CTA, so ragged batches load every SM alike; a CTA
@@ -17,33 +17,43 @@
 // a list of cut units, no counters: the workspace carries nothing from call to
 // call and the sums' order is fixed).
 //
-// A CTA is a producer warp and four compute warps.
-//   - The producer loads blocks by TMA (K unpacked to one byte slot a value,
-//     the layout the tensor core reads; V packed; the scales as they lie) and
-//     issues, per block, four tcgen05.mma block-scaled by the cache's own e8m0
-//     bytes: z^T = K Q^T, M = 128 tokens, N = 16 rows, K = 32 = one scale group
-//     each, in TMEM, double-buffered.  A bf16 query is the sum of two e4m3
-//     parts (see stage_q), eight MMAs.
-//   - A compute warp takes the exponentials of 32 tokens (thread = token) and
-//     leaves the f16 weights in shared memory, where it and its partner pick
-//     them up as mma A fragments: a pair of warps shares 64 tokens, each
-//     multiplies them by its half of V's dims (mma.sync m16n8k16 f16), so that O
-//     takes 32 registers.  V comes through ldmatrix.trans as four
-//     nibbles of two tokens a register; bit moves turn them into f16 pairs,
-//     times 2^-14 exactly.  V's scales go onto P: 2^(ev - R_c), a power of two
-//     at most 1, multiplies the weights of each group.  R_c is at least
-//     the largest scale byte so far (O is rescaled when it grows).  Tokens whose
-//     scale is 15 or more binades below R_c, which f16 could not hold, make the pair
-//     take its tokens again in bands of 15.
-//   - p is f16, at most half a step, 2^-11, off; weights are kept times 2^9 and
-//     R_c two binades high, so that f16's range, down to 2^-25, reaches 2^-32 of the
-//     largest.  Row sums
-//     are an mma column of ones over the rounded weights.
-// tcgen05 takes the scores because it reads e2m1 and the scales itself: on
-// mma.sync the conversions of K cost more issue slots than all else.  PV stays
-// on mma.sync: with V^T as A its dequantised tile would have to go through
-// shared memory, 32 KB written and read a block, more than a block's time at
-// the memory's rate.
+// Both products are tcgen05 MMAs with the block's tokens or V's dims as their 128
+// rows and the unit's N = 16, 32 or 64 rows as their columns:
+//   z^T = K Q^T      A = K from shared memory, e2m1, block-scaled by the cache's own
+//                    e8m0 bytes (K = 32 = one scale group an MMA), B = q; a bf16
+//                    query is the sum of two e4m3 parts (see stage_q)
+//   O^T += V^T P     A = V^T, f16, from TMEM, B = P, f16, from shared memory
+// so that O, N columns of 128 dims, stays in TMEM, and what the warps do per
+// block is the exponentials of N rows and the conversion of V, once for all rows.
+// V goes to TMEM: through shared memory its f16 tile would be 32 KB written and
+// 32 KB read a block, more than a block's time at the memory's rate.
+//
+// A CTA is a producer warp, which loads blocks by TMA (K unpacked to one byte
+// slot a value, the layout the tensor core reads; V packed; scales as they lie)
+// and issues all MMAs, and four or eight compute warps.  Thread = token of the
+// logits: it takes its exponentials 2^(z - m + kBias) against the row's reference m
+// and adds them up (one reduction at the end of the unit).  References move only
+// when a row's maximum passes its reference by kMaxGrow; a vote of the CTA finds
+// those blocks, and the ones that some row does not see whole, and takes them
+// through an uncommon way that rescales O and l.  Then the warp turns a quarter of
+// V's dims into f16: ldmatrix.trans hands a thread four nibbles of two tokens in a
+// register, bit moves make f16 pairs of them, times 2^-14 exactly, and a product
+// with 2^(byte - kVRef + 14) puts the scale on, exact for bytes kVLow .. kVHigh.
+// Blocks with other scales are multiplied in bf16, which holds any v * 2^e, with the
+// weights in two bf16 parts (2^-17 off), in two rounds.  Outputs of 2^90 and more
+// may overflow on the way.
+//
+// Roundings: a weight is f16, at most half a step, 2^-11, off, and with a reference
+// of 2^kBias f16's range, down to 2^-25, reaches 2^-32 of the row's largest.  z, m,
+// l and O are fp32.  The sums l are those of the unrounded weights.
+//
+// Measured (64 requests x 131072 tokens, 16 rows: 1.14 GB): 249 us, 4.6 TB/s; 128 x
+// 32768 with 64 rows: 0.57 GB in 260 us.  What bounds it is the chain of a block
+// through a CTA, about 2 700 clocks (wait, logits, vote, exponentials, V's
+// conversion, fences) of which three CTAs an SM (two of 64 rows) overlap: at 16
+// rows about 2 800 warp instructions a block, 51 % of the issue slots, the tensor
+// cores 6 %.  PV on mma.sync, weights and V as register fragments, took 289 us and
+// 536 us: V's conversion and the loads of P were repeated for every 16 rows.
 //
 // Every wait for a copy or an MMA is bounded; after a timed-out wait a role
 // waits no more (the error word is set, the results are void), walks through its
@@ -70,7 +80,7 @@ constexpr float kBias = 7.f;      // weights are 2^(z - m + kBias): at most 2^15
 constexpr float kNoMax = -1e30f;  // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
 // V enters the MMA as v * 2^(scale byte - kVRef).  f16 holds that exactly for
 // bytes from kVLow to kVHigh (2^-17 to 2^7); see scale_words.
-constexpr uint32_t kNever = 0x80000000u;  // of a token no row sees
+
 constexpr int kVRef = 133, kVLow = kVRef - 23, kVHigh = kVRef + 1;
 
 // bytes of the list of cut units at the start of the workspace
@@ -155,12 +165,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[C]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < C; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  return __uint_as_float(r);
 }
 template <int C>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[C]) {
@@ -382,7 +386,7 @@ struct Walk {
       ++g;
       nb = blocks_of(a, __reduce_max_sync(0xffffffffu, group_len(a, g, lane, 32)));
     }
-    h = static_cast<int>((at - c0 * a.hkv) / nb);
+    h = a.hkv == 1 ? 0 : static_cast<int>((at - c0 * a.hkv) / nb);
     const int64_t ustart = c0 * a.hkv + static_cast<int64_t>(h) * nb, uend = ustart + nb;
     unit = (g * a.hkv + h) * p.subs + sub;
     const int gtok = g * a.q_group;
@@ -591,6 +595,7 @@ struct Tmem {
 };
 // what a PV round is
 constexpr uint32_t kAccumulate = 1, kBf16 = 2, kMore = 4, kNothing = 8;
+constexpr uint32_t kWide = 1, kSkip = 2;
 
 template <int N, bool Q16>
 __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
@@ -928,7 +933,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         if (alive) alive = wait_for(v_full + 8 * vst, v_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 + kBlock <= min_len;
-        bool skip = false;
         const uint32_t z = z_at + zb * N, voff = vst * kVTile;
         float2 x[CH / 2];
         auto exact = [&]() {
@@ -999,15 +1003,14 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
         }
-        bool wide = false;
+        uint32_t mode = 0;  // kWide: V in bf16; kSkip: a block whose id is out of range
         if (__builtin_expect(!all_of<32 * kCompute>(!bad && whole && in && top <= kBias + kMaxGrow), 0)) {
           // The uncommon way: the rows' maxima, where a row may not see the
           // token, new references, and O and l in their terms; are V's scales
           // outside f16's range?
-          skip = any_of<32 * kCompute>(bad);  // (a block whose id is out of range)
-          wide = any_of<32 * kCompute>(!exact());
+          const bool skip = any_of<32 * kCompute>(bad), wide = any_of<32 * kCompute>(!exact()) && !skip;
+          mode = skip ? kSkip : wide ? kWide : 0;
           const int n = n0 + tok;
-          if (skip) wide = false;
 #pragma unroll 1
           for (int c = 0; c < (skip ? 0 : R); c += CH) {
             float y[CH];
@@ -1056,13 +1059,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         }
         // second pass: the weights, and V as the MMA reads it.  Where V's scales
         // are beyond f16, both are bf16 and the weights go in two parts.
-        if (__builtin_expect(wide, 0)) {
+        if (__builtin_expect(mode == 0, 1)) {
+          send(std::false_type{}, 0);
+        } else if (mode == kWide) {
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) send(std::true_type{}, part);
-        } else if (!skip) {
-          send(std::false_type{}, 0);
-        }
-        if (__builtin_expect(skip, 0)) {
+        } else {
           done(round);
           if (tid == 0) misc[5 + (round & 1)] = kNothing;
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1086,39 +1088,51 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, sum);
       }
       bar_sync(1, 32 * kCompute);
-      if (!first) done(round);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const bool all = w.starts && w.ends;
       // a CTA's slots: 2 * CTA for a unit that began before its share, + 1 for one
       // that goes on after it
       float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
                   (2LL * blockIdx.x + (w.starts ? 1 : 0)) * N * (kDim + 2);
+      const int rows = w.tokens * a.group;
+      if (tid < N) {  // what O is multiplied by: V's 2^(kVRef - 127), over the sum
+        const float sum = (ldsf(tops + tid * 4) + ldsf(tops + (N + tid) * 4)) +
+                          (ldsf(tops + (2 * N + tid) * 4) + ldsf(tops + (3 * N + tid) * 4));
+        stsf(fac + tid * 4, static_cast<float>(1 << (kVRef - 127)) * (!all ? 1.f : sum == 0.f ? 0.f : 1.f / sum));
+        if (!all && tid < rows)
+          *reinterpret_cast<float2*>(po + N * kDim + 2 * tid) =
+              make_float2(kBias - ldsf(base + S::refs + (cur * N + tid) * 4), sum);
+      }
+      bar_sync(1, 32 * kCompute);
+      if (!first) done(round);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int d = 32 * quad + 4 * (lane & 7) + (lane >> 3);  // the lane's dim (see put_v)
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                            (static_cast<int64_t>(w.tok0) * a.hkv + w.h) * a.group * kDim + d;
-      const int rows = w.tokens * a.group;
-      const int64_t skip_rows = static_cast<int64_t>(a.hkv - 1) * a.group * kDim;  // from a token's rows to the next's
+      const int64_t hop = static_cast<int64_t>(a.hkv - 1) * a.group * kDim;  // from a token's rows to the next's
       int in_token = (half * R) % a.group;
-      out += (half * R) / a.group * skip_rows + half * R * kDim;
+      out += (half * R) / a.group * hop + half * R * kDim;
 #pragma unroll 1
-      for (int i = 0; i < R; ++i) {
-        const int r = half * R + i;
-        if (r >= rows) break;
-        float o = 0.f;
-        if (!first) o = tmem_ld1(o_at + i);
-        const float sum = (ldsf(tops + r * 4) + ldsf(tops + (N + r) * 4)) +
-                          (ldsf(tops + (2 * N + r) * 4) + ldsf(tops + (3 * N + r) * 4));
-        o *= static_cast<float>(1 << (kVRef - 127));
-        if (nan_of[r] >> quad & 1) o = __uint_as_float(0x7FC00000u);
-        if (all) {
-          *out = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
-          out += kDim;
-          if (++in_token == a.group) in_token = 0, out += skip_rows;
+      for (int c = 0; c < R; c += 8) {
+        float y[8];
+        if (!first) {
+          tmem_ld<8>(o_at + c, y);
         } else {
-          po[r * kDim + d] = o;
-          if (quad == 0 && lane == 0)
-            *reinterpret_cast<float2*>(po + N * kDim + 2 * r) =
-                make_float2(kBias - ldsf(base + S::refs + (cur * N + r) * 4), sum);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = half * R + c + i;
+          if (r < rows) {
+            const float o = lds32(base + S::nan + r * 4) >> quad & 1 ? __uint_as_float(0x7FC00000u) : y[i] * ldsf(fac + r * 4);
+            if (all) {
+              *out = __float2bfloat16_rn(o);
+              out += kDim;
+              if (++in_token == a.group) in_token = 0, out += hop;
+            } else {
+              po[r * kDim + d] = o;
+            }
+          }
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
