@@ -498,8 +498,7 @@ bsp_status bsp_norm_rope_write(const bsp_norm_rope_args* a, bsp_stream_t stream)
     const int64_t row = static_cast<int64_t>(heads[i]) * kDim;
     if (heads[i] < 1 || stride[i] < row || stride[i] % 8 || !al(src[i], 16) || !al(weight[i], 16) || !al(out[i], 16))
       return BSP_ERR_INVALID_ARG;
-    if (heads[i] > (1 << 20)) return BSP_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(heads[i]) * T > (int64_t{1} << 40)) return BSP_ERR_UNSUPPORTED;
+    if (heads[i] > (1 << 16) || stride[i] > (int64_t{1} << 32)) return BSP_ERR_UNSUPPORTED;
     p.src[i] = static_cast<const uint16_t*>(src[i]);
     p.stride[i] = stride[i];
     p.heads[i] = heads[i];

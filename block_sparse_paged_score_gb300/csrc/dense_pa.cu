@@ -1298,8 +1298,8 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   p.subs = pl.subs;
   p.sub_tokens = pl.sub_tokens;
   p.rows = pl.rows;
+  // (a group of more than 64 rows, two units, has five tokens or more: units <= num_rows)
   const int64_t pairs = static_cast<int64_t>(p.groups) * a.hkv, units = pairs * pl.subs;
-  if (units > INT32_MAX) return cudaErrorNotSupported;
   p.units = static_cast<int32_t>(units);
   p.shares = static_cast<int32_t>(
       std::min<int64_t>(static_cast<int64_t>(pl.ctas_per_sm) * num_sms / pl.subs, pairs * a.bt_stride));

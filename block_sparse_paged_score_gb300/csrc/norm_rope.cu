@@ -329,7 +329,6 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t 
   // (measured at 24 heads: 10.2 and 14.5 us at 2048 tokens, 17.8 and 17.2 at 4096,
   // 35.1 and 26.9 at 8192, 85.5 and 44.2 at 16456)
   const bool many = groups >= static_cast<int64_t>(num_sms) * 3;
-  if (!many && groups * total > INT32_MAX) return cudaErrorInvalidConfiguration;
   const cudaError_t e =
       many ? launch_kernel(norm_rope_token_kernel, dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s, 0, p)
            : launch_kernel(norm_rope_kernel, dim3(static_cast<unsigned>(groups * total)), dim3(kThreads), 0, s, 0, p,

@@ -509,7 +509,8 @@ bsp_status bsp_step_tables(const bsp_step_tables_args* a, bsp_stream_t stream);
  *    position is a pad row: its outputs are zeros and nothing is cached.  A
  *    position >= rope_rows sets BSP_DEVERR_POSITION and counts as a pad row.
  *  - slot int64 [T] as in bsp_kv_page_write (negative: not cached); needed
- *    with kv or idx.  The same slot twice in a call: one of the rows is kept.
+ *    with kv or idx.  The same slot twice in a call leaves that slot's bytes
+ *    unspecified (a mixture of the two rows).
  *  - q_out, k_out and idx_q_out are dense [T, heads, 128].  A bf16 output may
  *    be its own dense input; any other overlap of an output with an input or
  *    another output is BSP_ERR_INVALID_ARG.  The inputs must be device memory.
@@ -577,11 +578,15 @@ bsp_status bsp_kv_page_read(const bsp_kv_cache* kv, const bsp_index_cache* idx, 
  *         tokens * Hkv; L_r is clamped to [0, 128 * bt_stride]; a row with
  *         L_r = 0 gets zeros
  *   q_group 1..8 as in bsp_index_score: consecutive tokens that share a
- *         sequence; the cache is streamed once per group and KV head.  Rows of
- *         a group that name another sequence set BSP_DEVERR_GROUP_SEQ and are
+ *         sequence; the cache is read once per group and KV head (twice, the
+ *         second time mostly from L2, where q_group * G > 64).  Rows of a
+ *         group that name another sequence set BSP_DEVERR_GROUP_SEQ and are
  *         computed with the first row's.
  * A block id out of range sets BSP_DEVERR_BLOCK_ID and its tokens are left
- * out.  Bytes at and past L_r are never used, whatever they hold.
+ * out.  Bytes at and past L_r are never used by row r, whatever they hold.  A
+ * scale byte 255 is a NaN.  Weights are rounded to f16 and sums are fp32; values
+ * of V of 2^90 and more may come out as infinite.
+ * One launch, two where shares of the work cut a sequence.
  * ws: device workspace of bsp_dense_pa_workspace_bytes() bytes, 16-byte
  * aligned (its contents need not be set, and carry nothing from call to
  * call).  Calls that may overlap on the GPU, captured ones included, need

@@ -1,7 +1,8 @@
 """bsp_dense_pa_decode against softmax(scale q K^T) V in 64 bits.
 
 Tolerance.  With a = sum p |v| / sum p of an output element: a softmax weight
-is rounded to at most 2^-11 relative (f16), a logit is off by at most
+is rounded to at most 2^-11 relative (f16; in two bf16 parts, 2^-17, where V's
+scales are beyond f16, and V's values are exact either way), a logit is off by at most
 e = 2^-18 * scale * sum |q k| (fp32 sums of at most 512 exact products, and
 the split of a bf16 query into two e4m3 parts, 2^-18 of its row's largest
 value), which moves a weight and the sum by e each, and the exponentials, the
@@ -325,3 +326,81 @@ def test_offsets_past_32_bits():
     torch.cuda.synchronize()
     assert c.err.item() == 0
     c.check(out)
+
+
+def _tolerance(c, o, a):
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.0 ** -13 + 2 * c.logit_slack()) * a
+    for r in range(len(c.row_len)):
+        t, h = divmod(r, c.hkv)
+        tol[t, h * c.group:(h + 1) * c.group] += c.floor(r)
+    return tol
+
+
+def _f64(out):
+    return bf16_to_f64(out.view(torch.int16).cpu().numpy().view(np.uint16))
+
+
+@pytest.mark.parametrize("byte", [9, 40, 109, 110, 134, 135, 180])
+@pytest.mark.parametrize("q_len", [1, 2, 4])
+def test_one_scale_in_v(byte, q_len):
+    """On both sides of what f16 holds (bytes 110 to 134)."""
+    c = Case([900, 70], q_len=q_len, seed=byte)
+    c.fields[:, c.hkv:, 8192:] = byte
+    _close(c)
+
+
+@pytest.mark.parametrize("q_len,group", [(1, 16), (2, 16), (4, 16), (8, 16), (3, 4)])
+@pytest.mark.parametrize("q8", [True, False])
+def test_logits_that_grow_along_the_context(q_len, group, q8):
+    """Every few blocks some row's maximum passes its reference."""
+    c = Case([2500, 1800, 400], group=group, q_len=q_len, q8=q8, seed=21)
+    for s in range(3):
+        for i, b in enumerate(c.table[s]):
+            c.fields[b, 0, 8192:] = 118 + min(i, 12)
+    _close(c)
+
+
+@pytest.mark.parametrize("side", [0, 1])
+def test_a_nan_reaches_only_the_rows_that_see_it(side):
+    """A scale byte of 255 in K (the whole row) or in one group of V, in the last
+    two tokens of four rows of growing length."""
+    lens = [130, 700, 3]
+    c = Case(lens, q_len=4, seed=22)
+    o, a = c.want()
+    tol = _tolerance(c, o, a)
+    for s, n in enumerate(lens):
+        for t in (n - 1, n - 2):
+            c.fields[c.table[s, t // 128], side, 8192 + 4 * (t % 128) + 1] = 255
+    c.device()
+    g = _f64(c.call())
+    for s in range(3):
+        for j in range(4):
+            r = 4 * s + j
+            hit = j >= 2  # row j sees tokens below n - 3 + j
+            dims = np.zeros(128, bool)
+            if hit:
+                dims[slice(None) if side == 0 else slice(32, 64)] = True
+            assert np.isnan(g[r][:, dims]).all(), (s, j)
+            assert (np.abs(g[r] - o[r]) <= tol[r])[:, ~dims].all(), (s, j)
+
+
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 0.3])
+def test_other_logit_scales(scale):
+    c = Case([700, 129, 4000], q_len=2, seed=23).device()
+    b = c.bsp
+    got = _f64(b.dense_pa_decode(c.kv, c.dq, b.FP8_E4M3, 16, c.dtable, c.dseq, c.dlen, 2, sm_scale=scale))
+    o, a = dense_attention(lambda blk, side, h: mx_field(c.fields[blk, side * c.hkv + h]), c.table, c.q, c.row_seq,
+                           c.row_len, c.hkv, c.group, scale)
+    tol = _tolerance(c, o, a) + 2 * (abs(scale) / SCALE) * c.logit_slack() * a
+    assert (np.abs(got - o) <= tol).all()
+
+
+def test_calls_of_other_sizes_in_one_workspace_one_after_another():
+    cases = [Case([9000, 40], q_len=4, seed=24).device(), Case([300, 12000, 5], q_len=1, seed=25).device(),
+             Case([5000], q_len=2, group=8, q8=False, seed=26).device()]
+    ws = torch.empty(max(c.bsp.dense_pa_workspace_bytes(len(c.row_len), 1, c.group, c.q_len) for c in cases),
+                     dtype=torch.uint8, device="cuda")
+    want = [c.call().clone() for c in cases]
+    for _ in range(3):
+        for c, w in zip(cases, want):
+            assert torch.equal(c.call(ws=ws), w)

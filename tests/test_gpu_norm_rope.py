@@ -241,3 +241,54 @@ def test_captured_and_replayed_on_another_stream():
         g.replay()
     s.synchronize()
     assert torch.equal(out[0], q) and torch.equal(out[1], iq) and torch.equal(c.kv.buffer, kept)
+
+
+@pytest.mark.parametrize("kv,idx", [(BF16, BF16), (FP8, FP8), (MX, MX)])
+@pytest.mark.parametrize("hkv,group,rot,pairs,q8", [(1, 3, 64, False, True), (3, 1, 128, True, False)])
+def test_batches_long_enough_for_a_half_warp_a_token(kv, idx, hkv, group, rot, pairs, q8):
+    c = Case(3801, hkv, group, kv, idx, rot, pairs, q8, pads=9, seed=kv)
+    q, iq = c.run()
+    assert c.op.dev_err.item() == 0
+    _check_queries(c, q, "q")
+    _check_queries(c, iq, "idx_q")
+    _check_caches(c)
+
+
+def test_the_same_row_in_a_short_and_a_long_batch():
+    """Both kernels round alike: a long batch's rows are bit for bit those of its parts."""
+    c = Case(4000, 1, 4, MX, FP8, 64, q8=True, seed=31)
+    q, iq = (t.clone() for t in c.run())
+    kv, idx = c.kv.buffer.clone(), c.idx.buffer.clone()
+    c.kv.buffer.zero_(), c.idx.buffer.zero_()
+    x, pos, slot = c.x, c.pos.cuda(), c.slot.cuda()
+    for a in range(0, 4000, 700):
+        s = slice(a, min(a + 700, 4000))
+        got = c.op.run(x["q"][s], x["k"][s], x["v"][s], x["idx_q"][s], x["idx_k"][s], pos[s], slot[s])
+        assert torch.equal(got[0], q[s]) and torch.equal(got[1], iq[s])
+    assert torch.equal(c.kv.buffer, kv) and torch.equal(c.idx.buffer, idx)
+
+
+@pytest.mark.parametrize("T", [30, 4100])
+def test_without_a_kv_cache_without_an_index_cache_and_keys_as_rows(T):
+    from block_sparse_paged_score_gb300 import step
+    c = Case(T, 2, 2, FP8, MX, 64, seed=T)
+    q, iq = (t.clone() for t in c.run())
+    x, pos, slot = c.x, c.pos.cuda(), c.slot.cuda()
+    kv, idx = c.kv.buffer.clone(), c.idx.buffer.clone()
+    w = dict(q_weight=c.w["q"], k_weight=c.w["k"], idx_q_weight=c.w["idx_q"], idx_k_weight=c.w["idx_k"],
+             rope_table=c.rope)
+    c.kv.buffer.zero_(), c.idx.buffer.zero_()
+    a = step.NormRopeWrite(None, c.idx, c.hq, T, **w)
+    got = a.run(x["q"], None, None, x["idx_q"], x["idx_k"], pos, slot)
+    assert torch.equal(got[0], q) and torch.equal(got[1], iq)
+    assert not c.kv.buffer.any() and torch.equal(c.idx.buffer, idx)
+    c.idx.buffer.zero_()
+    b = step.NormRopeWrite(c.kv, None, c.hq, T, **w)
+    k_out = torch.full((T + 1, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    b.args.k_out = k_out.data_ptr()
+    got = b.run(x["q"], x["k"], x["v"], None, None, pos, slot)
+    assert torch.equal(got[0], q) and got[1] is None
+    assert torch.equal(c.kv.buffer, kv) and not c.idx.buffer.any()
+    y, mag = c.want("k")
+    _near(bf16_to_f64(k_out[:T].view(torch.int16).cpu().numpy().view(np.uint16)), y, 2.0 ** -8 * np.abs(y) + SLACK * mag, "k")
+    assert (k_out[T:] == 7).all()
