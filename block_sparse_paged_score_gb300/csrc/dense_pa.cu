@@ -860,7 +860,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     // 32 * quad .. and O's dims of 32-dim group quad; R rows of both.  Of V it takes
     // that group of VT tokens.
     constexpr int R = Shape<N>::kRows, CH = 16, VT = Shape<N>::kTokens;  // rows of a warp, and of them at a time
-    constexpr bool kHold = R == CH;                 // the logits stay in registers between the two passes
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t tops = base + S::tops, lens_at = base + S::len, fac = base + S::fac;
     int* lens = reinterpret_cast<int*>(smem + S::len);
@@ -934,7 +933,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 + kBlock <= min_len;
         const uint32_t z = z_at + zb * N, voff = vst * kVTile;
-        float2 x[CH / 2];
         auto exact = [&]() {
           bool in = true;
 #pragma unroll 1
@@ -951,10 +949,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           if (T::kV == 2) done(round < 2 ? 0 : round - 1);
 #pragma unroll
           for (int c = 0; c < R; c += CH) {
-            if (!kHold) {
-              load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
-              if (!whole) mask_logits<CH>(x, n0 + tok, lens_at + (half * R + c) * 4);
-            }
+            float2 x[CH / 2];  // (read again rather than held: registers)
+            load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+            if (!whole) mask_logits<CH>(x, n0 + tok, lens_at + (half * R + c) * 4);
             uint32_t pk[CH / 2];
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) {
@@ -999,6 +996,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < R; c += CH) {
+          float2 x[CH / 2];
           load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
@@ -1050,8 +1048,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
               tmem_st<CH>(o_at + c, y);
             }
           }
-          if (kHold) load_logits<CH>(x, z, base + S::refs + (cur * N + half * R) * 4, p.qk_scale);
-          if (kHold && !whole) mask_logits<CH>(x, n, lens_at + half * R * 4);
           if (wide)
 #pragma unroll 1
             for (int i = 0; i < VT; i += 64)
@@ -1298,7 +1294,6 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   p.subs = pl.subs;
   p.sub_tokens = pl.sub_tokens;
   p.rows = pl.rows;
-  // (a group of more than 64 rows, two units, has five tokens or more: units <= num_rows)
   const int64_t pairs = static_cast<int64_t>(p.groups) * a.hkv, units = pairs * pl.subs;
   p.units = static_cast<int32_t>(units);
   p.shares = static_cast<int32_t>(
