@@ -610,7 +610,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
   int64_t* s_start = s_sum + kThreads / 32;  // the share's first group, the blocks before it, its blocks
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::misc);
   const DensePaParams& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (uniform, and known to be)
   using B = Bars<N, Q16>;
   const uint32_t base = smem_u32(smem);
   if (tid == 0) {
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = misc[4];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, misc[4], 0);
   Walk w;
   w.at = at, w.end = min(at + share, total * a.hkv);
   w.g = 0, w.c0 = 0, w.nb = 1;
