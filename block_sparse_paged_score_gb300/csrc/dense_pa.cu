@@ -96,20 +96,20 @@ struct Params {
 };
 
 // ---- shared memory -----------------------------------------------------------
-// Units of 16 rows: four compute warps a CTA, three CTAs an SM; of more: eight, two.
+// Units of 16 rows: four compute warps a CTA, four CTAs an SM; of more: eight, two.
 // Then the producer.
 template <int N>
 struct Shape {
-  static constexpr int kCompute = N == 16 ? 4 : 8, kThreads = 32 * (kCompute + 1), kCtasPerSm = N == 16 ? 3 : 2;
+  static constexpr int kCompute = N == 16 ? 4 : 8, kThreads = 32 * (kCompute + 1), kCtasPerSm = N == 16 ? 4 : 2;
   static constexpr int kHalves = kCompute / 4;          // warps that share 32 TMEM lanes
   static constexpr int kRows = N / kHalves;             // a compute warp's
   static constexpr int kTokens = kBlock / kHalves;      // of V
 };
 template <int N, bool Q16>
 struct Smem {
-  // (as much as two CTAs an SM leave room for)
+  // (as much as the CTAs of an SM leave room for)
   static constexpr int kCompute = Shape<N>::kCompute;
-  static constexpr int kKStages = N == 32 ? 3 : 2, kVStages = N == 16 && Q16 ? 2 : 3;
+  static constexpr int kKStages = N == 16 ? 1 : N == 32 ? 3 : 2, kVStages = N == 16 ? 2 : 3;
   static constexpr int kPBytes = kBlock * N * 2;  // P [128 tokens][N rows] f16, two of them
   static constexpr int v = kKStages * kKTile;
   static constexpr int p = v + kVStages * kVTile;
