@@ -1027,7 +1027,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll
             for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + tid) * 4));
             const float old = ldsf(base + S::refs + (cur * N + tid) * 4);  // kBias - m
-            const float ref = mx > kBias - old + kMaxGrow ? kBias - mx : old;
+            const float ref = mx > kBias - old ? kBias - mx : old;  // (every row: fewer such blocks to come)
             f = ex2_approx(ref - old);
             stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, ref);
             stsf(fac + tid * 4, f);
