@@ -122,8 +122,8 @@ struct Smem {
   static constexpr int nan = len + N * 4;                     // [N] 32-dim groups that hold a NaN scale
   static constexpr int sfq = nan + N * 4;                     // [2][N] scale cells of q
   static constexpr int bars = sfq + 2 * N * 4;
-  static constexpr int misc = bars + 24 * 8;  // bad[4], TMEM address, commands[2]
-  static constexpr int total = misc + 32;
+  static constexpr int misc = bars + 24 * 8;  // bad[4], TMEM address, commands[2], what is uncommon[2]
+  static constexpr int total = misc + 48;
   static_assert(p % 1024 == 0 && q % 1024 == 0 && refs % 16 == 0);
 };
 
@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     init(B::z_empty, 2, kCompute);
     init(B::pv_full, 2, kCompute), init(B::pv_done, 2, 1);
     init(B::q_full, 1, 4);
+    misc[7] = misc[8] = 0;
     mbar_fence_init();
   }
   pdl_wait();
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     const uint32_t vt_at = tmem + lane_base + T::v + half * (VT / 2);
     const uint32_t z_empty = base + B::z_empty, v_full = base + B::v_full;
     const uint32_t v_empty = base + B::v_empty, pv_full = base + B::pv_full, pv_done = base + B::pv_done;
-    const uint32_t bad_at = base + S::misc;
+    const uint32_t bad_at = base + S::misc, flags = base + S::misc + 28;  // V beyond f16; a bad block
     // scales of V: the lane's tokens vtok, vtok + 1 (and 64 further on); their cells,
     // in row 64 + token / 32
     const int vtok = VT * half + 2 * lane;
@@ -992,7 +993,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         bool in = true;
 #pragma unroll
         for (int i = 0; i < VT; i += 64) in &= scale_words(cell_at + voff, word_at, pick, i);
-        if (__builtin_expect(!in, 0)) in = exact();
+        if (__builtin_expect(!in || !whole, 0)) in = exact();
+        if (__builtin_expect(bad || !in, 0))
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(flags + (bad ? 4 : 0)), "r"(1u) : "memory");
         // first pass: does a row's maximum grow?
         float top = -INFINITY;
 #pragma unroll
@@ -1007,21 +1010,27 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           // The uncommon way: the rows' maxima, where a row may not see the
           // token, new references, and O and l in their terms; are V's scales
           // outside f16's range?
-          const bool skip = any_of<32 * kCompute>(bad), wide = any_of<32 * kCompute>(!exact()) && !skip;
+          const bool skip = lds32(flags + 4) != 0, wide = !skip && lds32(flags) != 0;
           mode = skip ? kSkip : wide ? kWide : 0;
-          const int n = n0 + tok;
+          if (!skip) {
 #pragma unroll 1
-          for (int c = 0; c < (skip ? 0 : R); c += CH) {
-            float y[CH];
-            tmem_ld<CH>(z + c, y);
+            for (int c = 0; c < R; c += CH) {
+              float y[CH];
+              tmem_ld<CH>(z + c, y);
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
-              y[i] = n < static_cast<int>(lds32(lens_at + (half * R + c + i) * 4)) ? y[i] * p.qk_scale : -INFINITY;
-            const float mx = warp_reduce<CH>(y, lane, [](float u, float v) { return fmaxf(u, v); });
-            if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, mx);
+              for (int i = 0; i < CH; ++i) y[i] *= p.qk_scale;
+              if (!whole) {
+#pragma unroll
+                for (int i = 0; i < CH; ++i)
+                  if (n0 + tok >= static_cast<int>(lds32(lens_at + (half * R + c + i) * 4))) y[i] = -INFINITY;
+              }
+              const float mx = warp_reduce<CH>(y, lane, [](float u, float v) { return fmaxf(u, v); });
+              if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, mx);
+            }
           }
           bar_sync(1, 32 * kCompute);
           float f = 1.f;
+          if (tid == 0 && mode) misc[7] = misc[8] = 0;  // (every warp has read them, and sets none before the next vote)
           if (tid < N && !skip) {
             float mx = ldsf(tops + tid * 4);
 #pragma unroll
