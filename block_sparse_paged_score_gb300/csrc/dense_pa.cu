@@ -47,13 +47,15 @@
 // of 2^kBias f16's range, down to 2^-25, reaches 2^-32 of the row's largest.  z, m,
 // l and O are fp32.  The sums l are those of the unrounded weights.
 //
-// Measured (64 requests x 131072 tokens, 16 rows: 1.14 GB): 249 us, 4.6 TB/s; 128 x
-// 32768 with 64 rows: 0.57 GB in 260 us.  What bounds it is the chain of a block
-// through a CTA, about 2 700 clocks (wait, logits, vote, exponentials, V's
-// conversion, fences) of which three CTAs an SM (two of 64 rows) overlap: at 16
-// rows about 2 800 warp instructions a block, 51 % of the issue slots, the tensor
-// cores 6 %.  PV on mma.sync, weights and V as register fragments, took 289 us and
-// 536 us: V's conversion and the loads of P were repeated for every 16 rows.
+// Measured (64 requests x 131072 tokens, 16 rows: 1.14 GB): 226 us, 5.1 TB/s; 128 x
+// 32768 with 64 rows: 0.57 GB in 231 us.  What bounds it is instruction issue and
+// the chain of a block through a CTA (wait, logits, vote, exponentials, V's
+// conversion, fences), which four CTAs an SM (two of 64 rows) overlap: 2 500 warp
+// instructions a block of 16 rows, 1 000 of them V's conversion, at 67 % of the
+// issue slots; 4 600 of 64 rows, at 60 %.  The tensor cores are 10 and 20 % busy.
+// With three CTAs an SM 16 rows took 249 us.  PV on mma.sync, weights and V as
+// register fragments, took 289 us and 536 us: V's conversion and the loads of P
+// were repeated for every 16 rows.
 //
 // Every wait for a copy or an MMA is bounded; after a timed-out wait a role
 // waits no more (the error word is set, the results are void), walks through its
@@ -1258,7 +1260,9 @@ bool make_map_side(CUtensorMap* m, bool unpack, const void* base, uint64_t heads
 }
 
 // How a group's rows are cut into units of at most 64, and the rows the kernel is
-// built for.
+// built for.  128 requests of 32768 tokens, us, units of at most 16, 32 and 64 rows:
+// 32 rows a group 220, 187, 186; 64 rows 413, 348, 231; 128 rows 803, 673, 418; a
+// group of 32 rows in the kernel for 64: 223.
 struct Plan {
   int sub_tokens, subs, rows, ctas_per_sm;
 };

@@ -11,6 +11,9 @@
 // page holds 16 (fp8) or 8 (bf16) tokens of one dim together; there a lane
 // is a token, a warp reads two dims at a time, and the tile is turned around
 // in shared memory before it is stored in rows.
+//
+// Measured: 333 fp8 tokens 2.5 us, a launch; 131072 MXFP4 tokens of a shuffled cache
+// 15.4 us for 86 MB, 5.6 TB/s, 84 % of the copy rate: memory.
 #include "common.cuh"
 #include "kernels.h"
 

@@ -15,6 +15,12 @@
 // 16 lanes hold a head, 8 dims each (16-byte loads; mean and MXFP4 group
 // maxima are shuffles within 16 and 4 lanes).  A half-warp takes one token; the
 // head's type and number are the same for a whole warp.
+//
+// Measured: 1 token 1.9 us (a launch); 16456 tokens of 16 + 1 + 1 + 1 + 1 heads, bf16
+// queries and fp8 caches, 44 us for 167 MB: 3.8 TB/s, 57 % of the copy rate.  There
+// issue bounds it: some 50 warp instructions for two tokens' heads, 59 % of the
+// issue slots, the rest waits for the shuffles of the mean and for loads (four
+// tokens' worth of heads in flight a warp; deeper loads cost registers and lose).
 #include <algorithm>
 
 #include "common.cuh"
@@ -288,8 +294,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   put_heads(p, ty, h, t, w, raw);
 }
 
-// Many tokens: a half-warp takes its token's heads kStep at a time, the next in
-// flight.
+// Many tokens: a half-warp takes all heads of its token, kStep at a time, the next
+// in flight: positions, angles and addresses are worked out once a token (a head a
+// CTA: 60 us where this takes 44; kStep 4 at 5 or 6 CTAs an SM 48 and 51; the heads
+// shared by two or four half-warps 49 and 55).
 constexpr int kStep = 2;
 __global__ void __launch_bounds__(kThreads, 8) norm_rope_token_kernel(const __grid_constant__ NormRopeParams p) {
   pdl_wait();

@@ -13,6 +13,11 @@
 // blocks by a binary search in the tile's sums.  The scan is repeated by
 // every CTA, which costs less than a second launch as long as the requests
 // fit a few tiles; the loads of up to 1024 requests are one round trip.
+// Measured: 1 request 2.5 us and 64 with four 4096-token chunks 3.3 us, a launch and
+// two round trips; 4112 requests with 135 184 tokens 10.6 us, most of it the five
+// tiles' chain of loads, shuffles and barriers (the bytes are worth 0.34 us).  Tiles
+// twice as wide, in CTAs of 512 or 1024 threads: 10.5 and 11.7 us there, 2.7 and 4.1
+// for 1 request.
 // Sums saturate at 2^31 - 1 (saturating addition of non-negative numbers is
 // associative, so the scan's order does not matter).
 #include <algorithm>
