@@ -16,11 +16,11 @@
 // maxima are shuffles within 16 and 4 lanes).  A half-warp takes one token; the
 // head's type and number are the same for a whole warp.
 //
-// Measured: 1 token 1.9 us (a launch); 16456 tokens of 16 + 1 + 1 + 1 + 1 heads, bf16
-// queries and fp8 caches, 44 us for 167 MB: 3.8 TB/s, 57 % of the copy rate.  There
-// issue bounds it: some 50 warp instructions for two tokens' heads, 59 % of the
-// issue slots, the rest waits for the shuffles of the mean and for loads (four
-// tokens' worth of heads in flight a warp; deeper loads cost registers and lose).
+// Measured: 1 token 2.0 us (a launch); 16456 tokens of 16 + 1 + 1 + 1 + 1 heads, bf16
+// queries and fp8 caches, 42 us for 167 MB: 3.9 TB/s, 59 % of the copy rate.  There
+// issue bounds it: some 200 warp instructions for a head of two tokens (unpacking,
+// the shuffles of the mean and of the rotation's partners, packing, the caches'
+// layouts) at 67 % of the issue slots, the rest waits for shuffles and loads.
 #include <algorithm>
 
 #include "common.cuh"
@@ -220,22 +220,34 @@ __device__ __forceinline__ void load_heads(const NormRopeParams& p, int ty, int 
     raw[i] = h0 + i < p.heads[ty] ? *reinterpret_cast<const uint4*>(src + i * kDim) : make_uint4(0, 0, 0, 0);
 }
 
-// heads h0 .. of type ty: norm, rotation, stores.  The type and head are the
+// What the heads of one type share.
+struct Type {
+  int ty, heads;
+  bool normed, bf16, cached;
+  uint8_t* out;  // the lane's place in head 0, NULL: none
+};
+__device__ __forceinline__ Type type_of(const NormRopeParams& p, int ty, const Token& t) {
+  Type a;
+  a.ty = ty, a.heads = p.heads[ty];
+  a.normed = ty != kHeadV, a.bf16 = p.out_dtype[ty] == BSP_BF16;
+  a.cached = ty == kHeadIdxK ? p.cache.idx_base != nullptr : (ty == kHeadK || ty == kHeadV) && p.cache.k_base;
+  a.out = static_cast<uint8_t*>(p.out[ty]);
+  if (!t.live) a.out = nullptr;
+  if (a.out) a.out += (t.token * a.heads * kDim + 8 * t.l) * (a.bf16 ? 2 : 1);
+  return a;
+}
+
+// heads h0 .. of a type: norm, rotation, stores.  The type and head are the
 // same for the whole warp.
 template <int kHeads>
-__device__ __forceinline__ void put_heads(const NormRopeParams& p, int ty, int h0, const Token& t, const float (&w)[8],
-                                          const uint4 (&raw)[kHeads]) {
-  const int heads = p.heads[ty];
-  const bool normed = ty != kHeadV, bf16 = p.out_dtype[ty] == BSP_BF16;
-  const bool cached = ty == kHeadIdxK ? p.cache.idx_base != nullptr : (ty == kHeadK || ty == kHeadV) && p.cache.k_base;
-  uint8_t* out = static_cast<uint8_t*>(p.out[ty]);
-  if (out) out += ((t.token * heads + h0) * kDim + 8 * t.l) * (bf16 ? 2 : 1);
+__device__ __forceinline__ void put_heads(const NormRopeParams& p, const Type& a, int h0, const Token& t,
+                                          const float (&w)[8], const uint4 (&raw)[kHeads]) {
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
-    if (h0 + i >= heads) break;
+    if (h0 + i >= a.heads) break;
     float x[8];
     unpack8(raw[i], x);
-    if (normed) {
+    if (a.normed) {
       float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) s2 = ffma2({x[j], x[j + 1]}, {x[j], x[j + 1]}, s2);
@@ -266,13 +278,13 @@ __device__ __forceinline__ void put_heads(const NormRopeParams& p, int ty, int h
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = 0.f;
     }
-    if (out && t.live) {
-      if (bf16)
-        *reinterpret_cast<uint4*>(out + i * kDim * 2) = pack8_bf16(x);
+    if (a.out) {
+      if (a.bf16)
+        *reinterpret_cast<uint4*>(a.out + (h0 + i) * (kDim * 2)) = pack8_bf16(x);
       else
-        *reinterpret_cast<uint2*>(out + i * kDim) = pack8_e4m3(x);
+        *reinterpret_cast<uint2*>(a.out + (h0 + i) * kDim) = pack8_e4m3(x);
     }
-    if (cached) store_cached(p, ty, h0 + i, t.slot, t.live && !t.pad && t.slot >= 0, t.l, x);
+    if (a.cached) store_cached(p, a.ty, h0 + i, t.slot, t.live && !t.pad && t.slot >= 0, t.l, x);
   }
 }
 
@@ -291,38 +303,42 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   load_heads(p, ty, h, t, raw);
   float w[8];
   load_weights(p, ty, t.l, w);
-  put_heads(p, ty, h, t, w, raw);
+  put_heads(p, type_of(p, ty, t), h, t, w, raw);
 }
 
 // Many tokens: a half-warp takes all heads of its token, kStep at a time, the next
-// in flight: positions, angles and addresses are worked out once a token (a head a
-// CTA: 60 us where this takes 44; kStep 4 at 5 or 6 CTAs an SM 48 and 51; the heads
-// shared by two or four half-warps 49 and 55).
+// in flight: positions, angles and addresses are worked out once a token.  (16456
+// tokens, us: a head a CTA 60; kStep 1, 2 at 7 CTAs an SM 47, 42; kStep 2 at 5, 6 and
+// 8 CTAs 48, 49, 48; the heads shared by two or four half-warps 49, 55.)
 constexpr int kStep = 2;
-__global__ void __launch_bounds__(kThreads, 8) norm_rope_token_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, 7) norm_rope_token_kernel(const __grid_constant__ NormRopeParams p) {
   pdl_wait();
   pdl_trigger();
   const Token t = load_token(p, static_cast<int64_t>(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 4));
-  int ty = -1, nty = 0, nh = -kStep;
-  auto advance = [&]() {  // (nty, nh): a step on, kHeadTypes at the end
-    nh += kStep;
-    while (nty < kHeadTypes && nh >= p.heads[nty]) ++nty, nh = 0;
-  };
-  advance();
+  // (type nty, head nh): the step whose loads are in flight
+  int nty = 0, nh = 0;
+  while (nty < kHeadTypes && p.heads[nty] == 0) ++nty;
   uint4 next[kStep];
-  if (nty < kHeadTypes) load_heads(p, nty, nh, t, next);
+  if (nty < kHeadTypes) load_heads(p, nty, 0, t, next);
   float w[8];
 #pragma unroll 1
   while (nty < kHeadTypes) {
-    if (nty != ty) load_weights(p, nty, t.l, w);
-    const int h = nh;
-    ty = nty;
-    uint4 raw[kStep];
+    const Type a = type_of(p, nty, t);
+    load_weights(p, nty, t.l, w);
+#pragma unroll 1
+    for (int h = 0; h < a.heads; h += kStep) {
+      uint4 raw[kStep];
 #pragma unroll
-    for (int i = 0; i < kStep; ++i) raw[i] = next[i];
-    advance();
-    if (nty < kHeadTypes) load_heads(p, nty, nh, t, next);
-    put_heads(p, ty, h, t, w, raw);
+      for (int i = 0; i < kStep; ++i) raw[i] = next[i];
+      nh = h + kStep;
+      if (nh >= a.heads) {
+        nh = 0;
+        do ++nty;
+        while (nty < kHeadTypes && p.heads[nty] == 0);
+      }
+      if (nty < kHeadTypes) load_heads(p, nty, nh, t, next);
+      put_heads(p, a, h, t, w, raw);
+    }
   }
 }
 
@@ -334,8 +350,8 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t 
   if (total == 0 || p.num_tokens == 0) return cudaSuccess;
   const int64_t groups = (static_cast<int64_t>(p.num_tokens) + kThreads / 16 - 1) / (kThreads / 16);
   // all heads of a token in one half-warp once that gives each SM three CTAs
-  // (measured at 24 heads: 10.2 and 14.5 us at 2048 tokens, 17.8 and 17.2 at 4096,
-  // 35.1 and 26.9 at 8192, 85.5 and 44.2 at 16456)
+  // (measured at 20 heads: 9.9 and 13.7 us at 2048 tokens, 17.1 and 16.2 at 4096,
+  // 34.0 and 22.8 at 8192, 80.5 and 42.5 at 16456)
   const bool many = groups >= static_cast<int64_t>(num_sms) * 3;
   const cudaError_t e =
       many ? launch_kernel(norm_rope_token_kernel, dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s, 0, p)
