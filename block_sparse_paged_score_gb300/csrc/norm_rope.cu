@@ -18,9 +18,9 @@
 //
 // Measured: 1 token 2.0 us (a launch); 16456 tokens of 16 + 1 + 1 + 1 + 1 heads, bf16
 // queries and fp8 caches, 42 us for 167 MB: 3.9 TB/s, 59 % of the copy rate.  There
-// issue bounds it: some 200 warp instructions for a head of two tokens (unpacking,
+// issue bounds it: 190 warp instructions for a head of two tokens (unpacking,
 // the shuffles of the mean and of the rotation's partners, packing, the caches'
-// layouts) at 67 % of the issue slots, the rest waits for shuffles and loads.
+// layouts) at 65 % of the issue slots, the rest waits for shuffles and loads.
 #include <algorithm>
 
 #include "common.cuh"
