@@ -172,9 +172,26 @@ def _io_ptr(t):
     return t.data_ptr()
 
 
+class _Current:
+    """The current stream's handle and device (torch.cuda.current_stream() takes
+    longer than everything else the binding does for a small call)."""
+    __slots__ = ("cuda_stream", "device")
+    raw = staticmethod(getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                       (lambda index: torch.cuda.current_stream(index).cuda_stream))
+    devices = {}
+
+    def __init__(self):
+        index = torch.cuda.current_device()
+        self.cuda_stream = self.raw(index)
+        self.device = self.devices.get(index) or self.devices.setdefault(index, torch.device("cuda", index))
+
+
+def _on(stream):
+    return stream if stream is not None else _Current()
+
+
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    return C.c_void_p(_on(stream).cuda_stream)
 
 
 def launch_count():
@@ -405,7 +422,7 @@ def norm_rope_write(args, stream=None):
 def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream=None):
     """Cached tokens by slot as bf16 rows: (k, v, idx_k), k and v of the K/V
     cache `kv`, idx_k of the index cache `idx`; either cache may be None."""
-    s = stream if stream is not None else torch.cuda.current_stream()
+    s = _on(stream)
     dev = s.device
     T = slot.numel()
     if kv is not None:
@@ -445,7 +462,7 @@ def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, 
                     ws=None, dev_err=None, stream=None):
     """Attention of each row over its whole context in an MXFP4 cache
     (bsp_dense_pa_decode); q [tokens, num_q_heads, 128], rows = tokens * Hkv."""
-    s = stream if stream is not None else torch.cuda.current_stream()
+    s = _on(stream)
     dev, i32 = s.device, torch.int32
     rows, hkv = row_len.numel(), kv.num_kv_heads
     n = rows // hkv * num_q_heads * 128

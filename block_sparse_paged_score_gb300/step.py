@@ -242,7 +242,7 @@ class StepTables:
         """int32 lengths [num_seqs] before the step and of the step, the free
         block ids, and how many of them were taken before (a device scalar;
         None: 0); fills the outputs."""
-        s = stream if stream is not None else torch.cuda.current_stream()
+        s = bsp._on(stream)
         a, i32, dev = self.args, torch.int32, s.device
         if self.seq_lens.device != dev:
             raise ValueError(f"the tables are on {self.seq_lens.device}, the stream on {dev}")
@@ -296,7 +296,7 @@ class NormRopeWrite:
         apart; idx_q and idx_k None without an index cache), int32 positions
         and int64 slots [T]; returns the queries and index queries (views of
         the object's buffers)."""
-        s = stream if stream is not None else torch.cuda.current_stream()
+        s = bsp._on(stream)
         a, dev, rows = self.args, self.device, bsp._head_rows
         T = q.shape[0]
         if T > self.max_tokens:
