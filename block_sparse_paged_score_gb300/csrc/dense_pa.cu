@@ -629,9 +629,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     mbar_fence_init();
   }
   pdl_wait();
-  pdl_trigger();
   // TMEM only after the wait: a CTA that held columns while it waited could
-  // keep the kernel before it from getting its own
+  // keep the kernel before it from getting its own.  And the next kernel's CTAs
+  // come (at the trigger below) only once this one has got its columns.
   if (warp == kCompute) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      base + S::misc + 16),
@@ -639,51 +639,39 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
 
-  // the groups' blocks, kThreads groups at a time: first their sum, then the
-  // group the share starts in
+  // The groups' blocks: a thread sums those of some neighbouring groups, and the
+  // one whose groups hold the share's start looks through them again.
   const int sub = blockIdx.x % p.subs, turn = blockIdx.x / p.subs;
-  int64_t total = 0, at = 0, share = 0;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t sum = 0;
-#pragma unroll 1
-    for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
-      const int g = g0 + tid;
-      const int nb = g < p.groups ? blocks_of(a, group_len(a, g, 0, 1)) : 0;
-      int64_t x = nb;
+  const int per = (p.groups + kThreads - 1) / kThreads;
+  const int g_lo = static_cast<int>(min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(p.groups)));
+  const int g_hi = min(g_lo + per, p.groups);
+  int64_t mine = 0;
+#pragma unroll 4
+  for (int g = g_lo; g < g_hi; ++g) mine += blocks_of(a, group_len(a, g, 0, 1));
+  int64_t upto = mine;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_sum[warp] = x;
-      __syncthreads();
-      int64_t before = sum;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += y;
+  }
+  if (lane == 31) s_sum[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
 #pragma unroll 1
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += s_sum[w];
-        sum += s_sum[w];
-      }
-      const int64_t c1 = before + x, c0 = c1 - nb;  // blocks before and up to group g
-      if (pass == 0 && p.groups <= kThreads) {  // one tile: the sum and the start at once
-        total = sum;
-        share = (total * a.hkv + p.shares - 1) / p.shares;
-        at = turn * share;
-      }
-      if ((pass == 1 || p.groups <= kThreads) && nb && c0 * a.hkv <= at && at < c1 * a.hkv)
-        s_start[0] = g, s_start[1] = c0, s_start[2] = nb;
-      if (pass == 1 && sum * a.hkv > at) break;
-    }
-    if (pass == 0) {
-      total = sum;
-      share = (total * a.hkv + p.shares - 1) / p.shares;
-      at = turn * share;
-      if (p.groups <= kThreads) break;
-    }
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) upto += s_sum[w];
+    total += s_sum[w];
+  }
+  const int64_t share = (total * a.hkv + p.shares - 1) / p.shares, at = turn * share;
+  if ((upto - mine) * a.hkv <= at && at < upto * a.hkv) {
+    int64_t c = upto - mine;
+    int g = g_lo, nb = blocks_of(a, group_len(a, g, 0, 1));
+    while (at >= (c + nb) * a.hkv) c += nb, nb = blocks_of(a, group_len(a, ++g, 0, 1));
+    s_start[0] = g, s_start[1] = c, s_start[2] = nb;
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  pdl_trigger();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = __shfl_sync(0xffffffffu, misc[4], 0);
   Walk w;
