@@ -303,6 +303,9 @@ class NormRopeWrite:
             raise ValueError(f"{T} tokens, the buffers hold {self.max_tokens}")
         if s.device != dev:
             raise ValueError(f"the buffers are on {dev}, the stream on {s.device}")
+        has_idx_q = idx_q is not None and self.idx_q_out is not None
+        if T == 0:  # (empty tensors have no address)
+            return self.q_out[:0], self.idx_q_out[:0] if has_idx_q else None
         hq, hkv, hidx = self.heads
         a.num_tokens = T
         a.q, a.q_stride = rows("q", q, T, hq, dev)
@@ -312,7 +315,6 @@ class NormRopeWrite:
         a.idx_k, a.idx_k_stride = rows("idx_k", idx_k, T, hidx, dev)
         a.positions = bsp._dense("positions", positions, torch.int32, dev, T)
         a.slot = bsp._dense("slot", slot, torch.int64, dev, T)
-        has_idx_q = idx_q is not None and self.idx_q_out is not None
         a.idx_q_out = self.idx_q_out.data_ptr() if has_idx_q else None
         bsp.norm_rope_write(a, s)
         if T == self.max_tokens:

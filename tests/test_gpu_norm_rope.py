@@ -292,3 +292,11 @@ def test_without_a_kv_cache_without_an_index_cache_and_keys_as_rows(T):
     y, mag = c.want("k")
     _near(bf16_to_f64(k_out[:T].view(torch.int16).cpu().numpy().view(np.uint16)), y, 2.0 ** -8 * np.abs(y) + SLACK * mag, "k")
     assert (k_out[T:] == 7).all()
+
+
+def test_no_tokens():
+    c = Case(5, 1, 4, MX, FP8, 64)
+    x, pos, slot = c.x, c.pos.cuda(), c.slot.cuda()
+    q, iq = c.op.run(x["q"][:0], x["k"][:0], x["v"][:0], x["idx_q"][:0], x["idx_k"][:0], pos[:0], slot[:0])
+    assert q.shape == (0, 4, 128) and iq.shape == (0, 1, 128)
+    assert not c.kv.buffer.any() and not c.idx.buffer.any()
