@@ -47,8 +47,8 @@
 // of 2^kBias f16's range, down to 2^-25, reaches 2^-32 of the row's largest.  z, m,
 // l and O are fp32.  The sums l are those of the unrounded weights.
 //
-// Measured (64 requests x 131072 tokens, 16 rows: 1.14 GB): 226 us, 5.1 TB/s; 128 x
-// 32768 with 64 rows: 0.57 GB in 231 us.  What bounds it is instruction issue and
+// Measured (64 requests x 131072 tokens, 16 rows: 1.14 GB): 225 us, 5.1 TB/s; 128 x
+// 32768 with 64 rows: 0.57 GB in 227 us.  What bounds it is instruction issue and
 // the chain of a block through a CTA (wait, logits, vote, exponentials, V's
 // conversion, fences), which four CTAs an SM (two of 64 rows) overlap: 2 500 warp
 // instructions a block of 16 rows, 1 000 of them V's conversion, at 67 % of the
@@ -699,6 +699,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     const uint32_t q_full = base + B::q_full, bad_at = base + S::misc;
     const uint64_t k_desc = smem_desc_sw128(base), q_desc = smem_desc_sw128(base + S::q);
     const int limit = static_cast<int>(min(a.num_blocks, int64_t{0x7FFFFFFF}));
+    const int bad_id = max(limit, 1);  // outside the map, which has a block at least: its copies write zeros
     // scales of tokens 32j + lane in K's unpacked rows 128..: 16 tokens a row, two an
     // 8-byte piece, each piece in a 16-byte chunk at j ^ (row % 8)
     uint32_t from[4];
@@ -711,8 +712,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     int left = 0, at_id = 32, head = 0;  // blocks left of the piece, the next one's lane in ids
     int32_t ids = 0;
     bool done = false;
-    // the next blocks to be multiplied: id (limit: a bad one, out of the map's
-    // range: its copies write zeros; kNone: none) and head (~head: the first of its piece)
+    // the next blocks to be multiplied: id (kNone: none) and head (~head: the first of its piece)
     constexpr int kNone = -1;
     int q_id[kAhead + 1], q_head[kAhead + 1];
     uint32_t vst = 0, v_phase = 1;  // of the next V load (an empty stage's wait passes at once)
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         ids = lane < left ? table[lane] : 0;
         if (static_cast<uint32_t>(ids) >= static_cast<uint32_t>(limit)) {
           set_err(a.err, BSP_DEVERR_BLOCK_ID);
-          ids = limit;
+          ids = bad_id;
         }
         table += 32, at_id = 0;
       }
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     auto load_v = [&](int id, int hd) {
       if (alive) alive = wait_warp(v_empty + 8 * vst, v_phase, a.err);
       const uint32_t bar = v_full + 8 * vst;
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(bad_at + 4 * vst), "r"(static_cast<uint32_t>(id == limit)) : "memory");
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(bad_at + 4 * vst), "r"(static_cast<uint32_t>(id == bad_id)) : "memory");
       __syncwarp();
       arrive_expect(bar, kMxField);
       tile_g2s(base + S::v + vst * kVTile, &map_v, hd ^ (hd >> 31), id, bar);

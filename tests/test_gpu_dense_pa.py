@@ -404,3 +404,22 @@ def test_calls_of_other_sizes_in_one_workspace_one_after_another():
     for _ in range(3):
         for c, w in zip(cases, want):
             assert torch.equal(c.call(ws=ws), w)
+
+
+def test_no_rows():
+    c = Case([300], seed=27).device()
+    c.dq, c.dseq, c.dlen = c.dq[:0], c.dseq[:0], c.dlen[:0]
+    assert c.call().shape == (0, 16, 128) and c.err.item() == 0
+
+
+def test_many_short_requests():
+    """More units than CTAs, and groups than a CTA has threads."""
+    r = np.random.default_rng(28)
+    _close(Case([int(x) for x in r.integers(0, 400, 1500)], group=16, seed=28))
+    _close(Case([int(x) for x in r.integers(0, 300, 700)], group=8, q_len=4, seed=29))
+
+
+def test_a_cache_of_no_blocks():
+    c = Case([300, 0], q_len=2, seed=30).device()
+    c.kv.desc.num_blocks = 0
+    assert not c.call().any() and c.err.item() == 2
