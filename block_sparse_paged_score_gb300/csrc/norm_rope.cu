@@ -17,11 +17,12 @@
 // head's type and number are the same for a whole warp.
 //
 // Measured: 1 token 2.0 us (a launch); 16456 tokens of 16 + 1 + 1 + 1 + 1 heads, bf16
-// queries and fp8 caches, 42 us for 167 MB: 3.9 TB/s, 59 % of the copy rate.  There
-// issue bounds it: 190 warp instructions for a head of two tokens (unpacking,
-// the shuffles of the mean and of the rotation's partners, packing, the caches'
-// layouts) at 65 % of the issue slots, the rest waits for shuffles and loads.
+// queries and fp8 caches, 42 us for 167 MB: 4.0 TB/s, 60 % of the copy rate.  There
+// the latency of loads and of shuffles (the mean's, the rotation's partners') bounds
+// it, beside 160 warp instructions for a head of two tokens at 57 % of the issue
+// slots; fewer instructions (190, 65 %) or loads further ahead did not shorten it.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "encode.cuh"
@@ -237,9 +238,38 @@ __device__ __forceinline__ Type type_of(const NormRopeParams& p, int ty, const T
   return a;
 }
 
+// norm, weight and rotation of a head
+template <bool PAIRS>
+__device__ __forceinline__ void norm_rotate(const NormRopeParams& p, const Token& t, const float (&w)[8], float (&x)[8]) {
+  float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) s2 = ffma2({x[j], x[j + 1]}, {x[j], x[j + 1]}, s2);
+  float ss = s2.x + s2.y;
+#pragma unroll
+  for (int m = 1; m < 16; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+  const float inv = rsqrtf(fmaf(ss, 1.f / kDim, p.eps));
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 y = fmul2(fmul2({x[j], x[j + 1]}, {inv, inv}), {w[j], w[j + 1]});
+    x[j] = y.x, x[j + 1] = y.y;
+  }
+  if (p.rot_dim) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = PAIRS ? x[j ^ 1] : __shfl_sync(0xffffffffu, x[j], t.partner);
+    if (t.turns) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float2 z = ffma2({x[j], x[j + 1]}, {t.cs[j], t.cs[j + 1]}, fmul2({y[j], y[j + 1]}, {t.sn[j], t.sn[j + 1]}));
+        x[j] = z.x, x[j + 1] = z.y;
+      }
+    }
+  }
+}
+
 // heads h0 .. of a type: norm, rotation, stores.  The type and head are the
-// same for the whole warp.
-template <int kHeads>
+// same for the whole warp.  QUERY: neither V nor cached.
+template <bool PAIRS, bool QUERY, int kHeads>
 __device__ __forceinline__ void put_heads(const NormRopeParams& p, const Type& a, int h0, const Token& t,
                                           const float (&w)[8], const uint4 (&raw)[kHeads]) {
 #pragma unroll
@@ -247,33 +277,7 @@ __device__ __forceinline__ void put_heads(const NormRopeParams& p, const Type& a
     if (h0 + i >= a.heads) break;
     float x[8];
     unpack8(raw[i], x);
-    if (a.normed) {
-      float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) s2 = ffma2({x[j], x[j + 1]}, {x[j], x[j + 1]}, s2);
-      float ss = s2.x + s2.y;
-#pragma unroll
-      for (int m = 1; m < 16; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      const float inv = rsqrtf(fmaf(ss, 1.f / kDim, p.eps));
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float2 y = fmul2(fmul2({x[j], x[j + 1]}, {inv, inv}), {w[j], w[j + 1]});
-        x[j] = y.x, x[j + 1] = y.y;
-      }
-      if (p.rot_dim) {
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = p.rope_pairs ? x[j ^ 1] : __shfl_sync(0xffffffffu, x[j], t.partner);
-        if (t.turns) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const float2 z =
-                ffma2({x[j], x[j + 1]}, {t.cs[j], t.cs[j + 1]}, fmul2({y[j], y[j + 1]}, {t.sn[j], t.sn[j + 1]}));
-            x[j] = z.x, x[j + 1] = z.y;
-          }
-        }
-      }
-    }
+    if (QUERY || a.normed) norm_rotate<PAIRS>(p, t, w, x);
     if (t.pad) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = 0.f;
@@ -284,12 +288,13 @@ __device__ __forceinline__ void put_heads(const NormRopeParams& p, const Type& a
       else
         *reinterpret_cast<uint2*>(a.out + (h0 + i) * kDim) = pack8_e4m3(x);
     }
-    if (a.cached) store_cached(p, a.ty, h0 + i, t.slot, t.live && !t.pad && t.slot >= 0, t.l, x);
+    if (!QUERY && a.cached) store_cached(p, a.ty, h0 + i, t.slot, t.live && !t.pad && t.slot >= 0, t.l, x);
   }
 }
 
 // Few tokens: a CTA takes one head of eight tokens (latency: everything is in
 // flight at once).
+template <bool PAIRS>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p, unsigned total) {
   pdl_wait();
   pdl_trigger();
@@ -303,41 +308,60 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   load_heads(p, ty, h, t, raw);
   float w[8];
   load_weights(p, ty, t.l, w);
-  put_heads(p, type_of(p, ty, t), h, t, w, raw);
+  put_heads<PAIRS, false>(p, type_of(p, ty, t), h, t, w, raw);
 }
 
 // Many tokens: a half-warp takes all heads of its token, kStep at a time, the next
-// in flight: positions, angles and addresses are worked out once a token.  (16456
-// tokens, us: a head a CTA 60; kStep 1, 2 at 7 CTAs an SM 47, 42; kStep 2 at 5, 6 and
-// 8 CTAs 48, 49, 48; the heads shared by two or four half-warps 49, 55.)
+// in flight: positions, angles and addresses are worked out once a token, and query
+// heads go through a loop of their own.  (16456 tokens, us: a head a CTA 60; kStep 2
+// at 5, 6, 7 and 8 CTAs an SM 47, 47, 42, 45; kStep 1 and 4 47; the heads shared by
+// two or four half-warps 49, 55.  40000 tokens: 92, with loads two steps ahead 97.)
 constexpr int kStep = 2;
+template <bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 7) norm_rope_token_kernel(const __grid_constant__ NormRopeParams p) {
   pdl_wait();
   pdl_trigger();
   const Token t = load_token(p, static_cast<int64_t>(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 4));
-  // (type nty, head nh): the step whose loads are in flight
-  int nty = 0, nh = 0;
-  while (nty < kHeadTypes && p.heads[nty] == 0) ++nty;
+  // the loads, a step before their use: type lty, `left` of its heads from src on
+  int lty = -1, left = 0;
+  const uint16_t* src = nullptr;
+  auto fetch = [&](uint4 (&to)[kStep]) {
+    if (left <= 0) {
+      do ++lty;
+      while (lty < kHeadTypes && p.heads[lty] == 0);
+      if (lty >= kHeadTypes) {
+        lty = kHeadTypes - 1;  // (nothing more)
+        return;
+      }
+      left = p.heads[lty];
+      src = p.src[lty] + t.token * p.stride[lty] + 8 * t.l;
+    }
+#pragma unroll
+    for (int i = 0; i < kStep; ++i)
+      if (i < left) to[i] = *reinterpret_cast<const uint4*>(src + i * kDim);
+    left -= kStep, src += kStep * kDim;
+  };
   uint4 next[kStep];
-  if (nty < kHeadTypes) load_heads(p, nty, 0, t, next);
+  fetch(next);
   float w[8];
 #pragma unroll 1
-  while (nty < kHeadTypes) {
-    const Type a = type_of(p, nty, t);
-    load_weights(p, nty, t.l, w);
-#pragma unroll 1
-    for (int h = 0; h < a.heads; h += kStep) {
+  for (int ty = 0; ty < kHeadTypes; ++ty) {
+    if (p.heads[ty] == 0) continue;
+    const Type a = type_of(p, ty, t);
+    load_weights(p, ty, t.l, w);
+    auto step = [&](int h, auto query) {
       uint4 raw[kStep];
 #pragma unroll
       for (int i = 0; i < kStep; ++i) raw[i] = next[i];
-      nh = h + kStep;
-      if (nh >= a.heads) {
-        nh = 0;
-        do ++nty;
-        while (nty < kHeadTypes && p.heads[nty] == 0);
-      }
-      if (nty < kHeadTypes) load_heads(p, nty, nh, t, next);
-      put_heads(p, a, h, t, w, raw);
+      fetch(next);
+      put_heads<PAIRS, query>(p, a, h, t, w, raw);
+    };
+    if (a.normed && !a.cached) {
+#pragma unroll 1
+      for (int h = 0; h < a.heads; h += kStep) step(h, std::true_type{});
+    } else {
+#pragma unroll 1
+      for (int h = 0; h < a.heads; h += kStep) step(h, std::false_type{});
     }
   }
 }
@@ -350,13 +374,16 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t 
   if (total == 0 || p.num_tokens == 0) return cudaSuccess;
   const int64_t groups = (static_cast<int64_t>(p.num_tokens) + kThreads / 16 - 1) / (kThreads / 16);
   // all heads of a token in one half-warp once that gives each SM three CTAs
-  // (measured at 20 heads: 9.9 and 13.7 us at 2048 tokens, 17.1 and 16.2 at 4096,
-  // 34.0 and 22.8 at 8192, 80.5 and 42.5 at 16456)
+  // (measured at 20 heads: 9.9 and 13.7 us at 2048 tokens, 17.1 and 15.0 at 4096,
+  // 34.0 and 20.8 at 8192, 80.5 and 42.1 at 16456)
   const bool many = groups >= static_cast<int64_t>(num_sms) * 3;
-  const cudaError_t e =
-      many ? launch_kernel(norm_rope_token_kernel, dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s, 0, p)
-           : launch_kernel(norm_rope_kernel, dim3(static_cast<unsigned>(groups * total)), dim3(kThreads), 0, s, 0, p,
-                           static_cast<unsigned>(total));
+  auto launch = [&](auto pairs) {
+    return many ? launch_kernel(norm_rope_token_kernel<pairs>, dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s,
+                                0, p)
+                : launch_kernel(norm_rope_kernel<pairs>, dim3(static_cast<unsigned>(groups * total)), dim3(kThreads), 0,
+                                s, 0, p, static_cast<unsigned>(total));
+  };
+  const cudaError_t e = p.rope_pairs ? launch(std::true_type{}) : launch(std::false_type{});
   return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
