@@ -238,7 +238,9 @@ __device__ __forceinline__ Type type_of(const NormRopeParams& p, int ty, const T
   return a;
 }
 
-// norm, weight and rotation of a head
+// norm, weight and rotation of a head.  The weight (of bf16 values, exact or nearly)
+// and the rotation come first: neither waits for the mean, and the one factor at the
+// end rounds once.
 template <bool PAIRS>
 __device__ __forceinline__ void norm_rotate(const NormRopeParams& p, const Token& t, const float (&w)[8], float (&x)[8]) {
   float2 s2 = make_float2(0.f, 0.f);
@@ -247,10 +249,10 @@ __device__ __forceinline__ void norm_rotate(const NormRopeParams& p, const Token
   float ss = s2.x + s2.y;
 #pragma unroll
   for (int m = 1; m < 16; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-  const float inv = rsqrtf(fmaf(ss, 1.f / kDim, p.eps));
+  const float inv = __frsqrt_rn(fmaf(ss, 1.f / kDim, p.eps));
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const float2 y = fmul2(fmul2({x[j], x[j + 1]}, {inv, inv}), {w[j], w[j + 1]});
+    const float2 y = fmul2({x[j], x[j + 1]}, {w[j], w[j + 1]});
     x[j] = y.x, x[j + 1] = y.y;
   }
   if (p.rot_dim) {
@@ -264,6 +266,11 @@ __device__ __forceinline__ void norm_rotate(const NormRopeParams& p, const Token
         x[j] = z.x, x[j + 1] = z.y;
       }
     }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float2 y = fmul2({x[j], x[j + 1]}, {inv, inv});
+    x[j] = y.x, x[j + 1] = y.y;
   }
 }
 
