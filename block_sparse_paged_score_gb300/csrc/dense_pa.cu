@@ -277,11 +277,8 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t* err) {
-  if (__builtin_expect(test_wait(bar, parity), 1)) return true;
-  return wait_slow(bar, parity, err);
-}
-// the same for a converged warp, with one answer for all of its lanes
+// A converged warp waits, with one answer for all of its lanes, and comes out
+// converged (what follows are .aligned loads, stores and barriers).
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* err) {
   if (__builtin_expect(__all_sync(0xffffffffu, test_wait(bar, parity)), 1)) return true;
   return __all_sync(0xffffffffu, wait_slow(bar, parity, err));
@@ -881,7 +878,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     uint32_t round = 0;                                  // of PV
     uint32_t cur = 0;                                    // which reference maxima
     auto done = [&](uint32_t r) {  // round r - 1 has ended
-      if (r && alive) alive = wait_for(pv_done + 8 * ((r - 1) & 1), ((r - 1) >> 1) & 1, a.err);
+      if (r && alive) alive = wait_warp(pv_done + 8 * ((r - 1) & 1), ((r - 1) >> 1) & 1, a.err);
     };
     while (w.next(p, sub, lane)) {
       bar_sync(1, 32 * kCompute);  // the last unit's q, lengths and sums are no longer read
@@ -921,7 +918,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       for (int k = w.nblk; k > 0; --k, n0 += kBlock) {
         // after a timed-out wait the warp goes on without waits (the barriers need
         // every warp); its results are void
-        if (alive) alive = wait_for(v_full + 8 * vst, v_phase, a.err);
+        if (alive) alive = wait_warp(v_full + 8 * vst, v_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 + kBlock <= min_len;
         const uint32_t z = z_at + zb * N, voff = vst * kVTile;
@@ -986,6 +983,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         if (__builtin_expect(!in || !whole, 0)) in = exact();
         if (__builtin_expect(bad || !in, 0))
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(flags + (bad ? 4 : 0)), "r"(1u) : "memory");
+        __syncwarp();  // (lanes differ in `in`; the loads and the vote below are the whole warp's)
         // first pass: does a row's maximum grow?
         float top = -INFINITY;
 #pragma unroll
@@ -1016,6 +1014,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
               }
               const float mx = warp_reduce<CH>(y, lane, [](float u, float v) { return fmaxf(u, v); });
               if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, mx);
+              __syncwarp();
             }
           }
           bar_sync(1, 32 * kCompute);
@@ -1052,6 +1051,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll 1
             for (int i = 0; i < VT; i += 64)
               wide_words(cell_at + voff, n0 + vtok, max_len, word_at, quad, i, lens, nan_of, N);
+          __syncwarp();  // (its lanes' ways differ)
         }
         // second pass: the weights, and V as the MMA reads it.  Where V's scales
         // are beyond f16, both are bf16 and the weights go in two parts.
