@@ -57,9 +57,11 @@
 // register fragments, took 289 us and 536 us: V's conversion and the loads of P
 // were repeated for every 16 rows.
 //
-// Every wait for a copy or an MMA is bounded; after a timed-out wait a role
-// waits no more (the error word is set, the results are void), walks through its
-// blocks and the CTA frees its TMEM and returns.
+// Every wait for a copy or an MMA is bounded.  After a timed-out wait (the error word
+// is set, the results are void) the producer issues nothing more and waits, with a
+// limit again, for what it has under way; a compute warp walks through its blocks
+// without waits and arrives nowhere, so that the producer stops too.  Then the CTA
+// frees its TMEM and returns.
 #include <algorithm>
 #include <type_traits>
 
@@ -79,6 +81,13 @@ constexpr int kKTile = kKRows * 128, kVTile = (kVRows + 7) / 8 * 8 * 128;
 static_assert(kKRows * 64 == kMxField && kVRows * 128 == kMxField && kKTile % 1024 == 0);
 constexpr float kMaxGrow = 8.f;   // the reference maximum moves when a row's maximum grows by more (log2)
 constexpr float kBias = 7.f;      // weights are 2^(z - m + kBias): at most 2^15
+// rounds (of up to kSleepNs) before a wait gives up; a build may set fewer, to see what
+// a kernel whose waits run out leaves behind
+#ifdef BSP_DENSE_PA_WAIT_ROUNDS
+#define BSP_WAIT_ROUNDS (BSP_DENSE_PA_WAIT_ROUNDS)
+#else
+#define BSP_WAIT_ROUNDS kSleepWaitLimit
+#endif
 constexpr float kNoMax = -1e30f;  // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
 // V enters the MMA as v * 2^(scale byte - kVRef).  f16 holds that exactly for
 // bytes from kVLow to kVHigh (2^-17 to 2^7); see scale_words.
@@ -261,9 +270,9 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t* err) {
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t* err, uint32_t rounds) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kSleepWaitLimit; ++i)
+  for (uint32_t i = 0; i < rounds; ++i)
     if (try_wait(bar, parity)) return true;
   set_err(err, BSP_DEVERR_TIMEOUT);
   return false;
@@ -279,9 +288,10 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
 }
 // A converged warp waits, with one answer for all of its lanes, and comes out
 // converged (what follows are .aligned loads, stores and barriers).
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* err) {
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* err,
+                                          uint32_t rounds = BSP_WAIT_ROUNDS) {
   if (__builtin_expect(__all_sync(0xffffffffu, test_wait(bar, parity)), 1)) return true;
-  return __all_sync(0xffffffffu, wait_slow(bar, parity, err));
+  return __all_sync(0xffffffffu, wait_slow(bar, parity, err, rounds));
 }
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   uint64_t x, y, z, r;
@@ -739,8 +749,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       id = __shfl_sync(0xffffffffu, ids, at_id);
       ++at_id, --left;
     };
+    // (a wait that gives up ends the loop: nothing is issued after it)
+    auto ready = [&](uint32_t bar, uint32_t parity) { return alive = wait_warp(bar, parity, a.err); };
     auto load_v = [&](int id, int hd) {
-      if (alive) alive = wait_warp(v_empty + 8 * vst, v_phase, a.err);
+      if (!ready(v_empty + 8 * vst, v_phase)) return;
       const uint32_t bar = v_full + 8 * vst;
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(bad_at + 4 * vst), "r"(static_cast<uint32_t>(id == bad_id)) : "memory");
       __syncwarp();
@@ -749,7 +761,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
     };
     auto load_k = [&](int id, int hd) {
-      if (alive) alive = wait_warp(k_empty + 8 * kst, k_phase, a.err);
+      if (!ready(k_empty + 8 * kst, k_phase)) return;
       const uint32_t bar = k_full + 8 * kst;
       arrive_expect(bar, kMxField);
       tile_g2s(base + kst * kKTile, &map_k, hd ^ (hd >> 31), id, bar);
@@ -758,7 +770,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       learn(q_id[i], q_head[i]);
-      if (q_id[i] != kNone) {
+      if (q_id[i] != kNone) {  // (these stages are empty: no wait gives up)
         load_k(q_id[i], q_head[i]);
         if (i < kAheadV) load_v(q_id[i], q_head[i]);
       }
@@ -775,8 +787,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       uint32_t cmd = kMore;
       while (cmd & kMore) {
         const uint32_t b = round & 1;
-        if (alive) alive = wait_warp(base + B::pv_full + 8 * b, (round >> 1) & 1, a.err);
-        cmd = alive ? misc[5 + b] : +kNothing;
+        if (!ready(base + B::pv_full + 8 * b, (round >> 1) & 1)) return;
+        cmd = misc[5 + b];
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         // f32 += A (f16 or bf16, TMEM) B (the same, rows contiguous), M = 128
         const uint32_t id = (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24) |
@@ -798,14 +810,15 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       learn(q_id[kAhead], q_head[kAhead]);
       // PV of the block before the last; of all of them before another piece's q,
       // which comes once the piece's O has been read
-      while (behind > (q_head[0] < 0 ? 0 : 1)) {
+      while (alive && behind > (q_head[0] < 0 ? 0 : 1)) {
         multiply();
         --behind;
       }
+      if (!alive) break;
       ++behind;
       // K is there: its scales from token order to the cells tcgen05.cp reads,
       // lane i of column j = token 32j + i
-      if (alive) alive = wait_warp(k_full + 8 * mst, m_phase, a.err);
+      if (!ready(k_full + 8 * mst, m_phase)) break;
       const uint32_t off = mst * kKTile, cells = base + off + kBlock * 128;  // (in their own rows)
       const uint32_t cell[4] = {lds32(from[0] + off), lds32(from[1] + off), lds32(from[2] + off), lds32(from[3] + off)};
       __syncwarp();
@@ -813,10 +826,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       fence_proxy_async();
       __syncwarp();
       if (__builtin_expect(q_head[0] < 0, 0)) {
-        if (alive) alive = wait_warp(q_full, q_phase, a.err);
+        if (!ready(q_full, q_phase)) break;
         q_phase ^= 1;
       }
-      if (alive) alive = wait_warp(z_empty + 8 * buf, z_phase, a.err);
+      if (!ready(z_empty + 8 * buf, z_phase)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t sk = tmem + T::k + 4 * mst, z = tmem + T::z + buf * N;
       const uint64_t kd = k_desc + mst * (kKTile / 16);
@@ -831,17 +844,42 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       commit(k_empty + 8 * mst);
       commit(v_full + 8 * sst);
       if (++sst == S::kVStages) sst = 0;
-      if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);  // once the compute warps have left its stage
-      if (q_id[kAhead] != kNone) load_k(q_id[kAhead], q_head[kAhead]);     // once the MMAs that used it are done
       if (++mst == S::kKStages) mst = 0, m_phase ^= 1;
       if (++buf == T::kZ) buf = 0, z_phase ^= 1;
+      if (q_id[kAheadV] != kNone) load_v(q_id[kAheadV], q_head[kAheadV]);  // once the compute warps have left its stage
+      if (!alive) break;
+      if (q_id[kAhead] != kNone) load_k(q_id[kAhead], q_head[kAhead]);  // once the MMAs that used it are done
+      if (!alive) break;
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) q_id[j] = q_id[j + 1], q_head[j] = q_head[j + 1];
       __syncwarp();
     }
-    while (behind-- > 0) multiply();
-    // nothing may still write shared memory or TMEM when the CTA leaves
-    if (alive && round) wait_warp(base + B::pv_done + 8 * ((round - 1) & 1), ((round - 1) >> 1) & 1, a.err);
+    while (alive && behind-- > 0) multiply();
+    // Nothing may still write shared memory or TMEM when the CTA leaves.
+    auto settle = [&](uint32_t bar, uint32_t parity) { wait_warp(bar, parity, a.err, kSleepWaitLimit); };
+    if (round) settle(base + B::pv_done + 8 * ((round - 1) & 1), ((round - 1) >> 1) & 1);
+    if (__builtin_expect(!alive, 0)) {
+      // What a healthy end has waited for by now: the round before, the copies (a stage's
+      // last load is of this turn of the ring below the next load's, of the last turn
+      // from there on) and the commits of the logits.
+      if (round > 1) settle(base + B::pv_done + 8 * (round & 1), ((round - 2) >> 1) & 1);
+      // V's barriers take a copy and a commit a block; one of the two may have come alone
+      if (vst != sst) {
+        if (kAheadV > 0) {  // a block's V that no logits follow
+          commit(v_full + 8 * sst);
+        } else {  // logits that no V follows
+          if (lane == 0) arrive(v_full + 8 * vst);
+          if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
+        }
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < S::kVStages; ++i) settle(v_full + 8 * i, i < vst ? v_phase ^ 1 : v_phase);
+#pragma unroll
+      for (uint32_t i = 0; i < S::kKStages; ++i) {
+        settle(k_full + 8 * i, i < kst ? k_phase ^ 1 : k_phase);
+        settle(k_empty + 8 * i, i < mst ? m_phase : m_phase ^ 1);
+      }
+    }
     __syncwarp();
   } else {
     // ---- compute ----
@@ -909,15 +947,15 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         __syncwarp();
-        if (lane == 0) arrive(base + B::q_full);
+        if (lane == 0 && alive) arrive(base + B::q_full);
       }
       bool first = true;  // no PV round of the unit yet
       const int max_len = w.max_len, min_len = w.min_len;
       int n0 = w.b0 * kBlock;
 #pragma unroll 1
       for (int k = w.nblk; k > 0; --k, n0 += kBlock) {
-        // after a timed-out wait the warp goes on without waits (the barriers need
-        // every warp); its results are void
+        // after a timed-out wait the warp goes on without waits and arrivals (the
+        // barriers of the compute warps need every one); its results are void
         if (alive) alive = wait_warp(v_full + 8 * vst, v_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 + kBlock <= min_len;
@@ -963,7 +1001,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           }
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();  // the logits are read, V's factors written
-          if ((!wide || part) && lane == 0) arrive(z_empty + 8 * zb);
+          if ((!wide || part) && lane == 0 && alive) arrive(z_empty + 8 * zb);
           if (T::kV == 1) done(round);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           put_v<wide, VT>(vt_at + (T::kV == 2 ? b * 64 : 0), ld_at + voff, my_words);
@@ -973,7 +1011,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          if (lane == 0) arrive(pv_full + 8 * b);
+          if (lane == 0 && alive) arrive(pv_full + 8 * b);
           ++round;
         };
         // V's factors
@@ -1065,11 +1103,11 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           if (tid == 0) misc[5 + (round & 1)] = kNothing;
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          if (lane == 0) arrive(z_empty + 8 * zb), arrive(pv_full + 8 * (round & 1));
+          if (lane == 0 && alive) arrive(z_empty + 8 * zb), arrive(pv_full + 8 * (round & 1));
           ++round;
         }
         __syncwarp();
-        if (lane == 0) arrive(v_empty + 8 * vst);
+        if (lane == 0 && alive) arrive(v_empty + 8 * vst);
         if (++zb == T::kZ) zb = 0;
         if (++vst == S::kVStages) vst = 0, v_phase ^= 1;
       }
