@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Tensors are torch CUDA tensors; the stream is torch's current stream unless
-one is given.  A call whose library is missing raises -- there is no CPU
-fallback.
+one is given.  Outputs and workspaces that a call makes itself come from its
+stream's memory pool; whoever uses such an output on another stream orders the
+two, as for any tensor made on a side stream.  A call whose library is missing
+raises -- there is no CPU fallback.
 """
 import ctypes as C
 import math
@@ -194,6 +196,17 @@ def _stream(stream):
     return C.c_void_p(_on(stream).cuda_stream)
 
 
+def _new(shape, dtype, device, stream, zeroed=False):
+    """A buffer of a call's own.  From the pool of the stream the call runs on:
+    memory of another stream's could still be in use there, and could be
+    handed out there again while the call runs."""
+    make = torch.zeros if zeroed else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def launch_count():
     return int(lib().bsp_launch_count())
 
@@ -240,15 +253,15 @@ def kv_page_write(kv, idx, k, v, idx_k, slot, dev_err=None, stream=None):
 
 
 def cast_e4m3(x, out=None, stream=None):
-    out = out if out is not None else torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    out = out if out is not None else _new(x.shape, torch.uint8, x.device, stream)
     _check("bsp_cast_e4m3", lib().bsp_cast_e4m3(_io_ptr(x), _io_ptr(out), x.numel(), _stream(stream)))
     return out
 
 
 def row_lengths_decode(seq_lens, q_len, num_heads, row_seq=None, row_len=None, stream=None):
     rows = seq_lens.numel() * q_len * num_heads
-    row_seq = row_seq if row_seq is not None else torch.empty(rows, dtype=torch.int32, device=seq_lens.device)
-    row_len = row_len if row_len is not None else torch.empty(rows, dtype=torch.int32, device=seq_lens.device)
+    row_seq = row_seq if row_seq is not None else _new(rows, torch.int32, seq_lens.device, stream)
+    row_len = row_len if row_len is not None else _new(rows, torch.int32, seq_lens.device, stream)
     _check("bsp_row_lengths_decode", lib().bsp_row_lengths_decode(_io_ptr(seq_lens), seq_lens.numel(), q_len, num_heads,
                                                                   _ptr(row_seq), _ptr(row_len), _stream(stream)))
     return row_seq, row_len
@@ -257,8 +270,8 @@ def row_lengths_decode(seq_lens, q_len, num_heads, row_seq=None, row_len=None, s
 def row_lengths_prefill(query_req_id, query_abs_pos, num_heads, row_seq=None, row_len=None, stream=None):
     rows = query_req_id.numel() * num_heads
     dev = query_req_id.device
-    row_seq = row_seq if row_seq is not None else torch.empty(rows, dtype=torch.int32, device=dev)
-    row_len = row_len if row_len is not None else torch.empty(rows, dtype=torch.int32, device=dev)
+    row_seq = row_seq if row_seq is not None else _new(rows, torch.int32, dev, stream)
+    row_len = row_len if row_len is not None else _new(rows, torch.int32, dev, stream)
     _check("bsp_row_lengths_prefill",
            lib().bsp_row_lengths_prefill(_ptr(query_req_id), _ptr(query_abs_pos), query_req_id.numel(), num_heads,
                                          _ptr(row_seq), _ptr(row_len), _stream(stream)))
@@ -268,8 +281,7 @@ def row_lengths_prefill(query_req_id, query_abs_pos, num_heads, row_seq=None, ro
 def index_score(idx, idx_q, q_dtype, block_table, row_seq, row_len, q_group, max_pages, scores=None, dev_err=None,
                 stream=None):
     rows = row_seq.numel()
-    scores = scores if scores is not None else torch.empty((rows, max_pages), dtype=torch.float32,
-                                                           device=idx_q.device)
+    scores = scores if scores is not None else _new((rows, max_pages), torch.float32, idx_q.device, stream)
     _check("bsp_index_score",
            lib().bsp_index_score(C.byref(idx.desc), _ptr(idx_q), q_dtype, _ptr(block_table), block_table.shape[1],
                                  _ptr(row_seq), _ptr(row_len), rows, q_group, max_pages, _ptr(scores), _ptr(dev_err),
@@ -286,8 +298,7 @@ def prefill_tiles(cu_tokens_host):
 def index_score_prefill(idx, idx_q, q_dtype, block_table, row_seq, row_len, cu_tokens, num_chunks, max_tiles,
                         max_pages, scores=None, dev_err=None, stream=None):
     rows = row_seq.numel()
-    scores = scores if scores is not None else torch.empty((rows, max_pages), dtype=torch.float32,
-                                                           device=idx_q.device)
+    scores = scores if scores is not None else _new((rows, max_pages), torch.float32, idx_q.device, stream)
     _check("bsp_index_score_prefill",
            lib().bsp_index_score_prefill(C.byref(idx.desc), _ptr(idx_q), q_dtype, _ptr(block_table),
                                          block_table.shape[1], _ptr(row_seq), _ptr(row_len), rows, _ptr(cu_tokens),
@@ -300,9 +311,9 @@ def topk_select(scores, row_seq, row_len, block_table, kv_dtype, k_pages, flags=
                 sparse_bt=None, sparse_ctx=None, stream=None):
     rows, max_pages = scores.shape
     dev = scores.device
-    topk_idx = topk_idx if topk_idx is not None else torch.empty((rows, k_pages), dtype=torch.int32, device=dev)
-    sparse_bt = sparse_bt if sparse_bt is not None else torch.empty((rows, k_pages), dtype=torch.int32, device=dev)
-    sparse_ctx = sparse_ctx if sparse_ctx is not None else torch.empty(rows, dtype=torch.int32, device=dev)
+    topk_idx = topk_idx if topk_idx is not None else _new((rows, k_pages), torch.int32, dev, stream)
+    sparse_bt = sparse_bt if sparse_bt is not None else _new((rows, k_pages), torch.int32, dev, stream)
+    sparse_ctx = sparse_ctx if sparse_ctx is not None else _new(rows, torch.int32, dev, stream)
     _check("bsp_topk_select",
            lib().bsp_topk_select(_ptr(scores), rows, max_pages, _ptr(row_seq), _ptr(row_len), _ptr(block_table),
                                  block_table.shape[1], kv_dtype, k_pages, flags, _ptr(topk_idx), _ptr(sparse_bt),
@@ -320,19 +331,19 @@ def decode_splits(kv_dtype, num_rows, k_pages):
     return int(lib().bsp_sparse_pa_decode_splits(kv_dtype, num_rows, k_pages))
 
 
-def decode_workspace(num_rows, k_pages, group, device="cuda"):
+def decode_workspace(num_rows, k_pages, group, device="cuda", stream=None):
     """A zeroed split-K workspace (its arrival counters must start at zero)."""
     n = decode_workspace_bytes(num_rows, k_pages, group)
-    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+    return _new(max(n, 16), torch.uint8, device, stream, zeroed=True)
 
 
 def sparse_pa_decode(kv, q, q_dtype, num_q_heads, sparse_bt, sparse_ctx, k_pages, sm_scale=None, out=None, ws=None,
                      dev_err=None, stream=None):
     rows = sparse_ctx.numel()
     sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
-    out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    out = out if out is not None else _new(q.shape, torch.bfloat16, q.device, stream)
     if ws is None:
-        ws = decode_workspace(rows, k_pages, num_q_heads // kv.num_kv_heads, q.device)
+        ws = decode_workspace(rows, k_pages, num_q_heads // kv.num_kv_heads, q.device, stream)
     _check("bsp_sparse_pa_decode",
            lib().bsp_sparse_pa_decode(C.byref(kv.desc), _io_ptr(q), q_dtype, num_q_heads, _ptr(sparse_bt),
                                       _ptr(sparse_ctx), rows, k_pages, sm_scale, _io_ptr(out), _ptr(ws), ws.numel(),
@@ -346,7 +357,7 @@ def sparse_pa_decode_noalloc(kv, q, q_dtype, num_q_heads, sparse_bt, sparse_ctx,
     fixed scratch; see include/bsp.h for the size limit and the sharing rule)."""
     rows = sparse_ctx.numel()
     sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
-    out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    out = out if out is not None else _new(q.shape, torch.bfloat16, q.device, stream)
     _check("bsp_sparse_pa_decode_noalloc",
            lib().bsp_sparse_pa_decode_noalloc(C.byref(kv.desc), _io_ptr(q), q_dtype, num_q_heads, _ptr(sparse_bt),
                                               _ptr(sparse_ctx), rows, k_pages, sm_scale, _io_ptr(out), _ptr(dev_err),
@@ -358,7 +369,7 @@ def sparse_pa_prefill(kv, q, q_dtype, num_q_heads, sparse_bt, sparse_ctx, k_page
                       dev_err=None, stream=None):
     rows = sparse_ctx.numel()
     sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
-    out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    out = out if out is not None else _new(q.shape, torch.bfloat16, q.device, stream)
     _check("bsp_sparse_pa_prefill",
            lib().bsp_sparse_pa_prefill(C.byref(kv.desc), _io_ptr(q), q_dtype, num_q_heads, _ptr(sparse_bt),
                                        _ptr(sparse_ctx), rows, k_pages, sm_scale, _io_ptr(out), _ptr(dev_err),
@@ -427,13 +438,13 @@ def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream
     T = slot.numel()
     if kv is not None:
         shape = (T, kv.num_kv_heads, 128)
-        k = k if k is not None else torch.empty(shape, dtype=torch.bfloat16, device=slot.device)
-        v = v if v is not None else torch.empty(shape, dtype=torch.bfloat16, device=slot.device)
+        k = k if k is not None else _new(shape, torch.bfloat16, slot.device, stream)
+        v = v if v is not None else _new(shape, torch.bfloat16, slot.device, stream)
     elif k is not None or v is not None:
         raise ValueError("k and v need a K/V cache")
     if idx is not None:
         shape = (T, idx.num_heads, 128)
-        idx_k = idx_k if idx_k is not None else torch.empty(shape, dtype=torch.bfloat16, device=slot.device)
+        idx_k = idx_k if idx_k is not None else _new(shape, torch.bfloat16, slot.device, stream)
     elif idx_k is not None:
         raise ValueError("idx_k needs an index cache")
     bf = torch.bfloat16
@@ -451,11 +462,11 @@ def dense_pa_workspace_bytes(num_rows, num_kv_heads, group, q_group):
     return int(lib().bsp_dense_pa_workspace_bytes(num_rows, num_kv_heads, group, q_group))
 
 
-def dense_pa_workspace(num_rows, num_kv_heads, group, q_group, device="cuda"):
+def dense_pa_workspace(num_rows, num_kv_heads, group, q_group, device="cuda", stream=None):
     """A workspace for dense attention calls of these sizes that never overlap
     on the GPU (its contents need not be set)."""
     n = dense_pa_workspace_bytes(num_rows, num_kv_heads, group, q_group)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    return _new(max(n, 16), torch.uint8, device, stream)
 
 
 def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, q_group, sm_scale=None, out=None,
@@ -467,9 +478,9 @@ def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, 
     rows, hkv = row_len.numel(), kv.num_kv_heads
     n = rows // hkv * num_q_heads * 128
     sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
-    out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    out = out if out is not None else _new(q.shape, torch.bfloat16, q.device, stream)
     if ws is None:
-        ws = dense_pa_workspace(rows, hkv, num_q_heads // hkv, q_group, q.device)
+        ws = dense_pa_workspace(rows, hkv, num_q_heads // hkv, q_group, q.device, stream)
     if block_table.dim() != 2:
         raise ValueError("block_table is not [sequences, blocks]")
     # e4m3 queries may be given as the type or as bytes
