@@ -421,7 +421,9 @@ struct Walk {
 // by 2^-a, its largest magnitude then in [128, 256), and split: hi = e4m3(x), lo
 // = e4m3((x - hi) * 2^4), multiplied by 2^a and 2^(a-4) in the MMAs.  bf16 has 8
 // significant bits and each part 4, so the sum is exact for elements down to
-// 2^-13 of the group's largest, and off by at most 2^-21 of it below.
+// 2^-13 of the group's largest, and off by at most 2^-21 of it below.  A group with an
+// infinite element is NaN: the conversions saturate, and every logit of the row is
+// infinite or NaN, so the row is NaN either way.
 template <bool Q16>
 __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int tokens, int h, uint8_t* q, int rows,
                                         uint8_t* cells, int tid) {
@@ -450,6 +452,10 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
     top = fmaxf(top, fabsf(x[k]));
   }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the group's other chunk
+  if (top == INFINITY) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(0x7FC00000u);
+  }
   const int ex = max(-110, static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127) - 7;
   uint32_t hi[4], lo[4];
 #pragma unroll

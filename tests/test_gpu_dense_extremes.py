@@ -1,0 +1,35 @@
+"""bsp_dense_pa_decode at the ends of its inputs' ranges."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_dense_pa import Case, _f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("q_len", [1, 2, 4])
+def test_a_query_that_is_not_finite_gives_nan_in_its_row_alone(value, q_len):
+    """Every logit of such a row is infinite or NaN, whatever the keys hold, so
+    softmax has no value there: all of the row is NaN (zeros where it sees nothing)."""
+    c = Case([700, 1, 0, 129], q_len=q_len, q8=False, seed=31)
+    # keys of 0 and of 0.5 in the dims that are hit, and ordinary ones
+    for b in range(c.blocks):
+        c.fields[b, 0, :8192].reshape(128, 64)[:, 0] = 0x10
+    c.device()
+    want = c.call().clone()
+    hit = []
+    for i, (tok, head, dim) in enumerate([(0, 3, 0), (q_len, 0, 1), (2 * q_len, 7, 77), (4 * q_len - 1, 15, 127)]):
+        c.dq[tok, head, dim] = -value if i % 2 else value
+        hit.append((tok, head))
+    got = c.call()
+    assert c.err.item() == 0
+    for t in range(4 * q_len):
+        for h in range(16):
+            if (t, h) in hit and c.row_len[t] > 0:
+                assert got[t, h].isnan().all(), (t, h)
+            else:
+                assert torch.equal(got[t, h], want[t, h]), (t, h)
