@@ -31,9 +31,11 @@
 // A CTA is a producer warp, which loads blocks by TMA (K unpacked to one byte
 // slot a value, the layout the tensor core reads; V packed; scales as they lie)
 // and issues all MMAs, and four or eight compute warps.  Thread = token of the
-// logits: it takes its exponentials 2^(z - m + kBias) against the row's reference m
-// and adds them up (one reduction at the end of the unit).  References move only
-// when a row's maximum passes its reference by kMaxGrow; a vote of the CTA finds
+// logits: it takes its exponentials 2^((z - m) qk + kBias) against the row's reference
+// m and adds them up (one reduction at the end of the unit); z and m are the MMA's
+// sums, the scale qk comes after the difference, so that equal logits of any size have
+// equal weights.  References move only when a row's maximum passes its reference by
+// kMaxGrow; a vote of the CTA finds
 // those blocks, and the ones that some row does not see whole, and takes them
 // through an uncommon way that rescales O and l.  Then the warp turns a quarter of
 // V's dims into f16: ldmatrix.trans hands a thread four nibbles of two tokens in a
@@ -63,6 +65,7 @@
 // without waits and arrives nowhere, so that the producer stops too.  Then the CTA
 // frees its TMEM and returns.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -80,7 +83,7 @@ constexpr int kKRows = 136, kVRows = 68;
 constexpr int kKTile = kKRows * 128, kVTile = (kVRows + 7) / 8 * 8 * 128;
 static_assert(kKRows * 64 == kMxField && kVRows * 128 == kMxField && kKTile % 1024 == 0);
 constexpr float kMaxGrow = 8.f;   // the reference maximum moves when a row's maximum grows by more (log2)
-constexpr float kBias = 7.f;      // weights are 2^(z - m + kBias): at most 2^15
+constexpr float kBias = 7.f;      // weights are 2^((z - m) qk + kBias): at most 2^15
 // rounds (of up to kSleepNs) before a wait gives up; a build may set fewer, to see what
 // a kernel whose waits run out leaves behind
 #ifdef BSP_DENSE_PA_WAIT_ROUNDS
@@ -88,7 +91,7 @@ constexpr float kBias = 7.f;      // weights are 2^(z - m + kBias): at most 2^15
 #else
 #define BSP_WAIT_ROUNDS kSleepWaitLimit
 #endif
-constexpr float kNoMax = -1e30f;  // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
+constexpr float kNoMax = -3.402823466e38f;  // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
 // V enters the MMA as v * 2^(scale byte - kVRef).  f16 holds that exactly for
 // bytes from kVLow to kVHigh (2^-17 to 2^7); see scale_words.
 
@@ -99,7 +102,7 @@ __host__ __device__ constexpr int64_t list_bytes(int64_t ctas) { return (ctas * 
 
 struct Params {
   DensePaParams a;
-  float qk_scale;  // sm_scale * log2(e)
+  float qk_scale;  // |sm_scale| * log2(e): a negative scale's sign goes to q
   int32_t groups, subs, sub_tokens;  // query groups; units each is cut into, of sub_tokens tokens
   int32_t units, ctas, shares;       // shares = ctas / subs
   int32_t rows;                      // of a unit's slot in the workspace
@@ -126,7 +129,7 @@ struct Smem {
   static constexpr int p = v + kVStages * kVTile;
   static constexpr int q = p + 2 * kPBytes;
   static constexpr int scales = q + N * 128 * (Q16 ? 2 : 1);  // per compute warp: a word for two tokens
-  static constexpr int refs = scales + kCompute * Shape<N>::kTokens * 2;        // [2][N] kBias - m
+  static constexpr int refs = scales + kCompute * Shape<N>::kTokens * 2;        // [2][N] -m
   static constexpr int fac = refs + 2 * N * 4;                // [N] rescale factors
   static constexpr int tops = fac + N * 4;                    // [4][N] maxima, later sums
   static constexpr int len = tops + 4 * N * 4;                // [N] lengths
@@ -345,6 +348,10 @@ __device__ __forceinline__ float scale_pow2(float x, int e) {
   const int a = max(-126, min(127, e)), b = max(-126, min(127, e - a));
   return x * __uint_as_float(static_cast<uint32_t>(a + 127) << 23) * __uint_as_float(static_cast<uint32_t>(b + 127) << 23);
 }
+// what a sum with the reference `from` is multiplied by to have the reference `to` >= from
+__device__ __forceinline__ float rescale(float from, float to, float qk) {
+  return ex2_approx(fminf((from - to) * qk, 0.f));  // (NaN, of a scale of 0: 0)
+}
 // R values of each lane reduced over the warp, all of them at once: each step hands
 // half of the values to the lane that differs in one bit.  Lane i ends with value
 // i * R / 32 (of R = 16, lanes 2j and 2j + 1 both with value j).
@@ -435,7 +442,8 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
   if (!Q16) {
     uint4 w = make_uint4(0, 0, 0, 0);
     if (live) w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + e);
-    *reinterpret_cast<uint4*>(dst) = w;
+    const uint32_t sign = a.sm_scale < 0.f ? 0x80808080u : 0u;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w.x ^ sign, w.y ^ sign, w.z ^ sign, w.w ^ sign);
     if (!(j & 1)) cells[n * 4 + (j >> 1)] = 127;
     return;
   }
@@ -449,6 +457,7 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     x[k] = bf16_bits_to_float(k & 1 ? ws[k >> 1] >> 16 : ws[k >> 1] & 0xFFFF);
+    if (a.sm_scale < 0.f) x[k] = -x[k];
     top = fmaxf(top, fabsf(x[k]));
   }
   top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the group's other chunk
@@ -535,16 +544,16 @@ __device__ __noinline__ void wide_words(uint32_t cell, int n, int max_len, uint3
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(word_at + 2 * i), "r"(word) : "memory");
 }
 
-// x = z * qk + (kBias - m) of CH rows
+// z - m of CH rows
 template <int CH>
-__device__ __forceinline__ void load_logits(float2 (&x)[CH / 2], uint32_t zt, uint32_t refs, float qk) {
+__device__ __forceinline__ void load_logits(float2 (&x)[CH / 2], uint32_t zt, uint32_t refs) {
   float z[CH];
   tmem_ld<CH>(zt, z);
 #pragma unroll
   for (int i = 0; i < CH / 4; ++i) {
     const float4 m = lds128f(refs + 16 * i);
-    x[2 * i] = ffma2({z[4 * i], z[4 * i + 1]}, {qk, qk}, {m.x, m.y});
-    x[2 * i + 1] = ffma2({z[4 * i + 2], z[4 * i + 3]}, {qk, qk}, {m.z, m.w});
+    x[2 * i] = fadd2({z[4 * i], z[4 * i + 1]}, {m.x, m.y});
+    x[2 * i + 1] = fadd2({z[4 * i + 2], z[4 * i + 3]}, {m.z, m.w});
   }
 }
 template <int CH>
@@ -935,7 +944,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         lens[tid] = j < w.tokens ? min(max(a.row_len[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h], 0), w.max_len)
                                  : w.max_len;
         nan_of[tid] = 0;
-        stsf(base + S::refs + (cur * N + tid) * 4, kBias - kNoMax);
+        stsf(base + S::refs + (cur * N + tid) * 4, -kNoMax);
       }
       if (tid < w.tokens && a.row_seq[static_cast<int64_t>(w.tok0 + tid) * a.hkv + w.h] != w.seq)
         set_err(a.err, BSP_DEVERR_GROUP_SEQ);
@@ -983,7 +992,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll
           for (int c = 0; c < R; c += CH) {
             float2 x[CH / 2];  // (read again rather than held: registers)
-            load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+            load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4);
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) x[i] = ffma2(x[i], {p.qk_scale, p.qk_scale}, {kBias, kBias});
             if (!whole) mask_logits<CH>(x, n0 + tok, lens_at + (half * R + c) * 4);
             uint32_t pk[CH / 2];
 #pragma unroll
@@ -1033,12 +1044,12 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll
         for (int c = 0; c < R; c += CH) {
           float2 x[CH / 2];
-          load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4, p.qk_scale);
+          load_logits<CH>(x, z + c, base + S::refs + (cur * N + half * R + c) * 4);
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
         }
         uint32_t mode = 0;  // kWide: V in bf16; kSkip: a block whose id is out of range
-        if (__builtin_expect(!all_of<32 * kCompute>(!bad && whole && in && top <= kBias + kMaxGrow), 0)) {
+        if (__builtin_expect(!all_of<32 * kCompute>(!bad && whole && in && top * p.qk_scale <= kMaxGrow), 0)) {
           // The uncommon way: the rows' maxima, where a row may not see the
           // token, new references, and O and l in their terms; are V's scales
           // outside f16's range?
@@ -1049,8 +1060,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
             for (int c = 0; c < R; c += CH) {
               float y[CH];
               tmem_ld<CH>(z + c, y);
-#pragma unroll
-              for (int i = 0; i < CH; ++i) y[i] *= p.qk_scale;
               if (!whole) {
 #pragma unroll
                 for (int i = 0; i < CH; ++i)
@@ -1068,10 +1077,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
             float mx = ldsf(tops + tid * 4);
 #pragma unroll
             for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + tid) * 4));
-            const float old = ldsf(base + S::refs + (cur * N + tid) * 4);  // kBias - m
-            const float ref = mx > kBias - old ? kBias - mx : old;  // (every row: fewer such blocks to come)
-            f = ex2_approx(ref - old);
-            stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, ref);
+            const float old = -ldsf(base + S::refs + (cur * N + tid) * 4);
+            const float ref = mx > old ? mx : old;  // (every row: fewer such blocks to come)
+            f = rescale(old, ref, p.qk_scale);
+            stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, -ref);
             stsf(fac + tid * 4, f);
           }
           if (!skip) cur ^= 1;
@@ -1140,7 +1149,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         stsf(fac + tid * 4, static_cast<float>(1 << (kVRef - 127)) * (!all ? 1.f : sum == 0.f ? 0.f : 1.f / sum));
         if (!all && tid < rows)
           *reinterpret_cast<float2*>(po + N * kDim + 2 * tid) =
-              make_float2(kBias - ldsf(base + S::refs + (cur * N + tid) * 4), sum);
+              make_float2(-ldsf(base + S::refs + (cur * N + tid) * 4), sum);
       }
       bar_sync(1, 32 * kCompute);
       if (!first) done(round);
@@ -1232,7 +1241,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
       float mx = ml.x;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const float mn = fmaxf(M, mx), f = ex2_approx(M - mn), w = ex2_approx(ml.x - mn);
+      const float mn = fmaxf(M, mx), f = rescale(M, mn, p.qk_scale), w = rescale(ml.x, mn, p.qk_scale);
       float ls = w * ml.y;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
@@ -1259,7 +1268,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
     for (int k = 0; k < parts; ++k) mn = fmaxf(mn, s_ml[warp + k].x);
     x = make_float4(0.f, 0.f, 0.f, 0.f), L = 0.f;
     for (int k = 0; k < parts; ++k) {
-      const float w = ex2_approx(s_ml[warp + k].x - mn);
+      const float w = rescale(s_ml[warp + k].x, mn, p.qk_scale);
       const float4 y = s_o[warp + k][lane];
       L += w * s_ml[warp + k].y;
       x.x += w * y.x, x.y += w * y.y, x.z += w * y.z, x.w += w * y.w;
@@ -1334,7 +1343,7 @@ cudaError_t launch_dense_pa(const DensePaParams& a, int num_sms, cudaStream_t s,
   const bool q16 = a.q_dtype == BSP_BF16;
   Params p{};
   p.a = a;
-  p.qk_scale = a.sm_scale * kLog2e;
+  p.qk_scale = std::fabs(a.sm_scale) * kLog2e;
   const int tokens = a.num_rows / a.hkv;
   p.groups = (tokens + a.q_group - 1) / a.q_group;
   p.subs = pl.subs;

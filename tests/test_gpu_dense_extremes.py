@@ -33,3 +33,24 @@ def test_a_query_that_is_not_finite_gives_nan_in_its_row_alone(value, q_len):
                 assert got[t, h].isnan().all(), (t, h)
             else:
                 assert torch.equal(got[t, h], want[t, h]), (t, h)
+
+
+@pytest.mark.parametrize("byte", [127, 200, 215, 230, 239])
+@pytest.mark.parametrize("q8,q_len", [(True, 1), (False, 2), (True, 4)])
+@pytest.mark.parametrize("code", [0xFF, 0x77])  # -6 and 6
+def test_equal_logits_of_any_size_average_the_values(byte, q8, q_len, code):
+    """Keys and queries of one value: 128 equal products sum exactly, so the logits of
+    a row are the same number, bit for bit, and no error of theirs enters.  Sums of
+    up to 8e36, logits of up to 1e36 in units of ln 2: well inside fp32."""
+    c = Case([1, 77, 300, 2500], q_len=q_len, q8=q8, seed=byte)
+    c.fields[:, 0, :8192], c.fields[:, 0, 8192:] = code, byte
+    c.q_t = torch.full_like(c.q_t, 0x40 if byte > 235 else 0x7E) if q8 else torch.full_like(c.q_t, 2.0 if byte > 235 else 448.0)
+    c.q[:] = 2.0 if byte > 235 else 448.0
+    c.device()
+    got = _f64(c.call())
+    assert c.err.item() == 0
+    o, a = c.want()
+    tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.0 ** -13) * a
+    for r in range(len(c.row_len)):
+        tol[r] += c.floor(r)
+    assert (np.abs(got - o) <= tol).all(), (got[0, 0, :4], o[0, 0, :4])
