@@ -966,14 +966,14 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       }
       bool first = true;  // no PV round of the unit yet
       const int max_len = w.max_len, min_len = w.min_len;
-      int n0 = w.b0 * kBlock;
+      int n0 = w.b0 * kBlock;  // at most 2^31 - 128 in the loop
 #pragma unroll 1
-      for (int k = w.nblk; k > 0; --k, n0 += kBlock) {
+      for (int k = w.nblk; k > 0; --k, n0 = static_cast<int>(n0 + static_cast<uint32_t>(kBlock))) {
         // after a timed-out wait the warp goes on without waits and arrivals (the
         // barriers of the compute warps need every one); its results are void
         if (alive) alive = wait_warp(v_full + 8 * vst, v_phase, a.err);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 + kBlock <= min_len;
+        const bool bad = lds32(bad_at + 4 * vst) != 0, whole = n0 <= min_len - kBlock;
         const uint32_t z = z_at + zb * N, voff = vst * kVTile;
         auto exact = [&]() {
           bool in = true;

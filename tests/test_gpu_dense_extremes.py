@@ -54,3 +54,24 @@ def test_equal_logits_of_any_size_average_the_values(byte, q8, q_len, code):
     for r in range(len(c.row_len)):
         tol[r] += c.floor(r)
     assert (np.abs(got - o) <= tol).all(), (got[0, 0, :4], o[0, 0, :4])
+
+
+def test_a_context_of_two_to_the_31_minus_one_tokens():
+    """The last block's last token is not seen.  Every token seen has the logit 0
+    and the value 1; weights of 2^7 and their sums over a share of the blocks are
+    exact in fp32, so the mean is off by bf16's half step and the join's roundings."""
+    from block_sparse_paged_score_gb300 import bsp
+    n = 4096  # blocks that the context goes through again and again, and the last one
+    kv = bsp.KvCache(bsp.MXFP4, 1, n + 1)
+    f = kv.buffer.view(n + 1, 2, 8704)
+    f[:, :, 8192:] = 127
+    f[:, 1, :8192] = 0x22  # V: 1
+    f[n, 0, 127 * 64:8192], f[n, 1, 127 * 64:8192] = 0x77, 0xFF  # the unseen token: a logit of 70, V -6
+    table = (torch.arange(1 << 24, dtype=torch.int32, device="cuda") % n)[None]
+    table[0, -1] = n
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.ones(1, 16, 128, dtype=torch.bfloat16, device="cuda")
+    one = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")  # noqa: E731
+    out = bsp.dense_pa_decode(kv, q, bsp.BF16, 16, table, one(0), one(2 ** 31 - 1), 1, dev_err=err)
+    assert err.item() == 0
+    assert (out.float() - 1).abs().max() <= 2.0 ** -8
