@@ -2,7 +2,8 @@
 // slot and dequantised to bf16 rows (bsp_kv_page_read).
 //
 //   bf16   as stored;  fp8  e4m3 * scale, rounded to bf16
-//   MXFP4  e2m1 * 2^(e8m0 - 127), exact in bf16 (until it leaves its range)
+//   MXFP4  e2m1 * 2^(e8m0 - 127), exact in bf16 (until it leaves its range); NaN for
+//          a scale byte 255
 //
 // One CTA reads 16 consecutive tokens of one head, so that slots which follow
 // each other (the usual case: a sequence's page) share sectors.  Rows that
@@ -38,7 +39,8 @@ __device__ __forceinline__ uint4 from_e4m3(uint2 w, float sc) {
 // dims 8*l.. of token o of an MXFP4 field
 __device__ __forceinline__ uint4 from_mx(const uint8_t* field, int o, int l) {
   const uint32_t w = *reinterpret_cast<const uint32_t*>(field + o * 64 + 4 * l);
-  const float sc = e8m0_to_float(field[kMxScaleOff + o * 4 + (l >> 2)]);
+  const uint32_t e = field[kMxScaleOff + o * 4 + (l >> 2)];
+  const float sc = e == 255 ? __uint_as_float(0x7FC00000u) : e8m0_to_float(e);
   float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -559,7 +559,8 @@ bsp_status bsp_norm_rope_write(const bsp_norm_rope_args* a, bsp_stream_t stream)
  *   slot   int64 [T]: block*128 + offset; negative gives a row of zeros, one
  *          beyond the cache too, and sets BSP_DEVERR_SLOT
  * fp8 values are e4m3 * scale in fp32, rounded to bf16; MXFP4 values are
- * exact in bf16 (scale bytes 255 are never written).
+ * exact in bf16, infinite past its range; a scale byte 255, which the writers
+ * never store, is a NaN.
  * ---------------------------------------------------------------------- */
 bsp_status bsp_kv_page_read(const bsp_kv_cache* kv, const bsp_index_cache* idx, const int64_t* slot,
                             int32_t num_tokens, void* k, void* v, void* idx_k, int32_t* dev_err,
