@@ -238,18 +238,34 @@ __device__ __forceinline__ Type type_of(const NormRopeParams& p, int ty, const T
   return a;
 }
 
-// norm, weight and rotation of a head.  The weight (of bf16 values, exact or nearly)
-// and the rotation come first: neither waits for the mean, and the one factor at the
-// end rounds once.
-template <bool PAIRS>
-__device__ __forceinline__ void norm_rotate(const NormRopeParams& p, const Token& t, const float (&w)[8], float (&x)[8]) {
+// sum of x^2 over the head, in every lane
+__device__ __forceinline__ float sum_squares(const float (&x)[8]) {
   float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) s2 = ffma2({x[j], x[j + 1]}, {x[j], x[j + 1]}, s2);
   float ss = s2.x + s2.y;
 #pragma unroll
   for (int m = 1; m < 16; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-  const float inv = __frsqrt_rn(fmaf(ss, 1.f / kDim, p.eps));
+  return ss;
+}
+
+// norm, weight and rotation of a head.  The weight (of bf16 values, exact or nearly)
+// and the rotation come first: neither waits for the mean, and the one factor at the
+// end rounds once.
+template <bool PAIRS>
+__device__ __forceinline__ void norm_rotate(const NormRopeParams& p, const Token& t, const float (&w)[8], float (&x)[8]) {
+  float m = fmaf(sum_squares(x), 1.f / kDim, p.eps);
+  // Rows of such a size that squares, or products with the weight, would leave fp32's
+  // range are brought to an ordinary one first, by a power of two, exactly.
+  constexpr uint32_t kLow = (127u - 80) << 23, kHigh = (127u + 80) << 23;
+  const bool odd = __float_as_uint(m) - kLow >= kHigh - kLow;
+  if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
+    const float k = !odd ? 1.f : m < 1.f ? 0x1p96f : 0x1p-96f;  // (odd and NaN: any)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= k;
+    m = fmaf(sum_squares(x), 1.f / kDim, p.eps * k * k);
+  }
+  const float inv = __frsqrt_rn(m);
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const float2 y = fmul2({x[j], x[j + 1]}, {w[j], w[j + 1]});
