@@ -388,6 +388,37 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return a && b && an > 0 && bn > 0 && x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
 }
 
+// whether [a, a + an) shares a byte with one of the pieces [b + i * step, + bn), i < n
+bool overlap_pieces(const void* a, int64_t an, const void* b, int64_t bn, int64_t step, int64_t n) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (!a || !b || an <= 0 || bn <= 0 || n <= 0 || x + static_cast<uintptr_t>(an) <= y) return false;
+  // the last piece that starts before the range ends
+  const auto i = std::min<uintptr_t>((x + static_cast<uintptr_t>(an) - 1 - y) / static_cast<uintptr_t>(step),
+                                     static_cast<uintptr_t>(n - 1));
+  return x < y + i * static_cast<uintptr_t>(step) + static_cast<uintptr_t>(bn);
+}
+
+// whether a range shares a byte with what a cache's blocks hold
+bool overlap_cache(const void* a, int64_t an, const bsp_kv_cache* kv) {
+  if (!kv) return false;
+  const int64_t heads = kv->num_kv_heads;
+  if (kv->dtype == BSP_MXFP4)
+    return overlap_pieces(a, an, kv->k_base, heads * kMxField, kv->id_stride_bytes, kv->num_blocks) ||
+           overlap_pieces(a, an, kv->v_base, heads * kMxField, kv->id_stride_bytes, kv->num_blocks);
+  const int64_t page = heads * (kv->dtype == BSP_BF16 ? 4096 : 2048), step = 16 * kv->id_stride_bytes;
+  for (int j = 0; j < 8; ++j)
+    if (overlap_pieces(a, an, static_cast<const uint8_t*>(kv->k_base) + j * kv->id_stride_bytes, page, step,
+                       kv->num_blocks) ||
+        overlap_pieces(a, an, static_cast<const uint8_t*>(kv->v_base) + j * kv->id_stride_bytes, page, step,
+                       kv->num_blocks))
+      return true;
+  return false;
+}
+bool overlap_cache(const void* a, int64_t an, const bsp_index_cache* idx) {
+  return idx && overlap_pieces(a, an, idx->base, idx->num_heads * index_field(idx->dtype), idx->block_stride_bytes,
+                               idx->num_blocks);
+}
+
 // the cache fields of a writer or reader
 void set_caches(KvWriteParams& p, const bsp_kv_cache* kv, const bsp_index_cache* idx) {
   if (kv) {
@@ -506,17 +537,35 @@ bsp_status bsp_norm_rope_write(const bsp_norm_rope_args* a, bsp_stream_t stream)
     p.out[i] = out[i];
     p.out_dtype[i] = out_dtype[i];
   }
+  // no output on an input or another output, but a bf16 one in place
+  struct Range {
+    const void* p;
+    int64_t bytes;
+  };
+  Range in[2 * kHeadTypes + 3], out_of[kHeadTypes + 1];
   for (int i = 0; i < kHeadTypes; ++i) {
-    if (!p.out[i]) continue;
-    const int64_t bytes = T * p.heads[i] * kDim * (p.out_dtype[i] == BSP_BF16 ? 2 : 1);
-    for (int j = 0; j < kHeadTypes; ++j) {
-      if (j != i && overlap(p.out[i], bytes, p.out[j], T * p.heads[j] * kDim * (p.out_dtype[j] == BSP_BF16 ? 2 : 1)))
-        return BSP_ERR_INVALID_ARG;
-      const bool in_place = j == i && p.out[i] == src[j] && p.out_dtype[i] == BSP_BF16 && stride[j] == p.heads[j] * kDim;
-      if (!in_place && p.src[j] && overlap(p.out[i], bytes, src[j], ((T - 1) * stride[j] + p.heads[j] * kDim) * 2))
-        return BSP_ERR_INVALID_ARG;
-    }
+    in[i] = {p.src[i], p.src[i] ? ((T - 1) * stride[i] + p.heads[i] * kDim) * 2 : 0};
+    in[kHeadTypes + i] = {p.weight[i], 2 * kDim};
+    out_of[i] = {p.out[i], p.out[i] ? T * p.heads[i] * kDim * (p.out_dtype[i] == BSP_BF16 ? 2 : 1) : 0};
   }
+  in[2 * kHeadTypes] = {a->positions, 4 * T};
+  in[2 * kHeadTypes + 1] = {a->kv || a->idx ? a->slot : nullptr, 8 * T};
+  in[2 * kHeadTypes + 2] = {a->rot_dim ? a->rope_table : nullptr, 4 * a->rope_rows * a->rot_dim};
+  out_of[kHeadTypes] = {a->dev_err, 4};
+  for (int i = 0; i <= kHeadTypes; ++i) {
+    const Range& o = out_of[i];
+    if (!o.p) continue;
+    for (int j = 0; j < 2 * kHeadTypes + 3; ++j) {
+      const bool in_place = i < kHeadTypes && j == i && o.p == in[j].p && p.out_dtype[i] == BSP_BF16 &&
+                            stride[i] == p.heads[i] * kDim;
+      if (!in_place && overlap(o.p, o.bytes, in[j].p, in[j].bytes)) return BSP_ERR_INVALID_ARG;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(o.p, o.bytes, out_of[j].p, out_of[j].bytes)) return BSP_ERR_INVALID_ARG;
+    if (overlap_cache(o.p, o.bytes, a->kv) || overlap_cache(o.p, o.bytes, a->idx)) return BSP_ERR_INVALID_ARG;
+  }
+  for (const Range& r : in)
+    if (overlap_cache(r.p, r.bytes, a->kv) || overlap_cache(r.p, r.bytes, a->idx)) return BSP_ERR_INVALID_ARG;
   p.weight_offset = a->weight_offset;
   p.eps = a->eps;
   p.rope = a->rope_table;

@@ -512,8 +512,10 @@ bsp_status bsp_step_tables(const bsp_step_tables_args* a, bsp_stream_t stream);
  *    with kv or idx.  The same slot twice in a call leaves that slot's bytes
  *    unspecified (a mixture of the two rows).
  *  - q_out, k_out and idx_q_out are dense [T, heads, 128].  A bf16 output may
- *    be its own dense input; any other overlap of an output with an input or
- *    another output is BSP_ERR_INVALID_ARG.  The inputs must be device memory.
+ *    be its own dense input; any other overlap of an output or dev_err with an
+ *    input or another output, and of a cache's pages with any of them, is
+ *    BSP_ERR_INVALID_ARG (the two caches are not compared with each other).
+ *    The inputs must be device memory.
  * One launch.
  * ---------------------------------------------------------------------- */
 typedef struct bsp_norm_rope_args {
