@@ -405,6 +405,15 @@ def _complain(name, t, dtype, device, numel):
     raise ValueError(f"{name} has {t.numel()} elements, {numel} are needed")
 
 
+def _cache_desc(name, cache, device):
+    """A reference to a cache's descriptor (None: NULL)."""
+    if cache is None:
+        return None
+    if cache.buffer.device != device:
+        raise ValueError(f"the {name} cache is on {cache.buffer.device}, the stream on {device}")
+    return C.byref(cache.desc)
+
+
 def _head_rows(name, t, tokens, heads, device):
     """(address, token stride) of bf16 rows [tokens, heads, 128] whose heads
     lie side by side; the tokens may be any distance apart."""
@@ -436,6 +445,7 @@ def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream
     s = _on(stream)
     dev = s.device
     T = slot.numel()
+    kv_desc, idx_desc = _cache_desc("K/V", kv, dev), _cache_desc("index", idx, dev)
     if kv is not None:
         shape = (T, kv.num_kv_heads, 128)
         k = k if k is not None else _new(shape, torch.bfloat16, slot.device, stream)
@@ -450,8 +460,7 @@ def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream
     bf = torch.bfloat16
     n, ni = T * kv.num_kv_heads * 128 if kv is not None else 0, T * idx.num_heads * 128 if idx is not None else 0
     _check("bsp_kv_page_read",
-           lib().bsp_kv_page_read(C.byref(kv.desc) if kv is not None else None,
-                                  C.byref(idx.desc) if idx is not None else None,
+           lib().bsp_kv_page_read(kv_desc, idx_desc,
                                   _dense("slot", slot, torch.int64, dev), T, _dense("k", k, bf, dev, n),
                                   _dense("v", v, bf, dev, n), _dense("idx_k", idx_k, bf, dev, ni),
                                   _dense("dev_err", dev_err, torch.int32, dev, 1), s.cuda_stream))
@@ -475,6 +484,7 @@ def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, 
     (bsp_dense_pa_decode); q [tokens, num_q_heads, 128], rows = tokens * Hkv."""
     s = _on(stream)
     dev, i32 = s.device, torch.int32
+    desc = _cache_desc("K/V", kv, dev)
     rows, hkv = row_len.numel(), kv.num_kv_heads
     n = rows // hkv * num_q_heads * 128
     sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
@@ -486,7 +496,7 @@ def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, 
     # e4m3 queries may be given as the type or as bytes
     qt = torch.bfloat16 if q_dtype == BF16 else torch.float8_e4m3fn if q.dtype is torch.float8_e4m3fn else torch.uint8
     _check("bsp_dense_pa_decode",
-           lib().bsp_dense_pa_decode(C.byref(kv.desc), _dense("q", q, qt, dev, n), q_dtype, num_q_heads,
+           lib().bsp_dense_pa_decode(desc, _dense("q", q, qt, dev, n), q_dtype, num_q_heads,
                                      _dense("block_table", block_table, i32, dev), block_table.shape[1],
                                      _dense("row_seq", row_seq, i32, dev, rows), _dense("row_len", row_len, i32, dev),
                                      rows, q_group, sm_scale, _dense("out", out, torch.bfloat16, dev, n),

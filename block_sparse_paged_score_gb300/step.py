@@ -271,6 +271,7 @@ class NormRopeWrite:
         self.idx_q_out = None
         self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
         dev = self.device = self.q_out.device
+        bsp._cache_desc("K/V", kv, dev), bsp._cache_desc("index", idx, dev)
         self.heads = (num_q_heads, kv.num_kv_heads if kv is not None else 0, idx.num_heads if idx is not None else 0)
         a.num_q_heads, a.q_out_dtype, a.idx_q_out_dtype = num_q_heads, q_dtype, idx_q_dtype
         if kv is not None:
