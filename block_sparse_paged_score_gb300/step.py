@@ -215,9 +215,9 @@ class StepTables:
     no tokens are -1 at first, or block_table is the caller's), seq_lens,
     cu_tokens, blocks_taken, and slot, query_req_id, query_abs_pos of
     token_capacity rows, the last of them pad rows where the step has fewer
-    tokens."""
+    tokens; dev_err is the caller's error word (None: one of its own)."""
 
-    def __init__(self, num_seqs, bt_stride, token_capacity, num_blocks, block_table=None, device="cuda"):
+    def __init__(self, num_seqs, bt_stride, token_capacity, num_blocks, block_table=None, device="cuda", dev_err=None):
         e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device=device)  # noqa: E731
         self.num_seqs, self.token_capacity = num_seqs, token_capacity
         if block_table is None:
@@ -228,7 +228,7 @@ class StepTables:
         self.seq_lens, self.cu_tokens, self.blocks_taken = e(num_seqs), e(num_seqs + 1), e(1)
         self.slot = e(token_capacity, torch.int64)
         self.query_req_id, self.query_abs_pos = e(token_capacity), e(token_capacity)
-        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.dev_err = dev_err if dev_err is not None else torch.zeros(1, dtype=torch.int32, device=device)
         a = self.args = bsp.StepTablesArgs()
         a.num_seqs, a.bt_stride, a.token_capacity, a.num_blocks = num_seqs, bt_stride, token_capacity, num_blocks
         a.block_table = bsp._dense("block_table", block_table, torch.int32, self.seq_lens.device)
@@ -236,7 +236,7 @@ class StepTables:
                                                    self.blocks_taken.data_ptr())
         a.slot, a.query_req_id, a.query_abs_pos = (self.slot.data_ptr(), self.query_req_id.data_ptr(),
                                                    self.query_abs_pos.data_ptr())
-        a.dev_err = self.dev_err.data_ptr()
+        a.dev_err = bsp._dense("dev_err", self.dev_err, torch.int32, self.seq_lens.device, 1)
 
     def run(self, context_lens, new_lens, free_blocks, free_head=None, stream=None):
         """int32 lengths [num_seqs] before the step and of the step, the free
@@ -259,17 +259,18 @@ class NormRopeWrite:
     (bsp_norm_rope_write) for up to max_tokens tokens.  kv and idx are the
     caches (idx None: a layer without an indexer; kv None: queries and index
     keys alone).  Weights are bf16 [128] or None; rope_table is fp32
-    [positions, rot_dim], cosines then sines (see rope_table), or None."""
+    [positions, rot_dim], cosines then sines (see rope_table), or None; dev_err is
+    the caller's error word (None: one of its own)."""
 
     def __init__(self, kv, idx, num_q_heads, max_tokens, q_weight=None, k_weight=None, idx_q_weight=None,
                  idx_k_weight=None, weight_offset=0.0, eps=1e-6, rope_table=None, rope_pairs=False, q_dtype=bsp.BF16,
-                 idx_q_dtype=bsp.BF16, device="cuda"):
+                 idx_q_dtype=bsp.BF16, device="cuda", dev_err=None):
         self.kv, self.idx, self.max_tokens = kv, idx, max_tokens
         a = self.args = bsp.NormRopeArgs()
         self.q_out = torch.empty(max_tokens, num_q_heads, 128, device=device,
                                  dtype=torch.uint8 if q_dtype == bsp.FP8_E4M3 else torch.bfloat16)
         self.idx_q_out = None
-        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.dev_err = dev_err if dev_err is not None else torch.zeros(1, dtype=torch.int32, device=device)
         dev = self.device = self.q_out.device
         bsp._cache_desc("K/V", kv, dev), bsp._cache_desc("index", idx, dev)
         self.heads = (num_q_heads, kv.num_kv_heads if kv is not None else 0, idx.num_heads if idx is not None else 0)
@@ -289,7 +290,7 @@ class NormRopeWrite:
             a.rope_table = bsp._dense("rope_table", rope_table, torch.float32, dev)
             a.rope_rows, a.rot_dim = rope_table.shape
             a.rope_pairs = int(rope_pairs)
-        a.dev_err = self.dev_err.data_ptr()
+        a.dev_err = bsp._dense("dev_err", self.dev_err, torch.int32, dev, 1)
         a.q_out = self.q_out.data_ptr()
 
     def run(self, q, k, v, idx_q, idx_k, positions, slot, stream=None):
@@ -337,20 +338,22 @@ class DenseStep:
     requests' lengths to the attention output: the step's tables, norms and
     rotation with the cache write, row lengths, dense attention.  Every
     request brings q_len tokens (1..8) or none; batches padded to num_seqs
-    have requests of context 0 and no tokens."""
+    have requests of context 0 and no tokens.  dev_err collects the error bits of
+    all its calls."""
 
     def __init__(self, kv, num_q_heads, num_seqs, q_len, bt_stride, sm_scale=None, q_dtype=bsp.FP8_E4M3,
                  device="cuda", **norm):
         tokens = num_seqs * q_len
         self.kv, self.q_len, self.num_q_heads, self.sm_scale, self.q_dtype = kv, q_len, num_q_heads, sm_scale, q_dtype
-        self.tables = StepTables(num_seqs, bt_stride, tokens, kv.num_blocks, device=device)
-        self.norm = NormRopeWrite(kv, None, num_q_heads, tokens, q_dtype=q_dtype, device=device, **norm)
+        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.tables = StepTables(num_seqs, bt_stride, tokens, kv.num_blocks, device=device, dev_err=self.dev_err)
+        self.norm = NormRopeWrite(kv, None, num_q_heads, tokens, q_dtype=q_dtype, device=device, dev_err=self.dev_err,
+                                  **norm)
         rows = tokens * kv.num_kv_heads
         self.row_seq = torch.empty(rows, dtype=torch.int32, device=device)
         self.row_len = torch.empty(rows, dtype=torch.int32, device=device)
         self.ws = bsp.dense_pa_workspace(rows, kv.num_kv_heads, num_q_heads // kv.num_kv_heads, q_len, device)
         self.out = torch.empty(tokens, num_q_heads, 128, dtype=torch.bfloat16, device=device)
-        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
 
     def run(self, context_lens, new_lens, free_blocks, free_head, q, k, v, stream=None):
         """Lengths and free blocks as in StepTables.run; q, k, v bf16 rows of
