@@ -457,6 +457,8 @@ def kv_page_read(kv, idx, slot, k=None, v=None, idx_k=None, dev_err=None, stream
         idx_k = idx_k if idx_k is not None else _new(shape, torch.bfloat16, slot.device, stream)
     elif idx_k is not None:
         raise ValueError("idx_k needs an index cache")
+    if T == 0:  # (empty tensors have no address)
+        return k, v, idx_k
     bf = torch.bfloat16
     n, ni = T * kv.num_kv_heads * 128 if kv is not None else 0, T * idx.num_heads * 128 if idx is not None else 0
     _check("bsp_kv_page_read",

@@ -13,6 +13,9 @@ class Lib:
     def __getattr__(self, name):
         return lambda *a: 4096 if name.endswith("_bytes") else 0
 
+    def bsp_kv_page_read(self, kv, idx, slot, n, k, v, idx_k, *a):
+        return int(bool(k) != bool(v))
+
 
 class Stream:
     device, cuda_stream = torch.device("cpu"), 0
@@ -84,3 +87,10 @@ def test_a_workspace_for_a_stream_comes_from_its_pool(made, name):
     make(*args, device="cpu", stream=side)
     make(*args, device="cpu")
     assert made == [side, None]
+
+
+def test_a_read_of_no_tokens_into_given_rows(made):
+    """Empty tensors have no address: a given k beside an empty v is not a missing one."""
+    k = torch.ones(4, 1, 128, dtype=torch.bfloat16)
+    got = bsp.kv_page_read(KV, IDX, torch.ones(0, dtype=torch.int64), k=k, stream=Stream())
+    assert got[0] is k and got[1].shape == got[2].shape == (0, 1, 128)
