@@ -587,8 +587,12 @@ bsp_status bsp_kv_page_read(const bsp_kv_cache* kv, const bsp_index_cache* idx, 
  *         computed with the first row's.
  * A block id out of range sets BSP_DEVERR_BLOCK_ID and its tokens are left
  * out.  Bytes at and past L_r are never used by row r, whatever they hold.  A
- * scale byte 255 is a NaN.  Weights are rounded to f16 and sums are fp32; values
- * of V of 2^90 and more may come out as infinite.
+ * scale byte 255 is a NaN, and a row whose query holds an infinity or a NaN is
+ * NaN.  Weights are rounded to f16 and sums are fp32; a bf16 query is taken as
+ * two e4m3 parts with a scale for 32 dims (exact for elements down to 2^-13 of
+ * their 32's largest, off by at most 2^-21 of it below); values of V of 2^90 and
+ * more may come out as infinite, as may rows whose q k sums leave fp32's range
+ * come out as NaN or zeros.
  * One launch, two where shares of the work cut a sequence.
  * ws: device workspace of bsp_dense_pa_workspace_bytes() bytes, 16-byte
  * aligned (its contents need not be set, and carry nothing from call to
