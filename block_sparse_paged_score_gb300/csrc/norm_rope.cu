@@ -396,10 +396,16 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t 
   for (int k = 0; k < kHeadTypes; ++k) total += p.heads[k];
   if (total == 0 || p.num_tokens == 0) return cudaSuccess;
   const int64_t groups = (static_cast<int64_t>(p.num_tokens) + kThreads / 16 - 1) / (kThreads / 16);
-  // all heads of a token in one half-warp once that gives each SM three CTAs
-  // (measured at 20 heads: 9.9 and 13.7 us at 2048 tokens, 17.1 and 15.0 at 4096,
-  // 34.0 and 20.8 at 8192, 80.5 and 42.1 at 16456)
-  const bool many = groups >= static_cast<int64_t>(num_sms) * 3;
+  // All heads of a token in one half-warp, from 2 + 15 / (heads - 4) CTAs an SM on: what
+  // a token costs once is spared only with some heads more, and the chain of a token's
+  // heads has to fit the batch.  Measured, us, a head a CTA and a token a half-warp:
+  //   5 heads    4096 tokens  8.4, 10.1   8192 13.5, 14.2   16456  23.6, 24.6
+  //   8 heads    4096        10.1, 11.2   6000 13.2, 14.9    8192  17.1, 15.5
+  //   20 heads   2048        10.0, 13.3   3648 15.9, 15.0    8192  33.3, 21.5
+  //   40 heads   2560        21.2, 23.8   4096 33.2, 27.1   16456 149.7, 76.9
+  //   80 heads   2048        33.1, 42.8   2560 45.2, 45.1    4096  75.2, 54.8
+  const int64_t more = total - 4;
+  const bool many = more > 0 && groups * more >= num_sms * (2 * more + 15);
   auto launch = [&](auto pairs) {
     return many ? launch_kernel(norm_rope_token_kernel<pairs>, dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, s,
                                 0, p)
