@@ -49,12 +49,12 @@
 // of 2^kBias f16's range, down to 2^-25, reaches 2^-32 of the row's largest.  z, m,
 // l and O are fp32.  The sums l are those of the unrounded weights.
 //
-// Measured (64 requests x 131072 tokens, 16 rows: 1.14 GB): 225 us, 5.1 TB/s; 128 x
-// 32768 with 64 rows: 0.57 GB in 227 us.  What bounds it is instruction issue and
-// the chain of a block through a CTA (wait, logits, vote, exponentials, V's
-// conversion, fences), which four CTAs an SM (two of 64 rows) overlap: 2 500 warp
+// Measured (64 requests x 131072 tokens, 16 rows: 1.14 GB): 226 us, 5.1 TB/s; 128 x
+// 32768 with 64 rows: 0.57 GB in 224 to 233 us.  What bounds it is the chain of a block
+// through a CTA (wait, logits, vote, exponentials, V's conversion, fences), which four
+// CTAs an SM (two of 64 rows) overlap, beside instruction issue: 2 560 warp
 // instructions a block of 16 rows, 1 000 of them V's conversion, at 67 % of the
-// issue slots; 4 600 of 64 rows, at 60 %.  The tensor cores are 10 and 20 % busy.
+// issue slots; 4 670 of 64 rows, at 61 %.  The tensor cores are 10 and 20 % busy.
 // With three CTAs an SM 16 rows took 249 us.  PV on mma.sync, weights and V as
 // register fragments, took 289 us and 536 us: V's conversion and the loads of P
 // were repeated for every 16 rows.

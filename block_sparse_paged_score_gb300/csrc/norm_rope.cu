@@ -18,9 +18,10 @@
 //
 // Measured: 1 token 2.0 us (a launch); 16456 tokens of 16 + 1 + 1 + 1 + 1 heads, bf16
 // queries and fp8 caches, 42 us for 167 MB: 4.0 TB/s, 60 % of the copy rate.  There
-// the latency of loads and of shuffles (the mean's, the rotation's partners') bounds
-// it, beside 170 warp instructions for a head of two tokens at 59 % of the issue
-// slots; fewer instructions (190, 65 %) or loads further ahead did not shorten it.
+// the latency of loads and of shuffles (the mean's, and of rotation by halves the
+// partners', which this lane layout puts into another lane) bounds it, beside 177 warp
+// instructions for a head of two tokens at 60 % of the issue slots; loads further
+// ahead did not shorten it.
 #include <algorithm>
 #include <type_traits>
 
