@@ -77,6 +77,18 @@ class NormRopeArgs(C.Structure):
                 ("dev_err", C.c_void_p)]
 
 
+class KvScalesDesc(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p)]
+
+
+class PromptAttentionArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_stride", C.c_int64),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("num_tokens", C.c_int32), ("num_keys", C.c_int32),
+                ("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32), ("cu_q", C.c_void_p), ("cu_k", C.c_void_p),
+                ("num_seqs", C.c_int32), ("sm_scale", C.c_float), ("out", C.c_void_p), ("ws", C.c_void_p),
+                ("ws_bytes", C.c_size_t), ("dev_err", C.c_void_p)]
+
+
 _lib = None
 SYMBOLS = {
     "bsp_kv_cache_interleaved": [C.c_int32, C.c_int32, C.c_void_p, C.c_int64, C.c_float, C.c_float,
@@ -113,6 +125,16 @@ SYMBOLS = {
     "bsp_dense_pa_decode": [C.POINTER(KvCacheDesc), C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_int32,
                             C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_float, C.c_void_p, C.c_void_p,
                             C.c_size_t, C.c_void_p, C.c_void_p],
+    "bsp_kv_scaled_write": [C.POINTER(KvCacheDesc), C.POINTER(KvScalesDesc), C.c_void_p, C.c_int64, C.c_void_p,
+                            C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p],
+    "bsp_kv_scaled_read": [C.POINTER(KvCacheDesc), C.POINTER(KvScalesDesc), C.c_void_p, C.c_int32, C.c_void_p,
+                           C.c_void_p, C.c_void_p, C.c_void_p],
+    "bsp_dense_pa_fp8_workspace_bytes": [C.c_int32, C.c_int32, C.c_int32, C.c_int32],
+    "bsp_dense_pa_decode_fp8": [C.POINTER(KvCacheDesc), C.POINTER(KvScalesDesc), C.c_void_p, C.c_int32, C.c_int32,
+                                C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_float,
+                                C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p],
+    "bsp_prompt_attention_workspace_bytes": [C.c_int32, C.c_int32, C.c_int32, C.c_int32],
+    "bsp_prompt_attention": [C.POINTER(PromptAttentionArgs), C.c_void_p],
     "bsp_kv_block_bytes": [C.c_int32, C.c_int32],
     "bsp_index_field_bytes": [C.c_int32],
     "bsp_status_str": [C.c_int32],
@@ -121,6 +143,7 @@ SYMBOLS = {
     "bsp_version": [],
 }
 RESTYPES = {"bsp_sparse_pa_decode_workspace_bytes": C.c_size_t, "bsp_dense_pa_workspace_bytes": C.c_size_t,
+            "bsp_dense_pa_fp8_workspace_bytes": C.c_size_t, "bsp_prompt_attention_workspace_bytes": C.c_size_t,
             "bsp_kv_block_bytes": C.c_int64,
             "bsp_index_field_bytes": C.c_int64, "bsp_status_str": C.c_char_p, "bsp_launch_count": C.c_int64}
 
@@ -231,6 +254,22 @@ class KvCache:
         _check("bsp_kv_cache_interleaved",
                lib().bsp_kv_cache_interleaved(dtype, num_kv_heads, _ptr(self.buffer), num_blocks, k_scale, v_scale,
                                               C.byref(self.desc)))
+
+
+class BlockScaledKvCache(KvCache):
+    """An interleaved fp8 K/V cache with a scale for each 128-token block and
+    head: k_scales and v_scales, fp32 [num_blocks, num_kv_heads], the caller's
+    or of its own.  Written by kv_scaled_write, read by kv_scaled_read and
+    dense_pa_decode_fp8."""
+
+    def __init__(self, num_kv_heads, num_blocks, buffer=None, k_scales=None, v_scales=None, device="cuda"):
+        super().__init__(FP8_E4M3, num_kv_heads, num_blocks, buffer=buffer, device=device)
+        n = num_blocks * num_kv_heads
+        self.k_scales, self.v_scales = (
+            t if t is not None else torch.zeros(num_blocks, num_kv_heads, device=self.buffer.device)
+            for t in (k_scales, v_scales))
+        self.scales = KvScalesDesc(_dense("k_scales", self.k_scales, torch.float32, self.buffer.device, n),
+                                   _dense("v_scales", self.v_scales, torch.float32, self.buffer.device, n))
 
 
 class IndexCache:
@@ -504,4 +543,135 @@ def dense_pa_decode(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, 
                                      rows, q_group, sm_scale, _dense("out", out, torch.bfloat16, dev, n),
                                      _dense("ws", ws, torch.uint8, dev), ws.numel(),
                                      _dense("dev_err", dev_err, i32, dev, 1), s.cuda_stream))
+    return out
+
+
+def _scales_desc(cache):
+    if not isinstance(cache, BlockScaledKvCache):
+        raise ValueError("the cache has no scales per block and head")
+    return C.byref(cache.scales)
+
+
+def kv_scaled_write(cache, k, v, slot, dev_err=None, stream=None):
+    """New tokens into a BlockScaledKvCache (bsp_kv_scaled_write): bf16 rows
+    k, v [T, Hkv, 128] (heads side by side, tokens any distance apart), int64
+    slots [T]; the tokens of a block follow each other."""
+    s = _on(stream)
+    dev = s.device
+    desc, scales = _cache_desc("K/V", cache, dev), _scales_desc(cache)
+    T = slot.numel()
+    if T == 0 and k.shape[0] == 0 and v.shape[0] == 0:  # (empty tensors have no address)
+        return
+    kp, ks = _head_rows("k", k, T, cache.num_kv_heads, dev)
+    vp, vs = _head_rows("v", v, T, cache.num_kv_heads, dev)
+    _check("bsp_kv_scaled_write",
+           lib().bsp_kv_scaled_write(desc, scales, kp, ks, vp, vs, _dense("slot", slot, torch.int64, dev), T,
+                                     _dense("dev_err", dev_err, torch.int32, dev, 1), s.cuda_stream))
+
+
+def kv_scaled_read(cache, slot, k=None, v=None, dev_err=None, stream=None):
+    """Tokens of a BlockScaledKvCache by slot as bf16 rows: (k, v)."""
+    s = _on(stream)
+    dev = s.device
+    desc, scales = _cache_desc("K/V", cache, dev), _scales_desc(cache)
+    T = slot.numel()
+    shape = (T, cache.num_kv_heads, 128)
+    k = k if k is not None else _new(shape, torch.bfloat16, slot.device, stream)
+    v = v if v is not None else _new(shape, torch.bfloat16, slot.device, stream)
+    if T == 0:
+        return k, v
+    n = T * cache.num_kv_heads * 128
+    _check("bsp_kv_scaled_read",
+           lib().bsp_kv_scaled_read(desc, scales, _dense("slot", slot, torch.int64, dev), T,
+                                    _dense("k", k, torch.bfloat16, dev, n), _dense("v", v, torch.bfloat16, dev, n),
+                                    _dense("dev_err", dev_err, torch.int32, dev, 1), s.cuda_stream))
+    return k, v
+
+
+def dense_pa_fp8_workspace_bytes(num_rows, num_kv_heads, group, q_group):
+    return int(lib().bsp_dense_pa_fp8_workspace_bytes(num_rows, num_kv_heads, group, q_group))
+
+
+def dense_pa_fp8_workspace(num_rows, num_kv_heads, group, q_group, device="cuda", stream=None):
+    """A workspace for dense attention calls of these sizes over fp8 caches that
+    never overlap on the GPU (its contents need not be set)."""
+    n = dense_pa_fp8_workspace_bytes(num_rows, num_kv_heads, group, q_group)
+    return _new(max(n, 16), torch.uint8, device, stream)
+
+
+def dense_pa_decode_fp8(kv, q, q_dtype, num_q_heads, block_table, row_seq, row_len, q_group, sm_scale=None, out=None,
+                        ws=None, dev_err=None, stream=None):
+    """dense_pa_decode over an fp8 cache (bsp_dense_pa_decode_fp8): a
+    BlockScaledKvCache, or a KvCache with its per-tensor scales."""
+    s = _on(stream)
+    dev, i32 = s.device, torch.int32
+    desc = _cache_desc("K/V", kv, dev)
+    scales = C.byref(kv.scales) if isinstance(kv, BlockScaledKvCache) else None
+    rows, hkv = row_len.numel(), kv.num_kv_heads
+    n = rows // hkv * num_q_heads * 128
+    sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
+    out = out if out is not None else _new(q.shape, torch.bfloat16, q.device, stream)
+    if ws is None:
+        ws = dense_pa_fp8_workspace(rows, hkv, num_q_heads // hkv, q_group, q.device, stream)
+    if block_table.dim() != 2:
+        raise ValueError("block_table is not [sequences, blocks]")
+    # e4m3 queries may be given as the type or as bytes
+    qt = torch.bfloat16 if q_dtype == BF16 else torch.float8_e4m3fn if q.dtype is torch.float8_e4m3fn else torch.uint8
+    _check("bsp_dense_pa_decode_fp8",
+           lib().bsp_dense_pa_decode_fp8(desc, scales, _dense("q", q, qt, dev, n), q_dtype, num_q_heads,
+                                         _dense("block_table", block_table, i32, dev), block_table.shape[1],
+                                         _dense("row_seq", row_seq, i32, dev, rows),
+                                         _dense("row_len", row_len, i32, dev), rows, q_group, sm_scale,
+                                         _dense("out", out, torch.bfloat16, dev, n),
+                                         _dense("ws", ws, torch.uint8, dev), ws.numel(),
+                                         _dense("dev_err", dev_err, i32, dev, 1), s.cuda_stream))
+    return out
+
+
+def prompt_attention_workspace_bytes(num_tokens, num_seqs, num_kv_heads, group):
+    return int(lib().bsp_prompt_attention_workspace_bytes(num_tokens, num_seqs, num_kv_heads, group))
+
+
+def prompt_attention_workspace(num_tokens, num_seqs, num_kv_heads, group, device="cuda", stream=None):
+    """A workspace for prompt attention calls of up to these sizes that never
+    overlap on the GPU (its contents need not be set)."""
+    n = prompt_attention_workspace_bytes(num_tokens, num_seqs, num_kv_heads, group)
+    return _new(max(n, 16), torch.uint8, device, stream)
+
+
+def prompt_attention(q, k, v, cu_q, cu_k=None, sm_scale=None, out=None, ws=None, dev_err=None, stream=None):
+    """Causal attention of packed prompts, or of chunks over their contexts
+    (bsp_prompt_attention): bf16 q [T, Hq, 128] and k, v [K, Hkv, 128] (heads
+    side by side, tokens any distance apart), int32 cu_q and cu_k (None: cu_q)
+    [sequences + 1].  Rows of no sequence are left as they were in `out`, or
+    are zero in one that the call makes."""
+    s = _on(stream)
+    dev, i32 = s.device, torch.int32
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v are not [tokens, heads, 128]")
+    (T, hq), (K, hkv) = q.shape[:2], k.shape[:2]
+    n = cu_q.numel() - 1
+    cu_k = cu_k if cu_k is not None else cu_q
+    if n < 0 or cu_k.numel() != n + 1:
+        raise ValueError("cu_q and cu_k are not of the same number of sequences")
+    if out is None:
+        out = _new(q.shape, torch.bfloat16, q.device, stream, zeroed=True)
+    if hq < 1 or hkv < 1 or hq % hkv:
+        raise ValueError(f"{hq} query heads over {hkv} KV heads")
+    a = PromptAttentionArgs()
+    a.q, a.q_stride = _head_rows("q", q, T, hq, dev)
+    # (a tensor of no rows has no address, and any strides)
+    a.k, a.k_stride = _head_rows("k", k, K, hkv, dev) if K else (None, hkv * 128)
+    a.v, a.v_stride = _head_rows("v", v, K, hkv, dev) if K or v.shape[0] else (None, hkv * 128)
+    a.num_tokens, a.num_keys, a.num_q_heads, a.num_kv_heads, a.num_seqs = T, K, hq, hkv, n
+    a.cu_q, a.cu_k = _dense("cu_q", cu_q, i32, dev), _dense("cu_k", cu_k, i32, dev)
+    a.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128)
+    a.out = _dense("out", out, torch.bfloat16, dev, T * hq * 128)
+    if T == 0 or n == 0:  # (empty tensors have no address)
+        return out
+    if ws is None:
+        ws = prompt_attention_workspace(T, n, hkv, hq // hkv, q.device, stream)
+    a.ws, a.ws_bytes = _dense("ws", ws, torch.uint8, dev), ws.numel()
+    a.dev_err = _dense("dev_err", dev_err, i32, dev, 1)
+    _check("bsp_prompt_attention", lib().bsp_prompt_attention(C.byref(a), s.cuda_stream))
     return out

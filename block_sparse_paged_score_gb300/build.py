@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libbsp.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "kv_write.cu", "index_score.cu", "index_score_mx_tc.cu", "index_score_prefill_tc.cu",
            "index_score_prefill_mx_tc.cu", "topk_select.cu", "sparse_pa.cu", "noalloc.cu",
-           "step_tables.cu", "norm_rope.cu", "kv_read.cu", "dense_pa.cu"]
+           "step_tables.cu", "norm_rope.cu", "kv_read.cu", "dense_pa.cu", "kv_scaled_write.cu",
+           "dense_pa_fp8.cu", "prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -659,6 +659,220 @@ bsp_status bsp_dense_pa_decode(const bsp_kv_cache* kv, const void* q, int32_t q_
 
 }  // extern "C"
 
+namespace {
+
+bsp_status check_scaled(const bsp_kv_cache* kv, const bsp_kv_scales* scales) {
+  const bsp_status st = check_kv(kv);
+  if (st != BSP_OK) return st;
+  if (kv->dtype != BSP_FP8_E4M3) return BSP_ERR_UNSUPPORTED;
+  if (!scales || !scales->k || !scales->v || !al(scales->k, 4) || !al(scales->v, 4)) return BSP_ERR_INVALID_ARG;
+  if (kv->num_kv_heads > (1 << 16)) return BSP_ERR_UNSUPPORTED;
+  return BSP_OK;
+}
+
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// whether one of `out` shares a byte with one of `in`, with another of `out` or with the cache
+template <size_t NO, size_t NI>
+bool spans_collide(const Span (&out)[NO], const Span (&in)[NI], const bsp_kv_cache* kv) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < NI; ++j)
+      if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+    if (overlap_cache(out[i].p, out[i].bytes, kv)) return true;
+  }
+  return false;
+}
+
+int64_t row_span(int64_t rows, int64_t stride, int64_t heads) { return rows ? ((rows - 1) * stride + heads * kDim) * 2 : 0; }
+
+}  // namespace
+
+extern "C" {
+
+bsp_status bsp_kv_scaled_write(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, const int64_t* slot, int32_t num_tokens,
+                               int32_t* dev_err, bsp_stream_t stream) {
+  bsp_status st = check_scaled(kv, scales);
+  if (st != BSP_OK) return st;
+  if (num_tokens < 0) return BSP_ERR_INVALID_ARG;
+  const int64_t heads = kv->num_kv_heads, T = num_tokens;
+  if (k_stride < heads * kDim || v_stride < heads * kDim || k_stride % 8 || v_stride % 8) return BSP_ERR_INVALID_ARG;
+  if (k_stride > (int64_t{1} << 32) || v_stride > (int64_t{1} << 32)) return BSP_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return BSP_OK;
+  if (!k || !v || !slot || !al(k, 16) || !al(v, 16) || !al(slot, 8) || !al(dev_err, 4)) return BSP_ERR_INVALID_ARG;
+  const Span in[] = {{k, row_span(T, k_stride, heads)}, {v, row_span(T, v_stride, heads)}, {slot, 8 * T}};
+  const Span out[] = {{scales->k, 4 * kv->num_blocks * heads}, {scales->v, 4 * kv->num_blocks * heads}, {dev_err, 4}};
+  if (spans_collide(out, in, kv)) return BSP_ERR_INVALID_ARG;
+  for (const Span& i : in)
+    if (overlap_cache(i.p, i.bytes, kv)) return BSP_ERR_INVALID_ARG;
+  KvScaledWriteParams p{};
+  p.base[0] = static_cast<uint8_t*>(kv->k_base);
+  p.base[1] = static_cast<uint8_t*>(kv->v_base);
+  p.scales[0] = scales->k;
+  p.scales[1] = scales->v;
+  p.src[0] = static_cast<const uint16_t*>(k);
+  p.src[1] = static_cast<const uint16_t*>(v);
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.id_stride = kv->id_stride_bytes;
+  p.num_blocks = kv->num_blocks;
+  p.hkv = kv->num_kv_heads;
+  p.slot = slot;
+  p.num_tokens = num_tokens;
+  p.err = dev_err;
+  st = cuda_status(launch_kv_scaled_write(p, device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+  if (st == BSP_OK) ++g_launches;
+  return st;
+}
+
+bsp_status bsp_kv_scaled_read(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const int64_t* slot,
+                              int32_t num_tokens, void* k, void* v, int32_t* dev_err, bsp_stream_t stream) {
+  bsp_status st = check_scaled(kv, scales);
+  if (st != BSP_OK) return st;
+  if (num_tokens < 0) return BSP_ERR_INVALID_ARG;
+  if (num_tokens == 0) return BSP_OK;
+  if (!slot || !k || !v || !al(slot, 8) || !al(k, 16) || !al(v, 16) || !al(dev_err, 4)) return BSP_ERR_INVALID_ARG;
+  const int64_t heads = kv->num_kv_heads, T = num_tokens;
+  if ((T + 15) / 16 * heads > INT32_MAX) return BSP_ERR_UNSUPPORTED;
+  const Span in[] = {{slot, 8 * T}, {scales->k, 4 * kv->num_blocks * heads}, {scales->v, 4 * kv->num_blocks * heads}};
+  const Span out[] = {{k, T * heads * kDim * 2}, {v, T * heads * kDim * 2}, {dev_err, 4}};
+  if (spans_collide(out, in, kv)) return BSP_ERR_INVALID_ARG;
+  KvReadParams p{};
+  set_caches(p.cache, kv, nullptr);
+  p.cache.slot = slot;
+  p.cache.num_tokens = num_tokens;
+  p.cache.err = dev_err;
+  p.k = static_cast<uint16_t*>(k);
+  p.v = static_cast<uint16_t*>(v);
+  p.k_scales = scales->k;
+  p.v_scales = scales->v;
+  st = cuda_status(launch_kv_page_read(p, reinterpret_cast<cudaStream_t>(stream)));
+  if (st == BSP_OK) ++g_launches;
+  return st;
+}
+
+size_t bsp_dense_pa_fp8_workspace_bytes(int32_t num_rows, int32_t num_kv_heads, int32_t group, int32_t q_group) {
+  if (num_rows <= 0 || num_kv_heads < 1 || num_rows % num_kv_heads || !valid_group(group) || q_group < 1 || q_group > 8)
+    return 0;
+  return dense_pa_fp8_ws_bytes(num_rows, num_kv_heads, group, q_group, device_sms());
+}
+
+bsp_status bsp_dense_pa_decode_fp8(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const void* q, int32_t q_dtype,
+                                   int32_t num_q_heads, const int32_t* block_table, int32_t bt_stride,
+                                   const int32_t* row_seq, const int32_t* row_len, int32_t num_rows, int32_t q_group,
+                                   float sm_scale, void* out, void* ws, size_t ws_bytes, int32_t* dev_err,
+                                   bsp_stream_t stream) {
+  bsp_status st = scales ? check_scaled(kv, scales) : check_kv(kv);
+  if (st != BSP_OK) return st;
+  if (kv->dtype != BSP_FP8_E4M3 || (q_dtype != BSP_BF16 && q_dtype != BSP_FP8_E4M3)) return BSP_ERR_UNSUPPORTED;
+  if (num_rows < 0 || num_q_heads < 1 || bt_stride < 1) return BSP_ERR_INVALID_ARG;
+  if (num_q_heads % kv->num_kv_heads || num_rows % kv->num_kv_heads) return BSP_ERR_INVALID_ARG;
+  const int32_t group = num_q_heads / kv->num_kv_heads;
+  if (!valid_group(group) || q_group < 1 || q_group > 8) return BSP_ERR_UNSUPPORTED;
+  if (!(sm_scale - sm_scale == 0.f)) return BSP_ERR_INVALID_ARG;  // infinite or NaN
+  if (num_rows == 0) return BSP_OK;
+  if (!q || !block_table || !row_seq || !row_len || !out || !al(q, 16) || !al(out, 16) || !al(block_table, 4) ||
+      !al(row_seq, 4) || !al(row_len, 4) || !al(dev_err, 4))
+    return BSP_ERR_INVALID_ARG;
+  const size_t need = dense_pa_fp8_ws_bytes(num_rows, kv->num_kv_heads, group, q_group, device_sms());
+  if (need && (!ws || ws_bytes < need || !al(ws, 16))) return BSP_ERR_WORKSPACE;
+  const int64_t heads = kv->num_kv_heads, n = num_rows, qn = n * group * kDim;
+  const Span in[] = {{q, qn * (q_dtype == BSP_BF16 ? 2 : 1)}, {row_seq, 4 * n}, {row_len, 4 * n},
+                     {scales ? scales->k : nullptr, 4 * kv->num_blocks * heads},
+                     {scales ? scales->v : nullptr, 4 * kv->num_blocks * heads}};
+  const Span outs[] = {{out, qn * 2}, {need ? ws : nullptr, static_cast<int64_t>(need)}, {dev_err, 4}};
+  if (spans_collide(outs, in, kv)) return BSP_ERR_INVALID_ARG;
+  DensePaFp8Params p{};
+  p.a.k_base = static_cast<const uint8_t*>(kv->k_base);
+  p.a.v_base = static_cast<const uint8_t*>(kv->v_base);
+  p.a.id_stride = kv->id_stride_bytes;
+  p.a.num_blocks = kv->num_blocks;
+  p.a.hkv = kv->num_kv_heads;
+  p.a.group = group;
+  p.a.q = q;
+  p.a.q_dtype = q_dtype;
+  p.a.block_table = block_table;
+  p.a.bt_stride = bt_stride;
+  p.a.row_seq = row_seq;
+  p.a.row_len = row_len;
+  p.a.num_rows = num_rows;
+  p.a.q_group = q_group;
+  p.a.sm_scale = sm_scale;
+  p.a.out = out;
+  p.a.ws = ws;
+  p.a.err = dev_err;
+  p.k_scales = scales ? scales->k : nullptr;
+  p.v_scales = scales ? scales->v : nullptr;
+  p.k_scale = kv->k_scale;
+  p.v_scale = kv->v_scale;
+  int launches = 0;
+  st = cuda_status(launch_dense_pa_fp8(p, device_sms(), reinterpret_cast<cudaStream_t>(stream), &launches));
+  g_launches += launches;
+  return st;
+}
+
+size_t bsp_prompt_attention_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t num_kv_heads, int32_t group) {
+  if (num_tokens < 1 || num_seqs < 1 || num_kv_heads < 1 || !valid_group(group)) return 0;
+  return prompt_ws_bytes(num_tokens, num_seqs, num_kv_heads, group, device_sms());
+}
+
+bsp_status bsp_prompt_attention(const bsp_prompt_attention_args* a, bsp_stream_t stream) {
+  if (!a || a->num_tokens < 0 || a->num_keys < 0 || a->num_seqs < 0 || a->num_q_heads < 1 || a->num_kv_heads < 1 ||
+      a->num_q_heads % a->num_kv_heads)
+    return BSP_ERR_INVALID_ARG;
+  const int32_t group = a->num_q_heads / a->num_kv_heads;
+  if (!valid_group(group)) return BSP_ERR_UNSUPPORTED;
+  const int64_t hq = a->num_q_heads, hkv = a->num_kv_heads, T = a->num_tokens, K = a->num_keys, n = a->num_seqs;
+  // (int32 tile counts, and the copies' strides)
+  if (hq > (1 << 16) || n > (1 << 20) || (T + n) * hq > INT32_MAX) return BSP_ERR_UNSUPPORTED;
+  for (int64_t st : {a->q_stride, a->k_stride, a->v_stride})
+    if (st % 8) return BSP_ERR_INVALID_ARG;
+  if (a->q_stride < hq * kDim || a->k_stride < hkv * kDim || a->v_stride < hkv * kDim) return BSP_ERR_INVALID_ARG;
+  if (a->q_stride > (int64_t{1} << 32) || a->k_stride > (int64_t{1} << 32) || a->v_stride > (int64_t{1} << 32))
+    return BSP_ERR_UNSUPPORTED;
+  if (!(a->sm_scale - a->sm_scale == 0.f)) return BSP_ERR_INVALID_ARG;  // infinite or NaN
+  if (T == 0 || n == 0) return BSP_OK;
+  if (!a->q || !a->out || !a->cu_q || !a->cu_k || !al(a->q, 16) || !al(a->out, 16) || !al(a->cu_q, 4) ||
+      !al(a->cu_k, 4) || !al(a->dev_err, 4))
+    return BSP_ERR_INVALID_ARG;
+  if (K && (!a->k || !a->v || !al(a->k, 16) || !al(a->v, 16))) return BSP_ERR_INVALID_ARG;
+  const size_t need = prompt_ws_bytes(a->num_tokens, a->num_seqs, a->num_kv_heads, group, device_sms());
+  if (need && (!a->ws || a->ws_bytes < need || !al(a->ws, 16))) return BSP_ERR_WORKSPACE;
+  const Span in[] = {{a->q, row_span(T, a->q_stride, hq)}, {a->k, row_span(K, a->k_stride, hkv)},
+                     {a->v, row_span(K, a->v_stride, hkv)}, {a->cu_q, 4 * (n + 1)}, {a->cu_k, 4 * (n + 1)}};
+  const Span out[] = {{a->out, T * hq * kDim * 2}, {need ? a->ws : nullptr, static_cast<int64_t>(need)},
+                      {a->dev_err, 4}};
+  if (spans_collide(out, in, nullptr)) return BSP_ERR_INVALID_ARG;
+  PromptParams p{};
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.k = static_cast<const uint16_t*>(a->k);
+  p.v = static_cast<const uint16_t*>(a->v);
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.num_tokens = a->num_tokens;
+  p.num_keys = a->num_keys;
+  p.hkv = a->num_kv_heads;
+  p.group = group;
+  p.cu_q = a->cu_q;
+  p.cu_k = a->cu_k;
+  p.num_seqs = a->num_seqs;
+  p.sm_scale = a->sm_scale;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.ws = a->ws;
+  p.err = a->dev_err;
+  int launches = 0;
+  const bsp_status st = cuda_status(launch_prompt(p, device_sms(), reinterpret_cast<cudaStream_t>(stream), &launches));
+  g_launches += launches;
+  return st;
+}
+
+}  // extern "C"
+
 extern "C" {
 
 static bsp_status sparse_pa_common(const bsp_kv_cache* kv, const void* q, int32_t q_dtype, int32_t num_q_heads,

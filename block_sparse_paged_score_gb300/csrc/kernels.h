@@ -269,6 +269,8 @@ struct KvReadParams {
   uint16_t* k;
   uint16_t* v;
   uint16_t* idx_k;
+  const float* k_scales;  // fp8: [blocks][hkv], or NULL: the cache's k_scale and v_scale
+  const float* v_scales;
 };
 cudaError_t launch_kv_page_read(const KvReadParams& p, cudaStream_t s);
 
@@ -292,5 +294,47 @@ struct DensePaParams {
 };
 size_t dense_pa_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms);
 cudaError_t launch_dense_pa(const DensePaParams& p, int num_sms, cudaStream_t s, int* launches);
+
+// new tokens into an fp8 cache with a scale per block and head
+struct KvScaledWriteParams {
+  uint8_t* base[2];          // K, V
+  float* scales[2];
+  const uint16_t* src[2];
+  int64_t stride[2];         // elements between tokens
+  int64_t id_stride, num_blocks;
+  int32_t hkv;
+  const int64_t* slot;
+  int32_t num_tokens;
+  int32_t* err;
+};
+cudaError_t launch_kv_scaled_write(const KvScaledWriteParams& p, int num_sms, cudaStream_t s);
+
+// dense attention over an fp8 cache: the cache's fields as in DensePaParams
+struct DensePaFp8Params {
+  DensePaParams a;
+  const float* k_scales;  // [blocks][hkv], or NULL: k_scale and v_scale
+  const float* v_scales;
+  float k_scale, v_scale;
+};
+size_t dense_pa_fp8_ws_bytes(int32_t num_rows, int32_t hkv, int32_t group, int32_t q_group, int num_sms);
+cudaError_t launch_dense_pa_fp8(const DensePaFp8Params& p, int num_sms, cudaStream_t s, int* launches);
+
+// causal attention of packed prompts
+struct PromptParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  int32_t num_tokens, num_keys, hkv, group;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int32_t num_seqs;
+  float sm_scale;
+  uint16_t* out;
+  void* ws;
+  int32_t* err;
+};
+size_t prompt_ws_bytes(int32_t num_tokens, int32_t num_seqs, int32_t hkv, int32_t group, int num_sms);
+cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t s, int* launches);
 
 }  // namespace bsp

@@ -1,7 +1,7 @@
 // kv_read.cu -- the writer's inverse: cached K, V and index keys gathered by
-// slot and dequantised to bf16 rows (bsp_kv_page_read).
+// slot and dequantised to bf16 rows (bsp_kv_page_read, bsp_kv_scaled_read).
 //
-//   bf16   as stored;  fp8  e4m3 * scale, rounded to bf16
+//   bf16   as stored;  fp8  e4m3 * scale (the cache's, or the block's and head's), rounded to bf16
 //   MXFP4  e2m1 * 2^(e8m0 - 127), exact in bf16 (until it leaves its range); NaN for
 //          a scale byte 255
 //
@@ -94,9 +94,10 @@ __global__ void __launch_bounds__(128) kv_page_read_kernel(KvReadParams p) {
         uint8_t b[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) b[i] = src[(dd + 8 * i) * 16];
+        const float sc = p.v_scales ? p.v_scales[slot / kBlock * heads + h] : c.v_scale;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          s_v[t][dd + 8 * i] = static_cast<uint16_t>(pack_bf16x2(e4m3_to_float(b[i]) * c.v_scale, 0.f));
+          s_v[t][dd + 8 * i] = static_cast<uint16_t>(pack_bf16x2(e4m3_to_float(b[i]) * sc, 0.f));
       } else {
         const uint16_t* src = reinterpret_cast<const uint16_t*>(c.v_base + page * c.id_stride +
                                                                 static_cast<int64_t>(h) * 4096) +
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(128) kv_page_read_kernel(KvReadParams p) {
           if (dtype == BSP_FP8_E4M3)
             w = from_e4m3(*reinterpret_cast<const uint2*>(page + static_cast<int64_t>(h) * 2048 + (l >> 1) * 256 +
                                                           t * 16 + (l & 1) * 8),
-                          c.k_scale);
+                          p.k_scales ? p.k_scales[block * heads + h] : c.k_scale);
           else
             w = *reinterpret_cast<const uint4*>(page + static_cast<int64_t>(h) * 4096 + l * 256 + t * 16);
         }

@@ -30,6 +30,11 @@
  * MXFP4 cache, for layers without an indexer; bsp_kv_page_read gathers
  * cached tokens back as bf16.
  *
+ * Layers without an indexer over 8 bits: bsp_kv_scaled_write and
+ * bsp_kv_scaled_read keep an fp8 cache whose scales are per block and head,
+ * bsp_dense_pa_decode_fp8 attends over it (or over one with per-tensor
+ * scales), and bsp_prompt_attention attends within whole prompts or chunks.
+ *
  * Conventions shared by every call
  *  - Fixed sizes: 128-token blocks, 16-token pages, 8 pages per block side,
  *    head_dim 128 (the index key dim is 128 too).  Query heads per KV head
@@ -604,6 +609,124 @@ bsp_status bsp_dense_pa_decode(const bsp_kv_cache* kv, const void* q, int32_t q_
                                const int32_t* block_table, int32_t bt_stride, const int32_t* row_seq,
                                const int32_t* row_len, int32_t num_rows, int32_t q_group, float sm_scale, void* out,
                                void* ws, size_t ws_bytes, int32_t* dev_err, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Block-scaled 8-bit caches: an interleaved fp8 cache (see bsp_kv_cache; its
+ * k_scale and v_scale are not used) with a scale for each 128-token block and
+ * KV head, K and V apart:
+ *   K of token t of block b, head h = e4m3 * k[b * num_kv_heads + h]
+ * Both arrays are fp32 [num_blocks, num_kv_heads] in device memory.  A block's
+ * scales need not be set before its first token is written.
+ * ---------------------------------------------------------------------- */
+typedef struct bsp_kv_scales {
+  float* k;
+  float* v;
+} bsp_kv_scales;
+
+/* ------------------------------------------------------------------------
+ * bsp_kv_scaled_write -- new tokens quantised into a block-scaled cache, whose
+ * scales grow with what they hold.
+ *   k, v   bf16, head h of token t at base + t*stride + h*128 (strides in
+ *          elements, multiples of 8, >= Hkv*128); post-RoPE rows
+ *   slot   int64 [T] as in bsp_kv_page_write (negative: skipped; beyond the
+ *          cache: skipped, BSP_DEVERR_SLOT)
+ * A run is a stretch of consecutive tokens of the call whose slots are in one
+ * block.  For each run, head, and K and V apart, with a the largest finite
+ * magnitude of the run's rows,
+ *   s_run = the smallest power of two with a <= 448 * s_run, at least 2^-60
+ *           (also of zeros) and at most 2^119
+ *   s     = s_run where the run has offset 0 of the block: the block starts
+ *           anew, and what it held is void; else max(s_run, the block's scale)
+ *   the run's bytes = e4m3_sat(x / s), a NaN as NaN
+ *   where s is above the block's scale, every other byte of the block
+ *           = e4m3_sat(byte * (old scale / s)): exact but for values that
+ *           leave e4m3's normal range
+ * Of tokens of a run with the same slot the last one counts.  A block in two
+ * runs of one call: the block's bytes and scales are unspecified.
+ * No part of k, v, slot, the scales or dev_err may lie in the cache's pages,
+ * and the scales overlap nothing (else BSP_ERR_INVALID_ARG).  All inputs are
+ * device memory.  One launch.
+ * ---------------------------------------------------------------------- */
+bsp_status bsp_kv_scaled_write(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, const int64_t* slot, int32_t num_tokens,
+                               int32_t* dev_err, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsp_kv_scaled_read -- tokens of a block-scaled cache gathered by slot as bf16
+ * rows k, v [T, Hkv, 128]: e4m3 * scale in fp32, rounded to bf16.  Slots as in
+ * bsp_kv_page_read.
+ * ---------------------------------------------------------------------- */
+bsp_status bsp_kv_scaled_read(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const int64_t* slot,
+                              int32_t num_tokens, void* k, void* v, int32_t* dev_err, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsp_dense_pa_decode_fp8 -- bsp_dense_pa_decode over an fp8 cache:
+ *   out = softmax(sm_scale * q K^T) V over tokens t < L_r
+ * with the block-scaled cache's scales, or with kv's per-tensor scales where
+ * `scales` is NULL.  Arguments, row lengths, bad block ids, workspaces and the
+ * order of sums are as in bsp_dense_pa_decode, its alignment rules aside.
+ *   k scales  any value (z is what the formula makes of it)
+ *   v scales  positive; below 2^-60 (zero too) they count as 2^-60, negative
+ *             ones and NaN give rows of NaN
+ * Bytes and scales at and past L_r are never used by row r, whatever they
+ * hold.  A NaN byte of K gives NaN rows, one of V NaN in its dim of the rows
+ * that see it.  Weights are rounded to f16; sums and references are fp32.  A
+ * bf16 query row is taken as two e4m3 parts with one scale: exact for elements
+ * down to 2^-10 of the row's largest, off by at most 2^-18 of that below.
+ * ---------------------------------------------------------------------- */
+size_t bsp_dense_pa_fp8_workspace_bytes(int32_t num_rows, int32_t num_kv_heads, int32_t group, int32_t q_group);
+bsp_status bsp_dense_pa_decode_fp8(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const void* q, int32_t q_dtype,
+                                   int32_t num_q_heads, const int32_t* block_table, int32_t bt_stride,
+                                   const int32_t* row_seq, const int32_t* row_len, int32_t num_rows, int32_t q_group,
+                                   float sm_scale, void* out, void* ws, size_t ws_bytes, int32_t* dev_err,
+                                   bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * bsp_prompt_attention -- causal grouped-query attention of whole prompts, or of
+ * chunks over their contexts, packed one behind the other (layers without an
+ * indexer; [MSA-API] forward: prefill rows of different requests in one call):
+ *   sequence s has the queries cu_q[s] .. cu_q[s+1]-1 and the keys cu_k[s] ..
+ *   cu_k[s+1]-1, the last query aligned with the last key: of nq queries and nk
+ *   keys query i sees the first L_i = max(0, nk - nq + i + 1)
+ *   out_i = softmax(sm_scale * q_i K^T) V over them, zeros where L_i = 0
+ *   q     bf16 [num_tokens, Hq, 128], k, v bf16 [num_keys, Hkv, 128]; head h of
+ *         token t at base + t*stride + h*128 (strides in elements, multiples
+ *         of 8, >= heads*128)
+ *   cu_q, cu_k  int32 [num_seqs + 1], not decreasing; cu_k may be cu_q.  What
+ *         lies outside [0, num_tokens] or [0, num_keys], or decreases, is cut to
+ *         it and sets BSP_DEVERR_CAPACITY
+ *   out   bf16 [num_tokens, Hq, 128], dense; rows of no sequence are left as
+ *         they were.  It overlaps no input, nor does the workspace (else
+ *         BSP_ERR_INVALID_ARG)
+ * Keys that a query does not see never reach its row, whatever they hold; an
+ * infinity or NaN in one that it sees does.  Weights are rounded to bf16; sums
+ * and references are fp32.  The same inputs give the same bits.
+ * ws: device workspace of bsp_prompt_attention_workspace_bytes() bytes, 16-byte
+ * aligned (its contents need not be set, and carry nothing from call to
+ * call).  Calls that may overlap on the GPU, captured ones included, need
+ * workspaces of their own.
+ * ---------------------------------------------------------------------- */
+typedef struct bsp_prompt_attention_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  int32_t num_tokens; /* rows of q and out */
+  int32_t num_keys;   /* rows of k and v */
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int32_t num_seqs;
+  float sm_scale;
+  void* out;
+  void* ws;
+  size_t ws_bytes;
+  int32_t* dev_err;
+} bsp_prompt_attention_args;
+
+size_t bsp_prompt_attention_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t num_kv_heads, int32_t group);
+bsp_status bsp_prompt_attention(const bsp_prompt_attention_args* a, bsp_stream_t stream);
 
 /* ---- misc -------------------------------------------------------------- */
 const char* bsp_status_str(bsp_status s);
