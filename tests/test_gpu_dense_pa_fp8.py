@@ -54,9 +54,12 @@ def attend(p, scale=SCALE, per_tensor=None, err=None, **kw):
                                    v_scales=t(p["scales"][1]))
     else:
         c = bsp.KvCache(bsp.FP8_E4M3, p["hkv"], p["blocks"], *per_tensor, buffer=t(p["cache"]))
-    return bsp.dense_pa_decode_fp8(c, p["q"].cuda(), bsp.FP8_E4M3 if p["q8"] else bsp.BF16, p["hkv"] * p["group"],
-                                   t(p["table"]), t(p["row_seq"]), t(p["row_len"]), p["q_len"], sm_scale=scale,
-                                   dev_err=err, **kw)
+    own = err if err is not None else torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = bsp.dense_pa_decode_fp8(c, p["q"].cuda(), bsp.FP8_E4M3 if p["q8"] else bsp.BF16, p["hkv"] * p["group"],
+                                  t(p["table"]), t(p["row_seq"]), t(p["row_len"]), p["q_len"], sm_scale=scale,
+                                  dev_err=own, **kw)
+    assert err is not None or own.item() == 0
+    return out
 
 
 def close(got, o, a):

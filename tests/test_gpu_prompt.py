@@ -22,10 +22,13 @@ def problem(seed, nq, nk, hkv, group, pad=0):
                 cu_q=cu_q, cu_k=cu_k)
 
 
-def attend(p, scale=SCALE, **kw):
+def attend(p, scale=SCALE, dev_err=None, **kw):
     from block_sparse_paged_score_gb300 import bsp
     i = lambda a: torch.from_numpy(np.asarray(a, np.int32)).cuda()  # noqa: E731
-    return bsp.prompt_attention(p["q"], p["k"], p["v"], i(p["cu_q"]), i(p["cu_k"]), sm_scale=scale, **kw)
+    err = dev_err if dev_err is not None else torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = bsp.prompt_attention(p["q"], p["k"], p["v"], i(p["cu_q"]), i(p["cu_k"]), sm_scale=scale, dev_err=err, **kw)
+    assert dev_err is not None or err.item() == 0
+    return out
 
 
 def expected(p, scale=SCALE):
