@@ -672,7 +672,8 @@ bsp_status bsp_kv_scaled_read(const bsp_kv_cache* kv, const bsp_kv_scales* scale
  * hold.  A NaN byte of K gives NaN rows, one of V NaN in its dim of the rows
  * that see it.  Weights are rounded to f16; sums and references are fp32.  A
  * bf16 query row is taken as two e4m3 parts with one scale: exact for elements
- * down to 2^-10 of the row's largest, off by at most 2^-18 of that below.
+ * down to 2^-9 of the row's largest, off by at most 2^-17 of that below.  A row
+ * whose query holds an infinity or a NaN is NaN.
  * ---------------------------------------------------------------------- */
 size_t bsp_dense_pa_fp8_workspace_bytes(int32_t num_rows, int32_t num_kv_heads, int32_t group, int32_t q_group);
 bsp_status bsp_dense_pa_decode_fp8(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const void* q, int32_t q_dtype,
