@@ -8,24 +8,31 @@
 // a unit's keys end together.  It is two tiles of 128 rows.  Units' 128-key blocks laid
 // end to end, causal ones only, are cut into equal shares, one per CTA: the blocks of
 // a sequence's units are a closed sum, and a CTA finds its share by a prefix sum over the
-// sequences.  Of a unit that share borders cut each CTA leaves (m, l, O) in the
-// workspace, and a second kernel joins them; the order of all sums is fixed.
+// sequences.  Units of at most kWhole blocks stay whole.  Of a unit that share borders
+// cut each CTA leaves (m, l, O) in the workspace, and a second kernel joins them; the
+// order of all sums is fixed.
 //
 // Both products are tcgen05 MMAs, 128 x 128 x 16:
 //   S = Q K^T     A = Q, B = K, both from shared memory (TMA, 128-byte swizzle)
 //   O += P V      A = P, bf16, from TMEM, where it takes the place of S; B = V from
 //                 shared memory, its dims contiguous
 // TMEM holds S and O of both tiles, 512 columns.  While the tensor core works on one
-// tile, four warps take the exponentials of the other: a thread has a whole row, so
-// maxima and sums need no exchange.  Weights are 2^((z - m) c) against the row's
-// reference m, which moves (and O and l with it) only when the row's maximum passes it by
-// kMaxGrow.  That S of a block is there says that P V of the one before has ended: the
-// MMAs run in order, so the thread may then rescale its row of O.
+// tile, four warps take the exponentials of the other: a thread has a whole row, so sums
+// need no exchange.  Weights are 2^((z - m) c) against the row's reference m, the maximum of
+// its first block; there is no maximum in the loop.  A half block whose weights sum to
+// more than kMaxSum (each is at most that) takes a new reference from its own maximum, and O
+// and l with it.  P leaves in halves, and P V of the first runs while the second's
+// exponentials are taken.
 //
 // Keys that a row does not see have p = 0, and V's rows of such keys may hold
-// infinities and NaN, which 0 does not silence: two warps look through V's tile of
+// infinities and NaN, which 0 does not silence: four warps look through V's tile of
 // those blocks that some row does not see whole, put zeros in place of what is not
 // finite, and the rows that do see it get it added at the end.
+//
+// A producer warp finds the pieces, announces them to the others in a ring, and loads Q, K
+// and V; an issuer warp issues the MMAs; a fourth kind stores O: bf16 rows are staged in a
+// stage of the K / V ring that the producer grants after a piece's last block, and leave by
+// TMA (a row's 256 bytes from one thread touch 16 lines, 4096 clocks of a tile).
 //
 // Roundings: a weight is bf16, half a step 2^-8 off; z, m, l and O are fp32, and l sums
 // the unrounded weights.
@@ -46,31 +53,45 @@ namespace bsp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaxGrow = 8.f;             // log2
+constexpr float kMaxSum = 512.f;            // of a half block's weights
 constexpr float kNoMax = -3.402823466e38f;  // the maximum of no keys (finite: -inf - kNoMax stays -inf)
 constexpr float kBigRef = 1048576.f;        // references above it: (z - m) c instead of z c - (m c), whose rounding then counts
 constexpr int kRows = 256, kTile = 128;     // rows of a unit, of a tile
-constexpr int kThreads = 384;               // four warps for each tile, a producer, an issuer, two that check V
-constexpr int kWarpTma = 8, kWarpMma = 9;
+constexpr int kWhole = 4;                   // blocks of a unit that is not cut
+// four warps for each tile, then a producer, an issuer, one that stores, one that idles, four that check V
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpStore = 10, kWarpCheck = 12, kThreads = 512;
+constexpr int kReaders = 8 + 2 + 4;         // warps that read the announced pieces
 constexpr int kHalf = 16384, kTileBytes = 2 * kHalf;  // 128 rows of 64 dims; of 128
-constexpr int kStages = 5;                  // of K and V tiles, in the order K V K V
-constexpr int kRegsRow = 208, kRegsRest = 88;
-static_assert((8 * kRegsRow + 4 * kRegsRest) * 32 <= kThreads * 168);
+constexpr int kStages = 5, kPieces = 4;     // of K, V and O tiles; of announced pieces
+constexpr int kRegsRow = 184, kRegsRest = 64;
+static_assert((kRegsRow + kRegsRest) * 256 <= kThreads * 128);
 
 struct Params {
   PromptParams a;
   float c;  // |sm_scale| * log2(e)
   int32_t tokens, log_tokens;  // of a unit: 256 / G
-  int32_t ctas, least;         // shares have `least` blocks at least
+  int32_t ctas;
 };
 
+// A part of a unit, as its CTA's producer announces it.
+struct Piece {
+  int32_t tok0, tokens, see;  // first token, tokens, keys that the first one sees (may be <= 0)
+  int32_t b0, nblk;           // blocks; nblk 0: no more pieces
+  int32_t h, k0;              // KV head, the sequence's first key
+  uint32_t item;              // number of its first K tile in the ring's order
+  int32_t starts, ends;       // whether the unit's first and last blocks are in it
+  int32_t pieces, pad;        // of the unit, where it starts here and goes on
+};
 struct Smem {
   static constexpr int q = 0, kv = 2 * kTileBytes, bars = kv + kStages * kTileBytes;
   static constexpr int q_full = bars, q_empty = bars + 8, kv_full = bars + 16, kv_empty = kv_full + 8 * kStages,
-                       s_full = kv_empty + 8 * kStages, p_full = s_full + 16, o_full = p_full + 16, v_ok = o_full + 16,
-                       fin = v_ok + 8 * kStages, misc = fin + 8;
-  static constexpr int tmem = misc, bad = misc + 8;  // bad[8]: pieces with values of V that are not finite
-  static constexpr int walks = (bad + 32 + 7) / 8 * 8;
+                       v_look = kv_empty + 8 * kStages, v_ok = v_look + 8 * kStages, s_full = v_ok + 8 * kStages, p_full = s_full + 16, half = p_full + 32,
+                       o_full = half + 16, staged = o_full + 16, piece_full = staged + 16, piece_empty = piece_full + 8 * kPieces,
+                       fin = piece_empty + 8 * kPieces;
+  static constexpr int pieces = fin + 8;
+  static constexpr int tmem = pieces + kPieces * sizeof(Piece), bad = tmem + 8;  // bad[8]: pieces with values of V that are not finite
+  static constexpr int total = bad + 32;
+  static_assert(pieces % 8 == 0 && total <= 227 * 1024);
 };
 
 // a unit that share borders cut, by its first CTA
@@ -96,90 +117,82 @@ __device__ __forceinline__ Seq load_seq(const PromptParams& a, int s) {
   return r;
 }
 __device__ __forceinline__ int units_of(const Seq& s, const Params& p) { return (s.nq + p.tokens - 1) >> p.log_tokens; }
-// blocks of unit u: at least one (rows without keys still get their zeros)
+// blocks of unit u < units_of: at least one (rows without keys still get their zeros)
 __device__ __forceinline__ int blocks_of(const Seq& s, const Params& p, int u) {
-  const int64_t see = static_cast<int64_t>(s.nk) - s.nq + min((static_cast<int64_t>(u) + 1) << p.log_tokens, static_cast<int64_t>(s.nq));
-  return max(1, static_cast<int>((max(see, int64_t{0}) + 127) >> 7));
+  const int after = max(s.nq - static_cast<int>(min((static_cast<int64_t>(u) + 1) << p.log_tokens, int64_t{0x7FFFFFFF})), 0);
+  return static_cast<int>((static_cast<uint32_t>(max(s.nk - after, 1)) + 127u) >> 7);
 }
 // blocks of the units before u.  Unit i but the last sees off + (i + 1) T keys: the first
 // units have one block, the others ceil((off + (i + 1) T) / 128), T a power of two.
 __device__ __forceinline__ int64_t blocks_before(const Seq& s, const Params& p, int u) {
-  const int n = units_of(s, p);
-  const int64_t off = static_cast<int64_t>(s.nk) - s.nq, m = min(u, n - 1);
-  const int lg = p.log_tokens;
-  const int64_t one = max(int64_t{0}, min(m, (128 - off) >> lg));
+  const int n = units_of(s, p), m = min(u, n - 1), lg = p.log_tokens, off = s.nk - s.nq;  // (of both signs)
+  const int one = max(0, min(m, off > 128 ? 0 : static_cast<int>((128 - static_cast<int64_t>(off)) >> lg)));
   int64_t sum = one;
-  if (lg <= 7) {  // ceil((A + i + 1) / R), A = ceil(off / T), R = 128 / T
-    const int64_t A = -((-off) >> lg);
-    const int lr = 7 - lg;
-    auto upto = [&](int64_t x) {  // sum of ceil(y / R), 1 <= y <= x
-      const int64_t q = x >> lr, r = x & ((1 << lr) - 1);
-      return ((q * (q + 1) / 2) << lr) + r * (q + 1);
-    };
-    if (m > one) sum += upto(A + m) - upto(A + one);
-  } else {  // T = 256
-    const int64_t A = -((-off) >> 7);
-    if (m > one) sum += (m - one) * A + (m * (m + 1) - one * (one + 1));
+  if (m > one) {
+    if (lg <= 7) {  // ceil((A + i + 1) / R), A = ceil(off / T), R = 128 / T
+      const int A = -((-off) >> lg), lr = 7 - lg;
+      auto upto = [&](int x) {  // sum of ceil(y / R), 1 <= y <= x
+        const int64_t q = x >> lr;
+        return ((q * (q + 1) >> 1) << lr) + (x & ((1 << lr) - 1)) * (q + 1);
+      };
+      sum += upto(A + m) - upto(A + one);
+    } else {  // T = 256
+      sum += static_cast<int64_t>(m - one) * -((-off) >> 7) + (static_cast<int64_t>(m) * (m + 1) - static_cast<int64_t>(one) * (one + 1));
+    }
   }
   return u == n && n > 0 ? sum + blocks_of(s, p, n - 1) : sum;
 }
 __device__ __forceinline__ int64_t blocks_of_seq(const Seq& s, const Params& p) { return blocks_before(s, p, units_of(s, p)); }
 
-// A warp's walk over the pieces of a share [at, end) of the units' blocks, in shared
-// memory (a thread of a row has no registers for it); every lane writes the same values.
+// The producer's walk over the pieces of its share [at, end) of the units' blocks.  A
+// border inside a unit of at most kWhole blocks stands for the unit's end.
 struct Walk {
-  int64_t at, end, c0;  // c0: blocks of the sequences before s
-  int64_t per;          // blocks of a KV head of sequence s
-  int s, piece;
+  int64_t at, end, share;
+  int64_t ustart;  // of unit (s, h, u)
+  int s, h, u, nb;
   Seq q;
-  // the piece at `at`
-  int64_t uend;
-  int h, tok0, tokens, see, b0, nblk;  // see: keys that the unit's first token sees
-  bool starts, ends;
 
-  __device__ __forceinline__ bool next(const Params& p) {
-    __syncwarp();  // (the lanes have read the piece before)
-    if (at >= end) return false;
-    const int64_t at = this->at;
-    const int number = piece + 1;
-    int s = this->s;
-    int64_t c0 = this->c0, per = this->per;
-    Seq q = this->q;
-    while (c0 + per * p.a.hkv <= at) {
-      c0 += per * p.a.hkv;
-      q = load_seq(p.a, ++s);
-      per = blocks_of_seq(q, p);
-    }
-    const int h = static_cast<int>((at - c0) / per);
+  // the unit that holds block `at`, of sequence s0 with c0 blocks before it
+  __device__ __forceinline__ void find(const Params& p, int s0, int64_t c0) {
+    s = s0, q = load_seq(p.a, s);
+    const int64_t per = blocks_of_seq(q, p);
+    h = static_cast<int>((at - c0) / per);
     const int64_t x = at - c0 - h * per;
     int lo = 0, hi = units_of(q, p) - 1;  // the last unit with blocks_before <= x
+#pragma unroll 1
     while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
+      const int mid = lo + ((hi - lo + 1) >> 1);
       if (blocks_before(q, p, mid) <= x)
         lo = mid;
       else
         hi = mid - 1;
     }
-    const int64_t ustart = c0 + h * per + blocks_before(q, p, lo), uend = ustart + blocks_of(q, p, lo);
-    const int t = lo << p.log_tokens;
-    __syncwarp();
-    this->s = s, this->c0 = c0, this->per = per, this->q = q, this->h = h;
-    this->uend = uend;
-    piece = number;
-    tok0 = q.q0 + t;
-    tokens = min(p.tokens, q.nq - t);
-    see = q.nk - q.nq + t + 1;
-    b0 = static_cast<int>(at - ustart);
-    nblk = static_cast<int>(min(end, uend) - at);
-    starts = at == ustart, ends = end >= uend;
-    this->at = min(end, uend);
-    __syncwarp();
+    u = lo, nb = blocks_of(q, p, u), ustart = c0 + h * per + blocks_before(q, p, u);
+    if (at > ustart && nb <= kWhole) at = ustart + nb;
+  }
+  __device__ __forceinline__ bool next(const Params& p, Piece& e) {
+    if (at >= end) return false;
+    if (at == ustart + nb) {  // the next unit
+      ustart = at, ++u;
+#pragma unroll 1
+      while (u >= units_of(q, p)) {
+        u = 0;
+        if (++h == p.a.hkv || units_of(q, p) == 0) h = 0, q = load_seq(p.a, ++s);
+      }
+      nb = blocks_of(q, p, u);
+    }
+    const int64_t uend = ustart + nb, to = nb <= kWhole ? uend : min(end, uend);
+    const int t = u << p.log_tokens;
+    e.tok0 = q.q0 + t, e.tokens = min(p.tokens, q.nq - t), e.see = q.nk - q.nq + t + 1;
+    e.b0 = static_cast<int>(at - ustart), e.nblk = static_cast<int>(to - at);
+    e.h = h, e.k0 = q.k0;
+    e.starts = at == ustart, e.ends = to == uend;
+    // pieces of the unit: shares from this one to that of its last block
+    e.pieces = e.starts && !e.ends ? static_cast<int>((uend - 1) / share) - static_cast<int>(blockIdx.x) + 1 : 0;
+    at = to;
     return true;
   }
 };
-
-constexpr int kSmem = Smem::walks + kThreads / 32 * static_cast<int>(sizeof(Walk));
-static_assert(kSmem <= 227 * 1024);
 
 // ---- device helpers ------------------------------------------------------------------
 __device__ __forceinline__ void tile_g2s_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
@@ -188,6 +201,12 @@ __device__ __forceinline__ void tile_g2s_3d(uint32_t dst, const CUtensorMap* m, 
                 "[%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+// by the calling thread
+__device__ __forceinline__ void tile_s2g_3d(const CUtensorMap* m, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x), "r"(y),
+               "r"(z), "r"(src)
+               : "memory");
 }
 // D (+)= A B, both bf16 in shared memory
 __device__ __forceinline__ void umma_ss_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -206,19 +225,22 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// After the wait for loads: what reads the registers comes behind it.
+// Waits for the warp's loads; what reads the registers comes behind it.
 __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; i += 8)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                  "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 // K-major rows of 128 bytes, 128-byte swizzle (see smem_desc_sw128); V as the B operand
@@ -237,12 +259,20 @@ constexpr uint32_t kIdescO = kIdescS | (1u << 16);
 
 // one 32-bit word of two bf16: bits 15 and 31 where a half is infinite or NaN
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+// acc + 0 * w, both halves: NaN once a half of a w was infinite or NaN
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t acc, uint32_t w) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(acc));
+  return r;
+}
 
-// What rows see of V's values that are not finite, in keys [from, to) (the tiles that
-// the MMAs read hold zeros in their place), added to dims d0 .. d0 + 31 of a row.
+// What a row sees of V's values that are not finite, in keys [from, to) (the tiles that
+// the MMAs read hold zeros in their place), added to its dims d0 .. d0 + 31.
 __device__ __forceinline__ void add_not_finite(const PromptParams& a, float (&o)[32], int k0, int h, int from, int to, int d0) {
+#pragma unroll 1
   for (int t = from; t < to; ++t) {
     const uint16_t* v = a.v + (k0 + static_cast<int64_t>(t)) * a.v_stride + h * kDim + d0;
+#pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if ((v[i] & 0x7F80) == 0x7F80) {
 #pragma unroll
@@ -255,7 +285,8 @@ __device__ __forceinline__ void add_not_finite(const PromptParams& a, float (&o)
 // ---- the main kernel -------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
+                  const __grid_constant__ CUtensorMap map_o1, const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   // before the first tile Q's place serves the scan
   int64_t* s_sum = reinterpret_cast<int64_t*>(smem);  // [warps]
@@ -269,9 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + at) + i, count);
     };
     init(Smem::q_full, 1, 1), init(Smem::q_empty, 1, 1);
-    init(Smem::kv_full, kStages, 1), init(Smem::kv_empty, kStages, 1);
-    init(Smem::s_full, 2, 1), init(Smem::p_full, 2, 4), init(Smem::o_full, 2, 1);
-    init(Smem::v_ok, kStages, 2), init(Smem::fin, 1, 1);
+    init(Smem::kv_full, kStages, 1), init(Smem::kv_empty, kStages, 1), init(Smem::v_look, kStages, 1), init(Smem::v_ok, kStages, 4);
+    init(Smem::s_full, 2, 1), init(Smem::p_full, 4, 4), init(Smem::half, 2, 1), init(Smem::o_full, 2, 1);
+    init(Smem::staged, 2, 4), init(Smem::piece_full, kPieces, 1), init(Smem::piece_empty, kPieces, kReaders);
+    init(Smem::fin, 1, 1);
     mbar_fence_init();
   }
   if (tid < 8) reinterpret_cast<volatile int*>(smem + Smem::bad)[tid] = 0;
@@ -305,16 +337,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 31) s_sum[warp] = upto;
   __syncthreads();
   int64_t total = 0;
-#pragma unroll 1
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) upto += s_sum[w];
-    total += s_sum[w];
+    const int64_t x = s_sum[w];
+    if (w < warp) upto += x;
+    total += x;
   }
-  const int64_t share = max((total + p.ctas - 1) / p.ctas, static_cast<int64_t>(p.least)), at = blockIdx.x * share;
+  const int64_t share = max((total + p.ctas - 1) / p.ctas, int64_t{1}), at = blockIdx.x * share;
   if (upto - mine <= at && at < upto) {
     int64_t c = upto - mine;
     int s = s_lo;
-    for (; s < s_hi; ++s) {
+#pragma unroll 1
+    for (; s + 1 < s_hi; ++s) {
       const int64_t b = blocks_of_seq(load_seq(a, s), p) * a.hkv;
       if (at < c + b) break;
       c += b;
@@ -326,57 +360,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(smem + Smem::tmem), 0);
-  Walk& w = reinterpret_cast<Walk*>(smem + Smem::walks)[warp];
-  if (lane == 0) {
-    w.at = at, w.end = min(at + share, total);
-    w.piece = -1, w.s = 0, w.c0 = 0, w.per = 0;
-    if (at < w.end) {
-      w.s = static_cast<int>(s_start[0]), w.c0 = s_start[1];
-      w.q = load_seq(a, w.s);
-      w.per = blocks_of_seq(w.q, p);
-    }
-  }
+  const int start_s = at < total ? static_cast<int>(s_start[0]) : 0;
+  const int64_t start_c = at < total ? s_start[1] : 0;
   __syncthreads();  // the scan's place is Q's again
-  Cut* cut = static_cast<Cut*>(a.ws);
-  if (tid == 0) cut[blockIdx.x].pieces = 0;
   bool alive = true;
   auto wait = [&](uint32_t bar, uint32_t parity) { return alive = alive && wait_warp(bar, parity, a.err); };
+  // the next announced piece (nblk 0: no more)
+  uint32_t number = 0;
+  auto next = [&](Piece& e) {
+    const uint32_t i = number % kPieces;
+    if (!wait(base + Smem::piece_full + 8 * i, number / kPieces & 1)) return false;
+    e = reinterpret_cast<const Piece*>(smem + Smem::pieces)[i];
+    __syncwarp();
+    if (lane == 0) arrive(base + Smem::piece_empty + 8 * i);
+    ++number;
+    return e.nblk > 0;
+  };
+  auto stage_of = [](uint32_t item) { return item % kStages; };
+  auto phase_of = [](uint32_t item) { return item / kStages & 1; };
+  Piece e;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kWarpTma) {
-      // ---- producer: Q of each piece, then K and V of its blocks ----
-      uint32_t st = 0, phase = 1, q_phase = 1;  // (an empty stage's wait passes at once)
+      // ---- producer: announces each piece, loads Q, and K and V of its blocks ----
+      Walk w;
+      w.at = at, w.end = min(at + share, total), w.share = share;
+      const bool any = at < w.end;
+      if (any) w.find(p, start_s, start_c);
+      Cut* cut = static_cast<Cut*>(a.ws);
+      if (lane == 0) cut[blockIdx.x].pieces = 0;
+      uint32_t item = 0, q_loads = 0;
       auto load = [&](const CUtensorMap* m, int h, int row) {
-        if (!wait(base + Smem::kv_empty + 8 * st, phase)) return;
+        const uint32_t st = stage_of(item);
+        if (!wait(base + Smem::kv_empty + 8 * st, phase_of(item) ^ 1)) return;
         const uint32_t bar = base + Smem::kv_full + 8 * st, dst = base + Smem::kv + st * kTileBytes;
         arrive_expect(bar, kTileBytes);
         tile_g2s_3d(dst, m, 0, h, row, bar);
         tile_g2s_3d(dst + kHalf, m, 64, h, row, bar);
-        if (++st == kStages) st = 0, phase ^= 1;
+        ++item;
       };
-      while (alive && w.next(p)) {
-        if (!wait(base + Smem::q_empty, q_phase)) break;
-        const bool two = w.tokens > p.tokens / 2;
-        arrive_expect(base + Smem::q_full, two ? 2 * kTileBytes : kTileBytes);
-        for (int i = 0; i < (two ? 2 : 1); ++i)
-          for (int d = 0; d < 2; ++d)
-            tile_g2s_3d(base + Smem::q + i * kTileBytes + d * kHalf, &map_q, 64 * d, w.h * a.group,
-                        w.tok0 + i * (p.tokens / 2), base + Smem::q_full);
-        q_phase ^= 1;
+      bool more = true;
 #pragma unroll 1
-        for (int b = w.b0; alive && b < w.b0 + w.nblk; ++b) {
-          load(&map_k, w.h, w.q.k0 + b * kBlock);
-          if (alive) load(&map_v, w.h, w.q.k0 + b * kBlock);
+      for (uint32_t k = 0; alive && more; ++k) {
+        more = any && w.next(p, e);
+        if (!more) e.nblk = 0;
+        e.item = item;
+        const uint32_t i = k % kPieces;
+        if (!wait(base + Smem::piece_empty + 8 * i, (k / kPieces & 1) ^ 1)) break;
+        if (lane == 0) {
+          reinterpret_cast<Piece*>(smem + Smem::pieces)[i] = e;
+          if (more && e.pieces) cut[blockIdx.x] = {e.pieces, e.tok0, e.tokens, e.h, e.see, {0, 0, 0}};
+          arrive(base + Smem::piece_full + 8 * i);
+        }
+        __syncwarp();
+        if (!more) break;
+        const bool two = e.tokens > p.tokens / 2;
+        load(&map_k, e.h, e.k0 + e.b0 * kBlock);
+        if (!wait(base + Smem::q_empty, (q_loads & 1) ^ 1)) break;
+        arrive_expect(base + Smem::q_full, two ? 2 * kTileBytes : kTileBytes);
+        for (int t = 0; t < (two ? 2 : 1); ++t)
+          for (int d = 0; d < 2; ++d)
+            tile_g2s_3d(base + Smem::q + t * kTileBytes + d * kHalf, &map_q, 64 * d, e.h * a.group,
+                        e.tok0 + t * (p.tokens / 2), base + Smem::q_full);
+        ++q_loads;
+        load(&map_v, e.h, e.k0 + e.b0 * kBlock);
+#pragma unroll 1
+        for (int b = e.b0 + 1; alive && b < e.b0 + e.nblk; ++b) {
+          load(&map_k, e.h, e.k0 + b * kBlock);
+          if (alive) load(&map_v, e.h, e.k0 + b * kBlock);
+        }
+        if (e.starts && e.ends) {  // a stage each for O of the tiles
+          for (int t = 0; alive && t < (two ? 2 : 1); ++t) {
+            const uint32_t st = stage_of(item);
+            if (!wait(base + Smem::kv_empty + 8 * st, phase_of(item) ^ 1)) break;
+            if (lane == 0) arrive(base + Smem::kv_full + 8 * st);
+            ++item;
+          }
         }
       }
       // nothing may still write shared memory when the CTA leaves
-      if (q_phase == 0 || w.piece > 0) wait_warp(base + Smem::q_full, q_phase, a.err, kSleepWaitLimit);
-      for (uint32_t i = 0; i < kStages; ++i)
-        wait_warp(base + Smem::kv_full + 8 * i, i < st ? phase ^ 1 : phase, a.err, kSleepWaitLimit);
+      if (q_loads) wait_warp(base + Smem::q_full, (q_loads - 1) & 1, a.err, kSleepWaitLimit);
+      for (uint32_t i = item > kStages ? item - kStages : 0; i < item; ++i)
+        wait_warp(base + Smem::kv_full + 8 * stage_of(i), phase_of(i), a.err, kSleepWaitLimit);
     } else if (warp == kWarpMma) {
       // ---- issuer ----
-      uint32_t st = 0, phase = 0, q_phase = 0, p_phase = 0, ok_phase = 0;
+      uint32_t q_phase = 0, p_phase = 0, ok_phase = 0;
       const uint64_t q_desc = smem_desc_sw128(base + Smem::q), k_desc = smem_desc_sw128(base + Smem::kv);
       const uint64_t v_desc = desc_v(base + Smem::kv);
       auto scores = [&](int i, uint32_t stage) {  // S = Q K^T of a tile
@@ -388,48 +457,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(base + Smem::s_full + 8 * i);
       };
-      auto values = [&](int i, uint32_t stage, bool accumulate) {  // O (+)= P V of a tile
-        const uint64_t vd = v_desc + stage * (kTileBytes / 16);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * k, vd + k * (2048 / 16), kIdescO, accumulate || k > 0);
-      };
       auto fence = [] { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); };
-      auto step = [&] {
-        const uint32_t was = st;
-        if (++st == kStages) st = 0, phase ^= 1;
-        return was;
-      };
-      while (alive && w.next(p)) {
-        const bool two = w.tokens > p.tokens / 2;
-        const int masked = w.see >> 7;  // blocks from here on some row does not see whole (see < 0: all)
+      while (alive && next(e)) {
+        const bool two = e.tokens > p.tokens / 2;
+        const int masked = e.see >> 7;  // blocks from here on some row does not see whole (see < 0: all)
+        uint32_t item = e.item;
         if (!wait(base + Smem::q_full, q_phase)) break;
         q_phase ^= 1;
-        if (!wait(base + Smem::kv_full + 8 * st, phase)) break;
-        uint32_t ks = step();
+        if (!wait(base + Smem::kv_full + 8 * stage_of(item), phase_of(item))) break;
         fence();
-        scores(0, ks);
-        if (two) scores(1, ks);
-        commit(base + Smem::kv_empty + 8 * ks);
-        if (w.nblk == 1) commit(base + Smem::q_empty);
+        scores(0, stage_of(item));
+        if (two) scores(1, stage_of(item));
+        commit(base + Smem::kv_empty + 8 * stage_of(item));
+        if (e.nblk == 1) commit(base + Smem::q_empty);
 #pragma unroll 1
-        for (int j = 0; j < w.nblk; ++j) {
-          const bool more = j + 1 < w.nblk;
-          if (!wait(base + Smem::kv_full + 8 * st, phase)) break;
-          const uint32_t vs = step();
-          if (w.b0 + j >= masked) {
+        for (int j = 0; j < e.nblk; ++j, item += 2) {
+          const bool more = j + 1 < e.nblk;
+          const uint32_t vs = stage_of(item + 1), ks = stage_of(item + 2);
+          if (!wait(base + Smem::kv_full + 8 * vs, phase_of(item + 1))) break;
+          // (the ones that check wait for this one's word, not for the copy: of a stage whose
+          // turns they do not follow one by one its parity says nothing)
+          const bool check = e.b0 + j >= masked;
+          if (check && lane == 0) arrive(base + Smem::v_look + 8 * vs);
+          __syncwarp();
+          if (more && !wait(base + Smem::kv_full + 8 * ks, phase_of(item + 2))) break;
+          if (check) {
             if (!wait(base + Smem::v_ok + 8 * vs, ok_phase >> vs & 1)) break;
             ok_phase ^= 1u << vs;
           }
-          if (more && !wait(base + Smem::kv_full + 8 * st, phase)) break;
-          if (more) ks = step();
+          const uint64_t vd = v_desc + vs * (kTileBytes / 16);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i && !two) break;
-            if (!wait(base + Smem::p_full + 8 * i, p_phase >> i & 1)) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // O (+)= P V of 64 keys
+              if (!wait(base + Smem::p_full + 16 * i + 8 * half, p_phase >> i & 1)) break;
+              fence();
+#pragma unroll
+              for (int k = 4 * half; k < 4 * half + 4; ++k)
+                umma_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * k, vd + k * (2048 / 16), kIdescO, j > 0 || k > 0);
+              if (half == 0) commit(base + Smem::half + 8 * i);
+            }
+            if (!alive) break;
             p_phase ^= 1u << i;
-            fence();
-            values(i, vs, j > 0);
             if (more)
               scores(i, ks);
             else
@@ -438,47 +508,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!alive) break;
           commit(base + Smem::kv_empty + 8 * vs);
           if (more) commit(base + Smem::kv_empty + 8 * ks);
-          if (j + 2 == w.nblk) commit(base + Smem::q_empty);
+          if (j + 2 == e.nblk) commit(base + Smem::q_empty);
         }
       }
       // every MMA and commit has ended
       commit(base + Smem::fin);
       wait_warp(base + Smem::fin, 0, a.err, kSleepWaitLimit);
-    } else {
-      // ---- V of the blocks that some row does not see whole: each warp takes 64 dims ----
-      uint32_t st = 0, phase = 0;
-      const uint32_t half = base + Smem::kv + (warp - 10) * kHalf;
-      while (alive && w.next(p)) {
-        const int masked = w.see >> 7;
-#pragma unroll 1
-        for (int b = w.b0; b < w.b0 + w.nblk; ++b) {
-          if (++st == kStages) st = 0, phase ^= 1;  // (K's stage)
-          if (!wait(base + Smem::kv_full + 8 * st, phase)) break;  // (every one: a parity tells two turns of the ring apart)
-          if (b >= masked) {
-            const uint32_t at = half + st * kTileBytes + lane * 16;
-            uint32_t any = 0;
-#pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-              const uint4 v = lds128(at + i * 512);
-              any |= not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w);
-            }
-            if (__any_sync(0xffffffffu, any != 0)) {
-#pragma unroll 1
-              for (int i = 0; i < 32; ++i) {
-                const uint4 v = lds128(at + i * 512);
-                auto clean = [](uint32_t x) {
-                  const uint32_t m = not_finite(x);
-                  return x & ~((m >> 15) * 0xFFFFu);
-                };
-                sts128(at + i * 512, clean(v.x), clean(v.y), clean(v.z), clean(v.w));
-              }
-              if (lane == 0) reinterpret_cast<volatile int*>(smem + Smem::bad)[w.piece & 7] = w.piece + 1;
-              fence_proxy_async();
-            }
-            __syncwarp();
-            if (lane == 0) arrive(base + Smem::v_ok + 8 * st);
+    } else if (warp == kWarpStore) {
+      // ---- the staged rows of O to global memory ----
+      uint32_t phase = 0;
+      while (alive && next(e)) {
+        if (!(e.starts && e.ends)) continue;
+        const bool two = e.tokens > p.tokens / 2;
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+          const uint32_t st = stage_of(e.item + 2 * e.nblk + t), src = base + Smem::kv + st * kTileBytes;
+          if (!wait(base + Smem::staged + 8 * t, phase >> t & 1)) break;
+          phase ^= 1u << t;
+          const int tok0 = e.tok0 + t * (p.tokens / 2), tokens = min(e.tokens - t * (p.tokens / 2), p.tokens / 2);
+          if (tokens == p.tokens / 2) {
+            if (lane < 2) tile_s2g_3d(&map_o, 64 * lane, e.h * a.group, tok0, src + lane * kHalf);
+          } else {  // a token at a time: the rows behind are another sequence's
+            for (int i = lane; i < 2 * tokens; i += 32)
+              tile_s2g_3d(&map_o1, 64 * (i & 1), e.h * a.group, tok0 + (i >> 1), src + (i & 1) * kHalf + (i >> 1) * a.group * 128);
           }
-          if (++st == kStages) st = 0, phase ^= 1;
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) arrive(base + Smem::kv_empty + 8 * st);
+        }
+      }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    } else if (warp >= kWarpCheck) {
+      // ---- V of the blocks that some row does not see whole: a warp takes 64 rows of 64 dims ----
+      uint32_t look_phase = 0;
+      const uint32_t part = base + Smem::kv + (warp - kWarpCheck) * (kTileBytes / 4) + lane * 16;
+      while (alive && next(e)) {
+        const int masked = max(e.see >> 7, e.b0);
+#pragma unroll 1
+        for (int b = masked; b < e.b0 + e.nblk; ++b) {
+          const uint32_t item = e.item + 2 * (b - e.b0) + 1, st = stage_of(item);
+          if (!wait(base + Smem::v_look + 8 * st, look_phase >> st & 1)) break;
+          look_phase ^= 1u << st;
+          if (!wait(base + Smem::kv_full + 8 * st, phase_of(item))) break;
+          const uint32_t at = part + st * kTileBytes;
+          uint32_t acc[4] = {0, 0, 0, 0};
+#pragma unroll 8
+          for (int i = 0; i < 16; ++i) {
+            const uint4 v = lds128(at + i * 512);
+            acc[0] = add_zero_times(acc[0], v.x), acc[1] = add_zero_times(acc[1], v.y);
+            acc[2] = add_zero_times(acc[2], v.z), acc[3] = add_zero_times(acc[3], v.w);
+          }
+          const uint32_t any = not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]);
+          if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+              const uint4 v = lds128(at + i * 512);
+              auto clean = [](uint32_t x) { return x & ~((not_finite(x) >> 15) * 0xFFFFu); };
+              sts128(at + i * 512, clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+            }
+            if (lane == 0) reinterpret_cast<volatile int*>(smem + Smem::bad)[number & 7] = number;
+            fence_proxy_async();
+          }
+          __syncwarp();
+          if (lane == 0) arrive(base + Smem::v_ok + 8 * st);
         }
       }
     }
@@ -489,142 +581,170 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = warp >> 2, row = tid;  // of the unit
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * 128;
-    const uint32_t s_full = base + Smem::s_full + 8 * tile, p_full = base + Smem::p_full + 8 * tile;
+    const uint32_t s_full = base + Smem::s_full + 8 * tile, p_full = base + Smem::p_full + 16 * tile;
     uint32_t s_phase = 0, o_phase = 0;
-    const float c = p.c;
-    const bool neg = a.sm_scale < 0.f;
-    const int log_group = 8 - p.log_tokens;
-    while (alive && w.next(p)) {
-      const int tok = row >> log_group;  // of the unit
-      if (tile && w.tokens <= p.tokens / 2) continue;
-      const int see = tok < w.tokens ? max(w.see + tok, 0) : 0;                  // keys that the row sees
-      const int whole = (w.see + (tile ? p.tokens / 2 : 0)) >> 7;               // blocks that all rows of the tile see whole
-      float ref = kNoMax;
-      float2 l[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    const float c = p.c, sign = a.sm_scale < 0.f ? -1.f : 1.f, cs = c * sign;
+    const float none = -sign * INFINITY;  // a logit that is not seen
+    const int log_group = 8 - p.log_tokens, tok = row >> log_group;
+    const int tok_lo = (row & ~31) >> log_group, tok_hi = (row | 31) >> log_group;  // the warp's
+    while (alive && next(e)) {
+      if (tile && e.tokens <= p.tokens / 2) continue;
+      float ref = kNoMax, l = 0.f;
+      bool huge = false;
 #pragma unroll 1
-      for (int j = 0; j < w.nblk; ++j) {
+      for (int j = 0; j < e.nblk; ++j) {
         if (!wait(s_full, s_phase)) break;
-        s_phase ^= 1;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        uint32_t r[4][32];
+        // keys of the block that the row, and the first and last rows of the warp, see
+        const int from = (e.b0 + j) * kBlock, lim = e.see + tok - from, lim_lo = e.see + tok_lo - from,
+                  lim_hi = e.see + tok_hi - from;
+        uint32_t r[2][32];
+        auto load = [&](int half) {
+          tmem_ld32_issue(s_at + 64 * half, r[0]);
+          tmem_ld32_issue(s_at + 64 * half + 32, r[1]);
+          loaded(r[0]), loaded(r[1]);
+          if (lim_lo < 64 * half + 64) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32_issue(s_at + 32 * k, r[k]);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            for (int q = 0; q < 2; ++q)
+              if (lim_lo < 64 * half + 32 * q + 32) {
+                const int m = lim - 64 * half - 32 * q;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) loaded(r[k]);
-        const int b = w.b0 + j;
-        auto z = [&](int i) { return __uint_as_float(r[i >> 5][i & 31]); };
-        bool slow = b >= whole || neg;
-        if (slow) {
-          const int lim = b >= whole ? see - b * kBlock : kBlock;
-#pragma unroll
-          for (int i = 0; i < 128; ++i) {
-            const float x = neg ? -z(i) : z(i);
-            r[i >> 5][i & 31] = __float_as_uint(i < lim ? x : -INFINITY);
+                for (int i = 0; i < 32; ++i) r[q][i] = i < m ? r[q][i] : __float_as_uint(none);
+              }
           }
-        }
-        float mx[4];
+        };
+        auto largest = [&] {  // of the loaded half
+          float mx[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mx[k] = fmax3(z(32 * k), z(32 * k + 1), z(32 * k + 2));
+          for (int k = 0; k < 4; ++k) {
+            auto z = [&](int i) { return sign * __uint_as_float(r[k >> 1][16 * (k & 1) + i]); };
+            mx[k] = fmax3(z(0), z(1), z(2));
 #pragma unroll
-          for (int i = 3; i < 31; i += 2) mx[k] = fmax3(mx[k], z(32 * k + i), z(32 * k + i + 1));
-          mx[k] = fmaxf(mx[k], z(32 * k + 31));
-        }
-        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-        const bool moves = !((top - ref) * c <= kMaxGrow);
-        if (__any_sync(0xffffffffu, moves)) {
-          // the rows' references, and O and l in their terms
-          const float to = moves && top > ref ? top : ref, f = rescale(ref, to, c);
+            for (int i = 3; i < 15; i += 2) mx[k] = fmax3(mx[k], z(i), z(i + 1));
+            mx[k] = fmaxf(mx[k], z(15));
+          }
+          return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+        };
+        auto set_ref = [&](float to) {
           ref = to;
-          l[0].x *= f, l[0].y *= f, l[1].x *= f, l[1].y *= f;
-          if (j) {
+          huge = __any_sync(0xffffffffu, !(fabsf(ref * c) < kBigRef));
+        };
+        if (j == 0) {
+          load(0);
+          const float top = largest();
+          load(1);
+          set_ref(fmax3(ref, top, largest()));
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+          float sum;
+          auto weights = [&] {
+            float2 t[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            if (lim_hi <= 64 * half) {  // no row of the warp sees any
+#pragma unroll
+              for (int i = 0; i < 32; ++i) pk[i] = 0;
+            } else if (__builtin_expect(!huge, 1)) {
+              const float rc = -ref * c;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float2 x = ffma2({__uint_as_float(r[i >> 4][2 * (i & 15)]), __uint_as_float(r[i >> 4][2 * (i & 15) + 1])},
+                                       {cs, cs}, {rc, rc});
+                const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                t[i & 1] = fadd2(t[i & 1], w);
+                pk[i] = pack_bf16x2(w.x, w.y);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float u = (sign * __uint_as_float(r[i >> 4][2 * (i & 15)]) - ref) * c,
+                            v = (sign * __uint_as_float(r[i >> 4][2 * (i & 15) + 1]) - ref) * c;
+                const float2 w = make_float2(ex2_approx(u), ex2_approx(v));
+                t[i & 1] = fadd2(t[i & 1], w);
+                pk[i] = pack_bf16x2(w.x, w.y);
+              }
+            }
+            sum = (t[0].x + t[0].y) + (t[1].x + t[1].y);
+          };
+          load(half);
+          weights();
+          if (__builtin_expect(__any_sync(0xffffffffu, sum > kMaxSum), 0)) {
+            // the rows' references pass this half's maxima; O and l in their terms
+            load(half);
+            const float to = fmaxf(ref, largest()), f = rescale(ref, to, c);
+            set_ref(to);
+            l *= f;
+            if (j > 0 || half) {  // (S says that the block before is in O)
+              if (half) {
+                wait(base + Smem::half + 8 * tile, s_phase);
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              }
 #pragma unroll 1
-            for (int k = 0; k < 128; k += 16) {
-              float y[16];
-              tmem_ld<16>(o_at + k, y);
+              for (int k = 0; k < 128; k += 16) {
+                float y[16];
+                tmem_ld<16>(o_at + k, y);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] *= f;
-              tmem_st<16>(o_at + k, y);
+                for (int i = 0; i < 16; ++i) y[i] *= f;
+                tmem_st<16>(o_at + k, y);
+              }
             }
+            load(half);
+            weights();
           }
+          l += sum;
+          tmem_st32(s_at + 32 * half, pk);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && alive) arrive(p_full + 8 * half);
         }
-        const float rc = ref * c;
-        slow |= __any_sync(0xffffffffu, !(fabsf(rc) < kBigRef));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t pk[16];
-          if (__builtin_expect(!slow, 1)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = ffma2({z(32 * k + 2 * i), z(32 * k + 2 * i + 1)}, {c, c}, {-rc, -rc});
-              const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-              l[i & 1] = fadd2(l[i & 1], e);
-              pk[i] = pack_bf16x2(e.x, e.y);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = fmul2(fadd2({z(32 * k + 2 * i), z(32 * k + 2 * i + 1)}, {-ref, -ref}), {c, c});
-              const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-              l[i & 1] = fadd2(l[i & 1], e);
-              pk[i] = pack_bf16x2(e.x, e.y);
-            }
-          }
-          tmem_st16(s_at + 16 * k, pk);
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) arrive(p_full);
+        s_phase ^= 1;
       }
       if (!wait(base + Smem::o_full + 8 * tile, o_phase)) break;
       o_phase ^= 1;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       // -- O to where it goes
-      const float sum = (l[0].x + l[0].y) + (l[1].x + l[1].y);
-      const bool all = w.starts && w.ends;
-      const float f = !all ? 1.f : see == 0 ? 0.f : 1.f / sum;
-      const bool fix = reinterpret_cast<volatile int*>(smem + Smem::bad)[w.piece & 7] == w.piece + 1;
+      const bool all = e.starts && e.ends;
+      const int see = max(e.see + tok, 0);
+      const float f = !all ? 1.f : see == 0 ? 0.f : 1.f / l;
+      const bool fix = reinterpret_cast<volatile int*>(smem + Smem::bad)[number & 7] == static_cast<int>(number);
+      const uint32_t item = e.item + 2 * e.nblk + tile, stage = base + Smem::kv + stage_of(item) * kTileBytes + (row & 127) * 128;
+      if (all && !wait(base + Smem::kv_full + 8 * stage_of(item), phase_of(item))) break;
       // a CTA's slots: 2 * CTA for a unit that began before its share, + 1 for one that
-      // goes on after it
+      // goes on after it; [dims / 4][rows][4], then (m, l) of the rows
       float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
-                  (2LL * blockIdx.x + (w.starts ? 1 : 0)) * kSlotFloats;
-      const bool live = tok < w.tokens;
-      uint16_t* out = a.out + (static_cast<int64_t>(w.tok0 + tok) * a.hkv * a.group + w.h * a.group + (row & (a.group - 1))) * kDim;
+                  (2LL * blockIdx.x + (e.starts ? 1 : 0)) * kSlotFloats;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         uint32_t r[32];
         tmem_ld32_issue(o_at + 32 * k, r);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
         loaded(r);
         float o[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);
         if (__builtin_expect(fix, 0))
-          add_not_finite(a, o, w.q.k0, w.h, max(w.b0, max(w.see >> 7, 0)) * kBlock,
-                         live ? min(see, (w.b0 + w.nblk) * kBlock) : 0, 32 * k);
-        if (live) {
-          if (all) {
+          add_not_finite(a, o, e.k0, e.h, max(e.b0, max(e.see >> 7, 0)) * kBlock,
+                         tok < e.tokens ? min(see, (e.b0 + e.nblk) * kBlock) : 0, 32 * k);
+        if (all) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(out + 32 * k + i) =
-                  make_uint4(pack_bf16x2(o[i] * f, o[i + 1] * f), pack_bf16x2(o[i + 2] * f, o[i + 3] * f),
-                             pack_bf16x2(o[i + 4] * f, o[i + 5] * f), pack_bf16x2(o[i + 6] * f, o[i + 7] * f));
-          } else {
+          for (int i = 0; i < 4; ++i)  // 16-byte chunks of the swizzled row
+            sts128(stage + (k >> 1) * kHalf + (((4 * (k & 1) + i) ^ (row & 7)) << 4),
+                   pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
+                   pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
+        } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(po + row * kDim + 32 * k + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-          }
+          for (int i = 0; i < 8; ++i)
+            reinterpret_cast<float4*>(po)[(8 * k + i) * kRows + row] =
+                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
         __syncwarp();
       }
-      if (!all) *reinterpret_cast<float2*>(po + kRows * kDim + 2 * row) = make_float2(ref, sum);
+      if (!all) *reinterpret_cast<float2*>(po + kRows * kDim + 2 * row) = make_float2(ref, l);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      if (w.starts && !w.ends && tid == 0) {
-        // the pieces of the unit: shares from this one to that of its last block
-        cut[blockIdx.x] = {static_cast<int>((w.uend - 1) / share) - static_cast<int>(blockIdx.x) + 1, w.tok0, w.tokens, w.h,
-                           w.see, {0, 0, 0}};
+      if (all) {
+        fence_proxy_async();  // the copies read the stage through the async proxy
+        __syncwarp();
+        if (lane == 0) arrive(base + Smem::staged + 8 * tile);
       }
     }
     __syncwarp();
@@ -638,47 +758,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- cut units -----------------------------------------------------------------------------
-// Joins the pieces of the units that share borders cut: a warp takes a row.
+// Joins the pieces of the units that share borders cut.  A warp takes eight rows, a lane 32
+// dims of one of them, a fourth of each 16.
+constexpr int kJoinParts = 4;  // CTAs of a unit
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   pdl_trigger();
   const PromptParams& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x / (kRows / 8), row = (blockIdx.x % (kRows / 8)) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, log_group = 8 - p.log_tokens;
+  const int c0 = blockIdx.x / kJoinParts;
   const Cut u = static_cast<const Cut*>(a.ws)[c0];
-  const int log_group = 8 - p.log_tokens, tok = row >> log_group;
-  if (u.pieces == 0 || tok >= u.tokens) return;
+  if (u.pieces == 0) return;
+  const int row = blockIdx.x % kJoinParts * (kRows / kJoinParts) + (threadIdx.x >> 5) * 8 + (lane & 7), part = lane >> 3;
+  static_assert(kRows / kJoinParts == 64);
+  const int tok = row >> log_group;
+  if (tok >= u.tokens) return;
   const float* base = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + list_bytes(p.ctas));
-  float M = kNoMax, L = 0.f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < u.pieces; k0 += 32) {
-    const int k = k0 + lane;  // lane j: piece k0 + j
-    float2 ml = make_float2(kNoMax, 0.f);
-    if (k < u.pieces)
-      ml = *reinterpret_cast<const float2*>(base + (k ? 2LL * (c0 + k) : 2LL * c0 + 1) * kSlotFloats + kRows * kDim + 2 * row);
-    float mx = ml.x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const float mn = fmaxf(M, mx), f = rescale(M, mn, p.c), wt = rescale(ml.x, mn, p.c);
-    float ls = wt * ml.y;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
-    L = L * f + ls;
-    M = mn;
-    x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-    const int here = min(32, u.pieces - k0);
+  auto slot = [&](int k) { return base + (k ? 2LL * (c0 + k) : 2LL * c0 + 1) * kSlotFloats; };
+  float M = kNoMax;
 #pragma unroll 8
-    for (int j = 0; j < here; ++j) {
-      const int kj = k0 + j;
-      const float wj = __shfl_sync(0xffffffffu, wt, j);
-      const float4 y = *reinterpret_cast<const float4*>(base + (kj ? 2LL * (c0 + kj) : 2LL * c0 + 1) * kSlotFloats +
-                                                        row * kDim + 4 * lane);
-      x.x += wj * y.x, x.y += wj * y.y, x.z += wj * y.z, x.w += wj * y.w;
+  for (int k = 0; k < u.pieces; ++k) M = fmaxf(M, slot(k)[kRows * kDim + 2 * row]);
+  float L = 0.f;
+  float4 x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < u.pieces; ++k) {
+    const float2 ml = *reinterpret_cast<const float2*>(slot(k) + kRows * kDim + 2 * row);
+    const float w = rescale(ml.x, M, p.c);
+    L += w * ml.y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 y = reinterpret_cast<const float4*>(slot(k))[(4 * i + part) * kRows + row];
+      x[i].x += w * y.x, x[i].y += w * y.y, x[i].z += w * y.z, x[i].w += w * y.w;
     }
   }
   const float f = u.see + tok <= 0 ? 0.f : 1.f / L;
-  const int64_t e = (static_cast<int64_t>(u.tok0 + tok) * a.hkv * a.group + u.h * a.group + (row & (a.group - 1))) * kDim + 4 * lane;
-  *reinterpret_cast<uint2*>(a.out + e) = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+  uint16_t* out = a.out + (static_cast<int64_t>(u.tok0 + tok) * a.hkv * a.group + u.h * a.group + (row & (a.group - 1))) * kDim;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint2*>(out + 16 * i + 4 * part) =
+        make_uint2(pack_bf16x2(x[i].x * f, x[i].y * f), pack_bf16x2(x[i].z * f, x[i].w * f));
 }
 
 // ---- host ------------------------------------------------------------------------------------
@@ -710,26 +830,29 @@ cudaError_t launch_prompt(const PromptParams& a, int num_sms, cudaStream_t s, in
   p.tokens = kRows / a.group;
   while ((1 << p.log_tokens) < p.tokens) ++p.log_tokens;
   p.ctas = num_sms;
-  p.least = 2;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo, mo1;
   // (no keys at all: the maps of K and V have one row, Q's first, which no row sees)
   const bool keys = a.num_keys > 0;
   const int64_t hq = static_cast<int64_t>(a.hkv) * a.group;
   if (!make_map_rows(&mq, a.q, hq, a.num_tokens, a.q_stride, a.group, kTile / a.group) ||
       !make_map_rows(&mk, keys ? a.k : a.q, a.hkv, keys ? a.num_keys : 1, keys ? a.k_stride : a.q_stride, 1, kBlock) ||
-      !make_map_rows(&mv, keys ? a.v : a.q, a.hkv, keys ? a.num_keys : 1, keys ? a.v_stride : a.q_stride, 1, kBlock))
+      !make_map_rows(&mv, keys ? a.v : a.q, a.hkv, keys ? a.num_keys : 1, keys ? a.v_stride : a.q_stride, 1, kBlock) ||
+      !make_map_rows(&mo, a.out, hq, a.num_tokens, hq * kDim, a.group, kTile / a.group) ||
+      !make_map_rows(&mo1, a.out, hq, a.num_tokens, hq * kDim, a.group, 1))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = once_per_device(done, [] {  // the shared-memory opt-in
-    return cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::total);
   });
   if (e != cudaSuccess) return e;
-  e = launch_kernel(prompt_kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), kSmem, s, 0, mq, mk, mv, p);
+  e = launch_kernel(prompt_kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), Smem::total, s, 0, mq, mk, mv, mo, mo1, p);
   if (e != cudaSuccess) return e;
   ++*launches;
-  e = launch_kernel(prompt_join_kernel, dim3(static_cast<unsigned>(p.ctas * (kRows / 8))), dim3(256), 0, s, 0, p);
-  if (e != cudaSuccess) return e;
-  ++*launches;
+  if (a.num_keys > kWhole * kBlock) {  // units may be cut
+    e = launch_kernel(prompt_join_kernel, dim3(static_cast<unsigned>(p.ctas * kJoinParts)), dim3(256), 0, s, 0, p);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
   return cudaPeekAtLastError();
 }
 
