@@ -6,8 +6,8 @@
 // Work.  A unit = (sequence, KV head, 256 rows): 256 / G neighbouring tokens with the G
 // query heads of the KV head, so that short prompts fill the tensor cores' rows too and
 // a unit's keys end together.  It is two tiles of 128 rows.  Units' 128-key blocks laid
-// end to end, causal ones only, are cut into equal shares, one per CTA: the blocks of
-// a sequence's units are a closed sum, and a CTA finds its share by a prefix sum over the
+// end to end, causal ones only, and kUnitCost for each unit's beginning and end, are cut into
+// equal shares, one per CTA: the length of a sequence's units is a closed sum, and a CTA finds its share by a prefix sum over the
 // sequences.  Units of at most kWhole blocks stay whole.  Of a unit that share borders
 // cut each CTA leaves (m, l, O) in the workspace, and a second kernel joins them; the
 // order of all sums is fixed.
@@ -53,11 +53,12 @@ namespace bsp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaxSum = 512.f;            // of a half block's weights
+constexpr float kMaxSum = 1073741824.f;     // of a half block's weights (bf16 and fp32 hold any; V of 2^80 and more may overflow)
 constexpr float kNoMax = -3.402823466e38f;  // the maximum of no keys (finite: -inf - kNoMax stays -inf)
 constexpr float kBigRef = 1048576.f;        // references above it: (z - m) c instead of z c - (m c), whose rounding then counts
 constexpr int kRows = 256, kTile = 128;     // rows of a unit, of a tile
 constexpr int kWhole = 4;                   // blocks of a unit that is not cut
+constexpr int kUnitCost = 2;                // what a unit costs beside its blocks, in blocks
 // four warps for each tile, then a producer, an issuer, one that stores, one that idles, four that check V
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpStore = 10, kWarpCheck = 12, kThreads = 512;
 constexpr int kReaders = 8 + 2 + 4;         // warps that read the announced pieces
@@ -142,37 +143,42 @@ __device__ __forceinline__ int64_t blocks_before(const Seq& s, const Params& p, 
   }
   return u == n && n > 0 ? sum + blocks_of(s, p, n - 1) : sum;
 }
-__device__ __forceinline__ int64_t blocks_of_seq(const Seq& s, const Params& p) { return blocks_before(s, p, units_of(s, p)); }
+// the length of a sequence's units, and of those before u, as shares are measured
+__device__ __forceinline__ int64_t length_before(const Seq& s, const Params& p, int u) {
+  return blocks_before(s, p, u) + static_cast<int64_t>(u) * kUnitCost;
+}
+__device__ __forceinline__ int64_t length_of_seq(const Seq& s, const Params& p) { return length_before(s, p, units_of(s, p)); }
 
-// The producer's walk over the pieces of its share [at, end) of the units' blocks.  A
-// border inside a unit of at most kWhole blocks stands for the unit's end.
+// The producer's walk over the pieces of its share [at, end).  A unit is nb + kUnitCost
+// long; a border behind its blocks, or inside a unit of at most kWhole blocks, stands for
+// its end.
 struct Walk {
   int64_t at, end, share;
   int64_t ustart;  // of unit (s, h, u)
   int s, h, u, nb;
   Seq q;
 
-  // the unit that holds block `at`, of sequence s0 with c0 blocks before it
+  // the unit that holds `at`, of sequence s0 with a length of c0 before it
   __device__ __forceinline__ void find(const Params& p, int s0, int64_t c0) {
     s = s0, q = load_seq(p.a, s);
-    const int64_t per = blocks_of_seq(q, p);
-    h = static_cast<int>((at - c0) / per);
+    const int64_t per = length_of_seq(q, p);
+    h = p.a.hkv == 1 ? 0 : static_cast<int>((at - c0) / per);
     const int64_t x = at - c0 - h * per;
-    int lo = 0, hi = units_of(q, p) - 1;  // the last unit with blocks_before <= x
+    int lo = 0, hi = units_of(q, p) - 1;  // the last unit with length_before <= x
 #pragma unroll 1
     while (lo < hi) {
       const int mid = lo + ((hi - lo + 1) >> 1);
-      if (blocks_before(q, p, mid) <= x)
+      if (length_before(q, p, mid) <= x)
         lo = mid;
       else
         hi = mid - 1;
     }
-    u = lo, nb = blocks_of(q, p, u), ustart = c0 + h * per + blocks_before(q, p, u);
-    if (at > ustart && nb <= kWhole) at = ustart + nb;
+    u = lo, nb = blocks_of(q, p, u), ustart = c0 + h * per + length_before(q, p, u);
+    if (at > ustart && (nb <= kWhole || at >= ustart + nb)) at = ustart + nb + kUnitCost;
   }
   __device__ __forceinline__ bool next(const Params& p, Piece& e) {
     if (at >= end) return false;
-    if (at == ustart + nb) {  // the next unit
+    if (at == ustart + nb + kUnitCost) {  // the next unit
       ustart = at, ++u;
 #pragma unroll 1
       while (u >= units_of(q, p)) {
@@ -189,7 +195,7 @@ struct Walk {
     e.starts = at == ustart, e.ends = to == uend;
     // pieces of the unit: shares from this one to that of its last block
     e.pieces = e.starts && !e.ends ? static_cast<int>((uend - 1) / share) - static_cast<int>(blockIdx.x) + 1 : 0;
-    at = to;
+    at = to == uend ? uend + kUnitCost : to;
     return true;
   }
 };
@@ -266,22 +272,6 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t acc, uint32_t w) {
   return r;
 }
 
-// What a row sees of V's values that are not finite, in keys [from, to) (the tiles that
-// the MMAs read hold zeros in their place), added to its dims d0 .. d0 + 31.
-__device__ __forceinline__ void add_not_finite(const PromptParams& a, float (&o)[32], int k0, int h, int from, int to, int d0) {
-#pragma unroll 1
-  for (int t = from; t < to; ++t) {
-    const uint16_t* v = a.v + (k0 + static_cast<int64_t>(t)) * a.v_stride + h * kDim + d0;
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if ((v[i] & 0x7F80) == 0x7F80) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (k == i) o[k] += bf16_bits_to_float(v[i]);
-      }
-  }
-}
-
 // ---- the main kernel -------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -290,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   // before the first tile Q's place serves the scan
   int64_t* s_sum = reinterpret_cast<int64_t*>(smem);  // [warps]
-  int64_t* s_start = s_sum + kThreads / 32;           // the share's first sequence, the blocks before it
+  int64_t* s_start = s_sum + kThreads / 32;           // the share's first sequence, the length before it
   const PromptParams& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -305,6 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(Smem::staged, 2, 4), init(Smem::piece_full, kPieces, 1), init(Smem::piece_empty, kPieces, kReaders);
     init(Smem::fin, 1, 1);
     mbar_fence_init();
+    for (const CUtensorMap* m : {&map_k, &map_q, &map_v, &map_o, &map_o1})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
   }
   if (tid < 8) reinterpret_cast<volatile int*>(smem + Smem::bad)[tid] = 0;
   pdl_wait();
@@ -325,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int s = s_lo; s < s_hi; ++s) {
     const Seq q = load_seq(a, s);
     bad |= q.bad;
-    mine += blocks_of_seq(q, p) * a.hkv;
+    mine += length_of_seq(q, p) * a.hkv;
   }
   if (bad && blockIdx.x == 0) set_err(a.err, BSP_DEVERR_CAPACITY);
   int64_t upto = mine;
@@ -349,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = s_lo;
 #pragma unroll 1
     for (; s + 1 < s_hi; ++s) {
-      const int64_t b = blocks_of_seq(load_seq(a, s), p) * a.hkv;
+      const int64_t b = length_of_seq(load_seq(a, s), p) * a.hkv;
       if (at < c + b) break;
       c += b;
     }
@@ -363,8 +355,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int start_s = at < total ? static_cast<int>(s_start[0]) : 0;
   const int64_t start_c = at < total ? s_start[1] : 0;
   __syncthreads();  // the scan's place is Q's again
+  // (short: the code of all kinds of warps shares the instruction cache; who gave up says so at the end)
   bool alive = true;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return alive = alive && wait_warp(bar, parity, a.err); };
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    bool there = false;
+#pragma unroll 1
+    for (uint32_t i = 0; alive && !there && i < BSP_WAIT_ROUNDS; ++i) there = __all_sync(0xffffffffu, try_wait(bar, parity));
+    return alive = there;
+  };
   // the next announced piece (nblk 0: no more)
   uint32_t number = 0;
   auto next = [&](Piece& e) {
@@ -461,53 +459,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (alive && next(e)) {
         const bool two = e.tokens > p.tokens / 2;
         const int masked = e.see >> 7;  // blocks from here on some row does not see whole (see < 0: all)
-        uint32_t item = e.item;
-        if (!wait(base + Smem::q_full, q_phase)) break;
-        q_phase ^= 1;
-        if (!wait(base + Smem::kv_full + 8 * stage_of(item), phase_of(item))) break;
-        fence();
-        scores(0, stage_of(item));
-        if (two) scores(1, stage_of(item));
-        commit(base + Smem::kv_empty + 8 * stage_of(item));
-        if (e.nblk == 1) commit(base + Smem::q_empty);
-#pragma unroll 1
-        for (int j = 0; j < e.nblk; ++j, item += 2) {
-          const bool more = j + 1 < e.nblk;
-          const uint32_t vs = stage_of(item + 1), ks = stage_of(item + 2);
-          if (!wait(base + Smem::kv_full + 8 * vs, phase_of(item + 1))) break;
+        uint32_t st = stage_of(e.item), ph = phase_of(e.item);
+        auto step = [&] {
+          if (++st == kStages) st = 0, ph ^= 1;
+        };
+        uint32_t vs = 0, ks = st;
+        // V of block j and K of the one behind it
+        auto ready = [&](int j) {
+          vs = st;
+          if (!wait(base + Smem::kv_full + 8 * st, ph)) return;
+          step();
           // (the ones that check wait for this one's word, not for the copy: of a stage whose
           // turns they do not follow one by one its parity says nothing)
-          const bool check = e.b0 + j >= masked;
-          if (check && lane == 0) arrive(base + Smem::v_look + 8 * vs);
+          if (e.b0 + j >= masked && lane == 0) arrive(base + Smem::v_look + 8 * vs);
           __syncwarp();
-          if (more && !wait(base + Smem::kv_full + 8 * ks, phase_of(item + 2))) break;
-          if (check) {
-            if (!wait(base + Smem::v_ok + 8 * vs, ok_phase >> vs & 1)) break;
-            ok_phase ^= 1u << vs;
+          if (j + 1 < e.nblk) {
+            ks = st;
+            if (!wait(base + Smem::kv_full + 8 * st, ph)) return;
+            step();
           }
-          const uint64_t vd = v_desc + vs * (kTileBytes / 16);
+        };
+        if (!wait(base + Smem::q_full, q_phase)) break;
+        q_phase ^= 1;
+        if (!wait(base + Smem::kv_full + 8 * st, ph)) break;
+        step();
+        fence();
+        scores(0, ks);
+        if (two) scores(1, ks);
+        commit(base + Smem::kv_empty + 8 * ks);
+        if (e.nblk == 1) commit(base + Smem::q_empty);
+        ready(0);
+#pragma unroll 1
+        for (int j = 0; alive && j < e.nblk; ++j) {
+          const bool more = j + 1 < e.nblk;
+          const uint32_t v = vs, k = ks;
+          const uint64_t vd = v_desc + v * (kTileBytes / 16);
+          if (e.b0 + j >= masked) {
+            if (!wait(base + Smem::v_ok + 8 * v, ok_phase >> v & 1)) break;
+            ok_phase ^= 1u << v;
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i && !two) break;
+            if (!wait(base + Smem::p_full + 16 * i, p_phase >> i & 1)) break;
+            fence();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // O (+)= P V of 64 keys
-              if (!wait(base + Smem::p_full + 16 * i + 8 * half, p_phase >> i & 1)) break;
-              fence();
-#pragma unroll
-              for (int k = 4 * half; k < 4 * half + 4; ++k)
-                umma_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * k, vd + k * (2048 / 16), kIdescO, j > 0 || k > 0);
-              if (half == 0) commit(base + Smem::half + 8 * i);
-            }
-            if (!alive) break;
+            for (int c = 0; c < 4; ++c)  // O (+)= P V of 64 keys
+              umma_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * c, vd + c * (2048 / 16), kIdescO, j > 0 || c > 0);
+            commit(base + Smem::half + 8 * i);
+            if (!wait(base + Smem::p_full + 16 * i + 8, p_phase >> i & 1)) break;
             p_phase ^= 1u << i;
+            fence();
+#pragma unroll
+            for (int c = 4; c < 8; ++c)
+              umma_ts(tmem + 256 + i * 128, tmem + i * 128 + 8 * c, vd + c * (2048 / 16), kIdescO, 1);
+            if (i == (two ? 1 : 0)) {
+              commit(base + Smem::kv_empty + 8 * v);
+              // (the next block's V and K are waited for while the tensor core has work queued)
+              if (more) ready(j + 1);
+              if (!alive) break;
+            }
             if (more)
-              scores(i, ks);
+              scores(i, k);
             else
               commit(base + Smem::o_full + 8 * i);
           }
-          if (!alive) break;
-          commit(base + Smem::kv_empty + 8 * vs);
-          if (more) commit(base + Smem::kv_empty + 8 * ks);
+          if (more) commit(base + Smem::kv_empty + 8 * k);
           if (j + 2 == e.nblk) commit(base + Smem::q_empty);
         }
       }
@@ -537,7 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive(base + Smem::kv_empty + 8 * st);
         }
       }
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (warp >= kWarpCheck) {
       // ---- V of the blocks that some row does not see whole: a warp takes 64 rows of 64 dims ----
       uint32_t look_phase = 0;
@@ -583,8 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * 128;
     const uint32_t s_full = base + Smem::s_full + 8 * tile, p_full = base + Smem::p_full + 16 * tile;
     uint32_t s_phase = 0, o_phase = 0;
-    const float c = p.c, sign = a.sm_scale < 0.f ? -1.f : 1.f, cs = c * sign;
-    const float none = -sign * INFINITY;  // a logit that is not seen
+    const float c = p.c, cs = a.sm_scale < 0.f ? -c : c;
     const int log_group = 8 - p.log_tokens, tok = row >> log_group;
     const int tok_lo = (row & ~31) >> log_group, tok_hi = (row | 31) >> log_group;  // the warp's
     while (alive && next(e)) {
@@ -598,105 +613,116 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys of the block that the row, and the first and last rows of the warp, see
         const int from = (e.b0 + j) * kBlock, lim = e.see + tok - from, lim_lo = e.see + tok_lo - from,
                   lim_hi = e.see + tok_hi - from;
-        uint32_t r[2][32];
-        auto load = [&](int half) {
-          tmem_ld32_issue(s_at + 64 * half, r[0]);
-          tmem_ld32_issue(s_at + 64 * half + 32, r[1]);
-          loaded(r[0]), loaded(r[1]);
-          if (lim_lo < 64 * half + 64) {
+        // the weights of 64 logits against the rows' references, as P's words, and their sum
+        auto weights = [&](const uint32_t(&r)[2][32], uint32_t(&pk)[32]) {
+          const float rc = -ref * c;
+          float2 t[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              if (lim_lo < 64 * half + 32 * q + 32) {
-                const int m = lim - 64 * half - 32 * q;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) r[q][i] = i < m ? r[q][i] : __float_as_uint(none);
-              }
+          for (int i = 0; i < 32; ++i) {
+            const float2 x = ffma2({__uint_as_float(r[i >> 4][2 * (i & 15)]), __uint_as_float(r[i >> 4][2 * (i & 15) + 1])},
+                                   {cs, cs}, {rc, rc});
+            const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            t[i & 1] = fadd2(t[i & 1], w);
+            pk[i] = pack_bf16x2(w.x, w.y);
           }
+          return (t[0].x + t[0].y) + (t[1].x + t[1].y);
         };
-        auto largest = [&] {  // of the loaded half
-          float mx[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            auto z = [&](int i) { return sign * __uint_as_float(r[k >> 1][16 * (k & 1) + i]); };
-            mx[k] = fmax3(z(0), z(1), z(2));
-#pragma unroll
-            for (int i = 3; i < 15; i += 2) mx[k] = fmax3(mx[k], z(i), z(i + 1));
-            mx[k] = fmaxf(mx[k], z(15));
-          }
-          return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-        };
-        auto set_ref = [&](float to) {
-          ref = to;
-          huge = __any_sync(0xffffffffu, !(fabsf(ref * c) < kBigRef));
-        };
-        if (j == 0) {
-          load(0);
-          const float top = largest();
-          load(1);
-          set_ref(fmax3(ref, top, largest()));
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-          float sum;
-          auto weights = [&] {
-            float2 t[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            if (lim_hi <= 64 * half) {  // no row of the warp sees any
-#pragma unroll
-              for (int i = 0; i < 32; ++i) pk[i] = 0;
-            } else if (__builtin_expect(!huge, 1)) {
-              const float rc = -ref * c;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float2 x = ffma2({__uint_as_float(r[i >> 4][2 * (i & 15)]), __uint_as_float(r[i >> 4][2 * (i & 15) + 1])},
-                                       {cs, cs}, {rc, rc});
-                const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                t[i & 1] = fadd2(t[i & 1], w);
-                pk[i] = pack_bf16x2(w.x, w.y);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float u = (sign * __uint_as_float(r[i >> 4][2 * (i & 15)]) - ref) * c,
-                            v = (sign * __uint_as_float(r[i >> 4][2 * (i & 15) + 1]) - ref) * c;
-                const float2 w = make_float2(ex2_approx(u), ex2_approx(v));
-                t[i & 1] = fadd2(t[i & 1], w);
-                pk[i] = pack_bf16x2(w.x, w.y);
-              }
-            }
-            sum = (t[0].x + t[0].y) + (t[1].x + t[1].y);
-          };
-          load(half);
-          weights();
-          if (__builtin_expect(__any_sync(0xffffffffu, sum > kMaxSum), 0)) {
-            // the rows' references pass this half's maxima; O and l in their terms
-            load(half);
-            const float to = fmaxf(ref, largest()), f = rescale(ref, to, c);
-            set_ref(to);
-            l *= f;
-            if (j > 0 || half) {  // (S says that the block before is in O)
-              if (half) {
-                wait(base + Smem::half + 8 * tile, s_phase);
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-              }
-#pragma unroll 1
-              for (int k = 0; k < 128; k += 16) {
-                float y[16];
-                tmem_ld<16>(o_at + k, y);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] *= f;
-                tmem_st<16>(o_at + k, y);
-              }
-            }
-            load(half);
-            weights();
-          }
+        auto send = [&](int half, const uint32_t(&pk)[32], float sum) {
           l += sum;
           tmem_st32(s_at + 32 * half, pk);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
           if (lane == 0 && alive) arrive(p_full + 8 * half);
+        };
+        int half = 0;
+        if (__builtin_expect(j > 0 && lim_lo >= kBlock && !huge, 1)) {  // the common way
+          uint32_t r[2][32], r2[2][32], pk[32];
+          tmem_ld32_issue(s_at, r[0]), tmem_ld32_issue(s_at + 32, r[1]);
+          loaded(r[0]), loaded(r[1]);
+          tmem_ld32_issue(s_at + 64, r2[0]), tmem_ld32_issue(s_at + 96, r2[1]);
+          float sum = weights(r, pk);
+          const bool fits = !__any_sync(0xffffffffu, sum > kMaxSum);
+          loaded(r2[0]), loaded(r2[1]);
+          if (__builtin_expect(fits, 1)) {
+            send(0, pk, sum);
+            half = 1;
+            sum = weights(r2, pk);
+            if (__builtin_expect(!__any_sync(0xffffffffu, sum > kMaxSum), 1)) {
+              send(1, pk, sum);
+              half = 2;
+            }
+          }
+        }
+#pragma unroll 1
+        for (; half < 2; ++half) {
+          uint32_t r[2][32], pk[32];
+          float sum = 0.f;
+          if (lim_hi <= 64 * half) {  // no row of the warp sees any
+#pragma unroll
+            for (int i = 0; i < 32; ++i) pk[i] = 0;
+          } else {
+            tmem_ld32_issue(s_at + 64 * half, r[0]), tmem_ld32_issue(s_at + 64 * half + 32, r[1]);
+            loaded(r[0]), loaded(r[1]);
+            if (cs < 0.f) {  // (c is positive from here on)
+#pragma unroll
+              for (int i = 0; i < 64; ++i) r[i >> 5][i & 31] ^= 0x80000000u;
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              if (lim_lo < 64 * half + 32 * q + 32) {
+                const int m = lim - 64 * half - 32 * q;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[q][i] = i < m ? r[q][i] : 0xFF800000u;
+              }
+            bool again = half == 0 && j == 0;  // the first reference is the half's maximum
+#pragma unroll 1
+            for (int turn = 0; turn < 2; ++turn) {
+              if (again) {
+                // the rows' references pass this half's maxima; O and l in their terms
+                float mx[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  auto z = [&](int i) { return __uint_as_float(r[k >> 1][16 * (k & 1) + i]); };
+                  mx[k] = fmax3(z(0), z(1), z(2));
+#pragma unroll
+                  for (int i = 3; i < 15; i += 2) mx[k] = fmax3(mx[k], z(i), z(i + 1));
+                  mx[k] = fmaxf(mx[k], z(15));
+                }
+                const float to = fmaxf(fmax3(ref, mx[0], mx[1]), fmaxf(mx[2], mx[3])), f = rescale(ref, to, c);
+                ref = to;
+                huge = __any_sync(0xffffffffu, !(fabsf(ref * c) < kBigRef));
+                l *= f;
+                if (j > 0 || half) {  // (S says that the block before is in O)
+                  if (half) {
+                    wait(base + Smem::half + 8 * tile, s_phase);
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                  }
+#pragma unroll 1
+                  for (int k = 0; k < 128; k += 8) {
+                    float y[8];
+                    tmem_ld<8>(o_at + k, y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] *= f;
+                    tmem_st<8>(o_at + k, y);
+                  }
+                }
+              }
+              float2 t[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float2 x = fmul2(fadd2({__uint_as_float(r[i >> 4][2 * (i & 15)]), __uint_as_float(r[i >> 4][2 * (i & 15) + 1])},
+                                             {-ref, -ref}), {c, c});
+                const float2 w = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                t[i & 1] = fadd2(t[i & 1], w);
+                pk[i] = pack_bf16x2(w.x, w.y);
+              }
+              sum = (t[0].x + t[0].y) + (t[1].x + t[1].y);
+              if (again || !__any_sync(0xffffffffu, sum > kMaxSum)) break;
+              again = true;
+            }
+          }
+          send(half, pk, sum);
         }
         s_phase ^= 1;
       }
@@ -719,26 +745,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t r[32];
         tmem_ld32_issue(o_at + 32 * k, r);
         loaded(r);
-        float o[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(r[i]);
-        if (__builtin_expect(fix, 0))
-          add_not_finite(a, o, e.k0, e.h, max(e.b0, max(e.see >> 7, 0)) * kBlock,
-                         tok < e.tokens ? min(see, (e.b0 + e.nblk) * kBlock) : 0, 32 * k);
+        auto o = [&](int i) { return __uint_as_float(r[i]); };
         if (all) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)  // 16-byte chunks of the swizzled row
-            sts128(stage + (k >> 1) * kHalf + (((4 * (k & 1) + i) ^ (row & 7)) << 4),
-                   pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                   pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f), pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
+          for (int i = 0; i < 4; ++i) {  // 16-byte chunks of the swizzled row
+            uint32_t w[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const float2 x = fmul2({o(8 * i + 2 * n), o(8 * i + 2 * n + 1)}, {f, f});
+              w[n] = pack_bf16x2(x.x, x.y);
+            }
+            sts128(stage + (k >> 1) * kHalf + (((4 * (k & 1) + i) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(po)[(8 * k + i) * kRows + row] =
-                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            reinterpret_cast<float4*>(po)[(8 * k + i) * kRows + row] = make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
         }
-        __syncwarp();
       }
+      if (__builtin_expect(fix, 0) && tok < e.tokens) {
+        // what the row sees of V's values that are not finite (the MMAs read zeros in their place)
+        const int to = min(see, (e.b0 + e.nblk) * kBlock);
+#pragma unroll 1
+        for (int t = max(e.b0, max(e.see >> 7, 0)) * kBlock; t < to; ++t) {
+          const uint16_t* v = a.v + (e.k0 + static_cast<int64_t>(t)) * a.v_stride + e.h * kDim;
+#pragma unroll 1
+          for (int d = 0; d < kDim; ++d) {
+            if ((v[d] & 0x7F80) != 0x7F80) continue;
+            uint16_t* x = reinterpret_cast<uint16_t*>(smem + (stage - base) + (d >> 6) * kHalf + ((((d & 63) >> 3) ^ (row & 7)) << 4)) + (d & 7);
+            float* y = po + (d >> 2) * (kRows * 4) + row * 4 + (d & 3);
+            const float sum = (all ? bf16_bits_to_float(*x) : *y) + bf16_bits_to_float(v[d]);
+            if (all)
+              *x = static_cast<uint16_t>(pack_bf16x2(sum, 0.f));
+            else
+              *y = sum;
+          }
+        }
+      }
+      __syncwarp();
       if (!all) *reinterpret_cast<float2*>(po + kRows * kDim + 2 * row) = make_float2(ref, l);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       if (all) {
@@ -749,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   }
+  if (!alive && lane == 0) set_err(a.err, BSP_DEVERR_TIMEOUT);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (warp == kWarpMma) {
