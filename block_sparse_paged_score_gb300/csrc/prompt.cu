@@ -25,8 +25,8 @@
 // exponentials are taken.
 //
 // Keys that a row does not see have p = 0, and V's rows of such keys may hold
-// infinities and NaN, which 0 does not silence: four warps look through V's tile of
-// those blocks that some row does not see whole, put zeros in place of what is not
+// infinities and NaN, which 0 does not silence: four warps look through those keys of
+// V's tiles that some row does not see, put zeros in place of what is not
 // finite, and the rows that do see it get it added at the end.
 //
 // A producer warp finds the pieces, announces them to the others in a ring, and loads Q, K
@@ -555,9 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp >= kWarpCheck) {
-      // ---- V of the blocks that some row does not see whole: a warp takes 64 rows of 64 dims ----
+      // ---- V of the blocks that some row does not see whole: a warp takes 64 dims of half the keys ----
       uint32_t look_phase = 0;
-      const uint32_t part = base + Smem::kv + (warp - kWarpCheck) * (kTileBytes / 4) + lane * 16;
+      const uint32_t part = base + Smem::kv + ((warp - kWarpCheck) & 1) * kHalf + lane * 16;
       while (alive && next(e)) {
         const int masked = max(e.see >> 7, e.b0);
 #pragma unroll 1
@@ -567,20 +567,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           look_phase ^= 1u << st;
           if (!wait(base + Smem::kv_full + 8 * st, phase_of(item))) break;
           const uint32_t at = part + st * kTileBytes;
+          // keys from the first that some row does not see on, four at a time
+          const int from = (max(e.see - b * kBlock, 0) & ~3) + 4 * ((warp - kWarpCheck) >> 1);
           uint32_t acc[4] = {0, 0, 0, 0};
-#pragma unroll 8
-          for (int i = 0; i < 16; ++i) {
-            const uint4 v = lds128(at + i * 512);
+#pragma unroll 4
+          for (int i = from; i < kBlock; i += 8) {
+            const uint4 v = lds128(at + i * 128);
             acc[0] = add_zero_times(acc[0], v.x), acc[1] = add_zero_times(acc[1], v.y);
             acc[2] = add_zero_times(acc[2], v.z), acc[3] = add_zero_times(acc[3], v.w);
           }
           const uint32_t any = not_finite(acc[0]) | not_finite(acc[1]) | not_finite(acc[2]) | not_finite(acc[3]);
           if (__any_sync(0xffffffffu, any != 0)) {
 #pragma unroll 1
-            for (int i = 0; i < 16; ++i) {
-              const uint4 v = lds128(at + i * 512);
+            for (int i = from; i < kBlock; i += 8) {
+              const uint4 v = lds128(at + i * 128);
               auto clean = [](uint32_t x) { return x & ~((not_finite(x) >> 15) * 0xFFFFu); };
-              sts128(at + i * 512, clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+              sts128(at + i * 128, clean(v.x), clean(v.y), clean(v.z), clean(v.w));
             }
             if (lane == 0) reinterpret_cast<volatile int*>(smem + Smem::bad)[number & 7] = number;
             fence_proxy_async();
