@@ -48,7 +48,12 @@ namespace bsp {
 namespace {
 
 constexpr int kTileBytes = kBlock * kDim;  // of K or V
+constexpr int kMetas = 8;                  // blocks that may be loaded ahead of the compute warps, at least
 constexpr float kLeastScale = 0x1p-60f;
+// A share's blocks at least, where there are 512 in all (2 from 256 on): few long pieces are
+// joined faster than many short ones are attended.  Requests of 128k tokens, us, shares of at
+// least 1 and 4 blocks: one 36.4, 28.7, four of 32k 25.5, 24.4; one of 1000 tokens 15.8, 19.8.
+constexpr int kLeastBlocks = 4;
 
 struct Fp8Params {
   Params w;  // qk_scale 1: references are log2 of weights
@@ -61,19 +66,19 @@ struct Fp8Params {
 // ---- shared memory -----------------------------------------------------------
 template <int N>
 struct Shape {
-  static constexpr int kCompute = N == 16 ? 4 : 8, kThreads = 32 * (kCompute + 2), kCtasPerSm = N == 16 ? 3 : 2;
+  static constexpr int kCompute = N == 16 ? 4 : 8, kThreads = 32 * (kCompute + 2), kCtasPerSm = N == 16 ? 4 : 2;
   static constexpr int kHalves = kCompute / 4;  // warps that share 32 TMEM lanes
   static constexpr int kRows = N / kHalves;     // a compute warp's
   static constexpr int kPages = 8 / kHalves;    // of V
 };
 template <int N, bool Q16>
 struct Smem {
-  static constexpr int kK = N == 32 ? 3 : 2, kV = 2;  // stages (as much as the CTAs of an SM leave room for)
+  static constexpr int kK = N == 32 ? 3 : N == 16 ? 1 : 2, kV = N == 16 ? 1 : 2;  // stages (as much as the CTAs of an SM leave room for)
   static constexpr int v = kK * kTileBytes;
   static constexpr int p = v + kV * kTileBytes;        // P [128 tokens][N rows] f16
   static constexpr int q = p + kBlock * N * 2;
-  static constexpr int meta = q + N * 128 * (Q16 ? 2 : 1);  // per V stage: k factor, log2 vs, 1 / vs, a bad block
-  static constexpr int refs = meta + kV * 16;          // [2][N] kBias - R
+  static constexpr int meta = q + N * 128 * (Q16 ? 2 : 1);  // [kMetas] k factor, log2 vs, 1 / vs of a block
+  static constexpr int refs = meta + kMetas * 16;      // [2][N] kBias - R
   static constexpr int rowfac = refs + 2 * N * 4;      // [N] scales of the query rows
   static constexpr int fac = rowfac + N * 4;           // [N] rescale factors
   static constexpr int tops = fac + N * 4;             // [4][N] maxima, later sums
@@ -83,8 +88,9 @@ struct Smem {
   static constexpr int k_full = bars, k_empty = k_full + 8 * kK, v_full = k_empty + 8 * kK, v_empty = v_full + 8 * kV,
                        z_full = v_empty + 8 * kV, z_empty = z_full + 16, pv_full = z_empty + 16, pv_done = pv_full + 16,
                        q_full = pv_done + 16, fin = q_full + 8;
-  static constexpr int misc = fin + 8;  // TMEM address, commands[2]
+  static constexpr int misc = fin + 8;  // TMEM address
   static constexpr int total = misc + 16;
+  static_assert(kK + 3 <= kMetas);
   static_assert(p % 1024 == 0 && q % 1024 == 0 && meta % 16 == 0 && refs % 16 == 0);
 };
 // TMEM columns: V's tile (64 columns of token pairs), O, two buffers of logits
@@ -93,7 +99,6 @@ struct Tmem {
   static constexpr int v = 0, o = 64, z = o + N, kColumns = N == 16 ? 128 : 256;
   static_assert(z + 2 * N <= kColumns && kColumns * Shape<N>::kCtasPerSm <= 512);
 };
-constexpr uint32_t kAccumulate = 1, kNothing = 2;  // what a PV round is
 
 // ---- device helpers ------------------------------------------------------------
 // a K or V tile of a block and head; the 5-d map's innermost dims are in the tile's order
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     // ---- loader: walks the share, reads the block table and the scales, 32 blocks at a time ----
     const int limit = static_cast<int>(min(a.num_blocks, int64_t{0x7FFFFFFF}));
     const int bad_id = max(limit, 1);  // outside the map, which has a block at least: its copies write zeros
-    uint32_t ks = 0, k_phase = 1, vs = 0, v_phase = 1;  // (an empty stage's wait passes at once)
+    uint32_t ks = 0, k_phase = 1, vs = 0, v_phase = 1, number = 0;  // (an empty stage's wait passes at once)
     while (alive && w.next(p, sub, lane)) {
       const int32_t* table = a.block_table + static_cast<int64_t>(w.seq) * a.bt_stride + w.b0;
       int32_t ids = 0;
@@ -281,18 +286,19 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           v = v >= 0.f ? fmaxf(v, kLeastScale) : __uint_as_float(0x7FC00000u);
           lv = __log2f(v);
           inv = 1.f / v;
+          if (ids == bad_id) kc = 0.f, lv = -INFINITY, inv = 0.f;  // no weights (K and V are zeros)
           __syncwarp();
         }
         const int id = __shfl_sync(0xffffffffu, ids, i & 31);
         const float k = __shfl_sync(0xffffffffu, kc, i & 31), l = __shfl_sync(0xffffffffu, lv, i & 31),
                     v = __shfl_sync(0xffffffffu, inv, i & 31);
         if (!wait(base + S::k_empty + 8 * ks, k_phase)) break;
+        sts128(base + S::meta + 16 * (number++ % kMetas), __float_as_uint(k), __float_as_uint(l), __float_as_uint(v), 0u);
+        __syncwarp();
         arrive_expect(base + S::k_full + 8 * ks, kTileBytes);
         tile_g2s_5d(base + ks * kTileBytes, &map_k, w.h, id, base + S::k_full + 8 * ks);
         if (++ks == S::kK) ks = 0, k_phase ^= 1;
         if (!wait(base + S::v_empty + 8 * vs, v_phase)) break;
-        sts128(base + S::meta + 16 * vs, __float_as_uint(k), __float_as_uint(l), __float_as_uint(v), id == bad_id);
-        __syncwarp();
         arrive_expect(base + S::v_full + 8 * vs, kTileBytes);
         tile_g2s_5d(base + S::v + vs * kTileBytes, &map_v, w.h, id, base + S::v_full + 8 * vs);
         if (++vs == S::kV) vs = 0, v_phase ^= 1;
@@ -316,16 +322,13 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     // f32 += A (f16, TMEM) B (f16, rows contiguous), M = 128
     constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);
     uint32_t ks = 0, k_phase = 0, q_phase = 0, buf = 0, z_phase = 1, round = 0;
-    auto multiply = [&] {
+    auto multiply = [&](bool accumulate) {
       const uint32_t b = round & 1;
       if (!wait(base + S::pv_full + 8 * b, (round >> 1) & 1)) return;
-      const uint32_t cmd = misc[1 + b];
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      if (!(cmd & kNothing)) {
 #pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)
-          umma_ts(tmem + T::o, tmem + T::v + 8 * k, p_desc + (k * 16 * 2 * N) / 16, kIdescO, k > 0 || (cmd & kAccumulate));
-      }
+      for (int k = 0; k < kBlock / 16; ++k)
+        umma_ts(tmem + T::o, tmem + T::v + 8 * k, p_desc + (k * 16 * 2 * N) / 16, kIdescO, k > 0 || accumulate);
       commit(base + S::pv_done + 8 * b);
       ++round;
     };
@@ -349,10 +352,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         commit(base + S::z_full + 8 * buf);
         if (++ks == S::kK) ks = 0, k_phase ^= 1;
         if (++buf == 2) buf = 0, z_phase ^= 1;
-        if (i) multiply();
+        if (i) multiply(i > 1);
         if (!alive) break;
       }
-      if (alive) multiply();
+      if (alive) multiply(w.nblk > 1);
     }
     // every MMA and commit has ended
     commit(base + S::fin);
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     const uint32_t v_at = base + S::v + half * VP * 2048 + dim * 16;
     const uint32_t swz = (tok & 7) >> (N == 16 ? 2 : N == 32 ? 1 : 0);
     const uint32_t p_at = base + S::p + tok * 2 * N;
-    uint32_t zb = 0, z_phase = 0, vst = 0, v_phase = 0;  // of the next block
+    uint32_t zb = 0, z_phase = 0, vst = 0, v_phase = 0, number = 0;  // of the next block
     uint32_t round = 0;                                  // of PV
     uint32_t cur = 0;                                    // which references
     auto done = [&](uint32_t r) {  // round r - 1 has ended
@@ -410,12 +413,11 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       for (int k = w.nblk; k > 0; --k, n0 = static_cast<int>(n0 + static_cast<uint32_t>(kBlock))) {
         // after a timed-out wait the warp goes on without waits and arrivals (the
         // barriers of the compute warps need every one); its results are void
-        wait(base + S::v_full + 8 * vst, v_phase);
         wait(base + S::z_full + 8 * zb, z_phase);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint4 m4 = lds128(base + S::meta + 16 * vst);
-        const float kc = __uint_as_float(m4.x), lv = __uint_as_float(m4.y), inv = __uint_as_float(m4.z);
-        const bool bad = m4.w != 0, whole = n0 <= min_len - kBlock;
+        const float4 m4 = lds128f(base + S::meta + 16 * (number++ % kMetas));
+        const float kc = m4.x, lv = m4.y, inv = m4.z;
+        const bool whole = n0 <= min_len - kBlock;
         const uint32_t z = z_at + zb * N;
         float2 x[R / 2];
         float top = -INFINITY;
@@ -436,28 +438,26 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         load();
 #pragma unroll
         for (int i = 0; i < R / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
-        if (__builtin_expect(!all_of<32 * kCompute>(!bad && whole && top <= kMaxGrow + kBias), 0)) {
+        if (__builtin_expect(!all_of<32 * kCompute>(whole && top <= kMaxGrow + kBias), 0)) {
           // The uncommon way: the rows' maxima over what they see, new references, and
           // O and l in their terms.
-          if (!bad) {
 #pragma unroll 1
-            for (int c = 0; c < R; c += CH) {
-              float2 t[CH / 2];
-              load_t<CH, Q16>(t, z + c, rowfac + 4 * c, kc, lv);
-              float y[CH];
+          for (int c = 0; c < R; c += CH) {
+            float2 t[CH / 2];
+            load_t<CH, Q16>(t, z + c, rowfac + 4 * c, kc, lv);
+            float y[CH];
 #pragma unroll
-              for (int i = 0; i < CH; ++i) {
-                y[i] = i & 1 ? t[i >> 1].y : t[i >> 1].x;
-                if (n0 + tok >= static_cast<int>(lds32(lens_at + (half * R + c + i) * 4))) y[i] = -INFINITY;
-              }
-              const float mx = warp_reduce<CH>(y, lane, [](float u, float v) { return fmaxf(u, v); });
-              if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, mx);
-              __syncwarp();
+            for (int i = 0; i < CH; ++i) {
+              y[i] = i & 1 ? t[i >> 1].y : t[i >> 1].x;
+              if (n0 + tok >= static_cast<int>(lds32(lens_at + (half * R + c + i) * 4))) y[i] = -INFINITY;
             }
+            const float mx = warp_reduce<CH>(y, lane, [](float u, float v) { return fmaxf(u, v); });
+            if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, mx);
+            __syncwarp();
           }
           bar_sync(1, 32 * kCompute);
           float f = 1.f;
-          if (tid < N && !bad) {
+          if (tid < N) {
             float mx = ldsf(tops + tid * 4);
 #pragma unroll
             for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + tid) * 4));
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
             stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, ref);
             stsf(fac + tid * 4, f);
           }
-          if (!bad) cur ^= 1;
+          cur ^= 1;
           if (any_of<32 * kCompute>(f != 1.f) && !first) {
             done(round);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -501,40 +501,38 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
 #pragma unroll
         for (int i = 0; i < R / 2; ++i) {
           const float2 e = make_float2(ex2_approx(x[i].x), ex2_approx(x[i].y));
-          if (!bad) l[i] = ffma2(e, {inv, inv}, l[i]);
+          l[i] = ffma2(e, {inv, inv}, l[i]);
           pk[i] = pack_f16x2(e.x, e.y);
         }
         __syncwarp();
         done(round);  // P and V's tile are free
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (__builtin_expect(!bad, 1)) {
 #pragma unroll
-          for (int i = 0; i < R / 8; ++i)
-            sts128(p_at + ((half * R / 8 + i) ^ swz) * 16, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        for (int i = 0; i < R / 8; ++i)
+          sts128(p_at + ((half * R / 8 + i) ^ swz) * 16, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        wait(base + S::v_full + 8 * vst, v_phase);
 #pragma unroll
-          for (int g = 0; g < VP; g += 4) {
-            uint32_t r[32];
+        for (int g = 0; g < VP; g += 4) {
+          uint32_t r[32];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint4 b = lds128(v_at + vst * kTileBytes + (g + j) * 2048);
-              uint32_t b4[4] = {b.x, b.y, b.z, b.w};
-              if (__builtin_expect(!whole, 0)) {
+          for (int j = 0; j < 4; ++j) {
+            const uint4 b = lds128(v_at + vst * kTileBytes + (g + j) * 2048);
+            uint32_t b4[4] = {b.x, b.y, b.z, b.w};
+            if (__builtin_expect(!whole, 0)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t m = nan_bytes(b4[i]);
-                  if (m) atomicMin(nans + dim, n0 + (half * VP + g + j) * kPage + 4 * i + ((__ffs(m) - 1) >> 3));
-                  b4[i] &= ~m;
-                }
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t m = nan_bytes(b4[i]);
+                if (m) atomicMin(nans + dim, n0 + (half * VP + g + j) * kPage + 4 * i + ((__ffs(m) - 1) >> 3));
+                b4[i] &= ~m;
               }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2_cvt(b4[i], r[8 * j + 2 * i], r[8 * j + 2 * i + 1]);
             }
-            __syncwarp();
-            tmem_st32(vt_at + 8 * g, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2_cvt(b4[i], r[8 * j + 2 * i], r[8 * j + 2 * i + 1]);
           }
+          __syncwarp();
+          tmem_st32(vt_at + 8 * g, r);
         }
-        if (tid == 0) misc[1 + (round & 1)] = bad ? kNothing : first ? 0 : kAccumulate;
-        if (!bad) first = false;
+        first = false;
         fence_proxy_async();  // the tensor core reads P through the async proxy
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -678,6 +676,7 @@ cudaError_t launch_dense_pa_fp8(const DensePaFp8Params& a, int num_sms, cudaStre
   p.qk = a.a.sm_scale * kLog2e;
   p.k_scales = a.k_scales, p.v_scales = a.v_scales, p.k_scale = a.k_scale, p.v_scale = a.v_scale;
   set_work(p.w, pl, num_sms);
+  p.w.least = kLeastBlocks;
   CUtensorMap mk, mv;
   const uint64_t blocks = std::max<int64_t>(a.a.num_blocks, 1);
   if (!make_map_side(&mk, true, a.a.k_base, a.a.hkv, blocks, a.a.id_stride) ||

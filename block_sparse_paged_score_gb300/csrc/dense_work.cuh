@@ -26,6 +26,7 @@ struct Params {
   int32_t units, ctas, shares;       // shares = ctas / subs
   int32_t rows;                      // of a unit's slot in the workspace
   int32_t by_unit;                   // the list of cut units has an entry per unit (else per CTA)
+  int32_t least;                     // shares of enough blocks in all (128 of them for each) have so many at least
 };
 
 // ---- units ---------------------------------------------------------------------
@@ -110,7 +111,8 @@ __device__ __forceinline__ Share find_share(const Params& p, int turn, int64_t* 
     if (w < warp) upto += s_sum[w];
     total += s_sum[w];
   }
-  const int64_t share = (total * a.hkv + p.shares - 1) / p.shares, at = turn * share;
+  const int64_t least = min(static_cast<int64_t>(p.least), max(total * a.hkv >> 7, int64_t{1}));
+  const int64_t share = max((total * a.hkv + p.shares - 1) / p.shares, least), at = turn * share;
   if ((upto - mine) * a.hkv <= at && at < upto * a.hkv) {
     int64_t c = upto - mine;
     int g = g_lo, nb = blocks_of(a, group_len(a, g, 0, 1));
@@ -224,6 +226,7 @@ inline void set_work(Params& p, const Plan& pl, int num_sms) {
       std::min<int64_t>(static_cast<int64_t>(pl.ctas_per_sm) * num_sms / pl.subs, pairs * a.bt_stride));
   p.ctas = p.shares * pl.subs;
   p.by_unit = units <= p.ctas;
+  p.least = 1;
 }
 
 // the second launch, where shares may cut units
