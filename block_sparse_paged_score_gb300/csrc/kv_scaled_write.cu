@@ -10,11 +10,20 @@
 // they become subnormal.  What is written token by token is what a whole block at
 // once gives, but for those.
 //
-// A CTA owns a run, a head and a side: no two CTAs touch the same bytes or scale.  It
-// is found by its first token (the one before lies in another block); which token of
+// A run, a head and a side have one owner, so that no two touch the same bytes or
+// scale: a CTA, or of short runs that lie close together a warp.  It is found by the
+// run's first token (the one before lies in another block).  In a CTA, which token of
 // the run is at which offset goes to a table in shared memory, so that the bytes are
-// made page by page however the tokens are ordered, and V's pages, 16 tokens of a dim
-// side by side, leave as 16-byte stores.
+// made page by page however the tokens are ordered.  The run's rows stay in registers
+// between the maximum and the bytes: of K a thread has 8 dims of a token of each page,
+// of V two dims of the 32 tokens of two pages, which its pages hold side by side, so
+// that both leave as vectors.
+//
+// Measured (one call of a row of them): 64 decode tokens of a head 4.0 us, about a
+// launch and a block's new scale; 8 prompts of 300 to 2400 tokens, two heads, 12 us for
+// 17 MB.  There a run's chain of dependent steps is what it takes (slots, table, rows,
+// maximum, bytes), not bandwidth: loading a run's slots at once, and more tokens
+// a CTA, did not shorten it.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -22,7 +31,8 @@ namespace bsp {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kShort = 8;  // tokens of a run that a warp takes
 
 // the block of token i, -1 for a skipped one
 __device__ __forceinline__ int64_t block_of(const KvScaledWriteParams& p, int64_t i) {
@@ -37,127 +47,234 @@ __device__ __forceinline__ float scale_for(float a) {
   return __uint_as_float(static_cast<uint32_t>(max(-60, min(119, e)) + 127) << 23);
 }
 
+// what a CTA works on: a head of K or of V
+struct Side {
+  const uint16_t* src;  // rows, `stride` apart
+  int64_t stride;
+  uint8_t* base;        // of the head's pages
+  float* scales;        // of the head, hkv apart
+  bool v;
+};
+
+// four e4m3 bytes times f, rounded again
+__device__ __forceinline__ uint32_t times(uint32_t w, float f) {
+  return float2_to_e4m3x2(e4m3_to_float(w) * f, e4m3_to_float(w >> 8) * f) |
+         float2_to_e4m3x2(e4m3_to_float(w >> 16) * f, e4m3_to_float(w >> 24) * f) << 16;
+}
+// A block's bytes in a new scale's terms: 16-byte chunks first, first + step .. of 1024.
+__device__ __forceinline__ void rescale_block(uint8_t* block, int64_t id_stride, float f, int first, int step) {
+#pragma unroll 4
+  for (int c = first; c < 1024; c += step) {
+    uint4* at = reinterpret_cast<uint4*>(block + (c >> 7) * id_stride) + (c & 127);
+    const uint4 w = *at;
+    *at = make_uint4(times(w.x, f), times(w.y, f), times(w.z, f), times(w.w, f));
+  }
+}
+// two of a run's bytes, of the scale s
+struct Encode {
+  float s, inv;
+  bool pow2;
+  __device__ __forceinline__ uint32_t operator()(float u, float v) const {
+    return pow2 ? float2_to_e4m3x2(u * inv, v * inv) : float2_to_e4m3x2(u / s, v / s);
+  }
+};
+__device__ __forceinline__ Encode encode_by(float s) { return {s, 1.f / s, (__float_as_uint(s) & 0x7FFFFFu) == 0}; }
+__device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// the larger of top and the finite magnitudes (as bits) of two bf16
+__device__ __forceinline__ uint32_t larger(uint32_t top, uint32_t w) {
+  const uint32_t u = w & 0x7FFFu, v = w >> 16 & 0x7FFFu;
+  if (u < 0x7F80u) top = max(top, u);
+  if (v < 0x7F80u) top = max(top, v);
+  return top;
+}
+
+// A run of at most kShort tokens, from token i on, by a warp: a lane has four dims.
+__device__ __forceinline__ void write_short(const KvScaledWriteParams& p, const Side& d, int64_t i, int n, int lane) {
+  const int64_t slot = lane < n ? p.slot[i + lane] : -1 - lane, b = __shfl_sync(0xffffffffu, slot, 0) / kBlock;
+  float* const scale_at = d.scales + b * p.hkv;
+  const float old = *scale_at;
+  // of tokens with the same slot the last one counts
+  const uint32_t same = __match_any_sync(0xffffffffu, slot);
+  const uint32_t live = __ballot_sync(0xffffffffu, lane < n && 31 - __clz(same) == lane);
+  uint2 x[kShort];
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < kShort; ++k) {
+    x[k] = make_uint2(0, 0);
+    if (live >> k & 1) x[k] = *reinterpret_cast<const uint2*>(d.src + (i + k) * d.stride + 4 * lane);
+  }
+#pragma unroll
+  for (int k = 0; k < kShort; ++k) top = larger(larger(top, x[k].x), x[k].y);
+  top = __reduce_max_sync(0xffffffffu, top);
+  const bool anew = __any_sync(0xffffffffu, lane < n && slot % kBlock == 0);
+  const float run = scale_for(__uint_as_float(top << 16)), s = anew ? run : fmaxf(old, run);
+  if (lane == 0) *scale_at = s;
+  uint8_t* const block = d.base + b * 16 * p.id_stride;
+  if (!anew && !(s <= old)) {
+    rescale_block(block, p.id_stride, old / s, lane, 32);
+    __syncwarp();
+  }
+  const Encode bytes = encode_by(s);
+#pragma unroll
+  for (int k = 0; k < kShort; ++k) {
+    if (!(live >> k & 1)) continue;
+    const int o = static_cast<int>(__shfl_sync(0xffffffffu, slot, k) % kBlock), t = o % kPage;
+    uint8_t* const page = block + o / kPage * p.id_stride;
+    const uint32_t w = bytes(lo(x[k].x), hi(x[k].x)) | bytes(lo(x[k].y), hi(x[k].y)) << 16;
+    if (!d.v) {  // K page [128 / 16][16 tokens][16]
+      *reinterpret_cast<uint32_t*>(page + (lane >> 2) * 256 + t * 16 + (lane & 3) * 4) = w;
+    } else {  // V page [128][16 tokens]
+#pragma unroll
+      for (int j = 0; j < 4; ++j) page[(4 * lane + j) * 16 + t] = static_cast<uint8_t>(w >> (8 * j));
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads) kv_scaled_write_kernel(KvScaledWriteParams p, int per) {
   __shared__ int s_at[kBlock];  // token of an offset, + 1
   __shared__ int s_end;
-  __shared__ float s_top[kThreads / 32];
-  __shared__ __align__(16) uint8_t s_v[kDim][16];
+  __shared__ uint32_t s_long, s_short;  // the CTA's tokens that begin a run
+  __shared__ int s_len[32];
+  __shared__ uint32_t s_top[kWarps];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, l = tid & 15, t16 = tid >> 4;
-  const int h = blockIdx.y, side = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const Side d{(is_v ? p.src[1] : p.src[0]) + h * kDim, is_v ? p.stride[1] : p.stride[0],
+               (is_v ? p.base[1] : p.base[0]) + static_cast<int64_t>(h) * 2048, (is_v ? p.scales[1] : p.scales[0]) + h, is_v};
   const int64_t first = static_cast<int64_t>(blockIdx.x) * per;
-#pragma unroll 1
-  for (int64_t i = first; i < min(first + per, static_cast<int64_t>(p.num_tokens)); ++i) {
-    const int64_t b = block_of(p, i);
-    if (b < 0) {
-      if (tid == 0 && p.slot[i] >= 0) set_err(p.err, BSP_DEVERR_SLOT);
-      continue;
+  if (tid < 32) {
+    const int64_t i = first + lane;
+    int len = 0;
+    if (lane < per && i < p.num_tokens) {
+      const int64_t b = block_of(p, i);
+      if (b < 0 && p.slot[i] >= 0) set_err(p.err, BSP_DEVERR_SLOT);
+      if (b >= 0 && (i == 0 || block_of(p, i - 1) != b))
+        for (len = 1; len <= kShort && i + len < p.num_tokens && block_of(p, i + len) == b;) ++len;
     }
-    if (i > 0 && block_of(p, i - 1) == b) continue;
+    // (a single run takes all warps: most of its time may be its block's new scale)
+    const uint32_t runs = __ballot_sync(0xffffffffu, len > 0);
+    const uint32_t brief = __popc(runs) > 1 ? __ballot_sync(0xffffffffu, len > 0 && len <= kShort) : 0;
+    s_len[lane] = len;
+    if (lane == 0) s_long = runs & ~brief, s_short = brief;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (uint32_t left = s_short, k = 0; left; left &= left - 1, ++k) {
+    const int at = __ffs(left) - 1;
+    if (k % kWarps == static_cast<uint32_t>(warp)) write_short(p, d, first + at, s_len[at], lane);
+  }
+#pragma unroll 1
+  for (uint32_t left = s_long; left; left &= left - 1) {
+    const int64_t i = first + __ffs(left) - 1, b = p.slot[i] / kBlock;
     // the run's tokens by offset (the last of a slot)
-    __syncthreads();
     if (tid < kBlock) s_at[tid] = 0;
     int64_t at = i;
+    int end;
     do {
       if (tid == 0) s_end = kThreads;
       __syncthreads();
       const int64_t j = at + tid;
-      if (j >= p.num_tokens || block_of(p, j) != b) atomicMin(&s_end, tid);
+      const bool in = j < p.num_tokens && block_of(p, j) == b;
+      if (!in) atomicMin(&s_end, tid);
       __syncthreads();
-      if (tid < s_end) atomicMax(&s_at[p.slot[j] % kBlock], static_cast<int>(j) + 1);
-      at += s_end;
+      end = s_end;
+      if (tid < end) atomicMax(&s_at[p.slot[j] % kBlock], static_cast<int>(j) + 1);
+      at += end;
       __syncthreads();
-    } while (s_end == kThreads);
-    // the rows, 16 lanes a token, and their largest magnitude
-    uint4 x[kPagesPerSide];
-    uint32_t top = 0;
-#pragma unroll
-    for (int g = 0; g < kPagesPerSide; ++g) {
-      const int tok = s_at[kPage * g + t16] - 1;
-      x[g] = make_uint4(0, 0, 0, 0);
-      if (tok >= 0)
-        x[g] = *reinterpret_cast<const uint4*>(p.src[side] + tok * p.stride[side] + h * kDim + 8 * l);
-    }
-#pragma unroll
-    for (int g = 0; g < kPagesPerSide; ++g) {
-      const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t m = (k & 1 ? w[k >> 1] >> 16 : w[k >> 1]) & 0x7FFFu;
-        if (m < 0x7F80u) top = max(top, m);
-      }
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) s_top[tid >> 5] = __uint_as_float(top << 16);
-    float* const scale_at = p.scales[side] + b * p.hkv + h;
+    } while (end == kThreads);
+    float* const scale_at = d.scales + b * p.hkv;
     const float old = *scale_at;
-    __syncthreads();
-    float a = s_top[0];
+    // the rows and their largest magnitude
+    uint32_t x[32], top = 0;
+    const int l = tid & 15, t16 = tid >> 4, dims = 2 * (tid & 63), page0 = tid >> 6 << 1;
+    if (!d.v) {
 #pragma unroll
-    for (int k = 1; k < kThreads / 32; ++k) a = fmaxf(a, s_top[k]);
-    const bool anew = s_at[0] > 0;
-    const float run = scale_for(a), s = anew ? run : fmaxf(old, run);
-    if (tid == 0) *scale_at = s;
-    uint8_t* const block = p.base[side] + b * 16 * p.id_stride + static_cast<int64_t>(h) * 2048;
-    if (!anew && !(s <= old)) {  // what the block holds, in the new scale's terms
-      const float f = old / s;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = tid + kThreads * k;
-        uint4* at16 = reinterpret_cast<uint4*>(block + (c >> 7) * p.id_stride) + (c & 127);
-        uint4 w = *at16;
-        uint32_t* ws = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          ws[n] = float2_to_e4m3x2(e4m3_to_float(ws[n]) * f, e4m3_to_float(ws[n] >> 8) * f) |
-                  float2_to_e4m3x2(e4m3_to_float(ws[n] >> 16) * f, e4m3_to_float(ws[n] >> 24) * f) << 16;
-        *at16 = w;
+      for (int g = 0; g < kPagesPerSide; ++g) {  // 16 lanes a token
+        const int64_t tok = s_at[kPage * g + t16] - 1;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (tok >= 0) w = *reinterpret_cast<const uint4*>(d.src + tok * d.stride + 8 * l);
+        x[4 * g] = w.x, x[4 * g + 1] = w.y, x[4 * g + 2] = w.z, x[4 * g + 3] = w.w;
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2 * kPage; ++k) {  // 64 threads a token
+        const int64_t tok = s_at[kPage * page0 + k] - 1;
+        x[k] = 0;
+        if (tok >= 0) x[k] = *reinterpret_cast<const uint32_t*>(d.src + tok * d.stride + dims);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) top = larger(top, x[k]);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) top = max(top, s_top[k]);
+    const bool anew = s_at[0] > 0;
+    const float run = scale_for(__uint_as_float(top << 16)), s = anew ? run : fmaxf(old, run);
+    if (tid == 0) *scale_at = s;
+    uint8_t* const block = d.base + b * 16 * p.id_stride;
+    if (!anew && !(s <= old)) {  // what the block holds, in the new scale's terms
+      rescale_block(block, p.id_stride, old / s, tid, kThreads);
       __syncthreads();
     }
-    const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
-    const float inv = 1.f / s;
+    const Encode bytes = encode_by(s);
+    if (!d.v) {
 #pragma unroll
-    for (int g = 0; g < kPagesPerSide; ++g) {
-      const bool here = s_at[kPage * g + t16] > 0;
-      const int n = __syncthreads_count(here);
-      if (n == 0) continue;
-      const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
-      uint32_t r[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float u = __uint_as_float(w[k] << 16), v = __uint_as_float(w[k] & 0xFFFF0000u);
-        r[k] = pow2 ? float2_to_e4m3x2(u * inv, v * inv) : float2_to_e4m3x2(u / s, v / s);
+      for (int g = 0; g < kPagesPerSide; ++g) {  // K page [128 / 16][16 tokens][16]
+        if (s_at[kPage * g + t16] == 0) continue;
+        const uint32_t* w = x + 4 * g;
+        *reinterpret_cast<uint2*>(block + g * p.id_stride + (l >> 1) * 256 + t16 * 16 + (l & 1) * 8) =
+            make_uint2(bytes(lo(w[0]), hi(w[0])) | bytes(lo(w[1]), hi(w[1])) << 16,
+                       bytes(lo(w[2]), hi(w[2])) | bytes(lo(w[3]), hi(w[3])) << 16);
       }
-      uint8_t* const page = block + g * p.id_stride;
-      if (side == 0) {  // K page [128 / 16][16 tokens][16]
-        if (here)
-          *reinterpret_cast<uint2*>(page + (l >> 1) * 256 + t16 * 16 + (l & 1) * 8) =
-              make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
-        continue;
-      }
+    } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s_v[8 * l + k][t16] = static_cast<uint8_t>(r[k >> 1] >> (8 * (k & 1)));
-      __syncthreads();
-      if (n == kThreads) {  // V page [128][16 tokens], all of them new
-        if (tid < kDim) reinterpret_cast<uint4*>(page)[tid] = *reinterpret_cast<const uint4*>(s_v[tid]);
-      } else {
+      for (int g = 0; g < 2; ++g) {  // V page [128][16 tokens]
+        uint8_t* const to = block + (page0 + g) * p.id_stride + dims * 16;
+        uint32_t d0[4], d1[4];
+        bool all = true, any = false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int d = 16 * k + (tid >> 4), t = tid & 15;
-          if (s_at[kPage * g + t] > 0) page[d * 16 + t] = s_v[d][t];
+        for (int t = 0; t < kPage; ++t) {
+          const bool here = s_at[kPage * (page0 + g) + t] > 0;
+          all &= here, any |= here;
+        }
+        if (!any) continue;
+#pragma unroll
+        for (int t = 0; t < kPage; t += 4) {
+          const uint32_t* w = x + kPage * g + t;
+          d0[t / 4] = bytes(lo(w[0]), lo(w[1])) | bytes(lo(w[2]), lo(w[3])) << 16;
+          d1[t / 4] = bytes(hi(w[0]), hi(w[1])) | bytes(hi(w[2]), hi(w[3])) << 16;
+        }
+        if (all) {
+          reinterpret_cast<uint4*>(to)[0] = make_uint4(d0[0], d0[1], d0[2], d0[3]);
+          reinterpret_cast<uint4*>(to)[1] = make_uint4(d1[0], d1[1], d1[2], d1[3]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < kPage; ++t)
+            if (s_at[kPage * (page0 + g) + t] > 0) {
+              to[t] = static_cast<uint8_t>(d0[t / 4] >> (8 * (t & 3)));
+              to[16 + t] = static_cast<uint8_t>(d1[t / 4] >> (8 * (t & 3)));
+            }
         }
       }
     }
+    __syncthreads();  // the table may be made anew
   }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_scaled_write(const KvScaledWriteParams& p, int num_sms, cudaStream_t s) {
-  // a token a CTA while that is at most some waves of CTAs; else 16 (most of which begin no run)
-  const int per = static_cast<int64_t>(p.num_tokens) * p.hkv * 2 <= 32LL * num_sms ? 1 : 16;
+  // A token a CTA while the CTAs are resident together (three an SM), so that a decode
+  // token's block has eight warps for its new scale; else 32, whose runs share the warps.
+  // Measured, us, a token a CTA and 32: 64 tokens of a head 7.3, 11.5; 256 of a head 11.2,
+  // 11.5; 256 of two 15.4, 11.6; 1024 of a head 23.5, 11.6; 16000 of a prompt 60, 13.4.
+  // (64 and 128 tokens a CTA: 1024 of a head 18.0, 32.7, 16000 of a prompt 13.2, 11.5.)
+  const int per = static_cast<int64_t>(p.num_tokens) * p.hkv * 2 <= 3LL * num_sms ? 1 : 32;
   const dim3 grid(static_cast<unsigned>((p.num_tokens + per - 1) / per), static_cast<unsigned>(p.hkv), 2);
   const cudaError_t e = launch_kernel(kv_scaled_write_kernel, grid, dim3(kThreads), 0, s, 0, p, per);
   return e != cudaSuccess ? e : cudaPeekAtLastError();
