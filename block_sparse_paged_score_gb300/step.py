@@ -19,6 +19,9 @@ without an indexer over a 4-bit cache, from the requests' lengths and the
 projections' rows to the attention output: the block table and slot map, the
 norms and rotation with the cache write, and the dense attention.
 ``StepTables`` and ``NormRopeWrite`` serve layers with an indexer as well.
+``ScaledPromptStep`` and ``ScaledDecodeStep`` are the steps of such a layer over
+an 8-bit cache with a scale for each block and head: prompts, or chunks of them
+over what the cache holds, and decode tokens.
 """
 import ctypes as C
 
@@ -258,13 +261,16 @@ class NormRopeWrite:
     """Norms, position rotation and cache write of a step's projections
     (bsp_norm_rope_write) for up to max_tokens tokens.  kv and idx are the
     caches (idx None: a layer without an indexer; kv None: queries and index
-    keys alone).  Weights are bf16 [128] or None; rope_table is fp32
+    keys alone, or with k_out_heads the keys of that many heads too, as bf16 rows
+    in k_out).  Weights are bf16 [128] or None; rope_table is fp32
     [positions, rot_dim], cosines then sines (see rope_table), or None; dev_err is
     the caller's error word (None: one of its own)."""
 
     def __init__(self, kv, idx, num_q_heads, max_tokens, q_weight=None, k_weight=None, idx_q_weight=None,
                  idx_k_weight=None, weight_offset=0.0, eps=1e-6, rope_table=None, rope_pairs=False, q_dtype=bsp.BF16,
-                 idx_q_dtype=bsp.BF16, device="cuda", dev_err=None):
+                 idx_q_dtype=bsp.BF16, device="cuda", dev_err=None, k_out_heads=0):
+        if k_out_heads and kv is not None:
+            raise ValueError("the keys go to the cache or to k_out")
         self.kv, self.idx, self.max_tokens = kv, idx, max_tokens
         a = self.args = bsp.NormRopeArgs()
         self.q_out = torch.empty(max_tokens, num_q_heads, 128, device=device,
@@ -273,10 +279,15 @@ class NormRopeWrite:
         self.dev_err = dev_err if dev_err is not None else torch.zeros(1, dtype=torch.int32, device=device)
         dev = self.device = self.q_out.device
         bsp._cache_desc("K/V", kv, dev), bsp._cache_desc("index", idx, dev)
-        self.heads = (num_q_heads, kv.num_kv_heads if kv is not None else 0, idx.num_heads if idx is not None else 0)
+        self.heads = (num_q_heads, kv.num_kv_heads if kv is not None else k_out_heads,
+                      idx.num_heads if idx is not None else 0)
         a.num_q_heads, a.q_out_dtype, a.idx_q_out_dtype = num_q_heads, q_dtype, idx_q_dtype
         if kv is not None:
             a.kv, a.num_kv_heads = C.pointer(kv.desc), kv.num_kv_heads
+        self.k_out = None
+        if k_out_heads:
+            self.k_out = torch.empty(max_tokens, k_out_heads, 128, dtype=torch.bfloat16, device=device)
+            a.k_out, a.num_kv_heads = self.k_out.data_ptr(), k_out_heads
         if idx is not None:
             a.idx, a.num_idx_heads = C.pointer(idx.desc), idx.num_heads
             self.idx_q_out = torch.empty(max_tokens, idx.num_heads, 128, device=device,
@@ -296,8 +307,8 @@ class NormRopeWrite:
     def run(self, q, k, v, idx_q, idx_k, positions, slot, stream=None):
         """bf16 rows [T, heads, 128] (heads side by side, tokens any distance
         apart; idx_q and idx_k None without an index cache), int32 positions
-        and int64 slots [T]; returns the queries and index queries (views of
-        the object's buffers)."""
+        and int64 slots [T] (None without a cache); returns the queries and index
+        queries (views of the object's buffers)."""
         s = bsp._on(stream)
         a, dev, rows = self.args, self.device, bsp._head_rows
         T = q.shape[0]
@@ -367,3 +378,113 @@ class DenseStep:
         return bsp.dense_pa_decode(self.kv, qr, self.q_dtype, self.num_q_heads, t.block_table, self.row_seq,
                                    self.row_len, self.q_len, sm_scale=self.sm_scale, out=self.out, ws=self.ws,
                                    dev_err=self.dev_err, stream=stream)
+
+
+class _ScaledStep:
+    """What prompt and decode steps over a BlockScaledKvCache share: the step's
+    tables, norms and rotation, and the write of the new tokens."""
+
+    def __init__(self, cache, num_q_heads, num_seqs, token_capacity, bt_stride, sm_scale, q_dtype, block_table, device,
+                 norm):
+        self.cache, self.num_q_heads, self.sm_scale, self.q_dtype = cache, num_q_heads, sm_scale, q_dtype
+        self.group = num_q_heads // cache.num_kv_heads
+        self.dev_err = torch.zeros(1, dtype=torch.int32, device=device)
+        self.tables = StepTables(num_seqs, bt_stride, token_capacity, cache.num_blocks, block_table, device=device,
+                                 dev_err=self.dev_err)
+        self.norm = NormRopeWrite(None, None, num_q_heads, token_capacity, q_dtype=q_dtype, device=device,
+                                  dev_err=self.dev_err, k_out_heads=cache.num_kv_heads, **norm)
+        self.out = torch.zeros(token_capacity, num_q_heads, 128, dtype=torch.bfloat16, device=device)
+
+    def _write(self, context_lens, new_lens, free_blocks, free_head, q, k, v, stream):
+        t = self.tables.run(context_lens, new_lens, free_blocks, free_head, stream=stream)
+        T = q.shape[0]
+        qr, _ = self.norm.run(q, k, None, None, None, t.query_abs_pos[:T], None, stream=stream)
+        kr = self.norm.k_out[:T]
+        bsp.kv_scaled_write(self.cache, kr, v, t.slot[:T], dev_err=self.dev_err, stream=stream)
+        return qr, kr
+
+
+class ScaledPromptStep(_ScaledStep):
+    """Prompts of a layer without an indexer, from the requests' lengths to the
+    attention output: the step's tables, norms and rotation, the write into a
+    BlockScaledKvCache, causal attention.  A request brings any number of tokens.
+    With key_capacity 0 every request is new (run's context_lens is None), and its
+    queries see the step's own bf16 rows.  Else they see all of their request's tokens
+    as the cache holds them, read back into key_capacity rows: a chunk over its
+    context sees what its decode steps will.  block_table is the requests' (None: one
+    of its own); dev_err collects the error bits of all calls."""
+
+    def __init__(self, cache, num_q_heads, num_seqs, token_capacity, bt_stride, key_capacity=0, sm_scale=None,
+                 block_table=None, device="cuda", **norm):
+        super().__init__(cache, num_q_heads, num_seqs, token_capacity, bt_stride, sm_scale, bsp.BF16, block_table,
+                         device, norm)
+        hkv = cache.num_kv_heads
+        self.key_capacity = key_capacity
+        if not key_capacity:
+            self.no_context = torch.zeros(num_seqs, dtype=torch.int32, device=device)
+        else:
+            e = lambda: torch.empty(key_capacity, hkv, 128, dtype=torch.bfloat16, device=device)  # noqa: E731
+            self.k, self.v = e(), e()
+            self.key = torch.arange(key_capacity, dtype=torch.int32, device=device)
+            self.cu_k = torch.zeros(num_seqs + 1, dtype=torch.int32, device=device)
+        self.ws = bsp.prompt_attention_workspace(token_capacity, num_seqs, hkv, self.group, device)
+
+    def _key_slots(self, new_lens):
+        """Slots of all tokens of the requests that have new ones, one request
+        behind the other (-1 behind the last), and their offsets into cu_k."""
+        t, n = self.tables, self.tables.num_seqs
+        lens = torch.where(new_lens > 0, t.seq_lens, 0)
+        torch.cumsum(lens, 0, dtype=torch.int32, out=self.cu_k[1:])
+        seq = torch.searchsorted(self.cu_k[1:], self.key, right=True)
+        live = seq < n
+        seq = seq.clamp(max=n - 1)
+        pos = torch.where(live, self.key - self.cu_k[seq], 0)
+        block = t.block_table[seq, (pos // 128).clamp(max=t.block_table.shape[1] - 1)].long()
+        return torch.where(live & (block >= 0), block * 128 + pos % 128, -1)
+
+    def run(self, context_lens, new_lens, free_blocks, free_head, q, k, v, stream=None):
+        """Lengths and free blocks as in StepTables.run; q, k, v bf16 rows of the
+        step's tokens, any pad rows last.  Returns the attention output; a request's
+        rows are consecutive from tables.cu_tokens, rows of no request are
+        unspecified."""
+        if (context_lens is None) != (self.key_capacity == 0):
+            raise ValueError("contexts need key_capacity, and only they do")
+        if context_lens is None:
+            context_lens = self.no_context
+        s = bsp._on(stream)
+        qr, kr = self._write(context_lens, new_lens, free_blocks, free_head, q, k, v, s)
+        T, cu_q, cu_k = q.shape[0], self.tables.cu_tokens, None
+        if self.key_capacity:
+            with torch.cuda.stream(stream):
+                slot = self._key_slots(new_lens)
+            kr, v = bsp.kv_scaled_read(self.cache, slot, self.k, self.v, dev_err=self.dev_err, stream=s)
+            cu_k = self.cu_k
+        return bsp.prompt_attention(qr, kr, v, cu_q, cu_k, sm_scale=self.sm_scale, out=self.out[:T], ws=self.ws,
+                                    dev_err=self.dev_err, stream=s)
+
+
+class ScaledDecodeStep(_ScaledStep):
+    """Decode tokens of a layer without an indexer over a BlockScaledKvCache: as
+    DenseStep, every request brings q_len tokens (1..8) or none.  block_table is
+    the requests' (None: one of its own)."""
+
+    def __init__(self, cache, num_q_heads, num_seqs, q_len, bt_stride, sm_scale=None, q_dtype=bsp.BF16,
+                 block_table=None, device="cuda", **norm):
+        tokens = num_seqs * q_len
+        super().__init__(cache, num_q_heads, num_seqs, tokens, bt_stride, sm_scale, q_dtype, block_table, device, norm)
+        self.q_len = q_len
+        rows = tokens * cache.num_kv_heads
+        self.row_seq = torch.empty(rows, dtype=torch.int32, device=device)
+        self.row_len = torch.empty(rows, dtype=torch.int32, device=device)
+        self.ws = bsp.dense_pa_fp8_workspace(rows, cache.num_kv_heads, self.group, q_len, device)
+
+    def run(self, context_lens, new_lens, free_blocks, free_head, q, k, v, stream=None):
+        """As DenseStep.run: num_seqs * q_len rows, pad rows last; pad rows of the
+        output are zero."""
+        t, s = self.tables, bsp._on(stream)
+        qr, _ = self._write(context_lens, new_lens, free_blocks, free_head, q, k, v, s)
+        bsp.row_lengths_prefill(t.query_req_id, t.query_abs_pos, self.cache.num_kv_heads, self.row_seq, self.row_len,
+                                stream=s)
+        return bsp.dense_pa_decode_fp8(self.cache, qr, self.q_dtype, self.num_q_heads, t.block_table, self.row_seq,
+                                       self.row_len, self.q_len, sm_scale=self.sm_scale, out=self.out, ws=self.ws,
+                                       dev_err=self.dev_err, stream=s)
