@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           kc = k * fp.qk;
           v = v >= 0.f ? fmaxf(v, kLeastScale) : __uint_as_float(0x7FC00000u);
           lv = __log2f(v);
-          inv = 1.f / v;
+          inv = v == v ? 1.f / v : 1.f;  // (a NaN comes with the weights, to the rows that have any)
           if (ids == bad_id) kc = 0.f, lv = -INFINITY, inv = 0.f;  // no weights (K and V are zeros)
           __syncwarp();
         }

@@ -109,6 +109,7 @@ __device__ __forceinline__ void write_short(const KvScaledWriteParams& p, const 
   top = __reduce_max_sync(0xffffffffu, top);
   const bool anew = __any_sync(0xffffffffu, lane < n && slot % kBlock == 0);
   const float run = scale_for(__uint_as_float(top << 16)), s = anew ? run : fmaxf(old, run);
+  __syncwarp();  // (every lane has the old one)
   if (lane == 0) *scale_at = s;
   uint8_t* const block = d.base + b * 16 * p.id_stride;
   if (!anew && !(s <= old)) {

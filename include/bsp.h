@@ -667,7 +667,7 @@ bsp_status bsp_kv_scaled_read(const bsp_kv_cache* kv, const bsp_kv_scales* scale
  * order of sums are as in bsp_dense_pa_decode, its alignment rules aside.
  *   k scales  any value (z is what the formula makes of it)
  *   v scales  positive; below 2^-60 (zero too) they count as 2^-60, negative
- *             ones and NaN give rows of NaN
+ *             ones and NaN give the rows that see their block NaN
  * Bytes and scales at and past L_r are never used by row r, whatever they
  * hold.  A NaN byte of K gives NaN rows, one of V NaN in its dim of the rows
  * that see it.  Weights are rounded to f16; sums and references are fp32.  A
@@ -701,7 +701,9 @@ bsp_status bsp_dense_pa_decode_fp8(const bsp_kv_cache* kv, const bsp_kv_scales* 
  *         BSP_ERR_INVALID_ARG)
  * Keys that a query does not see never reach its row, whatever they hold; an
  * infinity or NaN in one that it sees does.  Weights are rounded to bf16; sums
- * and references are fp32.  The same inputs give the same bits.
+ * and references are fp32, and a reference may lag behind by 2^30: of values of
+ * V beyond 2^72 a sum may overflow.  The same inputs give the same bits.  One
+ * launch, two with more than 512 keys.
  * ws: device workspace of bsp_prompt_attention_workspace_bytes() bytes, 16-byte
  * aligned (its contents need not be set, and carry nothing from call to
  * call).  Calls that may overlap on the GPU, captured ones included, need
