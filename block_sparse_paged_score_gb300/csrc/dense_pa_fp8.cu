@@ -54,6 +54,11 @@ constexpr float kLeastScale = 0x1p-60f;
 // joined faster than many short ones are attended.  Requests of 128k tokens, us, shares of at
 // least 1 and 4 blocks: one 36.4, 28.7, four of 32k 25.5, 24.4; one of 1000 tokens 15.8, 19.8.
 constexpr int kLeastBlocks = 4;
+// Blocks that a share may grow by so as to hold one unit's only: a second unit costs a CTA some 5 us
+// (its queries, the first one's output), a block of a CTA 1.8 to 2.8.  us, shares as they come and of
+// one unit: 32 requests of 4k to 8k 32.6, 28.6, 100 of 2k 32.3, 27.3, 32 of 16k 43.6, 39.1, 64 of
+// 8k with 64 rows 57.5, 50.4; they grow by 2, 1, 1 and 3 blocks.  Long shares (64 x 128k: by 13) stay.
+constexpr int kMoreBlocks = 6;
 
 struct Fp8Params {
   Params w;  // qk_scale 1: references are log2 of weights
@@ -269,34 +274,36 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     while (alive && w.next(p, sub, lane)) {
       const int32_t* table = a.block_table + static_cast<int64_t>(w.seq) * a.bt_stride + w.b0;
       int32_t ids = 0;
-      float kc = 0.f, lv = 0.f, inv = 0.f;
+      float k_raw = 0.f, v_raw = 0.f, kc = 0.f, lv = 0.f, inv = 0.f;
 #pragma unroll 1
       for (int i = 0; i < w.nblk; ++i) {
         if ((i & 31) == 0) {
           ids = i + lane < w.nblk ? table[i + lane] : 0;
-          float k = fp.k_scale, v = fp.v_scale;
+          k_raw = fp.k_scale, v_raw = fp.v_scale;
           if (static_cast<uint32_t>(ids) >= static_cast<uint32_t>(limit)) {
             set_err(a.err, BSP_DEVERR_BLOCK_ID);
             ids = bad_id;
           } else if (fp.k_scales) {
-            k = fp.k_scales[static_cast<int64_t>(ids) * a.hkv + w.h];
-            v = fp.v_scales[static_cast<int64_t>(ids) * a.hkv + w.h];
+            k_raw = fp.k_scales[static_cast<int64_t>(ids) * a.hkv + w.h];
+            v_raw = fp.v_scales[static_cast<int64_t>(ids) * a.hkv + w.h];
           }
-          kc = k * fp.qk;
-          v = v >= 0.f ? fmaxf(v, kLeastScale) : __uint_as_float(0x7FC00000u);
-          lv = __log2f(v);
-          inv = v == v ? 1.f / v : 1.f;  // (a NaN comes with the weights, to the rows that have any)
-          if (ids == bad_id) kc = 0.f, lv = -INFINITY, inv = 0.f;  // no weights (K and V are zeros)
           __syncwarp();
         }
         const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+        if (!wait(base + S::k_empty + 8 * ks, k_phase)) break;
+        tile_g2s_5d(base + ks * kTileBytes, &map_k, w.h, id, base + S::k_full + 8 * ks);
+        if ((i & 31) == 0) {  // (the scales' loads are on their way while K's copy is)
+          kc = k_raw * fp.qk;
+          const float v = v_raw >= 0.f ? fmaxf(v_raw, kLeastScale) : __uint_as_float(0x7FC00000u);
+          lv = __log2f(v);
+          inv = v == v ? 1.f / v : 1.f;  // (a NaN comes with the weights, to the rows that have any)
+          if (ids == bad_id) kc = 0.f, lv = -INFINITY, inv = 0.f;  // no weights (K and V are zeros)
+        }
         const float k = __shfl_sync(0xffffffffu, kc, i & 31), l = __shfl_sync(0xffffffffu, lv, i & 31),
                     v = __shfl_sync(0xffffffffu, inv, i & 31);
-        if (!wait(base + S::k_empty + 8 * ks, k_phase)) break;
         sts128(base + S::meta + 16 * (number++ % kMetas), __float_as_uint(k), __float_as_uint(l), __float_as_uint(v), 0u);
         __syncwarp();
-        arrive_expect(base + S::k_full + 8 * ks, kTileBytes);
-        tile_g2s_5d(base + ks * kTileBytes, &map_k, w.h, id, base + S::k_full + 8 * ks);
+        arrive_expect(base + S::k_full + 8 * ks, kTileBytes);  // (with the block's word there)
         if (++ks == S::kK) ks = 0, k_phase ^= 1;
         if (!wait(base + S::v_empty + 8 * vs, v_phase)) break;
         arrive_expect(base + S::v_full + 8 * vs, kTileBytes);
@@ -677,6 +684,7 @@ cudaError_t launch_dense_pa_fp8(const DensePaFp8Params& a, int num_sms, cudaStre
   p.k_scales = a.k_scales, p.v_scales = a.v_scales, p.k_scale = a.k_scale, p.v_scale = a.v_scale;
   set_work(p.w, pl, num_sms);
   p.w.least = kLeastBlocks;
+  p.w.more = kMoreBlocks;
   CUtensorMap mk, mv;
   const uint64_t blocks = std::max<int64_t>(a.a.num_blocks, 1);
   if (!make_map_side(&mk, true, a.a.k_base, a.a.hkv, blocks, a.a.id_stride) ||

@@ -27,6 +27,7 @@ struct Params {
   int32_t rows;                      // of a unit's slot in the workspace
   int32_t by_unit;                   // the list of cut units has an entry per unit (else per CTA)
   int32_t least;                     // shares of enough blocks in all (128 of them for each) have so many at least
+  int32_t more;                      // blocks that a share may grow by so as to hold one unit's only; < 0: none
 };
 
 // ---- units ---------------------------------------------------------------------
@@ -44,11 +45,18 @@ __device__ __forceinline__ int group_len(const DensePaParams& a, int g, int firs
   return len;
 }
 
+// ... as shares are measured: a multiple of `pad`, the share's length where no share is to
+// hold parts of two units, else 1
+__device__ __forceinline__ int length_of(const DensePaParams& a, int len, int pad) {
+  const int nb = blocks_of(a, len);
+  return pad == 1 ? nb : (nb + pad - 1) / pad * pad;
+}
+
 // A warp's walk over the pieces of a share [at, end) of the units' blocks.
 // Every lane holds the same values.
 struct Walk {
-  int64_t at, end, c0;  // c0: blocks of the groups before g
-  int g, nb;
+  int64_t at, end, c0;  // c0: length of the groups before g
+  int g, nb, pad;       // nb: length of g
   // the piece at `at`
   int unit, h, tok0, tokens, seq, b0, nblk, max_len, min_len;
   bool starts, ends;  // the unit's first and last blocks are in the piece
@@ -59,7 +67,7 @@ struct Walk {
     while ((c0 + nb) * a.hkv <= at) {
       c0 += nb;
       ++g;
-      nb = blocks_of(a, __reduce_max_sync(0xffffffffu, group_len(a, g, lane, 32)));
+      nb = length_of(a, __reduce_max_sync(0xffffffffu, group_len(a, g, lane, 32)), pad);
     }
     h = a.hkv == 1 ? 0 : static_cast<int>((at - c0 * a.hkv) / nb);
     const int64_t ustart = c0 * a.hkv + static_cast<int64_t>(h) * nb, uend = ustart + nb;
@@ -86,6 +94,7 @@ struct Walk {
 // group, the blocks before it, its blocks to `start`, which the next barrier publishes.
 struct Share {
   int64_t at, share, total;
+  int pad;
 };
 template <int THREADS>
 __device__ __forceinline__ Share find_share(const Params& p, int turn, int64_t* s_sum, int64_t* s_start) {
@@ -94,37 +103,51 @@ __device__ __forceinline__ Share find_share(const Params& p, int turn, int64_t* 
   const int per = (p.groups + THREADS - 1) / THREADS;
   const int g_lo = static_cast<int>(min(static_cast<int64_t>(tid) * per, static_cast<int64_t>(p.groups)));
   const int g_hi = min(g_lo + per, p.groups);
-  int64_t mine = 0;
-#pragma unroll 4
-  for (int g = g_lo; g < g_hi; ++g) mine += blocks_of(a, group_len(a, g, 0, 1));
-  int64_t upto = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += y;
-  }
-  if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
+  int64_t mine, upto, total, share = 0;
+  int pad = 1;
 #pragma unroll 1
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) upto += s_sum[w];
-    total += s_sum[w];
+  for (bool again = false;; again = true) {
+    mine = 0;
+#pragma unroll 4
+    for (int g = g_lo; g < g_hi; ++g) mine += length_of(a, group_len(a, g, 0, 1), pad);
+    upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    total = 0;
+#pragma unroll 1
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) upto += s_sum[w];
+      total += s_sum[w];
+    }
+    if (again) break;
+    const int64_t blocks = total * a.hkv, least = min(static_cast<int64_t>(p.least), max(blocks >> 7, int64_t{1}));
+    share = max((blocks + p.shares - 1) / p.shares, least);
+    // Shares of one unit's blocks only: as many as there are do for this length (a unit's last may be short).
+    const int64_t pairs = static_cast<int64_t>(p.groups) * a.hkv, spare = p.shares - pairs;
+    if (p.more < 0 || pairs == 1 || spare <= 0) break;
+    const int64_t whole = max((blocks + spare - 1) / spare, least);
+    if (whole == 1 || whole > share + p.more) break;
+    share = whole, pad = static_cast<int>(whole);
+    __syncthreads();  // the sums are read
   }
-  const int64_t least = min(static_cast<int64_t>(p.least), max(total * a.hkv >> 7, int64_t{1}));
-  const int64_t share = max((total * a.hkv + p.shares - 1) / p.shares, least), at = turn * share;
+  const int64_t at = turn * share;
   if ((upto - mine) * a.hkv <= at && at < upto * a.hkv) {
     int64_t c = upto - mine;
-    int g = g_lo, nb = blocks_of(a, group_len(a, g, 0, 1));
-    while (at >= (c + nb) * a.hkv) c += nb, nb = blocks_of(a, group_len(a, ++g, 0, 1));
+    int g = g_lo, nb = length_of(a, group_len(a, g, 0, 1), pad);
+    while (at >= (c + nb) * a.hkv) c += nb, nb = length_of(a, group_len(a, ++g, 0, 1), pad);
     s_start[0] = g, s_start[1] = c, s_start[2] = nb;
   }
-  return {at, share, total};
+  return {at, share, total, pad};
 }
 __device__ __forceinline__ Walk walk_of(const Params& p, const Share& sh, const int64_t* s_start) {
   Walk w;
   w.at = sh.at, w.end = min(sh.at + sh.share, sh.total * p.a.hkv);
-  w.g = 0, w.c0 = 0, w.nb = 1;
+  w.g = 0, w.c0 = 0, w.nb = 1, w.pad = sh.pad;
   if (w.at < w.end) w.g = static_cast<int>(s_start[0]), w.c0 = s_start[1], w.nb = static_cast<int>(s_start[2]);
   return w;
 }
@@ -163,6 +186,18 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
       const int64_t slot = k == 0 ? 2LL * c0 + 1 : 2LL * (c0 + static_cast<int64_t>(k) * p.subs);
       float2 ml = make_float2(kNoMax, 0.f);
       if (k < pieces) ml = *reinterpret_cast<const float2*>(base + slot * slot_floats + p.rows * kDim + 2 * row);
+      const int here = min(32, (pieces - k0 + parts - 1) / parts);
+      // the first pieces' rows, on their way while the weights are worked out (16 of them took
+      // longer where there are few)
+      constexpr int kFirst = 8;
+      float4 first[kFirst];
+#pragma unroll
+      for (int j = 0; j < kFirst; ++j) {
+        const int kj = k0 + j * parts;
+        const int64_t sj = kj == 0 ? 2LL * c0 + 1 : 2LL * (c0 + static_cast<int64_t>(kj) * p.subs);
+        first[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < here) first[j] = *reinterpret_cast<const float4*>(base + sj * slot_floats + row * kDim + 4 * lane);
+      }
       float mx = ml.x;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -173,9 +208,14 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
       L = L * f + ls;
       M = mn;
       x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-      const int here = min(32, (pieces - k0 + parts - 1) / parts);
+#pragma unroll
+      for (int j = 0; j < kFirst; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const float4 y = first[j];
+        if (j < here) x.x += wj * y.x, x.y += wj * y.y, x.z += wj * y.z, x.w += wj * y.w;
+      }
 #pragma unroll 8
-      for (int j = 0; j < here; ++j) {
+      for (int j = kFirst; j < here; ++j) {
         const int kj = k0 + j * parts;
         const int64_t sj = kj == 0 ? 2LL * c0 + 1 : 2LL * (c0 + static_cast<int64_t>(kj) * p.subs);
         const float wj = __shfl_sync(0xffffffffu, w, j);
@@ -227,6 +267,7 @@ inline void set_work(Params& p, const Plan& pl, int num_sms) {
   p.ctas = p.shares * pl.subs;
   p.by_unit = units <= p.ctas;
   p.least = 1;
+  p.more = -1;
 }
 
 // the second launch, where shares may cut units
