@@ -59,6 +59,8 @@ constexpr float kBigRef = 1048576.f;        // references above it: (z - m) c in
 constexpr int kRows = 256, kTile = 128;     // rows of a unit, of a tile
 constexpr int kWhole = 4;                   // blocks of a unit that is not cut
 constexpr int kUnitCost = 2;                // what a unit costs beside its blocks, in blocks
+// Shares of so many blocks, over so many keys and heads (60 MB), may be lengthened, see aligned_share.
+constexpr int kLongShare = 64, kManyKeys = 60 * 1024 * 1024 / (4 * kDim);
 // four warps for each tile, then a producer, an issuer, one that stores, one that idles, four that check V
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpStore = 10, kWarpCheck = 12, kThreads = 512;
 constexpr int kReaders = 8 + 2 + 4;         // warps that read the announced pieces
@@ -272,6 +274,45 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t acc, uint32_t w) {
   return r;
 }
 
+// Few long units, such as some tokens of each request over long contexts: a head's units
+// read the same keys, and each key comes from DRAM once if the shares of those units begin at
+// nearly the same blocks, as they do when a unit is about a whole number of shares
+// long.  Of 16 lengths, the given one and up to 15 / 128 more, the first with the least part
+// of a share left over in all, counted in 64ths of the units.  us, without and with: 3 x 77
+// queries of 16 heads over 100000 keys of two 172, 149; 8 x 25-200 of 8 over 4k-30k of one
+// (69 MB) 68 to 76, 66; but 2 x 500 of 8 over 50000 of one (52 MB, which L2 holds) 145, 150.
+__device__ __noinline__ int64_t aligned_share(const Params& p, int64_t total, int64_t share, Seq q, int64_t* smem) {
+  int* const s_count = reinterpret_cast<int*>(smem + kThreads / 32 + 2);
+  int* const s_left = s_count + 1;
+  int* const s_list = s_left + kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, most = p.ctas / p.a.hkv;
+  if (tid == 0) s_count[0] = 0;
+  __syncthreads();
+  const int mine = min(units_of(q, p), most + 1);
+  const int slot = mine ? atomicAdd(s_count, mine) : 0;
+  __syncthreads();
+  const int units = s_count[0];
+  if (units > most || units * p.a.hkv < 2) return share;
+#pragma unroll 1
+  for (int u = 0; u < mine; ++u) s_list[slot + u] = blocks_of(q, p, u) + kUnitCost;
+  __syncthreads();
+  const int64_t trial = share + (share * warp >> 7);
+  int left = 0;
+#pragma unroll 1
+  for (int i = lane; i < units; i += 32) {
+    const int over = static_cast<int>(s_list[i] % trial);
+    left += static_cast<int>(64 * (over ? trial - over : 0) / trial);
+  }
+  left = __reduce_add_sync(0xffffffffu, left);
+  if (lane == 0) s_left[warp] = left;
+  __syncthreads();
+  int best = 0;
+#pragma unroll 1
+  for (int w = 1; w < kThreads / 32; ++w)
+    if (s_left[w] < s_left[best]) best = w;
+  return share + (share * best >> 7);
+}
+
 // ---- the main kernel -------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -335,7 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w < warp) upto += x;
     total += x;
   }
-  const int64_t share = max((total + p.ctas - 1) / p.ctas, int64_t{1}), at = blockIdx.x * share;
+  int64_t share = max((total + p.ctas - 1) / p.ctas, int64_t{1});
+  if (chunk <= 1 && share >= kLongShare && a.num_keys * static_cast<int64_t>(a.hkv) >= kManyKeys) share = aligned_share(p, total, share, tid < n ? load_seq(a, tid) : Seq{}, s_sum);
+  const int64_t at = blockIdx.x * share;
   if (upto - mine <= at && at < upto) {
     int64_t c = upto - mine;
     int s = s_lo;

@@ -49,6 +49,13 @@ def test_many_heads(hkv, group):
     A.close(A.attend(p), *A.expected(p))
 
 
+def test_shares_that_are_lengthened_to_fit_the_units():
+    """some tokens of each request, three units a head, over more keys than L2 holds"""
+    nk = (13000, 12000, 14001, 13000, 13100, 12900, 13000, 13333)
+    p = A.problem(26, (33, 40, 33, 47, 33, 33, 35, 33), nk, 4, 16)
+    A.close(A.attend(p), *A.expected(p))
+
+
 def test_a_cache_past_32_bits():
     """Write, read and attention in the last of 131100 blocks (4.3 GB) give what a
     small cache with the same tokens gives."""
