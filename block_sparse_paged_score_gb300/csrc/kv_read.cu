@@ -35,10 +35,14 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 
 // 8 e4m3 bytes times sc
 __device__ __forceinline__ uint4 from_e4m3(uint2 w, float sc) {
-  float x[8];
+  uint32_t h[4], o[4];
+  e4m3x4_to_f16x2_cvt(w.x, h[0], h[1]), e4m3x4_to_f16x2_cvt(w.y, h[2], h[3]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = e4m3_to_float((i < 4 ? w.x : w.y) >> (8 * (i & 3))) * sc;
-  return pack8(x);
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = fmul2(f16x2_to_float2(h[i]), {sc, sc});
+    o[i] = pack_bf16x2(x.x, x.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // dims 8*l.. of token o of an MXFP4 field
@@ -83,37 +87,46 @@ __global__ void __launch_bounds__(128) kv_page_read_kernel(KvReadParams p) {
     // sixteen tokens of a block, one behind the other?
     const int64_t s0 = s_slot[0];
     if (__all_sync(0xffffffffu, s0 >= 0 && s_slot[l] == s0 + l) && s0 / kBlock == (s0 + kTok - 1) / kBlock) {
-      // K and V are on their way together: of K a thread has 8 dims of two tokens, of V its
-      // dim's bytes of the two pages that the tokens may lie in
+      // K and V are on their way together: of K a thread has 8 dims of two tokens, of V two
+      // dims of 8 tokens, which begin anywhere in the dims' 8-byte pieces (of one page or two)
       const int64_t block = s0 / kBlock;
-      const int o = static_cast<int>(s0 % kBlock), r = o % kPage;
+      const int o = static_cast<int>(s0 % kBlock), r = o % kPage, j = tid & 63, t0 = tid >> 6 << 3;
       const float ks = p.k_scales ? p.k_scales[block * c.hkv + h] : c.k_scale;
       const float vs = p.v_scales ? p.v_scales[block * c.hkv + h] : c.v_scale;
       const uint8_t* const kp = c.k_base + block * 16 * c.id_stride + static_cast<int64_t>(h) * 2048;
-      const uint8_t* const vp = c.v_base + (block * 16 + o / kPage) * c.id_stride + static_cast<int64_t>(h) * 2048 + tid * 16;
-      uint2 kw[2];
+      const uint8_t* const vp = c.v_base + (block * 16 + o / kPage) * c.id_stride + static_cast<int64_t>(h) * 2048 + j * 32;
+      uint2 kw[2], va[2], vb[2] = {};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = o + (tid >> 4) + 8 * i;
         kw[i] = *reinterpret_cast<const uint2*>(kp + (t / kPage) * c.id_stride + (l >> 1) * 256 + t % kPage * 16 + (l & 1) * 8);
       }
-      const uint4 va = *reinterpret_cast<const uint4*>(vp);
-      uint4 vb = zero;
-      if (r) vb = *reinterpret_cast<const uint4*>(vp + c.id_stride);
+      const int piece = (r + t0) >> 3;
+      const uint8_t* const at = vp + (piece >> 1) * c.id_stride + (piece & 1) * 8;
+      const uint8_t* const next = vp + ((piece + 1) >> 1) * c.id_stride + ((piece + 1) & 1) * 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) va[i] = *reinterpret_cast<const uint2*>(at + i * 16);
+      if (r & 7) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) vb[i] = *reinterpret_cast<const uint2*>(next + i * 16);
+      }
       const int64_t row = ((tok0 + (tid >> 4)) * c.hkv + h) * kDim + 8 * l, hop = 8LL * c.hkv * kDim;
 #pragma unroll
       for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(p.k + row + i * hop) = from_e4m3(kw[i], ks);
-      // the 16 bytes from the first token on
-      const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-      uint32_t y[5];
+      float2 x[2][4];  // of a dim, pairs of tokens
 #pragma unroll
-      for (int i = 0; i < 5; ++i) y[i] = r < 4 ? w[i] : r < 8 ? w[i + 1] : r < 12 ? w[i + 2] : w[i + 3];
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t y0 = r & 4 ? va[i].y : va[i].x, y1 = r & 4 ? vb[i].x : va[i].y, y2 = r & 4 ? vb[i].y : vb[i].x;
+        uint32_t f[4];
+        e4m3x4_to_f16x2_cvt(__funnelshift_r(y0, y1, 8 * (r & 3)), f[0], f[1]);
+        e4m3x4_to_f16x2_cvt(__funnelshift_r(y1, y2, 8 * (r & 3)), f[2], f[3]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t z = __funnelshift_r(y[i], y[i + 1], 8 * (r & 3));
+        for (int k = 0; k < 4; ++k) x[i][k] = fmul2(f16x2_to_float2(f[k]), {vs, vs});
+      }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          s_v[4 * i + k][tid] = static_cast<uint16_t>(pack_bf16x2(e4m3_to_float(z >> (8 * k)) * vs, 0.f));
+      for (int k = 0; k < 4; ++k) {
+        *reinterpret_cast<uint32_t*>(&s_v[t0 + 2 * k][2 * j]) = pack_bf16x2(x[0][k].x, x[1][k].x);
+        *reinterpret_cast<uint32_t*>(&s_v[t0 + 2 * k + 1][2 * j]) = pack_bf16x2(x[0][k].y, x[1][k].y);
       }
       __syncthreads();
 #pragma unroll

@@ -58,8 +58,10 @@ struct Side {
 
 // four e4m3 bytes times f, rounded again
 __device__ __forceinline__ uint32_t times(uint32_t w, float f) {
-  return float2_to_e4m3x2(e4m3_to_float(w) * f, e4m3_to_float(w >> 8) * f) |
-         float2_to_e4m3x2(e4m3_to_float(w >> 16) * f, e4m3_to_float(w >> 24) * f) << 16;
+  uint32_t l, h;
+  e4m3x4_to_f16x2_cvt(w, l, h);
+  const float2 x = fmul2(f16x2_to_float2(l), {f, f}), y = fmul2(f16x2_to_float2(h), {f, f});
+  return float2_to_e4m3x2(x.x, x.y) | float2_to_e4m3x2(y.x, y.y) << 16;
 }
 // A block's bytes in a new scale's terms: 16-byte chunks first, first + step .. of 1024.
 __device__ __forceinline__ void rescale_block(uint8_t* block, int64_t id_stride, float f, int first, int step) {
@@ -70,12 +72,14 @@ __device__ __forceinline__ void rescale_block(uint8_t* block, int64_t id_stride,
     *at = make_uint4(times(w.x, f), times(w.y, f), times(w.z, f), times(w.w, f));
   }
 }
+// (out of the way: a division's code at each use would be most of the kernel's 100 KB)
+__device__ __noinline__ uint32_t divided(float u, float v, float s) { return float2_to_e4m3x2(u / s, v / s); }
 // two of a run's bytes, of the scale s
 struct Encode {
   float s, inv;
   bool pow2;
   __device__ __forceinline__ uint32_t operator()(float u, float v) const {
-    return pow2 ? float2_to_e4m3x2(u * inv, v * inv) : float2_to_e4m3x2(u / s, v / s);
+    return pow2 ? float2_to_e4m3x2(u * inv, v * inv) : divided(u, v, s);
   }
 };
 __device__ __forceinline__ Encode encode_by(float s) { return {s, 1.f / s, (__float_as_uint(s) & 0x7FFFFFu) == 0}; }
