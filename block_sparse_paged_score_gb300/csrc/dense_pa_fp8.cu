@@ -30,6 +30,12 @@
 // V is NaN: in blocks that some row does not see whole such bytes are read as 0, and
 // the rows that see the first of them get their NaN at the end.
 //
+// Measured: 64 requests of 131072 tokens, 16 rows each, 320 to 325 us, 6.6 to 6.7 TB/s, 98 % of
+// the copy rate: memory; 128 of 32768 with 64 rows 208 us, 5.2 TB/s, and with bf16 queries 235: a
+// block's chain of logits, exponentials, P and V, with the two CTAs that TMEM has room for;
+// 32 of 4k to 8k 24.7 us: 6 us to a CTA's first block, 1.8 for each of four, 2.5 for sums and O,
+// 4.5 for the join; one of 1000 tokens 10.6 us.
+//
 // Every wait is bounded: after one that gave up (the error word is set, the results are
 // void) loader and issuer issue nothing more and wait for what they have under way; a
 // compute warp walks through its blocks without waits and arrivals.
@@ -78,7 +84,8 @@ struct Shape {
 };
 template <int N, bool Q16>
 struct Smem {
-  static constexpr int kK = N == 32 ? 3 : N == 16 ? 1 : 2, kV = N == 16 ? 1 : 2;  // stages (as much as the CTAs of an SM leave room for)
+  // stages (as much as the CTAs of an SM leave room for)
+  static constexpr int kK = N == 32 ? 3 : N == 16 ? 1 : 2, kV = N == 16 ? 1 : 2;
   static constexpr int v = kK * kTileBytes;
   static constexpr int p = v + kV * kTileBytes;        // P [128 tokens][N rows] f16
   static constexpr int q = p + kBlock * N * 2;
@@ -194,7 +201,8 @@ __device__ __noinline__ void stage_q(const DensePaParams& a, int tok0, int token
   }
   *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   *reinterpret_cast<uint4*>(dst + rows * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  if (j == 0) rowfac[n] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+  if (j == 0)
+    rowfac[n] = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
 }
 
 // CH logits of a lane's token as t, in the rows' and the block's terms

@@ -19,8 +19,8 @@
 // of V two dims of the 32 tokens of two pages, which its pages hold side by side, so
 // that both leave as vectors.
 //
-// Measured (one call of a row of them): 64 decode tokens of a head 4.0 us, about a
-// launch and a block's new scale; 8 prompts of 300 to 2400 tokens, two heads, 12 us for
+// Measured (one call of a row of them): 64 decode tokens of a head 3.7 us, about a
+// launch and a block's new scale; 8 prompts of 300 to 2400 tokens, two heads, 11 us for
 // 17 MB.  There a run's chain of dependent steps is what it takes (slots, table, rows,
 // maximum, bytes), not bandwidth: loading a run's slots at once, and more tokens
 // a CTA, did not shorten it.

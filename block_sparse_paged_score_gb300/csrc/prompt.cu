@@ -7,8 +7,9 @@
 // query heads of the KV head, so that short prompts fill the tensor cores' rows too and
 // a unit's keys end together.  It is two tiles of 128 rows.  Units' 128-key blocks laid
 // end to end, causal ones only, and kUnitCost for each unit's beginning and end, are cut into
-// equal shares, one per CTA: the length of a sequence's units is a closed sum, and a CTA finds its share by a prefix sum over the
-// sequences.  Units of at most kWhole blocks stay whole.  Of a unit that share borders
+// equal shares, one per CTA: the length of a sequence's units is a closed sum, and a CTA
+// finds its share by a prefix sum over the sequences.  Units of at most kWhole blocks stay
+// whole.  Of a unit that share borders
 // cut each CTA leaves (m, l, O) in the workspace, and a second kernel joins them; the
 // order of all sums is fixed.
 //
@@ -37,6 +38,12 @@
 // Roundings: a weight is bf16, half a step 2^-8 off; z, m, l and O are fp32, and l sums
 // the unrounded weights.
 //
+// Measured: a prompt of 32768 tokens of 16 heads 2.22 to 2.52 ms, 1.75 to 1.98 PFLOP/s by the
+// clock that the power limit leaves (cuBLAS 1.87); 32 prompts of 250 to 2000 tokens 172 us, 1.15
+// PFLOP/s: there a unit's beginning and end, a chain of some 6000 clocks, bound it; 3 x 77
+// tokens over 100000 keys 150 us; one prompt of 100 tokens 8.3 us.  The kernels' code counts: at
+// 117 KB instead of 81 instruction fetches were the first stall.
+//
 // Every wait is bounded: after one that gave up (the error word is set, the results are
 // void) its warp issues nothing more and waits for what it has under way, with a limit
 // again; the others' waits run out in turn.
@@ -53,12 +60,17 @@ namespace bsp {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaxSum = 1073741824.f;     // of a half block's weights (bf16 and fp32 hold any; V of 2^80 and more may overflow)
+constexpr float kMaxSum = 1073741824.f;     // of a half block's weights (bf16 and fp32 hold any)
 constexpr float kNoMax = -3.402823466e38f;  // the maximum of no keys (finite: -inf - kNoMax stays -inf)
-constexpr float kBigRef = 1048576.f;        // references above it: (z - m) c instead of z c - (m c), whose rounding then counts
+// references above it: (z - m) c instead of z c - (m c), whose rounding then counts
+constexpr float kBigRef = 1048576.f;
 constexpr int kRows = 256, kTile = 128;     // rows of a unit, of a tile
-constexpr int kWhole = 4;                   // blocks of a unit that is not cut
-constexpr int kUnitCost = 2;                // what a unit costs beside its blocks, in blocks
+// Blocks of a unit that is not cut.  2, 4, 8: 132, 132, 130 us on 32 prompts of 1024 tokens of 16
+// heads, 32, 34, 34 on 6 of 2500 of one.  (Up to as many there is no second launch.)
+constexpr int kWhole = 4;
+// What a unit costs beside its blocks, in blocks: 0, 1, 2, 3 take 220, 181, 171, 178 us on 32
+// prompts of 250 to 2000 tokens and 155, 141, 132, 136 on 32 of 1024.
+constexpr int kUnitCost = 2;
 // Shares of so many blocks, over so many keys and heads (60 MB), may be lengthened, see aligned_share.
 constexpr int kLongShare = 64, kManyKeys = 60 * 1024 * 1024 / (4 * kDim);
 // four warps for each tile, then a producer, an issuer, one that stores, one that idles, four that check V
@@ -88,11 +100,12 @@ struct Piece {
 struct Smem {
   static constexpr int q = 0, kv = 2 * kTileBytes, bars = kv + kStages * kTileBytes;
   static constexpr int q_full = bars, q_empty = bars + 8, kv_full = bars + 16, kv_empty = kv_full + 8 * kStages,
-                       v_look = kv_empty + 8 * kStages, v_ok = v_look + 8 * kStages, s_full = v_ok + 8 * kStages, p_full = s_full + 16, half = p_full + 32,
-                       o_full = half + 16, staged = o_full + 16, piece_full = staged + 16, piece_empty = piece_full + 8 * kPieces,
-                       fin = piece_empty + 8 * kPieces;
+                       v_look = kv_empty + 8 * kStages, v_ok = v_look + 8 * kStages, s_full = v_ok + 8 * kStages,
+                       p_full = s_full + 16, half = p_full + 32, o_full = half + 16, staged = o_full + 16,
+                       piece_full = staged + 16, piece_empty = piece_full + 8 * kPieces, fin = piece_empty + 8 * kPieces;
   static constexpr int pieces = fin + 8;
-  static constexpr int tmem = pieces + kPieces * sizeof(Piece), bad = tmem + 8;  // bad[8]: pieces with values of V that are not finite
+  static constexpr int tmem = pieces + kPieces * sizeof(Piece);
+  static constexpr int bad = tmem + 8;  // [8]: pieces with values of V that are not finite
   static constexpr int total = bad + 32;
   static_assert(pieces % 8 == 0 && total <= 227 * 1024);
 };
@@ -140,7 +153,8 @@ __device__ __forceinline__ int64_t blocks_before(const Seq& s, const Params& p, 
       };
       sum += upto(A + m) - upto(A + one);
     } else {  // T = 256
-      sum += static_cast<int64_t>(m - one) * -((-off) >> 7) + (static_cast<int64_t>(m) * (m + 1) - static_cast<int64_t>(one) * (one + 1));
+      sum += static_cast<int64_t>(m - one) * -((-off) >> 7) +
+             (static_cast<int64_t>(m) * (m + 1) - static_cast<int64_t>(one) * (one + 1));
     }
   }
   return u == n && n > 0 ? sum + blocks_of(s, p, n - 1) : sum;
@@ -377,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += x;
   }
   int64_t share = max((total + p.ctas - 1) / p.ctas, int64_t{1});
-  if (chunk <= 1 && share >= kLongShare && a.num_keys * static_cast<int64_t>(a.hkv) >= kManyKeys) share = aligned_share(p, total, share, tid < n ? load_seq(a, tid) : Seq{}, s_sum);
+  if (chunk <= 1 && share >= kLongShare && a.num_keys * static_cast<int64_t>(a.hkv) >= kManyKeys)
+    share = aligned_share(p, total, share, tid < n ? load_seq(a, tid) : Seq{}, s_sum);
   const int64_t at = blockIdx.x * share;
   if (upto - mine <= at && at < upto) {
     int64_t c = upto - mine;
@@ -805,7 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(po)[(8 * k + i) * kRows + row] = make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
+            reinterpret_cast<float4*>(po)[(8 * k + i) * kRows + row] =
+                make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
         }
       }
       if (__builtin_expect(fix, 0) && tok < e.tokens) {
@@ -817,7 +833,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int d = 0; d < kDim; ++d) {
             if ((v[d] & 0x7F80) != 0x7F80) continue;
-            uint16_t* x = reinterpret_cast<uint16_t*>(smem + (stage - base) + (d >> 6) * kHalf + ((((d & 63) >> 3) ^ (row & 7)) << 4)) + (d & 7);
+            uint16_t* x = reinterpret_cast<uint16_t*>(smem + (stage - base) + (d >> 6) * kHalf +
+                                                      ((((d & 63) >> 3) ^ (row & 7)) << 4)) + (d & 7);
             float* y = po + (d >> 2) * (kRows * 4) + row * 4 + (d & 3);
             const float sum = (all ? bf16_bits_to_float(*x) : *y) + bf16_bits_to_float(v[d]);
             if (all)
