@@ -20,7 +20,7 @@
 // that both leave as vectors.
 //
 // Measured (one call of a row of them): 64 decode tokens of a head 3.7 us, about a
-// launch and a block's new scale; 8 prompts of 300 to 2400 tokens, two heads, 11 us for
+// launch and a block's new scale; 8 prompts of 300 to 2400 tokens, two heads, 10.7 us for
 // 17 MB.  There a run's chain of dependent steps is what it takes (slots, table, rows,
 // maximum, bytes), not bandwidth: loading a run's slots at once, and more tokens
 // a CTA, did not shorten it.
