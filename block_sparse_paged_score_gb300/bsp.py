@@ -260,10 +260,11 @@ class BlockScaledKvCache(KvCache):
     """An interleaved fp8 K/V cache with a scale for each 128-token block and
     head: k_scales and v_scales, fp32 [num_blocks, num_kv_heads], the caller's
     or of its own.  Written by kv_scaled_write, read by kv_scaled_read and
-    dense_pa_decode_fp8."""
+    dense_pa_decode_fp8; its per-tensor scales are NaN, so that calls which know
+    only those show that they do not fit."""
 
     def __init__(self, num_kv_heads, num_blocks, buffer=None, k_scales=None, v_scales=None, device="cuda"):
-        super().__init__(FP8_E4M3, num_kv_heads, num_blocks, buffer=buffer, device=device)
+        super().__init__(FP8_E4M3, num_kv_heads, num_blocks, math.nan, math.nan, buffer=buffer, device=device)
         n = num_blocks * num_kv_heads
         self.k_scales, self.v_scales = (
             t if t is not None else torch.zeros(num_blocks, num_kv_heads, device=self.buffer.device)

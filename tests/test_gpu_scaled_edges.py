@@ -112,6 +112,23 @@ def calls():
             lambda: bsp.dense_pa_fp8_workspace(len(lens), 2, 4, 2), lambda: torch.zeros_like(q))
 
 
+def test_calls_that_know_only_per_tensor_scales_give_nan():
+    from block_sparse_paged_score_gb300 import bsp
+    c = bsp.BlockScaledKvCache(1, 2)
+    x = torch.ones(20, 1, 128, dtype=torch.bfloat16, device="cuda")
+    slot = torch.arange(20, device="cuda")
+    bsp.kv_scaled_write(c, x, x, slot)
+    k, v = bsp.kv_scaled_read(c, slot)
+    assert equal(k, x) and equal(v, x)
+    k, v, _ = bsp.kv_page_read(c, None, slot)
+    assert k.isnan().all() and v.isnan().all()
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = i(0, 1).view(1, 2)
+    kv = bsp.KvCache(bsp.FP8_E4M3, 1, 2, c.desc.k_scale, c.desc.v_scale, buffer=c.buffer)
+    assert bsp.dense_pa_decode_fp8(kv, x[:1], bsp.BF16, 1, table, i(0), i(20), 1).isnan().all()
+    assert equal(bsp.dense_pa_decode_fp8(c, x[:1], bsp.BF16, 1, table, i(0), i(20), 1), x[:1])
+
+
 def test_calls_at_once():
     """both operators on four streams, each with its own workspace"""
     both = calls()
