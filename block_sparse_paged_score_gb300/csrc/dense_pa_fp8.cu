@@ -24,14 +24,14 @@
 //
 // A CTA is a loader warp, an issuer warp and four or eight compute warps.  Thread = token
 // of the logits: its exponentials against the rows' references, which move only when a
-// row's maximum passes its own by kMaxGrow; a vote of the compute warps finds those
-// blocks, and the ones that some row does not see whole, and takes them through an
-// uncommon way.  Then thread = dim turns V to f16, 16 tokens a load.  0 times a NaN byte of
+// row's maximum passes its own by kMaxGrow; a vote of the four warps that share rows
+// finds those blocks, and the ones that some row does not see whole, and takes them
+// through an uncommon way (of eight warps: 214.5 us for 207 of 64 rows a request).  Then thread = dim turns V to f16, 16 tokens a load.  0 times a NaN byte of
 // V is NaN: in blocks that some row does not see whole such bytes are read as 0, and
 // the rows that see the first of them get their NaN at the end.
 //
 // Measured: 64 requests of 131072 tokens, 16 rows each, 320 to 325 us, 6.6 to 6.7 TB/s, 98 % of
-// the copy rate: memory; 128 of 32768 with 64 rows 208 us, 5.2 TB/s, and with bf16 queries 235: a
+// the copy rate: memory; 128 of 32768 with 64 rows 201 us, 5.3 TB/s, and with bf16 queries 225: a
 // block's chain of logits, exponentials, P and V, with the two CTAs that TMEM has room for;
 // 32 of 4k to 8k 24.7 us: 6 us to a CTA's first block, 1.8 for each of four, 2.5 for sums and O,
 // 4.5 for the join; one of 1000 tokens 10.6 us.
@@ -222,6 +222,17 @@ __device__ __forceinline__ void load_t(float2 (&t)[CH / 2], uint32_t z_at, uint3
   }
 }
 
+// barrier of four warps that returns whether every thread says so
+__device__ __forceinline__ bool four_agree(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
 // ---- the main kernel -----------------------------------------------------------
 template <int N, bool Q16>
 __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
@@ -381,7 +392,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     // Warp: TMEM lanes 32 * quad .., that is the logits of the block's tokens 32 * quad ..
     // and O's and V's dims 32 * quad ..; R rows of the former, VP pages of V.
     constexpr int R = Shape<N>::kRows, CH = 16, VP = Shape<N>::kPages;
-    const int quad = warp & 3, half = warp >> 2;
+    // The four warps of a half look after its rows by themselves.
+    const int quad = warp & 3, half = warp >> 2, group = 2 + half;           // group: their barrier
+    const int mine = (tid & 127) < R ? half * R + (tid & 127) : 0x7FFFFFFF;  // a row of theirs
     const uint32_t tops = base + S::tops, lens_at = base + S::len, fac = base + S::fac;
     int* lens = reinterpret_cast<int*>(smem + S::len);
     int* nans = reinterpret_cast<int*>(smem + S::nan);
@@ -409,8 +422,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         // (rows that no token has see what the longest sees: they must not look uncommon)
         lens[tid] = j < w.tokens ? min(max(a.row_len[static_cast<int64_t>(w.tok0 + j) * a.hkv + w.h], 0), w.max_len)
                                  : w.max_len;
-        stsf(base + S::refs + (cur * N + tid) * 4, -kNoMax);
       }
+      if (mine < N) stsf(base + S::refs + (cur * N + mine) * 4, -kNoMax);
       if (tid < kDim) nans[tid] = 0x7FFFFFFF;
       if (tid < w.tokens && a.row_seq[static_cast<int64_t>(w.tok0 + tid) * a.hkv + w.h] != w.seq)
         set_err(a.err, BSP_DEVERR_GROUP_SEQ);
@@ -453,7 +466,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         load();
 #pragma unroll
         for (int i = 0; i < R / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
-        if (__builtin_expect(!all_of<32 * kCompute>(whole && top <= kMaxGrow + kBias), 0)) {
+        if (__builtin_expect(!four_agree(group, whole && top <= kMaxGrow + kBias), 0)) {
           // The uncommon way: the rows' maxima over what they see, new references, and
           // O and l in their terms.
 #pragma unroll 1
@@ -470,19 +483,19 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
             if (!(lane & 1)) stsf(tops + (quad * N + half * R + c + (lane >> 1)) * 4, mx);
             __syncwarp();
           }
-          bar_sync(1, 32 * kCompute);
+          bar_sync(group, 128);
           float f = 1.f;
-          if (tid < N) {
-            float mx = ldsf(tops + tid * 4);
+          if (mine < N) {
+            float mx = ldsf(tops + mine * 4);
 #pragma unroll
-            for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + tid) * 4));
-            const float old = ldsf(base + S::refs + (cur * N + tid) * 4), ref = fminf(old, kBias - mx);
+            for (int i = 1; i < 4; ++i) mx = fmaxf(mx, ldsf(tops + (i * N + mine) * 4));
+            const float old = ldsf(base + S::refs + (cur * N + mine) * 4), ref = fminf(old, kBias - mx);
             f = rescale(-old, -ref, 1.f);
-            stsf(base + S::refs + ((cur ^ 1) * N + tid) * 4, ref);
-            stsf(fac + tid * 4, f);
+            stsf(base + S::refs + ((cur ^ 1) * N + mine) * 4, ref);
+            stsf(fac + mine * 4, f);
           }
           cur ^= 1;
-          if (any_of<32 * kCompute>(f != 1.f) && !first) {
+          if (!four_agree(group, f == 1.f) && !first) {
             done(round);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
@@ -574,13 +587,13 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + list_bytes(p.ctas)) +
                   (2LL * blockIdx.x + (w.starts ? 1 : 0)) * N * (kDim + 2);
       const int rows = w.tokens * a.group;
-      if (tid < N) {  // what O is multiplied by
-        const float sum = (ldsf(tops + tid * 4) + ldsf(tops + (N + tid) * 4)) +
-                          (ldsf(tops + (2 * N + tid) * 4) + ldsf(tops + (3 * N + tid) * 4));
-        stsf(fac + tid * 4, !all ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
-        if (!all && tid < rows)
-          *reinterpret_cast<float2*>(po + N * kDim + 2 * tid) =
-              make_float2(-ldsf(base + S::refs + (cur * N + tid) * 4), sum);
+      if (mine < N) {  // what O is multiplied by
+        const float sum = (ldsf(tops + mine * 4) + ldsf(tops + (N + mine) * 4)) +
+                          (ldsf(tops + (2 * N + mine) * 4) + ldsf(tops + (3 * N + mine) * 4));
+        stsf(fac + mine * 4, !all ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
+        if (!all && mine < rows)
+          *reinterpret_cast<float2*>(po + N * kDim + 2 * mine) =
+              make_float2(-ldsf(base + S::refs + (cur * N + mine) * 4), sum);
       }
       bar_sync(1, 32 * kCompute);
       if (!first) done(round);
