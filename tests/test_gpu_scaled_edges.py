@@ -49,6 +49,20 @@ def test_many_heads(hkv, group):
     A.close(A.attend(p), *A.expected(p))
 
 
+@pytest.mark.parametrize("power", [70, -70])
+def test_values_far_from_one(power):
+    """V times a power of two gives the output times it, bit for bit, also where later
+    logits are up to e^20 times the first block's: nothing overflows on the way"""
+    p = A.problem(27, (300, 1, 40), (300, 3000, 1500), 2, 8)
+    ramp = torch.linspace(0, 1, len(p["k"]), device="cuda")[:, None]
+    p["k"][..., 0] = (ramp * 20 * 128 ** 0.5).bfloat16()
+    p["q"][..., 0] = 1
+    want = A.attend(p)
+    A.close(want, *A.expected(p))
+    p["v"] = p["v"] * 2.0 ** power
+    assert equal(A.attend(p), want * 2.0 ** power)
+
+
 def test_shares_that_are_lengthened_to_fit_the_units():
     """some tokens of each request, three units a head, over more keys than L2 holds"""
     nk = (13000, 12000, 14001, 13000, 13100, 12900, 13000, 13333)
