@@ -6,7 +6,11 @@
 //
 // with k8, v8 the e4m3 values: a block's V scale is part of its tokens' weights, so that
 // V enters the product as it lies, and a row's reference R counts it; the sums l get the
-// weights without it, a multiplication by 1 / vs that the addition takes along.
+// weights without it, a multiplication by 1 / vs that the addition takes along.  Where V's
+// scales lie far apart a token may have a weight below fp32's range whose share of l counts: a
+// block 2^64 below an earlier one's scale has its l from exponentials of its own, and where a
+// reference moves by more than 2^126, l moves in two steps.  l itself stays in range: it is at
+// least the row's largest exp(z) 2^(kBias - R), and that is 2^(kBias - 128) or more.
 //
 // Work: units, equal shares and the join of cut units as in the MXFP4 kernel
 // (dense_work.cuh).  Both products are tcgen05 MMAs with the block's tokens or V's dims as
@@ -56,6 +60,7 @@ namespace {
 constexpr int kTileBytes = kBlock * kDim;  // of K or V
 constexpr int kMetas = 8;                  // blocks that may be loaded ahead of the compute warps, at least
 constexpr float kLeastScale = 0x1p-60f;
+constexpr float kFarScales = 64.f;  // log2 between V scales from which l does not go by the weights with the scale
 // A share's blocks at least, where there are 512 in all (2 from 256 on): few long pieces are
 // joined faster than many short ones are attended.  Requests of 128k tokens, us, shares of at
 // least 1 and 4 blocks: one 36.4, 28.7, four of 32k 25.5, 24.4; one of 1000 tokens 15.8, 19.8.
@@ -89,7 +94,9 @@ struct Smem {
   static constexpr int v = kK * kTileBytes;
   static constexpr int p = v + kV * kTileBytes;        // P [128 tokens][N rows] f16
   static constexpr int q = p + kBlock * N * 2;
-  static constexpr int meta = q + N * 128 * (Q16 ? 2 : 1);  // [kMetas] k factor, log2 vs, 1 / vs of a block
+  // [kMetas] of a block: k factor, log2 vs, 1 / vs (negative where vs is far below an earlier one of the
+  // piece), whether it is not and every row sees the block whole
+  static constexpr int meta = q + N * 128 * (Q16 ? 2 : 1);
   static constexpr int refs = meta + kMetas * 16;      // [2][N] kBias - R
   static constexpr int rowfac = refs + 2 * N * 4;      // [N] scales of the query rows
   static constexpr int fac = rowfac + N * 4;           // [N] rescale factors
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
     while (alive && w.next(p, sub, lane)) {
       const int32_t* table = a.block_table + static_cast<int64_t>(w.seq) * a.bt_stride + w.b0;
       int32_t ids = 0;
-      float k_raw = 0.f, v_raw = 0.f, kc = 0.f, lv = 0.f, inv = 0.f;
+      float k_raw = 0.f, v_raw = 0.f, kc = 0.f, lv = 0.f, inv = 0.f, most = -INFINITY;
 #pragma unroll 1
       for (int i = 0; i < w.nblk; ++i) {
         if ((i & 31) == 0) {
@@ -320,7 +327,10 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         }
         const float k = __shfl_sync(0xffffffffu, kc, i & 31), l = __shfl_sync(0xffffffffu, lv, i & 31),
                     v = __shfl_sync(0xffffffffu, inv, i & 31);
-        sts128(base + S::meta + 16 * (number++ % kMetas), __float_as_uint(k), __float_as_uint(l), __float_as_uint(v), 0u);
+        const bool far = l < most - kFarScales && l > -INFINITY;
+        most = fmaxf(most, l);
+        sts128(base + S::meta + 16 * (number++ % kMetas), __float_as_uint(k), __float_as_uint(l), __float_as_uint(far ? -v : v),
+               __float_as_uint(!far && (w.b0 + i) * kBlock <= w.min_len - kBlock ? 1.f : 0.f));
         __syncwarp();
         arrive_expect(base + S::k_full + 8 * ks, kTileBytes);  // (with the block's word there)
         if (++ks == S::kK) ks = 0, k_phase ^= 1;
@@ -435,7 +445,6 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
       if (w.nblk && lane == 0 && alive) arrive(base + S::q_full);
       __syncwarp();
       bool first = true;  // no PV round of the unit yet
-      const int min_len = w.min_len;
       int n0 = w.b0 * kBlock;  // at most 2^31 - 128 in the loop
 #pragma unroll 1
       for (int k = w.nblk; k > 0; --k, n0 = static_cast<int>(n0 + static_cast<uint32_t>(kBlock))) {
@@ -444,8 +453,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         wait(base + S::z_full + 8 * zb, z_phase);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const float4 m4 = lds128f(base + S::meta + 16 * (number++ % kMetas));
-        const float kc = m4.x, lv = m4.y, inv = m4.z;
-        const bool whole = n0 <= min_len - kBlock;
+        const float kc = m4.x, lv = m4.y;
+        float inv = m4.z;
+        const bool plain = m4.w != 0.f;
         const uint32_t z = z_at + zb * N;
         float2 x[R / 2];
         float top = -INFINITY;
@@ -466,9 +476,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
         load();
 #pragma unroll
         for (int i = 0; i < R / 2; ++i) top = fmax3(top, x[i].x, x[i].y);
-        if (__builtin_expect(!four_agree(group, whole && top <= kMaxGrow + kBias), 0)) {
+        if (__builtin_expect(!four_agree(group, plain && top <= kMaxGrow + kBias), 0)) {
           // The uncommon way: the rows' maxima over what they see, new references, and
-          // O and l in their terms.
+          // O and l in their terms; and the blocks whose scale is far below.
 #pragma unroll 1
           for (int c = 0; c < R; c += CH) {
             float2 t[CH / 2];
@@ -492,7 +502,8 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
             const float old = ldsf(base + S::refs + (cur * N + mine) * 4), ref = fminf(old, kBias - mx);
             f = rescale(-old, -ref, 1.f);
             stsf(base + S::refs + ((cur ^ 1) * N + mine) * 4, ref);
-            stsf(fac + mine * 4, f);
+            // (below fp32's range as a factor to apply twice, which the sign says)
+            stsf(fac + mine * 4, f != 0.f ? f : -ex2_approx((ref - old) * 0.5f));
           }
           cur ^= 1;
           if (!four_agree(group, f == 1.f) && !first) {
@@ -504,15 +515,31 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
               tmem_ld<CH>(o_at + c, y);
 #pragma unroll
               for (int i = 0; i < CH; ++i) {
-                const float g = ldsf(fac + (half * R + c + i) * 4);
-                y[i] *= g;
-                (i & 1 ? l[(c + i) >> 1].y : l[(c + i) >> 1].x) *= g;
+                const float g = ldsf(fac + (half * R + c + i) * 4), again = g < 0.f ? g : 1.f;
+                y[i] = y[i] * g * again;
+                float& sum = i & 1 ? l[(c + i) >> 1].y : l[(c + i) >> 1].x;
+                sum = sum * g * again;
               }
               tmem_st<CH>(o_at + c, y);
             }
           }
+          if (inv < 0.f) {  // l by itself (here, not of x below: 60 bytes of spills, not 108)
+#pragma unroll
+            for (int c = 0; c < R; c += CH) {
+              float2 t[CH / 2];
+              load_t<CH, Q16>(t, z + c, rowfac + 4 * c, kc, 0.f);
+#pragma unroll
+              for (int i = 0; i < CH; ++i) {
+                const int r = half * R + c + i;
+                const float e = ex2_approx((i & 1 ? t[i >> 1].y : t[i >> 1].x) + ldsf(base + S::refs + (cur * N + r) * 4));
+                (i & 1 ? l[(c + i) >> 1].y : l[(c + i) >> 1].x) += n0 + tok < static_cast<int>(lds32(lens_at + r * 4)) ? e : 0.f;
+              }
+              __syncwarp();
+            }
+            inv = 0.f;
+          }
           load();
-          if (!whole) {
+          if (!plain) {
 #pragma unroll
             for (int i = 0; i < R / 2; ++i) {
               if (n0 + tok >= static_cast<int>(lds32(lens_at + (half * R + 2 * i) * 4))) x[i].x = -INFINITY;
@@ -546,7 +573,7 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, Shape<N>::kCtasPerSm)
           for (int j = 0; j < 4; ++j) {
             const uint4 b = lds128(v_at + vst * kTileBytes + (g + j) * 2048);
             uint32_t b4[4] = {b.x, b.y, b.z, b.w};
-            if (__builtin_expect(!whole, 0)) {
+            if (__builtin_expect(!plain, 0)) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const uint32_t m = nan_bytes(b4[i]);

@@ -155,7 +155,8 @@ __device__ __forceinline__ Walk walk_of(const Params& p, const Share& sh, const 
 // ---- cut units -----------------------------------------------------------------
 // Joins the pieces of the units that share borders cut.  A warp takes one row
 // and every `parts`-th of its pieces; the `parts` warps of a row are joined in
-// shared memory.
+// shared memory.  A piece's O that lies 2^126 below the row's is gone; its sum of weights
+// need not be (over fp8 references count V's scales, the sums do not): see rescaled.
 __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constant__ Params p, int parts) {
   __shared__ float4 s_o[8][32];
   __shared__ float2 s_ml[8];
@@ -202,10 +203,10 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
       const float mn = fmaxf(M, mx), f = rescale(M, mn, p.qk_scale), w = rescale(ml.x, mn, p.qk_scale);
-      float ls = w * ml.y;
+      float ls = rescaled(ml.y, ml.x, mn, p.qk_scale);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
-      L = L * f + ls;
+      L = rescaled(L, M, mn, p.qk_scale) + ls;
       M = mn;
       x.x *= f, x.y *= f, x.z *= f, x.w *= f;
 #pragma unroll
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(256) dense_pa_join_kernel(const __grid_constan
     for (int k = 0; k < parts; ++k) {
       const float w = rescale(s_ml[warp + k].x, mn, p.qk_scale);
       const float4 y = s_o[warp + k][lane];
-      L += w * s_ml[warp + k].y;
+      L += rescaled(s_ml[warp + k].y, s_ml[warp + k].x, mn, p.qk_scale);
       x.x += w * y.x, x.y += w * y.y, x.z += w * y.z, x.w += w * y.w;
     }
   }

@@ -154,6 +154,13 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
 __device__ __forceinline__ float rescale(float from, float to, float qk) {
   return ex2_approx(fminf((from - to) * qk, 0.f));  // (NaN, of a scale of 0: 0)
 }
+// x times that, in two steps where the factor itself is below fp32's range
+__device__ __forceinline__ float rescaled(float x, float from, float to, float qk) {
+  const float f = rescale(from, to, qk);
+  if (f != 0.f) return x * f;
+  const float half = ex2_approx(fminf((from - to) * qk, 0.f) * 0.5f);
+  return x * half * half;
+}
 // R values of each lane reduced over the warp, all of them at once: each step hands
 // half of the values to the lane that differs in one bit.  Lane i ends with value
 // i * R / 32 (of R = 16, lanes 2j and 2j + 1 both with value j).
