@@ -699,6 +699,7 @@ bsp_status bsp_kv_scaled_write(const bsp_kv_cache* kv, const bsp_kv_scales* scal
   bsp_status st = check_scaled(kv, scales);
   if (st != BSP_OK) return st;
   if (num_tokens < 0) return BSP_ERR_INVALID_ARG;
+  if (kv->num_kv_heads > 65535) return BSP_ERR_UNSUPPORTED;  // (a grid dimension)
   const int64_t heads = kv->num_kv_heads, T = num_tokens;
   if (k_stride < heads * kDim || v_stride < heads * kDim || k_stride % 8 || v_stride % 8) return BSP_ERR_INVALID_ARG;
   if (k_stride > (int64_t{1} << 32) || v_stride > (int64_t{1} << 32)) return BSP_ERR_UNSUPPORTED;

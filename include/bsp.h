@@ -617,6 +617,8 @@ bsp_status bsp_dense_pa_decode(const bsp_kv_cache* kv, const void* q, int32_t q_
  *   K of token t of block b, head h = e4m3 * k[b * num_kv_heads + h]
  * Both arrays are fp32 [num_blocks, num_kv_heads] in device memory.  A block's
  * scales need not be set before its first token is written.
+ * At most 65536 heads, 65535 of a cache that is written (else
+ * BSP_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 typedef struct bsp_kv_scales {
   float* k;
