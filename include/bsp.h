@@ -633,8 +633,9 @@ typedef struct bsp_kv_scales {
  *   slot   int64 [T] as in bsp_kv_page_write (negative: skipped; beyond the
  *          cache: skipped, BSP_DEVERR_SLOT)
  * A run is a stretch of consecutive tokens of the call whose slots are in one
- * block.  For each run, head, and K and V apart, with a the largest finite
- * magnitude of the run's rows,
+ * block.  Of its tokens with the same slot the last one counts, for bytes and
+ * scale alike.  For each run, head, and K and V apart, with a the largest finite
+ * magnitude of the run's rows that count,
  *   s_run = the smallest power of two with a <= 448 * s_run, at least 2^-60
  *           (also of zeros) and at most 2^119
  *   s     = s_run where the run has offset 0 of the block: the block starts
@@ -643,8 +644,7 @@ typedef struct bsp_kv_scales {
  *   where s is above the block's scale, every other byte of the block
  *           = e4m3_sat(byte * (old scale / s)): exact but for values that
  *           leave e4m3's normal range
- * Of tokens of a run with the same slot the last one counts.  A block in two
- * runs of one call: the block's bytes and scales are unspecified.
+ * A block in two runs of one call: the block's bytes and scales are unspecified.
  * No part of k, v, slot, the scales or dev_err may lie in the cache's pages,
  * and the scales overlap nothing (else BSP_ERR_INVALID_ARG).  All inputs are
  * device memory.  One launch.
