@@ -19,11 +19,11 @@
 // of V two dims of the 32 tokens of two pages, which its pages hold side by side, so
 // that both leave as vectors.
 //
-// Measured (one call of a row of them): 64 decode tokens of a head 3.7 us, about a
-// launch and a block's new scale; 8 prompts of 300 to 2400 tokens, two heads, 10.7 us for
-// 17 MB.  There a run's chain of dependent steps is what it takes (slots, table, rows,
-// maximum, bytes), not bandwidth: loading a run's slots at once, and more tokens
-// a CTA, did not shorten it.
+// Measured (a call of a row of twenty in a graph, warm, no scale growing): 64 decode tokens of
+// a head 3.7 us, a launch; 8 prompts of 300 to 2400 tokens, two heads, 10.7 us for 17 MB.  There a
+// run's chain of dependent steps is what it takes (slots, table, rows, maximum, bytes), not
+// bandwidth: loading a run's slots at once, and more tokens a CTA, did not shorten it.  What
+// growing scales add is beside the launch.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kShort = 8;  // tokens of a run that a warp takes
+constexpr int kCtasPerSm = 4;
 
 // the block of token i, -1 for a skipped one
 __device__ __forceinline__ int64_t block_of(const KvScaledWriteParams& p, int64_t i) {
@@ -137,8 +138,8 @@ __device__ __forceinline__ void write_short(const KvScaledWriteParams& p, const 
 }
 
 // (four CTAs an SM: most begin no run, and leave; with three, of 80 registers, 8 prompts of 300 to
-// 2400 tokens take 15.4 us of a graph's replay for 14.2, with five, which spill, 15.7)
-__global__ void __launch_bounds__(kThreads, 4) kv_scaled_write_kernel(KvScaledWriteParams p, int per) {
+// 2400 tokens take 15.4 us of a graph's replay for 14.2, with five 15.7; four spill 32 bytes, five more)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_scaled_write_kernel(KvScaledWriteParams p, int per) {
   __shared__ int s_at[kBlock];  // token of an offset, + 1
   __shared__ int s_end;
   __shared__ uint32_t s_long, s_short;  // the CTA's tokens that begin a run
@@ -276,12 +277,13 @@ __global__ void __launch_bounds__(kThreads, 4) kv_scaled_write_kernel(KvScaledWr
 }  // namespace
 
 cudaError_t launch_kv_scaled_write(const KvScaledWriteParams& p, int num_sms, cudaStream_t s) {
-  // A token a CTA while the CTAs are resident together (three an SM), so that a decode
-  // token's block has eight warps for its new scale; else 32, whose runs share the warps.
-  // Measured, us, a token a CTA and 32: 64 tokens of a head 7.3, 11.5; 256 of a head 11.2,
-  // 11.5; 256 of two 15.4, 11.6; 1024 of a head 23.5, 11.6; 16000 of a prompt 60, 13.4.
-  // (64 and 128 tokens a CTA: 1024 of a head 18.0, 32.7, 16000 of a prompt 13.2, 11.5.)
-  const int per = static_cast<int64_t>(p.num_tokens) * p.hkv * 2 <= 3LL * num_sms ? 1 : 32;
+  // A token a CTA while the CTAs are resident together, so that a decode token's block has
+  // eight warps for its new scale; else 32, whose runs share the warps.  us of a graph's replay
+  // of one call (cold L2, from event to event), a token a CTA and 32, where no block's scale grows, one in
+  // eight, all: 64 tokens of a head 12, 17 / 14, 48 / 14, 49; 256 15, 17 / 17, 49 / 17, 51; 304 15, 17 /
+  // 17, 49 / 18, 50; 320 16, 17 / 18.5, 49 / 20.5, 51; 512 18, 17 / 21, 49 / 25, 51; 1024 26, 17 / 29, 49 /
+  // 36, 53; heads count as tokens do (64 of four as 256).  A prompt of 16000 tokens 56, 17.
+  const int per = static_cast<int64_t>(p.num_tokens) * p.hkv * 2 <= int64_t{kCtasPerSm} * num_sms ? 1 : 32;
   const dim3 grid(static_cast<unsigned>((p.num_tokens + per - 1) / per), static_cast<unsigned>(p.hkv), 2);
   const cudaError_t e = launch_kernel(kv_scaled_write_kernel, grid, dim3(kThreads), 0, s, 0, p, per);
   return e != cudaSuccess ? e : cudaPeekAtLastError();
