@@ -34,11 +34,12 @@
 // V is NaN: in blocks that some row does not see whole such bytes are read as 0, and
 // the rows that see the first of them get their NaN at the end.
 //
-// Measured: 64 requests of 131072 tokens, 16 rows each, 320 to 325 us, 6.6 to 6.7 TB/s, 98 % of
-// the copy rate: memory; 128 of 32768 with 64 rows 201 us, 5.3 TB/s, and with bf16 queries 225: a
+// Measured (a call of a row of twenty in a graph): 64 requests of 131072 tokens, 16 rows each, 318 to
+// 323 us, 6.6 to 6.7 TB/s, 98 to 100 % of the copy rate: memory; 128 of 32768 with 64 rows 200 us, 5.4
+// TB/s, and with bf16 queries, whose logits take twice the MMAs and a factor each, 227: a
 // block's chain of logits, exponentials, P and V, with the two CTAs that TMEM has room for;
-// 32 of 4k to 8k 24.7 us: 6 us to a CTA's first block, 1.8 for each of four, 2.5 for sums and O,
-// 4.5 for the join; one of 1000 tokens 10.6 us.
+// 32 of 4k to 8k 22.8 us (24.9 with other inputs each time): 6 us to a CTA's first block, 1.8 for
+// each of four, 2.5 for sums and O, 4.5 for the join; one of 1000 tokens 10.9 us.
 //
 // Every wait is bounded: after one that gave up (the error word is set, the results are
 // void) loader and issuer issue nothing more and wait for what they have under way; a

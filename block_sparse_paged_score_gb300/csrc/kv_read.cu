@@ -16,10 +16,11 @@
 // Sixteen tokens of an fp8 block one behind the other are read with all loads in flight
 // at once, V's page rows as 8-byte pieces of a dim's tokens.
 //
-// Measured: 333 fp8 tokens 2.5 us, a launch; 131072 MXFP4 tokens of a shuffled cache
-// 15.4 us for 86 MB, 5.6 TB/s, 84 % of the copy rate: memory.  131072 fp8 tokens from
-// offset 5 of a block on, block-scaled: 19.2 us for 102 MB, 5.3 TB/s, 78 % (byte by byte
-// 22.4 us), 500000 64 us, 6.0 TB/s.
+// Measured (a call of a row of twenty in a graph): 333 fp8 tokens 2.5 us, a launch; 131072 MXFP4
+// tokens of a shuffled cache 16.2 us for 86 MB, 5.3 TB/s, 78 % of the copy rate: memory.  131072
+// fp8 tokens from offset 5 of a block on, block-scaled: 17.8 us for 102 MB, 5.7 TB/s, 85 % (byte by
+// byte 20.7; 19.0 with other inputs each time), 500000 62.9 us, 6.2 TB/s.  Tokens in no order pay
+// for the look at their slots: 20000 13.1 us for 12.5, 131072 44.6 for 44.5.
 #include "common.cuh"
 #include "kernels.h"
 

@@ -20,7 +20,7 @@
 // that both leave as vectors.
 //
 // Measured (a call of a row of twenty in a graph, warm, no scale growing): 64 decode tokens of
-// a head 3.7 us, a launch; 8 prompts of 300 to 2400 tokens, two heads, 10.7 us for 17 MB.  There a
+// a head 3.8 us, a launch; 8 prompts of 300 to 2400 tokens, two heads, 10.8 us for 17 MB.  There a
 // run's chain of dependent steps is what it takes (slots, table, rows, maximum, bytes), not
 // bandwidth: loading a run's slots at once, and more tokens a CTA, did not shorten it.  What
 // growing scales add is beside the launch.

@@ -36,13 +36,18 @@
 // TMA (a row's 256 bytes from one thread touch 16 lines, 4096 clocks of a tile).
 //
 // Roundings: a weight is bf16, half a step 2^-8 off; z, m, l and O are fp32, and l sums
-// the unrounded weights.
+// the unrounded weights.  The MMA wants P and V of one type, and V is bf16 with its range; the
+// rest of a weight as a second bf16 (as the sparse attention over bf16 keeps it, which memory
+// bounds) would be half as many MMAs again where MMAs are what bounds it.  Against 64 bits the
+// outputs are off by 0.0018 to 0.0023 of their norm, where their own rounding to bf16 alone
+// makes 0.0016 to 0.0017.
 //
-// Measured: a prompt of 32768 tokens of 16 heads 2.22 to 2.52 ms, 1.75 to 1.98 PFLOP/s by the
-// clock that the power limit leaves (cuBLAS 1.87); 32 prompts of 250 to 2000 tokens 172 us, 1.15
-// PFLOP/s: there a unit's beginning and end, a chain of some 6000 clocks, bound it; 3 x 77
-// tokens over 100000 keys 150 us; one prompt of 100 tokens 8.3 us.  The kernels' code counts: at
-// 117 KB instead of 81 instruction fetches were the first stall.
+// Measured (a call of a row of twenty in a graph): a prompt of 32768 tokens of 16 heads 2.22 to
+// 2.54 ms, 1.73 to 1.98 PFLOP/s by the clock that the power limit leaves (cuBLAS 1.87); 32 prompts of
+// 250 to 2000 tokens 165 us, 1.22 PFLOP/s: there a unit's beginning and end, a chain of some 6000
+// clocks, bound it; 3 x 77 tokens over 100000 keys 144 us; one prompt of 100 tokens 8.4 us.  With other
+// inputs each time 179, 153 and 11.3.  The kernels' code counts: at 117 KB instead of 81 instruction
+// fetches were the first stall.
 //
 // Every wait is bounded: after one that gave up (the error word is set, the results are
 // void) its warp issues nothing more and waits for what it has under way, with a limit
@@ -65,13 +70,15 @@ constexpr float kNoMax = -3.402823466e38f;  // the maximum of no keys (finite: -
 // references above it: (z - m) c instead of z c - (m c), whose rounding then counts
 constexpr float kBigRef = 1048576.f;
 constexpr int kRows = 256, kTile = 128;     // rows of a unit, of a tile
-// Blocks of a unit that is not cut.  2, 4, 8: 132, 132, 130 us on 32 prompts of 1024 tokens of 16
-// heads, 32, 34, 34 on 6 of 2500 of one.  (Up to as many there is no second launch.)
+// Blocks of a unit that is not cut.  2, 4, 8: 165.6, 165.2, 165.6 us on 32 prompts of 250 to 2000
+// tokens of 16 heads, 27.6, 29.0, 29.3 on 6 of 2500 of one.  (Up to as many there is no second launch.)
 constexpr int kWhole = 4;
-// What a unit costs beside its blocks, in blocks: 0, 1, 2, 3 take 220, 181, 171, 178 us on 32
-// prompts of 250 to 2000 tokens and 155, 141, 132, 136 on 32 of 1024.
+// What a unit costs beside its blocks, in blocks: 0, 1, 2, 3 take 214.7, 174.3, 165.2, 173.8 us on 32
+// prompts of 250 to 2000 tokens, 2.65, 2.53, 2.48, 2.48 ms on one of 32768.
 constexpr int kUnitCost = 2;
 // Shares of so many blocks, over so many keys and heads (60 MB), may be lengthened, see aligned_share.
+// (The keys are the rows given: where only some are any sequence's, shares may be lengthened earlier,
+// which changes the time alone.)
 constexpr int kLongShare = 64, kManyKeys = 60 * 1024 * 1024 / (4 * kDim);
 // four warps for each tile, then a producer, an issuer, one that stores, one that idles, four that check V
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpStore = 10, kWarpCheck = 12, kThreads = 512;
@@ -293,8 +300,9 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t acc, uint32_t w) {
 // nearly the same blocks, as they do when a unit is about a whole number of shares
 // long.  Of 16 lengths, the given one and up to 15 / 128 more, the first with the least part
 // of a share left over in all, counted in 64ths of the units.  us, without and with: 3 x 77
-// queries of 16 heads over 100000 keys of two 172, 149; 8 x 25-200 of 8 over 4k-30k of one
-// (69 MB) 68 to 76, 66; but 2 x 500 of 8 over 50000 of one (52 MB, which L2 holds) 145, 150.
+// queries of 16 heads over 100000 keys of two (307 MB) 166, 144; 2 x 200 of 16 over 40000 of two (82 MB)
+// 105 to 112, 104 to 106; within 2 % on eleven others of 61 to 123 MB, of 1, 2 and 4 KV heads; but 2 x
+// 500 of 8 over 50000 of one (52 MB, which L2 holds) 127, 129, and 2000 of 8 over 100000 (52 MB) 465, 474.
 __device__ __noinline__ int64_t aligned_share(const Params& p, int64_t total, int64_t share, Seq q, int64_t* smem) {
   int* const s_count = reinterpret_cast<int*>(smem + kThreads / 32 + 2);
   int* const s_left = s_count + 1;

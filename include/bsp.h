@@ -633,9 +633,9 @@ typedef struct bsp_kv_scales {
  *   slot   int64 [T] as in bsp_kv_page_write (negative: skipped; beyond the
  *          cache: skipped, BSP_DEVERR_SLOT)
  * A run is a stretch of consecutive tokens of the call whose slots are in one
- * block.  Of its tokens with the same slot the last one counts, for bytes and
- * scale alike.  For each run, head, and K and V apart, with a the largest finite
- * magnitude of the run's rows that count,
+ * block (a skipped token ends it).  Of its tokens with the same slot the last
+ * one counts, for bytes and scale alike.  For each run, head, and K and V apart,
+ * with a the largest finite magnitude of the run's rows that count,
  *   s_run = the smallest power of two with a <= 448 * s_run, at least 2^-60
  *           (also of zeros) and at most 2^119
  *   s     = s_run where the run has offset 0 of the block: the block starts
@@ -672,10 +672,15 @@ bsp_status bsp_kv_scaled_read(const bsp_kv_cache* kv, const bsp_kv_scales* scale
  *             ones and NaN give the rows that see their block NaN
  * Bytes and scales at and past L_r are never used by row r, whatever they
  * hold.  A NaN byte of K gives NaN rows, one of V NaN in its dim of the rows
- * that see it.  Weights are rounded to f16; sums and references are fp32.  A
- * bf16 query row is taken as two e4m3 parts with one scale: exact for elements
- * down to 2^-9 of the row's largest, off by at most 2^-17 of that below.  A row
- * whose query holds an infinity or a NaN is NaN.
+ * that see it.  Sums and references are fp32, and every token counts in the sum
+ * of weights whatever its block's scale is.  For V a token's weight takes its block's
+ * scale along and is rounded to f16: where weight and scale together are 2^21
+ * and more below the row's largest it has fewer bits, down to 2^32 below, where
+ * its values are left out of O (each less than 2^-14 of the smallest step of the
+ * values that dominate).  A bf16 query row is taken as two e4m3 parts with one
+ * scale: exact for elements down to 2^-9 of the row's largest (of 2^-100 where
+ * that is smaller), off by at most 2^-17 of that below.  A row whose query
+ * holds an infinity or a NaN is NaN.
  * ---------------------------------------------------------------------- */
 size_t bsp_dense_pa_fp8_workspace_bytes(int32_t num_rows, int32_t num_kv_heads, int32_t group, int32_t q_group);
 bsp_status bsp_dense_pa_decode_fp8(const bsp_kv_cache* kv, const bsp_kv_scales* scales, const void* q, int32_t q_dtype,
@@ -702,9 +707,9 @@ bsp_status bsp_dense_pa_decode_fp8(const bsp_kv_cache* kv, const bsp_kv_scales* 
  *         they were.  It overlaps no input, nor does the workspace (else
  *         BSP_ERR_INVALID_ARG)
  * Keys that a query does not see never reach its row, whatever they hold; an
- * infinity or NaN in one that it sees does.  Weights are rounded to bf16; sums
- * and references are fp32, and a reference may lag behind by 2^30: of values of
- * V beyond 2^72 a sum may overflow.  The same inputs give the same bits.  One
+ * infinity or NaN in one that it sees does.  Weights are rounded to bf16, the
+ * type of V; sums and references are fp32, and a reference may lag behind by
+ * 2^30: of values of V beyond 2^72 a sum may overflow.  The same inputs give the same bits.  One
  * launch, two with more than 512 keys.
  * ws: device workspace of bsp_prompt_attention_workspace_bytes() bytes, 16-byte
  * aligned (its contents need not be set, and carry nothing from call to
