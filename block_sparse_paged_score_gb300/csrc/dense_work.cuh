@@ -11,10 +11,8 @@ namespace bsp {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxGrow = 8.f;   // the reference maximum moves when a row's maximum grows by more (log2)
 constexpr float kBias = 7.f;      // weights are 2^((z - m) qk + kBias): at most 2^15
-constexpr float kNoMax = -3.402823466e38f;  // the maximum of no tokens (finite: -inf - kNoMax stays -inf)
 
 // bytes of the list of cut units at the start of the workspace
 __host__ __device__ constexpr int64_t list_bytes(int64_t ctas) { return (ctas * 8 + 255) / 256 * 256; }

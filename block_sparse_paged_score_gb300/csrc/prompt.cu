@@ -64,9 +64,7 @@ namespace bsp {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxSum = 1073741824.f;     // of a half block's weights (bf16 and fp32 hold any)
-constexpr float kNoMax = -3.402823466e38f;  // the maximum of no keys (finite: -inf - kNoMax stays -inf)
 // references above it: (z - m) c instead of z c - (m c), whose rounding then counts
 constexpr float kBigRef = 1048576.f;
 constexpr int kRows = 256, kTile = 128;     // rows of a unit, of a tile
@@ -261,16 +259,6 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; i += 8)
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                  "+r"(r[i + 6]), "+r"(r[i + 7]));
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
 }
 // K-major rows of 128 bytes, 128-byte swizzle (see smem_desc_sw128); V as the B operand
 // with its dims contiguous: atoms of 64 dims x 8 keys, dims 64.. kHalf on
